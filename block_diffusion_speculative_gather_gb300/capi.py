@@ -16,7 +16,9 @@ LIB_PATH = os.path.join(_PKG, "libdflash.so")
 DFLASH_OK = 0
 ERRORS = {-1: "CONFIG", -2: "CAPACITY", -3: "ARG", -4: "CUDA", -5: "DEVICE", -6: "TIMEOUT",
           -7: "STATE"}
-DFLASH_F32, DFLASH_BF16, DFLASH_INT4G64 = 0, 1, 2
+DFLASH_F32, DFLASH_BF16, DFLASH_INT4G64, DFLASH_F16 = 0, 1, 2, 3
+ROPE_SCALING = {"none": 0, "linear": 1, "parts": 2}
+KV8_PAGE = 64
 MAX_TAPS = 8
 MAX_BLOCK = 16
 
@@ -69,6 +71,33 @@ class dflash_profile_t(C.Structure):
                 ("gemm_weight_bytes", C.c_double)]
 
 
+class dflash_kv8_cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("n_pages", C.c_int32), ("n_kv", C.c_int32),
+                ("head_dim", C.c_int32), ("pad_", C.c_int32)]
+
+
+class dflash_kv8_query(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p), ("table", C.c_void_p),
+                ("kv_len", C.c_void_p), ("row_start", C.c_void_p), ("q_row", C.c_int64),
+                ("q_head", C.c_int64), ("out_row", C.c_int64), ("out_head", C.c_int64),
+                ("rows", C.c_int32), ("n_q", C.c_int32), ("S", C.c_int32), ("max_pages", C.c_int32),
+                ("dtype", C.c_int32), ("causal", C.c_int32), ("window", C.c_int32),
+                ("scale", C.c_float)]
+
+
+class dflash_rope_config(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("scaling", C.c_int32),
+                ("original_len", C.c_int32), ("theta", C.c_double), ("factor", C.c_double),
+                ("alpha", C.c_double), ("beta", C.c_double), ("scale", C.c_float), ("pad_", C.c_int32)]
+
+
+class dflash_heads(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("out", C.c_void_p), ("heads", C.c_int32), ("pad_", C.c_int32),
+                ("x_row", C.c_int64), ("x_head", C.c_int64), ("out_row", C.c_int64),
+                ("out_head", C.c_int64)]
+
+
 def _load() -> C.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -112,6 +141,16 @@ def _load() -> C.CDLL:
         "dflash_batch_set_logits_out": (C.c_int, [vp, vp, vp]),
         "dflash_batch_check": (C.c_int, [vp, vp]),
         "dflash_batch_destroy": (None, [vp]),
+        "dflash_pages_plan": (C.c_int, [vp, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "dflash_pages_trim": (C.c_int, [vp, vp, i32, vp, i32, vp, vp, i32, vp]),
+        "dflash_kv8_append": (C.c_int, [C.POINTER(dflash_kv8_cache), vp, i64, i64, vp, i64, i64, i32, i32,
+                                        vp, vp, vp]),
+        "dflash_kv8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
+        "dflash_kv8_attention": (C.c_int, [C.POINTER(dflash_kv8_cache), C.POINTER(dflash_kv8_query), vp, sz,
+                                           vp, vp]),
+        "dflash_rope_turns": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp]),
+        "dflash_rope": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp, i32, i32, i32,
+                                  C.POINTER(dflash_heads), C.POINTER(dflash_heads), vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -132,7 +171,9 @@ EXPORTED = ("dflash_workspace_bytes", "dflash_kv_target_bytes", "dflash_kv_draft
             "dflash_progress", "dflash_attention_form", "dflash_linear_dense",
             "dflash_batch_workspace_bytes", "dflash_batch_init", "dflash_batch_context",
             "dflash_batch_draft", "dflash_batch_verify_accept", "dflash_batch_set_logits_out",
-            "dflash_batch_check", "dflash_batch_destroy")
+            "dflash_batch_check", "dflash_batch_destroy", "dflash_pages_plan", "dflash_pages_trim",
+            "dflash_kv8_append", "dflash_kv8_workspace_bytes", "dflash_kv8_attention",
+            "dflash_rope_turns", "dflash_rope")
 
 
 def check(rc: int) -> None:
@@ -392,3 +433,185 @@ def dflash_batch_check(b, stream=None):
 
 def dflash_batch_destroy(b) -> None:
     lib.dflash_batch_destroy(b)
+
+
+# ---- 8-bit paged KV cache and rotary positions
+
+def _here(**tensors) -> None:
+    """Every tensor on the current CUDA device, whose current stream (or a
+    stream of which) the call is enqueued on."""
+    import torch
+    _on_gpu(**tensors)
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise DFlashError(DFLASH_ERR_ARG, f"{name}: on {t.device}, the current device is cuda:{cur}")
+
+
+def _kinds():
+    import torch
+    return {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
+
+
+def _heads(t, name: str, dtypes, shape) -> None:
+    """A [rows][heads][head_dim] tensor by strides: contiguous heads."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: a torch tensor is required")
+    if t.dtype not in dtypes:
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 3 or any(e is not None and e != d for e, d in zip(shape, t.shape)):
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: the elements of a head must be contiguous")
+
+
+def _err2(err) -> None:
+    import torch
+    _need(err, "err", (torch.int32,), (2,))
+
+
+def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, positions, slots, kv_after,
+                      n_free_out, stream=None):
+    """Pages, row starts, positions and slots of the next step's rows (see
+    include/dflash.h); rows = positions.numel().  int32 tensors throughout."""
+    import torch
+    i32 = (torch.int32,)
+    _need(table, "table", i32, (None, None))
+    S, max_pages = table.shape
+    for name, t in (("kv_len", kv_len), ("q_len", q_len), ("kv_after", kv_after)):
+        _need(t, name, i32, (S,))
+    _need(free_pages, "free_pages", i32, (None,))
+    _need(n_free, "n_free", i32, (1,))
+    _need(n_free_out, "n_free_out", i32, (1,))
+    _need(row_start, "row_start", i32, (S + 1,))
+    _need(positions, "positions", i32, (None,))
+    _need(slots, "slots", i32, (positions.shape[0],))
+    _here(kv_len=kv_len, q_len=q_len, free_pages=free_pages, n_free=n_free, table=table,
+          row_start=row_start, positions=positions, slots=slots, kv_after=kv_after,
+          n_free_out=n_free_out)
+    check(lib.dflash_pages_plan(_ptr(kv_len), _ptr(q_len), S, _ptr(free_pages), free_pages.shape[0],
+                                _ptr(n_free), _ptr(table), max_pages, positions.shape[0],
+                                _ptr(row_start), _ptr(positions), _ptr(slots), _ptr(kv_after),
+                                _ptr(n_free_out), _stream(stream)))
+
+
+def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
+    """kv_len[s] = min(kv_len[s], new_len[s]); pages no longer needed go back
+    onto free_pages."""
+    import torch
+    i32 = (torch.int32,)
+    _need(table, "table", i32, (None, None))
+    S, max_pages = table.shape
+    _need(kv_len, "kv_len", i32, (S,))
+    _need(new_len, "new_len", i32, (S,))
+    _need(free_pages, "free_pages", i32, (None,))
+    _need(n_free, "n_free", i32, (1,))
+    _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
+    check(lib.dflash_pages_trim(_ptr(kv_len), _ptr(new_len), S, _ptr(free_pages), free_pages.shape[0],
+                                _ptr(n_free), _ptr(table), max_pages, _stream(stream)))
+
+
+def _kv8_cache(k_codes, v_codes, k_scale, v_scale) -> dflash_kv8_cache:
+    import torch
+    code = (torch.uint8, torch.float8_e4m3fn)
+    _need(k_codes, "k_codes", code, (None, None, KV8_PAGE, None))
+    n_pages, n_kv, _, hd = k_codes.shape
+    _need(v_codes, "v_codes", code, (n_pages, n_kv, KV8_PAGE, hd))
+    _need(k_scale, "k_scale", (torch.float32,), (n_pages, n_kv))
+    _need(v_scale, "v_scale", (torch.float32,), (n_pages, n_kv))
+    return dflash_kv8_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), n_pages, n_kv, hd, 0)
+
+
+def dflash_kv8_append(k, v, slots, k_codes, v_codes, k_scale, v_scale, err, stream=None):
+    """Quantise rows k, v [rows][n_kv][head_dim] (fp32, bf16 or f16, strided
+    rows and heads) into the pool at slots [rows]; negative slots skip."""
+    import torch
+    cache = _kv8_cache(k_codes, v_codes, k_scale, v_scale)
+    _need(slots, "slots", (torch.int32,), (None,))
+    rows, kinds = slots.shape[0], _kinds()
+    _heads(k, "k", kinds, (rows, cache.n_kv, cache.head_dim))
+    _heads(v, "v", (k.dtype,), (rows, cache.n_kv, cache.head_dim))
+    _err2(err)
+    _here(k=k, v=v, slots=slots, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, err=err)
+    check(lib.dflash_kv8_append(C.byref(cache), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                                v.stride(1), kinds[k.dtype], rows, _ptr(slots), _ptr(err),
+                                _stream(stream)))
+
+
+def dflash_kv8_workspace_bytes(rows: int, S: int, n_q: int, n_kv: int, head_dim: int, max_pages: int) -> int:
+    return lib.dflash_kv8_workspace_bytes(rows, S, n_q, n_kv, head_dim, max_pages)
+
+
+def dflash_kv8_attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, row_start, out, workspace,
+                         err, lse=None, scale=None, causal=True, window=0, stream=None):
+    """out = softmax(scale q k^T + mask) v of each sequence's rows over its
+    cached positions; q, out [rows][n_q][head_dim] bf16 or f16 by strides,
+    lse fp32 [rows][n_q]; scale None: head_dim ** -0.5."""
+    import torch
+    cache = _kv8_cache(k_codes, v_codes, k_scale, v_scale)
+    _heads(q, "q", (torch.bfloat16, torch.float16), (None, None, cache.head_dim))
+    rows, n_q, hd = q.shape
+    _heads(out, "out", (q.dtype,), (rows, n_q, hd))
+    i32 = (torch.int32,)
+    _need(table, "table", i32, (None, None))
+    S, max_pages = table.shape
+    _need(kv_len, "kv_len", i32, (S,))
+    _need(row_start, "row_start", i32, (S + 1,))
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), (rows, n_q))
+    _need(workspace, "workspace", None, None)
+    _err2(err)
+    _here(q=q, out=out, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
+          kv_len=kv_len, row_start=row_start, workspace=workspace, err=err, lse=lse)
+    args = dflash_kv8_query(_ptr(q), _ptr(out), _ptr(lse), _ptr(table), _ptr(kv_len), _ptr(row_start),
+                            q.stride(0), q.stride(1), out.stride(0), out.stride(1), rows, n_q, S,
+                            max_pages, _kinds()[q.dtype], 1 if causal else 0, window,
+                            hd ** -0.5 if scale is None else scale)
+    check(lib.dflash_kv8_attention(C.byref(cache), C.byref(args), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(err),
+                                   _stream(stream)))
+
+
+def rope_config(rotary_dim: int, theta: float = 1e6, interleaved: bool = False, scaling: str = "none",
+                factor: float = 1.0, original_len: int = 0, alpha: float = 1.0, beta: float = 32.0,
+                scale: float = 1.0) -> dflash_rope_config:
+    """Settings of dflash_rope; scaling "none", "linear" or "parts"."""
+    if scaling not in ROPE_SCALING:
+        raise DFlashError(DFLASH_ERR_ARG, f"scaling {scaling!r}, expected one of {tuple(ROPE_SCALING)}")
+    return dflash_rope_config(rotary_dim, 1 if interleaved else 0, ROPE_SCALING[scaling], original_len,
+                              theta, factor, alpha, beta, scale, 0)
+
+
+def dflash_rope_turns(cfg: dflash_rope_config, turns, stream=None):
+    """The frequency table of cfg: int64 [rotary_dim / 2], 2^-64 turns a position."""
+    import torch
+    _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
+    _here(turns=turns)
+    check(lib.dflash_rope_turns(C.byref(cfg), _ptr(turns), _stream(stream)))
+
+
+def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2=None, stream=None):
+    """Rotate x (and x2) [rows][heads][head_dim] into out (out2) at positions
+    [rows]; fp32, bf16 or f16, strided rows and heads, out may be x."""
+    import torch
+    kinds = _kinds()
+    _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
+    _need(positions, "positions", (torch.int32,), (None,))
+    rows = positions.shape[0]
+    _heads(x, "x", kinds, (rows, None, None))
+    hd = x.shape[2]
+    _heads(out, "out", (x.dtype,), tuple(x.shape))
+    if (x2 is None) != (out2 is None):
+        raise DFlashError(DFLASH_ERR_ARG, "x2 and out2 go together")
+    second = None
+    if x2 is not None:
+        _heads(x2, "x2", (x.dtype,), (rows, None, hd))
+        _heads(out2, "out2", (x.dtype,), tuple(x2.shape))
+        second = C.byref(dflash_heads(_ptr(x2), _ptr(out2), x2.shape[1], 0, x2.stride(0), x2.stride(1),
+                                      out2.stride(0), out2.stride(1)))
+    _here(turns=turns, positions=positions, x=x, out=out, x2=x2, out2=out2)
+    first = dflash_heads(_ptr(x), _ptr(out), x.shape[1], 0, x.stride(0), x.stride(1), out.stride(0),
+                         out.stride(1))
+    check(lib.dflash_rope(C.byref(cfg), _ptr(turns), _ptr(positions), rows, hd, kinds[x.dtype],
+                          C.byref(first), second, _stream(stream)))

@@ -1,0 +1,648 @@
+// Attention over the 8-bit paged KV cache.
+//
+//   o[r] = sum_j w_rj v_j / sum_j w_rj,  w_rj = exp(scale * q_r . k_j)
+// over the keys j that row r sees, k_j and v_j = code * (their page's scale).
+//
+// Rows of one kv head's q heads share its keys, so a tile's rows are (row,
+// q head of the group) pairs, packed row-major.  Scores are kept in base 2.
+// With page scales kp, vp (vp = 2^e for the cache's own scales) a page adds
+//   P = 2^(t + log2 vp - M),  O += P * vcode,  l += (sum P) / vp
+// with t the scores times kp and M the running maximum of t + log2 vp: P is
+// the key's weight on the value codes, at most 1, so it fits f16 whatever
+// the scales; l carries the plain softmax sum relative to 2^M in fp32.
+//
+// q enters the MMAs as f16: a row is scaled by the power of two that brings
+// its largest element into [1, 2) (folded into the score factor), which keeps
+// bf16 and f16 rows exact but for elements 2^-14 below the row's largest,
+// that lose low bits.  e4m3 codes are exact in f16.  P is rounded to f16
+// (half a step: 2^-11 of the weight); scores, sums and outputs are fp32.
+
+#include "attention_dev.cuh"
+#include "gemm.cuh"
+#include "kv8.cuh"
+
+namespace dfl {
+namespace {
+
+using adev::ldsm_x4_trans;
+
+constexpr int KT = 16;              // packed rows of a tile (the M side of the MMAs)
+constexpr int KW = 4;               // consumer warps; each takes 16 of a page's 64 keys
+constexpr int KSTAGES = 4;          // pages in flight of a CTA
+constexpr int KTHREADS = 32 * (KW + 1);
+constexpr int SITE_KV8_FULL = 301, SITE_KV8_EMPTY = 302, SITE_KV8_PAGE = 303, SITE_KV8_LEN = 304;
+
+template <int HD> constexpr int tile_bytes() { return KV8_PAGE * HD; }
+template <int HD> constexpr int red_ld() { return HD + 16; }   // row pitch of the merge buffer (floats)
+
+template <int HD> struct KvSmem {
+    static constexpr int ring = 0;
+    static constexpr int red = ring + KSTAGES * 2 * tile_bytes<HD>();
+    static constexpr int ml = red + KW * KT * red_ld<HD>() * 4;
+    static constexpr int scales = ml + KW * KT * 2 * 4;      // [stages] (k, v)
+    static constexpr int bars = scales + KSTAGES * 8;        // full, empty
+    static constexpr int flag = bars + KSTAGES * 16;
+    static constexpr int cum = flag + 16;                    // [S + 1] items before each sequence
+    static size_t bytes(int S) { return 1024 + cum + (size_t)(S + 1) * 4; }
+};
+
+__device__ __forceinline__ void report(int* err, int code, int info) {
+    if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
+}
+
+// One sequence of the call: its rows, keys and how they are cut.
+struct Seq {
+    int r0, n;          // rows r0 .. r0 + n - 1
+    int kv, first;      // cached tokens; position of the first row (may be negative: rows without keys)
+    int page_lo, page_hi;
+    int tiles, splits, len;   // row tiles, splits of the pages, pages of a split
+};
+
+__device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
+    Seq q;
+    const int r0 = a.row_start[s], r1 = a.row_start[s + 1];
+    q.r0 = r0;
+    q.n = r1 - r0;
+    int kv = a.kv_len[s];
+    const long long cap = (long long)a.max_pages * KV8_PAGE;
+    if (r0 < 0 || r1 < r0 || r1 > a.rows || kv < 0 || kv > cap) {
+        report(a.err, DERR_INDEX, SITE_KV8_LEN);   // such a sequence is skipped
+        q.n = 0;
+        q.r0 = 0;
+        kv = 0;
+    }
+    q.kv = kv;
+    q.first = kv - q.n;
+    int lo = 0;
+    if (a.window > 0) {
+        lo = a.causal ? q.first + 1 - a.window : q.first - a.window;
+        if (lo < 0) lo = 0;
+    }
+    q.page_lo = lo / KV8_PAGE;
+    q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
+    const int pages = q.page_hi > q.page_lo ? q.page_hi - q.page_lo : 0;
+    q.tiles = (int)(((long long)q.n * a.group + KT - 1) / KT);
+    q.len = (pages + a.split_cap - 1) / a.split_cap;
+    if (q.len < 1) q.len = 1;
+    q.splits = (pages + q.len - 1) / q.len;
+    if (q.splits < 1) q.splits = 1;
+    return q;
+}
+
+// One unit of work: a row tile, a kv head and a split of the tile's pages.
+struct Item {
+    int s, tile, kh, split;
+    int p0, p1;         // pages [p0, p1)
+    int lo, hi;         // keys that some row of the tile sees: [lo, hi)
+    int in_lo, in_hi;   // keys that every row of the tile sees: [in_lo, in_hi)
+};
+
+__device__ __forceinline__ void row_keys(const Kv8AttnArgs& a, const Seq& q, int i, int* lo, int* hi) {
+    const int pos = q.first + i;
+    *lo = 0;
+    if (a.causal) {
+        *hi = pos + 1;
+        if (a.window > 0) *lo = pos + 1 - a.window;
+    } else {
+        *hi = q.kv;
+        if (a.window > 0) *lo = q.first - a.window;
+    }
+    if (*lo < 0) *lo = 0;
+    if (*hi < 0) *hi = 0;
+}
+
+__device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, const Seq& q, int s, int idx) {
+    Item it;
+    it.s = s;
+    it.split = idx % q.splits;
+    const int rest = idx / q.splits;
+    it.kh = rest % a.n_kv;
+    it.tile = rest / a.n_kv;
+    const int i0 = it.tile * KT / a.group;
+    int i1 = (it.tile * KT + KT - 1) / a.group;
+    if (i1 > q.n - 1) i1 = q.n - 1;
+    int lo0, hi0, lo1, hi1;
+    row_keys(a, q, i0, &lo0, &hi0);
+    row_keys(a, q, i1, &lo1, &hi1);
+    it.lo = lo0;
+    it.hi = hi1;
+    it.in_lo = lo1;
+    it.in_hi = hi0;
+    int p0 = q.page_lo + it.split * q.len, p1 = p0 + q.len;
+    if (p1 > q.page_hi) p1 = q.page_hi;
+    const int tp0 = it.lo / KV8_PAGE, tp1 = (it.hi + KV8_PAGE - 1) / KV8_PAGE;
+    it.p0 = p0 > tp0 ? p0 : tp0;
+    it.p1 = p1 < tp1 ? p1 : tp1;
+    if (it.p1 < it.p0) it.p1 = it.p0;
+    return it;
+}
+
+// Items before each sequence, into shared memory, by the whole CTA.
+__device__ void count_items(const Kv8AttnArgs& a, int* cum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int wsum[KW + 1];
+    const int per = (a.S + KTHREADS - 1) / KTHREADS;
+    int mine = 0;
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s < a.S) {
+            const Seq q = seq_of(a, s);
+            mine += q.tiles * a.n_kv * q.splits;
+        }
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s < a.S) {
+            cum[s] = at;
+            const Seq q = seq_of(a, s);
+            at += q.tiles * a.n_kv * q.splits;
+            if (s == a.S - 1) cum[a.S] = at;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int find_item(const int* cum, int S, int item) {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= item) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two e4m3 codes (the low 16 bits) to a pair of f16, exactly.
+__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+
+// Byte offset of 16-byte chunk c of key row r in a tile that TMA wrote with
+// the 128-byte (head_dim 128) or 64-byte (head_dim 64) swizzle.
+template <int HD>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return HD == 128 ? swz128(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Key of MMA column n (0..7) inside a group of 8: for 128-byte rows columns
+// 2j, 2j + 1 are keys j, j + 4, whose swizzled chunks lie in different bank
+// halves; 64-byte rows need no reordering.
+template <int HD>
+__device__ __forceinline__ int key_of(int n) { return HD == 128 ? (n >> 1) + 4 * (n & 1) : n; }
+
+template <typename T>
+__device__ __forceinline__ void store_row4(T* p, float a, float b, float c, float d);
+template <>
+__device__ __forceinline__ void store_row4<__nv_bfloat16>(__nv_bfloat16* p, float a, float b, float c, float d) {
+    uint2 v{pack_bf16x2(a, b), pack_bf16x2(c, d)};
+    *reinterpret_cast<uint2*>(p) = v;
+}
+template <>
+__device__ __forceinline__ void store_row4<__half>(__half* p, float a, float b, float c, float d) {
+    uint2 v{pack_f16x2(a, b), pack_f16x2(c, d)};
+    *reinterpret_cast<uint2*>(p) = v;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(KTHREADS, 2)
+kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const Kv8AttnArgs a) {
+    using S_ = KvSmem<HD>;
+    constexpr int TB = tile_bytes<HD>();
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    float* red = reinterpret_cast<float*>(sm + S_::red);
+    float* ml = reinterpret_cast<float*>(sm + S_::ml);
+    float2* scales = reinterpret_cast<float2*>(sm + S_::scales);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + S_::bars);
+    uint64_t* empty = full + KSTAGES;
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] the same, as of the item's end
+    int* cum = reinterpret_cast<int*>(sm + S_::cum);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_trigger();
+    if (tid == 0) {
+        tma_prefetch_desc(&k_map);
+        tma_prefetch_desc(&v_map);
+        for (int i = 0; i < KSTAGES; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, KW);
+        }
+        fence_mbar_init();
+        flag[1] = 0;
+    }
+    pdl_wait();
+    count_items(a, cum);   // ends with a barrier
+    const int total = cum[a.S];
+
+    if (warp == KW) {
+        // ---- producer: pages of every item of this CTA, in order.  The lanes
+        // look up 32 pages and their scales at a time; lane 0 issues.
+        unsigned it = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const int s = find_item(cum, a.S, item);
+            const Seq q = seq_of(a, s);
+            const Item w = item_of(a, q, s, item - cum[s]);
+            for (int b = w.p0; b < w.p1 && ok; b += 32) {
+                int page = -1;
+                float ks = -1.f, vs = 1.f;
+                if (b + lane < w.p1) {
+                    page = a.table[(size_t)s * a.max_pages + b + lane];
+                    if (page < 0 || page >= a.n_pages) {
+                        report(a.err, DERR_INDEX, SITE_KV8_PAGE);   // its keys are left out
+                        page = -1;
+                    } else {
+                        ks = a.k_scale[(size_t)page * a.n_kv + w.kh];
+                        vs = a.v_scale[(size_t)page * a.n_kv + w.kh];
+                    }
+                }
+                const int m = w.p1 - b < 32 ? w.p1 - b : 32;
+                for (int j = 0; j < m; ++j) {
+                    const int pg = __shfl_sync(0xffffffffu, page, j);
+                    const float kj = __shfl_sync(0xffffffffu, ks, j), vj = __shfl_sync(0xffffffffu, vs, j);
+                    const int st = it % KSTAGES;
+                    bool issued = true;
+                    if (lane == 0) {
+                        if (it >= KSTAGES && !mbar_wait_bounded(empty + st, (it / KSTAGES - 1) & 1)) {
+                            report(a.err, DERR_TIMEOUT, SITE_KV8_EMPTY);
+                            flag[1] = 1;
+                            issued = false;
+                        } else {
+                            scales[st] = make_float2(kj, vj);
+                            uint8_t* kt = sm + S_::ring + st * 2 * TB;
+                            if (pg >= 0) {
+                                mbar_arrive_expect_tx(full + st, 2 * TB);
+                                const int y = (pg * a.n_kv + w.kh) * KV8_PAGE;
+                                tma_load_2d(kt, &k_map, full + st, 0, y);
+                                tma_load_2d(kt + TB, &v_map, full + st, 0, y);
+                            } else {
+                                mbar_arrive(full + st);
+                            }
+                        }
+                    }
+                    if (!__shfl_sync(0xffffffffu, (int)issued, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    ++it;
+                    ok = __shfl_sync(0xffffffffu, flag[1], 0) == 0;
+                    if (!ok) break;
+                }
+            }
+        }
+        // no copy of this CTA is in flight when it ends
+        if (lane == 0) {
+            const unsigned n = it < KSTAGES ? it : KSTAGES;
+            for (unsigned i = it - n; i < it; ++i) mbar_wait_bounded(full + i % KSTAGES, (i / KSTAGES) & 1);
+        }
+        return;
+    }
+
+    // ---- consumers
+    const int g = lane >> 2, c = lane & 3;
+    unsigned it = 0;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const int s = find_item(cum, a.S, item);
+        const Seq q = seq_of(a, s);
+        const Item w = item_of(a, q, s, item - cum[s]);
+
+        // q of rows g, g + 8 as A fragments: k step (h, j) of 16 covers the
+        // dims 64 h + 16 c + 4 j .. + 3 of every lane c of a quad, so a
+        // lane's fragments are its own 16 consecutive dims
+        uint32_t qa[HD / 16][4];
+        float fr[2];
+        int klo[2], khi[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int pr = w.tile * KT + g + 8 * r;
+            const int i = pr / a.group, hq = w.kh * a.group + pr % a.group;
+            const bool real = i < q.n;
+            float v[HD / 4];
+            float top = 0.f;
+            if (real) {
+                const T* src = reinterpret_cast<const T*>(a.q) + (long long)(q.r0 + i) * a.q_row + (long long)hq * a.q_head;
+#pragma unroll
+                for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 e = *reinterpret_cast<const uint4*>(src + 64 * h + 16 * c + 8 * k);
+                        const T* ev = reinterpret_cast<const T*>(&e);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[16 * h + 8 * k + j] = to_f32(ev[j]);
+                    }
+                row_keys(a, q, i, &klo[r], &khi[r]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < HD / 4; ++j) v[j] = 0.f;
+                klo[r] = 0;
+                khi[r] = 0x7fffffff;   // computed on zeros, never written
+            }
+#pragma unroll
+            for (int j = 0; j < HD / 4; ++j) {
+                const float x = fabsf(v[j]);
+                top = fmaxf(top, x < INFINITY ? x : 0.f);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            uint32_t e = __float_as_uint(top) >> 23;       // biased exponent
+            e = e < 1 ? 1 : (e > 253 ? 253 : e);
+            const float inv = top > 0.f ? __uint_as_float((254 - e) << 23) : 1.f;
+            fr[r] = (top > 0.f ? __uint_as_float(e << 23) : 1.f) * a.scale_log2;
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    qa[4 * h + j][r] = pack_f16x2(v[16 * h + 4 * j] * inv, v[16 * h + 4 * j + 1] * inv);
+                    qa[4 * h + j][2 + r] = pack_f16x2(v[16 * h + 4 * j + 2] * inv, v[16 * h + 4 * j + 3] * inv);
+                }
+        }
+
+        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[HD / 8][4];
+#pragma unroll
+        for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+
+        for (int p = w.p0; p < w.p1; ++p, ++it) {
+            const int st = it % KSTAGES;
+            if (flag[1]) break;
+            if (!mbar_wait_bounded(full + st, (it / KSTAGES) & 1)) {
+                report(a.err, DERR_TIMEOUT, SITE_KV8_FULL);
+                flag[1] = 1;
+            }
+            if (flag[1]) break;
+            const float2 sc = scales[st];
+            const uint8_t* kt = sm + S_::ring + st * 2 * TB;
+            const uint8_t* vt = kt + TB;
+            const int key0 = p * KV8_PAGE + 16 * warp;   // this warp's first key
+            if (sc.x >= 0.f && sc.y > 0.f && key0 < w.hi && key0 + 16 > w.lo) {
+                float acc[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+#pragma unroll
+                for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint4 kk = lds128(kt + tile_off<HD>(16 * warp + 8 * t + key_of<HD>(g), 4 * h + c));
+                        const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t b[2] = {f16_of_codes(kw[j]), f16_of_codes(kw[j] >> 16)};
+                            mma_f16_16816(acc[t], qa[4 * h + j], b);
+                        }
+                    }
+                const float ev = log2f(sc.y);
+                const bool whole = key0 >= w.in_lo && key0 + 16 <= w.in_hi;
+                const float f0 = fr[0] * sc.x, f1 = fr[1] * sc.x;
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(acc[t][e], e < 2 ? f0 : f1, ev);
+                        if (!whole) {
+                            const int key = key0 + 8 * t + key_of<HD>(2 * c + (e & 1));
+                            if (key < klo[e >> 1] || key >= khi[e >> 1]) x = -INFINITY;
+                        }
+                        acc[t][e] = x;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], x);
+                    }
+                float alpha[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                    mx[r] = fmaxf(mx[r], M[r]);
+                    alpha[r] = mx[r] == M[r] ? 1.f : ex2(M[r] - mx[r]);   // M = -inf: 0
+                    M[r] = mx[r];
+                }
+                const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
+                float sum[2] = {0.f, 0.f};
+                uint32_t pa[4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float p0 = ex2(acc[t][0] - m0), p1 = ex2(acc[t][1] - m0);
+                    const float p2 = ex2(acc[t][2] - m1), p3 = ex2(acc[t][3] - m1);
+                    sum[0] += p0 + p1;
+                    sum[1] += p2 + p3;
+                    pa[2 * t] = pack_f16x2(p0, p1);
+                    pa[2 * t + 1] = pack_f16x2(p2, p3);
+                }
+                const float iv = 1.f / sc.y;
+                l[0] = fmaf(sum[0], iv, l[0] * alpha[0]);
+                l[1] = fmaf(sum[1], iv, l[1] * alpha[1]);
+                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                    for (int d = 0; d < HD / 8; ++d) {
+                        o[d][0] *= alpha[0];
+                        o[d][1] *= alpha[0];
+                        o[d][2] *= alpha[1];
+                        o[d][3] *= alpha[1];
+                    }
+                }
+                // V: matrices (keys 0-7 | 8-15 of the warp) x (16-byte chunks d, d + 1),
+                // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
+                // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
+                const int vrow = 16 * warp + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
+                // codes of keys that no row sees may be anything, NaN included: as zeros
+                const bool edge = key0 < w.lo || key0 + 16 > w.hi;
+                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+                if (edge) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int ka = key0 + 8 * t + key_of<HD>(2 * c), kb = key0 + 8 * t + key_of<HD>(2 * c + 1);
+                        keep[t] = (ka >= w.lo && ka < w.hi ? 0x0000ffffu : 0u) | (kb >= w.lo && kb < w.hi ? 0xffff0000u : 0u);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < HD / 16; d += 2) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
+                    if (edge) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) r[k] &= keep[k & 1];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t be[2] = {f16_of_codes(r[2 * k]), f16_of_codes(r[2 * k + 1])};
+                        const uint32_t bo[2] = {f16_of_codes(r[2 * k] >> 16), f16_of_codes(r[2 * k + 1] >> 16)};
+                        mma_f16_16816(o[2 * (d + k)], pa, be);
+                        mma_f16_16816(o[2 * (d + k) + 1], pa, bo);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st);
+        }
+
+        // ---- the four warps' keys of the tile, merged in warp order
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            if (c == 0) {
+                ml[(warp * KT + g + 8 * r) * 2] = M[r];
+                ml[(warp * KT + g + 8 * r) * 2 + 1] = l[r];
+            }
+            float* dst = red + (warp * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
+#pragma unroll
+            for (int d = 0; d < HD / 16; ++d)
+                *reinterpret_cast<float4*>(dst + 16 * d) =
+                    make_float4(o[2 * d][2 * r], o[2 * d + 1][2 * r], o[2 * d][2 * r + 1], o[2 * d + 1][2 * r + 1]);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int row = tid >> 3, col = (tid & 7) * 4;   // columns col + 32 k
+        const int pr = w.tile * KT + row;
+        const int qi = pr / a.group, hq = w.kh * a.group + pr % a.group;
+        const bool real = qi < q.n;
+        float fm = -INFINITY, fl = 0.f;
+        float4 fo[HD / 32];
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < KW; ++v) fm = fmaxf(fm, ml[(v * KT + row) * 2]);
+#pragma unroll
+        for (int v = 0; v < KW; ++v) {
+            const float f = fm == -INFINITY ? 0.f : ex2(ml[(v * KT + row) * 2] - fm);
+            fl = fmaf(ml[(v * KT + row) * 2 + 1], f, fl);
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(red + (v * KT + row) * red_ld<HD>() + col + 32 * k);
+                fo[k].x = fmaf(x.x, f, fo[k].x);
+                fo[k].y = fmaf(x.y, f, fo[k].y);
+                fo[k].z = fmaf(x.z, f, fo[k].z);
+                fo[k].w = fmaf(x.w, f, fo[k].w);
+            }
+        }
+        bool write = true;
+        if (q.splits > 1) {
+            // partial of this split; the last split to arrive folds them all,
+            // in split order
+            const long long slot0 = (long long)item - w.split;   // splits of a tile are neighbours
+            const long long tk = ((long long)q.r0 * a.group / KT + s + w.tile) * a.n_kv + w.kh;
+            const bool fits = slot0 + q.splits <= a.part_cap && tk < a.ticket_cap;   // by the plan's bounds
+            constexpr int PL = KT * (HD + 4);   // floats of a partial: outputs, then (max, sum) pairs
+            if (fits && real) {
+                float* dst = a.part + (slot0 + w.split) * PL;
+#pragma unroll
+                for (int k = 0; k < HD / 32; ++k)
+                    *reinterpret_cast<float4*>(dst + row * HD + col + 32 * k) = fo[k];
+                if ((tid & 7) == 0) *reinterpret_cast<float2*>(dst + KT * HD + row * 2) = make_float2(fm, fl);
+            }
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (tid == 0) flag[0] = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            write = flag[0] != 0;
+            if (write) {
+                __threadfence();
+                if (tid == 0) a.tickets[tk] = 0;
+                fm = -INFINITY;
+                fl = 0.f;
+#pragma unroll
+                for (int k = 0; k < HD / 32; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (real) {
+                    const float* src = a.part + slot0 * PL;
+                    for (int v = 0; v < q.splits; ++v)
+                        fm = fmaxf(fm, __ldcg(src + (size_t)v * PL + KT * HD + row * 2));
+                    for (int v = 0; v < q.splits; ++v) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src + (size_t)v * PL + KT * HD + row * 2));
+                        const float f = fm == -INFINITY ? 0.f : ex2(x.x - fm);
+                        fl = fmaf(x.y, f, fl);
+#pragma unroll
+                        for (int k = 0; k < HD / 32; ++k) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)v * PL + row * HD + col + 32 * k));
+                            fo[k].x = fmaf(y.x, f, fo[k].x);
+                            fo[k].y = fmaf(y.y, f, fo[k].y);
+                            fo[k].z = fmaf(y.z, f, fo[k].z);
+                            fo[k].w = fmaf(y.w, f, fo[k].w);
+                        }
+                    }
+                }
+            }
+        }
+        if (write && real) {
+            const float inv = fl == 0.f ? 0.f : 1.f / fl;   // a row that sees no key: zeros
+            T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k)
+                store_row4<T>(dst + col + 32 * k, fo[k].x * inv, fo[k].y * inv, fo[k].z * inv, fo[k].w * inv);
+            if (a.lse && (tid & 7) == 0)
+                a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
+        }
+        // a wait that ran out ends the CTA, all warps at the same item (err says so)
+        if (tid == 0) flag[2] = flag[1];
+        asm volatile("bar.sync 1, 128;" ::: "memory");   // the merge buffer is free again
+        if (flag[2]) break;
+    }
+}
+
+template <typename T, int HD>
+int launch_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+    const size_t smem = KvSmem<HD>::bytes(a.S);
+    const cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return (int)e;
+    const long long most = a.ticket_cap * a.split_cap;   // items there can be
+    const long long grid = most < 2LL * sms ? most : 2LL * sms;
+    return (int)launch_k(kv8_attn_kernel<T, HD>, dim3((unsigned)grid), dim3(KTHREADS), smem, s, k_map, v_map, a);
+}
+
+}  // namespace
+
+// Splits.  A tile's keys are cut into at most split_cap splits of whole
+// pages: as many as give every resident CTA two items if all sequences had
+// the same tiles.  It follows from the call's row, sequence and head counts
+// alone, so a sequence's results depend on its own rows and length, not on
+// what the other sequences hold.
+Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int max_pages, int sms) {
+    Kv8AttnPlan p;
+    const long long packed = (long long)rows * (n_q / n_kv);
+    const long long tiles = packed / KT + S;               // slots: floor(first packed row / KT) + sequence
+    long long usual = (packed + KT - 1) / KT;
+    if (usual < S) usual = S;
+    long long cap = (4LL * sms + usual * n_kv - 1) / (usual * n_kv);
+    if (cap > max_pages) cap = max_pages;
+    if (cap > 64) cap = 64;
+    if (cap < 1) cap = 1;
+    p.split_cap = (int)cap;
+    p.ticket_cap = tiles * n_kv;
+    p.part_cap = cap > 1 ? tiles * n_kv * cap : 0;
+    p.ticket_bytes = (size_t)((p.ticket_cap * 4 + 255) / 256 * 256);
+    p.bytes = p.ticket_bytes + (size_t)p.part_cap * KT * (head_dim + 4) * 4;
+    return p;
+}
+
+int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
+                         int head_dim, int sms, cudaStream_t s) {
+    if (a.dtype == 1)
+        return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(k_map, v_map, a, sms, s)
+                               : launch_t<__nv_bfloat16, 64>(k_map, v_map, a, sms, s);
+    return head_dim == 128 ? launch_t<__half, 128>(k_map, v_map, a, sms, s)
+                           : launch_t<__half, 64>(k_map, v_map, a, sms, s);
+}
+
+}  // namespace dfl

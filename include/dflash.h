@@ -66,7 +66,7 @@ enum {
     DFLASH_ERR_STATE = -7     /* call out of order (e.g. verify before prefill) */
 };
 
-enum { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_INT4G64 = 2 };
+enum { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_INT4G64 = 2, DFLASH_F16 = 3 };
 
 #define DFLASH_MAX_TAPS 8
 #define DFLASH_MAX_BLOCK 16
@@ -484,6 +484,172 @@ int dflash_linear_noalloc(const void* w, const void* x, int32_t n, int32_t k, fl
  */
 int dflash_linear_dense(const void* w, const void* x, const void* x_lo, int32_t m, int32_t n, int32_t k,
                         float* y, int32_t* err, dflash_stream_t stream);
+
+/* ---- 8-bit paged KV cache --------------------------------------------- */
+
+/*
+ * A cache whose memory follows what its sequences hold, at half the bytes of
+ * the contexts' fp16 caches: one pool of pages shared by all sequences.  A
+ * page is DFLASH_KV8_PAGE consecutive positions of one sequence: for each kv
+ * head that many rows of head_dim e4m3 codes for K and for V, and one fp32
+ * scale each (a power of two); a cached value is code * scale.  Buffers are
+ * caller-owned, one set per layer:
+ *   k_codes, v_codes  uint8 [n_pages][n_kv][DFLASH_KV8_PAGE][head_dim], 16-byte aligned
+ *   k_scale, v_scale  fp32  [n_pages][n_kv]
+ * head_dim 64 or 128; n_pages * n_kv below 2^25.
+ * A sequence's pages are listed in order in its row of a block table, int32
+ * [S][max_pages]; slot = page * DFLASH_KV8_PAGE + offset names one position
+ * of the pool.  The pages hold no counterpart in the source pages (there the
+ * draft cache is one persistent run, "[RFC] DFlash", "Requested changes" 3):
+ * they are this library's extension for many sequences of unlike lengths.
+ *
+ * A step of a serving loop: dflash_pages_plan, then per layer dflash_rope,
+ * dflash_kv8_append, dflash_kv8_attention; dflash_pages_trim takes rejected
+ * rows or finished sequences back.  All of it is enqueued work on device
+ * memory (graph-capturable; a captured step advances from its own outputs).
+ *
+ * err (append, attention): device int32[2], zero before the first call; a
+ * kernel that meets an impossible index writes {2, where} and skips the
+ * access, an expired bounded wait writes {1, site}; the first error stays
+ * until the caller clears it.
+ */
+#define DFLASH_KV8_PAGE 64
+
+typedef struct {
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int32_t n_pages, n_kv, head_dim, pad_;
+} dflash_kv8_cache;
+
+/*
+ * Pages and row maps for the next step: sequence s holds kv_len[s] positions
+ * and wants q_len[s] new rows (0 allowed).  Sequences are admitted in order
+ * while both the free pages and the rows last: s is admitted if its lengths
+ * are not negative, max_pages pages can hold kv_len + q_len, and the new
+ * pages (and rows) of the sequences up to s that pass these checks do not
+ * exceed n_free (and rows).  An admitted sequence's new pages are taken from
+ * the end of free_pages[0 .. n_free): the i-th page handed out in the call is
+ * free_pages[n_free - 1 - i].  Others get no rows and keep their length.
+ * Outputs: the new entries of table [S][max_pages]; row_start [S + 1], the
+ * rows before each sequence; positions [rows] and slots [rows] of each new
+ * row, -1 behind the last; kv_after [S] = kv_len + rows given; n_free_out.
+ * kv_after may be kv_len and n_free_out may be n_free (a step that advances
+ * its own state).  Errors: ARG, CUDA.
+ */
+int dflash_pages_plan(const int32_t* kv_len, const int32_t* q_len, int32_t S, const int32_t* free_pages,
+                      int32_t free_cap, const int32_t* n_free, int32_t* table, int32_t max_pages, int32_t rows,
+                      int32_t* row_start, int32_t* positions, int32_t* slots, int32_t* kv_after,
+                      int32_t* n_free_out, dflash_stream_t stream);
+
+/*
+ * Shortens sequences: kv_len[s] becomes new_len[s] where that is smaller
+ * (negative counts as 0), the pages no longer needed go back onto free_pages
+ * (n_free grows; free_cap entries at most) in sequence order, each
+ * sequence's last page first, and their table entries become -1.  Nothing is
+ * moved.  Errors: ARG, CUDA.
+ */
+int dflash_pages_trim(int32_t* kv_len, const int32_t* new_len, int32_t S, int32_t* free_pages, int32_t free_cap,
+                      int32_t* n_free, int32_t* table, int32_t max_pages, dflash_stream_t stream);
+
+/*
+ * Appends K and V rows (dtype F32, BF16 or F16; element strides between rows
+ * and heads, head_dim elements contiguous) at slots [rows]; a negative slot
+ * skips its row.  Rows with consecutive slots inside one page are a run.
+ * Per run and kv head, for K and V each: the page's scale becomes the
+ * smallest power of two 2^e, -100 <= e <= 119, with largest finite magnitude
+ * of the run's rows <= 448 * 2^e, but not less than the page's scale unless
+ * the run starts at the page's first position (which starts the page anew);
+ * if the scale grew, the codes before the run are re-rounded to it; the rows
+ * are stored as code = e4m3(x / scale), round to nearest even, saturating
+ * (infinities too; NaN stays NaN).  Positions behind the run are left as
+ * they were.  Runs that follow one another in one page (skipped rows between
+ * them, repeated slots) are done in row order.  Rows of one page stand
+ * together, as dflash_pages_plan writes them: where rows of another page
+ * stand between them, that page's codes are unspecified.  A slot outside the
+ * pool: err {2, row}, the row is skipped.
+ * rows at any alignment of their type; 16-byte aligned ones are faster.
+ * Errors: CONFIG, ARG, CUDA.
+ */
+int dflash_kv8_append(const dflash_kv8_cache* cache /*host*/, const void* k, int64_t k_row, int64_t k_head,
+                      const void* v, int64_t v_row, int64_t v_head, int32_t dtype, int32_t rows,
+                      const int32_t* slots, int32_t* err, dflash_stream_t stream);
+
+/*
+ * Attention of each sequence's rows over its cached positions:
+ * o = softmax(scale * q k^T + mask) v.  Rows row_start[s] .. row_start[s+1]-1
+ * of q are the last ones of sequence s's kv_len[s] positions (their own K
+ * and V are in the cache); rows in no sequence are neither read nor written.
+ *   causal 1: row at position p sees keys <= p, with window W > 0 the last W
+ *     of them (p - W < key);
+ *   causal 0: the rows see each other and everything cached (a masked draft
+ *     block), with W > 0 no key before first row - W (the drafter's window).
+ * A row that sees no key gets zeros (lse -inf).  q and out are BF16 or F16
+ * (the same), fp32 inside; lse (fp32 [rows][n_q], natural log, or NULL) is
+ * the log of each row's softmax sum.  n_q a multiple of n_kv, at most 16 per
+ * kv head; up to 4096 sequences; strides in elements, every row of every head
+ * 16-byte aligned.  A sequence's results depend on its own rows and cached
+ * positions and on the call's row, sequence and head counts, not on the
+ * other sequences.  Codes of positions no row sees do not matter.
+ * Workspace: dflash_kv8_workspace_bytes, zero-filled before its first use
+ * (completed calls leave its counters at zero); calls that share one must
+ * not overlap on the GPU; zero it again after err was set.  A length or page
+ * out of range: err {2, site}, that sequence (page) is left out.
+ * Errors: CONFIG, ARG, CUDA.
+ */
+typedef struct {
+    const void* q;              /* [rows][n_q][head_dim] by strides */
+    void* out;                  /* the same shape, its own strides */
+    float* lse;                 /* [rows][n_q] or NULL */
+    const int32_t* table;       /* [S][max_pages] */
+    const int32_t* kv_len;      /* [S] positions held, the rows included */
+    const int32_t* row_start;   /* [S + 1] */
+    int64_t q_row, q_head, out_row, out_head;
+    int32_t rows, n_q, S, max_pages, dtype, causal, window;
+    float scale;                /* above 0 */
+} dflash_kv8_query;
+
+size_t dflash_kv8_workspace_bytes(int32_t rows, int32_t S, int32_t n_q, int32_t n_kv, int32_t head_dim,
+                                  int32_t max_pages);
+int dflash_kv8_attention(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_query* q /*host*/,
+                         void* workspace, size_t workspace_bytes, int32_t* err, dflash_stream_t stream);
+
+/* ---- rotary positions -------------------------------------------------- */
+
+/*
+ * y = scale * R(position * f) x on the first rotary_dim dimensions of each
+ * head, the others copied.  Pairs: (i, i + rotary_dim/2), or (2i, 2i + 1)
+ * with interleaved 1.  Frequencies f_i = theta^(-2i / rotary_dim);
+ * scaling LINEAR: f / factor; PARTS: with r = original_len f / (2 pi) turns
+ * over the original context and g = clamp((r - alpha) / (beta - alpha), 0, 1),
+ * (1 - g) f / factor + g f.  The contexts' own rotation is theta, rotary_dim
+ * = head_dim, halves, no scaling.  Angles are exact at any int32 position:
+ * turns [rotary_dim / 2] holds f / (2 pi) as 64-bit fractions of a turn,
+ * made once by dflash_rope_turns.
+ */
+enum { DFLASH_ROPE_NONE = 0, DFLASH_ROPE_LINEAR = 1, DFLASH_ROPE_PARTS = 2 };
+
+typedef struct {
+    int32_t rotary_dim, interleaved, scaling, original_len;
+    double theta, factor, alpha, beta;
+    float scale;
+    int32_t pad_;
+} dflash_rope_config;
+
+/* One tensor of heads: x, out [rows][heads][head_dim] by element strides. */
+typedef struct {
+    const void* x;
+    void* out;              /* may be x (with x's strides); no other overlap */
+    int32_t heads, pad_;
+    int64_t x_row, x_head, out_row, out_head;
+} dflash_heads;
+
+int dflash_rope_turns(const dflash_rope_config* cfg /*host*/, uint64_t* turns, dflash_stream_t stream);
+/* Rotates the heads of a and, if given, b (q and k in one launch); dtype F32,
+ * BF16 or F16; positions [rows], a row with a negative one is left as it was
+ * (out not written).  Errors: CONFIG, ARG, CUDA. */
+int dflash_rope(const dflash_rope_config* cfg /*host*/, const uint64_t* turns, const int32_t* positions,
+                int32_t rows, int32_t head_dim, int32_t dtype, const dflash_heads* a /*host*/,
+                const dflash_heads* b /*host*/, dflash_stream_t stream);
 
 #ifdef __cplusplus
 }
