@@ -9,6 +9,9 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
+
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdflash.so")
@@ -143,14 +146,14 @@ def _load() -> C.CDLL:
         "dflash_batch_destroy": (None, [vp]),
         "dflash_pages_plan": (C.c_int, [vp, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]),
         "dflash_pages_trim": (C.c_int, [vp, vp, i32, vp, i32, vp, vp, i32, vp]),
-        "dflash_kv8_append": (C.c_int, [C.POINTER(dflash_kv8_cache), vp, i64, i64, vp, i64, i64, i32, i32,
+        "dflash_kv8_append": (C.c_int, [vp, vp, i64, i64, vp, i64, i64, i32, i32,
                                         vp, vp, vp]),
         "dflash_kv8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
-        "dflash_kv8_attention": (C.c_int, [C.POINTER(dflash_kv8_cache), C.POINTER(dflash_kv8_query), vp, sz,
+        "dflash_kv8_attention": (C.c_int, [vp, vp, vp, sz,
                                            vp, vp]),
         "dflash_rope_turns": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp]),
         "dflash_rope": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp, i32, i32, i32,
-                                  C.POINTER(dflash_heads), C.POINTER(dflash_heads), vp]),
+                                  vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -436,11 +439,40 @@ def dflash_batch_destroy(b) -> None:
 
 
 # ---- 8-bit paged KV cache and rotary positions
+#
+# These calls sit in a serving loop's every layer, where a few microseconds of
+# checks are as long as the kernels: the common case is checked by plain
+# comparisons, and only a call that fails one goes through the checks that
+# name the tensor at fault.
+
+_I32 = torch.int32
+_KINDS = {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
+_HALVES = (torch.bfloat16, torch.float16)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_CACHE = struct.Struct("4Q4i")        # dflash_kv8_cache
+_QUERY = struct.Struct("6Q4q7if")     # dflash_kv8_query
+_HEADS = struct.Struct("2Q2i4q")      # dflash_heads
+
+
+def _device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _raw(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _flat(tensors, dev: int, dtype=_I32) -> bool:
+    """Every tensor of dtype, contiguous, on device dev."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
 
 def _here(**tensors) -> None:
-    """Every tensor on the current CUDA device, whose current stream (or a
-    stream of which) the call is enqueued on."""
-    import torch
+    """Every tensor on the current CUDA device (the call is enqueued on one of
+    its streams)."""
     _on_gpu(**tensors)
     cur = torch.cuda.current_device()
     for name, t in tensors.items():
@@ -448,14 +480,8 @@ def _here(**tensors) -> None:
             raise DFlashError(DFLASH_ERR_ARG, f"{name}: on {t.device}, the current device is cuda:{cur}")
 
 
-def _kinds():
-    import torch
-    return {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
-
-
-def _heads(t, name: str, dtypes, shape) -> None:
+def _need_heads(t, name: str, dtypes, shape) -> None:
     """A [rows][heads][head_dim] tensor by strides: contiguous heads."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise DFlashError(DFLASH_ERR_ARG, f"{name}: a torch tensor is required")
     if t.dtype not in dtypes:
@@ -466,41 +492,53 @@ def _heads(t, name: str, dtypes, shape) -> None:
         raise DFlashError(DFLASH_ERR_ARG, f"{name}: the elements of a head must be contiguous")
 
 
-def _err2(err) -> None:
-    import torch
-    _need(err, "err", (torch.int32,), (2,))
+def _vectors(*tensors) -> bool:
+    return all(isinstance(t, torch.Tensor) for t in tensors)
 
 
 def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, positions, slots, kv_after,
                       n_free_out, stream=None):
     """Pages, row starts, positions and slots of the next step's rows (see
     include/dflash.h); rows = positions.numel().  int32 tensors throughout."""
-    import torch
-    i32 = (torch.int32,)
-    _need(table, "table", i32, (None, None))
-    S, max_pages = table.shape
-    for name, t in (("kv_len", kv_len), ("q_len", q_len), ("kv_after", kv_after)):
-        _need(t, name, i32, (S,))
-    _need(free_pages, "free_pages", i32, (None,))
-    _need(n_free, "n_free", i32, (1,))
-    _need(n_free_out, "n_free_out", i32, (1,))
-    _need(row_start, "row_start", i32, (S + 1,))
-    _need(positions, "positions", i32, (None,))
-    _need(slots, "slots", i32, (positions.shape[0],))
-    _here(kv_len=kv_len, q_len=q_len, free_pages=free_pages, n_free=n_free, table=table,
-          row_start=row_start, positions=positions, slots=slots, kv_after=kv_after,
-          n_free_out=n_free_out)
-    check(lib.dflash_pages_plan(_ptr(kv_len), _ptr(q_len), S, _ptr(free_pages), free_pages.shape[0],
-                                _ptr(n_free), _ptr(table), max_pages, positions.shape[0],
-                                _ptr(row_start), _ptr(positions), _ptr(slots), _ptr(kv_after),
-                                _ptr(n_free_out), _stream(stream)))
+    named = (kv_len, q_len, kv_after, free_pages, n_free, n_free_out, row_start, positions, slots, table)
+    dev = _device() if _vectors(*named) and table.is_cuda and table.dim() == 2 else -1
+    if dev >= 0:
+        S, max_pages = table.shape
+        rows = positions.numel()
+        one = (S,)
+        if not (_flat(named, dev) and kv_len.shape == one and q_len.shape == one and kv_after.shape == one and
+                free_pages.dim() == 1 and n_free.shape == (1,) and n_free_out.shape == (1,) and
+                row_start.shape == (S + 1,) and positions.dim() == 1 and slots.shape == (rows,)):
+            dev = -1
+    if dev < 0:
+        i32 = (_I32,)
+        _need(table, "table", i32, (None, None))
+        S, max_pages = table.shape
+        for name, t in (("kv_len", kv_len), ("q_len", q_len), ("kv_after", kv_after)):
+            _need(t, name, i32, (S,))
+        _need(free_pages, "free_pages", i32, (None,))
+        _need(n_free, "n_free", i32, (1,))
+        _need(n_free_out, "n_free_out", i32, (1,))
+        _need(row_start, "row_start", i32, (S + 1,))
+        _need(positions, "positions", i32, (None,))
+        rows = positions.shape[0]
+        _need(slots, "slots", i32, (rows,))
+        _here(kv_len=kv_len, q_len=q_len, free_pages=free_pages, n_free=n_free, table=table,
+              row_start=row_start, positions=positions, slots=slots, kv_after=kv_after,
+              n_free_out=n_free_out)
+        dev = _device()
+    rc = lib.dflash_pages_plan(kv_len.data_ptr(), q_len.data_ptr(), S, free_pages.data_ptr(),
+                               free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages, rows,
+                               row_start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                               kv_after.data_ptr(), n_free_out.data_ptr(), _raw(stream, dev))
+    if rc:
+        check(rc)
 
 
 def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
     """kv_len[s] = min(kv_len[s], new_len[s]); pages no longer needed go back
     onto free_pages."""
-    import torch
-    i32 = (torch.int32,)
+    i32 = (_I32,)
     _need(table, "table", i32, (None, None))
     S, max_pages = table.shape
     _need(kv_len, "kv_len", i32, (S,))
@@ -508,35 +546,57 @@ def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
     _need(free_pages, "free_pages", i32, (None,))
     _need(n_free, "n_free", i32, (1,))
     _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
-    check(lib.dflash_pages_trim(_ptr(kv_len), _ptr(new_len), S, _ptr(free_pages), free_pages.shape[0],
-                                _ptr(n_free), _ptr(table), max_pages, _stream(stream)))
+    check(lib.dflash_pages_trim(kv_len.data_ptr(), new_len.data_ptr(), S, free_pages.data_ptr(),
+                                free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages,
+                                _raw(stream, _device())))
 
 
-def _kv8_cache(k_codes, v_codes, k_scale, v_scale) -> dflash_kv8_cache:
-    import torch
-    code = (torch.uint8, torch.float8_e4m3fn)
-    _need(k_codes, "k_codes", code, (None, None, KV8_PAGE, None))
+def _cache_ok(k_codes, v_codes, k_scale, v_scale, dev: int) -> bool:
+    shape = k_codes.shape
+    return (len(shape) == 4 and shape[2] == KV8_PAGE and v_codes.shape == shape and
+            k_scale.shape == shape[:2] and v_scale.shape == shape[:2] and k_codes.dtype in _CODES and
+            v_codes.dtype in _CODES and k_codes.get_device() == dev and v_codes.get_device() == dev and
+            k_codes.is_contiguous() and v_codes.is_contiguous() and
+            _flat((k_scale, v_scale), dev, torch.float32))
+
+
+def _need_cache(k_codes, v_codes, k_scale, v_scale) -> None:
+    _need(k_codes, "k_codes", _CODES, (None, None, KV8_PAGE, None))
     n_pages, n_kv, _, hd = k_codes.shape
-    _need(v_codes, "v_codes", code, (n_pages, n_kv, KV8_PAGE, hd))
+    _need(v_codes, "v_codes", _CODES, (n_pages, n_kv, KV8_PAGE, hd))
     _need(k_scale, "k_scale", (torch.float32,), (n_pages, n_kv))
     _need(v_scale, "v_scale", (torch.float32,), (n_pages, n_kv))
-    return dflash_kv8_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), n_pages, n_kv, hd, 0)
 
 
 def dflash_kv8_append(k, v, slots, k_codes, v_codes, k_scale, v_scale, err, stream=None):
     """Quantise rows k, v [rows][n_kv][head_dim] (fp32, bf16 or f16, strided
     rows and heads) into the pool at slots [rows]; negative slots skip."""
-    import torch
-    cache = _kv8_cache(k_codes, v_codes, k_scale, v_scale)
-    _need(slots, "slots", (torch.int32,), (None,))
-    rows, kinds = slots.shape[0], _kinds()
-    _heads(k, "k", kinds, (rows, cache.n_kv, cache.head_dim))
-    _heads(v, "v", (k.dtype,), (rows, cache.n_kv, cache.head_dim))
-    _err2(err)
-    _here(k=k, v=v, slots=slots, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, err=err)
-    check(lib.dflash_kv8_append(C.byref(cache), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-                                v.stride(1), kinds[k.dtype], rows, _ptr(slots), _ptr(err),
-                                _stream(stream)))
+    dev = _device() if _vectors(k, v, slots, k_codes, v_codes, k_scale, v_scale, err) and k.is_cuda else -1
+    if dev >= 0 and not (_cache_ok(k_codes, v_codes, k_scale, v_scale, dev) and _flat((slots, err), dev) and
+                         slots.dim() == 1 and err.shape == (2,) and k.dtype in _KINDS and v.dtype is k.dtype and
+                         k.shape == (slots.numel(), k_codes.shape[1], k_codes.shape[3]) and
+                         v.shape == k.shape and k.stride(2) == 1 and v.stride(2) == 1 and
+                         k.get_device() == dev and v.get_device() == dev):
+        dev = -1
+    if dev < 0:
+        _need_cache(k_codes, v_codes, k_scale, v_scale)
+        _need(slots, "slots", (_I32,), (None,))
+        shape = (slots.shape[0], k_codes.shape[1], k_codes.shape[3])
+        _need_heads(k, "k", _KINDS, shape)
+        _need_heads(v, "v", (k.dtype,), shape)
+        _need(err, "err", (_I32,), (2,))
+        _here(k=k, v=v, slots=slots, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale,
+              err=err)
+        dev = _device()
+    n_pages, n_kv, _, hd = k_codes.shape
+    cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        n_pages, n_kv, hd, 0)
+    ks, vs = k.stride(), v.stride()
+    rc = lib.dflash_kv8_append(cache, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                               _KINDS[k.dtype], slots.shape[0], slots.data_ptr(), err.data_ptr(),
+                               _raw(stream, dev))
+    if rc:
+        check(rc)
 
 
 def dflash_kv8_workspace_bytes(rows: int, S: int, n_q: int, n_kv: int, head_dim: int, max_pages: int) -> int:
@@ -548,29 +608,48 @@ def dflash_kv8_attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, r
     """out = softmax(scale q k^T + mask) v of each sequence's rows over its
     cached positions; q, out [rows][n_q][head_dim] bf16 or f16 by strides,
     lse fp32 [rows][n_q]; scale None: head_dim ** -0.5."""
-    import torch
-    cache = _kv8_cache(k_codes, v_codes, k_scale, v_scale)
-    _heads(q, "q", (torch.bfloat16, torch.float16), (None, None, cache.head_dim))
+    dev = _device() if _vectors(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, row_start, out,
+                                workspace, err) and q.is_cuda else -1
+    if dev >= 0:
+        shape = q.shape
+        if not (len(shape) == 3 and table.dim() == 2 and q.dtype in _HALVES and out.dtype is q.dtype and
+                out.shape == shape and _cache_ok(k_codes, v_codes, k_scale, v_scale, dev) and
+                shape[2] == k_codes.shape[3] and _flat((table, kv_len, row_start, err), dev) and
+                kv_len.shape == table.shape[:1] and row_start.shape == (table.shape[0] + 1,) and
+                err.shape == (2,) and q.get_device() == dev and out.get_device() == dev and
+                workspace.get_device() == dev and workspace.is_contiguous() and q.stride(2) == 1 and
+                out.stride(2) == 1 and
+                (lse is None or (_vectors(lse) and lse.shape == shape[:2] and
+                                 _flat((lse,), dev, torch.float32)))):
+            dev = -1
+    if dev < 0:
+        _need_cache(k_codes, v_codes, k_scale, v_scale)
+        _need_heads(q, "q", _HALVES, (None, None, k_codes.shape[3]))
+        _need_heads(out, "out", (q.dtype,), tuple(q.shape))
+        i32 = (_I32,)
+        _need(table, "table", i32, (None, None))
+        _need(kv_len, "kv_len", i32, (table.shape[0],))
+        _need(row_start, "row_start", i32, (table.shape[0] + 1,))
+        if lse is not None:
+            _need(lse, "lse", (torch.float32,), tuple(q.shape[:2]))
+        _need(workspace, "workspace", None, None)
+        _need(err, "err", i32, (2,))
+        _here(q=q, out=out, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
+              kv_len=kv_len, row_start=row_start, workspace=workspace, err=err, lse=lse)
+        dev = _device()
     rows, n_q, hd = q.shape
-    _heads(out, "out", (q.dtype,), (rows, n_q, hd))
-    i32 = (torch.int32,)
-    _need(table, "table", i32, (None, None))
     S, max_pages = table.shape
-    _need(kv_len, "kv_len", i32, (S,))
-    _need(row_start, "row_start", i32, (S + 1,))
-    if lse is not None:
-        _need(lse, "lse", (torch.float32,), (rows, n_q))
-    _need(workspace, "workspace", None, None)
-    _err2(err)
-    _here(q=q, out=out, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
-          kv_len=kv_len, row_start=row_start, workspace=workspace, err=err, lse=lse)
-    args = dflash_kv8_query(_ptr(q), _ptr(out), _ptr(lse), _ptr(table), _ptr(kv_len), _ptr(row_start),
-                            q.stride(0), q.stride(1), out.stride(0), out.stride(1), rows, n_q, S,
-                            max_pages, _kinds()[q.dtype], 1 if causal else 0, window,
-                            hd ** -0.5 if scale is None else scale)
-    check(lib.dflash_kv8_attention(C.byref(cache), C.byref(args), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(err),
-                                   _stream(stream)))
+    cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        k_codes.shape[0], k_codes.shape[1], hd, 0)
+    qs, os_ = q.stride(), out.stride()
+    args = _QUERY.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
+                       kv_len.data_ptr(), row_start.data_ptr(), qs[0], qs[1], os_[0], os_[1], rows, n_q, S,
+                       max_pages, _KINDS[q.dtype], 1 if causal else 0, window,
+                       hd ** -0.5 if scale is None else scale)
+    rc = lib.dflash_kv8_attention(cache, args, workspace.data_ptr(), workspace.nbytes, err.data_ptr(),
+                                  _raw(stream, dev))
+    if rc:
+        check(rc)
 
 
 def rope_config(rotary_dim: int, theta: float = 1e6, interleaved: bool = False, scaling: str = "none",
@@ -585,33 +664,51 @@ def rope_config(rotary_dim: int, theta: float = 1e6, interleaved: bool = False, 
 
 def dflash_rope_turns(cfg: dflash_rope_config, turns, stream=None):
     """The frequency table of cfg: int64 [rotary_dim / 2], 2^-64 turns a position."""
-    import torch
     _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
     _here(turns=turns)
-    check(lib.dflash_rope_turns(C.byref(cfg), _ptr(turns), _stream(stream)))
+    check(lib.dflash_rope_turns(C.byref(cfg), turns.data_ptr(), _raw(stream, _device())))
 
 
 def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2=None, stream=None):
     """Rotate x (and x2) [rows][heads][head_dim] into out (out2) at positions
     [rows]; fp32, bf16 or f16, strided rows and heads, out may be x."""
-    import torch
-    kinds = _kinds()
-    _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
-    _need(positions, "positions", (torch.int32,), (None,))
-    rows = positions.shape[0]
-    _heads(x, "x", kinds, (rows, None, None))
-    hd = x.shape[2]
-    _heads(out, "out", (x.dtype,), tuple(x.shape))
     if (x2 is None) != (out2 is None):
         raise DFlashError(DFLASH_ERR_ARG, "x2 and out2 go together")
+    both = (x, out) if x2 is None else (x, out, x2, out2)
+    dev = _device() if _vectors(turns, positions, *both) and x.is_cuda and x.dim() == 3 else -1
+    if dev >= 0:
+        rows, hd = positions.numel(), x.shape[2]
+        kind = x.dtype
+        fine = (kind in _KINDS and positions.dim() == 1 and x.shape[0] == rows and out.shape == x.shape and
+                turns.shape == (cfg.rotary_dim // 2,) and _flat((positions,), dev) and
+                _flat((turns,), dev, torch.int64) and
+                (x2 is None or (x2.dim() == 3 and x2.shape[0] == rows and x2.shape[2] == hd and
+                                out2.shape == x2.shape)))
+        if fine:
+            for t in both:
+                if t.dtype is not kind or t.get_device() != dev or t.stride(2) != 1:
+                    fine = False
+        if not fine:
+            dev = -1
+    if dev < 0:
+        _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
+        _need(positions, "positions", (_I32,), (None,))
+        rows = positions.shape[0]
+        _need_heads(x, "x", _KINDS, (rows, None, None))
+        hd = x.shape[2]
+        _need_heads(out, "out", (x.dtype,), tuple(x.shape))
+        if x2 is not None:
+            _need_heads(x2, "x2", (x.dtype,), (rows, None, hd))
+            _need_heads(out2, "out2", (x.dtype,), tuple(x2.shape))
+        _here(turns=turns, positions=positions, x=x, out=out, x2=x2, out2=out2)
+        dev = _device()
+    xs, os_ = x.stride(), out.stride()
+    first = _HEADS.pack(x.data_ptr(), out.data_ptr(), x.shape[1], 0, xs[0], xs[1], os_[0], os_[1])
     second = None
     if x2 is not None:
-        _heads(x2, "x2", (x.dtype,), (rows, None, hd))
-        _heads(out2, "out2", (x.dtype,), tuple(x2.shape))
-        second = C.byref(dflash_heads(_ptr(x2), _ptr(out2), x2.shape[1], 0, x2.stride(0), x2.stride(1),
-                                      out2.stride(0), out2.stride(1)))
-    _here(turns=turns, positions=positions, x=x, out=out, x2=x2, out2=out2)
-    first = dflash_heads(_ptr(x), _ptr(out), x.shape[1], 0, x.stride(0), x.stride(1), out.stride(0),
-                         out.stride(1))
-    check(lib.dflash_rope(C.byref(cfg), _ptr(turns), _ptr(positions), rows, hd, kinds[x.dtype],
-                          C.byref(first), second, _stream(stream)))
+        xs, os_ = x2.stride(), out2.stride()
+        second = _HEADS.pack(x2.data_ptr(), out2.data_ptr(), x2.shape[1], 0, xs[0], xs[1], os_[0], os_[1])
+    rc = lib.dflash_rope(C.byref(cfg), turns.data_ptr(), positions.data_ptr(), rows, hd, _KINDS[x.dtype],
+                         first, second, _raw(stream, dev))
+    if rc:
+        check(rc)

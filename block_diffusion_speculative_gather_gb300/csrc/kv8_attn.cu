@@ -17,6 +17,10 @@
 // that lose low bits.  e4m3 codes are exact in f16.  P is rounded to f16
 // (half a step: 2^-11 of the weight); scores, sums and outputs are fp32.
 
+#include <mutex>
+#include <utility>
+#include <vector>
+
 #include "attention_dev.cuh"
 #include "gemm.cuh"
 #include "kv8.cuh"
@@ -601,10 +605,31 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     }
 }
 
+// The largest dynamic shared memory, allowed once per kernel and device.
+cudaError_t allow_smem(const void* kern) {
+    static std::mutex mu;
+    static std::vector<std::pair<const void*, int>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const std::pair<const void*, int> key(kern, dev);
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto& d : done)
+        if (d == key) return cudaSuccess;
+    int most = 0;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+    if (e == cudaSuccess) done.push_back(key);
+    return e;
+}
+
 template <typename T, int HD>
 int launch_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int sms, cudaStream_t s) {
     const size_t smem = KvSmem<HD>::bytes(a.S);
-    const cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_attn_kernel<T, HD>));
     if (e != cudaSuccess) return (int)e;
     const long long most = a.ticket_cap * a.split_cap;   // items there can be
     const long long grid = most < 2LL * sms ? most : 2LL * sms;

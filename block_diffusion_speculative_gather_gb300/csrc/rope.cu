@@ -4,8 +4,7 @@
 // Angles.  f / (2 pi) is kept as a 64-bit fraction of a turn, so pos * f
 // modulo a whole turn is one integer multiply that wraps: exact to
 // pos * 2^-65 turns at any position, without the 64-bit floating point this
-// part has little of.  The top 32 bits become half-turns in [-1, 1) for
-// sincospif.
+// part has little of.
 //
 // A warp takes one row and some of its heads; a lane keeps its pairs' cosines
 // and sines in registers for all heads it visits.  Bound by the rows' bytes
@@ -44,12 +43,18 @@ __global__ void rope_turns_kernel(RopeTurnsArgs a) {
     a.turns[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;
 }
 
+// The turn is split exactly into a quarter and a remainder of at most an
+// eighth of a turn, so the fp32 angle is off by 2^-26 of it or less and
+// sincospif sees no large argument.
 __device__ __forceinline__ void angle_of(unsigned long long turn, int pos, float scale, float* c, float* s) {
     const unsigned long long t = turn * (unsigned long long)(unsigned)pos;
-    const int hi = (int)((t + 0x80000000ull) >> 32);   // the nearest 2^-32 of a turn
-    sincospif((float)hi * 0x1p-31f, s, c);
-    *c *= scale;
-    *s *= scale;
+    const unsigned q = (unsigned)((t + (1ull << 61)) >> 62);            // nearest quarter
+    const long long r = (long long)(t - ((unsigned long long)q << 62)); // 2^-64 turns, |r| <= 2^61
+    float sn, cs;
+    sincospif((float)r * 0x1p-63f, &sn, &cs);
+    const float a = (q & 1) ? -sn : cs, b = (q & 1) ? cs : sn;
+    *c = ((q & 2) ? -a : a) * scale;
+    *s = ((q & 2) ? -b : b) * scale;
 }
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec {

@@ -5,7 +5,7 @@ Tolerances.
 * Page plans, codes and scales: equal (scales are powers of two, so every
   value the append rounds is exact in fp32).
 * Rotary positions: the angle is off by at most 2^-26 turns * 2 pi (the
-  top 32 bits of the turn, then its fp32 rounding) plus the frequency
+  turn's fp32 rounding) plus the frequency
   table's 2^-53 relative, sine and cosine by 2 ulp of fp32 at most, products
   and sums by 3 roundings: |x|max * scale * (2 pi 2^-25 + 8 * 2^-24) for the
   pair, then half a step of the type.
