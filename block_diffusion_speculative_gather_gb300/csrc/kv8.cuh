@@ -88,6 +88,7 @@ struct Kv8AttnArgs {
     int causal, window;
     float scale_log2;           // softmax scale * log2(e)
     int split_cap;              // most splits of a tile's keys
+    int tile;                   // packed (row, q head) rows of an item
     float* part;                // [part_cap] partial tiles
     long long part_cap;
     int* tickets;               // [tile slots][n_kv], zero between calls
@@ -95,14 +96,21 @@ struct Kv8AttnArgs {
     int* err;
 };
 
-// Host: the split limit, workspace floats and tickets of an attention call.
+// Host: the kernel, split limit, workspace floats and tickets of an attention call.
+enum : int { KV8_MMA = 0, KV8_TC_KEYS = 1, KV8_TC_ROWS = 2 };
 struct Kv8AttnPlan {
+    int form;                   // KV8_MMA, KV8_TC_KEYS or KV8_TC_ROWS
+    int tile;
     int split_cap;
     long long part_cap, ticket_cap;
     size_t ticket_bytes, bytes;
 };
 Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int max_pages, int sms);
 int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
-                         int head_dim, int sms, cudaStream_t s);
+                         int form, int head_dim, int sms, cudaStream_t s);
+int launch_kv8_attention_tc(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
+                            int form, int head_dim, int sms, cudaStream_t s);
+// The largest dynamic shared memory, allowed once per kernel and device.
+cudaError_t allow_smem(const void* kern);
 
 }  // namespace dfl

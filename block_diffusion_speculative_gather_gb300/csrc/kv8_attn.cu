@@ -18,23 +18,20 @@
 // (half a step: 2^-11 of the weight); scores, sums and outputs are fp32.
 
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "attention_dev.cuh"
-#include "gemm.cuh"
-#include "kv8.cuh"
+#include "kv8_attn_dev.cuh"
 
 namespace dfl {
 namespace {
 
 using adev::ldsm_x4_trans;
+using namespace kv8;
 
 constexpr int KT = 16;              // packed rows of a tile (the M side of the MMAs)
 constexpr int KW = 4;               // consumer warps; each takes 16 of a page's 64 keys
 constexpr int KSTAGES = 4;          // pages in flight of a CTA
 constexpr int KTHREADS = 32 * (KW + 1);
-constexpr int SITE_KV8_FULL = 301, SITE_KV8_EMPTY = 302, SITE_KV8_PAGE = 303, SITE_KV8_LEN = 304;
 
 template <int HD> constexpr int tile_bytes() { return KV8_PAGE * HD; }
 template <int HD> constexpr int red_ld() { return HD + 16; }   // row pitch of the merge buffer (floats)
@@ -46,165 +43,9 @@ template <int HD> struct KvSmem {
     static constexpr int scales = ml + KW * KT * 2 * 4;      // [stages] (k, v)
     static constexpr int bars = scales + KSTAGES * 8;        // full, empty
     static constexpr int flag = bars + KSTAGES * 16;
-    static constexpr int cum = flag + 16;                    // [S + 1] items before each sequence
-    static size_t bytes(int S) { return 1024 + cum + (size_t)(S + 1) * 4; }
+    static constexpr int cum = flag + 16;                    // items before each group of sequences
+    static constexpr size_t bytes = 1024 + cum + (MAX_GROUPS + 1) * 4;
 };
-
-__device__ __forceinline__ void report(int* err, int code, int info) {
-    if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
-}
-
-// One sequence of the call: its rows, keys and how they are cut.
-struct Seq {
-    int r0, n;          // rows r0 .. r0 + n - 1
-    int kv, first;      // cached tokens; position of the first row (may be negative: rows without keys)
-    int page_lo, page_hi;
-    int tiles, splits, len;   // row tiles, splits of the pages, pages of a split
-};
-
-__device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
-    Seq q;
-    const int r0 = a.row_start[s], r1 = a.row_start[s + 1];
-    q.r0 = r0;
-    q.n = r1 - r0;
-    int kv = a.kv_len[s];
-    const long long cap = (long long)a.max_pages * KV8_PAGE;
-    if (r0 < 0 || r1 < r0 || r1 > a.rows || kv < 0 || kv > cap) {
-        report(a.err, DERR_INDEX, SITE_KV8_LEN);   // such a sequence is skipped
-        q.n = 0;
-        q.r0 = 0;
-        kv = 0;
-    }
-    q.kv = kv;
-    q.first = kv - q.n;
-    int lo = 0;
-    if (a.window > 0) {
-        lo = a.causal ? q.first + 1 - a.window : q.first - a.window;
-        if (lo < 0) lo = 0;
-    }
-    q.page_lo = lo / KV8_PAGE;
-    q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
-    const int pages = q.page_hi > q.page_lo ? q.page_hi - q.page_lo : 0;
-    q.tiles = (int)(((long long)q.n * a.group + KT - 1) / KT);
-    q.len = (pages + a.split_cap - 1) / a.split_cap;
-    if (q.len < 1) q.len = 1;
-    q.splits = (pages + q.len - 1) / q.len;
-    if (q.splits < 1) q.splits = 1;
-    return q;
-}
-
-// One unit of work: a row tile, a kv head and a split of the tile's pages.
-struct Item {
-    int s, tile, kh, split;
-    int p0, p1;         // pages [p0, p1)
-    int lo, hi;         // keys that some row of the tile sees: [lo, hi)
-    int in_lo, in_hi;   // keys that every row of the tile sees: [in_lo, in_hi)
-};
-
-__device__ __forceinline__ void row_keys(const Kv8AttnArgs& a, const Seq& q, int i, int* lo, int* hi) {
-    const int pos = q.first + i;
-    *lo = 0;
-    if (a.causal) {
-        *hi = pos + 1;
-        if (a.window > 0) *lo = pos + 1 - a.window;
-    } else {
-        *hi = q.kv;
-        if (a.window > 0) *lo = q.first - a.window;
-    }
-    if (*lo < 0) *lo = 0;
-    if (*hi < 0) *hi = 0;
-}
-
-__device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, const Seq& q, int s, int idx) {
-    Item it;
-    it.s = s;
-    it.split = idx % q.splits;
-    const int rest = idx / q.splits;
-    it.kh = rest % a.n_kv;
-    it.tile = rest / a.n_kv;
-    const int i0 = it.tile * KT / a.group;
-    int i1 = (it.tile * KT + KT - 1) / a.group;
-    if (i1 > q.n - 1) i1 = q.n - 1;
-    int lo0, hi0, lo1, hi1;
-    row_keys(a, q, i0, &lo0, &hi0);
-    row_keys(a, q, i1, &lo1, &hi1);
-    it.lo = lo0;
-    it.hi = hi1;
-    it.in_lo = lo1;
-    it.in_hi = hi0;
-    int p0 = q.page_lo + it.split * q.len, p1 = p0 + q.len;
-    if (p1 > q.page_hi) p1 = q.page_hi;
-    const int tp0 = it.lo / KV8_PAGE, tp1 = (it.hi + KV8_PAGE - 1) / KV8_PAGE;
-    it.p0 = p0 > tp0 ? p0 : tp0;
-    it.p1 = p1 < tp1 ? p1 : tp1;
-    if (it.p1 < it.p0) it.p1 = it.p0;
-    return it;
-}
-
-// Items before each sequence, into shared memory, by the whole CTA.
-__device__ void count_items(const Kv8AttnArgs& a, int* cum) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int wsum[KW + 1];
-    const int per = (a.S + KTHREADS - 1) / KTHREADS;
-    int mine = 0;
-    for (int k = 0; k < per; ++k) {
-        const int s = tid * per + k;
-        if (s < a.S) {
-            const Seq q = seq_of(a, s);
-            mine += q.tiles * a.n_kv * q.splits;
-        }
-    }
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += wsum[w];
-    for (int k = 0; k < per; ++k) {
-        const int s = tid * per + k;
-        if (s < a.S) {
-            cum[s] = at;
-            const Seq q = seq_of(a, s);
-            at += q.tiles * a.n_kv * q.splits;
-            if (s == a.S - 1) cum[a.S] = at;
-        }
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ int find_item(const int* cum, int S, int item) {
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= item) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// Two e4m3 codes (the low 16 bits) to a pair of f16, exactly.
-__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
-    return h;
-}
-
-// Byte offset of 16-byte chunk c of key row r in a tile that TMA wrote with
-// the 128-byte (head_dim 128) or 64-byte (head_dim 64) swizzle.
-template <int HD>
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-    return HD == 128 ? swz128(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
 
 // Key of MMA column n (0..7) inside a group of 8: for 128-byte rows columns
 // 2j, 2j + 1 are keys j, j + 4, whose swizzled chunks lie in different bank
@@ -254,31 +95,37 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         flag[1] = 0;
     }
     pdl_wait();
-    count_items(a, cum);   // ends with a barrier
-    const int total = cum[a.S];
+    count_items<KTHREADS>(a, cum);   // ends with a barrier
+    const int total = total_items(a, cum);
 
     if (warp == KW) {
         // ---- producer: pages of every item of this CTA, in order.  The lanes
-        // look up 32 pages and their scales at a time; lane 0 issues.
+        // look up 32 pages and their scales at a time, the next 32 while lane 0
+        // issues these.
         unsigned it = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const int s = find_item(cum, a.S, item);
-            const Seq q = seq_of(a, s);
-            const Item w = item_of(a, q, s, item - cum[s]);
-            for (int b = w.p0; b < w.p1 && ok; b += 32) {
-                int page = -1;
-                float ks = -1.f, vs = 1.f;
-                if (b + lane < w.p1) {
-                    page = a.table[(size_t)s * a.max_pages + b + lane];
-                    if (page < 0 || page >= a.n_pages) {
-                        report(a.err, DERR_INDEX, SITE_KV8_PAGE);   // its keys are left out
-                        page = -1;
-                    } else {
-                        ks = a.k_scale[(size_t)page * a.n_kv + w.kh];
-                        vs = a.v_scale[(size_t)page * a.n_kv + w.kh];
-                    }
+            Seq q;
+            const Item w = find_item(a, cum, item, &q);
+            auto look = [&](int b, int* page, float* ks, float* vs) {
+                *page = -1;
+                *ks = -1.f;
+                *vs = 1.f;
+                if (b + lane >= w.p1) return;
+                const int pg = a.table[(size_t)w.s * a.max_pages + b + lane];
+                if (pg < 0 || pg >= a.n_pages) {
+                    report(a.err, DERR_INDEX, SITE_PAGE);   // its keys are left out
+                    return;
                 }
+                *page = pg;
+                *ks = a.k_scale[(size_t)pg * a.n_kv + w.kh];
+                *vs = a.v_scale[(size_t)pg * a.n_kv + w.kh];
+            };
+            int page, next_page;
+            float ks, vs, next_ks, next_vs;
+            look(w.p0, &page, &ks, &vs);
+            for (int b = w.p0; b < w.p1 && ok; b += 32) {
+                look(b + 32, &next_page, &next_ks, &next_vs);
                 const int m = w.p1 - b < 32 ? w.p1 - b : 32;
                 for (int j = 0; j < m; ++j) {
                     const int pg = __shfl_sync(0xffffffffu, page, j);
@@ -287,7 +134,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                     bool issued = true;
                     if (lane == 0) {
                         if (it >= KSTAGES && !mbar_wait_bounded(empty + st, (it / KSTAGES - 1) & 1)) {
-                            report(a.err, DERR_TIMEOUT, SITE_KV8_EMPTY);
+                            report(a.err, DERR_TIMEOUT, SITE_EMPTY);
                             flag[1] = 1;
                             issued = false;
                         } else {
@@ -311,6 +158,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                     ok = __shfl_sync(0xffffffffu, flag[1], 0) == 0;
                     if (!ok) break;
                 }
+                page = next_page;
+                ks = next_ks;
+                vs = next_vs;
             }
         }
         // no copy of this CTA is in flight when it ends
@@ -325,9 +175,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     const int g = lane >> 2, c = lane & 3;
     unsigned it = 0;
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const int s = find_item(cum, a.S, item);
-        const Seq q = seq_of(a, s);
-        const Item w = item_of(a, q, s, item - cum[s]);
+        Seq q;
+        const Item w = find_item(a, cum, item, &q);
 
         // q of rows g, g + 8 as A fragments: k step (h, j) of 16 covers the
         // dims 64 h + 16 c + 4 j .. + 3 of every lane c of a quad, so a
@@ -367,10 +216,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            uint32_t e = __float_as_uint(top) >> 23;       // biased exponent
-            e = e < 1 ? 1 : (e > 253 ? 253 : e);
-            const float inv = top > 0.f ? __uint_as_float((254 - e) << 23) : 1.f;
-            fr[r] = (top > 0.f ? __uint_as_float(e << 23) : 1.f) * a.scale_log2;
+            float inv, back;
+            row_factor(top, &inv, &back);
+            fr[r] = back * a.scale_log2;
 #pragma unroll
             for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
@@ -391,7 +239,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             const int st = it % KSTAGES;
             if (flag[1]) break;
             if (!mbar_wait_bounded(full + st, (it / KSTAGES) & 1)) {
-                report(a.err, DERR_TIMEOUT, SITE_KV8_FULL);
+                report(a.err, DERR_TIMEOUT, SITE_FULL);
                 flag[1] = 1;
             }
             if (flag[1]) break;
@@ -547,7 +395,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             // partial of this split; the last split to arrive folds them all,
             // in split order
             const long long slot0 = (long long)item - w.split;   // splits of a tile are neighbours
-            const long long tk = ((long long)q.r0 * a.group / KT + s + w.tile) * a.n_kv + w.kh;
+            const long long tk = ((long long)q.r0 * a.group / KT + w.s + w.tile) * a.n_kv + w.kh;
             const bool fits = slot0 + q.splits <= a.part_cap && tk < a.ticket_cap;   // by the plan's bounds
             constexpr int PL = KT * (HD + 4);   // floats of a partial: outputs, then (max, sum) pairs
             if (fits && real) {
@@ -605,30 +453,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     }
 }
 
-// The largest dynamic shared memory, allowed once per kernel and device.
-cudaError_t allow_smem(const void* kern) {
-    static std::mutex mu;
-    static std::vector<std::pair<const void*, int>> done;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const std::pair<const void*, int> key(kern, dev);
-    std::lock_guard<std::mutex> lock(mu);
-    for (const auto& d : done)
-        if (d == key) return cudaSuccess;
-    int most = 0;
-    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    cudaFuncAttributes fa;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
-    if (e == cudaSuccess) done.push_back(key);
-    return e;
-}
-
 template <typename T, int HD>
 int launch_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int sms, cudaStream_t s) {
-    const size_t smem = KvSmem<HD>::bytes(a.S);
+    const size_t smem = KvSmem<HD>::bytes;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_attn_kernel<T, HD>));
     if (e != cudaSuccess) return (int)e;
     const long long most = a.ticket_cap * a.split_cap;   // items there can be
@@ -638,31 +465,66 @@ int launch_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnAr
 
 }  // namespace
 
+// The largest dynamic shared memory, allowed once per kernel and device.
+cudaError_t allow_smem(const void* kern) {
+    static std::mutex mu;
+    constexpr int MAX = 128;
+    static const void* kerns[MAX];
+    static int devs[MAX], n = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (kerns[i] == kern && devs[i] == dev) return cudaSuccess;
+    int most = 0;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+    if (e == cudaSuccess && n < MAX) {
+        kerns[n] = kern;
+        devs[n++] = dev;
+    }
+    return e;
+}
+
+// The form of a call, by its packed rows (rows x q heads of a kv head) per
+// sequence: the mma.sync kernel's 16-row tiles for few, one 128-row tensor
+// core tile whose two halves take alternate keys up to 128, two 128-row
+// tiles over the same keys above.
+//
 // Splits.  A tile's keys are cut into at most split_cap splits of whole
-// pages: as many as give every resident CTA two items if all sequences had
-// the same tiles.  It follows from the call's row, sequence and head counts
-// alone, so a sequence's results depend on its own rows and length, not on
-// what the other sequences hold.
+// pages: as many as give every resident CTA `waves` items if all sequences
+// had the same tiles.  Both follow from the call's row, sequence and head
+// counts alone, so a sequence's results depend on its own rows and length,
+// not on what the other sequences hold.
 Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int max_pages, int sms) {
     Kv8AttnPlan p;
     const long long packed = (long long)rows * (n_q / n_kv);
-    const long long tiles = packed / KT + S;               // slots: floor(first packed row / KT) + sequence
-    long long usual = (packed + KT - 1) / KT;
+    const long long each = (packed + S - 1) / S;
+    p.form = each <= 16 ? KV8_MMA : (each <= 128 ? KV8_TC_KEYS : KV8_TC_ROWS);
+    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_KEYS ? 128 : 256);
+    const long long resident = p.form == KV8_MMA ? 2LL * sms : sms;
+    const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
+    long long usual = (packed + p.tile - 1) / p.tile;
     if (usual < S) usual = S;
-    long long cap = (4LL * sms + usual * n_kv - 1) / (usual * n_kv);
+    long long cap = (2 * resident + usual * n_kv - 1) / (usual * n_kv);
     if (cap > max_pages) cap = max_pages;
     if (cap > 64) cap = 64;
     if (cap < 1) cap = 1;
     p.split_cap = (int)cap;
-    p.ticket_cap = tiles * n_kv;
+    p.ticket_cap = tiles * n_kv * (p.form == KV8_MMA ? 1 : 8);
     p.part_cap = cap > 1 ? tiles * n_kv * cap : 0;
     p.ticket_bytes = (size_t)((p.ticket_cap * 4 + 255) / 256 * 256);
-    p.bytes = p.ticket_bytes + (size_t)p.part_cap * KT * (head_dim + 4) * 4;
+    p.bytes = p.ticket_bytes + (size_t)p.part_cap * p.tile * (head_dim + 4) * 4;
     return p;
 }
 
 int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
-                         int head_dim, int sms, cudaStream_t s) {
+                         int form, int head_dim, int sms, cudaStream_t s) {
+    if (form != KV8_MMA) return launch_kv8_attention_tc(k_map, v_map, a, form, head_dim, sms, s);
     if (a.dtype == 1)
         return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(k_map, v_map, a, sms, s)
                                : launch_t<__nv_bfloat16, 64>(k_map, v_map, a, sms, s);

@@ -1,0 +1,206 @@
+// Work items of the attention over the 8-bit paged cache and the small
+// device helpers its two kernels share.
+#pragma once
+
+#include "gemm.cuh"
+#include "kv8.cuh"
+
+namespace dfl {
+namespace kv8 {
+
+// Sites of err words.
+constexpr int SITE_FULL = 301, SITE_EMPTY = 302, SITE_PAGE = 303, SITE_LEN = 304;
+
+__device__ __forceinline__ void report(int* err, int code, int info) {
+    if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
+}
+
+// One sequence of the call: its rows, keys and how they are cut.
+struct Seq {
+    int r0, n;          // rows r0 .. r0 + n - 1
+    int kv, first;      // cached tokens; position of the first row (may be negative: rows without keys)
+    int page_lo, page_hi;
+    int tiles, splits, len;   // row tiles, splits of the pages, pages of a split
+};
+
+__device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
+    Seq q;
+    const int r0 = a.row_start[s], r1 = a.row_start[s + 1];
+    q.r0 = r0;
+    q.n = r1 - r0;
+    int kv = a.kv_len[s];
+    const long long cap = (long long)a.max_pages * KV8_PAGE;
+    if (r0 < 0 || r1 < r0 || r1 > a.rows || kv < 0 || kv > cap) {
+        report(a.err, DERR_INDEX, SITE_LEN);   // such a sequence is skipped
+        q.n = 0;
+        q.r0 = 0;
+        kv = 0;
+    }
+    q.kv = kv;
+    q.first = kv - q.n;
+    int lo = 0;
+    if (a.window > 0) {
+        lo = a.causal ? q.first + 1 - a.window : q.first - a.window;
+        if (lo < 0) lo = 0;
+    }
+    q.page_lo = lo / KV8_PAGE;
+    q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
+    const int pages = q.page_hi > q.page_lo ? q.page_hi - q.page_lo : 0;
+    q.tiles = (int)(((long long)q.n * a.group + a.tile - 1) / a.tile);
+    q.len = (pages + a.split_cap - 1) / a.split_cap;
+    if (q.len < 1) q.len = 1;
+    q.splits = (pages + q.len - 1) / q.len;
+    if (q.splits < 1) q.splits = 1;
+    return q;
+}
+
+// One unit of work: a row tile, a kv head and a split of the tile's pages.
+struct Item {
+    int s, tile, kh, split;
+    int p0, p1;         // pages [p0, p1)
+    int lo, hi;         // keys that some row of the tile sees: [lo, hi)
+    int in_lo, in_hi;   // keys that every row of the tile sees: [in_lo, in_hi)
+};
+
+__device__ __forceinline__ void row_keys(const Kv8AttnArgs& a, const Seq& q, int i, int* lo, int* hi) {
+    const int pos = q.first + i;
+    *lo = 0;
+    if (a.causal) {
+        *hi = pos + 1;
+        if (a.window > 0) *lo = pos + 1 - a.window;
+    } else {
+        *hi = q.kv;
+        if (a.window > 0) *lo = q.first - a.window;
+    }
+    if (*lo < 0) *lo = 0;
+    if (*hi < 0) *hi = 0;
+}
+
+__device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, const Seq& q, int s, int idx) {
+    Item it;
+    it.s = s;
+    it.split = idx % q.splits;
+    const int rest = idx / q.splits;
+    it.kh = rest % a.n_kv;
+    // under the causal mask the last rows have the most keys: they go first
+    it.tile = q.tiles - 1 - rest / a.n_kv;
+    const int i0 = it.tile * a.tile / a.group;
+    int i1 = (it.tile * a.tile + a.tile - 1) / a.group;
+    if (i1 > q.n - 1) i1 = q.n - 1;
+    int lo0, hi0, lo1, hi1;
+    row_keys(a, q, i0, &lo0, &hi0);
+    row_keys(a, q, i1, &lo1, &hi1);
+    it.lo = lo0;
+    it.hi = hi1;
+    it.in_lo = lo1;
+    it.in_hi = hi0;
+    int p0 = q.page_lo + it.split * q.len, p1 = p0 + q.len;
+    if (p1 > q.page_hi) p1 = q.page_hi;
+    const int tp0 = it.lo / KV8_PAGE, tp1 = (it.hi + KV8_PAGE - 1) / KV8_PAGE;
+    it.p0 = p0 > tp0 ? p0 : tp0;
+    it.p1 = p1 < tp1 ? p1 : tp1;
+    if (it.p1 < it.p0) it.p1 = it.p0;
+    return it;
+}
+
+// Items before each group of `per` consecutive sequences (1 up to MAX_GROUPS
+// sequences), into shared memory, by the whole CTA.
+constexpr int MAX_GROUPS = 256;
+
+__host__ __device__ constexpr int seqs_per_group(int S) { return (S + MAX_GROUPS - 1) / MAX_GROUPS; }
+
+template <int THREADS>
+__device__ void count_items(const Kv8AttnArgs& a, int* cum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int wsum[THREADS / 32];
+    const int per = seqs_per_group(a.S), groups = (a.S + per - 1) / per;
+    const int mine_n = (groups + THREADS - 1) / THREADS;
+    int mine = 0;
+    for (int k = 0; k < mine_n; ++k) {
+        const int gr = tid * mine_n + k;
+        int n = 0;
+        for (int s = gr * per; gr < groups && s < gr * per + per && s < a.S; ++s) {
+            const Seq q = seq_of(a, s);
+            n += q.tiles * a.n_kv * q.splits;
+        }
+        if (gr < groups) cum[gr] = n;
+        mine += n;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    for (int k = 0; k < mine_n; ++k) {
+        const int gr = tid * mine_n + k;
+        if (gr < groups) {
+            const int n = cum[gr];
+            cum[gr] = at;
+            at += n;
+            if (gr == groups - 1) cum[groups] = at;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int total_items(const Kv8AttnArgs& a, const int* cum) {
+    const int per = seqs_per_group(a.S);
+    return cum[(a.S + per - 1) / per];
+}
+
+// Item `item`: its sequence, that sequence's shape, and the item itself.
+__device__ __forceinline__ Item find_item(const Kv8AttnArgs& a, const int* cum, int item, Seq* q) {
+    const int per = seqs_per_group(a.S);
+    int lo = 0, hi = (a.S + per - 1) / per - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= item) lo = mid;
+        else hi = mid - 1;
+    }
+    int idx = item - cum[lo], s = lo * per;
+    *q = seq_of(a, s);
+    for (; s + 1 < a.S; ++s) {
+        const int n = q->tiles * a.n_kv * q->splits;
+        if (idx < n) break;
+        idx -= n;
+        *q = seq_of(a, s + 1);
+    }
+    return item_of(a, *q, s, idx);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two e4m3 codes (the low 16 bits) to a pair of f16, exactly.
+__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+
+// Byte offset of 16-byte chunk c of key row r in a tile that TMA wrote with
+// the 128-byte (head_dim 128) or 64-byte (head_dim 64) swizzle.
+template <int HD>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return HD == 128 ? swz128(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// A row of q's power-of-two factor: `inv` brings its largest finite element
+// into [1, 2), `back` undoes it.
+__device__ __forceinline__ void row_factor(float top, float* inv, float* back) {
+    uint32_t e = __float_as_uint(top) >> 23;       // biased exponent
+    e = e < 1 ? 1 : (e > 253 ? 253 : e);
+    *inv = top > 0.f ? __uint_as_float((254 - e) << 23) : 1.f;
+    *back = top > 0.f ? __uint_as_float(e << 23) : 1.f;
+}
+
+}  // namespace kv8
+}  // namespace dfl

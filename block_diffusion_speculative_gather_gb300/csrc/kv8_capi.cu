@@ -250,13 +250,14 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     a.window = q->window;
     a.scale_log2 = q->scale * 1.4426950408889634f;
     a.split_cap = plan.split_cap;
+    a.tile = plan.tile;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.tickets = reinterpret_cast<int*>(ws);
     a.ticket_cap = plan.ticket_cap;
     a.part = reinterpret_cast<float*>(ws + plan.ticket_bytes);
     a.part_cap = plan.part_cap;
     a.err = err;
-    return launched(launch_kv8_attention(k_map, v_map, a, hd, sms, reinterpret_cast<cudaStream_t>(stream)),
+    return launched(launch_kv8_attention(k_map, v_map, a, plan.form, hd, sms, reinterpret_cast<cudaStream_t>(stream)),
                     "cache attention");
 }
 
