@@ -13,6 +13,7 @@
 namespace dfl {
 
 constexpr int KV8_PAGE = 64;
+constexpr size_t KV8_QUEUE_BYTES = 256;   // of an attention workspace, then its tickets, then partials
 
 struct PagesPlanArgs {
     const int* kv_len;
@@ -88,9 +89,11 @@ struct Kv8AttnArgs {
     int causal, window;
     float scale_log2;           // softmax scale * log2(e)
     int split_cap;              // most splits of a tile's keys
+    uint8_t caps[32];           // splits at most of a sequence with 2^b .. 2^(b+1) - 1 pages to read
     int tile;                   // packed (row, q head) rows of an item
     float* part;                // [part_cap] partial tiles
     long long part_cap;
+    int* queue;                 // [next item, CTAs done], zero between calls
     int* tickets;               // [tile slots][n_kv], zero between calls
     long long ticket_cap;
     int* err;
@@ -102,6 +105,7 @@ struct Kv8AttnPlan {
     int form;                   // KV8_MMA, KV8_TC_KEYS or KV8_TC_ROWS
     int tile;
     int split_cap;
+    uint8_t caps[32];
     long long part_cap, ticket_cap;
     size_t ticket_bytes, bytes;
 };

@@ -29,20 +29,22 @@ using adev::ldsm_x4_trans;
 using namespace kv8;
 
 constexpr int KT = 16;              // packed rows of a tile (the M side of the MMAs)
-constexpr int KW = 4;               // consumer warps; each takes 16 of a page's 64 keys
-constexpr int KSTAGES = 4;          // pages in flight of a CTA
-constexpr int KTHREADS = 32 * (KW + 1);
+constexpr int KW = 8;               // consumer warps; each takes whole pages, every eighth
+constexpr int KC = 32 * KW;         // consumer threads
+constexpr int KTHREADS = KC + 32;
+template <int HD> constexpr int stages() { return HD == 128 ? 10 : 20; }   // pages in flight: 160 KB
 
 template <int HD> constexpr int tile_bytes() { return KV8_PAGE * HD; }
 template <int HD> constexpr int red_ld() { return HD + 16; }   // row pitch of the merge buffer (floats)
 
 template <int HD> struct KvSmem {
     static constexpr int ring = 0;
-    static constexpr int red = ring + KSTAGES * 2 * tile_bytes<HD>();
-    static constexpr int ml = red + KW * KT * red_ld<HD>() * 4;
-    static constexpr int scales = ml + KW * KT * 2 * 4;      // [stages] (k, v)
-    static constexpr int bars = scales + KSTAGES * 8;        // full, empty
-    static constexpr int flag = bars + KSTAGES * 16;
+    static constexpr int red = ring + stages<HD>() * 2 * tile_bytes<HD>();
+    static constexpr int ml = red + KW / 2 * KT * red_ld<HD>() * 4;    // half of the warps at a time
+    static constexpr int scales = ml + KW / 2 * KT * 2 * 4;  // [stages] (k, v)
+    static constexpr int bars = scales + stages<HD>() * 8;   // full, empty
+    static constexpr int items = bars + stages<HD>() * 16;   // item ring: full, empty, values
+    static constexpr int flag = items + 2 * 16 + 16;
     static constexpr int cum = flag + 16;                    // items before each group of sequences
     static constexpr size_t bytes = 1024 + cum + (MAX_GROUPS + 1) * 4;
 };
@@ -67,11 +69,11 @@ __device__ __forceinline__ void store_row4<__half>(__half* p, float a, float b, 
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(KTHREADS, 2)
+__global__ void __launch_bounds__(KTHREADS, 1)
 kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const Kv8AttnArgs a) {
     using S_ = KvSmem<HD>;
-    constexpr int TB = tile_bytes<HD>();
+    constexpr int TB = tile_bytes<HD>(), KSTAGES = stages<HD>();
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     float* red = reinterpret_cast<float*>(sm + S_::red);
@@ -79,7 +81,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     float2* scales = reinterpret_cast<float2*>(sm + S_::scales);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S_::bars);
     uint64_t* empty = full + KSTAGES;
-    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] the same, as of the item's end
+    uint64_t* i_full = reinterpret_cast<uint64_t*>(sm + S_::items);   // [2] items on their way to the consumers
+    uint64_t* i_empty = i_full + 2;
+    volatile int* i_val = reinterpret_cast<volatile int*>(i_empty + 2);
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] the next item
     int* cum = reinterpret_cast<int*>(sm + S_::cum);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -89,7 +94,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         tma_prefetch_desc(&v_map);
         for (int i = 0; i < KSTAGES; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, KW);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(i_full + i, 1);
+            mbar_init(i_empty + i, 1);
         }
         fence_mbar_init();
         flag[1] = 0;
@@ -104,9 +113,23 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // issues these.
         unsigned it = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        int item = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
+        for (unsigned k = 0; item >= 0 && ok; ++k) {
             Seq q;
             const Item w = find_item(a, cum, item, &q);
+            // the next item, for the consumers and for after this one's pages
+            int next = 0;
+            if (lane == 0) {
+                next = next_item(a, total);
+                if (k >= 2 && !mbar_wait_bounded(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
+                    report(a.err, DERR_TIMEOUT, SITE_EMPTY);
+                    flag[1] = 1;
+                } else {
+                    i_val[k & 1] = next;
+                    mbar_arrive(i_full + (k & 1));
+                }
+            }
+            next = __shfl_sync(0xffffffffu, next, 0);
             auto look = [&](int b, int* page, float* ks, float* vs) {
                 *page = -1;
                 *ks = -1.f;
@@ -162,6 +185,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 ks = next_ks;
                 vs = next_vs;
             }
+            item = next;
         }
         // no copy of this CTA is in flight when it ends
         if (lane == 0) {
@@ -173,8 +197,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
 
     // ---- consumers
     const int g = lane >> 2, c = lane & 3;
-    unsigned it = 0;
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    unsigned base = 0;   // pages of the items before
+    int item = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
+    for (unsigned n_items = 0; item >= 0; ++n_items) {
         Seq q;
         const Item w = find_item(a, cum, item, &q);
 
@@ -235,50 +260,51 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
 
-        for (int p = w.p0; p < w.p1; ++p, ++it) {
+        for (int p = w.p0 + warp; p < w.p1; p += KW) {
+            const unsigned it = base + (p - w.p0);
             const int st = it % KSTAGES;
             if (flag[1]) break;
-            if (!mbar_wait_bounded(full + st, (it / KSTAGES) & 1)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + st, (it / KSTAGES) & 1))) {
                 report(a.err, DERR_TIMEOUT, SITE_FULL);
                 flag[1] = 1;
+                break;
             }
-            if (flag[1]) break;
             const float2 sc = scales[st];
             const uint8_t* kt = sm + S_::ring + st * 2 * TB;
             const uint8_t* vt = kt + TB;
-            const int key0 = p * KV8_PAGE + 16 * warp;   // this warp's first key
-            if (sc.x >= 0.f && sc.y > 0.f && key0 < w.hi && key0 + 16 > w.lo) {
-                float acc[2][4];
+            const int key0 = p * KV8_PAGE;
+            if (sc.x >= 0.f && sc.y > 0.f) {
+                float s[8][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
-                for (int h = 0; h < HD / 64; ++h)
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint4 kk = lds128(kt + tile_off<HD>(16 * warp + 8 * t + key_of<HD>(g), 4 * h + c));
+                    for (int h = 0; h < HD / 64; ++h) {
+                        const uint4 kk = lds128(kt + tile_off<HD>(8 * t + key_of<HD>(g), 4 * h + c));
                         const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t b[2] = {f16_of_codes(kw[j]), f16_of_codes(kw[j] >> 16)};
-                            mma_f16_16816(acc[t], qa[4 * h + j], b);
+                            mma_f16_16816(s[t], qa[4 * h + j], b);
                         }
                     }
                 const float ev = log2f(sc.y);
-                const bool whole = key0 >= w.in_lo && key0 + 16 <= w.in_hi;
+                const bool whole = key0 >= w.in_lo && key0 + KV8_PAGE <= w.in_hi;
                 const float f0 = fr[0] * sc.x, f1 = fr[1] * sc.x;
                 float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(acc[t][e], e < 2 ? f0 : f1, ev);
+                        float x = fmaf(s[t][e], e < 2 ? f0 : f1, ev);
                         if (!whole) {
                             const int key = key0 + 8 * t + key_of<HD>(2 * c + (e & 1));
                             if (key < klo[e >> 1] || key >= khi[e >> 1]) x = -INFINITY;
                         }
-                        acc[t][e] = x;
+                        s[t][e] = x;
                         mx[e >> 1] = fmaxf(mx[e >> 1], x);
                     }
                 float alpha[2];
@@ -292,15 +318,15 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 }
                 const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
                 float sum[2] = {0.f, 0.f};
-                uint32_t pa[4];
+                uint32_t pa[4][4];      // P of the four 16-key steps, as A fragments
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float p0 = ex2(acc[t][0] - m0), p1 = ex2(acc[t][1] - m0);
-                    const float p2 = ex2(acc[t][2] - m1), p3 = ex2(acc[t][3] - m1);
+                for (int t = 0; t < 8; ++t) {
+                    const float p0 = ex2(s[t][0] - m0), p1 = ex2(s[t][1] - m0);
+                    const float p2 = ex2(s[t][2] - m1), p3 = ex2(s[t][3] - m1);
                     sum[0] += p0 + p1;
                     sum[1] += p2 + p3;
-                    pa[2 * t] = pack_f16x2(p0, p1);
-                    pa[2 * t + 1] = pack_f16x2(p2, p3);
+                    pa[t >> 1][2 * (t & 1)] = pack_f16x2(p0, p1);
+                    pa[t >> 1][2 * (t & 1) + 1] = pack_f16x2(p2, p3);
                 }
                 const float iv = 1.f / sc.y;
                 l[0] = fmaf(sum[0], iv, l[0] * alpha[0]);
@@ -314,76 +340,106 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                         o[d][3] *= alpha[1];
                     }
                 }
-                // V: matrices (keys 0-7 | 8-15 of the warp) x (16-byte chunks d, d + 1),
-                // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
-                // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
-                const int vrow = 16 * warp + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
                 // codes of keys that no row sees may be anything, NaN included: as zeros
-                const bool edge = key0 < w.lo || key0 + 16 > w.hi;
-                uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                if (edge) {
+                const bool edge = key0 < w.lo || key0 + KV8_PAGE > w.hi;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int ka = key0 + 8 * t + key_of<HD>(2 * c), kb = key0 + 8 * t + key_of<HD>(2 * c + 1);
-                        keep[t] = (ka >= w.lo && ka < w.hi ? 0x0000ffffu : 0u) | (kb >= w.lo && kb < w.hi ? 0xffff0000u : 0u);
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < HD / 16; d += 2) {
-                    uint32_t r[4];
-                    ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
+                for (int k = 0; k < 4; ++k) {
+                    // V: matrices (keys 0-7 | 8-15 of the step) x (16-byte chunks d, d + 1),
+                    // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
+                    // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
+                    const int vrow = 16 * k + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
+                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
                     if (edge) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) r[k] &= keep[k & 1];
+                        for (int t = 0; t < 2; ++t) {
+                            const int ka = key0 + 16 * k + 8 * t + key_of<HD>(2 * c), kb = key0 + 16 * k + 8 * t + key_of<HD>(2 * c + 1);
+                            keep[t] = (ka >= w.lo && ka < w.hi ? 0x0000ffffu : 0u) | (kb >= w.lo && kb < w.hi ? 0xffff0000u : 0u);
+                        }
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+                    for (int d = 0; d < HD / 16; d += 2) {
+                        uint32_t r[4];
+                        ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t be[2] = {f16_of_codes(r[2 * k]), f16_of_codes(r[2 * k + 1])};
-                        const uint32_t bo[2] = {f16_of_codes(r[2 * k] >> 16), f16_of_codes(r[2 * k + 1] >> 16)};
-                        mma_f16_16816(o[2 * (d + k)], pa, be);
-                        mma_f16_16816(o[2 * (d + k) + 1], pa, bo);
+                        for (int x = 0; x < 4; ++x) r[x] = __byte_perm(edge ? r[x] & keep[x & 1] : r[x], 0, 0x3120);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t be[2] = {f16_of_codes(r[2 * x]), f16_of_codes(r[2 * x + 1])};
+                            const uint32_t bo[2] = {f16_of_codes(r[2 * x] >> 16), f16_of_codes(r[2 * x + 1] >> 16)};
+                            mma_f16_16816(o[2 * (d + x)], pa[k], be);
+                            mma_f16_16816(o[2 * (d + x) + 1], pa[k], bo);
+                        }
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + st);
         }
+        base += w.p1 - w.p0;
 
-        // ---- the four warps' keys of the tile, merged in warp order
+        // ---- the warps' pages merged: the upper half into the lower half's
+        // registers, then the lower half row by row, in warp order
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (c == 0) {
-                ml[(warp * KT + g + 8 * r) * 2] = M[r];
-                ml[(warp * KT + g + 8 * r) * 2 + 1] = l[r];
-            }
-            float* dst = red + (warp * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
-#pragma unroll
-            for (int d = 0; d < HD / 16; ++d)
-                *reinterpret_cast<float4*>(dst + 16 * d) =
-                    make_float4(o[2 * d][2 * r], o[2 * d + 1][2 * r], o[2 * d][2 * r + 1], o[2 * d + 1][2 * r + 1]);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const int row = tid >> 3, col = (tid & 7) * 4;   // columns col + 32 k
+        constexpr int HW = KW / 2;
+        auto put = [&](int slot) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (c == 0) *reinterpret_cast<float2*>(ml + (slot * KT + g + 8 * r) * 2) = make_float2(M[r], l[r]);
+                float* dst = red + (slot * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
+#pragma unroll
+                for (int d = 0; d < HD / 16; ++d)
+                    *reinterpret_cast<float4*>(dst + 16 * d) =
+                        make_float4(o[2 * d][2 * r], o[2 * d + 1][2 * r], o[2 * d][2 * r + 1], o[2 * d + 1][2 * r + 1]);
+            }
+        };
+        if (w.p1 - w.p0 > HW) {
+            if (warp >= HW) put(warp - HW);
+            asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
+            if (warp < HW) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 b = *reinterpret_cast<const float2*>(ml + (warp * KT + g + 8 * r) * 2);
+                    const float m = fmaxf(M[r], b.x);
+                    const float fa = M[r] == -INFINITY ? 0.f : ex2(M[r] - m), fb = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+                    l[r] = l[r] * fa + b.y * fb;
+                    M[r] = m;
+                    const float* src = red + (warp * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
+#pragma unroll
+                    for (int d = 0; d < HD / 16; ++d) {
+                        const float4 x = *reinterpret_cast<const float4*>(src + 16 * d);
+                        o[2 * d][2 * r] = fmaf(x.x, fb, o[2 * d][2 * r] * fa);
+                        o[2 * d + 1][2 * r] = fmaf(x.y, fb, o[2 * d + 1][2 * r] * fa);
+                        o[2 * d][2 * r + 1] = fmaf(x.z, fb, o[2 * d][2 * r + 1] * fa);
+                        o[2 * d + 1][2 * r + 1] = fmaf(x.w, fb, o[2 * d + 1][2 * r + 1] * fa);
+                    }
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
+        }
+        if (warp < HW) put(warp);
+        asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
+        constexpr int NF = HD / 64;                       // float4s of a thread
+        const int row = tid >> 4, col = (tid & 15) * 4;   // columns col + 64 k
         const int pr = w.tile * KT + row;
         const int qi = pr / a.group, hq = w.kh * a.group + pr % a.group;
         const bool real = qi < q.n;
         float fm = -INFINITY, fl = 0.f;
-        float4 fo[HD / 32];
+        float4 fo[NF];
 #pragma unroll
-        for (int k = 0; k < HD / 32; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < NF; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < KW; ++v) fm = fmaxf(fm, ml[(v * KT + row) * 2]);
+        for (int v = 0; v < HW; ++v) fm = fmaxf(fm, ml[(v * KT + row) * 2]);
 #pragma unroll
-        for (int v = 0; v < KW; ++v) {
+        for (int v = 0; v < HW; ++v) {
             const float f = fm == -INFINITY ? 0.f : ex2(ml[(v * KT + row) * 2] - fm);
             fl = fmaf(ml[(v * KT + row) * 2 + 1], f, fl);
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k) {
-                const float4 x = *reinterpret_cast<const float4*>(red + (v * KT + row) * red_ld<HD>() + col + 32 * k);
+            for (int k = 0; k < NF; ++k) {
+                const float4 x = *reinterpret_cast<const float4*>(red + (v * KT + row) * red_ld<HD>() + col + 64 * k);
                 fo[k].x = fmaf(x.x, f, fo[k].x);
                 fo[k].y = fmaf(x.y, f, fo[k].y);
                 fo[k].z = fmaf(x.z, f, fo[k].z);
@@ -401,14 +457,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             if (fits && real) {
                 float* dst = a.part + (slot0 + w.split) * PL;
 #pragma unroll
-                for (int k = 0; k < HD / 32; ++k)
-                    *reinterpret_cast<float4*>(dst + row * HD + col + 32 * k) = fo[k];
-                if ((tid & 7) == 0) *reinterpret_cast<float2*>(dst + KT * HD + row * 2) = make_float2(fm, fl);
+                for (int k = 0; k < NF; ++k)
+                    *reinterpret_cast<float4*>(dst + row * HD + col + 64 * k) = fo[k];
+                if ((tid & 15) == 0) *reinterpret_cast<float2*>(dst + KT * HD + row * 2) = make_float2(fm, fl);
             }
             __threadfence();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
             if (tid == 0) flag[0] = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
             write = flag[0] != 0;
             if (write) {
                 __threadfence();
@@ -416,22 +472,25 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 fm = -INFINITY;
                 fl = 0.f;
 #pragma unroll
-                for (int k = 0; k < HD / 32; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < NF; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (real) {
                     const float* src = a.part + slot0 * PL;
                     for (int v = 0; v < q.splits; ++v)
                         fm = fmaxf(fm, __ldcg(src + (size_t)v * PL + KT * HD + row * 2));
+#pragma unroll 4
                     for (int v = 0; v < q.splits; ++v) {
                         const float2 x = __ldcg(reinterpret_cast<const float2*>(src + (size_t)v * PL + KT * HD + row * 2));
+                        float4 y[NF];
+#pragma unroll
+                        for (int k = 0; k < NF; ++k) y[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)v * PL + row * HD + col + 64 * k));
                         const float f = fm == -INFINITY ? 0.f : ex2(x.x - fm);
                         fl = fmaf(x.y, f, fl);
 #pragma unroll
-                        for (int k = 0; k < HD / 32; ++k) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)v * PL + row * HD + col + 32 * k));
-                            fo[k].x = fmaf(y.x, f, fo[k].x);
-                            fo[k].y = fmaf(y.y, f, fo[k].y);
-                            fo[k].z = fmaf(y.z, f, fo[k].z);
-                            fo[k].w = fmaf(y.w, f, fo[k].w);
+                        for (int k = 0; k < NF; ++k) {
+                            fo[k].x = fmaf(y[k].x, f, fo[k].x);
+                            fo[k].y = fmaf(y[k].y, f, fo[k].y);
+                            fo[k].z = fmaf(y[k].z, f, fo[k].z);
+                            fo[k].w = fmaf(y[k].w, f, fo[k].w);
                         }
                     }
                 }
@@ -441,15 +500,27 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             const float inv = fl == 0.f ? 0.f : 1.f / fl;   // a row that sees no key: zeros
             T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k)
-                store_row4<T>(dst + col + 32 * k, fo[k].x * inv, fo[k].y * inv, fo[k].z * inv, fo[k].w * inv);
-            if (a.lse && (tid & 7) == 0)
+            for (int k = 0; k < NF; ++k)
+                store_row4<T>(dst + col + 64 * k, fo[k].x * inv, fo[k].y * inv, fo[k].z * inv, fo[k].w * inv);
+            if (a.lse && (tid & 15) == 0)
                 a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
         }
-        // a wait that ran out ends the CTA, all warps at the same item (err says so)
-        if (tid == 0) flag[2] = flag[1];
-        asm volatile("bar.sync 1, 128;" ::: "memory");   // the merge buffer is free again
-        if (flag[2]) break;
+        // the next item, the same for all warps; a wait that ran out ends the CTA
+        // (err says so)
+        if (warp == 0) {
+            const int k = n_items & 1;
+            const bool got = !flag[1] && mbar_wait_bounded(i_full + k, (n_items >> 1) & 1);
+            if (lane == 0) {
+                if (!got && !flag[1]) {
+                    report(a.err, DERR_TIMEOUT, SITE_FULL);
+                    flag[1] = 1;
+                }
+                flag[2] = got ? i_val[k] : -1;
+                if (got) mbar_arrive(i_empty + k);
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");   // the merge buffer is free again
+        item = flag[2];
     }
 }
 
@@ -459,7 +530,7 @@ int launch_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnAr
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_attn_kernel<T, HD>));
     if (e != cudaSuccess) return (int)e;
     const long long most = a.ticket_cap * a.split_cap;   // items there can be
-    const long long grid = most < 2LL * sms ? most : 2LL * sms;
+    const long long grid = most < sms ? most : sms;
     return (int)launch_k(kv8_attn_kernel<T, HD>, dim3((unsigned)grid), dim3(KTHREADS), smem, s, k_map, v_map, a);
 }
 
@@ -495,30 +566,48 @@ cudaError_t allow_smem(const void* kern) {
 // core tile whose two halves take alternate keys up to 128, two 128-row
 // tiles over the same keys above.
 //
-// Splits.  A tile's keys are cut into at most split_cap splits of whole
-// pages: as many as give every resident CTA `waves` items if all sequences
-// had the same tiles.  Both follow from the call's row, sequence and head
-// counts alone, so a sequence's results depend on its own rows and length,
-// not on what the other sequences hold.
+// Both this and the splits of a tile's pages follow from the call's row,
+// sequence and head counts and the sequence's own length alone: its results
+// do not depend on what the other sequences hold.
 Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int max_pages, int sms) {
     Kv8AttnPlan p;
     const long long packed = (long long)rows * (n_q / n_kv);
     const long long each = (packed + S - 1) / S;
     p.form = each <= 16 ? KV8_MMA : (each <= 128 ? KV8_TC_KEYS : KV8_TC_ROWS);
     p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_KEYS ? 128 : 256);
-    const long long resident = p.form == KV8_MMA ? 2LL * sms : sms;
     const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
     long long usual = (packed + p.tile - 1) / p.tile;
     if (usual < S) usual = S;
-    long long cap = (2 * resident + usual * n_kv - 1) / (usual * n_kv);
-    if (cap > max_pages) cap = max_pages;
-    if (cap > 64) cap = 64;
-    if (cap < 1) cap = 1;
+    // Splits of a sequence with P pages (a value for each power of two): the
+    // count that costs least if all sequences were like it.  Rounds of items
+    // over the SMs, each as long as its pages (the mma.sync form's eight warps
+    // take a page each in the time of four) plus an item's fixed cost (start,
+    // merge, partials), about 8 pages.
+    const double fixed = 8.0;
+    long long cap = 1;
+    for (int b = 0; b < 32; ++b) {
+        p.caps[b] = 1;
+        if ((1LL << b) > max_pages) continue;
+        const double pages = 1.5 * (double)(1LL << b);
+        double best = 0.0;
+        for (long long c = 1; c <= 64 && c <= (1LL << b); ++c) {
+            const long long rounds = (usual * n_kv * c + sms - 1) / sms;
+            double len = pages / (double)c;
+            const double four = 4.0 * (double)(long long)((len + 7.0) / 8.0);
+            if (p.form == KV8_MMA && len < four) len = four;
+            const double cost = (double)rounds * (len + fixed);
+            if (c == 1 || cost < 0.95 * best) {   // partials cost bandwidth: only for a clear gain
+                best = cost;
+                p.caps[b] = (uint8_t)c;
+            }
+        }
+        if (p.caps[b] > cap) cap = p.caps[b];
+    }
     p.split_cap = (int)cap;
     p.ticket_cap = tiles * n_kv * (p.form == KV8_MMA ? 1 : 8);
     p.part_cap = cap > 1 ? tiles * n_kv * cap : 0;
     p.ticket_bytes = (size_t)((p.ticket_cap * 4 + 255) / 256 * 256);
-    p.bytes = p.ticket_bytes + (size_t)p.part_cap * p.tile * (head_dim + 4) * 4;
+    p.bytes = KV8_QUEUE_BYTES + p.ticket_bytes + (size_t)p.part_cap * p.tile * (head_dim + 4) * 4;
     return p;
 }
 

@@ -15,6 +15,20 @@ __device__ __forceinline__ void report(int* err, int code, int info) {
     if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
 }
 
+// Items are handed out one by one, as sequences differ in length: a CTA's
+// first is its index, the others come from a counter in the workspace.  The
+// last CTA to be refused one puts the counters back to zero.
+__device__ __forceinline__ int next_item(const Kv8AttnArgs& a, int total) {
+    if (total <= (int)gridDim.x) return -1;      // each has had its only one
+    const int item = (int)gridDim.x + atomicAdd(a.queue, 1);
+    if (item < total) return item;
+    if (atomicAdd(a.queue + 1, 1) == (int)gridDim.x - 1) {
+        a.queue[0] = 0;
+        a.queue[1] = 0;
+    }
+    return -1;
+}
+
 // One sequence of the call: its rows, keys and how they are cut.
 struct Seq {
     int r0, n;          // rows r0 .. r0 + n - 1
@@ -47,7 +61,8 @@ __device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
     q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
     const int pages = q.page_hi > q.page_lo ? q.page_hi - q.page_lo : 0;
     q.tiles = (int)(((long long)q.n * a.group + a.tile - 1) / a.tile);
-    q.len = (pages + a.split_cap - 1) / a.split_cap;
+    const int most = a.caps[31 - __clz(pages | 1)];
+    q.len = (pages + most - 1) / most;
     if (q.len < 1) q.len = 1;
     q.splits = (pages + q.len - 1) / q.len;
     if (q.splits < 1) q.splits = 1;

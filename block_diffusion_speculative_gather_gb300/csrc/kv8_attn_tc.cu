@@ -9,20 +9,21 @@
 //     128-row tiles of q over the same keys, which are converted once;
 //   KEYS form: both take the same 128 rows and alternate 128-key steps; at
 //     the item's end the first reads the second's sums from tensor memory.
-// Roles: a warp brings the pages' codes by TMA and looks up pages and scales;
-// four warps turn a step's codes (two pages) into f16 operand tiles, K as it
-// stands and V transposed (keys contiguous); one thread issues the MMAs:
+// Roles: two warps bring the pages' K and V codes by TMA and look up pages and
+// scales; four warps turn a step's K codes (two pages) into an f16 operand
+// tile, five its V codes into a transposed one (keys contiguous); one thread issues the MMAs:
 // S = Q K^T, then O += P V with P read from tensor memory, where the softmax
 // warps wrote it over the scores.  While one group's softmax runs, the
 // tensor core works for the other.
 //
 // The running maximum that weights refer to moves only when a row's maximum
-// rises by more than 2^8 (weights stay within f16's range), so outputs are
+// rises by more than 2^14 (weights stay within f16's range), so outputs are
 // rescaled in tensor memory rarely.
 //
 // Tensor memory: scores at columns 0 and 128, outputs at 256 and 384.  A
-// step's P overwrites the first half of its scores, and the next step's
-// scores overwrite P: the two MMAs are issued in that order by one thread.
+// step's P overwrites its scores (32 keys' weights in the first 16 of their
+// 32 columns), and the next step's scores overwrite P: the two MMAs are
+// issued in that order by one thread.
 
 #include <type_traits>
 
@@ -36,10 +37,11 @@ namespace {
 using namespace kv8;
 using adev::ldsm_x4_trans;
 
-constexpr int CONV_WARP = 8, N_CONV = 4, MMA_WARP = 12, TC_THREADS = 32 * 14;   // the last warp loads
+// Warps: 0-7 softmax, then K's conversion, V's, the MMA issuer and two loaders.
+constexpr int KC_WARP = 8, KC = 4, VC_WARP = 12, VC = 5, MMA_WARP = 17, TMA_K = 18, TC_THREADS = 32 * 20;
 constexpr int STEP = 2 * KV8_PAGE;         // keys of a step
 constexpr int SITE_TC = 310;               // + role
-constexpr float LAZY = 8.f;                // rise of a row's maximum (base 2) that moves the reference
+constexpr float LAZY = 14.f;               // rise of a row's maximum (base 2) that moves the reference
 
 template <int HD, bool KEYS> struct TcSmem {
     static constexpr int QB = 128 * HD * 2;                    // one q tile, f16
@@ -50,9 +52,10 @@ template <int HD, bool KEYS> struct TcSmem {
     static constexpr int q = 0, k = q + QR, v = k + 2 * KB, raw = v + 2 * KB;
     static constexpr int steps = raw + RAW * 2 * PB;           // [4] step scales
     static constexpr int rsc = steps + 4 * 32;                 // [RAW] page scales
-    static constexpr int bars = rsc + RAW * 8;
-    static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1;
-    static constexpr int misc = bars + n_bars * 8;             // tensor-memory base, abort flag
+    static constexpr int rscv = rsc + RAW * 8;
+    static constexpr int bars = rscv + RAW * 8;
+    static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1 + 4;
+    static constexpr int misc = bars + n_bars * 8;             // tensor-memory base, abort flag, items
     static constexpr int cum = misc + 16;
     static constexpr size_t bytes = 1024 + cum + (MAX_GROUPS + 1) * 4;
 };
@@ -65,6 +68,22 @@ __device__ __forceinline__ void stsm_x4(void* p, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};"
                  ::"r"(smem_u32(p)), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 // Bounded wait that gives up early once another role has given up.
@@ -112,16 +131,20 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     extern __shared__ uint8_t raw_smem[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     StepScale* steps = reinterpret_cast<StepScale*>(sm + L::steps);
-    float2* rsc = reinterpret_cast<float2*>(sm + L::rsc);
+    float2* rsc = reinterpret_cast<float2*>(sm + L::rsc);     // with K's pages and with V's
+    float2* rscv = reinterpret_cast<float2*>(sm + L::rscv);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
     uint64_t *rawk_full = bars, *rawk_empty = bars + R, *rawv_full = bars + 2 * R, *rawv_empty = bars + 3 * R,
              *k_full = bars + 4 * R, *k_empty = k_full + 2, *v_full = k_full + 4, *v_empty = k_full + 6,
              *q_full = k_full + 8, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4,
-             *o_done = q_full + 6, *handed = q_full + 8, *drain = q_full + 9;
+             *o_done = q_full + 6, *handed = q_full + 8, *drain = q_full + 9, *i_full = q_full + 10,
+             *i_empty = q_full + 12;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
+    volatile int* i_val = reinterpret_cast<volatile int*>(sm + L::misc + 8);   // [2]
     int* cum = reinterpret_cast<int*>(sm + L::cum);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform, so each role's code is
 
     pdl_trigger();
     if (tid == 0) {
@@ -129,23 +152,27 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         tma_prefetch_desc(&v_map);
         for (int i = 0; i < R; ++i) {
             mbar_init(rawk_full + i, 1);
-            mbar_init(rawk_empty + i, N_CONV);
+            mbar_init(rawk_empty + i, KC);
             mbar_init(rawv_full + i, 1);
-            mbar_init(rawv_empty + i, N_CONV);
+            mbar_init(rawv_empty + i, VC);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(k_full + i, N_CONV);
+            mbar_init(k_full + i, KC);
             mbar_init(k_empty + i, 1);
-            mbar_init(v_full + i, N_CONV);
+            mbar_init(v_full + i, VC);
             mbar_init(v_empty + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
             mbar_init(o_done + i, 1);
         }
-        mbar_init(q_full, KEYS ? 4 : 8);
+        mbar_init(q_full, 8);
         mbar_init(q_free, 1);
-        mbar_init(handed, 4);
+        mbar_init(handed, 8);
         mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(i_full + i, 1);
+            mbar_init(i_empty + i, TC_THREADS / 32 - 1);
+        }
         fence_mbar_init();
         *abort = 0;
     }
@@ -155,7 +182,17 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     count_items<TC_THREADS>(a, cum);   // ends with a barrier
     tc::fence_after_sync();
     const int total = total_items(a, cum);
-    const uint32_t tm = *tmem_base;
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_base, 0);
+
+    // The item behind this warp's k-th, -1 at the end: the K loader posts them.
+    auto next = [&](unsigned k) -> int {
+        if (!__all_sync(0xffffffffu, wait_or(i_full + (k & 1), (k >> 1) & 1, abort, a.err, SITE_TC + 13))) return -1;
+        const int item = i_val[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty + (k & 1));
+        return item;
+    };
+    const int first = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
 
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
@@ -164,7 +201,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         const uint32_t s_tm = tm + t * 128 + lanes, o_tm = tm + 256 + t * 128 + lanes;
         unsigned cs = 0, xs = 0, base = 0, items = 0;   // this group's steps, hand-overs, all steps, items so far
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++items) {
+        for (int item = first; item >= 0 && ok; item = next(items++)) {
             Seq q;
             const Item w = find_item(a, cum, item, &q);
             // the issuing thread is done with the item before: Q is free, and no
@@ -180,35 +217,33 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             int klo = 0, khi = 0;
             float fr;
             {
-                // q: this thread's row, scaled into f16
-                uint4 e[HD / 8];
+                // q: this thread's row, scaled into f16 (read twice: its largest
+                // element, then the elements)
+                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
+                                                                  (long long)(q.r0 + qi) * a.q_row + (long long)hq * a.q_head);
                 float top = 0.f;
                 if (real) {
-                    const T* src = reinterpret_cast<const T*>(a.q) + (long long)(q.r0 + qi) * a.q_row + (long long)hq * a.q_head;
+#pragma unroll 4
+                    for (int k = 0; k < HD / 8; ++k) {
+                        const uint4 e = src[k];
+                        const T* ev = reinterpret_cast<const T*>(&e);
 #pragma unroll
-                    for (int k = 0; k < HD / 8; ++k) e[k] = reinterpret_cast<const uint4*>(src)[k];
-                    row_keys(a, q, qi, &klo, &khi);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < HD / 8; ++k) e[k] = make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int k = 0; k < HD / 8; ++k) {
-                    const T* ev = reinterpret_cast<const T*>(&e[k]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x = fabsf(to_f32(ev[j]));
-                        top = fmaxf(top, x < INFINITY ? x : 0.f);
+                        for (int j = 0; j < 8; ++j) {
+                            const float x = fabsf(to_f32(ev[j]));
+                            top = fmaxf(top, x < INFINITY ? x : 0.f);
+                        }
                     }
+                    row_keys(a, q, qi, &klo, &khi);
                 }
                 float inv, back;
                 row_factor(top, &inv, &back);
                 fr = back * a.scale_log2;
                 if (!KEYS || t == 0) {
                     uint8_t* qs = sm + L::q + (KEYS ? 0 : t * L::QB);
-#pragma unroll
+#pragma unroll 4
                     for (int k = 0; k < HD / 8; ++k) {
-                        const T* ev = reinterpret_cast<const T*>(&e[k]);
+                        const uint4 e = real ? src[k] : make_uint4(0, 0, 0, 0);
+                        const T* ev = reinterpret_cast<const T*>(&e);
                         uint4 h;
                         uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
 #pragma unroll
@@ -217,97 +252,104 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         *reinterpret_cast<uint4*>(qs + (k >> 3) * 128 * 128 + swz128(r, k & 7)) = h;
                     }
                     tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
 
+            // a warp without rows only takes part: its lanes' weights stay whatever
+            // tensor memory holds, and nothing of them is written
+            const bool any = __any_sync(0xffffffffu, real);
             float M = -INFINITY, l = 0.f;
             for (int i = 0; i < nt && ok; ++i, ++cs) {
                 const int j = KEYS ? 2 * i + t : i;
                 ok = __all_sync(0xffffffffu, wait_or(s_full + t, cs & 1, abort, a.err, SITE_TC + 1));
                 if (!ok) break;
+                if (!any) {
+                    if (lane == 0) mbar_arrive(p_full + t);
+                    continue;
+                }
                 tc::fence_after_sync();
                 const StepScale sc = steps[(base + j) & 3];
                 const int k0 = (w.p0 + 2 * j) * KV8_PAGE;
-                bool whole[2];
-                float f[2];
-                float mx = -INFINITY;
+                // 32 keys at a time, the next 32 scores on their way meanwhile
+                uint32_t buf[2][32];
+                tc::ld_x32_async(s_tm, buf[0]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f[h] = fr * sc.ks[h];
-                    const int kp = k0 + h * KV8_PAGE;
-                    whole[h] = kp >= w.in_lo && kp + KV8_PAGE <= w.in_hi;
-                    if (sc.ks[h] < 0.f) continue;
-                    float m = -INFINITY;
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t (&v)[32] = buf[c & 1];
+                    tc::ld_wait(v);
+                    const int kp = k0 + c * 32;
+                    const float ks = sc.ks[c >> 1], ev = sc.ev[c >> 1];
+                    const bool there = ks >= 0.f;
+                    const float f = there ? fmaxf(fr * ks, 0x1p-126f) : 1.f;   // above 0: a masked score stays -inf
+                    if (!there || kp < w.in_lo || kp + 32 > w.in_hi) {
+                        const int lo = there ? klo - kp : 32, hi = khi - kp;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float v[32];
-                        tc::ld_x32(s_tm + h * 64 + c * 32, v);
-                        if (whole[h]) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) m = fmaxf(m, v[x]);
-                        } else {
-                            const int lo = klo - (kp + c * 32), hi = khi - (kp + c * 32);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) m = fmaxf(m, x >= lo && x < hi ? v[x] : -INFINITY);
-                        }
+                        for (int x = 0; x < 32; ++x)
+                            v[x] = x >= lo && x < hi ? v[x] : 0xff800000u;      // -inf
                     }
-                    mx = fmaxf(mx, fmaf(m, f[h], sc.ev[h]));
-                }
-                // move the reference where this row's maximum has risen far
-                const bool need = mx > M + LAZY || (M == -INFINITY && mx > -INFINITY);
-                if (__any_sync(0xffffffffu, need)) {
-                    const float f0 = need ? (M == -INFINITY ? 0.f : ex2(M - mx)) : 1.f;
-                    if (need) M = mx;
-                    l *= f0;
-                    if (i > 0) {
-                        ok = __all_sync(0xffffffffu, wait_or(o_done + t, (cs - 1) & 1, abort, a.err, SITE_TC + 2));
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        for (int c = 0; c < HD / 32; ++c) {
-                            float v[32];
-                            tc::ld_x32(o_tm + c * 32, v);
+                    float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) v[x] *= f0;
-                            tc::st_x32(o_tm + c * 32, v);
-                        }
+                    for (int x = 0; x < 32; x += 4) {
+                        m[0] = fmaxf(m[0], fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])));
+                        m[1] = fmaxf(m[1], fmaxf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])));
                     }
-                }
-                const float m0 = M == -INFINITY ? 0.f : M;
+                    const float top = fmaxf(m[0], m[1]);
+                    const float mx = top == -INFINITY ? -INFINITY : fmaf(top, f, ev);
+                    // move the reference where this row's maximum has risen far: the sums,
+                    // the outputs and this step's weights so far follow
+                    const bool need = mx > M + LAZY || (M == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(0xffffffffu, need)) {
+                        const float f0 = need ? (M == -INFINITY ? 0.f : ex2(M - mx)) : 1.f;
+                        if (need) M = mx;
+                        l *= f0;
+                        // the weights and outputs of a row without any so far are zeros
+                        if (__any_sync(0xffffffffu, f0 != 1.f && f0 != 0.f)) {
+                            tc::st_wait();
+#pragma unroll 1
+                            for (int b = 0; b < c; ++b) {
+                                uint32_t p[16];
+                                tc::ld_x16(s_tm + b * 32, p);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int kp = k0 + h * KV8_PAGE;
-                    const float off = sc.ev[h] - m0;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t p[16];
-                        if (sc.ks[h] < 0.f) {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) p[x] = 0;
-                        } else {
-                            float v[32];
-                            tc::ld_x32(s_tm + h * 64 + c * 32, v);
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) v[x] = fmaf(v[x], f[h], off);
-                            if (!whole[h]) {
-                                const int lo = klo - (kp + c * 32), hi = khi - (kp + c * 32);
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) v[x] = x >= lo && x < hi ? v[x] : -INFINITY;
+                                for (int x = 0; x < 16; ++x) {
+                                    const float2 y = __half22float2(*reinterpret_cast<__half2*>(&p[x]));
+                                    p[x] = pack_f16x2(y.x * f0, y.y * f0);
+                                }
+                                tc::st_x16(s_tm + b * 32, p);
                             }
+                            if (i > 0) {
+                                ok = __all_sync(0xffffffffu, wait_or(o_done + t, (cs - 1) & 1, abort, a.err, SITE_TC + 2));
+                                tc::fence_after_sync();
+#pragma unroll 1
+                                for (int b = 0; b < HD / 16 && ok; ++b) {
+                                    uint32_t o[16];
+                                    tc::ld_x16(o_tm + b * 16, o);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                v[x] = ex2(v[x]);
-                                sum[x & 3] += v[x];
+                                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f0);
+                                    tc::st_x16(o_tm + b * 16, o);
+                                }
                             }
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) p[x] = pack_f16x2(v[2 * x], v[2 * x + 1]);
                         }
-                        tc::st_x16(s_tm + h * 32 + c * 16, p);
                     }
-                    l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), sc.iv[h], l);
+                    if (c < 3) tc::ld_x32_async(s_tm + (c + 1) * 32, buf[(c + 1) & 1]);
+                    const float off = ev - (M == -INFINITY ? 0.f : M);
+                    const float2 ff = make_float2(f, f), oo = make_float2(off, off);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t p[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        float2 y = fma2(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), ff, oo);
+                        y.x = ex2(y.x);
+                        y.y = ex2(y.y);
+                        sum[x & 1] = add2(sum[x & 1], y);
+                        p[x] = pack_f16x2(y.x, y.y);
+                    }
+                    tc::st_x16(s_tm + c * 32, p);
+                    const float2 s2 = add2(sum[0], sum[1]);
+                    l = fmaf(s2.x + s2.y, sc.iv[c >> 1], l);
                 }
+                if (!ok) break;
                 tc::st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -320,36 +362,36 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             base += n;
             if (!ok) break;
 
-            if (KEYS && t == 1) {
-                // (max, sum) go over the scores; the first group's warps read them
-                // and the outputs, as they see the same lanes
-                if (nt > 0) {
-                    tc::st_x2(s_tm, M, l);
-                    tc::st_wait();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(handed);
-                }
-                continue;
-            }
-            float fa = 1.f, fb = 0.f;
-            const bool two = KEYS && group_steps<KEYS>(a, q, w, 1) > 0;
-            if (two) {
+            // KEYS: the groups see the same lanes of tensor memory.  Each writes its
+            // (max, sum) over its scores, and takes half of the columns of both
+            // outputs.
+            float fa = 1.f, fb = 0.f;                      // factors of this group's and the other's sums
+            const int nt_other = KEYS ? group_steps<KEYS>(a, q, w, 1 - t) : 0;
+            const uint32_t other = t == 0 ? 128u : (uint32_t)-128;
+            if (KEYS) {
+                tc::st_x2(s_tm, M, l);
+                tc::st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(handed);
                 ok = __all_sync(0xffffffffu, wait_or(handed, xs & 1, abort, a.err, SITE_TC + 4));
                 if (!ok) break;
                 ++xs;
                 tc::fence_after_sync();
                 float bm, bl;
-                tc::ld_x2(s_tm + 128, &bm, &bl);
+                tc::ld_x2(s_tm + other, &bm, &bl);
                 const float m = fmaxf(M, bm);
                 fa = M == -INFINITY ? 0.f : ex2(M - m);
                 fb = bm == -INFINITY ? 0.f : ex2(bm - m);
-                l = (l != 0.f ? l * fa : 0.f) + (bl != 0.f ? bl * fb : 0.f);   // a NaN sum stays one
+                // a NaN sum stays one; in the groups' order, for the same bits in both
+                const float la = l != 0.f ? l * fa : 0.f, lb = bl != 0.f ? bl * fb : 0.f;
+                l = t == 0 ? la + lb : lb + la;
                 M = m;
             }
+            const int c_first = KEYS && t == 1 ? HD / 64 : 0, c_last = KEYS && t == 0 ? HD / 64 : HD / 32;
 
             // ---- the row's outputs, or its partial of this split
-            const int wi = KEYS ? warp : t * 4 + (warp & 3);
+            const int wi = warp;   // a ticket for each warp's rows (and columns)
             const long long slot0 = (long long)item - w.split;    // splits of a tile are neighbours
             const long long tk = (((long long)q.r0 * a.group / a.tile + w.s + w.tile) * a.n_kv + w.kh) * 8 + wi;
             const bool split = q.splits > 1;
@@ -361,7 +403,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
             const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no key: zeros
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
+            for (int c = c_first; c < c_last; ++c) {
                 float v[32];
                 __syncwarp();
                 if (nt > 0) {
@@ -370,9 +412,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
 #pragma unroll
                     for (int x = 0; x < 32; ++x) v[x] = 0.f;
                 }
-                if (two) {
+                if (KEYS && nt_other > 0) {
                     float u[32];
-                    tc::ld_x32(o_tm + 128 + c * 32, u);
+                    tc::ld_x32(o_tm + other + c * 32, u);
 #pragma unroll
                     for (int x = 0; x < 32; ++x) v[x] = fmaf(u[x], fb, v[x] * fa);
                 }
@@ -395,11 +437,11 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             __syncwarp();
             tc::fence_before_sync();   // the accumulator has been read
             if (!split) {
-                if (real && a.lse)
+                if (real && a.lse && c_first == 0)
                     a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
                 continue;
             }
-            if (real && fits) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow] = make_float2(M, l);
+            if (real && fits) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow + (c_first ? RT : 0)] = make_float2(M, l);
             __threadfence();
             __syncwarp();
             int last = 0;
@@ -411,61 +453,82 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             if (!real) continue;
             // the last split's warp folds its rows of all splits, in split order
             const float* src = a.part + slot0 * PL;
+            const float2* mls = reinterpret_cast<const float2*>(src + (size_t)RT * HD) + prow + (c_first ? RT : 0);
+            const long long PL2 = PL / 2;
             float fm = -INFINITY, fl = 0.f;
-            for (int v = 0; v < q.splits; ++v)
-                fm = fmaxf(fm, __ldcg(&reinterpret_cast<const float2*>(src + v * PL + (size_t)RT * HD)[prow]).x);
+            for (int v = 0; v < q.splits; ++v) fm = fmaxf(fm, __ldcg(mls + v * PL2).x);
             for (int v = 0; v < q.splits; ++v) {
-                const float2 x = __ldcg(&reinterpret_cast<const float2*>(src + v * PL + (size_t)RT * HD)[prow]);
+                const float2 x = __ldcg(mls + v * PL2);
                 fl = fmaf(x.y, x.x == -INFINITY ? 0.f : ex2(x.x - fm), fl);
             }
             const float finv = fl == 0.f ? 0.f : 1.f / fl;
-            for (int b = 0; b < HD / 16; ++b) {
+#pragma unroll 1
+            for (int b = 2 * c_first; b < 2 * c_last; ++b) {
                 float o[16];
 #pragma unroll
                 for (int x = 0; x < 16; ++x) o[x] = 0.f;
-                for (int v = 0; v < q.splits; ++v) {
-                    const float m = __ldcg(&reinterpret_cast<const float2*>(src + v * PL + (size_t)RT * HD)[prow]).x;
-                    const float f = m == -INFINITY ? 0.f : ex2(m - fm);
+                const float4* col = reinterpret_cast<const float4*>(src) + (size_t)b * 4 * RT + prow;
+                for (int v0 = 0; v0 < q.splits; v0 += 2) {     // two splits' loads in flight
+                    float4 y[2][4];
+                    float m[2];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 y = __ldcg(&reinterpret_cast<const float4*>(src + v * PL)[(size_t)(b * 4 + x) * RT + prow]);
-                        o[4 * x] = fmaf(y.x, f, o[4 * x]);
-                        o[4 * x + 1] = fmaf(y.y, f, o[4 * x + 1]);
-                        o[4 * x + 2] = fmaf(y.z, f, o[4 * x + 2]);
-                        o[4 * x + 3] = fmaf(y.w, f, o[4 * x + 3]);
+                    for (int k = 0; k < 2; ++k) {
+                        const int v = v0 + k < q.splits ? v0 + k : v0;
+                        m[k] = __ldcg(mls + v * PL2).x;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) y[k][x] = __ldcg(col + v * (PL / 4) + x * RT);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (v0 + k >= q.splits) break;
+                        const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - fm);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            o[4 * x] = fmaf(y[k][x].x, f, o[4 * x]);
+                            o[4 * x + 1] = fmaf(y[k][x].y, f, o[4 * x + 1]);
+                            o[4 * x + 2] = fmaf(y[k][x].z, f, o[4 * x + 2]);
+                            o[4 * x + 3] = fmaf(y[k][x].w, f, o[4 * x + 3]);
+                        }
                     }
                 }
                 store16<T>(dst + 16 * b, o, finv);
             }
-            if (a.lse) a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
+            if (a.lse && c_first == 0)
+                a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
         }
-    } else if (warp < MMA_WARP) {
-        // ---------------------------------------------------------- conversion
-        const int cw = warp - CONV_WARP;
+    } else if (warp < VC_WARP) {
+        // ---------------------------------------------------------- K's conversion
+        const int cw = warp - KC_WARP;
         unsigned g = 0;     // steps so far
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        unsigned items = 0;
+        for (int item = first; item >= 0 && ok; item = next(items++)) {
             Seq q;
             const Item w = find_item(a, cum, item, &q);
             const int n = (w.p1 - w.p0 + 1) / 2;
-            for (int j = 0; j < n && ok; ++j, ++g) {
+            for (int j = 0; j < n; ++j, ++g) {
                 const int st = g & 1;
-                if (g >= 2) ok = __all_sync(0xffffffffu, wait_or(k_empty + st, ((g >> 1) - 1) & 1, abort, a.err, SITE_TC + 5));
+                const unsigned r0 = (2 * g) % R, par = (2 * g / R) & 1;      // R is even: both pages share a parity
+                ok = (g < 2 || wait_or(k_empty + st, ((g >> 1) - 1) & 1, abort, a.err, SITE_TC + 5)) &&
+                     wait_or(rawk_full + r0, par, abort, a.err, SITE_TC + 6) &&
+                     wait_or(rawk_full + r0 + 1, par, abort, a.err, SITE_TC + 6);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                float2 sc[2];
+                if (cw == 0 && lane < 2) {
+                    const float2 sc = rsc[r0 + lane];
+                    StepScale* d = steps + (g & 3);
+                    d->ks[lane] = sc.y > 0.f ? sc.x : -1.f;
+                    d->ev[lane] = sc.y > 0.f ? log2f(sc.y) : 0.f;
+                    d->iv[lane] = sc.y > 0.f ? 1.f / sc.y : 0.f;
+                }
+                uint8_t* dst = sm + L::k + st * L::KB;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const unsigned rs = 2 * g + h;
-                    ok = __all_sync(0xffffffffu, wait_or(rawk_full + rs % R, (rs / R) & 1, abort, a.err, SITE_TC + 6));
-                    if (!ok) break;
-                    sc[h] = rsc[rs % R];
-                    if (sc[h].x < 0.f) continue;
-                    const uint8_t* src = sm + L::raw + (rs % R) * PB;
-                    uint8_t* dst = sm + L::k + st * L::KB;
+                for (int h = 0; h < 2; ++h) {                  // the step's pages
 #pragma unroll
-                    for (int x = cw; x < HD / 8; x += N_CONV) {
-                        const int key = (x & 1) * 32 + lane, c = x >> 1;     // 16 dims of a key
-                        const uint4 e = lds128(src + tile_off<HD>(key, c));
+                    for (int y = 0; y < HD / 8 / KC; ++y) {    // units of 32 keys x 16 dims
+                        const int u = cw + y * KC, key = (u & 1) * 32 + lane, c = u >> 1;
+                        // a page that is not there: its scores are masked whatever the bytes
+                        const uint4 e = lds128(sm + L::raw + (r0 + h) * PB + tile_off<HD>(key, c));
                         const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
                         uint32_t o[8];
 #pragma unroll
@@ -477,48 +540,57 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                }
-                if (!ok) break;
-                if (cw == 0 && lane < 2) {
-                    const float2 s = lane ? sc[1] : sc[0];
-                    StepScale* d = steps + (g & 3);
-                    d->ks[lane] = s.y > 0.f ? s.x : -1.f;
-                    d->ev[lane] = s.y > 0.f ? log2f(s.y) : 0.f;
-                    d->iv[lane] = s.y > 0.f ? 1.f / s.y : 0.f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawk_empty + r0 + h);   // its codes have been read
                 }
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(k_full + st);
-                    mbar_arrive(rawk_empty + (2 * g) % R);
-                    mbar_arrive(rawk_empty + (2 * g + 1) % R);
-                }
-                if (g >= 2) ok = __all_sync(0xffffffffu, wait_or(v_empty + st, ((g >> 1) - 1) & 1, abort, a.err, SITE_TC + 7));
+                if (lane == 0) mbar_arrive(k_full + st);
+            }
+        }
+    } else if (warp < MMA_WARP) {
+        // ---------------------------------------------------------- V's conversion
+        const int cw = warp - VC_WARP;
+        unsigned g = 0;
+        bool ok = true;
+        unsigned items = 0;
+        for (int item = first; item >= 0 && ok; item = next(items++)) {
+            Seq q;
+            const Item w = find_item(a, cum, item, &q);
+            const int n = (w.p1 - w.p0 + 1) / 2;
+            for (int j = 0; j < n; ++j, ++g) {
+                const int st = g & 1;
+                const unsigned r0 = (2 * g) % R, par = (2 * g / R) & 1;
+                ok = (g < 2 || wait_or(v_empty + st, ((g >> 1) - 1) & 1, abort, a.err, SITE_TC + 7)) &&
+                     wait_or(rawv_full + r0, par, abort, a.err, SITE_TC + 6) &&
+                     wait_or(rawv_full + r0 + 1, par, abort, a.err, SITE_TC + 6);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                const float2 sa = rscv[r0], sb = rscv[r0 + 1];
+                const bool there[2] = {sa.x >= 0.f && sa.y > 0.f, sb.x >= 0.f && sb.y > 0.f};
+                // codes of keys that no row sees may be anything, NaN included: as zeros
+                const int kp = (w.p0 + 2 * j) * KV8_PAGE;
+                const bool plain = kp >= w.lo && kp + STEP <= w.hi && there[0] && there[1];
+                uint8_t* dst = sm + L::v + st * L::KB;
+                constexpr int UNITS = HD / 8;                  // of 32 keys x 16 dims, in a page
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const unsigned rs = 2 * g + h;
-                    ok = __all_sync(0xffffffffu, wait_or(rawv_full + rs % R, (rs / R) & 1, abort, a.err, SITE_TC + 6));
-                    if (!ok) break;
-                    const uint8_t* src = sm + L::raw + (R + rs % R) * PB;
-                    uint8_t* dst = sm + L::v + st * L::KB + h * HD * 128;
-                    const bool valid = sc[h].x >= 0.f && sc[h].y > 0.f;
-                    const int kp = (w.p0 + 2 * j + h) * KV8_PAGE;
-                    // codes of keys that no row sees may be anything, NaN included: as zeros
-                    const bool edge = kp < w.lo || kp + KV8_PAGE > w.hi;
 #pragma unroll
-                    for (int x = cw; x < HD / 8; x += N_CONV) {
-                        const int kb = x & 1, d = x >> 1;        // 32 keys, 16 dims
-                        uint32_t r4[4] = {0, 0, 0, 0};
-                        if (valid) {
-                            ldsm_x4_trans(r4, src + tile_off<HD>(kb * 32 + lane, d));
-                            if (edge) {
+                    for (int y = 0; y < (UNITS + VC - 1) / VC; ++y) {
+                        // the second page's units begin with another warp, as they
+                        // do not divide evenly
+                        const int x = (cw + 2 * h) % VC + y * VC;
+                        if (x >= UNITS) break;
+                        const int kb = x & 1, d = x >> 1;
+                        uint32_t r4[4];
+                        ldsm_x4_trans(r4, sm + L::raw + (R + r0 + h) * PB + tile_off<HD>(kb * 32 + lane, d));
+                        if (!plain) {
+                            const bool valid = h ? there[1] : there[0];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int k = kp + kb * 32 + 8 * i + 2 * (lane & 3);
-                                    r4[i] &= (k >= w.lo && k < w.hi ? 0x0000ffffu : 0u) |
-                                             (k + 1 >= w.lo && k + 1 < w.hi ? 0xffff0000u : 0u);
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                const int k = kp + h * KV8_PAGE + kb * 32 + 8 * i + 2 * (lane & 3);
+                                r4[i] &= (valid && k >= w.lo && k < w.hi ? 0x0000ffffu : 0u) |
+                                         (valid && k + 1 >= w.lo && k + 1 < w.hi ? 0xffff0000u : 0u);
                             }
                         }
                         uint32_t e[4], o[4];
@@ -529,82 +601,113 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                             o[i] = f16_of_codes(p >> 16);
                         }
                         const int row = 16 * d + (lane & 7), ch = 4 * kb + (lane >> 3);
-                        stsm_x4(dst + swz128(row, ch), e);
-                        stsm_x4(dst + swz128(row + 8, ch), o);
+                        uint8_t* vd = dst + h * HD * 128;
+                        stsm_x4(vd + swz128(row, ch), e);
+                        stsm_x4(vd + swz128(row + 8, ch), o);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawv_empty + r0 + h);
                 }
-                if (!ok) break;
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v_full + st);
-                    mbar_arrive(rawv_empty + (2 * g) % R);
-                    mbar_arrive(rawv_empty + (2 * g + 1) % R);
-                }
+                if (lane == 0) mbar_arrive(v_full + st);
             }
         }
     } else if (warp == MMA_WARP) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0) {
-            constexpr uint32_t IS = tc::idesc_f16_f32(128, STEP), IO = tc::idesc_f16_f32(128, HD);
-            unsigned base = 0, items = 0, done[2] = {0, 0};
-            bool ok = true;
-            for (int item = blockIdx.x; item < total && ok; item += gridDim.x, ++items) {
-                Seq q;
-                const Item w = find_item(a, cum, item, &q);
-                const int n = (w.p1 - w.p0 + 1) / 2;
-                const int nt[2] = {group_steps<KEYS>(a, q, w, 0), group_steps<KEYS>(a, q, w, 1)};
-                ok = wait_or(q_full, items & 1, abort, a.err, SITE_TC + 8);
-                auto qk = [&](int t, int i) -> bool {
-                    const unsigned g = base + (KEYS ? 2 * i + t : i);
-                    const int st = g & 1;
-                    if (!wait_or(k_full + st, (g >> 1) & 1, abort, a.err, SITE_TC + 9)) return false;
-                    tc::fence_after_sync();
-                    const uint8_t* qs = sm + L::q + (KEYS ? 0 : t * L::QB);
-                    const uint8_t* ks = sm + L::k + st * L::KB;
+        // the warp stays converged and one lane issues: what an MMA names is
+        // uniform (issuing from a divergent lane took about twice as long)
+        constexpr uint32_t IS = tc::idesc_f16_f32(128, STEP), IO = tc::idesc_f16_f32(128, HD);
+        unsigned base = 0, items = 0, done[2] = {0, 0};
+        bool ok = true;
+        // descriptors of the tiles' first bytes; a k step adds 32 bytes, a
+        // 64-element half of K or Q its rows (in 16-byte units)
+        const uint64_t qd = tc::desc_sw128(sm + L::q), kd = tc::desc_sw128(sm + L::k), vd = tc::desc_sw128(sm + L::v);
+        for (int item = first; item >= 0 && ok; item = next(items++)) {
+            Seq q;
+            const Item w = find_item(a, cum, item, &q);
+            const int n = (w.p1 - w.p0 + 1) / 2;
+            const int nt[2] = {__shfl_sync(0xffffffffu, group_steps<KEYS>(a, q, w, 0), 0),
+                               __shfl_sync(0xffffffffu, group_steps<KEYS>(a, q, w, 1), 0)};
+            ok = __all_sync(0xffffffffu, wait_or(q_full, items & 1, abort, a.err, SITE_TC + 8));
+            auto qk = [&](int t, int i) -> bool {     // S_t = Q_t K^T of the group's step i
+                const unsigned g = __shfl_sync(0xffffffffu, base + (KEYS ? 2 * i + t : i), 0);
+                const unsigned st = g & 1;
+                if (!__all_sync(0xffffffffu, wait_or(k_full + st, (g >> 1) & 1, abort, a.err, SITE_TC + 9))) return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t qt = qd + (KEYS ? 0 : t * (L::QB >> 4)), kt = kd + st * (L::KB >> 4);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
-                        tc::mma_f16(tm + t * 128, tc::desc_sw128(qs + (k >> 2) * 128 * 128 + (k & 3) * 32),
-                                    tc::desc_sw128(ks + (k >> 2) * STEP * 128 + (k & 3) * 32), IS, k > 0);
+                        tc::mma_f16(tm + t * 128, qt + ((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2),
+                                    kt + ((k >> 2) * (STEP * 128 >> 4) + (k & 3) * 2), IS, k > 0);
                     tc::commit(s_full + t);
                     if (KEYS || t == 1 || nt[1] == 0) tc::commit(k_empty + st);
-                    return true;
-                };
-                for (int t = 0; t < 2 && ok; ++t)
-                    if (nt[t] > 0) ok = qk(t, 0);
-                for (int i = 0; i < nt[0] && ok; ++i)
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (i >= nt[t]) continue;
-                        const unsigned g = base + (KEYS ? 2 * i + t : i);
-                        const int st = g & 1;
-                        ok = wait_or(p_full + t, (done[t] + i) & 1, abort, a.err, SITE_TC + 10) &&
-                             wait_or(v_full + st, (g >> 1) & 1, abort, a.err, SITE_TC + 11);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        const uint8_t* vs = sm + L::v + st * L::KB;
+                }
+                __syncwarp();
+                return true;
+            };
+            auto pv = [&](int t, int i) -> bool {     // O_t += P_t V
+                const unsigned g = __shfl_sync(0xffffffffu, base + (KEYS ? 2 * i + t : i), 0);
+                const unsigned st = g & 1;
+                if (!__all_sync(0xffffffffu, wait_or(v_full + st, (g >> 1) & 1, abort, a.err, SITE_TC + 11) &&
+                                                 wait_or(p_full + t, (done[t] + i) & 1, abort, a.err, SITE_TC + 10)))
+                    return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t vt = vd + st * (L::KB >> 4);
+                    const uint32_t more = i > 0;
 #pragma unroll
-                        for (int k = 0; k < STEP / 16; ++k)
-                            tc::mma_f16_ta(tm + 256 + t * 128, tm + t * 128 + 8 * k,
-                                           tc::desc_sw128(vs + (k >> 2) * HD * 128 + (k & 3) * 32), IO, i > 0 || k > 0);
-                        tc::commit(o_done + t);
-                        if (KEYS || t == 1 || nt[1] == 0) tc::commit(v_empty + st);
-                        if (i + 1 < nt[t]) ok = qk(t, i + 1);
-                    }
-                done[0] += nt[0];
-                done[1] += nt[1];
-                base += n;
-                if (ok) tc::commit(q_free);
+                    for (int k = 0; k < STEP / 16; ++k)
+                        tc::mma_f16_ta(tm + 256 + t * 128, tm + t * 128 + 32 * (k >> 1) + 8 * (k & 1),
+                                       vt + ((k >> 2) * (HD * 128 >> 4) + (k & 3) * 2), IO, k > 0 ? 1u : more);
+                    tc::commit(o_done + t);
+                    if (KEYS || t == 1 || nt[1] == 0) tc::commit(v_empty + st);
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = ok && (nt[0] == 0 || qk(0, 0)) && (nt[1] == 0 || qk(1, 0));
+            for (int i = 0; i < nt[0] && ok; ++i) {
+                ok = pv(0, i) && (i + 1 >= nt[0] || qk(0, i + 1));
+                if (ok && i < nt[1]) ok = pv(1, i) && (i + 1 >= nt[1] || qk(1, i + 1));
             }
-            // every MMA has finished before tensor memory is given back
-            tc::commit(drain);
-            mbar_wait_bounded(drain, 0);
+            done[0] += nt[0];
+            done[1] += nt[1];
+            base += n;
+            if (ok && tc::elect_one()) tc::commit(q_free);
+            __syncwarp();
         }
+        // every MMA has finished before tensor memory is given back
+        if (tc::elect_one()) tc::commit(drain);
+        __syncwarp();
+        mbar_wait_bounded(drain, 0);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- pages
-        unsigned it = 0, ik = 0;   // pages issued: both tensors', K's
+        const bool is_k = warp == TMA_K;
+        const CUtensorMap* map = is_k ? &k_map : &v_map;
+        uint64_t *rfull = is_k ? rawk_full : rawv_full, *rempty = is_k ? rawk_empty : rawv_empty;
+        float2* scales = is_k ? rsc : rscv;
+        uint8_t* ring = sm + L::raw + (is_k ? 0 : R * PB);
+        unsigned it = 0;   // pages issued
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        unsigned items = 0;
+        int following = -1;
+        for (int item = first; item >= 0 && ok; item = following, ++items) {
+            if (is_k) {
+                int n = 0;
+                if (lane == 0) {
+                    n = next_item(a, total);
+                    if (items >= 2 && !wait_or(i_empty + (items & 1), ((items >> 1) - 1) & 1, abort, a.err, SITE_TC + 14)) {
+                        n = -1;
+                    } else {
+                        i_val[items & 1] = n;
+                        mbar_arrive(i_full + (items & 1));
+                    }
+                }
+                following = __shfl_sync(0xffffffffu, n, 0);
+            }
             Seq q;
             const Item w = find_item(a, cum, item, &q);
             const int slots = (w.p1 - w.p0 + 1) / 2 * 2;
@@ -636,26 +739,14 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     const int st = it % R;
                     bool issued = true;
                     if (lane == 0) {
-                        const int y = (pg * a.n_kv + w.kh) * KV8_PAGE;
-                        const uint32_t par = (it / R - 1) & 1;
-                        issued = it < R || wait_or(rawk_empty + st, par, abort, a.err, SITE_TC + 12);
+                        issued = it < R || wait_or(rempty + st, (it / R - 1) & 1, abort, a.err, SITE_TC + 12);
                         if (issued) {
-                            rsc[st] = make_float2(kj, vj);
+                            scales[st] = make_float2(kj, vj);
                             if (pg >= 0) {
-                                mbar_arrive_expect_tx(rawk_full + st, PB);
-                                tma_load_2d(sm + L::raw + st * PB, &k_map, rawk_full + st, 0, y);
+                                mbar_arrive_expect_tx(rfull + st, PB);
+                                tma_load_2d(ring + st * PB, map, rfull + st, 0, (pg * a.n_kv + w.kh) * KV8_PAGE);
                             } else {
-                                mbar_arrive(rawk_full + st);
-                            }
-                            ++ik;
-                            issued = it < R || wait_or(rawv_empty + st, par, abort, a.err, SITE_TC + 12);
-                        }
-                        if (issued) {
-                            if (pg >= 0) {
-                                mbar_arrive_expect_tx(rawv_full + st, PB);
-                                tma_load_2d(sm + L::raw + (R + st) * PB, &v_map, rawv_full + st, 0, y);
-                            } else {
-                                mbar_arrive(rawv_full + st);
+                                mbar_arrive(rfull + st);
                             }
                         }
                     }
@@ -669,12 +760,12 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 ks = next_ks;
                 vs = next_vs;
             }
+            if (!is_k && ok) following = next(items);
         }
         // no copy of this CTA is in flight when it ends
         if (lane == 0) {
-            const unsigned nk = ik < R ? ik : R, nv = it < R ? it : R;
-            for (unsigned i = ik - nk; i < ik; ++i) mbar_wait_bounded(rawk_full + i % R, (i / R) & 1);
-            for (unsigned i = it - nv; i < it; ++i) mbar_wait_bounded(rawv_full + i % R, (i / R) & 1);
+            const unsigned n = it < R ? it : R;
+            for (unsigned i = it - n; i < it; ++i) mbar_wait_bounded(rfull + i % R, (i / R) & 1);
         }
         __syncwarp();
     }

@@ -191,9 +191,14 @@ int dflash_kv8_append(const dflash_kv8_cache* cache, const void* k, int64_t k_ro
 size_t dflash_kv8_workspace_bytes(int32_t rows, int32_t S, int32_t n_q, int32_t n_kv, int32_t head_dim,
                                   int32_t max_pages) {
     if (check_attn_shape(rows, S, n_q, n_kv, head_dim, max_pages)) return 0;
-    // sized for the largest part of this family (the split limit grows with
-    // the SM count), so that it needs no device
-    return kv8_attn_plan(rows, S, n_q, n_kv, head_dim, max_pages, 256).bytes;
+    // the splits follow the current device's SM count (without a device: the
+    // part this library is made for)
+    int sms = 0;
+    if (sm_count(&sms)) {
+        cudaGetLastError();
+        sms = 152;
+    }
+    return kv8_attn_plan(rows, S, n_q, n_kv, head_dim, max_pages, sms > 256 ? 256 : sms).bytes;
 }
 
 int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* q, void* workspace,
@@ -250,11 +255,13 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     a.window = q->window;
     a.scale_log2 = q->scale * 1.4426950408889634f;
     a.split_cap = plan.split_cap;
+    memcpy(a.caps, plan.caps, sizeof a.caps);
     a.tile = plan.tile;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.tickets = reinterpret_cast<int*>(ws);
+    a.queue = reinterpret_cast<int*>(ws);
+    a.tickets = reinterpret_cast<int*>(ws + KV8_QUEUE_BYTES);
     a.ticket_cap = plan.ticket_cap;
-    a.part = reinterpret_cast<float*>(ws + plan.ticket_bytes);
+    a.part = reinterpret_cast<float*>(ws + KV8_QUEUE_BYTES + plan.ticket_bytes);
     a.part_cap = plan.part_cap;
     a.err = err;
     return launched(launch_kv8_attention(k_map, v_map, a, plan.form, hd, sms, reinterpret_cast<cudaStream_t>(stream)),
