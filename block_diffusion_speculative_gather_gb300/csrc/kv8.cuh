@@ -113,7 +113,7 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
 int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
                          int form, int head_dim, int sms, cudaStream_t s);
 int launch_kv8_attention_tc(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
-                            int form, int head_dim, int sms, cudaStream_t s);
+                            int head_dim, int sms, cudaStream_t s);
 // The largest dynamic shared memory, allowed once per kernel and device.
 cudaError_t allow_smem(const void* kern);
 

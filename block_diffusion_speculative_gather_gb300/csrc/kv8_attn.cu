@@ -43,10 +43,10 @@ template <int HD> struct KvSmem {
     static constexpr int ml = red + KW / 2 * KT * red_ld<HD>() * 4;    // half of the warps at a time
     static constexpr int scales = ml + KW / 2 * KT * 2 * 4;  // [stages] (k, v)
     static constexpr int bars = scales + stages<HD>() * 8;   // full, empty
-    static constexpr int items = bars + stages<HD>() * 16;   // item ring: full, empty, values
-    static constexpr int flag = items + 2 * 16 + 16;
-    static constexpr int cum = flag + 16;                    // items before each group of sequences
-    static constexpr size_t bytes = 1024 + cum + (MAX_GROUPS + 1) * 4;
+    static constexpr int items = bars + stages<HD>() * 16;   // item ring: full, empty
+    static constexpr int work = items + 2 * 16;
+    static constexpr int flag = work + 2 * sizeof(Work);
+    static constexpr size_t bytes = 1024 + flag + 16;
 };
 
 // Key of MMA column n (0..7) inside a group of 8: for 128-byte rows columns
@@ -83,9 +83,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     uint64_t* empty = full + KSTAGES;
     uint64_t* i_full = reinterpret_cast<uint64_t*>(sm + S_::items);   // [2] items on their way to the consumers
     uint64_t* i_empty = i_full + 2;
-    volatile int* i_val = reinterpret_cast<volatile int*>(i_empty + 2);
-    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] the next item
-    int* cum = reinterpret_cast<int*>(sm + S_::cum);
+    Work* ring = reinterpret_cast<Work*>(sm + S_::work);
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] there is a next item
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_trigger();
@@ -98,14 +97,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(i_full + i, 1);
-            mbar_init(i_empty + i, 1);
+            mbar_init(i_empty + i, KW);
         }
         fence_mbar_init();
         flag[1] = 0;
     }
+    __syncthreads();
     pdl_wait();
-    count_items<KTHREADS>(a, cum);   // ends with a barrier
-    const int total = total_items(a, cum);
 
     if (warp == KW) {
         // ---- producer: pages of every item of this CTA, in order.  The lanes
@@ -113,23 +111,26 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // issues these.
         unsigned it = 0;
         bool ok = true;
-        int item = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
-        for (unsigned k = 0; item >= 0 && ok; ++k) {
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
-            // the next item, for the consumers and for after this one's pages
-            int next = 0;
+        const Finder f = make_finder(a, lane);
+        int item = (int)blockIdx.x < f.total ? (int)blockIdx.x : -1;
+        for (unsigned k = 0; ok; ++k) {
+            Work wk;
+            wk.item = -1;
+            if (item >= 0) wk = find_item(a, f, item, lane);
+            int next = -1;
             if (lane == 0) {
-                next = next_item(a, total);
                 if (k >= 2 && !mbar_wait_bounded(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
                     report(a.err, DERR_TIMEOUT, SITE_EMPTY);
                     flag[1] = 1;
                 } else {
-                    i_val[k & 1] = next;
+                    ring[k & 1] = wk;
                     mbar_arrive(i_full + (k & 1));
                 }
+                if (item >= 0) next = next_item(a, f.total);
             }
+            if (item < 0) break;
             next = __shfl_sync(0xffffffffu, next, 0);
+            const Item& w = wk.w;
             auto look = [&](int b, int* page, float* ks, float* vs) {
                 *page = -1;
                 *ks = -1.f;
@@ -198,10 +199,29 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     // ---- consumers
     const int g = lane >> 2, c = lane & 3;
     unsigned base = 0;   // pages of the items before
-    int item = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
-    for (unsigned n_items = 0; item >= 0; ++n_items) {
-        Seq q;
-        const Item w = find_item(a, cum, item, &q);
+    for (unsigned n_items = 0;; ++n_items) {
+        // the next item, the same for all warps; a wait that ran out ends the CTA
+        // (err says so)
+        const int slot_i = n_items & 1;
+        if (warp == 0) {
+            const bool got = __all_sync(0xffffffffu, !flag[1] && mbar_wait_bounded(i_full + slot_i, (n_items >> 1) & 1));
+            if (lane == 0) {
+                if (!got && !flag[1]) {
+                    report(a.err, DERR_TIMEOUT, SITE_FULL);
+                    flag[1] = 1;
+                }
+                flag[2] = got;
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");   // the merge buffer is free again, too
+        if (!flag[2]) break;
+        const Work wk = ring[slot_i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i_empty + slot_i);
+        if (wk.item < 0) break;
+        const Seq& q = wk.q;
+        const Item& w = wk.w;
+        const int item = wk.item;
 
         // q of rows g, g + 8 as A fragments: k step (h, j) of 16 covers the
         // dims 64 h + 16 c + 4 j .. + 3 of every lane c of a quad, so a
@@ -505,22 +525,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             if (a.lse && (tid & 15) == 0)
                 a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
         }
-        // the next item, the same for all warps; a wait that ran out ends the CTA
-        // (err says so)
-        if (warp == 0) {
-            const int k = n_items & 1;
-            const bool got = !flag[1] && mbar_wait_bounded(i_full + k, (n_items >> 1) & 1);
-            if (lane == 0) {
-                if (!got && !flag[1]) {
-                    report(a.err, DERR_TIMEOUT, SITE_FULL);
-                    flag[1] = 1;
-                }
-                flag[2] = got ? i_val[k] : -1;
-                if (got) mbar_arrive(i_empty + k);
-            }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");   // the merge buffer is free again
-        item = flag[2];
     }
 }
 
@@ -562,8 +566,8 @@ cudaError_t allow_smem(const void* kern) {
 }
 
 // The form of a call, by its packed rows (rows x q heads of a kv head) per
-// sequence: the mma.sync kernel's 16-row tiles for few, one 128-row tensor
-// core tile whose two halves take alternate keys up to 128, two 128-row
+// sequence: the mma.sync kernel's 16-row tiles up to 16, a 64- or 128-row
+// tile whose two softmax groups take alternate keys up to 128, two 128-row
 // tiles over the same keys above.
 //
 // Both this and the splits of a tile's pages follow from the call's row,
@@ -574,16 +578,15 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
     const long long packed = (long long)rows * (n_q / n_kv);
     const long long each = (packed + S - 1) / S;
     p.form = each <= 16 ? KV8_MMA : (each <= 128 ? KV8_TC_KEYS : KV8_TC_ROWS);
-    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_KEYS ? 128 : 256);
+    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_ROWS ? 256 : (each <= 64 ? 64 : 128));
     const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
     long long usual = (packed + p.tile - 1) / p.tile;
     if (usual < S) usual = S;
     // Splits of a sequence with P pages (a value for each power of two): the
-    // count that costs least if all sequences were like it.  Rounds of items
-    // over the SMs, each as long as its pages (the mma.sync form's eight warps
-    // take a page each in the time of four) plus an item's fixed cost (start,
-    // merge, partials), about 8 pages.
-    const double fixed = 8.0;
+    // count that costs least if all sequences were like it, an item costing its
+    // pages (the mma.sync form's eight warps take a page each in the time of
+    // four) and about 6 more (start, merge, partials).
+    const double fixed = 6.0;
     long long cap = 1;
     for (int b = 0; b < 32; ++b) {
         p.caps[b] = 1;
@@ -591,11 +594,13 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
         const double pages = 1.5 * (double)(1LL << b);
         double best = 0.0;
         for (long long c = 1; c <= 64 && c <= (1LL << b); ++c) {
-            const long long rounds = (usual * n_kv * c + sms - 1) / sms;
             double len = pages / (double)c;
             const double four = 4.0 * (double)(long long)((len + 7.0) / 8.0);
             if (p.form == KV8_MMA && len < four) len = four;
-            const double cost = (double)rounds * (len + fixed);
+            // rounds of items over the SMs; behind the first, on average half an
+            // item is waited for at the end
+            const double rounds = (double)(usual * n_kv * c) / sms;
+            const double cost = rounds > 1.0 ? (rounds + 0.5) * (len + fixed) : len + fixed;
             if (c == 1 || cost < 0.95 * best) {   // partials cost bandwidth: only for a clear gain
                 best = cost;
                 p.caps[b] = (uint8_t)c;
@@ -604,7 +609,7 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
         if (p.caps[b] > cap) cap = p.caps[b];
     }
     p.split_cap = (int)cap;
-    p.ticket_cap = tiles * n_kv * (p.form == KV8_MMA ? 1 : 8);
+    p.ticket_cap = tiles * n_kv;
     p.part_cap = cap > 1 ? tiles * n_kv * cap : 0;
     p.ticket_bytes = (size_t)((p.ticket_cap * 4 + 255) / 256 * 256);
     p.bytes = KV8_QUEUE_BYTES + p.ticket_bytes + (size_t)p.part_cap * p.tile * (head_dim + 4) * 4;
@@ -613,7 +618,7 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
 
 int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
                          int form, int head_dim, int sms, cudaStream_t s) {
-    if (form != KV8_MMA) return launch_kv8_attention_tc(k_map, v_map, a, form, head_dim, sms, s);
+    if (form != KV8_MMA) return launch_kv8_attention_tc(k_map, v_map, a, head_dim, sms, s);
     if (a.dtype == 1)
         return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(k_map, v_map, a, sms, s)
                                : launch_t<__nv_bfloat16, 64>(k_map, v_map, a, sms, s);

@@ -118,74 +118,72 @@ __device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, const Seq& q, int 
     return it;
 }
 
-// Items before each group of `per` consecutive sequences (1 up to MAX_GROUPS
-// sequences), into shared memory, by the whole CTA.
-constexpr int MAX_GROUPS = 256;
+// What a CTA's warps need of an item; one warp finds it for all.
+struct Work {
+    Seq q;
+    Item w;
+    int item;           // -1: no more
+};
 
-__host__ __device__ constexpr int seqs_per_group(int S) { return (S + MAX_GROUPS - 1) / MAX_GROUPS; }
+// The finding warp's state: lane i holds the items before the i-th group of
+// `per` sequences.
+struct Finder {
+    int per, cum, total;
+};
 
-template <int THREADS>
-__device__ void count_items(const Kv8AttnArgs& a, int* cum) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int wsum[THREADS / 32];
-    const int per = seqs_per_group(a.S), groups = (a.S + per - 1) / per;
-    const int mine_n = (groups + THREADS - 1) / THREADS;
-    int mine = 0;
-    for (int k = 0; k < mine_n; ++k) {
-        const int gr = tid * mine_n + k;
-        int n = 0;
-        for (int s = gr * per; gr < groups && s < gr * per + per && s < a.S; ++s) {
-            const Seq q = seq_of(a, s);
-            n += q.tiles * a.n_kv * q.splits;
-        }
-        if (gr < groups) cum[gr] = n;
-        mine += n;
-    }
-    int inc = mine;
+__device__ __forceinline__ int items_of(const Kv8AttnArgs& a, const Seq& q) { return q.tiles * a.n_kv * q.splits; }
+
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
     }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int at = inc - mine;
-    for (int w = 0; w < warp; ++w) at += wsum[w];
-    for (int k = 0; k < mine_n; ++k) {
-        const int gr = tid * mine_n + k;
-        if (gr < groups) {
-            const int n = cum[gr];
-            cum[gr] = at;
-            at += n;
-            if (gr == groups - 1) cum[groups] = at;
+    return v;
+}
+
+__device__ __forceinline__ Finder make_finder(const Kv8AttnArgs& a, int lane) {
+    Finder f;
+    f.per = (a.S + 31) / 32;
+    int mine = 0;
+    for (int s = lane * f.per; s < a.S && s < (lane + 1) * f.per; ++s) mine += items_of(a, seq_of(a, s));
+    const int inc = warp_inclusive(mine, lane);
+    f.cum = inc - mine;
+    f.total = __shfl_sync(0xffffffffu, inc, 31);
+    return f;
+}
+
+// By the whole warp: item `item` (below the total), the same in all lanes.
+__device__ __forceinline__ Work find_item(const Kv8AttnArgs& a, const Finder& f, int item, int lane) {
+    // the last group that begins at or before it
+    const int group = __popc(__ballot_sync(0xffffffffu, f.cum <= item)) - 1;
+    int idx = item - __shfl_sync(0xffffffffu, f.cum, group);
+    int s0 = group * f.per;
+    const int end = s0 + f.per < a.S ? s0 + f.per : a.S;
+    Work k;
+    k.item = item;
+    while (true) {
+        Seq q{};
+        int n = 0;
+        if (s0 + lane < end) {
+            q = seq_of(a, s0 + lane);
+            n = items_of(a, q);
         }
+        const int inc = warp_inclusive(n, lane);
+        const unsigned at = __ballot_sync(0xffffffffu, idx < inc);
+        if (at || s0 + 32 >= end) {
+            const int l = at ? __ffs(at) - 1 : 0;
+            idx -= __shfl_sync(0xffffffffu, inc - n, l);
+            int* d = reinterpret_cast<int*>(&k.q);
+            const int* src = reinterpret_cast<const int*>(&q);
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(Seq) / 4); ++i) d[i] = __shfl_sync(0xffffffffu, src[i], l);
+            k.w = item_of(a, k.q, s0 + l, idx);
+            return k;
+        }
+        idx -= __shfl_sync(0xffffffffu, inc, 31);
+        s0 += 32;
     }
-    __syncthreads();
-}
-
-__device__ __forceinline__ int total_items(const Kv8AttnArgs& a, const int* cum) {
-    const int per = seqs_per_group(a.S);
-    return cum[(a.S + per - 1) / per];
-}
-
-// Item `item`: its sequence, that sequence's shape, and the item itself.
-__device__ __forceinline__ Item find_item(const Kv8AttnArgs& a, const int* cum, int item, Seq* q) {
-    const int per = seqs_per_group(a.S);
-    int lo = 0, hi = (a.S + per - 1) / per - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= item) lo = mid;
-        else hi = mid - 1;
-    }
-    int idx = item - cum[lo], s = lo * per;
-    *q = seq_of(a, s);
-    for (; s + 1 < a.S; ++s) {
-        const int n = q->tiles * a.n_kv * q->splits;
-        if (idx < n) break;
-        idx -= n;
-        *q = seq_of(a, s + 1);
-    }
-    return item_of(a, *q, s, idx);
 }
 
 __device__ __forceinline__ float ex2(float x) {

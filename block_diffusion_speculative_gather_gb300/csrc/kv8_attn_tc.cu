@@ -7,11 +7,13 @@
 // score tile and an output accumulator in tensor memory:
 //   ROWS form (more than 128 packed rows a sequence): the groups take two
 //     128-row tiles of q over the same keys, which are converted once;
-//   KEYS form: both take the same 128 rows and alternate 128-key steps; at
-//     the item's end the first reads the second's sums from tensor memory.
+//   KEYS form: both take the same rows and alternate 128-key steps; at the
+//     item's end each takes half of the columns of both sums from tensor
+//     memory.  Up to 64 packed rows a tile holds each row twice, and a copy's
+//     thread takes one of the step's two pages (a third less time a step).
 // Roles: two warps bring the pages' K and V codes by TMA and look up pages and
 // scales; four warps turn a step's K codes (two pages) into an f16 operand
-// tile, five its V codes into a transposed one (keys contiguous); one thread issues the MMAs:
+// tile, four its V codes into a transposed one (keys contiguous); one thread issues the MMAs:
 // S = Q K^T, then O += P V with P read from tensor memory, where the softmax
 // warps wrote it over the scores.  While one group's softmax runs, the
 // tensor core works for the other.
@@ -38,26 +40,27 @@ using namespace kv8;
 using adev::ldsm_x4_trans;
 
 // Warps: 0-7 softmax, then K's conversion, V's, the MMA issuer and two loaders.
-constexpr int KC_WARP = 8, KC = 4, VC_WARP = 12, VC = 5, MMA_WARP = 17, TMA_K = 18, TC_THREADS = 32 * 20;
+constexpr int KC_WARP = 8, KC = 4, VC_WARP = 12, VC = 4, MMA_WARP = 16, TMA_K = 17, TC_THREADS = 32 * 19;
 constexpr int STEP = 2 * KV8_PAGE;         // keys of a step
 constexpr int SITE_TC = 310;               // + role
 constexpr float LAZY = 14.f;               // rise of a row's maximum (base 2) that moves the reference
 
-template <int HD, bool KEYS> struct TcSmem {
+template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr int QB = 128 * HD * 2;                    // one q tile, f16
     static constexpr int QR = KEYS ? QB : 2 * QB;
     static constexpr int KB = STEP * HD * 2;                   // one step's K (or V), f16
     static constexpr int PB = KV8_PAGE * HD;                   // one page's K (or V) codes
     static constexpr int RAW = HD == 64 ? 8 : (KEYS ? 4 : 2);  // pages in flight, K and V each
     static constexpr int q = 0, k = q + QR, v = k + 2 * KB, raw = v + 2 * KB;
-    static constexpr int steps = raw + RAW * 2 * PB;           // [4] step scales
-    static constexpr int rsc = steps + 4 * 32;                 // [RAW] page scales
+    static constexpr int ml = raw + RAW * 2 * PB;              // DUP 2: the copies' (max, sum) of both groups
+    static constexpr int steps = ml + (DUP == 2 ? 1024 : 0);   // [8] step scales
+    static constexpr int rsc = steps + 8 * 32;                 // [RAW] page scales
     static constexpr int rscv = rsc + RAW * 8;
     static constexpr int bars = rscv + RAW * 8;
-    static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1 + 4;
-    static constexpr int misc = bars + n_bars * 8;             // tensor-memory base, abort flag, items
-    static constexpr int cum = misc + 16;
-    static constexpr size_t bytes = 1024 + cum + (MAX_GROUPS + 1) * 4;
+    static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1 + 4 + 3 + 2;
+    static constexpr int work = bars + n_bars * 8;             // [2] items
+    static constexpr int misc = work + 2 * sizeof(Work);       // tensor-memory base, abort flag, verdict
+    static constexpr size_t bytes = 1024 + misc + 16;
 };
 
 struct StepScale {      // of the two pages of a step: K scale (negative: no keys), log2 and reciprocal of V's
@@ -122,11 +125,11 @@ __device__ __forceinline__ void store16(T* p, const float (&v)[16], float f) {
     *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-template <typename T, int HD, bool KEYS>
+template <typename T, int HD, bool KEYS, int DUP>
 __global__ void __launch_bounds__(TC_THREADS, 1)
 kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                    const Kv8AttnArgs a) {
-    using L = TcSmem<HD, KEYS>;
+    using L = TcSmem<HD, KEYS, DUP>;
     constexpr int R = L::RAW, PB = L::PB;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -138,11 +141,12 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
              *k_full = bars + 4 * R, *k_empty = k_full + 2, *v_full = k_full + 4, *v_empty = k_full + 6,
              *q_full = k_full + 8, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4,
              *o_done = q_full + 6, *handed = q_full + 8, *drain = q_full + 9, *i_full = q_full + 10,
-             *i_empty = q_full + 12;
+             *i_empty = q_full + 12, *copy_full = q_full + 14, *copy_free = q_full + 16,
+             *stored = q_full + 17, *judged = q_full + 18;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
-    volatile int* i_val = reinterpret_cast<volatile int*>(sm + L::misc + 8);   // [2]
-    int* cum = reinterpret_cast<int*>(sm + L::cum);
+    volatile int* verdict = reinterpret_cast<volatile int*>(sm + L::misc + 8);
+    Work* works = reinterpret_cast<Work*>(sm + L::work);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform, so each role's code is
 
@@ -169,87 +173,104 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         mbar_init(q_free, 1);
         mbar_init(handed, 8);
         mbar_init(drain, 1);
+        mbar_init(copy_full, 2);
+        mbar_init(copy_full + 1, 2);
+        mbar_init(copy_free, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(i_full + i, 1);
             mbar_init(i_empty + i, TC_THREADS / 32 - 1);
         }
+        mbar_init(stored, 8);
+        mbar_init(judged, 1);
         fence_mbar_init();
         *abort = 0;
     }
-    pdl_wait();
     if (warp == MMA_WARP) tc::tmem_alloc(tmem_base, 512);
     tc::fence_before_sync();
-    count_items<TC_THREADS>(a, cum);   // ends with a barrier
+    __syncthreads();
     tc::fence_after_sync();
-    const int total = total_items(a, cum);
+    pdl_wait();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_base, 0);
 
-    // The item behind this warp's k-th, -1 at the end: the K loader posts them.
-    auto next = [&](unsigned k) -> int {
-        if (!__all_sync(0xffffffffu, wait_or(i_full + (k & 1), (k >> 1) & 1, abort, a.err, SITE_TC + 13))) return -1;
-        const int item = i_val[k & 1];
+    // This warp's k-th item; false at the end.  The K loader posts them.
+    auto take = [&](unsigned k, Work* wk) -> bool {
+        if (!__all_sync(0xffffffffu, wait_or(i_full + (k & 1), (k >> 1) & 1, abort, a.err, SITE_TC + 13))) return false;
+        *wk = works[k & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(i_empty + (k & 1));
-        return item;
+        return wk->item >= 0;
     };
-    const int first = (int)blockIdx.x < total ? (int)blockIdx.x : -1;
 
     if (warp < 8) {
         // ---------------------------------------------------------- softmax
         const int t = warp >> 2, r = tid & 127;      // group, row of its tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t s_tm = tm + t * 128 + lanes, o_tm = tm + 256 + t * 128 + lanes;
-        unsigned cs = 0, xs = 0, base = 0, items = 0;   // this group's steps, hand-overs, all steps, items so far
+        unsigned cs = 0, base = 0, folds = 0;   // this group's steps, all steps, split items so far
         bool ok = true;
-        for (int item = first; item >= 0 && ok; item = next(items++)) {
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
+        Work wk;
+        for (unsigned items = 0; ok && take(items, &wk); ++items) {
+            const Seq& q = wk.q;
+            const Item& w = wk.w;
+            const int item = wk.item;
             // the issuing thread is done with the item before: Q is free, and no
             // group is further ahead than the next item
             if (items > 0) {
                 ok = __all_sync(0xffffffffu, wait_or(q_free, (items - 1) & 1, abort, a.err, SITE_TC));
+                // and the copies' sums, which lie over Q, have been read
+                if (ok && DUP == 2) ok = __all_sync(0xffffffffu, wait_or(copy_free, (items - 1) & 1, abort, a.err, SITE_TC));
                 if (!ok) break;
             }
             const int n = (w.p1 - w.p0 + 1) / 2, nt = group_steps<KEYS>(a, q, w, t);
-            const int pr = w.tile * a.tile + (KEYS ? 0 : t * 128) + r;
+            const int copy = DUP == 2 ? r >> 6 : 0, row = DUP == 2 ? r & 63 : r;
+            const int pr = w.tile * a.tile + (KEYS ? 0 : t * 128) + row;
             const int qi = pr / a.group, hq = w.kh * a.group + pr % a.group;
             const bool real = qi < q.n;
             int klo = 0, khi = 0;
             float fr;
             {
-                // q: this thread's row, scaled into f16 (read twice: its largest
-                // element, then the elements)
+                // q: this thread's row, scaled into f16
                 const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
                                                                   (long long)(q.r0 + qi) * a.q_row + (long long)hq * a.q_head);
+                // 64 dims at a time, twice: the largest element, then the elements
+                uint4 e[8];
                 float top = 0.f;
-                if (real) {
-#pragma unroll 4
-                    for (int k = 0; k < HD / 8; ++k) {
-                        const uint4 e = src[k];
-                        const T* ev = reinterpret_cast<const T*>(&e);
+#pragma unroll 1
+                for (int h = 0; h < HD / 64; ++h) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) e[k] = real ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const T* ev = reinterpret_cast<const T*>(&e[k]);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float x = fabsf(to_f32(ev[j]));
                             top = fmaxf(top, x < INFINITY ? x : 0.f);
                         }
                     }
-                    row_keys(a, q, qi, &klo, &khi);
                 }
+                if (real) row_keys(a, q, qi, &klo, &khi);
                 float inv, back;
                 row_factor(top, &inv, &back);
                 fr = back * a.scale_log2;
                 if (!KEYS || t == 0) {
                     uint8_t* qs = sm + L::q + (KEYS ? 0 : t * L::QB);
-#pragma unroll 4
-                    for (int k = 0; k < HD / 8; ++k) {
-                        const uint4 e = real ? src[k] : make_uint4(0, 0, 0, 0);
-                        const T* ev = reinterpret_cast<const T*>(&e);
-                        uint4 h;
-                        uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
+#pragma unroll 1
+                    for (int h = 0; h < HD / 64; ++h) {
+                        if (HD > 64) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            hw[j] = pack_f16x2(to_f32(ev[2 * j]) * inv, to_f32(ev[2 * j + 1]) * inv);
-                        *reinterpret_cast<uint4*>(qs + (k >> 3) * 128 * 128 + swz128(r, k & 7)) = h;
+                            for (int k = 0; k < 8; ++k) e[k] = real ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const T* ev = reinterpret_cast<const T*>(&e[k]);
+                            uint4 o;
+                            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ow[j] = pack_f16x2(to_f32(ev[2 * j]) * inv, to_f32(ev[2 * j + 1]) * inv);
+                            *reinterpret_cast<uint4*>(qs + h * 128 * 128 + swz128(r, k)) = o;
+                        }
                     }
                     tc::fence_async_smem();
                 }
@@ -270,14 +291,23 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     continue;
                 }
                 tc::fence_after_sync();
-                const StepScale sc = steps[(base + j) & 3];
+                const StepScale& sc = steps[(base + j) & 7];
                 const int k0 = (w.p0 + 2 * j) * KV8_PAGE;
                 // 32 keys at a time, the next 32 scores on their way meanwhile
                 uint32_t buf[2][32];
-                tc::ld_x32_async(s_tm, buf[0]);
+                const int c0 = 2 * copy;
+                tc::ld_x32_async(s_tm + c0 * 32, buf[0]);
+                if (DUP == 2) {      // the other page's weights are the other copy's
+                    uint32_t p[16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t (&v)[32] = buf[c & 1];
+                    for (int x = 0; x < 16; ++x) p[x] = 0;
+                    tc::st_x16(s_tm + (2 - c0) * 32, p);
+                    tc::st_x16(s_tm + (3 - c0) * 32, p);
+                }
+#pragma unroll
+                for (int cc = 0; cc < 4 / DUP; ++cc) {
+                    const int c = c0 + cc;
+                    uint32_t (&v)[32] = buf[cc & 1];
                     tc::ld_wait(v);
                     const int kp = k0 + c * 32;
                     const float ks = sc.ks[c >> 1], ev = sc.ev[c >> 1];
@@ -308,7 +338,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         if (__any_sync(0xffffffffu, f0 != 1.f && f0 != 0.f)) {
                             tc::st_wait();
 #pragma unroll 1
-                            for (int b = 0; b < c; ++b) {
+                            for (int b = c0; b < c; ++b) {
                                 uint32_t p[16];
                                 tc::ld_x16(s_tm + b * 32, p);
 #pragma unroll
@@ -332,7 +362,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                             }
                         }
                     }
-                    if (c < 3) tc::ld_x32_async(s_tm + (c + 1) * 32, buf[(c + 1) & 1]);
+                    if (cc < 4 / DUP - 1) tc::ld_x32_async(s_tm + (c + 1) * 32, buf[(cc + 1) & 1]);
                     const float off = ev - (M == -INFINITY ? 0.f : M);
                     const float2 ff = make_float2(f, f), oo = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -374,9 +404,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(handed);
-                ok = __all_sync(0xffffffffu, wait_or(handed, xs & 1, abort, a.err, SITE_TC + 4));
+                ok = __all_sync(0xffffffffu, wait_or(handed, items & 1, abort, a.err, SITE_TC + 4));
                 if (!ok) break;
-                ++xs;
                 tc::fence_after_sync();
                 float bm, bl;
                 tc::ld_x2(s_tm + other, &bm, &bl);
@@ -391,14 +420,26 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             const int c_first = KEYS && t == 1 ? HD / 64 : 0, c_last = KEYS && t == 0 ? HD / 64 : HD / 32;
 
             // ---- the row's outputs, or its partial of this split
-            const int wi = warp;   // a ticket for each warp's rows (and columns)
             const long long slot0 = (long long)item - w.split;    // splits of a tile are neighbours
-            const long long tk = (((long long)q.r0 * a.group / a.tile + w.s + w.tile) * a.n_kv + w.kh) * 8 + wi;
+            const long long tk = ((long long)q.r0 * a.group / a.tile + w.s + w.tile) * a.n_kv + w.kh;
             const bool split = q.splits > 1;
             const bool fits = !split || (slot0 + q.splits <= a.part_cap && tk < a.ticket_cap);   // by the plan's bounds
             const int RT = a.tile;
             const long long PL = (long long)RT * (HD + 4);         // floats of a partial
-            const int prow = KEYS ? r : t * 128 + r;
+            const int prow = KEYS ? row : t * 128 + row;
+            float4* xb = reinterpret_cast<float4*>(sm + L::q + t * (L::QB / 2));       // [8 columns / 32][64 rows]
+            float2* xml = reinterpret_cast<float2*>(sm + L::ml) + t * 64;
+            float ga = 1.f, gb = 0.f;      // factors of this copy's and the other's sums
+            if (DUP == 2 && copy == 0) {
+                ok = __all_sync(0xffffffffu, wait_or(copy_full + t, items & 1, abort, a.err, SITE_TC + 15));
+                if (!ok) break;
+                const float2 b = xml[row];
+                const float m = fmaxf(M, b.x);
+                ga = M == -INFINITY ? 0.f : ex2(M - m);
+                gb = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+                l = (l != 0.f ? l * ga : 0.f) + (b.y != 0.f ? b.y * gb : 0.f);
+                M = m;
+            }
             float* part = split ? a.part + (slot0 + w.split) * PL : nullptr;
             T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
             const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no key: zeros
@@ -418,6 +459,22 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
 #pragma unroll
                     for (int x = 0; x < 32; ++x) v[x] = fmaf(u[x], fb, v[x] * fa);
                 }
+                if (DUP == 2) {
+                    float4* xc = xb + (c - c_first) * 8 * 64 + row;
+                    if (copy == 1) {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) xc[x * 64] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 y = xc[x * 64];
+                        v[4 * x] = fmaf(y.x, gb, v[4 * x] * ga);
+                        v[4 * x + 1] = fmaf(y.y, gb, v[4 * x + 1] * ga);
+                        v[4 * x + 2] = fmaf(y.z, gb, v[4 * x + 2] * ga);
+                        v[4 * x + 3] = fmaf(y.w, gb, v[4 * x + 3] * ga);
+                    }
+                }
                 if (real && split && fits) {
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
@@ -434,77 +491,88 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     }
                 }
             }
+            if (DUP == 2 && copy == 1) xml[row] = make_float2(M, l);
             __syncwarp();
             tc::fence_before_sync();   // the accumulator has been read
+            if (DUP == 2 && lane == 0) mbar_arrive(copy == 1 ? copy_full + t : copy_free);
             if (!split) {
-                if (real && a.lse && c_first == 0)
+                if (real && copy == 0 && a.lse && c_first == 0)
                     a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
                 continue;
             }
-            if (real && fits) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow + (c_first ? RT : 0)] = make_float2(M, l);
+            if (real && fits && copy == 0 && c_first == 0) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow] = make_float2(M, l);
+            // the CTA whose split of the tile is the last to arrive folds them all, in
+            // split order: a thread takes a row and a share of its columns
             __threadfence();
             __syncwarp();
-            int last = 0;
-            if (lane == 0) last = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
-            last = __shfl_sync(0xffffffffu, last, 0);
-            if (!last) continue;
-            __threadfence();
-            if (lane == 0) a.tickets[tk] = 0;
-            if (!real) continue;
-            // the last split's warp folds its rows of all splits, in split order
-            const float* src = a.part + slot0 * PL;
-            const float2* mls = reinterpret_cast<const float2*>(src + (size_t)RT * HD) + prow + (c_first ? RT : 0);
-            const long long PL2 = PL / 2;
-            float fm = -INFINITY, fl = 0.f;
-            for (int v = 0; v < q.splits; ++v) fm = fmaxf(fm, __ldcg(mls + v * PL2).x);
-            for (int v = 0; v < q.splits; ++v) {
-                const float2 x = __ldcg(mls + v * PL2);
-                fl = fmaf(x.y, x.x == -INFINITY ? 0.f : ex2(x.x - fm), fl);
+            if (lane == 0) mbar_arrive(stored);
+            if (warp == 0) {
+                ok = __all_sync(0xffffffffu, wait_or(stored, folds & 1, abort, a.err, SITE_TC + 15));
+                if (!ok) break;
+                if (lane == 0) {
+                    *verdict = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
+                    if (*verdict) a.tickets[tk] = 0;
+                    mbar_arrive(judged);
+                }
+                __syncwarp();
             }
-            const float finv = fl == 0.f ? 0.f : 1.f / fl;
+            ok = __all_sync(0xffffffffu, wait_or(judged, folds & 1, abort, a.err, SITE_TC + 15));
+            if (!ok) break;
+            ++folds;
+            if (!*verdict) continue;
+            __threadfence();
+            const int frow = tid % RT, shares = 256 / RT, share = tid / RT;
+            const int fr_ = w.tile * RT + frow, fi = fr_ / a.group, fh = w.kh * a.group + fr_ % a.group;
+            if (fi < q.n) {
+                const float* src = a.part + slot0 * PL;
+                const float2* mls = reinterpret_cast<const float2*>(src + (size_t)RT * HD) + frow;
+                const long long PL2 = PL / 2;
+                float fm = -INFINITY, fl = 0.f;
+#pragma unroll 4
+                for (int v = 0; v < q.splits; ++v) fm = fmaxf(fm, __ldcg(mls + v * PL2).x);
+#pragma unroll 4
+                for (int v = 0; v < q.splits; ++v) {
+                    const float2 x = __ldcg(mls + v * PL2);
+                    fl = fmaf(x.y, x.x == -INFINITY ? 0.f : ex2(x.x - fm), fl);
+                }
+                const float finv = fl == 0.f ? 0.f : 1.f / fl;
+                T* fdst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + fi) * a.out_row + (long long)fh * a.out_head;
 #pragma unroll 1
-            for (int b = 2 * c_first; b < 2 * c_last; ++b) {
-                float o[16];
+                for (int b = share * (HD / 16) / shares; b < (share + 1) * (HD / 16) / shares; ++b) {
+                    float o[16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = 0.f;
-                const float4* col = reinterpret_cast<const float4*>(src) + (size_t)b * 4 * RT + prow;
-                for (int v0 = 0; v0 < q.splits; v0 += 2) {     // two splits' loads in flight
-                    float4 y[2][4];
-                    float m[2];
+                    for (int x = 0; x < 16; ++x) o[x] = 0.f;
+                    const float4* col = reinterpret_cast<const float4*>(src) + (size_t)b * 4 * RT + frow;
+#pragma unroll 2
+                    for (int v = 0; v < q.splits; ++v) {
+                        float4 y[4];
+                        const float m = __ldcg(mls + v * PL2).x;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int v = v0 + k < q.splits ? v0 + k : v0;
-                        m[k] = __ldcg(mls + v * PL2).x;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) y[k][x] = __ldcg(col + v * (PL / 4) + x * RT);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (v0 + k >= q.splits) break;
-                        const float f = m[k] == -INFINITY ? 0.f : ex2(m[k] - fm);
+                        for (int x = 0; x < 4; ++x) y[x] = __ldcg(col + v * (PL / 4) + x * RT);
+                        const float f = m == -INFINITY ? 0.f : ex2(m - fm);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            o[4 * x] = fmaf(y[k][x].x, f, o[4 * x]);
-                            o[4 * x + 1] = fmaf(y[k][x].y, f, o[4 * x + 1]);
-                            o[4 * x + 2] = fmaf(y[k][x].z, f, o[4 * x + 2]);
-                            o[4 * x + 3] = fmaf(y[k][x].w, f, o[4 * x + 3]);
+                            o[4 * x] = fmaf(y[x].x, f, o[4 * x]);
+                            o[4 * x + 1] = fmaf(y[x].y, f, o[4 * x + 1]);
+                            o[4 * x + 2] = fmaf(y[x].z, f, o[4 * x + 2]);
+                            o[4 * x + 3] = fmaf(y[x].w, f, o[4 * x + 3]);
                         }
                     }
+                    store16<T>(fdst + 16 * b, o, finv);
                 }
-                store16<T>(dst + 16 * b, o, finv);
+                if (a.lse && share == 0)
+                    a.lse[(long long)(q.r0 + fi) * a.n_q + fh] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
             }
-            if (a.lse && c_first == 0)
-                a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
+            __syncwarp();
         }
     } else if (warp < VC_WARP) {
         // ---------------------------------------------------------- K's conversion
         const int cw = warp - KC_WARP;
         unsigned g = 0;     // steps so far
         bool ok = true;
-        unsigned items = 0;
-        for (int item = first; item >= 0 && ok; item = next(items++)) {
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
+        Work wk;
+        for (unsigned items = 0; ok && take(items, &wk); ++items) {
+            const Item& w = wk.w;
             const int n = (w.p1 - w.p0 + 1) / 2;
             for (int j = 0; j < n; ++j, ++g) {
                 const int st = g & 1;
@@ -516,7 +584,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 if (!ok) break;
                 if (cw == 0 && lane < 2) {
                     const float2 sc = rsc[r0 + lane];
-                    StepScale* d = steps + (g & 3);
+                    StepScale* d = steps + (g & 7);
                     d->ks[lane] = sc.y > 0.f ? sc.x : -1.f;
                     d->ev[lane] = sc.y > 0.f ? log2f(sc.y) : 0.f;
                     d->iv[lane] = sc.y > 0.f ? 1.f / sc.y : 0.f;
@@ -524,12 +592,20 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 uint8_t* dst = sm + L::k + st * L::KB;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {                  // the step's pages
+                    constexpr int MINE = HD / 8 / KC;          // units of 32 keys x 16 dims
+                    uint4 e[MINE];
 #pragma unroll
-                    for (int y = 0; y < HD / 8 / KC; ++y) {    // units of 32 keys x 16 dims
-                        const int u = cw + y * KC, key = (u & 1) * 32 + lane, c = u >> 1;
+                    for (int y = 0; y < MINE; ++y) {
+                        const int u = cw + y * KC;
                         // a page that is not there: its scores are masked whatever the bytes
-                        const uint4 e = lds128(sm + L::raw + (r0 + h) * PB + tile_off<HD>(key, c));
-                        const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+                        e[y] = lds128(sm + L::raw + (r0 + h) * PB + tile_off<HD>((u & 1) * 32 + lane, u >> 1));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawk_empty + r0 + h);   // its codes have been read
+#pragma unroll
+                    for (int y = 0; y < MINE; ++y) {
+                        const int u = cw + y * KC, key = (u & 1) * 32 + lane, c = u >> 1;
+                        const uint32_t ew[4] = {e[y].x, e[y].y, e[y].z, e[y].w};
                         uint32_t o[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -540,8 +616,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rawk_empty + r0 + h);   // its codes have been read
                 }
                 tc::fence_async_smem();
                 __syncwarp();
@@ -553,10 +627,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         const int cw = warp - VC_WARP;
         unsigned g = 0;
         bool ok = true;
-        unsigned items = 0;
-        for (int item = first; item >= 0 && ok; item = next(items++)) {
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
+        Work wk;
+        for (unsigned items = 0; ok && take(items, &wk); ++items) {
+            const Item& w = wk.w;
             const int n = (w.p1 - w.p0 + 1) / 2;
             for (int j = 0; j < n; ++j, ++g) {
                 const int st = g & 1;
@@ -572,31 +645,36 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 const int kp = (w.p0 + 2 * j) * KV8_PAGE;
                 const bool plain = kp >= w.lo && kp + STEP <= w.hi && there[0] && there[1];
                 uint8_t* dst = sm + L::v + st * L::KB;
-                constexpr int UNITS = HD / 8;                  // of 32 keys x 16 dims, in a page
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    constexpr int MINE = HD / 8 / VC;          // units of 32 keys x 16 dims
+                    uint32_t r4[MINE][4];
 #pragma unroll
-                    for (int y = 0; y < (UNITS + VC - 1) / VC; ++y) {
-                        // the second page's units begin with another warp, as they
-                        // do not divide evenly
-                        const int x = (cw + 2 * h) % VC + y * VC;
-                        if (x >= UNITS) break;
-                        const int kb = x & 1, d = x >> 1;
-                        uint32_t r4[4];
-                        ldsm_x4_trans(r4, sm + L::raw + (R + r0 + h) * PB + tile_off<HD>(kb * 32 + lane, d));
-                        if (!plain) {
-                            const bool valid = h ? there[1] : there[0];
+                    for (int y = 0; y < MINE; ++y) {
+                        const int x = cw + y * VC;
+                        ldsm_x4_trans(r4[y], sm + L::raw + (R + r0 + h) * PB + tile_off<HD>((x & 1) * 32 + lane, x >> 1));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawv_empty + r0 + h);
+                    if (!plain) {
+                        const bool valid = h ? there[1] : there[0];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int k = kp + h * KV8_PAGE + kb * 32 + 8 * i + 2 * (lane & 3);
-                                r4[i] &= (valid && k >= w.lo && k < w.hi ? 0x0000ffffu : 0u) |
-                                         (valid && k + 1 >= w.lo && k + 1 < w.hi ? 0xffff0000u : 0u);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            // VC is even, so all of this warp's units have the same 32 keys
+                            const int k = kp + h * KV8_PAGE + (cw & 1) * 32 + 8 * i + 2 * (lane & 3);
+                            const uint32_t keep = (valid && k >= w.lo && k < w.hi ? 0x0000ffffu : 0u) |
+                                                  (valid && k + 1 >= w.lo && k + 1 < w.hi ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int y = 0; y < MINE; ++y) r4[y][i] &= keep;
                         }
+                    }
+#pragma unroll
+                    for (int y = 0; y < MINE; ++y) {
+                        const int x = cw + y * VC, kb = x & 1, d = x >> 1;
                         uint32_t e[4], o[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t p = __byte_perm(r4[i], 0, 0x3120);
+                            const uint32_t p = __byte_perm(r4[y][i], 0, 0x3120);
                             e[i] = f16_of_codes(p);
                             o[i] = f16_of_codes(p >> 16);
                         }
@@ -605,8 +683,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         stsm_x4(vd + swz128(row, ch), e);
                         stsm_x4(vd + swz128(row + 8, ch), o);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rawv_empty + r0 + h);
                 }
                 tc::fence_async_smem();
                 __syncwarp();
@@ -618,14 +694,15 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         // the warp stays converged and one lane issues: what an MMA names is
         // uniform (issuing from a divergent lane took about twice as long)
         constexpr uint32_t IS = tc::idesc_f16_f32(128, STEP), IO = tc::idesc_f16_f32(128, HD);
-        unsigned base = 0, items = 0, done[2] = {0, 0};
+        unsigned base = 0, done[2] = {0, 0};
         bool ok = true;
         // descriptors of the tiles' first bytes; a k step adds 32 bytes, a
         // 64-element half of K or Q its rows (in 16-byte units)
         const uint64_t qd = tc::desc_sw128(sm + L::q), kd = tc::desc_sw128(sm + L::k), vd = tc::desc_sw128(sm + L::v);
-        for (int item = first; item >= 0 && ok; item = next(items++)) {
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
+        Work wk;
+        for (unsigned items = 0; ok && take(items, &wk); ++items) {
+            const Seq& q = wk.q;
+            const Item& w = wk.w;
             const int n = (w.p1 - w.p0 + 1) / 2;
             const int nt[2] = {__shfl_sync(0xffffffffu, group_steps<KEYS>(a, q, w, 0), 0),
                                __shfl_sync(0xffffffffu, group_steps<KEYS>(a, q, w, 1), 0)};
@@ -692,24 +769,32 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         uint8_t* ring = sm + L::raw + (is_k ? 0 : R * PB);
         unsigned it = 0;   // pages issued
         bool ok = true;
-        unsigned items = 0;
-        int following = -1;
-        for (int item = first; item >= 0 && ok; item = following, ++items) {
+        Finder f{};
+        int item = -1;
+        if (is_k) {
+            f = make_finder(a, lane);
+            item = (int)blockIdx.x < f.total ? (int)blockIdx.x : -1;
+        }
+        Work wk;
+        for (unsigned items = 0; ok; ++items) {
             if (is_k) {
-                int n = 0;
+                // finds and posts the item; the next one's number is on its way
+                wk.item = -1;
+                if (item >= 0) wk = find_item(a, f, item, lane);
+                int n = -1;
                 if (lane == 0) {
-                    n = next_item(a, total);
-                    if (items >= 2 && !wait_or(i_empty + (items & 1), ((items >> 1) - 1) & 1, abort, a.err, SITE_TC + 14)) {
-                        n = -1;
-                    } else {
-                        i_val[items & 1] = n;
+                    if (items < 2 || wait_or(i_empty + (items & 1), ((items >> 1) - 1) & 1, abort, a.err, SITE_TC + 14)) {
+                        works[items & 1] = wk;
                         mbar_arrive(i_full + (items & 1));
                     }
+                    if (item >= 0) n = next_item(a, f.total);
                 }
-                following = __shfl_sync(0xffffffffu, n, 0);
+                if (item < 0) break;
+                item = __shfl_sync(0xffffffffu, n, 0);
+            } else if (!take(items, &wk)) {
+                break;
             }
-            Seq q;
-            const Item w = find_item(a, cum, item, &q);
+            const Item& w = wk.w;
             const int slots = (w.p1 - w.p0 + 1) / 2 * 2;
             // lane i looks up page b + i and its scales; the next 32 are on their
             // way while these are issued
@@ -760,7 +845,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 ks = next_ks;
                 vs = next_vs;
             }
-            if (!is_k && ok) following = next(items);
         }
         // no copy of this CTA is in flight when it ends
         if (lane == 0) {
@@ -775,30 +859,32 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     if (warp == MMA_WARP) tc::tmem_dealloc(tm, 512);
 }
 
-template <typename T, int HD, bool KEYS>
+template <typename T, int HD, bool KEYS, int DUP>
 int launch_tc(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int sms, cudaStream_t s) {
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_attn_tc_kernel<T, HD, KEYS>));
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_attn_tc_kernel<T, HD, KEYS, DUP>));
     if (e != cudaSuccess) return (int)e;
-    const long long most = a.ticket_cap / 8 * a.split_cap;   // items there can be
+    const long long most = a.ticket_cap * a.split_cap;   // items there can be
     const long long grid = most < sms ? most : sms;
-    return (int)launch_k(kv8_attn_tc_kernel<T, HD, KEYS>, dim3((unsigned)grid), dim3(TC_THREADS),
-                         TcSmem<HD, KEYS>::bytes, s, k_map, v_map, a);
+    return (int)launch_k(kv8_attn_tc_kernel<T, HD, KEYS, DUP>, dim3((unsigned)grid), dim3(TC_THREADS),
+                         TcSmem<HD, KEYS, DUP>::bytes, s, k_map, v_map, a);
 }
 
-template <typename T>
-int launch_tc_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int form, int hd,
-                int sms, cudaStream_t s) {
-    if (form == KV8_TC_KEYS)
-        return hd == 128 ? launch_tc<T, 128, true>(k_map, v_map, a, sms, s) : launch_tc<T, 64, true>(k_map, v_map, a, sms, s);
-    return hd == 128 ? launch_tc<T, 128, false>(k_map, v_map, a, sms, s) : launch_tc<T, 64, false>(k_map, v_map, a, sms, s);
+template <typename T, int HD>
+int launch_tc_t(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a, int sms, cudaStream_t s) {
+    if (a.tile == 64) return launch_tc<T, HD, true, 2>(k_map, v_map, a, sms, s);
+    if (a.tile == 128) return launch_tc<T, HD, true, 1>(k_map, v_map, a, sms, s);
+    return launch_tc<T, HD, false, 1>(k_map, v_map, a, sms, s);
 }
 
 }  // namespace
 
 int launch_kv8_attention_tc(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
-                            int form, int head_dim, int sms, cudaStream_t s) {
-    return a.dtype == 1 ? launch_tc_t<__nv_bfloat16>(k_map, v_map, a, form, head_dim, sms, s)
-                        : launch_tc_t<__half>(k_map, v_map, a, form, head_dim, sms, s);
+                            int head_dim, int sms, cudaStream_t s) {
+    if (a.dtype == 1)
+        return head_dim == 128 ? launch_tc_t<__nv_bfloat16, 128>(k_map, v_map, a, sms, s)
+                               : launch_tc_t<__nv_bfloat16, 64>(k_map, v_map, a, sms, s);
+    return head_dim == 128 ? launch_tc_t<__half, 128>(k_map, v_map, a, sms, s)
+                           : launch_tc_t<__half, 64>(k_map, v_map, a, sms, s);
 }
 
 }  // namespace dfl
