@@ -90,7 +90,7 @@ struct Kv8AttnArgs {
     float scale_log2;           // softmax scale * log2(e)
     int split_cap;              // most splits of a tile's keys
     uint8_t caps[32];           // splits at most of a sequence with 2^b .. 2^(b+1) - 1 pages to read
-    int tile;                   // packed (row, q head) rows of an item
+    int tile, tile_log2;        // packed (row, q head) rows of an item
     float* part;                // [part_cap] partial tiles
     long long part_cap;
     int* queue;                 // [next item, CTAs done], zero between calls

@@ -566,9 +566,10 @@ cudaError_t allow_smem(const void* kern) {
 }
 
 // The form of a call, by its packed rows (rows x q heads of a kv head) per
-// sequence: the mma.sync kernel's 16-row tiles up to 16, a 64- or 128-row
-// tile whose two softmax groups take alternate keys up to 128, two 128-row
-// tiles over the same keys above.
+// sequence: the mma.sync kernel's 16-row tiles up to 16, a tile whose two
+// softmax groups take alternate keys up to 128 (64 rows where a block of 16
+// rows fits, as sequences differ and a second tile reads the keys again; 128
+// else), two 128-row tiles over the same keys above.
 //
 // Both this and the splits of a tile's pages follow from the call's row,
 // sequence and head counts and the sequence's own length alone: its results
@@ -578,15 +579,15 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
     const long long packed = (long long)rows * (n_q / n_kv);
     const long long each = (packed + S - 1) / S;
     p.form = each <= 16 ? KV8_MMA : (each <= 128 ? KV8_TC_KEYS : KV8_TC_ROWS);
-    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_ROWS ? 256 : (each <= 64 ? 64 : 128));
+    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_ROWS ? 256 : (each <= 64 && 16 * (n_q / n_kv) <= 64 ? 64 : 128));
     const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
     long long usual = (packed + p.tile - 1) / p.tile;
     if (usual < S) usual = S;
     // Splits of a sequence with P pages (a value for each power of two): the
     // count that costs least if all sequences were like it, an item costing its
     // pages (the mma.sync form's eight warps take a page each in the time of
-    // four) and about 6 more (start, merge, partials).
-    const double fixed = 6.0;
+    // four) and 12 (24) more for its start, merge and partials.
+    const double fixed = p.form == KV8_MMA ? 12.0 : 24.0;
     long long cap = 1;
     for (int b = 0; b < 32; ++b) {
         p.caps[b] = 1;
@@ -598,9 +599,9 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
             const double four = 4.0 * (double)(long long)((len + 7.0) / 8.0);
             if (p.form == KV8_MMA && len < four) len = four;
             // rounds of items over the SMs; behind the first, on average half an
-            // item is waited for at the end
+            // item is waited for at the end; folding costs more than a page a split
             const double rounds = (double)(usual * n_kv * c) / sms;
-            const double cost = rounds > 1.0 ? (rounds + 0.5) * (len + fixed) : len + fixed;
+            const double cost = (rounds > 1.0 ? (rounds + 0.5) * (len + fixed) : len + fixed) + 1.3 * (double)(c - 1);
             if (c == 1 || cost < 0.95 * best) {   // partials cost bandwidth: only for a clear gain
                 best = cost;
                 p.caps[b] = (uint8_t)c;

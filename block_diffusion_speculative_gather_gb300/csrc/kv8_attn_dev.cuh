@@ -60,7 +60,7 @@ __device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
     q.page_lo = lo / KV8_PAGE;
     q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
     const int pages = q.page_hi > q.page_lo ? q.page_hi - q.page_lo : 0;
-    q.tiles = (int)(((long long)q.n * a.group + a.tile - 1) / a.tile);
+    q.tiles = (int)(((long long)q.n * a.group + a.tile - 1) >> a.tile_log2);
     const int most = a.caps[31 - __clz(pages | 1)];
     q.len = (pages + most - 1) / most;
     if (q.len < 1) q.len = 1;
@@ -129,6 +129,7 @@ struct Work {
 // `per` sequences.
 struct Finder {
     int per, cum, total;
+    Seq q;              // of this lane's sequence where per is 1
 };
 
 __device__ __forceinline__ int items_of(const Kv8AttnArgs& a, const Seq& q) { return q.tiles * a.n_kv * q.splits; }
@@ -146,7 +147,11 @@ __device__ __forceinline__ Finder make_finder(const Kv8AttnArgs& a, int lane) {
     Finder f;
     f.per = (a.S + 31) / 32;
     int mine = 0;
-    for (int s = lane * f.per; s < a.S && s < (lane + 1) * f.per; ++s) mine += items_of(a, seq_of(a, s));
+    f.q = Seq{};
+    for (int s = lane * f.per; s < a.S && s < (lane + 1) * f.per; ++s) {
+        f.q = seq_of(a, s);
+        mine += items_of(a, f.q);
+    }
     const int inc = warp_inclusive(mine, lane);
     f.cum = inc - mine;
     f.total = __shfl_sync(0xffffffffu, inc, 31);
@@ -165,7 +170,13 @@ __device__ __forceinline__ Work find_item(const Kv8AttnArgs& a, const Finder& f,
     while (true) {
         Seq q{};
         int n = 0;
-        if (s0 + lane < end) {
+        if (f.per == 1) {          // the group's only sequence, into lane 0
+            int* d = reinterpret_cast<int*>(&q);
+            const int* src = reinterpret_cast<const int*>(&f.q);
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(Seq) / 4); ++i) d[i] = __shfl_sync(0xffffffffu, src[i], group);
+            n = lane == 0 ? items_of(a, q) : 0;
+        } else if (s0 + lane < end) {
             q = seq_of(a, s0 + lane);
             n = items_of(a, q);
         }

@@ -257,6 +257,7 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     a.split_cap = plan.split_cap;
     memcpy(a.caps, plan.caps, sizeof a.caps);
     a.tile = plan.tile;
+    while ((1 << a.tile_log2) < plan.tile) ++a.tile_log2;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.queue = reinterpret_cast<int*>(ws);
     a.tickets = reinterpret_cast<int*>(ws + KV8_QUEUE_BYTES);
