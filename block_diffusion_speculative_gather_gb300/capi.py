@@ -445,17 +445,13 @@ def dflash_batch_destroy(b) -> None:
 # comparisons, and only a call that fails one goes through the checks that
 # name the tensor at fault.
 
-_I32 = torch.int32
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _KINDS = {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
 _HALVES = (torch.bfloat16, torch.float16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _CACHE = struct.Struct("4Q4i")        # dflash_kv8_cache
 _QUERY = struct.Struct("6Q4q7if")     # dflash_kv8_query
 _HEADS = struct.Struct("2Q2i4q")      # dflash_heads
-
-
-def _device() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
 def _raw(stream, dev: int) -> int:
@@ -468,6 +464,13 @@ def _flat(tensors, dev: int, dtype=_I32) -> bool:
         if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
             return False
     return True
+
+
+def _current(t) -> int:
+    """The tensor's device where it is the current CUDA device, else -2 (no
+    tensor is there)."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -2
 
 
 def _here(**tensors) -> None:
@@ -492,25 +495,22 @@ def _need_heads(t, name: str, dtypes, shape) -> None:
         raise DFlashError(DFLASH_ERR_ARG, f"{name}: the elements of a head must be contiguous")
 
 
-def _vectors(*tensors) -> bool:
-    return all(isinstance(t, torch.Tensor) for t in tensors)
-
-
 def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, positions, slots, kv_after,
                       n_free_out, stream=None):
     """Pages, row starts, positions and slots of the next step's rows (see
     include/dflash.h); rows = positions.numel().  int32 tensors throughout."""
-    named = (kv_len, q_len, kv_after, free_pages, n_free, n_free_out, row_start, positions, slots, table)
-    dev = _device() if _vectors(*named) and table.is_cuda and table.dim() == 2 else -1
-    if dev >= 0:
+    try:
+        dev = _current(table)
         S, max_pages = table.shape
-        rows = positions.numel()
-        one = (S,)
-        if not (_flat(named, dev) and kv_len.shape == one and q_len.shape == one and kv_after.shape == one and
-                free_pages.dim() == 1 and n_free.shape == (1,) and n_free_out.shape == (1,) and
-                row_start.shape == (S + 1,) and positions.dim() == 1 and slots.shape == (rows,)):
-            dev = -1
-    if dev < 0:
+        one, (rows,), (pool,) = (S,), positions.shape, free_pages.shape
+        fine = (kv_len.shape == one and q_len.shape == one and kv_after.shape == one and
+                n_free.shape == (1,) and n_free_out.shape == (1,) and row_start.shape == (S + 1,) and
+                slots.shape == (rows,) and
+                _flat((table, kv_len, q_len, kv_after, free_pages, n_free, n_free_out, row_start, positions,
+                       slots), dev))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
         i32 = (_I32,)
         _need(table, "table", i32, (None, None))
         S, max_pages = table.shape
@@ -521,16 +521,15 @@ def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, posit
         _need(n_free_out, "n_free_out", i32, (1,))
         _need(row_start, "row_start", i32, (S + 1,))
         _need(positions, "positions", i32, (None,))
-        rows = positions.shape[0]
-        _need(slots, "slots", i32, (rows,))
+        _need(slots, "slots", i32, (positions.shape[0],))
         _here(kv_len=kv_len, q_len=q_len, free_pages=free_pages, n_free=n_free, table=table,
               row_start=row_start, positions=positions, slots=slots, kv_after=kv_after,
               n_free_out=n_free_out)
-        dev = _device()
-    rc = lib.dflash_pages_plan(kv_len.data_ptr(), q_len.data_ptr(), S, free_pages.data_ptr(),
-                               free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages, rows,
-                               row_start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
-                               kv_after.data_ptr(), n_free_out.data_ptr(), _raw(stream, dev))
+        dev, rows, pool = table.get_device(), positions.shape[0], free_pages.shape[0]
+    rc = lib.dflash_pages_plan(kv_len.data_ptr(), q_len.data_ptr(), S, free_pages.data_ptr(), pool,
+                               n_free.data_ptr(), table.data_ptr(), max_pages, rows, row_start.data_ptr(),
+                               positions.data_ptr(), slots.data_ptr(), kv_after.data_ptr(),
+                               n_free_out.data_ptr(), _raw(stream, dev))
     if rc:
         check(rc)
 
@@ -548,53 +547,56 @@ def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
     _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
     check(lib.dflash_pages_trim(kv_len.data_ptr(), new_len.data_ptr(), S, free_pages.data_ptr(),
                                 free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages,
-                                _raw(stream, _device())))
+                                _raw(stream, table.get_device())))
 
 
-def _cache_ok(k_codes, v_codes, k_scale, v_scale, dev: int) -> bool:
-    shape = k_codes.shape
-    return (len(shape) == 4 and shape[2] == KV8_PAGE and v_codes.shape == shape and
-            k_scale.shape == shape[:2] and v_scale.shape == shape[:2] and k_codes.dtype in _CODES and
-            v_codes.dtype in _CODES and k_codes.get_device() == dev and v_codes.get_device() == dev and
-            k_codes.is_contiguous() and v_codes.is_contiguous() and
-            _flat((k_scale, v_scale), dev, torch.float32))
+def _cache_ok(shape, k_codes, v_codes, k_scale, v_scale, dev: int) -> bool:
+    per_page = shape[:2]
+    return (shape[2] == KV8_PAGE and v_codes.shape == shape and k_scale.shape == per_page and
+            v_scale.shape == per_page and k_codes.dtype in _CODES and v_codes.dtype in _CODES and
+            v_codes.get_device() == dev and k_codes.is_contiguous() and v_codes.is_contiguous() and
+            k_scale.dtype is _F32 and v_scale.dtype is _F32 and k_scale.get_device() == dev and
+            v_scale.get_device() == dev and k_scale.is_contiguous() and v_scale.is_contiguous())
 
 
 def _need_cache(k_codes, v_codes, k_scale, v_scale) -> None:
     _need(k_codes, "k_codes", _CODES, (None, None, KV8_PAGE, None))
     n_pages, n_kv, _, hd = k_codes.shape
     _need(v_codes, "v_codes", _CODES, (n_pages, n_kv, KV8_PAGE, hd))
-    _need(k_scale, "k_scale", (torch.float32,), (n_pages, n_kv))
-    _need(v_scale, "v_scale", (torch.float32,), (n_pages, n_kv))
+    _need(k_scale, "k_scale", (_F32,), (n_pages, n_kv))
+    _need(v_scale, "v_scale", (_F32,), (n_pages, n_kv))
 
 
 def dflash_kv8_append(k, v, slots, k_codes, v_codes, k_scale, v_scale, err, stream=None):
     """Quantise rows k, v [rows][n_kv][head_dim] (fp32, bf16 or f16, strided
     rows and heads) into the pool at slots [rows]; negative slots skip."""
-    dev = _device() if _vectors(k, v, slots, k_codes, v_codes, k_scale, v_scale, err) and k.is_cuda else -1
-    if dev >= 0 and not (_cache_ok(k_codes, v_codes, k_scale, v_scale, dev) and _flat((slots, err), dev) and
-                         slots.dim() == 1 and err.shape == (2,) and k.dtype in _KINDS and v.dtype is k.dtype and
-                         k.shape == (slots.numel(), k_codes.shape[1], k_codes.shape[3]) and
-                         v.shape == k.shape and k.stride(2) == 1 and v.stride(2) == 1 and
-                         k.get_device() == dev and v.get_device() == dev):
-        dev = -1
-    if dev < 0:
+    try:
+        dev = _current(k_codes)
+        shape = k_codes.shape
+        n_pages, n_kv, _, hd = shape
+        (rows,) = slots.shape
+        kind, ks, vs = k.dtype, k.stride(), v.stride()
+        fine = (kind in _KINDS and v.dtype is kind and k.shape == (rows, n_kv, hd) and v.shape == k.shape and
+                ks[2] == 1 and vs[2] == 1 and k.get_device() == dev and v.get_device() == dev and
+                err.shape == (2,) and _flat((slots, err), dev) and
+                _cache_ok(shape, k_codes, v_codes, k_scale, v_scale, dev))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
         _need_cache(k_codes, v_codes, k_scale, v_scale)
         _need(slots, "slots", (_I32,), (None,))
-        shape = (slots.shape[0], k_codes.shape[1], k_codes.shape[3])
-        _need_heads(k, "k", _KINDS, shape)
-        _need_heads(v, "v", (k.dtype,), shape)
+        n_pages, n_kv, _, hd = k_codes.shape
+        rows = slots.shape[0]
+        _need_heads(k, "k", _KINDS, (rows, n_kv, hd))
+        _need_heads(v, "v", (k.dtype,), (rows, n_kv, hd))
         _need(err, "err", (_I32,), (2,))
         _here(k=k, v=v, slots=slots, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale,
               err=err)
-        dev = _device()
-    n_pages, n_kv, _, hd = k_codes.shape
+        dev, kind, ks, vs = k.get_device(), k.dtype, k.stride(), v.stride()
     cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         n_pages, n_kv, hd, 0)
-    ks, vs = k.stride(), v.stride()
-    rc = lib.dflash_kv8_append(cache, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                               _KINDS[k.dtype], slots.shape[0], slots.data_ptr(), err.data_ptr(),
-                               _raw(stream, dev))
+    rc = lib.dflash_kv8_append(cache, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _KINDS[kind],
+                               rows, slots.data_ptr(), err.data_ptr(), _raw(stream, dev))
     if rc:
         check(rc)
 
@@ -608,43 +610,45 @@ def dflash_kv8_attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, r
     """out = softmax(scale q k^T + mask) v of each sequence's rows over its
     cached positions; q, out [rows][n_q][head_dim] bf16 or f16 by strides,
     lse fp32 [rows][n_q]; scale None: head_dim ** -0.5."""
-    dev = _device() if _vectors(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, row_start, out,
-                                workspace, err) and q.is_cuda else -1
-    if dev >= 0:
+    try:
+        dev = _current(k_codes)
+        cshape = k_codes.shape
+        n_pages, n_kv, _, _ = cshape
         shape = q.shape
-        if not (len(shape) == 3 and table.dim() == 2 and q.dtype in _HALVES and out.dtype is q.dtype and
-                out.shape == shape and _cache_ok(k_codes, v_codes, k_scale, v_scale, dev) and
-                shape[2] == k_codes.shape[3] and _flat((table, kv_len, row_start, err), dev) and
-                kv_len.shape == table.shape[:1] and row_start.shape == (table.shape[0] + 1,) and
-                err.shape == (2,) and q.get_device() == dev and out.get_device() == dev and
-                workspace.get_device() == dev and workspace.is_contiguous() and q.stride(2) == 1 and
-                out.stride(2) == 1 and
-                (lse is None or (_vectors(lse) and lse.shape == shape[:2] and
-                                 _flat((lse,), dev, torch.float32)))):
-            dev = -1
-    if dev < 0:
+        rows, n_q, hd = shape
+        S, max_pages = table.shape
+        kind, qs, os_ = q.dtype, q.stride(), out.stride()
+        fine = (kind in _HALVES and out.dtype is kind and out.shape == shape and hd == cshape[3] and
+                qs[2] == 1 and os_[2] == 1 and q.get_device() == dev and out.get_device() == dev and
+                kv_len.shape == (S,) and row_start.shape == (S + 1,) and err.shape == (2,) and
+                _flat((table, kv_len, row_start, err), dev) and workspace.get_device() == dev and
+                workspace.is_contiguous() and _cache_ok(cshape, k_codes, v_codes, k_scale, v_scale, dev) and
+                (lse is None or (lse.shape == shape[:2] and _flat((lse,), dev, _F32))))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
         _need_cache(k_codes, v_codes, k_scale, v_scale)
-        _need_heads(q, "q", _HALVES, (None, None, k_codes.shape[3]))
-        _need_heads(out, "out", (q.dtype,), tuple(q.shape))
+        n_pages, n_kv, _, hd = k_codes.shape
+        _need_heads(q, "q", _HALVES, (None, None, hd))
+        rows, n_q, _ = q.shape
+        _need_heads(out, "out", (q.dtype,), (rows, n_q, hd))
         i32 = (_I32,)
         _need(table, "table", i32, (None, None))
-        _need(kv_len, "kv_len", i32, (table.shape[0],))
-        _need(row_start, "row_start", i32, (table.shape[0] + 1,))
+        S, max_pages = table.shape
+        _need(kv_len, "kv_len", i32, (S,))
+        _need(row_start, "row_start", i32, (S + 1,))
         if lse is not None:
-            _need(lse, "lse", (torch.float32,), tuple(q.shape[:2]))
+            _need(lse, "lse", (_F32,), (rows, n_q))
         _need(workspace, "workspace", None, None)
         _need(err, "err", i32, (2,))
         _here(q=q, out=out, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
               kv_len=kv_len, row_start=row_start, workspace=workspace, err=err, lse=lse)
-        dev = _device()
-    rows, n_q, hd = q.shape
-    S, max_pages = table.shape
+        dev, kind, qs, os_ = q.get_device(), q.dtype, q.stride(), out.stride()
     cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                        k_codes.shape[0], k_codes.shape[1], hd, 0)
-    qs, os_ = q.stride(), out.stride()
+                        n_pages, n_kv, hd, 0)
     args = _QUERY.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
                        kv_len.data_ptr(), row_start.data_ptr(), qs[0], qs[1], os_[0], os_[1], rows, n_q, S,
-                       max_pages, _KINDS[q.dtype], 1 if causal else 0, window,
+                       max_pages, _KINDS[kind], 1 if causal else 0, window,
                        hd ** -0.5 if scale is None else scale)
     rc = lib.dflash_kv8_attention(cache, args, workspace.data_ptr(), workspace.nbytes, err.data_ptr(),
                                   _raw(stream, dev))
@@ -666,7 +670,7 @@ def dflash_rope_turns(cfg: dflash_rope_config, turns, stream=None):
     """The frequency table of cfg: int64 [rotary_dim / 2], 2^-64 turns a position."""
     _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
     _here(turns=turns)
-    check(lib.dflash_rope_turns(C.byref(cfg), turns.data_ptr(), _raw(stream, _device())))
+    check(lib.dflash_rope_turns(C.byref(cfg), turns.data_ptr(), _raw(stream, turns.get_device())))
 
 
 def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2=None, stream=None):
@@ -674,41 +678,39 @@ def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2
     [rows]; fp32, bf16 or f16, strided rows and heads, out may be x."""
     if (x2 is None) != (out2 is None):
         raise DFlashError(DFLASH_ERR_ARG, "x2 and out2 go together")
-    both = (x, out) if x2 is None else (x, out, x2, out2)
-    dev = _device() if _vectors(turns, positions, *both) and x.is_cuda and x.dim() == 3 else -1
-    if dev >= 0:
-        rows, hd = positions.numel(), x.shape[2]
-        kind = x.dtype
-        fine = (kind in _KINDS and positions.dim() == 1 and x.shape[0] == rows and out.shape == x.shape and
-                turns.shape == (cfg.rotary_dim // 2,) and _flat((positions,), dev) and
-                _flat((turns,), dev, torch.int64) and
-                (x2 is None or (x2.dim() == 3 and x2.shape[0] == rows and x2.shape[2] == hd and
-                                out2.shape == x2.shape)))
-        if fine:
-            for t in both:
-                if t.dtype is not kind or t.get_device() != dev or t.stride(2) != 1:
-                    fine = False
-        if not fine:
-            dev = -1
-    if dev < 0:
-        _need(turns, "turns", (torch.int64,), (cfg.rotary_dim // 2,))
+    try:
+        dev = _current(x)
+        shape = x.shape
+        rows, heads, hd = shape
+        kind, xs, os_ = x.dtype, x.stride(), out.stride()
+        fine = (kind in _KINDS and out.dtype is kind and out.shape == shape and xs[2] == 1 and os_[2] == 1 and
+                out.get_device() == dev and positions.shape == (rows,) and _flat((positions,), dev) and
+                turns.shape == (cfg.rotary_dim // 2,) and _flat((turns,), dev, _I64))
+        if x2 is not None:
+            xs2, os2 = x2.stride(), out2.stride()
+            r2, heads2, h2 = x2.shape
+            fine = (fine and r2 == rows and h2 == hd and out2.shape == x2.shape and x2.dtype is kind and
+                    out2.dtype is kind and xs2[2] == 1 and os2[2] == 1 and x2.get_device() == dev and
+                    out2.get_device() == dev)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _need(turns, "turns", (_I64,), (cfg.rotary_dim // 2,))
         _need(positions, "positions", (_I32,), (None,))
         rows = positions.shape[0]
         _need_heads(x, "x", _KINDS, (rows, None, None))
-        hd = x.shape[2]
+        _, heads, hd = x.shape
         _need_heads(out, "out", (x.dtype,), tuple(x.shape))
         if x2 is not None:
             _need_heads(x2, "x2", (x.dtype,), (rows, None, hd))
             _need_heads(out2, "out2", (x.dtype,), tuple(x2.shape))
+            heads2, xs2, os2 = x2.shape[1], x2.stride(), out2.stride()
         _here(turns=turns, positions=positions, x=x, out=out, x2=x2, out2=out2)
-        dev = _device()
-    xs, os_ = x.stride(), out.stride()
-    first = _HEADS.pack(x.data_ptr(), out.data_ptr(), x.shape[1], 0, xs[0], xs[1], os_[0], os_[1])
-    second = None
-    if x2 is not None:
-        xs, os_ = x2.stride(), out2.stride()
-        second = _HEADS.pack(x2.data_ptr(), out2.data_ptr(), x2.shape[1], 0, xs[0], xs[1], os_[0], os_[1])
-    rc = lib.dflash_rope(C.byref(cfg), turns.data_ptr(), positions.data_ptr(), rows, hd, _KINDS[x.dtype],
-                         first, second, _raw(stream, dev))
+        dev, kind, xs, os_ = x.get_device(), x.dtype, x.stride(), out.stride()
+    first = _HEADS.pack(x.data_ptr(), out.data_ptr(), heads, 0, xs[0], xs[1], os_[0], os_[1])
+    second = None if x2 is None else _HEADS.pack(x2.data_ptr(), out2.data_ptr(), heads2, 0, xs2[0], xs2[1],
+                                                 os2[0], os2[1])
+    rc = lib.dflash_rope(C.byref(cfg), turns.data_ptr(), positions.data_ptr(), rows, hd, _KINDS[kind], first,
+                         second, _raw(stream, dev))
     if rc:
         check(rc)

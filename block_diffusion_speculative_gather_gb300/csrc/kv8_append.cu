@@ -13,11 +13,10 @@
 // them, slots repeated or out of order) are a chain and are done in row order
 // by the same threads, so a repeated slot keeps its last row.
 //
-// Work: rows are read twice (largest magnitude, then codes; the second read
-// comes from L1) and written once at 8 bits.  A CTA takes a window of rows
-// and finds the chains that begin in it: a few long ones (prompts) are done
-// by the whole CTA one after another, many short ones (single tokens) a warp
-// each.
+// Work: rows are read once into registers (largest magnitude, then codes) and
+// written once at 8 bits.  A CTA takes a window of rows and finds the chains
+// that begin in it: a few long ones (prompts) are done by the whole CTA one
+// after another, many short ones (single tokens) a warp each.
 
 #include "gemm.cuh"
 #include "kv8.cuh"
@@ -61,39 +60,55 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a < INFINITY ? a : 0.f;   // NaN compares false
 }
 
-// Eight elements of a row as fp32.
+// Eight elements of a row, as they stand and as fp32.
+template <typename T> struct alignas(16) Unit {
+    T e[8];
+};
+
 template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, Unit<T>& u) {
     if (WIDE) {
         constexpr int V = 16 / sizeof(T);
-        T e[8];
 #pragma unroll
         for (int i = 0; i < 8 / V; ++i)
-            reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+            reinterpret_cast<uint4*>(u.e)[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+        for (int i = 0; i < 8; ++i) u.e[i] = p[i];
     }
 }
 
 // One run: n rows from row r0 into page `page` at offset `off`, by `nt`
-// threads of which this is `t` (a warp or the CTA).
-template <typename T, bool WIDE, bool CTA>
+// threads of which this is `t` (a warp or the CTA).  A unit is 8 elements of
+// a row; a thread keeps up to KEEP units in registers (a whole page's run of
+// the CTA, or 8 rows of a warp at head_dim 128), so that they are read once.
+constexpr int KEEP = 4;
+
+template <typename T, int HD, bool WIDE, bool CTA>
 __device__ __forceinline__ void run_append(const Kv8AppendArgs& a, int which, int head, int r0, int n, int page,
-                                           int off, int t, int nt, float* red) {
-    const int hd = a.head_dim, per_row = hd / 8;
+                                           int off, int t, float* red) {
+    constexpr int PER_ROW = HD / 8, NT = CTA ? AT : 32;
     const long long ld = which ? a.row[1] : a.row[0];
     const T* x = reinterpret_cast<const T*>(which ? a.x[1] : a.x[0]) + (long long)r0 * ld +
                  (long long)head * (which ? a.head[1] : a.head[0]);
+    float* sp = (which ? a.scale[1] : a.scale[0]) + (long long)page * a.n_kv + head;
+    uint8_t* codes = (which ? a.codes[1] : a.codes[0]) + ((long long)page * a.n_kv + head) * KV8_PAGE * HD;
+    const float old = off > 0 ? *sp : 0.f;
+    const int total = n * PER_ROW;
+    Unit<T> v[KEEP];
     float top = 0.f;
-    const int total = n * per_row;
-    for (int i = t; i < total; i += nt) {
-        float v[8];
-        load8<T, WIDE>(x + (long long)(i / per_row) * ld + (i % per_row) * 8, v);
+    for (int base = 0; base < total; base += KEEP * NT) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(v[j]));
+        for (int k = 0; k < KEEP; ++k) {
+            const int i = base + k * NT + t;
+            if (i < total) load8<T, WIDE>(x + (long long)(i / PER_ROW) * ld + (i % PER_ROW) * 8, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (base + k * NT + t < total) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(to_f32(v[k].e[j])));
+            }
     }
     top = warp_max(top);
     if (CTA) {
@@ -103,16 +118,13 @@ __device__ __forceinline__ void run_append(const Kv8AppendArgs& a, int which, in
         for (int i = 0; i < AW; ++i) top = fmaxf(top, red[i]);
         __syncthreads();
     }
-    float* sp = (which ? a.scale[1] : a.scale[0]) + (long long)page * a.n_kv + head;
-    uint8_t* codes = (which ? a.codes[1] : a.codes[0]) + ((long long)page * a.n_kv + head) * KV8_PAGE * hd;
     float sc = scale_of(top);
     if (off > 0) {
-        const float old = *sp;
         if (old >= sc) {
             sc = old;
         } else {
             const float f = old * (1.f / sc);   // a power of two below 1
-            for (int i = t; i < off * per_row; i += nt) {
+            for (int i = t; i < off * PER_ROW; i += NT) {
                 uint2* p = reinterpret_cast<uint2*>(codes) + i;
                 uint2 c = *p;
                 uint32_t* w = reinterpret_cast<uint32_t*>(&c);
@@ -129,19 +141,24 @@ __device__ __forceinline__ void run_append(const Kv8AppendArgs& a, int which, in
     else __syncwarp();
     if (t == 0) *sp = sc;
     const float inv = 1.f / sc;   // exact: scales are powers of two
-    for (int i = t; i < total; i += nt) {
-        float v[8];
-        load8<T, WIDE>(x + (long long)(i / per_row) * ld + (i % per_row) * 8, v);
-        uint2 c;
-        c.x = codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        c.y = codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-        reinterpret_cast<uint2*>(codes + (long long)off * hd)[i] = c;
+    for (int base = 0; base < total; base += KEEP * NT) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) {
+            const int i = base + k * NT + t;
+            if (i >= total) continue;
+            if (total > KEEP * NT) load8<T, WIDE>(x + (long long)(i / PER_ROW) * ld + (i % PER_ROW) * 8, v[k]);
+            uint2 c;
+            const T* e = v[k].e;
+            c.x = codes4(to_f32(e[0]) * inv, to_f32(e[1]) * inv, to_f32(e[2]) * inv, to_f32(e[3]) * inv);
+            c.y = codes4(to_f32(e[4]) * inv, to_f32(e[5]) * inv, to_f32(e[6]) * inv, to_f32(e[7]) * inv);
+            reinterpret_cast<uint2*>(codes + (long long)off * HD)[i] = c;
+        }
     }
     if (CTA) __syncthreads();   // the next run of the chain reads this one's codes and scale
     else __syncwarp();
 }
 
-template <typename T, bool WIDE>
+template <typename T, int HD, bool WIDE>
 __global__ void __launch_bounds__(AT) kv8_append_kernel(Kv8AppendArgs a, int win) {
     __shared__ int s_slot[2 * WIN_MAX + 1];   // slots of the window, the row before and the longest run behind
     __shared__ int s_run[WIN_MAX], s_n;
@@ -199,10 +216,16 @@ __global__ void __launch_bounds__(AT) kv8_append_kernel(Kv8AppendArgs a, int win
         const int page = sl / KV8_PAGE;
         while (true) {
             const int off = sl % KV8_PAGE;
-            int n = 1;
-            while (off + n < KV8_PAGE && r + n < a.rows && slot_at(r + n) == sl + n) ++n;
-            if (by_cta) run_append<T, WIDE, true>(a, which, head, r, n, page, off, tid, AT, red);
-            else run_append<T, WIDE, false>(a, which, head, r, n, page, off, tid & 31, 32, red);
+            // rows that follow on, 64 tested at once by each warp
+            unsigned on[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int d = 32 * h + (tid & 31);
+                on[h] = __ballot_sync(0xffffffffu, off + d < KV8_PAGE && r + d < a.rows && slot_at(r + d) == sl + d);
+            }
+            const int n = ~on[0] ? __ffs(~on[0]) - 1 : 32 + (~on[1] ? __ffs(~on[1]) - 1 : 32);
+            if (by_cta) run_append<T, HD, WIDE, true>(a, which, head, r, n, page, off, tid, red);
+            else run_append<T, HD, WIDE, false>(a, which, head, r, n, page, off, tid & 31, red);
             r += n;
             while (r < a.rows && slot_at(r) < 0) ++r;
             if (r >= a.rows) break;
@@ -219,8 +242,11 @@ int launch_append_t(const Kv8AppendArgs& a, cudaStream_t s) {
     // for prompts.
     const int win = a.rows <= 256 ? 1 : WIN_MAX;
     const dim3 grid((unsigned)((a.rows + win - 1) / win), (unsigned)a.n_kv, 2);
-    return (int)(a.wide ? launch_k(kv8_append_kernel<T, true>, grid, dim3(AT), 0, s, a, win)
-                        : launch_k(kv8_append_kernel<T, false>, grid, dim3(AT), 0, s, a, win));
+    if (a.head_dim == 128)
+        return (int)(a.wide ? launch_k(kv8_append_kernel<T, 128, true>, grid, dim3(AT), 0, s, a, win)
+                            : launch_k(kv8_append_kernel<T, 128, false>, grid, dim3(AT), 0, s, a, win));
+    return (int)(a.wide ? launch_k(kv8_append_kernel<T, 64, true>, grid, dim3(AT), 0, s, a, win)
+                        : launch_k(kv8_append_kernel<T, 64, false>, grid, dim3(AT), 0, s, a, win));
 }
 
 }  // namespace

@@ -125,8 +125,19 @@ __global__ void __launch_bounds__(PT) pages_plan_kernel(PagesPlanArgs a, int inl
             if (s < PLAN_SMEM_SEQS) s_start[s] = (int)rg;
             a.kv_after[s] = kv + q;
         }
-        // a warp's lanes share each of its sequences' new entries
-        unsigned todo = __ballot_sync(0xffffffffu, need > 0);
+        // new entries: a lane its own sequence's while they are few (their loads
+        // are in flight together), else a warp's lanes share each sequence's
+        int most = need;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const int other = __shfl_xor_sync(0xffffffffu, most, o);
+            most = most > other ? most : other;
+        }
+        if (most <= 8) {
+            for (int i = 0; i < need; ++i)
+                a.table[(size_t)s * a.max_pages + old + i] = a.free_pages[n_free - 1 - pg - i];
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, most > 8 && need > 0);
         while (todo) {
             const int l = __ffs(todo) - 1;
             todo &= todo - 1;
@@ -151,12 +162,24 @@ __global__ void __launch_bounds__(PT) pages_plan_kernel(PagesPlanArgs a, int inl
     for (int r = tid; r < a.rows; r += PT) fill_row(a, start, total, r);
 }
 
+// Row maps of one sequence a CTA column (blockIdx.x, its rows dealt over
+// blockIdx.y), then this CTA's share of the rows behind the last.
 __global__ void pages_rows_kernel(PagesPlanArgs a) {
     pdl_trigger();
     pdl_wait();
-    const int total = a.row_start[a.S];
-    for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < a.rows; r += gridDim.x * blockDim.x)
-        fill_row(a, a.row_start, total, r);
+    const int s = blockIdx.x, step = gridDim.y * blockDim.x;
+    const int r0 = a.row_start[s], n = a.row_start[s + 1] - r0, total = a.row_start[a.S];
+    const int p0 = a.kv_after[s] - n;
+    for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int pos = p0 + i, page = a.table[(size_t)s * a.max_pages + pos / KV8_PAGE];
+        a.positions[r0 + i] = pos;
+        a.slots[r0 + i] = page >= 0 && page < (1 << 25) ? page * KV8_PAGE + pos % KV8_PAGE : -1;
+    }
+    const long long all = (long long)gridDim.x * step;
+    for (long long r = total + ((long long)blockIdx.y * gridDim.x + s) * blockDim.x + threadIdx.x; r < a.rows; r += all) {
+        a.positions[r] = -1;
+        a.slots[r] = -1;
+    }
 }
 
 __global__ void __launch_bounds__(PT) pages_trim_kernel(PagesTrimArgs a) {
@@ -207,8 +230,11 @@ int launch_pages_plan(const PagesPlanArgs& a, cudaStream_t s) {
     const int inl = a.rows <= PLAN_INLINE_ROWS;
     cudaError_t e = launch_k(pages_plan_kernel, dim3(1), dim3(PT), 0, s, a, inl);
     if (e == cudaSuccess && !inl) {
-        const int blocks = (a.rows + 255) / 256;
-        e = launch_k(pages_rows_kernel, dim3(blocks < 1024 ? blocks : 1024), dim3(256), 0, s, a);
+        // a CTA of 64 threads a sequence, more where they have many rows
+        const int each = (a.rows + a.S - 1) / a.S, tpb = each > 128 ? 256 : 64;
+        int y = (each + tpb - 1) / tpb;
+        y = y > 64 ? 64 : y;
+        e = launch_k(pages_rows_kernel, dim3(a.S, y), dim3(tpb), 0, s, a);
     }
     return (int)e;
 }

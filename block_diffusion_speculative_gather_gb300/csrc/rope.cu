@@ -61,6 +61,66 @@ template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
     T v[V];
 };
 
+// Two neighbouring elements rounded in one conversion.
+__device__ __forceinline__ void put2(float* p, float a, float b) { p[0] = a; p[1] = b; }
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void put2(__half* p, float a, float b) {
+    *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+}
+
+// The heads of one tensor that this lane visits: first, then every step-th.
+// V elements at i0 (and, halves, at i1) of each head; HB heads' loads are in
+// flight together.
+template <typename T, int V, bool IL, int P>
+__device__ __forceinline__ void rotate_heads(const RopeHeads& t, long long row, int first, int step, int i0, int i1,
+                                             bool rot, const float (&c)[P], const float (&s)[P]) {
+    constexpr int HB = V > 1 ? 4 : 1;
+    const T* x = reinterpret_cast<const T*>(t.x) + row * t.x_row + first * t.x_head + i0;
+    T* y = reinterpret_cast<T*>(t.out) + row * t.out_row + first * t.out_head + i0;
+    const long long xs = step * t.x_head, ys = step * t.out_head;
+    const int d = i1 - i0;
+    for (int h = first; h < t.heads; h += HB * step) {
+        Vec<T, V> e[HB], f[HB];
+#pragma unroll
+        for (int b = 0; b < HB; ++b) {
+            if (h + b * step >= t.heads) break;
+            e[b] = *reinterpret_cast<const Vec<T, V>*>(x + b * xs);
+            if (rot && !(IL && V > 1)) f[b] = *reinterpret_cast<const Vec<T, V>*>(x + b * xs + d);
+        }
+#pragma unroll
+        for (int b = 0; b < HB; ++b) {
+            if (h + b * step >= t.heads) break;
+            if (rot) {
+                if (V == 1) {
+                    const float p = to_f32(e[b].v[0]), q = to_f32(f[b].v[0]);
+                    y[b * ys + d] = from_f32<T>(q * c[0] + p * s[0]);
+                    e[b].v[0] = from_f32<T>(p * c[0] - q * s[0]);
+                } else if (IL) {
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        const float p = to_f32(e[b].v[2 * j]), q = to_f32(e[b].v[2 * j + 1]);
+                        put2(e[b].v + 2 * j, p * c[j] - q * s[j], q * c[j] + p * s[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        const float p0 = to_f32(e[b].v[j]), q0 = to_f32(f[b].v[j]);
+                        const float p1 = to_f32(e[b].v[j + 1]), q1 = to_f32(f[b].v[j + 1]);
+                        put2(e[b].v + j, p0 * c[j] - q0 * s[j], p1 * c[j + 1] - q1 * s[j + 1]);
+                        put2(f[b].v + j, q0 * c[j] + p0 * s[j], q1 * c[j + 1] + p1 * s[j + 1]);
+                    }
+                    *reinterpret_cast<Vec<T, V>*>(y + b * ys + d) = f[b];
+                }
+            }
+            *reinterpret_cast<Vec<T, V>*>(y + b * ys) = e[b];
+        }
+        x += HB * xs;
+        y += HB * ys;
+    }
+}
+
 // V elements (16 bytes, or one element where alignment or the dims forbid
 // more) are a unit.  Half layout: a rotary unit is V elements of the first
 // half and the V elements rotary/2 behind them.  Interleaved: V elements,
@@ -78,10 +138,12 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int splits, int u
     if (row >= a.rows) return;
     const int pos = a.positions[row];
     if (pos < 0) return;    // padding: the row stays as it was
-    const int heads = a.t[0].heads + a.t[1].heads;
-    const int half = a.rotary >> 1;
     const int sub = units <= 32 ? lane / units : 0;   // which head of an iteration
     if (sub >= per_iter) return;
+    const int step = splits * per_iter, first = part * per_iter + sub;
+    // heads are dealt over both tensors in a row: the second goes on where the first ends
+    int second = first - a.t[0].heads;
+    if (second < 0) second = (second % step + step) % step;
     for (int u = units <= 32 ? lane % units : lane; u < units; u += 32) {
         const bool rot = u < rot_units;
         int i0, i1 = 0;          // element offsets in the head
@@ -89,42 +151,14 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, int splits, int u
         if (rot) {
             const int p0 = u * P;
             i0 = IL ? 2 * p0 : p0;
-            i1 = IL ? i0 + 1 : p0 + half;
+            i1 = IL ? i0 + 1 : p0 + (a.rotary >> 1);
 #pragma unroll
             for (int j = 0; j < P; ++j) angle_of(a.turns[p0 + j], pos, a.scale, &c[j], &s[j]);
         } else {
             i0 = a.rotary + (u - rot_units) * V;
         }
-        for (int h = part * per_iter + sub; h < heads; h += splits * per_iter) {
-            const bool second = h >= a.t[0].heads;
-            const RopeHeads& t = a.t[second ? 1 : 0];
-            const int hh = second ? h - a.t[0].heads : h;
-            const T* x = reinterpret_cast<const T*>(t.x) + row * t.x_row + hh * t.x_head;
-            T* y = reinterpret_cast<T*>(t.out) + row * t.out_row + hh * t.out_head;
-            if (!rot) {
-                *reinterpret_cast<Vec<T, V>*>(y + i0) = *reinterpret_cast<const Vec<T, V>*>(x + i0);
-            } else if (IL && V > 1) {
-                Vec<T, V> e = *reinterpret_cast<const Vec<T, V>*>(x + i0);
-#pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float p = to_f32(e.v[2 * j]), q = to_f32(e.v[2 * j + 1]);
-                    e.v[2 * j] = from_f32<T>(p * c[j] - q * s[j]);
-                    e.v[2 * j + 1] = from_f32<T>(q * c[j] + p * s[j]);
-                }
-                *reinterpret_cast<Vec<T, V>*>(y + i0) = e;
-            } else {
-                Vec<T, V> e = *reinterpret_cast<const Vec<T, V>*>(x + i0);
-                Vec<T, V> f = *reinterpret_cast<const Vec<T, V>*>(x + i1);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float p = to_f32(e.v[j]), q = to_f32(f.v[j]);
-                    e.v[j] = from_f32<T>(p * c[j] - q * s[j]);
-                    f.v[j] = from_f32<T>(q * c[j] + p * s[j]);
-                }
-                *reinterpret_cast<Vec<T, V>*>(y + i0) = e;
-                *reinterpret_cast<Vec<T, V>*>(y + i1) = f;
-            }
-        }
+        rotate_heads<T, V, IL, P>(a.t[0], row, first, step, i0, i1, rot, c, s);
+        rotate_heads<T, V, IL, P>(a.t[1], row, second, step, i0, i1, rot, c, s);
     }
 }
 
