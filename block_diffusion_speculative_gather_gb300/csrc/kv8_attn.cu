@@ -32,7 +32,7 @@ constexpr int KT = 16;              // packed rows of a tile (the M side of the 
 constexpr int KW = 8;               // consumer warps; each takes whole pages, every eighth
 constexpr int KC = 32 * KW;         // consumer threads
 constexpr int KTHREADS = KC + 32;
-template <int HD> constexpr int stages() { return HD == 128 ? 10 : 20; }   // pages in flight: 160 KB
+template <int HD> constexpr int stages() { return HD == 128 ? 11 : 22; }   // pages in flight: 176 KB
 
 template <int HD> constexpr int tile_bytes() { return KV8_PAGE * HD; }
 template <int HD> constexpr int red_ld() { return HD + 16; }   // row pitch of the merge buffer (floats)
