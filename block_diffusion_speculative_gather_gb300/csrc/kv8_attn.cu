@@ -392,6 +392,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                     }
                 }
             }
+            // the page goes back once its codes have arrived: an arrival can
+            // overtake loads that are still queued
+            __threadfence_block();
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + st);
         }

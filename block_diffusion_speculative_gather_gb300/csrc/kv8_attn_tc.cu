@@ -600,8 +600,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         // a page that is not there: its scores are masked whatever the bytes
                         e[y] = lds128(sm + L::raw + (r0 + h) * PB + tile_off<HD>((u & 1) * 32 + lane, u >> 1));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rawk_empty + r0 + h);   // its codes have been read
 #pragma unroll
                     for (int y = 0; y < MINE; ++y) {
                         const int u = cw + y * KC, key = (u & 1) * 32 + lane, c = u >> 1;
@@ -616,6 +614,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(d + swz128(h * KV8_PAGE + key, 2 * (c & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
+                    // the page goes back once its codes have been used: an arrival can
+                    // overtake loads that are still queued
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawk_empty + r0 + h);
                 }
                 tc::fence_async_smem();
                 __syncwarp();
@@ -654,8 +656,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         const int x = cw + y * VC;
                         ldsm_x4_trans(r4[y], sm + L::raw + (R + r0 + h) * PB + tile_off<HD>((x & 1) * 32 + lane, x >> 1));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rawv_empty + r0 + h);
                     if (!plain) {
                         const bool valid = h ? there[1] : there[0];
 #pragma unroll
@@ -683,6 +683,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                         stsm_x4(vd + swz128(row, ch), e);
                         stsm_x4(vd + swz128(row + 8, ch), o);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rawv_empty + r0 + h);   // its codes have been used
                 }
                 tc::fence_async_smem();
                 __syncwarp();

@@ -705,3 +705,22 @@ def test_two_calls_at_once_with_their_own_workspaces(capi):
         torch.cuda.synchronize()
         assert err.tolist() == [0, 0]
         assert torch.equal(a["out"], want[0]) and torch.equal(b["out"], want[1])
+
+
+@pytest.mark.parametrize("n_q,rows,keys,dim", [(8, [16] * 4, [3000] * 4, 128),             # 64 packed rows
+                                               (8, [32] * 3, [2100] * 3, 128),             # 128
+                                               (8, [70, 33, 129], [2000, 1400, 1130], 128),
+                                               (8, [1] * 9, [2500] * 9, 128),
+                                               (10, [16] * 12, [1500] * 12, 64)])
+def test_repeats_have_the_same_bits(capi, n_q, rows, keys, dim):
+    # pages are overwritten in shared memory as soon as they are given back
+    st = attn_state(n_q, 2, dim, rows, keys, BF, seed=3)
+    ws = attend(capi, st)
+    want, lse, err = st["out"].clone(), st["lse"].clone(), ints([0, 0])
+    tabs = ints(st["table"]), ints(st["held"]), ints(st["start"])
+    other = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(400):
+        st["out"].fill_(3.0)
+        capi.dflash_kv8_attention(st["q"], *st["cache"], *tabs, st["out"], ws, err, lse=st["lse"])
+        other |= (st["out"] != want).any() | (st["lse"] != lse).any()
+    assert err.tolist() == [0, 0] and not other.item()
