@@ -80,6 +80,7 @@ struct Kv8AttnArgs {
     void* out;
     float* lse;                 // [rows][n_q] or NULL
     long long q_row, q_head, out_row, out_head;
+    const uint8_t* v_codes;
     const float* k_scale;
     const float* v_scale;
     const int* table;

@@ -21,6 +21,7 @@
 
 #include "attention_dev.cuh"
 #include "kv8_attn_dev.cuh"
+#include "tc_dev.cuh"
 
 namespace dfl {
 namespace {
@@ -71,7 +72,7 @@ __device__ __forceinline__ void store_row4<__half>(__half* p, float a, float b, 
 template <typename T, int HD>
 __global__ void __launch_bounds__(KTHREADS, 1)
 kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                const Kv8AttnArgs a) {
+                const __grid_constant__ Kv8AttnArgs a) {
     using S_ = KvSmem<HD>;
     constexpr int TB = tile_bytes<HD>(), KSTAGES = stages<HD>();
     extern __shared__ uint8_t raw[];
@@ -84,7 +85,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
     uint64_t* i_full = reinterpret_cast<uint64_t*>(sm + S_::items);   // [2] items on their way to the consumers
     uint64_t* i_empty = i_full + 2;
     Work* ring = reinterpret_cast<Work*>(sm + S_::work);
-    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);   // [0] last arriver, [1] a wait ran out, [2] there is a next item
+    // [0] last arriver, [1] a wait ran out, [2] there is a next item, [3] the last item (count) with NaN codes to look up
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_trigger();
@@ -101,6 +103,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         }
         fence_mbar_init();
         flag[1] = 0;
+        flag[3] = 0;
     }
     __syncthreads();
     pdl_wait();
@@ -291,7 +294,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             }
             const float2 sc = scales[st];
             const uint8_t* kt = sm + S_::ring + st * 2 * TB;
-            const uint8_t* vt = kt + TB;
+            uint8_t* vt = sm + S_::ring + st * 2 * TB + TB;
             const int key0 = p * KV8_PAGE;
             if (sc.x >= 0.f && sc.y > 0.f) {
                 float s[8][4];
@@ -360,28 +363,34 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                         o[d][3] *= alpha[1];
                     }
                 }
-                // codes of keys that no row sees may be anything, NaN included: as zeros
-                const bool edge = key0 < w.lo || key0 + KV8_PAGE > w.hi;
+                // a key's V must not reach a row that does not see it, and 0 * NaN is NaN:
+                // where not all rows see all keys, codes that no row sees and NaN ones
+                // are taken as zeros, and the rows that see a NaN get it after the merge
+                uint32_t seen = 0;
+                if (!whole) {
+#pragma unroll 1
+                    for (int x = lane; x < KV8_PAGE * HD / 16; x += 32) {
+                        const int key = x / (HD / 16);
+                        uint4* at = reinterpret_cast<uint4*>(vt + tile_off<HD>(key, x % (HD / 16)));
+                        const uint32_t keep = key0 + key >= w.lo && key0 + key < w.hi ? 0xffffffffu : 0u;
+                        const uint4 y = *at;
+                        *at = make_uint4(drop_nan(y.x & keep, &seen), drop_nan(y.y & keep, &seen),
+                                         drop_nan(y.z & keep, &seen), drop_nan(y.w & keep, &seen));
+                    }
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     // V: matrices (keys 0-7 | 8-15 of the step) x (16-byte chunks d, d + 1),
                     // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
                     // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
                     const int vrow = 16 * k + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
-                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                    if (edge) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const int ka = key0 + 16 * k + 8 * t + key_of<HD>(2 * c), kb = key0 + 16 * k + 8 * t + key_of<HD>(2 * c + 1);
-                            keep[t] = (ka >= w.lo && ka < w.hi ? 0x0000ffffu : 0u) | (kb >= w.lo && kb < w.hi ? 0xffff0000u : 0u);
-                        }
-                    }
 #pragma unroll
                     for (int d = 0; d < HD / 16; d += 2) {
                         uint32_t r[4];
                         ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) r[x] = __byte_perm(edge ? r[x] & keep[x & 1] : r[x], 0, 0x3120);
+                        for (int x = 0; x < 4; ++x) r[x] = __byte_perm(r[x], 0, 0x3120);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const uint32_t be[2] = {f16_of_codes(r[2 * x]), f16_of_codes(r[2 * x + 1])};
@@ -390,6 +399,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                             mma_f16_16816(o[2 * (d + x) + 1], pa[k], bo);
                         }
                     }
+                }
+                if (!whole) {
+                    if (seen) flag[3] = n_items + 1;
+                    tc::fence_async_smem();     // the next copy into this page comes after the zeros
                 }
             }
             // the page goes back once its codes have arrived: an arrival can
@@ -467,6 +480,18 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 fo[k].y = fmaf(x.y, f, fo[k].y);
                 fo[k].z = fmaf(x.z, f, fo[k].z);
                 fo[k].w = fmaf(x.w, f, fo[k].w);
+            }
+        }
+        if (flag[3] == (int)n_items + 1) {
+            const int idx = ((q.tiles - 1 - w.tile) * a.n_kv + w.kh) * q.splits + w.split;
+#pragma unroll
+            for (int k = 0; k < NF; ++k) {
+                const uint32_t m = nan_dims<HD>(a, w.s, idx, qi, col + 64 * k, 4);
+                const float nan = __int_as_float(0x7fffffff);
+                if (m & 1) fo[k].x = nan;
+                if (m & 2) fo[k].y = nan;
+                if (m & 4) fo[k].z = nan;
+                if (m & 8) fo[k].w = nan;
             }
         }
         bool write = true;

@@ -54,8 +54,8 @@ __device__ __forceinline__ Seq seq_of(const Kv8AttnArgs& a, int s) {
     q.first = kv - q.n;
     int lo = 0;
     if (a.window > 0) {
-        lo = a.causal ? q.first + 1 - a.window : q.first - a.window;
-        if (lo < 0) lo = 0;
+        const int end = q.first + (a.causal ? 1 : 0);
+        lo = end > a.window ? end - a.window : 0;
     }
     q.page_lo = lo / KV8_PAGE;
     q.page_hi = (kv + KV8_PAGE - 1) / KV8_PAGE;
@@ -82,12 +82,11 @@ __device__ __forceinline__ void row_keys(const Kv8AttnArgs& a, const Seq& q, int
     *lo = 0;
     if (a.causal) {
         *hi = pos + 1;
-        if (a.window > 0) *lo = pos + 1 - a.window;
+        if (a.window > 0 && pos + 1 > a.window) *lo = pos + 1 - a.window;
     } else {
         *hi = q.kv;
-        if (a.window > 0) *lo = q.first - a.window;
+        if (a.window > 0 && q.first > a.window) *lo = q.first - a.window;
     }
-    if (*lo < 0) *lo = 0;
     if (*hi < 0) *hi = 0;
 }
 
@@ -210,11 +209,45 @@ __device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
     return h;
 }
 
+// Four codes with NaN ones as zeros; `seen` collects that there were some.
+__device__ __forceinline__ uint32_t drop_nan(uint32_t w, uint32_t* seen) {
+    const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // codes 0x7f and 0xff
+    *seen |= m;
+    return w & ~((m >> 7) * 0xffu);
+}
+
 // Byte offset of 16-byte chunk c of key row r in a tile that TMA wrote with
 // the 128-byte (head_dim 128) or 64-byte (head_dim 64) swizzle.
 template <int HD>
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
     return HD == 128 ? swz128(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Which of dims d0 .. d0 + n - 1 (bits, n <= 32) have a NaN code in V among the
+// keys that row qi of the idx-th item of sequence s sees, in the pages that not
+// all of the item's rows see whole.  Rarely called: the item is found again, so
+// that its numbers need not stay in registers.
+template <int HD>
+__device__ __noinline__ uint32_t nan_dims(const Kv8AttnArgs& a, int s, int idx, int qi, int d0, int n) {
+    const Seq q = seq_of(a, s);
+    const Item w = item_of(a, q, s, idx);
+    if (qi >= q.n) return 0;
+    int klo, khi;
+    row_keys(a, q, qi, &klo, &khi);
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int p = w.p0; p < w.p1; ++p) {
+        const int key0 = p * KV8_PAGE, pg = a.table[(size_t)s * a.max_pages + p];
+        if ((key0 >= w.in_lo && key0 + KV8_PAGE <= w.in_hi) || pg < 0 || pg >= a.n_pages) continue;
+        const size_t at = (size_t)pg * a.n_kv + w.kh;
+        if (!(a.k_scale[at] >= 0.f && a.v_scale[at] > 0.f)) continue;
+        const int k1 = khi - key0 < KV8_PAGE ? khi - key0 : KV8_PAGE;
+#pragma unroll 1
+        for (int k = klo > key0 ? klo - key0 : 0; k < k1; ++k)
+            for (int d = 0; d < n; ++d)
+                m |= (uint32_t)((a.v_codes[(at * KV8_PAGE + k) * HD + d0 + d] & 0x7f) == 0x7f) << d;
+    }
+    return m;
 }
 
 // A row of q's power-of-two factor: `inv` brings its largest finite element

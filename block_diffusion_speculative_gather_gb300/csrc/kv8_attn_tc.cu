@@ -60,7 +60,8 @@ template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1 + 4 + 3 + 2;
     static constexpr int work = bars + n_bars * 8;             // [2] items
     static constexpr int misc = work + 2 * sizeof(Work);       // tensor-memory base, abort flag, verdict
-    static constexpr size_t bytes = 1024 + misc + 16;
+    static constexpr int nans = misc + 16;                     // [4] items with NaN codes to look up: (count, s, idx, tile)
+    static constexpr size_t bytes = 1024 + nans + 64;
 };
 
 struct StepScale {      // of the two pages of a step: K scale (negative: no keys), log2 and reciprocal of V's
@@ -125,10 +126,28 @@ __device__ __forceinline__ void store16(T* p, const float (&v)[16], float f) {
     *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// NaN into a thread's outputs (tensor memory at o) where its row sees NaN codes
+// of the item that `rec` names.
+template <int HD, bool KEYS, int DUP>
+__device__ __noinline__ void put_nans(const Kv8AttnArgs& a, const volatile int* rec, int t, int r, uint32_t o) {
+    const int s = rec[1], idx = rec[2], qi = (rec[3] * a.tile + (KEYS ? 0 : t * 128) + (DUP == 2 ? r & 63 : r)) / a.group;
+    for (int b = KEYS && t == 1 ? HD / 32 : 0; b < (KEYS && t == 0 ? HD / 32 : HD / 16); ++b) {
+        const uint32_t m = nan_dims<HD>(a, s, idx, qi, 16 * b, 16);
+        __syncwarp();
+        uint32_t y[16];
+        tc::ld_x16(o + b * 16, y);
+#pragma unroll
+        for (int n = 0; n < 16; ++n)      // the columns' order: store16
+            if ((m >> (2 * (n & 7) + (n >> 3))) & 1) y[n] = 0x7fffffffu;
+        tc::st_x16(o + b * 16, y);
+    }
+    tc::st_wait();
+}
+
 template <typename T, int HD, bool KEYS, int DUP>
 __global__ void __launch_bounds__(TC_THREADS, 1)
 kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                   const Kv8AttnArgs a) {
+                   const __grid_constant__ Kv8AttnArgs a) {
     using L = TcSmem<HD, KEYS, DUP>;
     constexpr int R = L::RAW, PB = L::PB;
     extern __shared__ uint8_t raw_smem[];
@@ -146,6 +165,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
     volatile int* verdict = reinterpret_cast<volatile int*>(sm + L::misc + 8);
+    volatile int* nan_rec = reinterpret_cast<volatile int*>(sm + L::nans);
     Work* works = reinterpret_cast<Work*>(sm + L::work);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform, so each role's code is
@@ -184,6 +204,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         mbar_init(judged, 1);
         fence_mbar_init();
         *abort = 0;
+        for (int i = 0; i < 4; ++i) nan_rec[4 * i] = 0;
     }
     if (warp == MMA_WARP) tc::tmem_alloc(tmem_base, 512);
     tc::fence_before_sync();
@@ -418,6 +439,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 M = m;
             }
             const int c_first = KEYS && t == 1 ? HD / 64 : 0, c_last = KEYS && t == 0 ? HD / 64 : HD / 32;
+            if ((KEYS || nt > 0) && nan_rec[4 * (items & 3)] == (int)items + 1)     // the same for all of a group's threads
+                put_nans<HD, KEYS, DUP>(a, nan_rec + 4 * (items & 3), t, r, nt > 0 ? o_tm : o_tm + other);
 
             // ---- the row's outputs, or its partial of this split
             const long long slot0 = (long long)item - w.split;    // splits of a tile are neighbours
@@ -643,9 +666,13 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 if (!ok) break;
                 const float2 sa = rscv[r0], sb = rscv[r0 + 1];
                 const bool there[2] = {sa.x >= 0.f && sa.y > 0.f, sb.x >= 0.f && sb.y > 0.f};
-                // codes of keys that no row sees may be anything, NaN included: as zeros
+                // a key's V must not reach a row that does not see it, and 0 * NaN is NaN:
+                // where not all rows see all keys, codes that no row sees and NaN ones
+                // are taken as zeros, and the item is marked: the rows that see a NaN
+                // get it with their outputs
                 const int kp = (w.p0 + 2 * j) * KV8_PAGE;
-                const bool plain = kp >= w.lo && kp + STEP <= w.hi && there[0] && there[1];
+                const bool plain = kp >= w.in_lo && kp + STEP <= w.in_hi && there[0] && there[1];
+                uint32_t seen = 0;
                 uint8_t* dst = sm + L::v + st * L::KB;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -658,6 +685,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     }
                     if (!plain) {
                         const bool valid = h ? there[1] : there[0];
+                        const bool whole = kp + h * KV8_PAGE >= w.in_lo && kp + (h + 1) * KV8_PAGE <= w.in_hi;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             // VC is even, so all of this warp's units have the same 32 keys
@@ -665,7 +693,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                             const uint32_t keep = (valid && k >= w.lo && k < w.hi ? 0x0000ffffu : 0u) |
                                                   (valid && k + 1 >= w.lo && k + 1 < w.hi ? 0xffff0000u : 0u);
 #pragma unroll
-                            for (int y = 0; y < MINE; ++y) r4[y][i] &= keep;
+                            for (int y = 0; y < MINE; ++y) {
+                                const uint32_t x = r4[y][i] & keep;
+                                r4[y][i] = whole ? x : drop_nan(x, &seen);
+                            }
                         }
                     }
 #pragma unroll
@@ -685,6 +716,14 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(rawv_empty + r0 + h);   // its codes have been used
+                }
+                // read at the item's end: no role is four items ahead
+                if (!plain && seen) {
+                    volatile int* rec = nan_rec + 4 * (items & 3);
+                    rec[1] = w.s;
+                    rec[2] = ((wk.q.tiles - 1 - w.tile) * a.n_kv + w.kh) * wk.q.splits + w.split;
+                    rec[3] = w.tile;
+                    rec[0] = items + 1;
                 }
                 tc::fence_async_smem();
                 __syncwarp();

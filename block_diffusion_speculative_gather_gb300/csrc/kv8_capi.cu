@@ -238,6 +238,7 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     a.q_head = q->q_head;
     a.out_row = q->out_row;
     a.out_head = q->out_head;
+    a.v_codes = cache->v_codes;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
     a.table = q->table;

@@ -589,7 +589,8 @@ int dflash_kv8_append(const dflash_kv8_cache* cache /*host*/, const void* k, int
  * kv head; up to 4096 sequences; strides in elements, every row of every head
  * 16-byte aligned.  A sequence's results depend on its own rows and cached
  * positions and on the call's row, sequence and head counts, not on the
- * other sequences.  Codes of positions no row sees do not matter.
+ * other sequences.  Codes of positions a row does not see do not matter to
+ * it, NaN included; a row that sees a NaN code gets NaN (V: in its dim).
  * Workspace: dflash_kv8_workspace_bytes, zero-filled before its first use
  * (completed calls leave its counters at zero); calls that share one must
  * not overlap on the GPU; zero it again after err was set.  A length or page

@@ -724,3 +724,71 @@ def test_repeats_have_the_same_bits(capi, n_q, rows, keys, dim):
         capi.dflash_kv8_attention(st["q"], *st["cache"], *tabs, st["out"], ws, err, lse=st["lse"])
         other |= (st["out"] != want).any() | (st["lse"] != lse).any()
     assert err.tolist() == [0, 0] and not other.item()
+
+
+def seen_by(st, s, causal, window):
+    """[rows of s][its keys]: which keys each row sees."""
+    n, kv = st["start"][s + 1] - st["start"][s], st["held"][s]
+    pos, key = kv - n + torch.arange(n)[:, None], torch.arange(kv)[None]
+    if causal:
+        see = key <= pos
+        return see & (key > pos - window) if window else see
+    see = torch.ones(n, kv, dtype=torch.bool)
+    return see & (key >= kv - n - window) if window else see
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows,held", [
+    (4, 1, 128, [5, 3, 1], [300, 1000, 70]),           # 16-row tiles
+    (4, 2, 64, [4, 8], [2000, 63]),
+    (8, 2, 128, [16, 9], [1500, 64]),                  # 64-row tiles, rows held twice
+    (8, 1, 64, [8, 8], [700, 129]),
+    (8, 2, 128, [30, 20], [500, 2000]),                # 128-row tiles
+    (6, 2, 64, [41, 1], [1000, 40]),
+    (8, 2, 128, [150, 70], [400, 1000]),               # two 128-row tiles
+    (4, 2, 64, [300], [310]),
+])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 90), (False, 0), (False, 33)])
+@pytest.mark.parametrize("where", ["v", "k", "q"])
+def test_nan_stays_with_the_rows_that_see_it(capi, n_q, n_kv, dim, rows, held, causal, window, where):
+    """Zeros in place of the NaNs must give the other rows the same bits."""
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=9, pad=0)
+    g = torch.Generator().manual_seed(1)
+    bad = torch.zeros(st["q"].shape, dtype=torch.bool)      # results that are NaN
+    spots, lost = [], []
+    for s, kv in enumerate(held):
+        see, r0, group = seen_by(st, s, causal, window), st["start"][s], n_q // n_kv
+        edge = torch.nonzero(~see.all(0)).flatten().tolist()
+        keys = sorted({kv - 1, max(kv - 2, 0), max(kv - 1 - window, 0), *([edge[0], edge[-1], edge[len(edge) // 2]] if edge else [])})
+        for i, key in enumerate(keys):
+            kh, d = i % n_kv, int(torch.randint(0, dim, (1,), generator=g))
+            spots.append((st["table"][s][key // 64], kh, key % 64, d, 0x7f if i % 2 else 0xff))
+            hit = torch.nonzero(see[:, key]).flatten()
+            for r in hit.tolist():
+                bad[r0 + r, kh * group:(kh + 1) * group, d if where == "v" else slice(None)] = True
+        lost.append((r0 + rows[s] // 2, s % n_q))
+    outs = []
+    for nan in (False, True):
+        if where == "q":
+            for i, (r, h) in enumerate(lost):
+                st["q"][r, h, 3 + i] = (math.nan if i % 2 else math.inf) if nan else 0.0
+        else:
+            for pg, kh, at, d, code in spots:
+                st["cache"][where == "v"][pg, kh, at, d] = code if nan else 0
+        attend(capi, st, causal, window)
+        outs.append(st["out"].clone().cpu())
+    if where == "q":
+        bad[:] = False
+        for r, h in lost:
+            bad[r, h] = True
+        assert torch.equal(outs[1][~bad], outs[0][~bad])
+        return
+    assert torch.equal(torch.isnan(outs[1]), bad)
+    assert torch.equal(outs[1][~bad], outs[0][~bad])
+
+
+@pytest.mark.parametrize("rows,held", [([3, 2], [2, 130]), ([20, 1], [7, 64]), ([200], [150])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_largest_window_and_more_rows_than_positions(capi, rows, held, causal):
+    st = attn_state(4, 1, 64, rows, held, BF, seed=4)
+    attend(capi, st, causal, window=2 ** 31 - 1)
+    check_attend(st, causal, window=2 ** 31 - 1)
