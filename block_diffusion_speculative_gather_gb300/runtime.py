@@ -350,3 +350,86 @@ class DFlashBatch(DFlash):
             capi.dflash_batch_destroy(self.batch)
             self.batch = None
             self.ctxs = []
+
+
+class PagedKV8:
+    """The 8-bit paged cache of up to S sequences of one model: `layers` pools
+    of `pages` pages over one block table, at most `rows` rows a step.
+
+        kv = PagedKV8(layers, n_q, n_kv, head_dim, S, pages, max_pages, rows, rope=capi.rope_config(head_dim))
+        kv.plan(q_len)                        # rows each sequence wants, -> kv.row_start, kv.positions
+        for i in range(layers):
+            ...                               # q, k, v [rows][heads][head_dim]
+            kv.rotate(q, k)
+            out = kv.attend(i, q, k, v)       # appends k and v, then attends
+        kv.trim(new_len)                      # rejected rows; 0 ends a sequence
+
+    Everything stays on the device, on the current stream (with the lengths
+    in `q_len` and `new_len` a step can be captured in a graph); `check`
+    raises what the kernels reported."""
+
+    def __init__(self, layers: int, n_q: int, n_kv: int, head_dim: int, S: int, pages: int, max_pages: int,
+                 rows: int, rope: Optional[capi.dflash_rope_config] = None, device: str = "cuda"):
+        self.S, self.rows = S, rows
+        with torch.cuda.device(torch.device(device)):
+            size = capi.dflash_kv8_workspace_bytes(rows, S, n_q, n_kv, head_dim, max_pages)
+            if size == 0:
+                capi.check(-1)
+            i32 = dict(dtype=torch.int32, device="cuda")
+            codes = lambda: torch.zeros(pages, n_kv, capi.KV8_PAGE, head_dim, dtype=torch.uint8, device="cuda")
+            scales = lambda: torch.ones(pages, n_kv, device="cuda")
+            self.caches = [(codes(), codes(), scales(), scales()) for _ in range(layers)]
+            self.table = torch.full((S, max_pages), -1, **i32)
+            self.free = torch.arange(pages - 1, -1, -1, **i32)     # page 0 is handed out first
+            self.n_free = torch.full((1,), pages, **i32)
+            self.kv_len, self.q_len, self.new_len = (torch.zeros(S, **i32) for _ in range(3))
+            self.row_start = torch.zeros(S + 1, **i32)
+            self.positions, self.slots = (torch.full((rows,), -1, **i32) for _ in range(2))
+            self.workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
+            self.err = torch.zeros(2, **i32)
+            self.rope, self.turns = rope, None
+            if rope is not None:
+                self.turns = torch.zeros(rope.rotary_dim // 2, dtype=torch.int64, device="cuda")
+                capi.dflash_rope_turns(rope, self.turns)
+            torch.cuda.synchronize()
+
+    def _set(self, buf: torch.Tensor, lens):
+        buf.copy_(torch.as_tensor(lens, dtype=torch.int32))
+
+    def plan(self, q_len=None):
+        """Pages and rows for q_len[s] more positions of each sequence (None:
+        as `self.q_len` stands); sequences that do not fit get none."""
+        if q_len is not None:
+            self._set(self.q_len, q_len)
+        capi.dflash_pages_plan(self.kv_len, self.q_len, self.free, self.n_free, self.table, self.row_start,
+                               self.positions, self.slots, self.kv_len, self.n_free)
+
+    def rotate(self, q: torch.Tensor, k: torch.Tensor):
+        """Rotary positions of the step's rows, in place."""
+        capi.dflash_rope(self.rope, self.turns, self.positions, q, q, k, k)
+
+    def attend(self, layer: int, q, k, v, out=None, lse=None, scale=None, causal=True, window=0):
+        """Append the step's rows to a layer's pool, attend over it."""
+        cache = self.caches[layer]
+        out = torch.empty_like(q) if out is None else out
+        capi.dflash_kv8_append(k, v, self.slots, *cache, self.err)
+        capi.dflash_kv8_attention(q, *cache, self.table, self.kv_len, self.row_start, out, self.workspace, self.err,
+                                  lse=lse, scale=scale, causal=causal, window=window)
+        return out
+
+    def trim(self, new_len=None):
+        """Shorten sequences to new_len[s] where that is smaller (None: as
+        `self.new_len` stands)."""
+        if new_len is not None:
+            self._set(self.new_len, new_len)
+        capi.dflash_pages_trim(self.kv_len, self.new_len, self.free, self.n_free, self.table)
+
+    def check(self):
+        """Raise if a kernel of an earlier step reported an error."""
+        code, where = self.err.tolist()
+        if code:
+            self.err.zero_()          # report once, then clear
+            self.workspace.zero_()    # a kernel that gave up may have left counters set
+            if code == 1:
+                raise capi.DFlashError(-6, f"bounded wait expired (site {where})")
+            raise capi.DFlashError(-5, f"cache kernels: index out of range (at {where})")

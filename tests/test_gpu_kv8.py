@@ -792,3 +792,35 @@ def test_largest_window_and_more_rows_than_positions(capi, rows, held, causal):
     st = attn_state(4, 1, 64, rows, held, BF, seed=4)
     attend(capi, st, causal, window=2 ** 31 - 1)
     check_attend(st, causal, window=2 ** 31 - 1)
+
+
+def test_the_paged_cache_class_runs_the_operators(capi):
+    """Two layers, three sequences, one of which does not fit at first: the
+    class's outputs against dense attention over what it cached."""
+    from block_diffusion_speculative_gather_gb300.runtime import PagedKV8
+    n_q, n_kv, dim, S, rows = 8, 2, 128, 3, 96
+    kv = PagedKV8(2, n_q, n_kv, dim, S, 5, 4, rows, rope=capi.rope_config(dim))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for q_len, given, back in (([70, 5, 200], [70, 5, 0], None), ([1, 16, 0], [1, 16, 0], [70, 12, 0]),
+                               ([1, 1, 0], [1, 1, 0], [0, 13, 0]), ([0, 1, 80], [0, 1, 80], None)):
+        had = kv.kv_len.tolist()
+        kv.plan(q_len)
+        start = kv.row_start.tolist()
+        assert [b - a for a, b in zip(start, start[1:])] == given
+        assert kv.kv_len.tolist() == [a + b for a, b in zip(had, given)]
+        for layer in range(2):
+            qkv = torch.randn((rows, n_q + 2 * n_kv, dim), generator=g, device="cuda").to(BF)
+            q, k, v = qkv.split([n_q, n_kv, n_kv], 1)
+            out, lse = torch.full_like(q, 3.0), torch.full((rows, n_q), 3.0, device="cuda")
+            kv.rotate(q, k)
+            assert kv.attend(layer, q, k, v, out=out, lse=lse, causal=layer == 0) is out
+            check_attend(dict(q=q, cache=kv.caches[layer], table=kv.table.tolist(), held=kv.kv_len.tolist(),
+                              start=start, out=out, lse=lse), causal=layer == 0)
+        if back is not None:
+            kv.trim(back)
+    kv.check()
+    assert kv.n_free.item() == 5 - 1 - 2
+    kv.err.copy_(ints([2, 7]))
+    with pytest.raises(capi.DFlashError):
+        kv.check()
+    kv.check()
