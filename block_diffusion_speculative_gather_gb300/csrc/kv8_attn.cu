@@ -105,8 +105,15 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         flag[1] = 0;
         flag[3] = 0;
     }
-    __syncthreads();
     pdl_wait();
+    Finder f{};
+    Work first;
+    first.item = -1;
+    if (warp == KW) {      // the first item, while the barriers are made ready
+        f = make_finder(a, lane);
+        if ((int)blockIdx.x < f.total) first = find_item(a, f, (int)blockIdx.x, lane);
+    }
+    __syncthreads();
 
     if (warp == KW) {
         // ---- producer: pages of every item of this CTA, in order.  The lanes
@@ -114,26 +121,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // issues these.
         unsigned it = 0;
         bool ok = true;
-        const Finder f = make_finder(a, lane);
-        int item = (int)blockIdx.x < f.total ? (int)blockIdx.x : -1;
+        Work wk = first;
         for (unsigned k = 0; ok; ++k) {
-            Work wk;
-            wk.item = -1;
-            if (item >= 0) wk = find_item(a, f, item, lane);
-            int next = -1;
+            const int item = wk.item;
+            int asked = 0;
             if (lane == 0) {
-                if (k >= 2 && !mbar_wait_bounded(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
+                if (k >= 2 && !mbar_wait(i_empty + (k & 1), ((k >> 1) - 1) & 1)) {
                     report(a.err, DERR_TIMEOUT, SITE_EMPTY);
                     flag[1] = 1;
                 } else {
                     ring[k & 1] = wk;
                     mbar_arrive(i_full + (k & 1));
                 }
-                if (item >= 0) next = next_item(a, f.total);
+                if (item >= 0) asked = ask_item(a, f.total);
             }
             if (item < 0) break;
-            next = __shfl_sync(0xffffffffu, next, 0);
-            const Item& w = wk.w;
+            const Item w = wk.w;
             auto look = [&](int b, int* page, float* ks, float* vs) {
                 *page = -1;
                 *ks = -1.f;
@@ -160,7 +163,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                     const int st = it % KSTAGES;
                     bool issued = true;
                     if (lane == 0) {
-                        if (it >= KSTAGES && !mbar_wait_bounded(empty + st, (it / KSTAGES - 1) & 1)) {
+                        if (it >= KSTAGES && !mbar_wait(empty + st, (it / KSTAGES - 1) & 1)) {
                             report(a.err, DERR_TIMEOUT, SITE_EMPTY);
                             flag[1] = 1;
                             issued = false;
@@ -189,12 +192,15 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 ks = next_ks;
                 vs = next_vs;
             }
-            item = next;
+            int next = lane == 0 ? settle_item(a, f.total, asked) : 0;
+            next = __shfl_sync(0xffffffffu, next, 0);
+            wk.item = -1;
+            if (next >= 0) wk = find_item(a, f, next, lane);
         }
         // no copy of this CTA is in flight when it ends
         if (lane == 0) {
             const unsigned n = it < KSTAGES ? it : KSTAGES;
-            for (unsigned i = it - n; i < it; ++i) mbar_wait_bounded(full + i % KSTAGES, (i / KSTAGES) & 1);
+            for (unsigned i = it - n; i < it; ++i) mbar_wait(full + i % KSTAGES, (i / KSTAGES) & 1);
         }
         return;
     }
@@ -207,7 +213,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // (err says so)
         const int slot_i = n_items & 1;
         if (warp == 0) {
-            const bool got = __all_sync(0xffffffffu, !flag[1] && mbar_wait_bounded(i_full + slot_i, (n_items >> 1) & 1));
+            const bool got = __all_sync(0xffffffffu, !flag[1] && mbar_wait(i_full + slot_i, (n_items >> 1) & 1));
             if (lane == 0) {
                 if (!got && !flag[1]) {
                     report(a.err, DERR_TIMEOUT, SITE_FULL);
@@ -287,7 +293,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             const unsigned it = base + (p - w.p0);
             const int st = it % KSTAGES;
             if (flag[1]) break;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(full + st, (it / KSTAGES) & 1))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (it / KSTAGES) & 1))) {
                 report(a.err, DERR_TIMEOUT, SITE_FULL);
                 flag[1] = 1;
                 break;
@@ -611,31 +617,23 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
     const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
     long long usual = (packed + p.tile - 1) / p.tile;
     if (usual < S) usual = S;
-    // Splits of a sequence with P pages (a value for each power of two): the
-    // count that costs least if all sequences were like it, an item costing its
-    // pages (the mma.sync form's eight warps take a page each in the time of
-    // four) and 12 (24) more for its start, merge and partials.
-    const double fixed = p.form == KV8_MMA ? 12.0 : 24.0;
+    // Splits of a sequence with P pages (a value for each power of two): as many
+    // as let every item start at once, an SM each, but not below 4 (6) pages an
+    // item.  An item behind another one costs far more than its pages: 8
+    // sequences of 16384 positions, 8 kv heads: 74, 104, 84 us with 2, 3, 4
+    // splits for single tokens, 92, 129, 109 us for 16 rows; one of 6000: 49,
+    // 25, 18 us with 1, 4, 16.  Where more items than SMs wait anyway, single tokens
+    // of long sequences are halved all the same, so that the last items are short:
+    // 32 of 4096 to 16384 positions 180 -> 159 us (equal ones of 10000: 162 -> 180).
+    const long long once = usual * n_kv < sms ? sms / (usual * n_kv) : 1, least = p.form == KV8_MMA ? 4 : 6;
     long long cap = 1;
     for (int b = 0; b < 32; ++b) {
-        p.caps[b] = 1;
-        if ((1LL << b) > max_pages) continue;
-        const double pages = 1.5 * (double)(1LL << b);
-        double best = 0.0;
-        for (long long c = 1; c <= 64 && c <= (1LL << b); ++c) {
-            double len = pages / (double)c;
-            const double four = 4.0 * (double)(long long)((len + 7.0) / 8.0);
-            if (p.form == KV8_MMA && len < four) len = four;
-            // rounds of items over the SMs; behind the first, on average half an
-            // item is waited for at the end; folding costs more than a page a split
-            const double rounds = (double)(usual * n_kv * c) / sms;
-            const double cost = (rounds > 1.0 ? (rounds + 0.5) * (len + fixed) : len + fixed) + 1.3 * (double)(c - 1);
-            if (c == 1 || cost < 0.95 * best) {   // partials cost bandwidth: only for a clear gain
-                best = cost;
-                p.caps[b] = (uint8_t)c;
-            }
-        }
-        if (p.caps[b] > cap) cap = p.caps[b];
+        long long c = (1LL << b) / least;
+        if (c > once) c = once;
+        if (c > 64) c = 64;
+        if (usual * n_kv > sms && p.form == KV8_MMA && b >= 7) c = 2;
+        p.caps[b] = (uint8_t)(c < 1 ? 1 : c);
+        if ((1LL << b) <= max_pages && p.caps[b] > cap) cap = p.caps[b];
     }
     p.split_cap = (int)cap;
     p.ticket_cap = tiles * n_kv;

@@ -15,12 +15,28 @@ __device__ __forceinline__ void report(int* err, int code, int info) {
     if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
 }
 
+// Bounded mbarrier wait, about two seconds by the SM's clock: reading the
+// global timer between polls held a finished wait back by XXXX cycles.
+constexpr long long WAIT_CYCLES = 4000000000ll;
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > WAIT_CYCLES) return false;
+    }
+}
+
 // Items are handed out one by one, as sequences differ in length: a CTA's
 // first is its index, the others come from a counter in the workspace.  The
 // last CTA to be refused one puts the counters back to zero.
-__device__ __forceinline__ int next_item(const Kv8AttnArgs& a, int total) {
+// `ask` has the answer on its way while the caller goes on; `settle` reads it.
+__device__ __forceinline__ int ask_item(const Kv8AttnArgs& a, int total) {
+    return total > (int)gridDim.x ? atomicAdd(a.queue, 1) : 0;
+}
+__device__ __forceinline__ int settle_item(const Kv8AttnArgs& a, int total, int asked) {
     if (total <= (int)gridDim.x) return -1;      // each has had its only one
-    const int item = (int)gridDim.x + atomicAdd(a.queue, 1);
+    const int item = (int)gridDim.x + asked;
     if (item < total) return item;
     if (atomicAdd(a.queue + 1, 1) == (int)gridDim.x - 1) {
         a.queue[0] = 0;
@@ -93,13 +109,13 @@ __device__ __forceinline__ void row_keys(const Kv8AttnArgs& a, const Seq& q, int
 __device__ __forceinline__ Item item_of(const Kv8AttnArgs& a, const Seq& q, int s, int idx) {
     Item it;
     it.s = s;
-    it.split = idx % q.splits;
-    const int rest = idx / q.splits;
-    it.kh = rest % a.n_kv;
+    const unsigned rest = (unsigned)idx / (unsigned)q.splits, top = rest / (unsigned)a.n_kv;
+    it.split = idx - (int)rest * q.splits;
+    it.kh = (int)(rest - top * (unsigned)a.n_kv);
     // under the causal mask the last rows have the most keys: they go first
-    it.tile = q.tiles - 1 - rest / a.n_kv;
-    const int i0 = it.tile * a.tile / a.group;
-    int i1 = (it.tile * a.tile + a.tile - 1) / a.group;
+    it.tile = q.tiles - 1 - (int)top;
+    const int i0 = (int)((unsigned)(it.tile * a.tile) / (unsigned)a.group);
+    int i1 = (int)((unsigned)(it.tile * a.tile + a.tile - 1) / (unsigned)a.group);
     if (i1 > q.n - 1) i1 = q.n - 1;
     int lo0, hi0, lo1, hi1;
     row_keys(a, q, i0, &lo0, &hi0);
@@ -128,7 +144,8 @@ struct Work {
 // `per` sequences.
 struct Finder {
     int per, cum, total;
-    Seq q;              // of this lane's sequence where per is 1
+    Seq q;              // of this lane's sequence where per is 1,
+    int s;              // and its index
 };
 
 __device__ __forceinline__ int items_of(const Kv8AttnArgs& a, const Seq& q) { return q.tiles * a.n_kv * q.splits; }
@@ -151,6 +168,25 @@ __device__ __forceinline__ Finder make_finder(const Kv8AttnArgs& a, int lane) {
         f.q = seq_of(a, s);
         mine += items_of(a, f.q);
     }
+    f.s = lane;
+    if (f.per == 1 && a.S > 1) {
+        // up to 32 sequences: those with the longest items go first, so that no
+        // long one is begun at the end (a bitonic sort; equal ones in order)
+        uint32_t key = (uint32_t)f.q.len << 5 | (uint32_t)(31 - lane);
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, key, j);
+                key = ((lane & k) == 0) == ((lane & j) == 0) ? max(key, o) : min(key, o);
+            }
+        const int from = 31 - (int)(key & 31);
+        int* d = reinterpret_cast<int*>(&f.q);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Seq) / 4); ++i) d[i] = __shfl_sync(0xffffffffu, d[i], from);
+        mine = __shfl_sync(0xffffffffu, mine, from);
+        f.s = from;
+    }
     const int inc = warp_inclusive(mine, lane);
     f.cum = inc - mine;
     f.total = __shfl_sync(0xffffffffu, inc, 31);
@@ -166,16 +202,18 @@ __device__ __forceinline__ Work find_item(const Kv8AttnArgs& a, const Finder& f,
     const int end = s0 + f.per < a.S ? s0 + f.per : a.S;
     Work k;
     k.item = item;
+    if (f.per == 1) {              // the group's only sequence
+        int* d = reinterpret_cast<int*>(&k.q);
+        const int* src = reinterpret_cast<const int*>(&f.q);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Seq) / 4); ++i) d[i] = __shfl_sync(0xffffffffu, src[i], group);
+        k.w = item_of(a, k.q, __shfl_sync(0xffffffffu, f.s, group), idx);
+        return k;
+    }
     while (true) {
         Seq q{};
         int n = 0;
-        if (f.per == 1) {          // the group's only sequence, into lane 0
-            int* d = reinterpret_cast<int*>(&q);
-            const int* src = reinterpret_cast<const int*>(&f.q);
-#pragma unroll
-            for (int i = 0; i < (int)(sizeof(Seq) / 4); ++i) d[i] = __shfl_sync(0xffffffffu, src[i], group);
-            n = lane == 0 ? items_of(a, q) : 0;
-        } else if (s0 + lane < end) {
+        if (s0 + lane < end) {
             q = seq_of(a, s0 + lane);
             n = items_of(a, q);
         }

@@ -52,8 +52,8 @@ template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr int PB = KV8_PAGE * HD;                   // one page's K (or V) codes
     static constexpr int RAW = HD == 64 ? 8 : (KEYS ? 4 : 2);  // pages in flight, K and V each
     static constexpr int q = 0, k = q + QR, v = k + 2 * KB, raw = v + 2 * KB;
-    static constexpr int ml = raw + RAW * 2 * PB;              // DUP 2: the copies' (max, sum) of both groups
-    static constexpr int steps = ml + (DUP == 2 ? 1024 : 0);   // [8] step scales
+    static constexpr int ml = raw + RAW * 2 * PB;              // rows' factors; at the item's end the copies' (max, sum)
+    static constexpr int steps = ml + 1024;                    // [8] step scales
     static constexpr int rsc = steps + 8 * 32;                 // [RAW] page scales
     static constexpr int rscv = rsc + RAW * 8;
     static constexpr int bars = rscv + RAW * 8;
@@ -93,11 +93,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Bounded wait that gives up early once another role has given up.
 __device__ __forceinline__ bool wait_or(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int site) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    const long long t0 = clock64();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
+        if (clock64() - t0 > WAIT_CYCLES) {
             report(err, DERR_TIMEOUT, site);
             *abort = 1;
             return false;
@@ -160,13 +160,14 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
              *k_full = bars + 4 * R, *k_empty = k_full + 2, *v_full = k_full + 4, *v_empty = k_full + 6,
              *q_full = k_full + 8, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4,
              *o_done = q_full + 6, *handed = q_full + 8, *drain = q_full + 9, *i_full = q_full + 10,
-             *i_empty = q_full + 12, *copy_full = q_full + 14, *copy_free = q_full + 16,
-             *stored = q_full + 17, *judged = q_full + 18;
+             *i_empty = q_full + 12, *copy_full = q_full + 14, *copy_free = q_full + 15,
+             *stored = q_full + 16, *judged = q_full + 17;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
     volatile int* verdict = reinterpret_cast<volatile int*>(sm + L::misc + 8);
     volatile int* nan_rec = reinterpret_cast<volatile int*>(sm + L::nans);
     Work* works = reinterpret_cast<Work*>(sm + L::work);
+    float* back_of = reinterpret_cast<float*>(sm + L::ml);     // what a row of q was divided by
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform, so each role's code is
 
@@ -193,9 +194,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         mbar_init(q_free, 1);
         mbar_init(handed, 8);
         mbar_init(drain, 1);
-        mbar_init(copy_full, 2);
-        mbar_init(copy_full + 1, 2);
-        mbar_init(copy_free, 4);
+        mbar_init(copy_full, 8);
+        mbar_init(copy_free, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(i_full + i, 1);
             mbar_init(i_empty + i, TC_THREADS / 32 - 1);
@@ -207,10 +207,17 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         for (int i = 0; i < 4; ++i) nan_rec[4 * i] = 0;
     }
     if (warp == MMA_WARP) tc::tmem_alloc(tmem_base, 512);
+    pdl_wait();
+    Finder f{};
+    Work first;
+    first.item = -1;
+    if (warp == TMA_K) {      // the first item, while the barriers are made ready
+        f = make_finder(a, lane);
+        if ((int)blockIdx.x < f.total) first = find_item(a, f, (int)blockIdx.x, lane);
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    pdl_wait();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_base, 0);
 
     // This warp's k-th item; false at the end.  The K loader posts them.
@@ -248,57 +255,59 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             const int qi = pr / a.group, hq = w.kh * a.group + pr % a.group;
             const bool real = qi < q.n;
             int klo = 0, khi = 0;
-            float fr;
             {
-                // q: this thread's row, scaled into f16
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
-                                                                  (long long)(q.r0 + qi) * a.q_row + (long long)hq * a.q_head);
-                // 64 dims at a time, twice: the largest element, then the elements
-                uint4 e[8];
-                float top = 0.f;
+                // q, scaled into f16: a warp takes rows whole, 16 bytes a lane, so that
+                // lanes read neighbours (a row a thread took 16 times the L1 lookups:
+                // 7500 of a draft block's cycles, now XXXX)
+                constexpr int LPR = HD / 8, RPI = 32 / LPR;           // lanes of a row, rows at a time
+                constexpr int MINE = (KEYS ? 128 / DUP : 256) / 8;     // rows of a warp
+                constexpr int N = MINE / RPI < 4 ? MINE / RPI : 4;
+                const int at = lane & (LPR - 1);
+                const int i0 = w.tile * a.tile / a.group, rest = w.tile * a.tile - i0 * a.group;
+                const int by_group = (65536 + a.group - 1) / a.group;  // x / group = x by_group >> 16 below 4096
+                const T* q0 = reinterpret_cast<const T*>(a.q) + (long long)(q.r0 + i0) * a.q_row +
+                              (long long)w.kh * a.group * a.q_head + 8 * at;
 #pragma unroll 1
-                for (int h = 0; h < HD / 64; ++h) {
+                for (int x0 = 0; x0 < MINE; x0 += N * RPI) {
+                    uint4 e[N];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) e[k] = real ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
+                    for (int x = 0; x < N; ++x) {
+                        const int p = rest + warp * MINE + x0 + x * RPI + lane / LPR, i = p * by_group >> 16;
+                        e[x] = make_uint4(0, 0, 0, 0);
+                        if (i0 + i < q.n)
+                            e[x] = *reinterpret_cast<const uint4*>(q0 + (long long)i * a.q_row + (long long)(p - i * a.group) * a.q_head);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const T* ev = reinterpret_cast<const T*>(&e[k]);
+                    for (int x = 0; x < N; ++x) {
+                        const T* ev = reinterpret_cast<const T*>(&e[x]);
+                        float v[8], top = 0.f;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float x = fabsf(to_f32(ev[j]));
-                            top = fmaxf(top, x < INFINITY ? x : 0.f);
+                            v[j] = to_f32(ev[j]);
+                            const float y = fabsf(v[j]);
+                            top = fmaxf(top, y < INFINITY ? y : 0.f);
                         }
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        float inv, back;
+                        row_factor(top, &inv, &back);
+                        uint4 o;
+                        uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ow[j] = pack_f16x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+                        const int lr = warp * MINE + x0 + x * RPI + lane / LPR;      // of the item's rows
+                        uint8_t* qs = sm + L::q + (KEYS ? 0 : (lr >> 7) * L::QB) + (at >> 3) * 128 * 128;
+                        *reinterpret_cast<uint4*>(qs + swz128(lr & 127, at & 7)) = o;
+                        if (DUP == 2) *reinterpret_cast<uint4*>(qs + swz128(lr + 64, at & 7)) = o;
+                        if (at == 0) back_of[lr] = back;
                     }
                 }
-                if (real) row_keys(a, q, qi, &klo, &khi);
-                float inv, back;
-                row_factor(top, &inv, &back);
-                fr = back * a.scale_log2;
-                if (!KEYS || t == 0) {
-                    uint8_t* qs = sm + L::q + (KEYS ? 0 : t * L::QB);
-#pragma unroll 1
-                    for (int h = 0; h < HD / 64; ++h) {
-                        if (HD > 64) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) e[k] = real ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const T* ev = reinterpret_cast<const T*>(&e[k]);
-                            uint4 o;
-                            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                ow[j] = pack_f16x2(to_f32(ev[2 * j]) * inv, to_f32(ev[2 * j + 1]) * inv);
-                            *reinterpret_cast<uint4*>(qs + h * 128 * 128 + swz128(r, k)) = o;
-                        }
-                    }
-                    tc::fence_async_smem();
-                }
+                tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
 
+            if (real) row_keys(a, q, qi, &klo, &khi);
             // a warp without rows only takes part: its lanes' weights stay whatever
             // tensor memory holds, and nothing of them is written
             const bool any = __any_sync(0xffffffffu, real);
@@ -313,6 +322,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 }
                 tc::fence_after_sync();
                 const StepScale& sc = steps[(base + j) & 7];
+                const float fr = back_of[KEYS ? row : t * 128 + row] * a.scale_log2;
                 const int k0 = (w.p0 + 2 * j) * KV8_PAGE;
                 // 32 keys at a time, the next 32 scores on their way meanwhile
                 uint32_t buf[2][32];
@@ -438,92 +448,97 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 l = t == 0 ? la + lb : lb + la;
                 M = m;
             }
-            const int c_first = KEYS && t == 1 ? HD / 64 : 0, c_last = KEYS && t == 0 ? HD / 64 : HD / 32;
+            constexpr int NB = HD / 16 / (KEYS ? 2 : 1);           // 16-column blocks of a group
+            const int b_first = KEYS && t == 1 ? NB : 0;
             if ((KEYS || nt > 0) && nan_rec[4 * (items & 3)] == (int)items + 1)     // the same for all of a group's threads
                 put_nans<HD, KEYS, DUP>(a, nan_rec + 4 * (items & 3), t, r, nt > 0 ? o_tm : o_tm + other);
 
             // ---- the row's outputs, or its partial of this split
             const long long slot0 = (long long)item - w.split;    // splits of a tile are neighbours
-            const long long tk = ((long long)q.r0 * a.group / a.tile + w.s + w.tile) * a.n_kv + w.kh;
+            const long long tk = (((long long)q.r0 * a.group >> a.tile_log2) + w.s + w.tile) * a.n_kv + w.kh;
             const bool split = q.splits > 1;
             const bool fits = !split || (slot0 + q.splits <= a.part_cap && tk < a.ticket_cap);   // by the plan's bounds
             const int RT = a.tile;
             const long long PL = (long long)RT * (HD + 4);         // floats of a partial
             const int prow = KEYS ? row : t * 128 + row;
-            float4* xb = reinterpret_cast<float4*>(sm + L::q + t * (L::QB / 2));       // [8 columns / 32][64 rows]
-            float2* xml = reinterpret_cast<float2*>(sm + L::ml) + t * 64;
-            float ga = 1.f, gb = 0.f;      // factors of this copy's and the other's sums
-            if (DUP == 2 && copy == 0) {
-                ok = __all_sync(0xffffffffu, wait_or(copy_full + t, items & 1, abort, a.err, SITE_TC + 15));
-                if (!ok) break;
-                const float2 b = xml[row];
-                const float m = fmaxf(M, b.x);
-                ga = M == -INFINITY ? 0.f : ex2(M - m);
-                gb = b.x == -INFINITY ? 0.f : ex2(b.x - m);
-                l = (l != 0.f ? l * ga : 0.f) + (b.y != 0.f ? b.y * gb : 0.f);
-                M = m;
-            }
             float* part = split ? a.part + (slot0 + w.split) * PL : nullptr;
             T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
-            const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no key: zeros
-#pragma unroll 1
-            for (int c = c_first; c < c_last; ++c) {
-                float v[32];
+            auto sums = [&](int b, float (&v)[16]) {      // of both groups, block b of 16 columns
                 __syncwarp();
+                uint32_t y[16];
                 if (nt > 0) {
-                    tc::ld_x32(o_tm + c * 32, v);
+                    tc::ld_x16(o_tm + b * 16, y);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(y[x]);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = 0.f;
+                    for (int x = 0; x < 16; ++x) v[x] = 0.f;
                 }
                 if (KEYS && nt_other > 0) {
-                    float u[32];
-                    tc::ld_x32(o_tm + other + c * 32, u);
+                    tc::ld_x16(o_tm + other + b * 16, y);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = fmaf(u[x], fb, v[x] * fa);
+                    for (int x = 0; x < 16; ++x) v[x] = fmaf(__uint_as_float(y[x]), fb, v[x] * fa);
                 }
+            };
+            // DUP: a copy gives the other one half of its group's blocks, and adds
+            // the other's half to its own; both write
+            constexpr int HALF = NB / DUP;
+            float4* xb = reinterpret_cast<float4*>(sm + L::q) + (size_t)t * NB * 4 * 64 + row;    // [copy][HALF][4][64]
+            float2* xml = reinterpret_cast<float2*>(sm + L::ml) + row;                            // [copy][64]
+            float ga = 1.f, gb = 0.f;      // factors of copy 0's and copy 1's sums
+            if (DUP == 2) {
+#pragma unroll 1
+                for (int x = 0; x < HALF; ++x) {
+                    float v[16];
+                    sums(b_first + (1 - copy) * HALF + x, v);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        xb[((copy * HALF + x) * 4 + y) * 64] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+                }
+                if (t == 0) xml[copy * 64] = make_float2(M, l);      // the same in both groups
+                __syncwarp();
+                if (lane == 0) mbar_arrive(copy_full);
+                ok = __all_sync(0xffffffffu, wait_or(copy_full, items & 1, abort, a.err, SITE_TC + 15));
+                if (!ok) break;
+                const float2 m0 = xml[0], m1 = xml[64];
+                M = fmaxf(m0.x, m1.x);
+                ga = m0.x == -INFINITY ? 0.f : ex2(m0.x - M);
+                gb = m1.x == -INFINITY ? 0.f : ex2(m1.x - M);
+                l = (m0.y != 0.f ? m0.y * ga : 0.f) + (m1.y != 0.f ? m1.y * gb : 0.f);
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no key: zeros
+#pragma unroll 1
+            for (int x = 0; x < HALF; ++x) {
+                const int b = b_first + copy * HALF + x;
+                float v[16];
+                sums(b, v);
                 if (DUP == 2) {
-                    float4* xc = xb + (c - c_first) * 8 * 64 + row;
-                    if (copy == 1) {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) xc[x * 64] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                        continue;
-                    }
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 z = xb[(((1 - copy) * HALF + x) * 4 + y) * 64];
+                        const float u[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float4 y = xc[x * 64];
-                        v[4 * x] = fmaf(y.x, gb, v[4 * x] * ga);
-                        v[4 * x + 1] = fmaf(y.y, gb, v[4 * x + 1] * ga);
-                        v[4 * x + 2] = fmaf(y.z, gb, v[4 * x + 2] * ga);
-                        v[4 * x + 3] = fmaf(y.w, gb, v[4 * x + 3] * ga);
+                        for (int k = 0; k < 4; ++k)
+                            v[4 * y + k] = copy == 0 ? fmaf(u[k], gb, v[4 * y + k] * ga) : fmaf(v[4 * y + k], gb, u[k] * ga);
                     }
                 }
                 if (real && split && fits) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        reinterpret_cast<float4*>(part)[(size_t)(c * 8 + x) * RT + prow] =
-                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    for (int y = 0; y < 4; ++y)
+                        reinterpret_cast<float4*>(part)[(size_t)(b * 4 + y) * RT + prow] =
+                            make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
                 }
-                if (real && !split) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float o[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = v[16 * b + x];
-                        store16<T>(dst + c * 32 + 16 * b, o, inv);
-                    }
-                }
+                if (real && !split) store16<T>(dst + b * 16, v, inv);
             }
-            if (DUP == 2 && copy == 1) xml[row] = make_float2(M, l);
             __syncwarp();
             tc::fence_before_sync();   // the accumulator has been read
-            if (DUP == 2 && lane == 0) mbar_arrive(copy == 1 ? copy_full + t : copy_free);
+            if (DUP == 2 && lane == 0) mbar_arrive(copy_free);
             if (!split) {
-                if (real && copy == 0 && a.lse && c_first == 0)
+                if (real && copy == 0 && a.lse && b_first == 0)
                     a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
                 continue;
             }
-            if (real && fits && copy == 0 && c_first == 0) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow] = make_float2(M, l);
+            if (real && fits && copy == 0 && b_first == 0) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow] = make_float2(M, l);
             // the CTA whose split of the tile is the last to arrive folds them all, in
             // split order: a thread takes a row and a share of its columns
             __threadfence();
@@ -799,7 +814,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         // every MMA has finished before tensor memory is given back
         if (tc::elect_one()) tc::commit(drain);
         __syncwarp();
-        mbar_wait_bounded(drain, 0);
+        mbar_wait(drain, 0);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- pages
@@ -810,28 +825,19 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         uint8_t* ring = sm + L::raw + (is_k ? 0 : R * PB);
         unsigned it = 0;   // pages issued
         bool ok = true;
-        Finder f{};
-        int item = -1;
-        if (is_k) {
-            f = make_finder(a, lane);
-            item = (int)blockIdx.x < f.total ? (int)blockIdx.x : -1;
-        }
-        Work wk;
+        int asked = 0;
+        Work wk = first;
         for (unsigned items = 0; ok; ++items) {
             if (is_k) {
-                // finds and posts the item; the next one's number is on its way
-                wk.item = -1;
-                if (item >= 0) wk = find_item(a, f, item, lane);
-                int n = -1;
+                // posts the item; the next one's number is on its way
                 if (lane == 0) {
                     if (items < 2 || wait_or(i_empty + (items & 1), ((items >> 1) - 1) & 1, abort, a.err, SITE_TC + 14)) {
                         works[items & 1] = wk;
                         mbar_arrive(i_full + (items & 1));
                     }
-                    if (item >= 0) n = next_item(a, f.total);
+                    if (wk.item >= 0) asked = ask_item(a, f.total);
                 }
-                if (item < 0) break;
-                item = __shfl_sync(0xffffffffu, n, 0);
+                if (wk.item < 0) break;
             } else if (!take(items, &wk)) {
                 break;
             }
@@ -886,11 +892,17 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 ks = next_ks;
                 vs = next_vs;
             }
+            if (is_k) {
+                int next = lane == 0 ? settle_item(a, f.total, asked) : 0;
+                next = __shfl_sync(0xffffffffu, next, 0);
+                wk.item = -1;
+                if (next >= 0) wk = find_item(a, f, next, lane);
+            }
         }
         // no copy of this CTA is in flight when it ends
         if (lane == 0) {
             const unsigned n = it < R ? it : R;
-            for (unsigned i = it - n; i < it; ++i) mbar_wait_bounded(rfull + i % R, (i / R) & 1);
+            for (unsigned i = it - n; i < it; ++i) mbar_wait(rfull + i % R, (i / R) & 1);
         }
         __syncwarp();
     }
