@@ -257,8 +257,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             int klo = 0, khi = 0;
             {
                 // q, scaled into f16: a warp takes rows whole, 16 bytes a lane, so that
-                // lanes read neighbours (a row a thread took 16 times the L1 lookups:
-                // 7500 of a draft block's cycles, now XXXX)
+                // lanes read neighbours (a row a thread, with 16 times the L1 lookups,
+                // took 7500 to 10500 cycles an item; this 3500)
                 constexpr int LPR = HD / 8, RPI = 32 / LPR;           // lanes of a row, rows at a time
                 constexpr int MINE = (KEYS ? 128 / DUP : 256) / 8;     // rows of a warp
                 constexpr int N = MINE / RPI < 4 ? MINE / RPI : 4;
@@ -324,6 +324,24 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 const StepScale& sc = steps[(base + j) & 7];
                 const float fr = back_of[KEYS ? row : t * 128 + row] * a.scale_log2;
                 const int k0 = (w.p0 + 2 * j) * KV8_PAGE;
+                // a step that not all rows see whole: masked scores become -inf in
+                // tensor memory first (code in the loop below would cost every step)
+                if (k0 < w.in_lo || k0 + STEP > w.in_hi || sc.ks[0] < 0.f || sc.ks[1] < 0.f) {
+#pragma unroll 1
+                    for (int c = 2 * copy; c < 2 * copy + 4 / DUP; ++c) {
+                        uint32_t v[32];
+                        tc::ld_x32_async(s_tm + c * 32, v);
+                        tc::ld_wait(v);
+                        const int lo = klo - k0 - c * 32, hi = sc.ks[c >> 1] < 0.f ? 0 : khi - k0 - c * 32;
+                        const uint32_t seen = lo < 32 && hi > 0 && lo < hi ? ~0u >> (hi < 32 ? 32 - hi : 0) & ~0u << (lo > 0 ? lo : 0) : 0u;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!(seen & (1u << x))) v[x] = 0xff800000u;      // -inf
+                        tc::st_x16(s_tm + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                        tc::st_x16(s_tm + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                    }
+                    tc::st_wait();
+                }
                 // 32 keys at a time, the next 32 scores on their way meanwhile
                 uint32_t buf[2][32];
                 const int c0 = 2 * copy;
@@ -340,16 +358,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     const int c = c0 + cc;
                     uint32_t (&v)[32] = buf[cc & 1];
                     tc::ld_wait(v);
-                    const int kp = k0 + c * 32;
                     const float ks = sc.ks[c >> 1], ev = sc.ev[c >> 1];
                     const bool there = ks >= 0.f;
                     const float f = there ? fmaxf(fr * ks, 0x1p-126f) : 1.f;   // above 0: a masked score stays -inf
-                    if (!there || kp < w.in_lo || kp + 32 > w.in_hi) {
-                        const int lo = there ? klo - kp : 32, hi = khi - kp;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            v[x] = x >= lo && x < hi ? v[x] : 0xff800000u;      // -inf
-                    }
                     float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
@@ -628,7 +639,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     d->iv[lane] = sc.y > 0.f ? 1.f / sc.y : 0.f;
                 }
                 uint8_t* dst = sm + L::k + st * L::KB;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {                  // the step's pages
                     constexpr int MINE = HD / 8 / KC;          // units of 32 keys x 16 dims
                     uint4 e[MINE];
@@ -689,7 +700,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 const bool plain = kp >= w.in_lo && kp + STEP <= w.in_hi && there[0] && there[1];
                 uint32_t seen = 0;
                 uint8_t* dst = sm + L::v + st * L::KB;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     constexpr int MINE = HD / 8 / VC;          // units of 32 keys x 16 dims
                     uint32_t r4[MINE][4];
