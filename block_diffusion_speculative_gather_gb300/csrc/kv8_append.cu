@@ -17,6 +17,11 @@
 // written once at 8 bits.  A CTA takes a window of rows and finds the chains
 // that begin in it: a few long ones (prompts) are done by the whole CTA one
 // after another, many short ones (single tokens) a warp each.
+//
+// Bound: at many rows by the chain of each CTA (slots, rows, maximum, codes:
+// three dependent trips to memory), which five CTAs an SM do not hide: four
+// ragged prompts of 10000 f16 rows x 8 kv heads of 128 take 24 us where their
+// bytes take 9 (2.6 TB/s); at few by latency: 34 rows 3.4 us.
 
 #include "gemm.cuh"
 #include "kv8.cuh"
@@ -82,8 +87,7 @@ __device__ __forceinline__ void load8(const T* p, Unit<T>& u) {
 // threads of which this is `t` (a warp or the CTA).  A unit is 8 elements of
 // a row; a thread keeps up to KEEP units in registers (a whole page's run of
 // the CTA, or 16 rows of a warp at head_dim 128), so that they are read once.
-// (10000 rows of ragged prompts: 256 threads keeping 4 22.8 us, 128 keeping 8
-// 22.1.)
+// (10000 rows of ragged prompts: 256 threads keeping 4 units 4 % slower.)
 constexpr int KEEP = 8;
 
 template <typename T, int HD, bool WIDE, bool CTA>
@@ -189,23 +193,47 @@ __global__ void __launch_bounds__(AT) kv8_append_kernel(Kv8AppendArgs a, int win
         const int sl = a.slots[r];
         return sl >= cap ? -1 : sl;
     };
-    // chains that begin in the window, in row order (a warp's ballots)
-    if (tid < 32) {
-        int n = 0;
-        for (int b = 0; b < rows; b += 32) {
-            const int i = b + tid;
-            bool begins = false;
-            if (i < rows) {
-                const int sl = s_slot[i + 1];
-                if (sl >= 0) {
-                    int r = w0 + i - 1;
-                    while (r >= 0 && slot_at(r) < 0) --r;   // the last row that is not skipped
-                    begins = r < 0 || slot_at(r) / KV8_PAGE != sl / KV8_PAGE;
+    // the first row from r on (step 1) or back (step -1) that is not skipped, for
+    // a whole warp; -1 if there is none.  512 rows at a time, all loads in
+    // flight: a padded call has many behind its last (32 of 4096 rows in use:
+    // row by row 455 us, so 21 us).
+    auto next_row = [&](int r, int step) -> int {
+        if (r >= 0 && r < a.rows && slot_at(r) >= 0) return r;
+        for (long long b = r; b >= 0 && b < a.rows; b += 512 * step) {
+            unsigned first = ~0u;
+#pragma unroll
+            for (int k = 15; k >= 0; --k) {
+                const int d = 32 * k + (tid & 31);
+                const long long x = b + (long long)step * d;
+                if (x >= 0 && x < a.rows) {
+                    const int sl = a.slots[x];
+                    if (sl >= 0 && sl < cap) first = d;
                 }
             }
+            first = __reduce_min_sync(0xffffffffu, first);
+            if (first != ~0u) return (int)(b + (long long)step * (int)first);
+        }
+        return -1;
+    };
+    // chains that begin in the window, in row order (a warp's ballots): rows on
+    // another page than the last row before them that is not skipped
+    if (tid < 32) {
+        int n = 0, last = -2;      // page of the last row so far; -2: not looked up
+        for (int b = 0; b < rows; b += 32) {
+            const int i = b + tid, sl = i < rows ? s_slot[i + 1] : -1, page = sl >= 0 ? sl / KV8_PAGE : -1;
+            const unsigned valid = __ballot_sync(0xffffffffu, sl >= 0);
+            if (!valid) continue;
+            if (last == -2) {
+                const int r = next_row(w0 - 1, -1);
+                last = r < 0 ? -1 : slot_at(r) / KV8_PAGE;
+            }
+            const unsigned below = valid & ((1u << tid) - 1);
+            const int from = __shfl_sync(0xffffffffu, page, below ? 31 - __clz(below) : 0);
+            const bool begins = sl >= 0 && (below ? from : last) != page;
             const unsigned m = __ballot_sync(0xffffffffu, begins);
             if (begins) s_run[n + __popc(m & ((1u << tid) - 1))] = i;
             n += __popc(m);
+            last = __shfl_sync(0xffffffffu, page, 31 - __clz(valid));
         }
         if (tid == 0) s_n = n;
     }
@@ -228,9 +256,8 @@ __global__ void __launch_bounds__(AT) kv8_append_kernel(Kv8AppendArgs a, int win
             const int n = ~on[0] ? __ffs(~on[0]) - 1 : 32 + (~on[1] ? __ffs(~on[1]) - 1 : 32);
             if (by_cta) run_append<T, HD, WIDE, true>(a, which, head, r, n, page, off, tid, red);
             else run_append<T, HD, WIDE, false>(a, which, head, r, n, page, off, tid & 31, red);
-            r += n;
-            while (r < a.rows && slot_at(r) < 0) ++r;
-            if (r >= a.rows) break;
+            r = next_row(r + n, 1);
+            if (r < 0) break;
             sl = slot_at(r);
             if (sl / KV8_PAGE != page) break;
         }

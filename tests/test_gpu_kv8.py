@@ -824,3 +824,20 @@ def test_the_paged_cache_class_runs_the_operators(capi):
     with pytest.raises(capi.DFlashError):
         kv.check()
     kv.check()
+
+
+@pytest.mark.parametrize("gap", [3, 31, 33, 70, 140, 700, 3000])
+def test_append_over_long_gaps_of_skipped_rows(capi, gap):
+    """Runs of one page with skipped rows between them, and a padded end."""
+    skip = [-1] * gap
+    slots = skip + [64, 65, 66] + skip + [67, 68] + skip + [69, -5, 70] + skip + [195, 196, 2, 3] + skip
+    g = torch.Generator().manual_seed(gap)
+    x = torch.randn(2, len(slots), 1, 64, generator=g) * torch.exp(3 * torch.randn(len(slots), 1, 1, generator=g))
+    check_append(capi, x[0].to(BF).cuda(), x[1].to(BF).cuda(), slots, pool(4, 1, 64, seed=2))
+
+
+@pytest.mark.parametrize("rows,held", [([2, 3, 1], [0, 0, 70]), ([20], [0]), ([160, 1], [0, 0])])
+def test_sequences_without_positions(capi, rows, held):
+    st = attn_state(4, 2, 64, rows, held, BF, seed=6)
+    attend(capi, st)
+    check_attend(st)
