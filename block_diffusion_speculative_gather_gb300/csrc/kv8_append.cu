@@ -19,9 +19,9 @@
 // after another, many short ones (single tokens) a warp each.
 //
 // Bound: at many rows by the chain of each CTA (slots, rows, maximum, codes:
-// three dependent trips to memory), which five CTAs an SM do not hide: four
+// three dependent trips to memory), which four CTAs an SM do not hide: four
 // ragged prompts of 10000 f16 rows x 8 kv heads of 128 take 24 us where their
-// bytes take 9 (2.6 TB/s); at few by latency: 34 rows 3.4 us.
+// bytes take 9 (2.6 TB/s); at few by latency: 32 rows 3.4 us.
 
 #include "gemm.cuh"
 #include "kv8.cuh"

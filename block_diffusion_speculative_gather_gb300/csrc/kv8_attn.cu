@@ -16,6 +16,18 @@
 // bf16 and f16 rows exact but for elements 2^-14 below the row's largest,
 // that lose low bits.  e4m3 codes are exact in f16.  P is rounded to f16
 // (half a step: 2^-11 of the weight); scores, sums and outputs are fp32.
+//
+// This form: 16 packed rows a tile, mma.sync (a tcgen05 tile would be an
+// eighth full at best, and a page's work is its bytes).  A warp takes whole
+// pages, so its warps never meet inside an item, and one TMA warp keeps 11
+// (head_dim 64: 22) pages in flight, 176 KB of an SM's shared memory.  Bound by
+// DRAM at many sequences: 19 of 16384 positions, 8 kv heads of 128, 117 us =
+// 5.4 TB/s (0.80 of a measured copy; 32 of 4096 to 16384 159 us, 4.6 TB/s, as
+// the last items run alone), by latency at few: one of 1088 10.8 us, of which
+// the launch, finding the item, tables, pages and the fold are a chain of
+// about nine trips to memory.
+//
+// Splits, items and the tcgen05 form's cases: kv8_attn_plan below.
 
 #include <mutex>
 
@@ -603,20 +615,58 @@ cudaError_t allow_smem(const void* kern) {
 // sequence: the mma.sync kernel's 16-row tiles up to 16, a tile whose two
 // softmax groups take alternate keys up to 128 (64 rows where a block of 16
 // rows fits, as sequences differ and a second tile reads the keys again; 128
-// else), two 128-row tiles over the same keys above.
+// else), two 128-row tiles over the same keys above.  While items are few, the
+// next smaller tiles are the faster ones though they read the keys again: more
+// SMs have work, and a small tile's own chain is shorter.  Microseconds, 8 kv
+// heads of 128, two tiles of each kind and the items of the smaller:
+//   rows of a call          positions   smaller tile       larger
+//   1 x 32 packed                4000   16 (16 items) 16.1  64  20.7
+//   1 x 64                       4000   16 (32)       19.2  64  21.2
+//   1 x 64                      16384   16 (32)       38.1  64  31.9
+//   16 x 32                      4000   16 (256)      70.4  64  44.7
+//   1 x 256                      8000   64 (32)       29.4  128 33.0
+//   1 x 512                      8000   64 (64)       43.3  128 38.1
+//   2 x 1024                     8000   128 (128)     88.3  256 91.4
+//   2 x 2048                     8000   128 (256)    167.7  256 149.2
+// so 16-row tiles up to a sixth of the SMs, 64-row ones up to a quarter,
+// 128-row ones up to all of them.
 //
 // Both this and the splits of a tile's pages follow from the call's row,
 // sequence and head counts and the sequence's own length alone: its results
 // do not depend on what the other sequences hold.
 Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int max_pages, int sms) {
     Kv8AttnPlan p;
-    const long long packed = (long long)rows * (n_q / n_kv);
+    const int group = n_q / n_kv;
+    const long long packed = (long long)rows * group;
     const long long each = (packed + S - 1) / S;
-    p.form = each <= 16 ? KV8_MMA : (each <= 128 ? KV8_TC_KEYS : KV8_TC_ROWS);
-    p.tile = p.form == KV8_MMA ? KT : (p.form == KV8_TC_ROWS ? 256 : (each <= 64 && 16 * (n_q / n_kv) <= 64 ? 64 : 128));
+    // items of a split each: were all rows dealt evenly, and at most
+    auto even = [&](int tile) { return S * ((each + tile - 1) / tile) * n_kv; };
+    auto most = [&](int tile) { return S == 1 ? even(tile) : (packed / tile + S) * n_kv; };
+    p.form = KV8_TC_KEYS;
+    long long at_once;
+    if (each <= KT || most(KT) * 6 <= sms) {
+        p.form = KV8_MMA;
+        p.tile = KT;
+        at_once = each <= KT ? even(KT) : most(KT);
+    } else if (each <= 64 && 16 * group <= 64) {
+        p.tile = 64;
+        at_once = even(64);
+    } else if (most(64) * 4 <= sms) {
+        p.tile = 64;
+        at_once = most(64);
+    } else if (each <= 128) {
+        p.tile = 128;
+        at_once = even(128);
+    } else if (most(128) <= sms) {
+        p.tile = 128;
+        at_once = most(128);
+    } else {
+        p.form = KV8_TC_ROWS;
+        p.tile = 256;
+        at_once = even(256);
+    }
+    if (at_once < 1) at_once = 1;
     const long long tiles = packed / p.tile + S;           // slots: floor(first packed row / tile) + sequence
-    long long usual = (packed + p.tile - 1) / p.tile;
-    if (usual < S) usual = S;
     // Splits of a sequence with P pages (a value for each power of two): as many
     // as let every item start at once, an SM each, but not below 4 (6) pages an
     // item.  An item behind another one costs far more than its pages: 8
@@ -625,13 +675,13 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
     // 25, 18 us with 1, 4, 16.  Where more items than SMs wait anyway, single tokens
     // of long sequences are halved all the same, so that the last items are short:
     // 32 of 4096 to 16384 positions 180 -> 159 us (equal ones of 10000: 162 -> 180).
-    const long long once = usual * n_kv < sms ? sms / (usual * n_kv) : 1, least = p.form == KV8_MMA ? 4 : 6;
+    const long long once = at_once < sms ? sms / at_once : 1, least = p.form == KV8_MMA ? 4 : 6;
     long long cap = 1;
     for (int b = 0; b < 32; ++b) {
         long long c = (1LL << b) / least;
         if (c > once) c = once;
         if (c > 64) c = 64;
-        if (usual * n_kv > sms && p.form == KV8_MMA && b >= 7) c = 2;
+        if (at_once > sms && p.form == KV8_MMA && b >= 7) c = 2;
         p.caps[b] = (uint8_t)(c < 1 ? 1 : c);
         if ((1LL << b) <= max_pages && p.caps[b] > cap) cap = p.caps[b];
     }

@@ -841,3 +841,46 @@ def test_sequences_without_positions(capi, rows, held):
     st = attn_state(4, 2, 64, rows, held, BF, seed=6)
     attend(capi, st)
     check_attend(st)
+
+
+# Calls with enough heads or rows that larger tiles are chosen (152 SMs).
+TILES = [
+    # n_q, n_kv, dim, rows, held
+    (32, 8, 128, [16], [300]),                              # 64 rows, held twice
+    (40, 10, 64, [12, 3], [700, 65]),
+    (8, 8, 64, [200], [260]),                               # several of 64
+    (100, 20, 64, [16, 9], [700, 64]),                      # 128 rows
+    (64, 16, 128, [30, 20, 5], [1000, 20, 333]),
+    (16, 16, 128, [130], [200]),                            # several of 128
+    (32, 16, 128, [90, 150, 130, 100, 70], [400, 150, 1000, 777, 64]),   # two tiles of 128
+    (40, 20, 64, [300, 280], [310, 900]),
+]
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows,held", TILES)
+@pytest.mark.parametrize("causal,window,kind", [(True, 0, BF), (True, 100, F16), (False, 0, F16), (False, 70, BF)])
+def test_larger_tiles(capi, n_q, n_kv, dim, rows, held, causal, window, kind):
+    st = attn_state(n_q, n_kv, dim, rows, held, kind, seed=12)
+    attend(capi, st, causal, window)
+    check_attend(st, causal, window)
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows,held", TILES)
+def test_larger_tiles_repeat_their_bits(capi, n_q, n_kv, dim, rows, held):
+    st = attn_state(n_q, n_kv, dim, rows, [h + 900 for h in held], BF, seed=13)
+    ws = attend(capi, st)
+    want, lse, err = st["out"].clone(), st["lse"].clone(), ints([0, 0])
+    tabs = ints(st["table"]), ints(st["held"]), ints(st["start"])
+    other = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(200):
+        st["out"].fill_(3.0)
+        capi.dflash_kv8_attention(st["q"], *st["cache"], *tabs, st["out"], ws, err, lse=st["lse"])
+        other |= (st["out"] != want).any() | (st["lse"] != lse).any()
+    assert err.tolist() == [0, 0] and not other.item()
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows,held", TILES)
+@pytest.mark.parametrize("causal,window", [(True, 90), (False, 33)])
+@pytest.mark.parametrize("where", ["v", "k"])
+def test_larger_tiles_keep_nan_with_its_rows(capi, n_q, n_kv, dim, rows, held, causal, window, where):
+    test_nan_stays_with_the_rows_that_see_it(capi, n_q, n_kv, dim, rows, held, causal, window, where)
