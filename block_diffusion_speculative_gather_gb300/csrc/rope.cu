@@ -9,8 +9,8 @@
 // A warp takes one row and some of its heads; a lane keeps its pairs' cosines
 // and sines in registers for all heads it visits.  Bound by the rows' bytes
 // (read once, written once) at many rows and by latency at few, where a row's
-// heads are spread over more warps.  16384 rows of 40 heads of 128, bf16: 60 us,
-// 5.6 TB/s; 16 rows: 2.6 us.
+// heads are spread over more warps.  16384 rows of 40 heads of 128, bf16, half of
+// the head rotated: 60 us, 5.6 TB/s; 16 rows: 2.5 us.
 
 #include "gemm.cuh"
 #include "kv8.cuh"
