@@ -73,7 +73,7 @@ template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr int bars = rscv + RAW * 8;
     static constexpr int n_bars = 4 * RAW + 8 + 2 + 6 + 1 + 1 + 4 + 3 + 2;
     static constexpr int work = bars + n_bars * 8;             // [2] items
-    static constexpr int misc = work + 2 * sizeof(Work);       // tensor-memory base, abort flag, verdict
+    static constexpr int misc = work + 2 * sizeof(Work);       // tensor-memory base, abort flag, last arriver
     static constexpr int nans = misc + 16;                     // [4] items with NaN codes to look up: (count, s, idx, tile)
     static constexpr size_t bytes = 1024 + nans + 64;
 };
@@ -175,10 +175,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
              *q_full = k_full + 8, *q_free = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 4,
              *o_done = q_full + 6, *handed = q_full + 8, *drain = q_full + 9, *i_full = q_full + 10,
              *i_empty = q_full + 12, *copy_full = q_full + 14, *copy_free = q_full + 15,
-             *stored = q_full + 16, *judged = q_full + 17;
+             *stored = q_full + 16, *counted = q_full + 17;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
-    volatile int* verdict = reinterpret_cast<volatile int*>(sm + L::misc + 8);
+    volatile int* last = reinterpret_cast<volatile int*>(sm + L::misc + 8);
     volatile int* nan_rec = reinterpret_cast<volatile int*>(sm + L::nans);
     Work* works = reinterpret_cast<Work*>(sm + L::work);
     float* back_of = reinterpret_cast<float*>(sm + L::ml);     // what a row of q was divided by
@@ -215,7 +215,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             mbar_init(i_empty + i, TC_THREADS / 32 - 1);
         }
         mbar_init(stored, 8);
-        mbar_init(judged, 1);
+        mbar_init(counted, 1);
         fence_mbar_init();
         *abort = 0;
         for (int i = 0; i < 4; ++i) nan_rec[4 * i] = 0;
@@ -573,16 +573,16 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 ok = __all_sync(0xffffffffu, wait_or(stored, folds & 1, abort, a.err, SITE_TC + 15));
                 if (!ok) break;
                 if (lane == 0) {
-                    *verdict = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
-                    if (*verdict) a.tickets[tk] = 0;
-                    mbar_arrive(judged);
+                    *last = fits && atomicAdd(a.tickets + tk, 1) == q.splits - 1;
+                    if (*last) a.tickets[tk] = 0;
+                    mbar_arrive(counted);
                 }
                 __syncwarp();
             }
-            ok = __all_sync(0xffffffffu, wait_or(judged, folds & 1, abort, a.err, SITE_TC + 15));
+            ok = __all_sync(0xffffffffu, wait_or(counted, folds & 1, abort, a.err, SITE_TC + 15));
             if (!ok) break;
             ++folds;
-            if (!*verdict) continue;
+            if (!*last) continue;
             __threadfence();
             const int frow = tid % RT, shares = 256 / RT, share = tid / RT;
             const int fr_ = w.tile * RT + frow, fi = fr_ / a.group, fh = w.kh * a.group + fr_ % a.group;

@@ -208,7 +208,7 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     if (const int r = check_attn_shape(q->rows, q->S, q->n_q, cache->n_kv, cache->head_dim, q->max_pages)) return r;
     if (q->dtype != DFLASH_BF16 && q->dtype != DFLASH_F16)
         return report_error(DFLASH_ERR_ARG, "dtype %d: BF16 or F16", q->dtype);
-    if (!(q->scale > 0.f) || !std::isfinite(q->scale) || q->window < 0)
+    if (!(q->scale > 0.f) || !std::isfinite(q->scale * 1.4426950408889634f) || q->window < 0)
         return report_error(DFLASH_ERR_ARG, "scale %g (above 0) window %d", (double)q->scale, q->window);
     if (q->rows == 0) return DFLASH_OK;
     if (!q->q || !q->out || !q->table || !q->kv_len || !q->row_start) return report_error(DFLASH_ERR_ARG, "NULL argument");

@@ -884,3 +884,17 @@ def test_larger_tiles_repeat_their_bits(capi, n_q, n_kv, dim, rows, held):
 @pytest.mark.parametrize("where", ["v", "k"])
 def test_larger_tiles_keep_nan_with_its_rows(capi, n_q, n_kv, dim, rows, held, causal, window, where):
     test_nan_stays_with_the_rows_that_see_it(capi, n_q, n_kv, dim, rows, held, causal, window, where)
+
+
+@pytest.mark.parametrize("S", [33, 100, 1000, 4096])
+def test_many_sequences(capi, S):
+    """More sequences than a warp's lanes, lengths of zero among them."""
+    g = torch.Generator().manual_seed(S)
+    held = torch.randint(0, 200, (S,), generator=g).tolist()
+    rows = [min(h, n) for h, n in zip(held, torch.randint(0, 4, (S,), generator=g).tolist())]
+    st = attn_state(2, 1, 64, rows, held, BF, seed=S)
+    ws = attend(capi, st)
+    check_attend(st)
+    first = st["out"].clone()
+    attend(capi, st, workspace=ws)
+    assert torch.equal(first, st["out"])

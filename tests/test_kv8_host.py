@@ -60,7 +60,7 @@ def test_cache_guards(capi, kw, code):
     (dict(n_q=3), CONFIG), (dict(n_q=34), CONFIG), (dict(n_q=0), CONFIG), (dict(S=0), CONFIG),
     (dict(S=4097), CONFIG), (dict(rows=-1), ARG), (dict(max_pages=0), ARG), (dict(dtype=0), ARG),
     (dict(dtype=2), ARG), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
-    (dict(scale=float("inf")), ARG), (dict(window=-1), ARG), (dict(q=PTR + 2), ARG),
+    (dict(scale=float("inf")), ARG), (dict(scale=3e38), ARG), (dict(window=-1), ARG), (dict(q=PTR + 2), ARG),
     (dict(q_row=513), ARG), (dict(out_head=4), ARG), (dict(table=None), ARG), (dict(out=None), ARG),
     (dict(rows=1 << 30, n_q=32), CONFIG)])
 def test_query_guards(capi, kw, code):
