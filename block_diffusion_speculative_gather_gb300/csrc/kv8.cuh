@@ -14,6 +14,7 @@ namespace dfl {
 
 constexpr int KV8_PAGE = 64;
 constexpr size_t KV8_QUEUE_BYTES = 256;   // of an attention workspace, then its tickets, then partials
+constexpr int KV8_TICKETS = 16384;        // tiles x kv heads of a call whose pages are split
 
 struct PagesPlanArgs {
     const int* kv_len;

@@ -682,13 +682,15 @@ Kv8AttnPlan kv8_attn_plan(int rows, int S, int n_q, int n_kv, int head_dim, int 
         if (c > once) c = once;
         if (c > 64) c = 64;
         if (at_once > sms && p.form == KV8_MMA && b >= 7) c = 2;
-        p.caps[b] = (uint8_t)(c < 1 ? 1 : c);
+        p.caps[b] = (uint8_t)(c < 1 || tiles * n_kv > KV8_TICKETS ? 1 : c);
         if ((1LL << b) <= max_pages && p.caps[b] > cap) cap = p.caps[b];
     }
     p.split_cap = (int)cap;
     p.ticket_cap = tiles * n_kv;
     p.part_cap = cap > 1 ? tiles * n_kv * cap : 0;
-    p.ticket_bytes = (size_t)((p.ticket_cap * 4 + 255) / 256 * 256);
+    // the tickets' place is the same in every call, so that calls of different
+    // shapes can share a workspace: none's partials lie where another counts
+    p.ticket_bytes = cap > 1 ? KV8_TICKETS * 4 : 0;
     p.bytes = KV8_QUEUE_BYTES + p.ticket_bytes + (size_t)p.part_cap * p.tile * (head_dim + 4) * 4;
     return p;
 }

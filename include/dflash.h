@@ -591,9 +591,10 @@ int dflash_kv8_append(const dflash_kv8_cache* cache /*host*/, const void* k, int
  * positions and on the call's row, sequence and head counts, not on the
  * other sequences.  Codes of positions a row does not see do not matter to
  * it, NaN included; a row that sees a NaN code gets NaN (V: in its dim).
- * Workspace: dflash_kv8_workspace_bytes, zero-filled before its first use
- * (completed calls leave its counters at zero); calls that share one must
- * not overlap on the GPU; zero it again after err was set.  A length or page
+ * Workspace: dflash_kv8_workspace_bytes of the call's counts (more rows may
+ * need less), zero-filled before its first use (completed calls leave its
+ * counters at zero).  Calls of any shapes can share one that is large enough
+ * for each, but must not overlap on the GPU; zero it again after err was set.  A length or page
  * out of range: err {2, site}, that sequence (page) is left out.
  * Errors: CONFIG, ARG, CUDA.
  */

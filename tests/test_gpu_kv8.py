@@ -898,3 +898,24 @@ def test_many_sequences(capi, S):
     first = st["out"].clone()
     attend(capi, st, workspace=ws)
     assert torch.equal(first, st["out"])
+
+
+def test_one_workspace_for_calls_of_many_shapes(capi):
+    """Counters stay apart from every shape's partial sums."""
+    shapes = [(32, 8, 128, [1], [4000]), (8, 2, 128, [16] * 4, [3000] * 4), (16, 8, 64, [1] * 40, [9000] + [500] * 39),
+              (8, 2, 128, [70, 33, 129], [2000, 1400, 1130]), (64, 16, 128, [30, 20, 5], [1000, 20, 333]),
+              (8, 1, 64, [300], [5000]), (2, 1, 64, [1], [64])]
+    states, size = [], 0
+    for i, s in enumerate(shapes):
+        st = attn_state(*s, BF, seed=i)
+        ws = attend(capi, st)
+        check_attend(st)
+        states.append((st, st["out"].clone(), st["lse"].clone()))
+        size = max(size, ws.numel())
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    order = [0, 1, 2, 3, 4, 5, 6, 5, 3, 1, 6, 4, 2, 0, 3, 0, 5, 1, 1, 2, 4]
+    for i in order:
+        st, out, lse = states[i]
+        st["out"].fill_(3.0), st["lse"].fill_(3.0)
+        attend(capi, st, workspace=ws)
+        assert torch.equal(st["out"], out) and torch.equal(st["lse"], lse), i
