@@ -23,9 +23,9 @@
 // (head_dim 64: 22) pages in flight, 176 KB of an SM's shared memory.  Bound by
 // DRAM at many sequences: 19 of 16384 positions, 8 kv heads of 128, 117 us =
 // 5.4 TB/s (0.80 of a measured copy; 32 of 4096 to 16384 159 us, 4.6 TB/s, as
-// the last items run alone), by latency at few: one of 1088 10.8 us, of which
+// the last items run alone), by latency at few: one of 1088 10.2 us, of which
 // the launch, finding the item, tables, pages and the fold are a chain of
-// about nine trips to memory.
+// about eight trips to memory.
 //
 // Splits, items and the tcgen05 form's cases: kv8_attn_plan below.
 
@@ -541,23 +541,40 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                 for (int k = 0; k < NF; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (real) {
                     const float* src = a.part + slot0 * PL;
-                    for (int v = 0; v < q.splits; ++v)
-                        fm = fmaxf(fm, __ldcg(src + (size_t)v * PL + KT * HD + row * 2));
-#pragma unroll 4
-                    for (int v = 0; v < q.splits; ++v) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src + (size_t)v * PL + KT * HD + row * 2));
-                        float4 y[NF];
+                    // four splits' loads in flight, the maximum running along: a pass for
+                    // it alone would be one more trip to memory
+#pragma unroll 1
+                    for (int v0 = 0; v0 < q.splits; v0 += 4) {
+                        float2 x[4];
+                        float4 y[4][NF];
 #pragma unroll
-                        for (int k = 0; k < NF; ++k) y[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)v * PL + row * HD + col + 64 * k));
-                        const float f = fm == -INFINITY ? 0.f : ex2(x.x - fm);
-                        fl = fmaf(x.y, f, fl);
+                        for (int v = 0; v < 4; ++v) {
+                            const bool in = v0 + v < q.splits;
+                            const float* from = src + (size_t)(v0 + v) * PL;
+                            x[v] = in ? __ldcg(reinterpret_cast<const float2*>(from + KT * HD + row * 2)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                        for (int k = 0; k < NF; ++k) {
-                            fo[k].x = fmaf(y[k].x, f, fo[k].x);
-                            fo[k].y = fmaf(y[k].y, f, fo[k].y);
-                            fo[k].z = fmaf(y[k].z, f, fo[k].z);
-                            fo[k].w = fmaf(y[k].w, f, fo[k].w);
+                            for (int k = 0; k < NF; ++k)
+                                y[v][k] = in ? __ldcg(reinterpret_cast<const float4*>(from + row * HD + col + 64 * k))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
+                        const float m = fmaxf(fm, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
+                        const float g = fm == -INFINITY ? 0.f : ex2(fm - m);
+                        fl *= g;
+#pragma unroll
+                        for (int k = 0; k < NF; ++k) fo[k] = make_float4(fo[k].x * g, fo[k].y * g, fo[k].z * g, fo[k].w * g);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const float f = x[v].x == -INFINITY ? 0.f : ex2(x[v].x - m);
+                            fl = fmaf(x[v].y, f, fl);
+#pragma unroll
+                            for (int k = 0; k < NF; ++k) {
+                                fo[k].x = fmaf(y[v][k].x, f, fo[k].x);
+                                fo[k].y = fmaf(y[v][k].y, f, fo[k].y);
+                                fo[k].z = fmaf(y[v][k].z, f, fo[k].z);
+                                fo[k].w = fmaf(y[v][k].w, f, fo[k].w);
+                            }
+                        }
+                        fm = m;
                     }
                 }
             }
