@@ -237,6 +237,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");   // the merge buffer is free again, too
         if (!flag[2]) break;
         const Work wk = ring[slot_i];
+        __threadfence_block();     // read before the slot goes back
         __syncwarp();
         if (lane == 0) mbar_arrive(i_empty + slot_i);
         if (wk.item < 0) break;

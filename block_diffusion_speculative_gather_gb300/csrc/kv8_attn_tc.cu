@@ -238,6 +238,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
     auto take = [&](unsigned k, Work* wk) -> bool {
         if (!__all_sync(0xffffffffu, wait_or(i_full + (k & 1), (k >> 1) & 1, abort, a.err, SITE_TC + 13))) return false;
         *wk = works[k & 1];
+        __threadfence_block();     // read before the slot goes back: an arrival can overtake queued loads
         __syncwarp();
         if (lane == 0) mbar_arrive(i_empty + (k & 1));
         return wk->item >= 0;
