@@ -635,8 +635,8 @@ cudaError_t allow_smem(const void* kern) {
 // rows fits, as sequences differ and a second tile reads the keys again; 128
 // else), two 128-row tiles over the same keys above.  While items are few, the
 // next smaller tiles are the faster ones though they read the keys again: more
-// SMs have work, and a small tile's own chain is shorter.  Microseconds, 8 kv
-// heads of 128, two tiles of each kind and the items of the smaller:
+// SMs have work, and a small tile's own chain is shorter.  Microseconds at 8 kv
+// heads of 128, by the smaller tile (and its items) and the larger:
 //   rows of a call          positions   smaller tile       larger
 //   1 x 32 packed                4000   16 (16 items) 16.1  64  20.7
 //   1 x 64                       4000   16 (32)       19.2  64  21.2

@@ -12,7 +12,7 @@ using namespace dfl;
 
 namespace {
 
-constexpr int KV8_MAX_SEQS = 4096;        // item counts of an attention call sit in shared memory
+constexpr int KV8_MAX_SEQS = 4096;        // a lane of an attention CTA's finding warp scans S / 32 of them
 constexpr int KV8_MAX_PAGES = 1 << 25;    // slots are int32
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
