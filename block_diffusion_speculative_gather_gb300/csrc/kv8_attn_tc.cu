@@ -388,11 +388,13 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     // the outputs and this step's weights so far follow
                     const bool need = mx > M + LAZY || (M == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xffffffffu, need)) {
-                        const float f0 = need ? (M == -INFINITY ? 0.f : ex2(M - mx)) : 1.f;
+                        const bool first = M == -INFINITY;
+                        const float f0 = need ? (first ? 0.f : ex2(M - mx)) : 1.f;
                         if (need) M = mx;
                         l *= f0;
-                        // the weights and outputs of a row without any so far are zeros
-                        if (__any_sync(0xffffffffu, f0 != 1.f && f0 != 0.f)) {
+                        // the weights and outputs of a row without any so far are zeros; others
+                        // follow, by 0 where the maximum has risen by 126 or more
+                        if (__any_sync(0xffffffffu, need && !first)) {
                             tc::st_wait();
 #pragma unroll 1
                             for (int b = c0; b < c; ++b) {

@@ -1,0 +1,149 @@
+"""Attention over the 8-bit paged cache where its numbers spread far: scores
+that rise by hundreds of powers of two, weights far below a row's largest, V
+scales at both ends of their range, pages and scales that are not there, many
+sequences; in each of the kernels' tile forms, against 64-bit definitions.
+
+Tolerances are those stated in tests/test_gpu_kv8.py, but for the weights' f16
+rounding: a weight is held relative to the row's largest (weight * V scale) with
+at least 9 powers of two of room, so a small one is off by half a step, 2^-25, of
+2^-9 of the largest: 2^-34 a key instead of 2^-25.  A sum of n weights is a
+chain of at most n / 32 + 16 fp32 additions, each off by 2^-24 of it.
+"""
+
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_kv8 import BF, F16, attend, attn_state, capi, half_step, ints, values   # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+# n_q, n_kv, dim, rows: tiles of 16, 64, 128 and two times 128 packed rows (152 SMs)
+FORMS = [
+    (8, 2, 128, [1, 3]),
+    (4, 2, 64, [7, 1]),
+    (32, 8, 128, [16]),
+    (40, 10, 64, [12, 3]),
+    (64, 16, 128, [30, 20, 5]),
+    (100, 20, 64, [16, 9]),
+    (32, 16, 128, [90, 150, 130, 100, 70]),
+    (40, 20, 64, [300, 280]),
+]
+LARGE = FORMS[2:]
+
+
+def define(st, causal=True, window=0, scale=None, gone=()):
+    """The definition in 64 bits, by whole matrices; the keys of pages in
+    `gone` are masked.  Keys as in kv8_plain.attend."""
+    q = st["q"].cpu().double()
+    kc, vc = (values(c) for c in st["cache"][:2])
+    k_scale, v_scale = (s.cpu().double() for s in st["cache"][2:])
+    rows, n_q, dim = q.shape
+    n_kv = kc.shape[1]
+    group = n_q // n_kv
+    scale = dim ** -0.5 if scale is None else scale
+    r = {"out": torch.zeros((rows, n_q, dim), dtype=torch.float64),
+         "mag": torch.zeros((rows, n_q, dim), dtype=torch.float64),
+         "lse": torch.full((rows, n_q), -math.inf, dtype=torch.float64),
+         "terms": torch.zeros((rows, n_q), dtype=torch.float64),
+         "qabs": torch.zeros((rows, n_q), dtype=torch.float64),
+         "unit": torch.zeros((rows, n_q, 1), dtype=torch.float64),
+         "chain": torch.zeros((rows, n_q), dtype=torch.float64)}
+    for s, kv in enumerate(st["held"]):
+        r0, n = st["start"][s], st["start"][s + 1] - st["start"][s]
+        if n == 0 or kv == 0:
+            continue
+        pages = torch.tensor(st["table"][s][:-(-kv // 64)])
+        there = torch.tensor([p not in gone for p in pages.tolist()]).repeat_interleave(64)[:kv]
+        pages = pages.clamp(0, kc.shape[0] - 1)
+        key, pos = torch.arange(kv)[None], kv - n + torch.arange(n)[:, None]
+        see = (key <= pos if causal else key < kv) & there
+        if window:
+            see = see & (key > pos - window if causal else key >= kv - n - window)
+        for h in range(n_kv):
+            ks = (kc[pages, h] * k_scale[pages, h][:, None, None]).reshape(-1, dim)[:kv]
+            vs = (vc[pages, h] * v_scale[pages, h][:, None, None]).reshape(-1, dim)[:kv]
+            ks, vs = (torch.where(there[:, None], x, 0.0) for x in (ks, vs))
+            sc = torch.where(there, v_scale[pages, h].repeat_interleave(64)[:kv], 0.0)
+            g = slice(h * group, (h + 1) * group)
+            qh = q[r0:r0 + n, g].transpose(0, 1)                       # [group][n][dim]
+            x = (qh @ ks.T * scale).masked_fill(~see, -math.inf)
+            w = torch.softmax(x, -1).nan_to_num(0.0)                   # rows without keys: zeros
+            put = lambda name, v: r[name][r0:r0 + n, g].copy_(v.transpose(0, 1))   # noqa: E731
+            put("out", w @ vs)
+            put("mag", w @ vs.abs())
+            put("lse", torch.logsumexp(x, -1))
+            put("terms", (qh.abs() @ ks.abs().T).masked_fill(~see, 0.0).amax(-1) * scale)
+            put("qabs", qh.abs().amax(-1) * torch.where(see.any(0), ks.abs().sum(1), 0.0).max() * scale)
+            put("unit", ((w * sc).amax(-1) * 448 * kv)[..., None])
+            r["chain"][r0:r0 + n, g] = kv / 32 + 16
+    return r
+
+
+def check(st, causal=True, window=0, scale=None, gone=()):
+    r = define(st, causal, window, scale, gone)
+    kind, dim, n = st["q"].dtype, st["q"].shape[2], st["start"][-1]
+    out, lse = st["out"].cpu().double(), st["lse"].cpu().double()
+    assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()          # rows behind the last sequence
+    d = (dim + 10) * 2.0 ** -24 * r["terms"] + 2.0 ** -25 * r["qabs"] + 2.0 ** -22
+    tol = r["mag"] * (2.0 ** -11 + 2 * d[..., None] + 2.0 ** -20) + r["unit"] * 2.0 ** -34
+    tol = tol * (1 + half_step(kind)) + half_step(kind) * r["out"].abs() + 2.0 ** -25
+    e = (out - r["out"]).abs()[:n]
+    assert (e <= tol[:n]).all(), (float((e / tol[:n]).nan_to_num(9e9).max()), float(e.nan_to_num(9e9).max()))
+    empty = torch.isinf(r["lse"][:n])
+    assert torch.equal(torch.isinf(lse[:n]), empty)
+    assert (lse[:n][empty] == -math.inf).all() and (out[:n][empty] == 0).all()
+    le = (lse - r["lse"]).abs()[:n][~empty]
+    lt = (d + 2.0 ** -22 * (1 + r["lse"].abs()) + 2.0 ** -24 * r["chain"])[:n][~empty]
+    assert (le <= lt).all(), float((le / lt).max())
+
+
+def codes(x):
+    return x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+
+
+def set_keys(st, level, bits, v=None, noise=0.05):
+    """Scores of `bits` powers of two times level[key] of every sequence (and
+    a little noise): dimension 0 of q is 16, of a key its level.  Values
+    v[key] in every dimension where given (codes; scales stay).  Returns the
+    softmax scale."""
+    g = torch.Generator().manual_seed(5)
+    q, (kc, vc, ks, vs) = st["q"], st["cache"]
+    q.copy_(noise * torch.randn(q.shape, generator=g))
+    q[..., 0] = 16.0
+    ks.fill_(1.0)
+    for s, kv in enumerate(st["held"]):
+        for p in range(-(-kv // 64)):
+            page, n = st["table"][s][p], min(64, kv - 64 * p)
+            k = 0.25 * torch.randn(kc.shape[1], n, kc.shape[3], generator=g)
+            k[..., 0] = level[64 * p:64 * p + n].float()
+            kc[page, :, :n] = codes(k)
+            if v is not None:
+                vc[page, :, :n] = codes(v[64 * p:64 * p + n, None].float().expand(n, vc.shape[3])[None].expand_as(k))
+    return bits * math.log(2) / 16
+
+
+# ------------------------------------------------------------------ scores that rise
+
+# 32-key blocks before which scores rise: inside a page, between a step's
+# pages, between steps; at an item's first step and behind it
+RISES = [[1], [2], [4], [5, 9], [1, 2, 3, 6, 8, 12], [7, 16]]
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("bits", [3, 9, 20, 100, 130, 300])
+def test_scores_that_rise(capi, n_q, n_kv, dim, rows, bits):       # noqa: F811
+    """What came before weighs 2^-bits of what comes: below 2^-126 as nothing."""
+    held = [max(n + 5, 700 + 37 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=bits)
+    for up in RISES:
+        level = torch.zeros(max(held))
+        for b in up:
+            level[32 * b:] += 1
+        scale = set_keys(st, level, bits)
+        st["out"].fill_(3.0), st["lse"].fill_(3.0)
+        attend(capi, st, scale=scale)
+        check(st, scale=scale)
+        attend(capi, st, causal=False, window=300, scale=scale)
+        check(st, causal=False, window=300, scale=scale)
