@@ -10,6 +10,13 @@
 // with t the scores times kp and M the running maximum of t + log2 vp: P is
 // the key's weight on the value codes, at most 1, so it fits f16 whatever
 // the scales; l carries the plain softmax sum relative to 2^M in fp32.
+// A page with a small scale (of zeros: 2^-100) counts in l however little it
+// adds to O, so one reference does only while the scales lie within 2^-32 and
+// 2^32: a weight is then lost from l below 2^-60 of the largest.  From the first
+// page on with another scale l is kept relative to 2^Z, Z the running maximum of
+// t, and takes (sum P) 2^(M - log2 vp - Z); where that factor passes 2^40, P are
+// zeros in f16 anyway, and l takes the sum of 2^(t - Z).  Parts (warps, groups,
+// splits) are joined as (M, Z, l), the row is O * 2^(M - Z) / l.
 //
 // q enters the MMAs as f16: a row is scaled by the power of two that brings
 // its largest element into [1, 2) (folded into the score factor), which keeps
@@ -54,7 +61,7 @@ template <int HD> struct KvSmem {
     static constexpr int ring = 0;
     static constexpr int red = ring + stages<HD>() * 2 * tile_bytes<HD>();
     static constexpr int ml = red + KW / 2 * KT * red_ld<HD>() * 4;    // half of the warps at a time
-    static constexpr int scales = ml + KW / 2 * KT * 2 * 4;  // [stages] (k, v)
+    static constexpr int scales = ml + KW / 2 * KT * 4 * 4;  // [stages] (k, v)
     static constexpr int bars = scales + stages<HD>() * 8;   // full, empty
     static constexpr int items = bars + stages<HD>() * 16;   // item ring: full, empty
     static constexpr int work = items + 2 * 16;
@@ -79,6 +86,193 @@ template <>
 __device__ __forceinline__ void store_row4<__half>(__half* p, float a, float b, float c, float d) {
     uint2 v{pack_f16x2(a, b), pack_f16x2(c, d)};
     *reinterpret_cast<uint2*>(p) = v;
+}
+
+// A warp's rows g and g + 8 of a tile: q, the keys they see, and what its pages
+// have left of them.
+template <int HD> struct Rows {
+    uint32_t qa[HD / 16][4];
+    float fr[2];                // score factors
+    int klo[2], khi[2];
+    float M[2], l[2], Z[2];     // l relative to 2^M, in far_pages to 2^Z
+    float o[HD / 8][4];
+};
+
+// Page p of item w; false: before its first use (FARS: the form for any scale, the
+// other one ends at a page that is not near()), or at the end (flag[1]).
+template <int HD, bool FARS>
+__device__ __forceinline__ bool take_page(const Kv8AttnArgs& a, const Item& w, uint8_t* sm, unsigned base,
+                                          unsigned n_items, int p, Rows<HD>& u) {
+    using S_ = KvSmem<HD>;
+    constexpr int TB = tile_bytes<HD>(), KSTAGES = stages<HD>();
+    const float2* scales = reinterpret_cast<const float2*>(sm + S_::scales);
+    uint64_t *full = reinterpret_cast<uint64_t*>(sm + S_::bars), *empty = full + KSTAGES;
+    volatile int* flag = reinterpret_cast<volatile int*>(sm + S_::flag);
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const unsigned it = base + (p - w.p0);
+    const int st = it % KSTAGES;
+    if (flag[1]) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(full + st, (it / KSTAGES) & 1))) {
+        report(a.err, DERR_TIMEOUT, SITE_FULL);
+        flag[1] = 1;
+        return false;
+    }
+    const float2 sc = scales[st];
+    const uint8_t* kt = sm + S_::ring + st * 2 * TB;
+    uint8_t* vt = sm + S_::ring + st * 2 * TB + TB;
+    const int key0 = p * KV8_PAGE;
+    if (sc.x >= 0.f && sc.y > 0.f) {
+        if (!FARS && !near(sc.y)) return false;
+        float s[8][4];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h) {
+                const uint4 kk = lds128(kt + tile_off<HD>(8 * t + key_of<HD>(g), 4 * h + c));
+                const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b[2] = {f16_of_codes(kw[j]), f16_of_codes(kw[j] >> 16)};
+                    mma_f16_16816(s[t], u.qa[4 * h + j], b);
+                }
+            }
+        const float ev = log2f(sc.y);
+        const bool whole = key0 >= w.in_lo && key0 + KV8_PAGE <= w.in_hi;
+        const float f0 = u.fr[0] * sc.x, f1 = u.fr[1] * sc.x;
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = fmaf(s[t][e], e < 2 ? f0 : f1, ev);
+                if (!whole) {
+                    const int key = key0 + 8 * t + key_of<HD>(2 * c + (e & 1));
+                    if (key < u.klo[e >> 1] || key >= u.khi[e >> 1]) x = -INFINITY;
+                }
+                s[t][e] = x;
+                mx[e >> 1] = fmaxf(mx[e >> 1], x);
+            }
+        float alpha[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            if (FARS) {
+                const float z = fmaxf(u.Z[r], mx[r] - ev);
+                if (z != u.Z[r] && u.Z[r] != -INFINITY) u.l[r] *= ex2(u.Z[r] - z);
+                u.Z[r] = z;
+            }
+            mx[r] = fmaxf(mx[r], u.M[r]);
+            alpha[r] = mx[r] == u.M[r] ? 1.f : ex2(u.M[r] - mx[r]);   // M = -inf: 0
+            u.M[r] = mx[r];
+        }
+        float m0 = u.M[0] == -INFINITY ? 0.f : u.M[0], m1 = u.M[1] == -INFINITY ? 0.f : u.M[1];
+        float k[2];                          // weights on values to the sum's
+        bool lost[2] = {false, false};
+        if (FARS) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                k[r] = u.M[r] == -INFINITY ? 0.f : ex2(u.M[r] - ev - u.Z[r]);
+                if (k[r] > FAR_PAGE) {
+                    lost[r] = true;
+                    k[r] = 1.f;
+                    (r ? m1 : m0) = u.Z[r] + ev;
+                }
+            }
+        }
+        float sum[2] = {0.f, 0.f};
+        uint32_t pa[4][4];      // P of the four 16-key steps, as A fragments
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const float p0 = ex2(s[t][0] - m0), p1 = ex2(s[t][1] - m0);
+            const float p2 = ex2(s[t][2] - m1), p3 = ex2(s[t][3] - m1);
+            sum[0] += p0 + p1;
+            sum[1] += p2 + p3;
+            pa[t >> 1][2 * (t & 1)] = pack_f16x2(p0, p1);
+            pa[t >> 1][2 * (t & 1) + 1] = pack_f16x2(p2, p3);
+        }
+        const float iv = 1.f / sc.y;
+        u.l[0] = FARS ? fmaf(sum[0], k[0], u.l[0]) : fmaf(sum[0], iv, u.l[0] * alpha[0]);
+        u.l[1] = FARS ? fmaf(sum[1], k[1], u.l[1]) : fmaf(sum[1], iv, u.l[1] * alpha[1]);
+        if (FARS) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pa[x][e] = lost[e & 1] ? 0u : pa[x][e];
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int d = 0; d < HD / 8; ++d) {
+                u.o[d][0] *= alpha[0];
+                u.o[d][1] *= alpha[0];
+                u.o[d][2] *= alpha[1];
+                u.o[d][3] *= alpha[1];
+            }
+        }
+        // a key's V must not reach a row that does not see it, and 0 * NaN is NaN:
+        // where not all rows see all keys, codes that no row sees and NaN ones
+        // are taken as zeros, and the rows that see a NaN get it after the merge
+        uint32_t seen = 0;
+        if (!whole) {
+#pragma unroll 1
+            for (int x = lane; x < KV8_PAGE * HD / 16; x += 32) {
+                const int key = x / (HD / 16);
+                uint4* at = reinterpret_cast<uint4*>(vt + tile_off<HD>(key, x % (HD / 16)));
+                const uint32_t keep = key0 + key >= w.lo && key0 + key < w.hi ? 0xffffffffu : 0u;
+                const uint4 y = *at;
+                *at = make_uint4(drop_nan(y.x & keep, &seen), drop_nan(y.y & keep, &seen),
+                                 drop_nan(y.z & keep, &seen), drop_nan(y.w & keep, &seen));
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // V: matrices (keys 0-7 | 8-15 of the step) x (16-byte chunks d, d + 1),
+            // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
+            // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
+            const int vrow = 16 * k + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
+#pragma unroll
+            for (int d = 0; d < HD / 16; d += 2) {
+                uint32_t r[4];
+                ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) r[x] = __byte_perm(r[x], 0, 0x3120);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t be[2] = {f16_of_codes(r[2 * x]), f16_of_codes(r[2 * x + 1])};
+                    const uint32_t bo[2] = {f16_of_codes(r[2 * x] >> 16), f16_of_codes(r[2 * x + 1] >> 16)};
+                    mma_f16_16816(u.o[2 * (d + x)], pa[k], be);
+                    mma_f16_16816(u.o[2 * (d + x) + 1], pa[k], bo);
+                }
+            }
+        }
+        if (!whole) {
+            if (seen) flag[3] = n_items + 1;
+            tc::fence_async_smem();     // the next copy into this page comes after the zeros
+        }
+    }
+    // the page goes back once its codes have arrived: an arrival can
+    // overtake loads that are still queued
+    __threadfence_block();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + st);
+    return true;
+}
+
+// The pages from p on once the V scales of the warp's pages lie far apart (top of
+// this file).  A call, so that usual pages keep their registers and their place
+// in the instruction cache (inline: one token of one sequence 10.9 us for 10.4).
+template <int HD>
+__device__ __noinline__ void far_pages(const Kv8AttnArgs& a, const Item& w, uint8_t* sm, unsigned base, unsigned n_items,
+                                       int p, Rows<HD>* rows) {
+    Rows<HD>& u = *rows;
+    u.Z[0] = u.M[0];
+    u.Z[1] = u.M[1];
+    while (p < w.p1 && take_page<HD, true>(a, w, sm, base, n_items, p, u)) p += KW;
 }
 
 template <typename T, int HD>
@@ -248,9 +442,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // q of rows g, g + 8 as A fragments: k step (h, j) of 16 covers the
         // dims 64 h + 16 c + 4 j .. + 3 of every lane c of a quad, so a
         // lane's fragments are its own 16 consecutive dims
-        uint32_t qa[HD / 16][4];
-        float fr[2];
-        int klo[2], khi[2];
+        Rows<HD> u;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int pr = w.tile * KT + g + 8 * r;
@@ -269,12 +461,12 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[16 * h + 8 * k + j] = to_f32(ev[j]);
                     }
-                row_keys(a, q, i, &klo[r], &khi[r]);
+                row_keys(a, q, i, &u.klo[r], &u.khi[r]);
             } else {
 #pragma unroll
                 for (int j = 0; j < HD / 4; ++j) v[j] = 0.f;
-                klo[r] = 0;
-                khi[r] = 0x7fffffff;   // computed on zeros, never written
+                u.klo[r] = 0;
+                u.khi[r] = 0x7fffffff;   // computed on zeros, never written
             }
 #pragma unroll
             for (int j = 0; j < HD / 4; ++j) {
@@ -285,150 +477,36 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             float inv, back;
             row_factor(top, &inv, &back);
-            fr[r] = back * a.scale_log2;
+            u.fr[r] = back * a.scale_log2;
 #pragma unroll
             for (int h = 0; h < HD / 64; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    qa[4 * h + j][r] = pack_f16x2(v[16 * h + 4 * j] * inv, v[16 * h + 4 * j + 1] * inv);
-                    qa[4 * h + j][2 + r] = pack_f16x2(v[16 * h + 4 * j + 2] * inv, v[16 * h + 4 * j + 3] * inv);
+                    u.qa[4 * h + j][r] = pack_f16x2(v[16 * h + 4 * j] * inv, v[16 * h + 4 * j + 1] * inv);
+                    u.qa[4 * h + j][2 + r] = pack_f16x2(v[16 * h + 4 * j + 2] * inv, v[16 * h + 4 * j + 3] * inv);
                 }
         }
 
-        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[HD / 8][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            u.M[r] = -INFINITY;
+            u.l[r] = 0.f;
+        }
 #pragma unroll
         for (int d = 0; d < HD / 8; ++d)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+            for (int e = 0; e < 4; ++e) u.o[d][e] = 0.f;
 
-        for (int p = w.p0 + warp; p < w.p1; p += KW) {
-            const unsigned it = base + (p - w.p0);
-            const int st = it % KSTAGES;
-            if (flag[1]) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(full + st, (it / KSTAGES) & 1))) {
-                report(a.err, DERR_TIMEOUT, SITE_FULL);
-                flag[1] = 1;
-                break;
-            }
-            const float2 sc = scales[st];
-            const uint8_t* kt = sm + S_::ring + st * 2 * TB;
-            uint8_t* vt = sm + S_::ring + st * 2 * TB + TB;
-            const int key0 = p * KV8_PAGE;
-            if (sc.x >= 0.f && sc.y > 0.f) {
-                float s[8][4];
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int h = 0; h < HD / 64; ++h) {
-                        const uint4 kk = lds128(kt + tile_off<HD>(8 * t + key_of<HD>(g), 4 * h + c));
-                        const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t b[2] = {f16_of_codes(kw[j]), f16_of_codes(kw[j] >> 16)};
-                            mma_f16_16816(s[t], qa[4 * h + j], b);
-                        }
-                    }
-                const float ev = log2f(sc.y);
-                const bool whole = key0 >= w.in_lo && key0 + KV8_PAGE <= w.in_hi;
-                const float f0 = fr[0] * sc.x, f1 = fr[1] * sc.x;
-                float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[t][e], e < 2 ? f0 : f1, ev);
-                        if (!whole) {
-                            const int key = key0 + 8 * t + key_of<HD>(2 * c + (e & 1));
-                            if (key < klo[e >> 1] || key >= khi[e >> 1]) x = -INFINITY;
-                        }
-                        s[t][e] = x;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], x);
-                    }
-                float alpha[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                    mx[r] = fmaxf(mx[r], M[r]);
-                    alpha[r] = mx[r] == M[r] ? 1.f : ex2(M[r] - mx[r]);   // M = -inf: 0
-                    M[r] = mx[r];
-                }
-                const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
-                float sum[2] = {0.f, 0.f};
-                uint32_t pa[4][4];      // P of the four 16-key steps, as A fragments
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const float p0 = ex2(s[t][0] - m0), p1 = ex2(s[t][1] - m0);
-                    const float p2 = ex2(s[t][2] - m1), p3 = ex2(s[t][3] - m1);
-                    sum[0] += p0 + p1;
-                    sum[1] += p2 + p3;
-                    pa[t >> 1][2 * (t & 1)] = pack_f16x2(p0, p1);
-                    pa[t >> 1][2 * (t & 1) + 1] = pack_f16x2(p2, p3);
-                }
-                const float iv = 1.f / sc.y;
-                l[0] = fmaf(sum[0], iv, l[0] * alpha[0]);
-                l[1] = fmaf(sum[1], iv, l[1] * alpha[1]);
-                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-                    for (int d = 0; d < HD / 8; ++d) {
-                        o[d][0] *= alpha[0];
-                        o[d][1] *= alpha[0];
-                        o[d][2] *= alpha[1];
-                        o[d][3] *= alpha[1];
-                    }
-                }
-                // a key's V must not reach a row that does not see it, and 0 * NaN is NaN:
-                // where not all rows see all keys, codes that no row sees and NaN ones
-                // are taken as zeros, and the rows that see a NaN get it after the merge
-                uint32_t seen = 0;
-                if (!whole) {
-#pragma unroll 1
-                    for (int x = lane; x < KV8_PAGE * HD / 16; x += 32) {
-                        const int key = x / (HD / 16);
-                        uint4* at = reinterpret_cast<uint4*>(vt + tile_off<HD>(key, x % (HD / 16)));
-                        const uint32_t keep = key0 + key >= w.lo && key0 + key < w.hi ? 0xffffffffu : 0u;
-                        const uint4 y = *at;
-                        *at = make_uint4(drop_nan(y.x & keep, &seen), drop_nan(y.y & keep, &seen),
-                                         drop_nan(y.z & keep, &seen), drop_nan(y.w & keep, &seen));
-                    }
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // V: matrices (keys 0-7 | 8-15 of the step) x (16-byte chunks d, d + 1),
-                    // transposed in units of two codes: a register holds dims 2g, 2g + 1 of
-                    // keys 2c, 2c + 1; one byte permute pairs the keys of each dim
-                    const int vrow = 16 * k + 8 * ((lane >> 3) & 1) + key_of<HD>(lane & 7);
-#pragma unroll
-                    for (int d = 0; d < HD / 16; d += 2) {
-                        uint32_t r[4];
-                        ldsm_x4_trans(r, vt + tile_off<HD>(vrow, d + (lane >> 4)));
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) r[x] = __byte_perm(r[x], 0, 0x3120);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t be[2] = {f16_of_codes(r[2 * x]), f16_of_codes(r[2 * x + 1])};
-                            const uint32_t bo[2] = {f16_of_codes(r[2 * x] >> 16), f16_of_codes(r[2 * x + 1] >> 16)};
-                            mma_f16_16816(o[2 * (d + x)], pa[k], be);
-                            mma_f16_16816(o[2 * (d + x) + 1], pa[k], bo);
-                        }
-                    }
-                }
-                if (!whole) {
-                    if (seen) flag[3] = n_items + 1;
-                    tc::fence_async_smem();     // the next copy into this page comes after the zeros
-                }
-            }
-            // the page goes back once its codes have arrived: an arrival can
-            // overtake loads that are still queued
-            __threadfence_block();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st);
+        int p = w.p0 + warp;
+        while (p < w.p1 && take_page<HD, false>(a, w, sm, base, n_items, p, u)) p += KW;
+        if (p < w.p1) {
+            const Item far_w = w;      // copies: what a call names lies in memory
+            Rows<HD> v = u;
+            far_pages<HD>(a, far_w, sm, base, n_items, p, &v);
+            u = v;
+        } else {
+            u.Z[0] = u.M[0];
+            u.Z[1] = u.M[1];
         }
         base += w.p1 - w.p0;
 
@@ -436,19 +514,19 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         // registers, then the lower half row by row, in warp order
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            u.l[r] += __shfl_xor_sync(0xffffffffu, u.l[r], 1);
+            u.l[r] += __shfl_xor_sync(0xffffffffu, u.l[r], 2);
         }
         constexpr int HW = KW / 2;
         auto put = [&](int slot) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                if (c == 0) *reinterpret_cast<float2*>(ml + (slot * KT + g + 8 * r) * 2) = make_float2(M[r], l[r]);
+                if (c == 0) *reinterpret_cast<float4*>(ml + (slot * KT + g + 8 * r) * 4) = make_float4(u.M[r], u.Z[r], u.l[r], 0.f);
                 float* dst = red + (slot * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
 #pragma unroll
                 for (int d = 0; d < HD / 16; ++d)
                     *reinterpret_cast<float4*>(dst + 16 * d) =
-                        make_float4(o[2 * d][2 * r], o[2 * d + 1][2 * r], o[2 * d][2 * r + 1], o[2 * d + 1][2 * r + 1]);
+                        make_float4(u.o[2 * d][2 * r], u.o[2 * d + 1][2 * r], u.o[2 * d][2 * r + 1], u.o[2 * d + 1][2 * r + 1]);
             }
         };
         if (w.p1 - w.p0 > HW) {
@@ -457,19 +535,20 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             if (warp < HW) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float2 b = *reinterpret_cast<const float2*>(ml + (warp * KT + g + 8 * r) * 2);
-                    const float m = fmaxf(M[r], b.x);
-                    const float fa = M[r] == -INFINITY ? 0.f : ex2(M[r] - m), fb = b.x == -INFINITY ? 0.f : ex2(b.x - m);
-                    l[r] = l[r] * fa + b.y * fb;
-                    M[r] = m;
+                    const float4 b = *reinterpret_cast<const float4*>(ml + (warp * KT + g + 8 * r) * 4);
+                    const float m = fmaxf(u.M[r], b.x), z = fmaxf(u.Z[r], b.y);
+                    const float fa = u.M[r] == -INFINITY ? 0.f : ex2(u.M[r] - m), fb = b.x == -INFINITY ? 0.f : ex2(b.x - m);
+                    u.l[r] = part_of(u.l[r], u.Z[r], z) + part_of(b.z, b.y, z);
+                    u.M[r] = m;
+                    u.Z[r] = z;
                     const float* src = red + (warp * KT + g + 8 * r) * red_ld<HD>() + 4 * c;
 #pragma unroll
                     for (int d = 0; d < HD / 16; ++d) {
                         const float4 x = *reinterpret_cast<const float4*>(src + 16 * d);
-                        o[2 * d][2 * r] = fmaf(x.x, fb, o[2 * d][2 * r] * fa);
-                        o[2 * d + 1][2 * r] = fmaf(x.y, fb, o[2 * d + 1][2 * r] * fa);
-                        o[2 * d][2 * r + 1] = fmaf(x.z, fb, o[2 * d][2 * r + 1] * fa);
-                        o[2 * d + 1][2 * r + 1] = fmaf(x.w, fb, o[2 * d + 1][2 * r + 1] * fa);
+                        u.o[2 * d][2 * r] = fmaf(x.x, fb, u.o[2 * d][2 * r] * fa);
+                        u.o[2 * d + 1][2 * r] = fmaf(x.y, fb, u.o[2 * d + 1][2 * r] * fa);
+                        u.o[2 * d][2 * r + 1] = fmaf(x.z, fb, u.o[2 * d][2 * r + 1] * fa);
+                        u.o[2 * d + 1][2 * r + 1] = fmaf(x.w, fb, u.o[2 * d + 1][2 * r + 1] * fa);
                     }
                 }
             }
@@ -482,16 +561,21 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
         const int pr = w.tile * KT + row;
         const int qi = pr / a.group, hq = w.kh * a.group + pr % a.group;
         const bool real = qi < q.n;
-        float fm = -INFINITY, fl = 0.f;
+        float fm = -INFINITY, fz = -INFINITY, fl = 0.f;
         float4 fo[NF];
 #pragma unroll
         for (int k = 0; k < NF; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < HW; ++v) fm = fmaxf(fm, ml[(v * KT + row) * 2]);
+        for (int v = 0; v < HW; ++v) {
+            const float4 x = *reinterpret_cast<const float4*>(ml + (v * KT + row) * 4);
+            fm = fmaxf(fm, x.x);
+            fz = fmaxf(fz, x.y);
+        }
 #pragma unroll
         for (int v = 0; v < HW; ++v) {
-            const float f = fm == -INFINITY ? 0.f : ex2(ml[(v * KT + row) * 2] - fm);
-            fl = fmaf(ml[(v * KT + row) * 2 + 1], f, fl);
+            const float4 mzl = *reinterpret_cast<const float4*>(ml + (v * KT + row) * 4);
+            const float f = fm == -INFINITY ? 0.f : ex2(mzl.x - fm);
+            fl += part_of(mzl.z, mzl.y, fz);
 #pragma unroll
             for (int k = 0; k < NF; ++k) {
                 const float4 x = *reinterpret_cast<const float4*>(red + (v * KT + row) * red_ld<HD>() + col + 64 * k);
@@ -526,7 +610,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
 #pragma unroll
                 for (int k = 0; k < NF; ++k)
                     *reinterpret_cast<float4*>(dst + row * HD + col + 64 * k) = fo[k];
-                if ((tid & 15) == 0) *reinterpret_cast<float2*>(dst + KT * HD + row * 2) = make_float2(fm, fl);
+                if ((tid & 15) == 0) *reinterpret_cast<float4*>(dst + KT * HD + row * 4) = make_float4(fm, fz, fl, 0.f);
             }
             __threadfence();
             asm volatile("bar.sync 1, %0;" ::"n"(KC) : "memory");
@@ -536,7 +620,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             if (write) {
                 __threadfence();
                 if (tid == 0) a.tickets[tk] = 0;
-                fm = -INFINITY;
+                fm = fz = -INFINITY;
                 fl = 0.f;
 #pragma unroll
                 for (int k = 0; k < NF; ++k) fo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -546,27 +630,28 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                     // it alone would be one more trip to memory
 #pragma unroll 1
                     for (int v0 = 0; v0 < q.splits; v0 += 4) {
-                        float2 x[4];
-                        float4 y[4][NF];
+                        float4 x[4], y[4][NF];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const bool in = v0 + v < q.splits;
                             const float* from = src + (size_t)(v0 + v) * PL;
-                            x[v] = in ? __ldcg(reinterpret_cast<const float2*>(from + KT * HD + row * 2)) : make_float2(-INFINITY, 0.f);
+                            x[v] = in ? __ldcg(reinterpret_cast<const float4*>(from + KT * HD + row * 4))
+                                      : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
 #pragma unroll
                             for (int k = 0; k < NF; ++k)
                                 y[v][k] = in ? __ldcg(reinterpret_cast<const float4*>(from + row * HD + col + 64 * k))
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
                         const float m = fmaxf(fm, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
+                        const float z = fmaxf(fz, fmaxf(fmaxf(x[0].y, x[1].y), fmaxf(x[2].y, x[3].y)));
                         const float g = fm == -INFINITY ? 0.f : ex2(fm - m);
-                        fl *= g;
+                        fl = part_of(fl, fz, z);
 #pragma unroll
                         for (int k = 0; k < NF; ++k) fo[k] = make_float4(fo[k].x * g, fo[k].y * g, fo[k].z * g, fo[k].w * g);
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const float f = x[v].x == -INFINITY ? 0.f : ex2(x[v].x - m);
-                            fl = fmaf(x[v].y, f, fl);
+                            fl += part_of(x[v].z, x[v].y, z);
 #pragma unroll
                             for (int k = 0; k < NF; ++k) {
                                 fo[k].x = fmaf(y[v][k].x, f, fo[k].x);
@@ -576,18 +661,19 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
                             }
                         }
                         fm = m;
+                        fz = z;
                     }
                 }
             }
         }
         if (write && real) {
-            const float inv = fl == 0.f ? 0.f : 1.f / fl;   // a row that sees no key: zeros
+            const float inv = out_factor(fm, fz, fl);
             T* dst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + qi) * a.out_row + (long long)hq * a.out_head;
 #pragma unroll
             for (int k = 0; k < NF; ++k)
                 store_row4<T>(dst + col + 64 * k, fo[k].x * inv, fo[k].y * inv, fo[k].z * inv, fo[k].w * inv);
             if (a.lse && (tid & 15) == 0)
-                a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
+                a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = row_lse(fz, fl);
         }
     }
 }

@@ -240,6 +240,22 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// What a part of a row's keys leaves (kv8_attn.cu): outputs relative to 2^M, -inf
+// without keys, and the sum l of the softmax relative to 2^Z.  Any Z near the
+// part's largest score does; a NaN sum stays one.
+__device__ __forceinline__ float sum_ref(float M, float Z) { return M == -INFINITY ? -INFINITY : Z; }
+__device__ __forceinline__ float part_of(float l, float Z, float z) { return l == 0.f ? 0.f : l * ex2(Z - z); }
+// The factor of outputs relative to 2^M: zeros for a row that sees no key.
+__device__ __forceinline__ float out_factor(float M, float Z, float l) { return l == 0.f ? 0.f : ex2(M - Z) / l; }
+__device__ __forceinline__ float row_lse(float Z, float l) {
+    return l == 0.f ? -INFINITY : (Z + log2f(l)) * 0.6931471805599453f;
+}
+
+// V scales that let outputs and sum share one reference.
+__device__ __forceinline__ bool near(float scale) { return scale >= 0x1p-32f && scale <= 0x1p32f; }
+// From this factor between weights on values and the sum's on, the former are zeros in f16.
+constexpr float FAR_PAGE = 0x1p40f;
+
 // Two e4m3 codes (the low 16 bits) to a pair of f16, exactly.
 __device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
     uint32_t h;

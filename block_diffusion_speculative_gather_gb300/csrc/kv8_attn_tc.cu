@@ -78,8 +78,11 @@ template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr size_t bytes = 1024 + nans + 64;
 };
 
-struct StepScale {      // of the two pages of a step: K scale (negative: no keys), log2 and reciprocal of V's
-    float ks[2], ev[2], iv[2], pad[2];
+// Of the two pages of a step: K scale (negative: no keys), log2 and reciprocal of
+// V's.  far: V scales of this step or an earlier one of the item are not near();
+// then ks are negative and iv are the K scales.
+struct StepScale {
+    float ks[2], ev[2], iv[2], far, pad_;
 };
 
 __device__ __forceinline__ void stsm_x4(void* p, const uint32_t (&r)[4]) {
@@ -326,8 +329,27 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             // a warp without rows only takes part: its lanes' weights stay whatever
             // tensor memory holds, and nothing of them is written
             const bool any = __any_sync(0xffffffffu, real);
+            // a step that not all rows see whole: masked scores become -inf in
+            // tensor memory first (code in the loop below would cost every step)
+            auto mask = [&](const float* ks, int k0) {
+#pragma unroll 1
+                for (int c = 2 * copy; c < 2 * copy + 4 / DUP; ++c) {
+                    uint32_t v[32];
+                    tc::ld_x32_async(s_tm + c * 32, v);
+                    tc::ld_wait(v);
+                    const int lo = klo - k0 - c * 32, hi = ks[c >> 1] < 0.f ? 0 : khi - k0 - c * 32;
+                    const uint32_t seen = lo < 32 && hi > 0 && lo < hi ? ~0u >> (hi < 32 ? 32 - hi : 0) & ~0u << (lo > 0 ? lo : 0) : 0u;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (!(seen & (1u << x))) v[x] = 0xff800000u;      // -inf
+                    tc::st_x16(s_tm + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+                    tc::st_x16(s_tm + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+                }
+                tc::st_wait();
+            };
             float M = -INFINITY, l = 0.f;
-            for (int i = 0; i < nt && ok; ++i, ++cs) {
+            int i = 0;
+            for (; i < nt && ok; ++i, ++cs) {
                 const int j = KEYS ? 2 * i + t : i;
                 ok = __all_sync(0xffffffffu, wait_or(s_full + t, cs & 1, abort, a.err, SITE_TC + 1));
                 if (!ok) break;
@@ -339,23 +361,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 const StepScale& sc = steps[(base + j) & 7];
                 const float fr = back_of[KEYS ? row : t * 128 + row] * a.scale_log2;
                 const int k0 = (w.p0 + 2 * j) * KV8_PAGE;
-                // a step that not all rows see whole: masked scores become -inf in
-                // tensor memory first (code in the loop below would cost every step)
                 if (k0 < w.in_lo || k0 + STEP > w.in_hi || sc.ks[0] < 0.f || sc.ks[1] < 0.f) {
-#pragma unroll 1
-                    for (int c = 2 * copy; c < 2 * copy + 4 / DUP; ++c) {
-                        uint32_t v[32];
-                        tc::ld_x32_async(s_tm + c * 32, v);
-                        tc::ld_wait(v);
-                        const int lo = klo - k0 - c * 32, hi = sc.ks[c >> 1] < 0.f ? 0 : khi - k0 - c * 32;
-                        const uint32_t seen = lo < 32 && hi > 0 && lo < hi ? ~0u >> (hi < 32 ? 32 - hi : 0) & ~0u << (lo > 0 ? lo : 0) : 0u;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (!(seen & (1u << x))) v[x] = 0xff800000u;      // -inf
-                        tc::st_x16(s_tm + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-                        tc::st_x16(s_tm + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
-                    }
-                    tc::st_wait();
+                    if (sc.far > 0.f) break;
+                    mask(sc.ks, k0);
                 }
                 // 32 keys at a time, the next 32 scores on their way meanwhile
                 uint32_t buf[2][32];
@@ -444,6 +452,87 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + t);
             }
+            // the steps from the first one on whose V scales lie far apart: two references,
+            // M and Z; the same for all of the group (the tensor core has done the first
+            // one's scores already: its wait is over at once)
+            float Z = M;
+#pragma unroll 1
+            for (; i < nt && ok; ++i, ++cs) {
+                const int j = KEYS ? 2 * i + t : i, c0 = 2 * copy;
+                ok = __all_sync(0xffffffffu, wait_or(s_full + t, cs & 1, abort, a.err, SITE_TC + 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const StepScale& sc = steps[(base + j) & 7];
+                const float fr = back_of[KEYS ? row : t * 128 + row] * a.scale_log2;
+                mask(sc.iv, (w.p0 + 2 * j) * KV8_PAGE);
+                if (DUP == 2) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) p[x] = 0;
+                    tc::st_x16(s_tm + (2 - c0) * 32, p);
+                    tc::st_x16(s_tm + (3 - c0) * 32, p);
+                }
+#pragma unroll 1
+                for (int c = c0; c < c0 + 4 / DUP && ok; ++c) {
+                    uint32_t v[32], p[16];
+                    tc::ld_x32_async(s_tm + c * 32, v);
+                    tc::ld_wait(v);
+                    const float ks = sc.iv[c >> 1], ev = sc.ev[c >> 1];
+                    const float f = ks >= 0.f ? fmaxf(fr * ks, 0x1p-126f) : 1.f;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(v[x]));
+                    const float mt = top == -INFINITY ? -INFINITY : top * f, mx = mt + ev;
+                    const bool first = M == -INFINITY;
+                    const float m = mx > M + LAZY || (first && mx > -INFINITY) ? mx : M;
+                    const float z = fmaxf(Z, mt);
+                    const float f0 = first ? 1.f : ex2(M - m);
+                    if (!first) l *= ex2(Z - z);
+                    M = m;
+                    Z = z;
+                    if (__any_sync(0xffffffffu, f0 != 1.f)) {
+                        tc::st_wait();
+#pragma unroll 1
+                        for (int b = c0; b < c; ++b) {
+                            tc::ld_x16(s_tm + b * 32, p);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                const float2 y = __half22float2(*reinterpret_cast<__half2*>(&p[x]));
+                                p[x] = pack_f16x2(y.x * f0, y.y * f0);
+                            }
+                            tc::st_x16(s_tm + b * 32, p);
+                        }
+                        if (i > 0) {
+                            ok = __all_sync(0xffffffffu, wait_or(o_done + t, (cs - 1) & 1, abort, a.err, SITE_TC + 2));
+                            tc::fence_after_sync();
+#pragma unroll 1
+                            for (int b = 0; b < HD / 16 && ok; ++b) {
+                                tc::ld_x16(o_tm + b * 16, p);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) p[x] = __float_as_uint(__uint_as_float(p[x]) * f0);
+                                tc::st_x16(o_tm + b * 16, p);
+                            }
+                        }
+                    }
+                    const float k = M == -INFINITY ? 0.f : ex2(M - ev - Z);      // weights on values to the sum's
+                    const bool lost = k > FAR_PAGE;
+                    const float off = lost ? -Z : ev - (M == -INFINITY ? 0.f : M);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const float y0 = ex2(fmaf(__uint_as_float(v[2 * x]), f, off)), y1 = ex2(fmaf(__uint_as_float(v[2 * x + 1]), f, off));
+                        sum += y0 + y1;
+                        p[x] = lost ? 0u : pack_f16x2(y0, y1);
+                    }
+                    tc::st_x16(s_tm + c * 32, p);
+                    l = fmaf(sum, lost ? 1.f : k, l);
+                }
+                if (!ok) break;
+                tc::st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + t);
+            }
             if (ok && nt > 0) {
                 ok = __all_sync(0xffffffffu, wait_or(o_done + t, (cs - 1) & 1, abort, a.err, SITE_TC + 2));
                 tc::fence_after_sync();
@@ -452,13 +541,14 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             if (!ok) break;
 
             // KEYS: the groups see the same lanes of tensor memory.  Each writes its
-            // (max, sum) over its scores, and takes half of the columns of both
-            // outputs.
+            // references and sum over its scores, and takes half of the columns of
+            // both outputs.
             float fa = 1.f, fb = 0.f;                      // factors of this group's and the other's sums
             const int nt_other = KEYS ? group_steps<KEYS>(a, q, w, 1 - t) : 0;
             const uint32_t other = t == 0 ? 128u : (uint32_t)-128;
             if (KEYS) {
                 tc::st_x2(s_tm, M, l);
+                tc::st_x2(s_tm + 2, Z, 0.f);
                 tc::st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -466,14 +556,15 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 ok = __all_sync(0xffffffffu, wait_or(handed, items & 1, abort, a.err, SITE_TC + 4));
                 if (!ok) break;
                 tc::fence_after_sync();
-                float bm, bl;
+                float bm, bl, bz, none;
                 tc::ld_x2(s_tm + other, &bm, &bl);
+                tc::ld_x2(s_tm + other + 2, &bz, &none);
                 const float m = fmaxf(M, bm);
                 fa = M == -INFINITY ? 0.f : ex2(M - m);
                 fb = bm == -INFINITY ? 0.f : ex2(bm - m);
-                // a NaN sum stays one; in the groups' order, for the same bits in both
-                const float la = l != 0.f ? l * fa : 0.f, lb = bl != 0.f ? bl * fb : 0.f;
-                l = t == 0 ? la + lb : lb + la;
+                const float z = fmaxf(sum_ref(M, Z), sum_ref(bm, bz));
+                l = part_of(l, Z, z) + part_of(bl, bz, z);
+                Z = z;
                 M = m;
             }
             constexpr int NB = HD / 16 / (KEYS ? 2 : 1);           // 16-column blocks of a group
@@ -512,7 +603,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             // the other's half to its own; both write
             constexpr int HALF = NB / DUP;
             float4* xb = reinterpret_cast<float4*>(sm + L::q) + (size_t)t * NB * 4 * 64 + row;    // [copy][HALF][4][64]
-            float2* xml = reinterpret_cast<float2*>(sm + L::ml) + row;                            // [copy][64]
+            float2* xml = reinterpret_cast<float2*>(sm + L::ml) + row;                            // [copy][64]: (M, log2 of the sum)
             float ga = 1.f, gb = 0.f;      // factors of copy 0's and copy 1's sums
             if (DUP == 2) {
 #pragma unroll 1
@@ -523,7 +614,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     for (int y = 0; y < 4; ++y)
                         xb[((copy * HALF + x) * 4 + y) * 64] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
                 }
-                if (t == 0) xml[copy * 64] = make_float2(M, l);      // the same in both groups
+                if (t == 0) xml[copy * 64] = make_float2(M, l == 0.f ? -INFINITY : Z + log2f(l));      // the same in both groups
                 __syncwarp();
                 if (lane == 0) mbar_arrive(copy_full);
                 ok = __all_sync(0xffffffffu, wait_or(copy_full, items & 1, abort, a.err, SITE_TC + 15));
@@ -532,9 +623,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 M = fmaxf(m0.x, m1.x);
                 ga = m0.x == -INFINITY ? 0.f : ex2(m0.x - M);
                 gb = m1.x == -INFINITY ? 0.f : ex2(m1.x - M);
-                l = (m0.y != 0.f ? m0.y * ga : 0.f) + (m1.y != 0.f ? m1.y * gb : 0.f);
+                Z = fmaxf(m0.y, m1.y);
+                l = (m0.y == -INFINITY ? 0.f : ex2(m0.y - Z)) + (m1.y == -INFINITY ? 0.f : ex2(m1.y - Z));
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;   // a row that sees no key: zeros
+            const float inv = out_factor(M, Z, l);
 #pragma unroll 1
             for (int x = 0; x < HALF; ++x) {
                 const int b = b_first + copy * HALF + x;
@@ -563,10 +655,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             if (DUP == 2 && lane == 0) mbar_arrive(copy_free);
             if (!split) {
                 if (real && copy == 0 && a.lse && b_first == 0)
-                    a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+                    a.lse[(long long)(q.r0 + qi) * a.n_q + hq] = row_lse(Z, l);
                 continue;
             }
-            if (real && fits && copy == 0 && b_first == 0) reinterpret_cast<float2*>(part + (size_t)RT * HD)[prow] = make_float2(M, l);
+            if (real && fits && copy == 0 && b_first == 0) reinterpret_cast<float4*>(part + (size_t)RT * HD)[prow] = make_float4(M, sum_ref(M, Z), l, 0.f);
             // the CTA whose split of the tile is the last to arrive folds them all, in
             // split order: a thread takes a row and a share of its columns
             __threadfence();
@@ -591,17 +683,21 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
             const int fr_ = w.tile * RT + frow, fi = fr_ / a.group, fh = w.kh * a.group + fr_ % a.group;
             if (fi < q.n) {
                 const float* src = a.part + slot0 * PL;
-                const float2* mls = reinterpret_cast<const float2*>(src + (size_t)RT * HD) + frow;
-                const long long PL2 = PL / 2;
-                float fm = -INFINITY, fl = 0.f;
-#pragma unroll 4
-                for (int v = 0; v < q.splits; ++v) fm = fmaxf(fm, __ldcg(mls + v * PL2).x);
+                const float4* mls = reinterpret_cast<const float4*>(src + (size_t)RT * HD) + frow;    // (M, Z, l)
+                const long long PL4 = PL / 4;
+                float fm = -INFINITY, fz = -INFINITY, fl = 0.f;
 #pragma unroll 4
                 for (int v = 0; v < q.splits; ++v) {
-                    const float2 x = __ldcg(mls + v * PL2);
-                    fl = fmaf(x.y, x.x == -INFINITY ? 0.f : ex2(x.x - fm), fl);
+                    const float4 x = __ldcg(mls + v * PL4);
+                    fm = fmaxf(fm, x.x);
+                    fz = fmaxf(fz, x.y);
                 }
-                const float finv = fl == 0.f ? 0.f : 1.f / fl;
+#pragma unroll 4
+                for (int v = 0; v < q.splits; ++v) {
+                    const float4 x = __ldcg(mls + v * PL4);
+                    fl += part_of(x.z, x.y, fz);
+                }
+                const float finv = out_factor(fm, fz, fl);
                 T* fdst = reinterpret_cast<T*>(a.out) + (long long)(q.r0 + fi) * a.out_row + (long long)fh * a.out_head;
 #pragma unroll 1
                 for (int b = share * (HD / 16) / shares; b < (share + 1) * (HD / 16) / shares; ++b) {
@@ -612,9 +708,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
 #pragma unroll 2
                     for (int v = 0; v < q.splits; ++v) {
                         float4 y[4];
-                        const float m = __ldcg(mls + v * PL2).x;
+                        const float m = __ldcg(mls + v * PL4).x;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) y[x] = __ldcg(col + v * (PL / 4) + x * RT);
+                        for (int x = 0; x < 4; ++x) y[x] = __ldcg(col + v * PL4 + x * RT);
                         const float f = m == -INFINITY ? 0.f : ex2(m - fm);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
@@ -627,7 +723,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     store16<T>(fdst + 16 * b, o, finv);
                 }
                 if (a.lse && share == 0)
-                    a.lse[(long long)(q.r0 + fi) * a.n_q + fh] = fl == 0.f ? -INFINITY : (fm + log2f(fl)) * 0.6931471805599453f;
+                    a.lse[(long long)(q.r0 + fi) * a.n_q + fh] = row_lse(fz, fl);
             }
             __syncwarp();
         }
@@ -640,6 +736,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
         for (unsigned items = 0; ok && take(items, &wk); ++items) {
             const Item& w = wk.w;
             const int n = (w.p1 - w.p0 + 1) / 2;
+            bool far = false;
             for (int j = 0; j < n; ++j, ++g) {
                 const int st = g & 1;
                 const unsigned r0 = (2 * g) % R, par = (2 * g / R) & 1;      // R is even: both pages share a parity
@@ -648,12 +745,18 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                      wait_or(rawk_full + r0 + 1, par, abort, a.err, SITE_TC + 6);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (cw == 0 && lane < 2) {
-                    const float2 sc = rsc[r0 + lane];
-                    StepScale* d = steps + (g & 7);
-                    d->ks[lane] = sc.y > 0.f ? sc.x : -1.f;
-                    d->ev[lane] = sc.y > 0.f ? log2f(sc.y) : 0.f;
-                    d->iv[lane] = sc.y > 0.f ? 1.f / sc.y : 0.f;
+                if (cw == 0) {
+                    const float2 sc = rsc[r0 + (lane & 1)];
+                    const bool there = sc.x >= 0.f && sc.y > 0.f;
+                    far = far || __any_sync(0xffffffffu, there && !near(sc.y));
+                    if (lane < 2) {
+                        StepScale* d = steps + (g & 7);
+                        const float ks = there ? sc.x : -1.f;
+                        d->ks[lane] = far ? -1.f : ks;
+                        d->ev[lane] = there ? log2f(sc.y) : 0.f;
+                        d->iv[lane] = far ? ks : (there ? 1.f / sc.y : 0.f);
+                        d->far = far ? 1.f : 0.f;
+                    }
                 }
                 uint8_t* dst = sm + L::k + st * L::KB;
 #pragma unroll 1

@@ -7,7 +7,9 @@ Tolerances are those stated in tests/test_gpu_kv8.py, but for the weights' f16
 rounding: a weight is held relative to the row's largest (weight * V scale) with
 at least 9 powers of two of room, so a small one is off by half a step, 2^-25, of
 2^-9 of the largest: 2^-34 a key instead of 2^-25.  A sum of n weights is a
-chain of at most n / 32 + 16 fp32 additions, each off by 2^-24 of it.
+chain of at most n / 32 + 16 fp32 additions, each off by 2^-24 of it.  A score
+is added to its page's log2 of the V scale and taken from a reference, two
+roundings of 2^-24 of that sum: 2^-23 |log2 scale| beside the score's own.
 """
 
 import math
@@ -29,8 +31,8 @@ FORMS = [
     (100, 20, 64, [16, 9]),
     (32, 16, 128, [90, 150, 130, 100, 70]),
     (40, 20, 64, [300, 280]),
+    (16, 8, 64, [1] * 10),                 # 16, a sequence's pages in one item
 ]
-LARGE = FORMS[2:]
 
 
 def define(st, causal=True, window=0, scale=None, gone=()):
@@ -49,7 +51,8 @@ def define(st, causal=True, window=0, scale=None, gone=()):
          "terms": torch.zeros((rows, n_q), dtype=torch.float64),
          "qabs": torch.zeros((rows, n_q), dtype=torch.float64),
          "unit": torch.zeros((rows, n_q, 1), dtype=torch.float64),
-         "chain": torch.zeros((rows, n_q), dtype=torch.float64)}
+         "chain": torch.zeros((rows, n_q), dtype=torch.float64),
+         "far": torch.zeros((rows, n_q), dtype=torch.float64)}
     for s, kv in enumerate(st["held"]):
         r0, n = st["start"][s], st["start"][s + 1] - st["start"][s]
         if n == 0 or kv == 0:
@@ -78,6 +81,7 @@ def define(st, causal=True, window=0, scale=None, gone=()):
             put("qabs", qh.abs().amax(-1) * torch.where(see.any(0), ks.abs().sum(1), 0.0).max() * scale)
             put("unit", ((w * sc).amax(-1) * 448 * kv)[..., None])
             r["chain"][r0:r0 + n, g] = kv / 32 + 16
+            r["far"][r0:r0 + n, g] = torch.where(sc > 0, sc, 1.0).log2().abs().max()
     return r
 
 
@@ -86,7 +90,7 @@ def check(st, causal=True, window=0, scale=None, gone=()):
     kind, dim, n = st["q"].dtype, st["q"].shape[2], st["start"][-1]
     out, lse = st["out"].cpu().double(), st["lse"].cpu().double()
     assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()          # rows behind the last sequence
-    d = (dim + 10) * 2.0 ** -24 * r["terms"] + 2.0 ** -25 * r["qabs"] + 2.0 ** -22
+    d = (dim + 10) * 2.0 ** -24 * r["terms"] + 2.0 ** -25 * r["qabs"] + 2.0 ** -22 + 2.0 ** -23 * r["far"]
     tol = r["mag"] * (2.0 ** -11 + 2 * d[..., None] + 2.0 ** -20) + r["unit"] * 2.0 ** -34
     tol = tol * (1 + half_step(kind)) + half_step(kind) * r["out"].abs() + 2.0 ** -25
     e = (out - r["out"]).abs()[:n]
@@ -147,3 +151,68 @@ def test_scores_that_rise(capi, n_q, n_kv, dim, rows, bits):       # noqa: F811
         check(st, scale=scale)
         attend(capi, st, causal=False, window=300, scale=scale)
         check(st, causal=False, window=300, scale=scale)
+
+
+# ------------------------------------------------------------------ V scales far apart
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("e", [0, 10, 27, 60, 119])
+def test_pages_of_zeros_beside_large_ones(capi, n_q, n_kv, dim, rows, e):      # noqa: F811
+    """Keys of pages whose values are zeros (V scale 2^-100) count in the sum
+    like any others, whatever the other pages' scales; scores rise and fall."""
+    held = [max(n + 5, 500 + 64 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=e)
+    v_codes = st["cache"][1].clone()
+    for zeros in ([0], [1], [2, 4, 5], [-1]):
+        for bits, ups in ((1, []), (40, [7]), (-20, [5, 8]), (-100, [4])):
+            st["cache"][1].copy_(v_codes)
+            st["out"].fill_(3.0), st["lse"].fill_(3.0)
+            level = torch.zeros(max(held))
+            for b in ups:
+                level[32 * b:] += 1
+            scale = set_keys(st, level, bits) * (1 if bits > 0 else -1)
+            if bits < 0:
+                st["q"][..., 0] = -16.0
+            st["cache"][3].fill_(2.0 ** e)
+            for s, t in enumerate(st["table"]):
+                n = -(-held[s] // 64)
+                for p in zeros:
+                    st["cache"][1][t[p % n]] = 0
+                    st["cache"][3][t[p % n]] = 2.0 ** -100
+            attend(capi, st, scale=scale)
+            check(st, scale=scale)
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("scales", [(-100, 119), (119, -100), (-100, 0, 100), (60, -60), (-100,), (119,), (-50, -90, -10)])
+@pytest.mark.parametrize("bits", [0, 13, 70, 200])
+def test_v_scales_over_their_whole_range(capi, n_q, n_kv, dim, rows, scales, bits):      # noqa: F811
+    """Pages of all scales in turn, each larger one with the smaller weights."""
+    held = [max(n + 5, 600 + 64 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=bits)
+    pages = -(-max(held) // 64)
+    e = torch.tensor([scales[p % len(scales)] for p in range(pages)])
+    order = torch.unique(e)
+    level = -(e[:, None] == order).float().argmax(1).repeat_interleave(64).float()
+    scale = set_keys(st, level, max(bits, 1))
+    for s, t in enumerate(st["table"]):
+        for p in range(-(-held[s] // 64)):
+            st["cache"][3][t[p]] = 2.0 ** int(e[p])
+    attend(capi, st, scale=scale)
+    check(st, scale=scale)
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+def test_a_long_cache_of_zeros(capi, n_q, n_kv, dim, rows):      # noqa: F811
+    """Values of zeros everywhere and scores that rise by less than a
+    reference moves for: the sum stays within fp32."""
+    rows = [min(rows[0], 40)]
+    st = attn_state(n_q, n_kv, dim, rows, [40000], BF, seed=1)
+    level = torch.ones(40000)
+    level[:32] = 0
+    st["cache"][1].zero_()
+    st["cache"][3].fill_(2.0 ** -100)
+    for bits in (3, 5.5, 13.9):
+        scale = set_keys(st, level, bits, noise=0.01)
+        attend(capi, st, scale=scale)
+        check(st, scale=scale)
