@@ -7,8 +7,8 @@
 // q head of the group) pairs, packed row-major.  Scores are kept in base 2.
 // With page scales kp, vp (vp = 2^e for the cache's own scales) a page adds
 //   P = 2^(t + log2 vp - M),  O += P * vcode,  l += (sum P) / vp
-// with t the scores times kp and M the running maximum of t + log2 vp: P is
-// the key's weight on the value codes, at most 1, so it fits f16 whatever
+// with t the scores times kp and M the running maximum of t + log2 vp less 15: P
+// is the key's weight on the value codes, at most 2^15, so it fits f16 whatever
 // the scales; l carries the plain softmax sum relative to 2^M in fp32.
 // A page with a small scale (of zeros: 2^-100) counts in l however little it
 // adds to O, so one reference does only while the scales lie within 2^-32 and
@@ -21,8 +21,11 @@
 // q enters the MMAs as f16: a row is scaled by the power of two that brings
 // its largest element into [1, 2) (folded into the score factor), which keeps
 // bf16 and f16 rows exact but for elements 2^-14 below the row's largest,
-// that lose low bits.  e4m3 codes are exact in f16.  P is rounded to f16
-// (half a step: 2^-11 of the weight); scores, sums and outputs are fp32.
+// that lose low bits.  e4m3 codes are exact in f16.  P is rounded to f16: half
+// a step, 2^-12 to 2^-11 of the weight, while that is above 2^-29 of the largest
+// weight times scale of the row (tcgen05 form: 2^-21), below 2^-25 of a step of
+// that, to nothing at 2^-40 (2^-32).  l has the weights before they are rounded.
+// Scores, sums and outputs are fp32.
 //
 // This form: 16 packed rows a tile, mma.sync (a tcgen05 tile would be an
 // eighth full at best, and a page's work is its bytes).  A warp takes whole
@@ -48,6 +51,7 @@ namespace {
 using adev::ldsm_x4_trans;
 using namespace kv8;
 
+constexpr float ROOM = 15.f;        // log2 of the largest P: f16 ends at 2^16, and what lies far below should count
 constexpr int KT = 16;              // packed rows of a tile (the M side of the MMAs)
 constexpr int KW = 8;               // consumer warps; each takes whole pages, every eighth
 constexpr int KC = 32 * KW;         // consumer threads
@@ -166,7 +170,7 @@ __device__ __forceinline__ bool take_page(const Kv8AttnArgs& a, const Item& w, u
                 if (z != u.Z[r] && u.Z[r] != -INFINITY) u.l[r] *= ex2(u.Z[r] - z);
                 u.Z[r] = z;
             }
-            mx[r] = fmaxf(mx[r], u.M[r]);
+            mx[r] = fmaxf(mx[r] - ROOM, u.M[r]);
             alpha[r] = mx[r] == u.M[r] ? 1.f : ex2(u.M[r] - mx[r]);   // M = -inf: 0
             u.M[r] = mx[r];
         }

@@ -32,9 +32,15 @@
 // about 10 us beside its steps: found, its first pages brought, its sums
 // joined and written.
 //
-// The running maximum that weights refer to moves only when a row's maximum
-// rises by more than 2^14 (weights stay within f16's range), so outputs are
-// rescaled in tensor memory rarely.
+// The reference of a row's weights is set 2^ROOM below its maximum and moves only
+// when that rises by more than 2^LAZY (weights stay within f16's range), so
+// outputs are rescaled in tensor memory rarely.  When one row of a warp moves,
+// all whose maximum has risen do: the warp's outputs are rewritten anyway.  Room
+// below the largest weight costs rescales; 4 prompt chunks, verify of 8
+// sequences, 32 draft blocks, in us, by ROOM and LAZY:
+//   3, 12: 484, 75.0, 27.3;  5, 10: 491, 75.1, 27.6;  7, 8: 500, 75.3, 28.0;
+//   9, 6: 519, 76.2, 29.5 (rows moving one by one 581, 83.9, 34.2)
+// (7: keys of 2^-21 of the largest weight keep their 11 bits, 2^-32 is lost.)
 //
 // Tensor memory: scores at columns 0 and 128, outputs at 256 and 384.  A
 // step's P overwrites its scores (32 keys' weights in the first 16 of their
@@ -57,7 +63,7 @@ using adev::ldsm_x4_trans;
 constexpr int KC_WARP = 8, KC = 4, VC_WARP = 12, VC = 4, MMA_WARP = 16, TMA_K = 17, TC_THREADS = 32 * 19;
 constexpr int STEP = 2 * KV8_PAGE;         // keys of a step
 constexpr int SITE_TC = 310;               // + role
-constexpr float LAZY = 14.f;               // rise of a row's maximum (base 2) that moves the reference
+constexpr float ROOM = 7.f, LAZY = 8.f;    // base 2; sum at most 15
 
 template <int HD, bool KEYS, int DUP> struct TcSmem {
     static constexpr int QB = 128 * HD * 2;                    // one q tile, f16
@@ -394,11 +400,12 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     const float mx = top == -INFINITY ? -INFINITY : fmaf(top, f, ev);
                     // move the reference where this row's maximum has risen far: the sums,
                     // the outputs and this step's weights so far follow
-                    const bool need = mx > M + LAZY || (M == -INFINITY && mx > -INFINITY);
+                    bool need = mx > M + (ROOM + LAZY) || (M == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xffffffffu, need)) {
                         const bool first = M == -INFINITY;
-                        const float f0 = need ? (first ? 0.f : ex2(M - mx)) : 1.f;
-                        if (need) M = mx;
+                        need = need || (!first && mx > M + ROOM);
+                        const float f0 = need ? (first ? 0.f : ex2(M + ROOM - mx)) : 1.f;
+                        if (need) M = mx - ROOM;
                         l *= f0;
                         // the weights and outputs of a row without any so far are zeros; others
                         // follow, by 0 where the maximum has risen by 126 or more
@@ -484,7 +491,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(v[x]));
                     const float mt = top == -INFINITY ? -INFINITY : top * f, mx = mt + ev;
                     const bool first = M == -INFINITY;
-                    const float m = mx > M + LAZY || (first && mx > -INFINITY) ? mx : M;
+                    const float m = mx > M + (ROOM + LAZY) || (first && mx > -INFINITY) ? mx - ROOM : M;
                     const float z = fmaxf(Z, mt);
                     const float f0 = first ? 1.f : ex2(M - m);
                     if (!first) l *= ex2(Z - z);

@@ -4,9 +4,9 @@ scales at both ends of their range, pages and scales that are not there, many
 sequences; in each of the kernels' tile forms, against 64-bit definitions.
 
 Tolerances are those stated in tests/test_gpu_kv8.py, but for the weights' f16
-rounding: a weight is held relative to the row's largest (weight * V scale) with
-at least 9 powers of two of room, so a small one is off by half a step, 2^-25, of
-2^-9 of the largest: 2^-34 a key instead of 2^-25.  A sum of n weights is a
+rounding: a weight is held relative to 2^-7 or less of the row's largest (weight *
+V scale), so a small one is off by half a step, 2^-25, of that: 2^-32 a key
+instead of 2^-25.  A sum of n weights is a
 chain of at most n / 32 + 16 fp32 additions, each off by 2^-24 of it.  A score
 is added to its page's log2 of the V scale and taken from a reference, two
 roundings of 2^-24 of that sum: 2^-23 |log2 scale| beside the score's own.
@@ -17,7 +17,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_kv8 import BF, F16, attend, attn_state, capi, half_step, ints, values   # noqa: F401 (a fixture)
+from tests.test_gpu_kv8 import BF, F16, attend, attn_state, capi, half_step, ints   # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -29,7 +29,7 @@ FORMS = [
     (40, 10, 64, [12, 3]),
     (64, 16, 128, [30, 20, 5]),
     (100, 20, 64, [16, 9]),
-    (32, 16, 128, [90, 150, 130, 100, 70]),
+    (32, 16, 128, [80, 100, 90, 70, 80]),
     (40, 20, 64, [300, 280]),
     (16, 8, 64, [1] * 10),                 # 16, a sequence's pages in one item
 ]
@@ -38,29 +38,26 @@ FORMS = [
 def define(st, causal=True, window=0, scale=None, gone=()):
     """The definition in 64 bits, by whole matrices; the keys of pages in
     `gone` are masked.  Keys as in kv8_plain.attend."""
-    q = st["q"].cpu().double()
-    kc, vc = (values(c) for c in st["cache"][:2])
-    k_scale, v_scale = (s.cpu().double() for s in st["cache"][2:])
+    q, dev = st["q"].double(), "cuda"
+    kc, vc = (c.view(torch.float8_e4m3fn).double() for c in st["cache"][:2])
+    k_scale, v_scale = (s.double() for s in st["cache"][2:])
     rows, n_q, dim = q.shape
     n_kv = kc.shape[1]
     group = n_q // n_kv
     scale = dim ** -0.5 if scale is None else scale
-    r = {"out": torch.zeros((rows, n_q, dim), dtype=torch.float64),
-         "mag": torch.zeros((rows, n_q, dim), dtype=torch.float64),
-         "lse": torch.full((rows, n_q), -math.inf, dtype=torch.float64),
-         "terms": torch.zeros((rows, n_q), dtype=torch.float64),
-         "qabs": torch.zeros((rows, n_q), dtype=torch.float64),
-         "unit": torch.zeros((rows, n_q, 1), dtype=torch.float64),
-         "chain": torch.zeros((rows, n_q), dtype=torch.float64),
-         "far": torch.zeros((rows, n_q), dtype=torch.float64)}
+    kw = dict(dtype=torch.float64, device=dev)
+    r = {"out": torch.zeros((rows, n_q, dim), **kw), "mag": torch.zeros((rows, n_q, dim), **kw),
+         "lse": torch.full((rows, n_q), -math.inf, **kw), "unit": torch.zeros((rows, n_q, 1), **kw),
+         "terms": torch.zeros((rows, n_q), **kw), "qabs": torch.zeros((rows, n_q), **kw),
+         "chain": torch.zeros((rows, n_q), **kw), "far": torch.zeros((rows, n_q), **kw)}
     for s, kv in enumerate(st["held"]):
         r0, n = st["start"][s], st["start"][s + 1] - st["start"][s]
         if n == 0 or kv == 0:
             continue
-        pages = torch.tensor(st["table"][s][:-(-kv // 64)])
-        there = torch.tensor([p not in gone for p in pages.tolist()]).repeat_interleave(64)[:kv]
+        pages = torch.tensor(st["table"][s][:-(-kv // 64)], device=dev)
+        there = torch.tensor([p not in gone for p in pages.tolist()], device=dev).repeat_interleave(64)[:kv]
         pages = pages.clamp(0, kc.shape[0] - 1)
-        key, pos = torch.arange(kv)[None], kv - n + torch.arange(n)[:, None]
+        key, pos = torch.arange(kv, device=dev)[None], kv - n + torch.arange(n, device=dev)[:, None]
         see = (key <= pos if causal else key < kv) & there
         if window:
             see = see & (key > pos - window if causal else key >= kv - n - window)
@@ -88,10 +85,10 @@ def define(st, causal=True, window=0, scale=None, gone=()):
 def check(st, causal=True, window=0, scale=None, gone=()):
     r = define(st, causal, window, scale, gone)
     kind, dim, n = st["q"].dtype, st["q"].shape[2], st["start"][-1]
-    out, lse = st["out"].cpu().double(), st["lse"].cpu().double()
+    out, lse = st["out"].double(), st["lse"].double()
     assert (out[n:] == 3.0).all() and (lse[n:] == 3.0).all()          # rows behind the last sequence
     d = (dim + 10) * 2.0 ** -24 * r["terms"] + 2.0 ** -25 * r["qabs"] + 2.0 ** -22 + 2.0 ** -23 * r["far"]
-    tol = r["mag"] * (2.0 ** -11 + 2 * d[..., None] + 2.0 ** -20) + r["unit"] * 2.0 ** -34
+    tol = r["mag"] * (2.0 ** -11 + 2 * d[..., None] + 2.0 ** -20) + r["unit"] * 2.0 ** -32
     tol = tol * (1 + half_step(kind)) + half_step(kind) * r["out"].abs() + 2.0 ** -25
     e = (out - r["out"]).abs()[:n]
     assert (e <= tol[:n]).all(), (float((e / tol[:n]).nan_to_num(9e9).max()), float(e.nan_to_num(9e9).max()))
@@ -156,7 +153,7 @@ def test_scores_that_rise(capi, n_q, n_kv, dim, rows, bits):       # noqa: F811
 # ------------------------------------------------------------------ V scales far apart
 
 @pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
-@pytest.mark.parametrize("e", [0, 10, 27, 60, 119])
+@pytest.mark.parametrize("e", [0, 27, 60, 119])
 def test_pages_of_zeros_beside_large_ones(capi, n_q, n_kv, dim, rows, e):      # noqa: F811
     """Keys of pages whose values are zeros (V scale 2^-100) count in the sum
     like any others, whatever the other pages' scales; scores rise and fall."""
@@ -184,22 +181,23 @@ def test_pages_of_zeros_beside_large_ones(capi, n_q, n_kv, dim, rows, e):      #
 
 
 @pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
-@pytest.mark.parametrize("scales", [(-100, 119), (119, -100), (-100, 0, 100), (60, -60), (-100,), (119,), (-50, -90, -10)])
 @pytest.mark.parametrize("bits", [0, 13, 70, 200])
-def test_v_scales_over_their_whole_range(capi, n_q, n_kv, dim, rows, scales, bits):      # noqa: F811
+def test_v_scales_over_their_whole_range(capi, n_q, n_kv, dim, rows, bits):      # noqa: F811
     """Pages of all scales in turn, each larger one with the smaller weights."""
     held = [max(n + 5, 600 + 64 * i) for i, n in enumerate(rows)]
     st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=bits)
     pages = -(-max(held) // 64)
-    e = torch.tensor([scales[p % len(scales)] for p in range(pages)])
-    order = torch.unique(e)
-    level = -(e[:, None] == order).float().argmax(1).repeat_interleave(64).float()
-    scale = set_keys(st, level, max(bits, 1))
-    for s, t in enumerate(st["table"]):
-        for p in range(-(-held[s] // 64)):
-            st["cache"][3][t[p]] = 2.0 ** int(e[p])
-    attend(capi, st, scale=scale)
-    check(st, scale=scale)
+    for scales in ((-100, 119), (119, -100), (-100, 0, 100), (60, -60), (-100,), (119,), (-50, -90, -10)):
+        e = torch.tensor([scales[p % len(scales)] for p in range(pages)])
+        order = torch.unique(e)
+        level = -(e[:, None] == order).float().argmax(1).repeat_interleave(64).float()
+        scale = set_keys(st, level, max(bits, 1))
+        for s, t in enumerate(st["table"]):
+            for p in range(-(-held[s] // 64)):
+                st["cache"][3][t[p]] = 2.0 ** int(e[p])
+        st["out"].fill_(3.0), st["lse"].fill_(3.0)
+        attend(capi, st, scale=scale)
+        check(st, scale=scale)
 
 
 @pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
@@ -216,3 +214,27 @@ def test_a_long_cache_of_zeros(capi, n_q, n_kv, dim, rows):      # noqa: F811
         scale = set_keys(st, level, bits, noise=0.01)
         attend(capi, st, scale=scale)
         check(st, scale=scale)
+
+
+# ------------------------------------------------------------------ weights far below the largest
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("at", [0, 2990])
+def test_a_long_tail_behind_one_key(capi, n_q, n_kv, dim, rows, at):      # noqa: F811
+    """One key without values, of 2^bits the weight of each other one, in a
+    page whose V scale is 2^above over the others': the values are the tail's."""
+    held = [3000 + n for n in rows]
+    st = attn_state(n_q, n_kv, dim, rows, held, F16, seed=at)
+    for bits, above in ((15, 8), (17, 8), (20, 8), (12, 0), (22, 0)):
+        level, v = torch.zeros(max(held)), torch.full((max(held),), 224.0)
+        level[at] = 1.0
+        v[64 * (at // 64):64 * (at // 64) + 64] = 224.0 * 2.0 ** -above
+        v[at] = 0.0
+        scale = set_keys(st, level, bits, v, noise=0.02)
+        st["cache"][3].fill_(0.125)
+        for t in st["table"]:
+            st["cache"][3][t[at // 64]] = 0.125 * 2.0 ** above
+        for causal in (True, False):
+            st["out"].fill_(3.0), st["lse"].fill_(3.0)
+            attend(capi, st, causal=causal, scale=scale)
+            check(st, causal=causal, scale=scale)
