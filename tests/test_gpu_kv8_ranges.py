@@ -61,24 +61,24 @@ def define(st, causal=True, window=0, scale=None, gone=()):
         see = (key <= pos if causal else key < kv) & there
         if window:
             see = see & (key > pos - window if causal else key >= kv - n - window)
-        for h in range(n_kv):
-            ks = (kc[pages, h] * k_scale[pages, h][:, None, None]).reshape(-1, dim)[:kv]
-            vs = (vc[pages, h] * v_scale[pages, h][:, None, None]).reshape(-1, dim)[:kv]
-            ks, vs = (torch.where(there[:, None], x, 0.0) for x in (ks, vs))
-            sc = torch.where(there, v_scale[pages, h].repeat_interleave(64)[:kv], 0.0)
-            g = slice(h * group, (h + 1) * group)
-            qh = q[r0:r0 + n, g].transpose(0, 1)                       # [group][n][dim]
-            x = (qh @ ks.T * scale).masked_fill(~see, -math.inf)
-            w = torch.softmax(x, -1).nan_to_num(0.0)                   # rows without keys: zeros
-            put = lambda name, v: r[name][r0:r0 + n, g].copy_(v.transpose(0, 1))   # noqa: E731
-            put("out", w @ vs)
-            put("mag", w @ vs.abs())
-            put("lse", torch.logsumexp(x, -1))
-            put("terms", (qh.abs() @ ks.abs().T).masked_fill(~see, 0.0).amax(-1) * scale)
-            put("qabs", qh.abs().amax(-1) * torch.where(see.any(0), ks.abs().sum(1), 0.0).max() * scale)
-            put("unit", ((w * sc).amax(-1) * 448 * kv)[..., None])
-            r["chain"][r0:r0 + n, g] = kv / 32 + 16
-            r["far"][r0:r0 + n, g] = torch.where(sc > 0, sc, 1.0).log2().abs().max()
+        cached = lambda c, sc: (c[pages] * sc[pages][..., None, None]).transpose(0, 1).reshape(n_kv, -1, dim)[:, :kv]  # noqa: E731
+        ks, vs = (torch.where(there[:, None], cached(c, x), 0.0) for c, x in ((kc, k_scale), (vc, v_scale)))
+        sc = torch.where(there, v_scale[pages].repeat_interleave(64, 0)[:kv].T, 0.0)            # [n_kv][kv]
+        qh = q[r0:r0 + n].view(n, n_kv, group, dim).permute(1, 2, 0, 3).reshape(n_kv, group * n, dim)
+        hide = ~see.expand(n, kv).repeat(group, 1)
+        x = (qh @ ks.mT * scale).masked_fill_(hide, -math.inf)
+        w = torch.softmax(x, -1).nan_to_num_(0.0)                      # rows without keys: zeros
+
+        def put(name, v):                                              # [n_kv][group * n]...
+            r[name][r0:r0 + n] = v.unflatten(1, (group, n)).movedim(2, 0).flatten(1, 2)
+        put("out", w @ vs)
+        put("mag", w @ vs.abs())
+        put("lse", torch.logsumexp(x, -1))
+        put("unit", ((w * sc[:, None]).amax(-1) * 448 * (~hide).sum(-1))[..., None])
+        put("terms", (qh.abs() @ ks.abs().mT).masked_fill_(hide, 0.0).amax(-1) * scale)
+        put("qabs", qh.abs().amax(-1) * torch.where(see.any(0), ks.abs().sum(-1), 0.0).amax(-1, keepdim=True) * scale)
+        put("far", torch.where(sc > 0, sc, 1.0).log2().abs().amax(-1, keepdim=True).expand(n_kv, group * n))
+        r["chain"][r0:r0 + n] = kv / 32 + 16
     return r
 
 
@@ -101,7 +101,7 @@ def check(st, causal=True, window=0, scale=None, gone=()):
 
 
 def codes(x):
-    return x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    return x.to(torch.float8_e4m3fn).view(torch.uint8)
 
 
 def set_keys(st, level, bits, v=None, noise=0.05):
@@ -109,19 +109,21 @@ def set_keys(st, level, bits, v=None, noise=0.05):
     a little noise): dimension 0 of q is 16, of a key its level.  Values
     v[key] in every dimension where given (codes; scales stay).  Returns the
     softmax scale."""
-    g = torch.Generator().manual_seed(5)
-    q, (kc, vc, ks, vs) = st["q"], st["cache"]
-    q.copy_(noise * torch.randn(q.shape, generator=g))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, (kc, vc, ks, _) = st["q"], st["cache"]
+    q.copy_(noise * torch.randn(q.shape, generator=g, device="cuda"))
     q[..., 0] = 16.0
     ks.fill_(1.0)
     for s, kv in enumerate(st["held"]):
-        for p in range(-(-kv // 64)):
-            page, n = st["table"][s][p], min(64, kv - 64 * p)
-            k = 0.25 * torch.randn(kc.shape[1], n, kc.shape[3], generator=g)
-            k[..., 0] = level[64 * p:64 * p + n].float()
-            kc[page, :, :n] = codes(k)
-            if v is not None:
-                vc[page, :, :n] = codes(v[64 * p:64 * p + n, None].float().expand(n, vc.shape[3])[None].expand_as(k))
+        pages = torch.tensor(st["table"][s][:-(-kv // 64)], device="cuda")
+        n = 64 * len(pages)
+        here = lambda x: torch.nn.functional.pad(x[:n].float().cuda(), (0, n - len(x[:n]))).view(-1, 1, 64)   # noqa: E731
+        held = (torch.arange(n, device="cuda") < kv).view(-1, 1, 64, 1)
+        k = 0.25 * torch.randn((len(pages), *kc.shape[1:]), generator=g, device="cuda")
+        k[..., 0] = here(level)
+        kc[pages] = torch.where(held, codes(k), kc[pages])
+        if v is not None:
+            vc[pages] = torch.where(held, codes(here(v)[..., None].expand_as(k)), vc[pages])
     return bits * math.log(2) / 16
 
 
@@ -238,3 +240,94 @@ def test_a_long_tail_behind_one_key(capi, n_q, n_kv, dim, rows, at):      # noqa
             st["out"].fill_(3.0), st["lse"].fill_(3.0)
             attend(capi, st, causal=causal, scale=scale)
             check(st, causal=causal, scale=scale)
+
+
+# ------------------------------------------------------------------ pages and scales that are not there
+
+GONE = [[0], [1], [0, 1], [2, 3], [3, 4], [5], [-1], list(range(64))]
+
+
+def _spoil(st, which, change):
+    """Applies change(table row, page index) to the pages `which` of every
+    sequence and returns the page numbers as the table then has them."""
+    gone = set()
+    for s, t in enumerate(st["table"]):
+        n = -(-st["held"][s] // 64)
+        for p in {w % n for w in which if w < n}:
+            change(t, p)
+            gone.add(t[p])
+    return gone
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("which", GONE)
+def test_pages_that_are_not_there(capi, n_q, n_kv, dim, rows, which):      # noqa: F811
+    """A page number out of range sets err; its keys are left out as if they
+    were masked.  The codes that stand in shared memory instead are NaN."""
+    held = [max(n + 5, 400 + 64 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=3)
+    stale = attn_state(n_q, n_kv, dim, rows, held, BF, seed=3)
+    for c in stale["cache"][:2]:
+        c.fill_(0x7f)
+    pages = st["cache"][0].shape[0]
+    for bad in (-1, pages, 2 ** 31 - 1, -(2 ** 31)):
+        cut = {**st, "table": [list(t) for t in st["table"]]}
+
+        def lose(t, p):
+            t[p] = bad
+        gone = _spoil(cut, which, lose)
+        for causal, window in ((True, 0), (False, 0), (True, 130)):
+            attend(capi, stale)                                        # fills the pages' places
+            cut["out"].fill_(3.0), cut["lse"].fill_(3.0)
+            # only pages that some row sees are looked up
+            read = any(t[p] in gone for s, t in enumerate(cut["table"])
+                       for p in range(max(0, held[s] - rows[s] + 1 - window) // 64 if window else 0, -(-held[s] // 64)))
+            attend(capi, cut, causal, window, want_err=(2, 303) if read else (0, 0))
+            check(cut, causal, window, gone=gone)
+
+
+# ------------------------------------------------------------------ many sequences, far pools
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", [
+    (8, 2, 64, [16] * 40),                                   # 64-row tiles
+    (8, 1, 128, [5, 0, 8, 1] * 20 + [16]),
+    (32, 2, 64, [8, 1, 16] * 15),                            # 128
+    (8, 2, 64, [30, 40, 1] * 100),
+    (4, 2, 64, [150, 40, 0] * 33 + [300]),                   # two times 128
+])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 40)])
+def test_larger_tiles_of_many_sequences(capi, n_q, n_kv, dim, rows, causal, window):      # noqa: F811
+    """More sequences than a warp's lanes in the tcgen05 form."""
+    g = torch.Generator().manual_seed(len(rows))
+    past = torch.randint(0, 500, (len(rows),), generator=g).tolist()
+    st = attn_state(n_q, n_kv, dim, rows, [n + p for n, p in zip(rows, past)], BF, seed=2, pad=0)
+    ws = attend(capi, st, causal, window)
+    check(st, causal, window)
+    first = st["out"].clone(), st["lse"].clone()
+    st["out"].fill_(3.0), st["lse"].fill_(3.0)
+    attend(capi, st, causal, window, workspace=ws)
+    assert torch.equal(first[0], st["out"]) and torch.equal(first[1], st["lse"])
+
+
+def test_larger_tiles_over_a_pool_past_4_gib(capi):      # noqa: F811
+    n_kv, dim = 8, 128
+    pages = (1 << 32) // (n_kv * 64 * dim) + 4000
+    if torch.cuda.mem_get_info()[0] < 3 * pages * n_kv * 64 * dim:
+        pytest.skip("not enough device memory")
+    kc = torch.zeros((pages, n_kv, 64, dim), dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    sc = [torch.ones((pages, n_kv), device="cuda") for _ in range(2)]
+    for rows in ([16] * 4, [40] * 6, [200] * 6):
+        small = attn_state(32, n_kv, dim, rows, [260 + n for n in rows], BF, seed=8)
+        attend(capi, small)
+        check(small)
+        table = [[-1 if p < 0 else pages - 1 - 7 * p for p in t] for t in small["table"]]
+        big = {**small, "cache": [kc, vc] + sc, "table": table, "out": torch.full_like(small["out"], 3.0),
+               "lse": torch.full_like(small["lse"], 3.0)}
+        for t, u in zip(small["table"], table):
+            for a, b in zip(t, u):
+                if a >= 0:
+                    for c, s in zip(big["cache"], small["cache"]):
+                        c[b] = s[a]
+        attend(capi, big)
+        assert torch.equal(big["out"], small["out"]) and torch.equal(big["lse"], small["lse"])
