@@ -366,6 +366,11 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant
             look(w.p0, &page, &ks, &vs);
             for (int b = w.p0; b < w.p1 && ok; b += 32) {
                 look(b + 32, &next_page, &next_ks, &next_vs);
+                if (page >= 0 && !scales_fit(ks, vs)) {      // not in look, which would wait for the scales
+                    report(a.err, DERR_INDEX, SITE_SCALE);
+                    page = -1;
+                    ks = -1.f;
+                }
                 const int m = w.p1 - b < 32 ? w.p1 - b : 32;
                 for (int j = 0; j < m; ++j) {
                     const int pg = __shfl_sync(0xffffffffu, page, j);

@@ -9,7 +9,7 @@ namespace dfl {
 namespace kv8 {
 
 // Sites of err words.
-constexpr int SITE_FULL = 301, SITE_EMPTY = 302, SITE_PAGE = 303, SITE_LEN = 304;
+constexpr int SITE_FULL = 301, SITE_EMPTY = 302, SITE_PAGE = 303, SITE_LEN = 304, SITE_SCALE = 305;
 
 __device__ __forceinline__ void report(int* err, int code, int info) {
     if (err && atomicCAS(err, 0, code) == 0) err[1] = info;
@@ -251,6 +251,9 @@ __device__ __forceinline__ float row_lse(float Z, float l) {
     return l == 0.f ? -INFINITY : (Z + log2f(l)) * 0.6931471805599453f;
 }
 
+// Scales that a page can have (the append's are powers of two from 2^-100 to
+// 2^119; K's may be 0, which makes all its scores 0).
+__device__ __forceinline__ bool scales_fit(float k, float v) { return k >= 0.f && k < INFINITY && v > 0.f && v < INFINITY; }
 // V scales that let outputs and sum share one reference.
 __device__ __forceinline__ bool near(float scale) { return scale >= 0x1p-32f && scale <= 0x1p32f; }
 // From this factor between weights on values and the sum's on, the former are zeros in f16.
@@ -294,7 +297,7 @@ __device__ __noinline__ uint32_t nan_dims(const Kv8AttnArgs& a, int s, int idx, 
         const int key0 = p * KV8_PAGE, pg = a.table[(size_t)s * a.max_pages + p];
         if ((key0 >= w.in_lo && key0 + KV8_PAGE <= w.in_hi) || pg < 0 || pg >= a.n_pages) continue;
         const size_t at = (size_t)pg * a.n_kv + w.kh;
-        if (!(a.k_scale[at] >= 0.f && a.v_scale[at] > 0.f)) continue;
+        if (!scales_fit(a.k_scale[at], a.v_scale[at])) continue;
         const int k1 = khi - key0 < KV8_PAGE ? khi - key0 : KV8_PAGE;
 #pragma unroll 1
         for (int k = klo > key0 ? klo - key0 : 0; k < k1; ++k)

@@ -594,8 +594,9 @@ int dflash_kv8_append(const dflash_kv8_cache* cache /*host*/, const void* k, int
  * Workspace: dflash_kv8_workspace_bytes of the call's counts (more rows may
  * need less), zero-filled before its first use (completed calls leave its
  * counters at zero).  Calls of any shapes can share one that is large enough
- * for each, but must not overlap on the GPU; zero it again after err was set.  A length or page
- * out of range: err {2, site}, that sequence (page) is left out.
+ * for each, but must not overlap on the GPU; zero it again after err was set.  A length, page
+ * or scale (K's below 0, V's not above 0, either not finite) out of range:
+ * err {2, site}, that sequence (page) is left out.
  * Errors: CONFIG, ARG, CUDA.
  */
 typedef struct {

@@ -331,3 +331,34 @@ def test_larger_tiles_over_a_pool_past_4_gib(capi):      # noqa: F811
                         c[b] = s[a]
         attend(capi, big)
         assert torch.equal(big["out"], small["out"]) and torch.equal(big["lse"], small["lse"])
+
+
+BAD_SCALES = [(3, 0.0), (3, -1.0), (3, math.nan), (3, math.inf), (2, -0.5), (2, math.nan), (2, math.inf)]
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("which", [[0], [1, 2], [5, 6, -1]])
+def test_scales_that_no_append_writes(capi, n_q, n_kv, dim, rows, which):      # noqa: F811
+    """A K scale that is negative, a V scale that is not above 0, one that is
+    not finite: err, and the page's keys are left out."""
+    held = [max(n + 5, 400 + 64 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=4)
+    good = st["cache"]
+    for tensor, value in BAD_SCALES:
+        bad = {**st, "cache": [c.clone() if i > 1 else c for i, c in enumerate(good)]}
+
+        def spoil(t, p):
+            bad["cache"][tensor][t[p]] = value
+        gone = _spoil(bad, which, spoil)
+        st["out"].fill_(3.0), st["lse"].fill_(3.0)
+        attend(capi, bad, want_err=(2, 305))
+        check(bad, gone=gone)
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+def test_k_scales_of_zero(capi, n_q, n_kv, dim, rows):      # noqa: F811
+    st = attn_state(n_q, n_kv, dim, rows, [max(n + 5, 300) for n in rows], BF, seed=4)
+    for t in st["table"]:
+        st["cache"][2][t[1]] = 0.0
+    attend(capi, st)
+    check(st)
