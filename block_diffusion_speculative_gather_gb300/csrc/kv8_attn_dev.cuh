@@ -150,11 +150,14 @@ struct Finder {
 
 __device__ __forceinline__ int items_of(const Kv8AttnArgs& a, const Seq& q) { return q.tiles * a.n_kv * q.splits; }
 
+// Sums of counts that stay at the largest int: row starts may be anything.
+__device__ __forceinline__ int add_counts(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
 __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        if (lane >= o) v = add_counts(v, u);
     }
     return v;
 }
@@ -166,7 +169,7 @@ __device__ __forceinline__ Finder make_finder(const Kv8AttnArgs& a, int lane) {
     f.q = Seq{};
     for (int s = lane * f.per; s < a.S && s < (lane + 1) * f.per; ++s) {
         f.q = seq_of(a, s);
-        mine += items_of(a, f.q);
+        mine = add_counts(mine, items_of(a, f.q));
     }
     f.s = lane;
     if (f.per == 1 && a.S > 1) {
@@ -190,6 +193,12 @@ __device__ __forceinline__ Finder make_finder(const Kv8AttnArgs& a, int lane) {
     const int inc = warp_inclusive(mine, lane);
     f.cum = inc - mine;
     f.total = __shfl_sync(0xffffffffu, inc, 31);
+    // sequences whose rows overlap can ask for any number of items: above what
+    // the call's rows can make nothing is done
+    if (f.total > a.ticket_cap * a.split_cap) {
+        report(a.err, DERR_INDEX, SITE_LEN);
+        f.total = 0;
+    }
     return f;
 }
 

@@ -596,7 +596,9 @@ int dflash_kv8_append(const dflash_kv8_cache* cache /*host*/, const void* k, int
  * counters at zero).  Calls of any shapes can share one that is large enough
  * for each, but must not overlap on the GPU; zero it again after err was set.  A length, page
  * or scale (K's below 0, V's not above 0, either not finite) out of range:
- * err {2, site}, that sequence (page) is left out.
+ * err {2, site}, that sequence (page) is left out; where the rows of sequences
+ * overlap so often that they make more work than the call's rows can, nothing
+ * is done.
  * Errors: CONFIG, ARG, CUDA.
  */
 typedef struct {

@@ -362,3 +362,21 @@ def test_k_scales_of_zero(capi, n_q, n_kv, dim, rows):      # noqa: F811
         st["cache"][2][t[1]] = 0.0
     attend(capi, st)
     check(st)
+
+
+# ------------------------------------------------------------------ row starts that overlap
+
+@pytest.mark.parametrize("n_q,n_kv,dim,S,rows", [(8, 2, 64, 64, 96), (8, 2, 128, 40, 2000), (256, 256, 64, 4096, 65536)])
+def test_overlapping_sequences_beyond_the_calls_rows(capi, n_q, n_kv, dim, S, rows):      # noqa: F811
+    """Row starts 0, rows, 0, rows, ...: every other sequence claims all rows
+    (at the largest more than 2^31 items).  err, and nothing is touched."""
+    cache = [torch.zeros((2, n_kv, 64, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.ones((2, n_kv), device="cuda") for _ in range(2)]
+    q = torch.zeros((rows, n_q, dim), dtype=BF, device="cuda")
+    out, lse = torch.full_like(q, 3.0), torch.full((rows, n_q), 3.0, device="cuda")
+    start = ints([0, rows] * (S // 2) + [0])
+    ws = torch.zeros(capi.dflash_kv8_workspace_bytes(rows, S, n_q, n_kv, dim, 2), dtype=torch.uint8, device="cuda")
+    err = ints([0, 0])
+    capi.dflash_kv8_attention(q, *cache, ints([[0, 1]] * S), ints([100] * S), start, out, ws, err, lse=lse)
+    assert err.tolist() == [2, 304]
+    assert (out == 3.0).all() and (lse == 3.0).all() and (ws == 0).all()
