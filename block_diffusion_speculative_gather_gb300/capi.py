@@ -449,6 +449,7 @@ _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _KINDS = {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
 _HALVES = (torch.bfloat16, torch.float16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_MOST = 0x7fffffff
 _CACHE = struct.Struct("4Q4i")        # dflash_kv8_cache
 _QUERY = struct.Struct("6Q4q7if")     # dflash_kv8_query
 _HEADS = struct.Struct("2Q2i4q")      # dflash_heads
@@ -471,6 +472,13 @@ def _current(t) -> int:
     tensor is there)."""
     dev = t.get_device()
     return dev if dev >= 0 and dev == torch._C._cuda_getDevice() else -2
+
+
+def _counts(**extents) -> None:
+    """Extents that the C ABI's int32 arguments hold (a longer one would wrap)."""
+    for name, n in extents.items():
+        if n > _MOST:
+            raise DFlashError(DFLASH_ERR_ARG, f"{name}: {n} is out of range")
 
 
 def _here(**tensors) -> None:
@@ -526,6 +534,8 @@ def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, posit
               row_start=row_start, positions=positions, slots=slots, kv_after=kv_after,
               n_free_out=n_free_out)
         dev, rows, pool = table.get_device(), positions.shape[0], free_pages.shape[0]
+    if S > _MOST or rows > _MOST or pool > _MOST or max_pages > _MOST:
+        _counts(S=S, rows=rows, free_pages=pool, max_pages=max_pages)
     rc = lib.dflash_pages_plan(kv_len.data_ptr(), q_len.data_ptr(), S, free_pages.data_ptr(), pool,
                                n_free.data_ptr(), table.data_ptr(), max_pages, rows, row_start.data_ptr(),
                                positions.data_ptr(), slots.data_ptr(), kv_after.data_ptr(),
@@ -545,6 +555,7 @@ def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
     _need(free_pages, "free_pages", i32, (None,))
     _need(n_free, "n_free", i32, (1,))
     _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
+    _counts(S=S, max_pages=max_pages, free_pages=free_pages.shape[0])
     check(lib.dflash_pages_trim(kv_len.data_ptr(), new_len.data_ptr(), S, free_pages.data_ptr(),
                                 free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages,
                                 _raw(stream, table.get_device())))
@@ -593,6 +604,8 @@ def dflash_kv8_append(k, v, slots, k_codes, v_codes, k_scale, v_scale, err, stre
         _here(k=k, v=v, slots=slots, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale,
               err=err)
         dev, kind, ks, vs = k.get_device(), k.dtype, k.stride(), v.stride()
+    if n_pages > _MOST or rows > _MOST:
+        _counts(n_pages=n_pages, rows=rows)
     cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         n_pages, n_kv, hd, 0)
     rc = lib.dflash_kv8_append(cache, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], _KINDS[kind],
@@ -644,6 +657,8 @@ def dflash_kv8_attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, r
         _here(q=q, out=out, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
               kv_len=kv_len, row_start=row_start, workspace=workspace, err=err, lse=lse)
         dev, kind, qs, os_ = q.get_device(), q.dtype, q.stride(), out.stride()
+    if n_pages > _MOST or rows > _MOST or S > _MOST or max_pages > _MOST:
+        _counts(n_pages=n_pages, rows=rows, S=S, max_pages=max_pages)
     cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         n_pages, n_kv, hd, 0)
     args = _QUERY.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
@@ -707,6 +722,8 @@ def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2
             heads2, xs2, os2 = x2.shape[1], x2.stride(), out2.stride()
         _here(turns=turns, positions=positions, x=x, out=out, x2=x2, out2=out2)
         dev, kind, xs, os_ = x.get_device(), x.dtype, x.stride(), out.stride()
+    if rows > _MOST:
+        _counts(rows=rows)
     first = _HEADS.pack(x.data_ptr(), out.data_ptr(), heads, 0, xs[0], xs[1], os_[0], os_[1])
     second = None if x2 is None else _HEADS.pack(x2.data_ptr(), out2.data_ptr(), heads2, 0, xs2[0], xs2[1],
                                                  os2[0], os2[1])

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int KV8_MAX_SEQS = 4096;        // a lane of an attention CTA's finding warp scans S / 32 of them
 constexpr int KV8_MAX_PAGES = 1 << 25;    // slots are int32
+constexpr int MAX_COUNT = 1 << 30;        // rows or sequences: sums of two of them, and a step beyond, are int32
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t size_of(int dtype) { return dtype == DFLASH_F32 ? 4 : 2; }
@@ -76,7 +77,8 @@ int dflash_pages_plan(const int32_t* kv_len, const int32_t* q_len, int32_t S, co
                       int32_t* n_free_out, dflash_stream_t stream) {
     if (!kv_len || !q_len || !n_free || !table || !row_start || !kv_after || !n_free_out)
         return report_error(DFLASH_ERR_ARG, "NULL argument");
-    if (S < 1 || free_cap < 0 || max_pages < 1 || max_pages >= KV8_MAX_PAGES || rows < 0)
+    if (S < 1 || S > MAX_COUNT || free_cap < 0 || max_pages < 1 || max_pages >= KV8_MAX_PAGES || rows < 0 ||
+        rows > MAX_COUNT)
         return report_error(DFLASH_ERR_ARG, "S %d free_cap %d max_pages %d rows %d out of range", S, free_cap,
                             max_pages, rows);
     if ((free_cap && !free_pages) || (rows && (!positions || !slots)))
@@ -91,7 +93,7 @@ int dflash_pages_trim(int32_t* kv_len, const int32_t* new_len, int32_t S, int32_
                       int32_t* n_free, int32_t* table, int32_t max_pages, dflash_stream_t stream) {
     if (!kv_len || !new_len || !n_free || !table || (free_cap && !free_pages))
         return report_error(DFLASH_ERR_ARG, "NULL argument");
-    if (S < 1 || free_cap < 0 || max_pages < 1 || max_pages >= KV8_MAX_PAGES)
+    if (S < 1 || S > MAX_COUNT || free_cap < 0 || max_pages < 1 || max_pages >= KV8_MAX_PAGES)
         return report_error(DFLASH_ERR_ARG, "S %d free_cap %d max_pages %d out of range", S, free_cap, max_pages);
     if (const int r = pending()) return r;
     PagesTrimArgs a{kv_len, new_len, free_pages, n_free, table, S, free_cap, max_pages};
@@ -130,7 +132,7 @@ int dflash_rope(const dflash_rope_config* cfg, const uint64_t* turns, const int3
     if (!turns || !a || (rows > 0 && !positions)) return report_error(DFLASH_ERR_ARG, "NULL argument");
     if (dtype != DFLASH_F32 && dtype != DFLASH_BF16 && dtype != DFLASH_F16)
         return report_error(DFLASH_ERR_ARG, "dtype %d: F32, BF16 or F16", dtype);
-    if (rows < 0 || head_dim < cfg->rotary_dim || head_dim > 1024)
+    if (rows < 0 || rows > MAX_COUNT || head_dim < cfg->rotary_dim || head_dim > 1024)
         return report_error(DFLASH_ERR_ARG, "rows %d head_dim %d (rotary_dim %d to 1024)", rows, head_dim,
                             cfg->rotary_dim);
     const size_t es = size_of(dtype);
@@ -172,7 +174,8 @@ int dflash_kv8_append(const dflash_kv8_cache* cache, const void* k, int64_t k_ro
     if (const int r = check_cache(cache)) return r;
     if (dtype != DFLASH_F32 && dtype != DFLASH_BF16 && dtype != DFLASH_F16)
         return report_error(DFLASH_ERR_ARG, "dtype %d: F32, BF16 or F16", dtype);
-    if (rows < 0 || !err || !aligned(err, 8)) return report_error(DFLASH_ERR_ARG, "rows %d or err", rows);
+    if (rows < 0 || rows > MAX_COUNT || !err || !aligned(err, 8))
+        return report_error(DFLASH_ERR_ARG, "rows %d or err", rows);
     if (rows == 0) return DFLASH_OK;
     if (!k || !v || !slots) return report_error(DFLASH_ERR_ARG, "NULL argument");
     const size_t es = size_of(dtype);

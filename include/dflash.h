@@ -534,7 +534,8 @@ typedef struct {
  * rows before each sequence; positions [rows] and slots [rows] of each new
  * row, -1 behind the last; kv_after [S] = kv_len + rows given; n_free_out.
  * kv_after may be kv_len and n_free_out may be n_free (a step that advances
- * its own state).  Errors: ARG, CUDA.
+ * its own state).  S and rows at most 2^30, here and in the calls below.
+ * Errors: ARG, CUDA.
  */
 int dflash_pages_plan(const int32_t* kv_len, const int32_t* q_len, int32_t S, const int32_t* free_pages,
                       int32_t free_cap, const int32_t* n_free, int32_t* table, int32_t max_pages, int32_t rows,
