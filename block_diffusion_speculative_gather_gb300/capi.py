@@ -661,10 +661,13 @@ def dflash_kv8_attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_len, r
         _counts(n_pages=n_pages, rows=rows, S=S, max_pages=max_pages)
     cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                         n_pages, n_kv, hd, 0)
-    args = _QUERY.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
-                       kv_len.data_ptr(), row_start.data_ptr(), qs[0], qs[1], os_[0], os_[1], rows, n_q, S,
-                       max_pages, _KINDS[kind], 1 if causal else 0, window,
-                       hd ** -0.5 if scale is None else scale)
+    try:
+        args = _QUERY.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(),
+                           kv_len.data_ptr(), row_start.data_ptr(), qs[0], qs[1], os_[0], os_[1], rows, n_q, S,
+                           max_pages, _KINDS[kind], 1 if causal else 0, window,
+                           hd ** -0.5 if scale is None else scale)
+    except struct.error as e:
+        raise DFlashError(DFLASH_ERR_ARG, f"window {window!r} (an int32), scale {scale!r} (a number): {e}") from None
     rc = lib.dflash_kv8_attention(cache, args, workspace.data_ptr(), workspace.nbytes, err.data_ptr(),
                                   _raw(stream, dev))
     if rc:

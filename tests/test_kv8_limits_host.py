@@ -31,3 +31,17 @@ def test_extents_beyond_int32_do_not_wrap(capi):      # noqa: F811
         with pytest.raises(capi.DFlashError) as e:
             capi._counts(S=1, rows=n)
         assert "rows" in str(e.value)
+
+
+@pytest.mark.parametrize("kw,word", [(dict(window=2 ** 31), "window"), (dict(window=-2 ** 31 - 1), "window"),
+                                     (dict(window=1.5), "window"), (dict(scale="x"), "scale")])
+def test_window_and_scale_outside_their_types(capi, monkeypatch, kw, word):      # noqa: F811
+    """The library's error, not the one of packing its struct."""
+    monkeypatch.setattr(capi, "_here", lambda **tensors: None)      # host tensors: refused before the call
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)   # noqa: E731
+    q, out = (torch.zeros((3, 4, 64), dtype=torch.bfloat16) for _ in range(2))
+    codes, scales = torch.zeros((4, 2, 64, 64), dtype=torch.uint8), torch.ones(4, 2)
+    with pytest.raises(capi.DFlashError) as e:
+        capi.dflash_kv8_attention(q, codes, codes, scales, scales, i32(2, 4), i32(2), i32(3), out,
+                                  torch.zeros(1 << 20, dtype=torch.uint8), i32(2), stream=0, **kw)
+    assert e.value.code == ARG and word in str(e.value)
