@@ -406,6 +406,8 @@ class PagedKV8:
 
     def rotate(self, q: torch.Tensor, k: torch.Tensor):
         """Rotary positions of the step's rows, in place."""
+        if self.rope is None:
+            raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without rope: no rotary settings")
         capi.dflash_rope(self.rope, self.turns, self.positions, q, q, k, k)
 
     def attend(self, layer: int, q, k, v, out=None, lse=None, scale=None, causal=True, window=0):

@@ -45,3 +45,13 @@ def test_window_and_scale_outside_their_types(capi, monkeypatch, kw, word):     
         capi.dflash_kv8_attention(q, codes, codes, scales, scales, i32(2, 4), i32(2), i32(3), out,
                                   torch.zeros(1 << 20, dtype=torch.uint8), i32(2), stream=0, **kw)
     assert e.value.code == ARG and word in str(e.value)
+
+
+def test_rotating_without_rotary_settings():
+    from block_diffusion_speculative_gather_gb300 import capi as c
+    from block_diffusion_speculative_gather_gb300.runtime import PagedKV8
+    kv = PagedKV8.__new__(PagedKV8)         # without its device buffers
+    kv.rope = None
+    with pytest.raises(c.DFlashError) as e:
+        kv.rotate(torch.zeros(3, 4, 64), torch.zeros(3, 2, 64))
+    assert "rope" in str(e.value)
