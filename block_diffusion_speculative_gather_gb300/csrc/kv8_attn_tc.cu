@@ -35,11 +35,14 @@
 // The reference of a row's weights is set 2^ROOM below its maximum and moves only
 // when that rises by more than 2^LAZY (weights stay within f16's range), so
 // outputs are rescaled in tensor memory rarely.  When one row of a warp moves,
-// all whose maximum has risen do: the warp's outputs are rewritten anyway.  Room
-// below the largest weight costs rescales; 4 prompt chunks, verify of 8
-// sequences, 32 draft blocks, in us, by ROOM and LAZY:
+// all whose maximum has risen do, as the warp's outputs are rewritten anyway, but
+// only while all rows have seen the same keys: a row's bits must not follow from
+// keys that it does not see.  Room below the largest weight costs rescales; 4
+// prompt chunks, verify of 8 sequences, 32 draft blocks, in us, by ROOM and LAZY,
+// rows moving together everywhere:
 //   3, 12: 484, 75.0, 27.3;  5, 10: 491, 75.1, 27.6;  7, 8: 500, 75.3, 28.0;
 //   9, 6: 519, 76.2, 29.5 (rows moving one by one 581, 83.9, 34.2)
+// and as it stands 496, 76.8, 28.4.
 // (7: keys of 2^-21 of the largest weight keep their 11 bits, 2^-32 is lost.)
 //
 // Tensor memory: scores at columns 0 and 128, outputs at 256 and 384.  A
@@ -353,6 +356,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                 }
                 tc::st_wait();
             };
+            // all rows have seen the same keys up to steps from here on
+            const int same = w.lo == w.in_lo || w.p0 * KV8_PAGE >= w.in_lo ? (w.hi == w.in_hi ? 0x7fffffff : w.in_hi - STEP + 1) : 0;
             float M = -INFINITY, l = 0.f;
             int i = 0;
             for (; i < nt && ok; ++i, ++cs) {
@@ -371,6 +376,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     if (sc.far > 0.f) break;
                     mask(sc.ks, k0);
                 }
+                const float rise = k0 < same ? ROOM : INFINITY;      // that moves a row beside another one
                 // 32 keys at a time, the next 32 scores on their way meanwhile
                 uint32_t buf[2][32];
                 const int c0 = 2 * copy;
@@ -403,7 +409,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_const
                     bool need = mx > M + (ROOM + LAZY) || (M == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xffffffffu, need)) {
                         const bool first = M == -INFINITY;
-                        need = need || (!first && mx > M + ROOM);
+                        // the others that have risen: only where all rows have seen the same keys
+                        // so far, as a row's bits must not follow from keys that it does not see
+                        need = need || (!first && mx > M + rise);
                         const float f0 = need ? (first ? 0.f : ex2(M + ROOM - mx)) : 1.f;
                         if (need) M = mx - ROOM;
                         l *= f0;

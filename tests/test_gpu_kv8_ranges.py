@@ -380,3 +380,37 @@ def test_overlapping_sequences_beyond_the_calls_rows(capi, n_q, n_kv, dim, S, ro
     capi.dflash_kv8_attention(q, *cache, ints([[0, 1]] * S), ints([100] * S), start, out, ws, err, lse=lse)
     assert err.tolist() == [2, 304]
     assert (out == 3.0).all() and (lse == 3.0).all() and (ws == 0).all()
+
+
+# ------------------------------------------------------------------ rows and what they do not see
+
+@pytest.mark.parametrize("n_q,n_kv,dim,rows", FORMS)
+@pytest.mark.parametrize("window", [0, 200, 333])
+def test_bits_do_not_follow_from_keys_a_row_does_not_see(capi, n_q, n_kv, dim, rows, window):      # noqa: F811
+    """Scores rise by a few powers of two along the cache, so that references
+    move; then the sequence's last key, which only the last row sees, and with
+    a window the first row's first key, get scores of another size: the other
+    rows keep their bits."""
+    held = [max(n + 5, 900 + 50 * i) for i, n in enumerate(rows)]
+    st = attn_state(n_q, n_kv, dim, rows, held, BF, seed=6)
+    level = torch.arange(max(held)).float() / max(held)
+    for bits in (6, 12, 25, 60):
+        scale = set_keys(st, level, bits, noise=0.3)
+        outs = []
+        for odd in (0.0, 2.0, -2.0):
+            for s, n in enumerate(rows):
+                at = [held[s] - 1] + ([max(held[s] - n + 1 - window, 0)] if window and n > 1 else [])
+                for key in at:
+                    st["cache"][0][st["table"][s][key // 64], :, key % 64, 0] = codes(torch.tensor(odd, device="cuda"))
+            attend(capi, st, window=window, scale=scale)
+            outs.append((st["out"].clone(), st["lse"].clone()))
+        keep = torch.ones(st["start"][-1], dtype=torch.bool)
+        for s, n in enumerate(rows):
+            keep[st["start"][s + 1] - 1] = False
+            if window and held[s] - n + 1 > window:
+                keep[st["start"][s]] = False
+            elif window:
+                keep[st["start"][s]:st["start"][s + 1]] = False
+        keep = torch.nonzero(keep).flatten().cuda()
+        for out, lse in outs[1:]:
+            assert torch.equal(out[keep], outs[0][0][keep]) and torch.equal(lse[keep], outs[0][1][keep])

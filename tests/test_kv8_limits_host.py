@@ -47,8 +47,8 @@ def test_window_and_scale_outside_their_types(capi, monkeypatch, kw, word):     
     assert e.value.code == ARG and word in str(e.value)
 
 
-def test_rotating_without_rotary_settings():
-    from block_diffusion_speculative_gather_gb300 import capi as c
+def test_rotating_without_rotary_settings(capi):      # noqa: F811
+    c = capi
     from block_diffusion_speculative_gather_gb300.runtime import PagedKV8
     kv = PagedKV8.__new__(PagedKV8)         # without its device buffers
     kv.rope = None
