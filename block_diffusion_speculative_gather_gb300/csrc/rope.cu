@@ -2,9 +2,10 @@
 // rotary dimensions of each head, the others copied.
 //
 // Angles.  f / (2 pi) is kept as a 64-bit fraction of a turn, so pos * f
-// modulo a whole turn is one integer multiply that wraps: exact to
-// pos * 2^-65 turns at any position, without the 64-bit floating point this
-// part has little of.
+// modulo a whole turn is one integer multiply that wraps, without the 64-bit
+// floating point this part has little of.  What is off is the table itself, by
+// its fp64 arithmetic (about 2^-52 of a turn, so pos * 2^-52 turns), and the
+// angle's rounding to fp32 (2^-28 turns).
 //
 // A warp takes one row and some of its heads; a lane keeps its pairs' cosines
 // and sines in registers for all heads it visits.  Bound by the rows' bytes
@@ -45,7 +46,7 @@ __global__ void rope_turns_kernel(RopeTurnsArgs a) {
 }
 
 // The turn is split exactly into a quarter and a remainder of at most an
-// eighth of a turn, so the fp32 angle is off by 2^-26 of it or less and
+// eighth of a turn, so the fp32 angle is off by 2^-28 turns or less and
 // sincospif sees no large argument.
 __device__ __forceinline__ void angle_of(unsigned long long turn, int pos, float scale, float* c, float* s) {
     const unsigned long long t = turn * (unsigned long long)(unsigned)pos;

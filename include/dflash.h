@@ -564,7 +564,11 @@ int dflash_pages_trim(int32_t* kv_len, const int32_t* new_len, int32_t S, int32_
  * are stored as code = e4m3(x / scale), round to nearest even, saturating
  * (infinities too; NaN stays NaN).  Positions behind the run are left as
  * they were.  Runs that follow one another in one page (skipped rows between
- * them, repeated slots) are done in row order.  Rows of one page stand
+ * them, repeated slots) are done in row order.  All rows of a run count for
+ * its scale, draft rows that are rejected later too, and dflash_pages_trim
+ * takes no scale back: the codes of the rows that stay can differ from those of
+ * the same rows appended one by one, by the rounding to the larger scale, and
+ * outputs over them with it.  Rows of one page stand
  * together, as dflash_pages_plan writes them: where rows of another page
  * stand between them, that page's codes are unspecified.  A slot outside the
  * pool: err {2, row}, the row is skipped.
@@ -628,9 +632,11 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache /*host*/, const dflash_kv
  * scaling LINEAR: f / factor; PARTS: with r = original_len f / (2 pi) turns
  * over the original context and g = clamp((r - alpha) / (beta - alpha), 0, 1),
  * (1 - g) f / factor + g f.  The contexts' own rotation is theta, rotary_dim
- * = head_dim, halves, no scaling.  Angles are exact at any int32 position:
- * turns [rotary_dim / 2] holds f / (2 pi) as 64-bit fractions of a turn,
- * made once by dflash_rope_turns.
+ * = head_dim, halves, no scaling.  turns [rotary_dim / 2] holds f / (2 pi) as
+ * 64-bit fractions of a turn, made once by dflash_rope_turns in fp64, each
+ * within about 2^-52 of a turn.  position * turns is exact modulo a turn and
+ * then rounded to fp32 (2^-28 turns), so an angle is off by about 2^-28 +
+ * position * 2^-52 turns at most.
  */
 enum { DFLASH_ROPE_NONE = 0, DFLASH_ROPE_LINEAR = 1, DFLASH_ROPE_PARTS = 2 };
 

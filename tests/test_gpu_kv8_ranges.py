@@ -414,3 +414,32 @@ def test_bits_do_not_follow_from_keys_a_row_does_not_see(capi, n_q, n_kv, dim, r
         keep = torch.nonzero(keep).flatten().cuda()
         for out, lse in outs[1:]:
             assert torch.equal(out[keep], outs[0][0][keep]) and torch.equal(lse[keep], outs[0][1][keep])
+
+
+# ------------------------------------------------------------------ verify's schedule and single tokens'
+
+@pytest.mark.parametrize("large", [1.0, 64.0, 2.0 ** 14])
+@pytest.mark.parametrize("off", [0, 9])
+def test_rejected_rows_leave_their_scale(capi, large, off):      # noqa: F811
+    """A run of four rows of which the last, `large` times the others, is
+    rejected, beside the first three appended one by one: each schedule's values
+    are the rows' rounded to its scale, and the run's scale is the larger one."""
+    g = torch.Generator().manual_seed(off)
+    x = torch.randn(4, 2, 64, generator=g).cuda()
+    x[3] *= large
+    made = []
+    for runs in ([range(4)], [[0], [1], [2]]):
+        cache = [torch.zeros((2, 2, 64, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        cache += [torch.full((2, 2), 2.0 ** -100, device="cuda") for _ in range(2)]
+        err = ints([0, 0])
+        for r in runs:
+            rows = x[list(r)].contiguous()
+            capi.dflash_kv8_append(rows, rows, ints([64 + off + i for i in r]), *cache, err)
+        assert err.tolist() == [0, 0]
+        sc = cache[2][1][None, :, None]
+        made.append((cache[0][1, :, off:off + 3].view(torch.float8_e4m3fn).float().transpose(0, 1) * sc, cache[2][1].clone()))
+        # later rows of the page can re-round earlier ones: twice half a step of the last scale
+        assert ((made[-1][0] - x[:3]).abs() <= 2 * torch.maximum(x[:3].abs() * 2.0 ** -4, sc * 2.0 ** -10)).all()
+    assert (made[0][1] >= made[1][1]).all()
+    if large > 1:
+        assert not torch.equal(made[0][1], made[1][1])
