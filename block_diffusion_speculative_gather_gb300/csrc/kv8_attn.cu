@@ -31,9 +31,9 @@
 // eighth full at best, and a page's work is its bytes).  A warp takes whole
 // pages, so its warps never meet inside an item, and one TMA warp keeps 11
 // (head_dim 64: 22) pages in flight, 176 KB of an SM's shared memory.  Bound by
-// DRAM at many sequences: 19 of 16384 positions, 8 kv heads of 128, 117 us =
-// 5.4 TB/s (0.80 of a measured copy; 32 of 4096 to 16384 159 us, 4.6 TB/s, as
-// the last items run alone), by latency at few: one of 1088 10.2 us, of which
+// DRAM at many sequences: 19 of 16384 positions, 8 kv heads of 128, 119 us =
+// 5.4 TB/s (0.79 of a measured copy; 32 of 4096 to 16384 159 us, 4.6 TB/s, as
+// the last items run alone), by latency at few: one of 1088 10.7 us, of which
 // the launch, finding the item, tables, pages and the fold are a chain of
 // about eight trips to memory.
 //
@@ -733,14 +733,14 @@ cudaError_t allow_smem(const void* kern) {
 // SMs have work, and a small tile's own chain is shorter.  Microseconds at 8 kv
 // heads of 128, by the smaller tile (and its items) and the larger:
 //   rows of a call          positions   smaller tile       larger
-//   1 x 32 packed                4000   16 (16 items) 16.1  64  20.7
-//   1 x 64                       4000   16 (32)       19.2  64  21.2
-//   1 x 64                      16384   16 (32)       38.1  64  31.9
-//   16 x 32                      4000   16 (256)      70.4  64  44.7
-//   1 x 256                      8000   64 (32)       29.4  128 33.0
-//   1 x 512                      8000   64 (64)       43.3  128 38.1
-//   2 x 1024                     8000   128 (128)     88.3  256 91.4
-//   2 x 2048                     8000   128 (256)    167.7  256 149.2
+//   1 x 32 packed                4000   16 (16 items) 14.6  64  20.4
+//   1 x 64                       4000   16 (32)       17.8  64  21.5
+//   1 x 64                      16384   16 (32)       37.5  64  33.8
+//   16 x 32                      4000   16 (256)      70.4  64  42.5
+//   1 x 256                      8000   64 (32)       30.9  128 33.9
+//   1 x 512                      8000   64 (64)       45.1  128 41.5
+//   2 x 1024                     8000   128 (128)     97.0  256 99.0
+//   2 x 2048                     8000   128 (256)    184.6  256 159.2
 // so 16-row tiles up to a sixth of the SMs, 64-row ones up to a quarter,
 // 128-row ones up to all of them.
 //

@@ -20,15 +20,15 @@
 // tensor core works for the other.
 //
 // Bound: a 128-key step of 128 rows takes about 1900 cycles where its MMAs
-// take 1030 (tensor pipe 38 % busy; 44 % with two tiles over the same keys).
+// take 1030 (tensor pipe 37 % busy; 41 % with two tiles over the same keys).
 // Each group waits in a chain (scores, softmax 1500 cycles, P V, the next
 // scores), shared memory moves 224 KB a step (codes in and out, f16 tiles in,
 // operands out: 1750 cycles at 128 bytes), and the roles' code together
 // exceeds the instruction cache, so what a step rarely needs is kept out of
 // its unrolled loops: masks as a pass over tensor memory before it instead of
-// selects in it took prompt chunks from 512 to 463 us.  19 sequences x 16 rows
-// x 16384 positions, 32 heads of 128: 136 us (600 TFLOP/s, 4.7 TB/s); 4 prompt
-// chunks of 2048 rows behind 6000: 464 us (980 TFLOP/s).  An item also costs
+// selects in it took a tenth off prompt chunks.  19 sequences x 16 rows x 16384
+// positions, 32 heads of 128: 140 us (580 TFLOP/s, 4.6 TB/s); 4 ragged prompt
+// chunks of up to 2048 rows behind 6000: 496 us (910 TFLOP/s).  An item also costs
 // about 10 us beside its steps: found, its first pages brought, its sums
 // joined and written.
 //

@@ -354,7 +354,8 @@ class DFlashBatch(DFlash):
 
 class PagedKV8:
     """The 8-bit paged cache of up to S sequences of one model: `layers` pools
-    of `pages` pages over one block table, at most `rows` rows a step.
+    of `pages` pages over one block table, at most `rows` rows a step (the
+    kernels' forms are chosen for that many, whatever a step uses).
 
         kv = PagedKV8(layers, n_q, n_kv, head_dim, S, pages, max_pages, rows, rope=capi.rope_config(head_dim))
         kv.plan(q_len)                        # rows each sequence wants, -> kv.row_start, kv.positions
