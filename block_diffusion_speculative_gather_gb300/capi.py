@@ -89,6 +89,20 @@ class dflash_kv8_query(C.Structure):
                 ("scale", C.c_float)]
 
 
+class dflash_drafts(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "probs", "draft_probs", "ids", "uniform", "row_start", "kv_len", "tokens", "n_tokens",
+        "new_len")] + [
+        ("probs_row", C.c_int64), ("draft_row", C.c_int64), ("rows", C.c_int32), ("vocab", C.c_int32),
+        ("S", C.c_int32), ("pad_", C.c_int32)]
+
+
+class dflash_evict(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "table", "kv_len", "weights", "weights_out", "budget", "new_len", "dropped", "source")] + [
+        ("S", C.c_int32), ("max_pages", C.c_int32), ("keep_first", C.c_int32), ("keep_last", C.c_int32)]
+
+
 class dflash_rope_config(C.Structure):
     _fields_ = [("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("scaling", C.c_int32),
                 ("original_len", C.c_int32), ("theta", C.c_double), ("factor", C.c_double),
@@ -154,6 +168,13 @@ def _load() -> C.CDLL:
         "dflash_rope_turns": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp]),
         "dflash_rope": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp, i32, i32, i32,
                                   vp, vp, vp]),
+        "dflash_probs": (C.c_int, [vp, i64, i32, vp, vp, i32, i32, vp, i64, vp]),
+        "dflash_verify_workspace_bytes": (sz, [i32, i32]),
+        "dflash_verify_drafts": (C.c_int, [vp, vp, sz, vp, vp]),
+        "dflash_kv8_weigh": (C.c_int, [vp, vp, vp, vp, i32, i32, vp, vp]),
+        "dflash_kv8_evict_workspace_bytes": (sz, [i32, i32]),
+        "dflash_kv8_evict": (C.c_int, [vp, i32, vp, vp, sz, vp, vp]),
+        "dflash_pages_shift": (C.c_int, [vp, vp, vp, i32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -176,7 +197,9 @@ EXPORTED = ("dflash_workspace_bytes", "dflash_kv_target_bytes", "dflash_kv_draft
             "dflash_batch_draft", "dflash_batch_verify_accept", "dflash_batch_set_logits_out",
             "dflash_batch_check", "dflash_batch_destroy", "dflash_pages_plan", "dflash_pages_trim",
             "dflash_kv8_append", "dflash_kv8_workspace_bytes", "dflash_kv8_attention",
-            "dflash_rope_turns", "dflash_rope")
+            "dflash_rope_turns", "dflash_rope", "dflash_probs", "dflash_verify_workspace_bytes",
+            "dflash_verify_drafts", "dflash_kv8_weigh", "dflash_kv8_evict_workspace_bytes",
+            "dflash_kv8_evict", "dflash_pages_shift")
 
 
 def check(rc: int) -> None:
@@ -453,6 +476,8 @@ _MOST = 0x7fffffff
 _CACHE = struct.Struct("4Q4i")        # dflash_kv8_cache
 _QUERY = struct.Struct("6Q4q7if")     # dflash_kv8_query
 _HEADS = struct.Struct("2Q2i4q")      # dflash_heads
+_DRAFTS = struct.Struct("9Q2q4i")     # dflash_drafts
+_EVICT = struct.Struct("8Q4i")        # dflash_evict
 
 
 def _raw(stream, dev: int) -> int:
@@ -732,5 +757,281 @@ def dflash_rope(cfg: dflash_rope_config, turns, positions, x, out, x2=None, out2
                                                  os2[0], os2[1])
     rc = lib.dflash_rope(C.byref(cfg), turns.data_ptr(), positions.data_ptr(), rows, hd, _KINDS[kind], first,
                          second, _raw(stream, dev))
+    if rc:
+        check(rc)
+
+
+# ---- sampled tokens
+
+def _need_rows(t, name: str, dtypes, shape) -> None:
+    """A [rows][vocab] tensor by its row stride: contiguous tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: a torch tensor is required")
+    if t.dtype not in dtypes:
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2 or any(e is not None and e != d for e, d in zip(shape, t.shape)):
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise DFlashError(DFLASH_ERR_ARG, f"{name}: the tokens of a row must be contiguous")
+
+
+def dflash_probs(logits, temperature, out, min_p=None, stream=None):
+    """out[r] = softmax(logits[r] / temperature[r]) over the tokens that min_p[r]
+    leaves (temperature 0: 1 at the first maximum); logits [rows][vocab] fp32,
+    bf16 or f16 by row stride, out fp32 (may be fp32 logits)."""
+    try:
+        dev = _current(logits)
+        shape = logits.shape
+        rows, vocab = shape
+        kind, xs, ps = logits.dtype, logits.stride(), out.stride()
+        fine = (kind in _KINDS and out.dtype is _F32 and out.shape == shape and xs[1] == 1 and ps[1] == 1 and
+                out.get_device() == dev and temperature.shape == (rows,) and _flat((temperature,), dev, _F32) and
+                (min_p is None or (min_p.shape == (rows,) and _flat((min_p,), dev, _F32))))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _need_rows(logits, "logits", _KINDS, (None, None))
+        rows, vocab = logits.shape
+        _need_rows(out, "out", (_F32,), (rows, vocab))
+        _need(temperature, "temperature", (_F32,), (rows,))
+        if min_p is not None:
+            _need(min_p, "min_p", (_F32,), (rows,))
+        _here(logits=logits, out=out, temperature=temperature, min_p=min_p)
+        dev, kind, xs, ps = logits.get_device(), logits.dtype, logits.stride(), out.stride()
+    if rows > _MOST or vocab > _MOST:
+        _counts(rows=rows, vocab=vocab)
+    rc = lib.dflash_probs(logits.data_ptr(), xs[0], _KINDS[kind], temperature.data_ptr(),
+                          None if min_p is None else min_p.data_ptr(), rows, vocab, out.data_ptr(), ps[0],
+                          _raw(stream, dev))
+    if rc:
+        check(rc)
+
+
+def dflash_verify_workspace_bytes(S: int, vocab: int) -> int:
+    return lib.dflash_verify_workspace_bytes(S, vocab)
+
+
+def dflash_verify_drafts(probs, ids, uniform, row_start, tokens, n_tokens, workspace, err, draft_probs=None,
+                         kv_len=None, new_len=None, stream=None):
+    """Accept or refuse the drafts ids[r] (rows behind each sequence's first)
+    against probs [rows][vocab] and draw each sequence's last token, from
+    uniform [rows]; draft_probs None: certain drafts.  Writes tokens [rows],
+    n_tokens [S] and, with kv_len, new_len [S]."""
+    try:
+        dev = _current(probs)
+        shape = probs.shape
+        rows, vocab = shape
+        (S,) = n_tokens.shape
+        one, ps = (rows,), probs.stride()
+        qs = ps if draft_probs is None else draft_probs.stride()
+        fine = (probs.dtype is _F32 and ps[1] == 1 and qs[1] == 1 and ids.shape == one and tokens.shape == one and
+                uniform.shape == one and row_start.shape == (S + 1,) and err.shape == (2,) and
+                _flat((ids, tokens, row_start, n_tokens, err), dev) and _flat((uniform,), dev, _F32) and
+                workspace.get_device() == dev and workspace.is_contiguous() and
+                (draft_probs is None or (draft_probs.dtype is _F32 and draft_probs.shape == shape and
+                                         draft_probs.get_device() == dev)) and
+                (kv_len is None) == (new_len is None) and
+                (kv_len is None or (kv_len.shape == (S,) and new_len.shape == (S,) and _flat((kv_len, new_len), dev))))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _need_rows(probs, "probs", (_F32,), (None, None))
+        rows, vocab = probs.shape
+        i32 = (_I32,)
+        _need(n_tokens, "n_tokens", i32, (None,))
+        S = n_tokens.shape[0]
+        if draft_probs is not None:
+            _need_rows(draft_probs, "draft_probs", (_F32,), (rows, vocab))
+        _need(ids, "ids", i32, (rows,))
+        _need(tokens, "tokens", i32, (rows,))
+        _need(uniform, "uniform", (_F32,), (rows,))
+        _need(row_start, "row_start", i32, (S + 1,))
+        if (kv_len is None) != (new_len is None):
+            raise DFlashError(DFLASH_ERR_ARG, "kv_len and new_len go together")
+        if kv_len is not None:
+            _need(kv_len, "kv_len", i32, (S,))
+            _need(new_len, "new_len", i32, (S,))
+        _need(workspace, "workspace", None, None)
+        _need(err, "err", i32, (2,))
+        _here(probs=probs, draft_probs=draft_probs, ids=ids, uniform=uniform, row_start=row_start, tokens=tokens,
+              n_tokens=n_tokens, workspace=workspace, err=err, kv_len=kv_len, new_len=new_len)
+        dev, ps = probs.get_device(), probs.stride()
+        qs = ps if draft_probs is None else draft_probs.stride()
+    if rows > _MOST or vocab > _MOST or S > _MOST:
+        _counts(rows=rows, vocab=vocab, S=S)
+    args = _DRAFTS.pack(probs.data_ptr(), 0 if draft_probs is None else draft_probs.data_ptr(), ids.data_ptr(),
+                        uniform.data_ptr(), row_start.data_ptr(), 0 if kv_len is None else kv_len.data_ptr(),
+                        tokens.data_ptr(), n_tokens.data_ptr(), 0 if new_len is None else new_len.data_ptr(),
+                        ps[0], qs[0], rows, vocab, S, 0)
+    rc = lib.dflash_verify_drafts(args, workspace.data_ptr(), workspace.nbytes, err.data_ptr(), _raw(stream, dev))
+    if rc:
+        check(rc)
+
+
+# ---- eviction from the 8-bit paged cache
+
+def dflash_kv8_weigh(q, lse, k_codes, v_codes, k_scale, v_scale, table, kv_len, row_start, weights, err, count=None,
+                     observe=0, fresh=False, scale=None, causal=True, window=0, stream=None):
+    """weights[page][offset] += the attention weight that the counted rows of q
+    [rows][n_q][head_dim] give each cached position; lse fp32 [rows][n_q] as
+    dflash_kv8_attention wrote it, weights fp32 [n_pages][64]; count int32 [S]:
+    the first rows that count, observe: the last of those (0: all); fresh: the
+    step's own positions start from 0."""
+    try:
+        dev = _current(k_codes)
+        cshape = k_codes.shape
+        n_pages, n_kv, _, _ = cshape
+        shape = q.shape
+        rows, n_q, hd = shape
+        S, max_pages = table.shape
+        kind, qs = q.dtype, q.stride()
+        fine = (kind in _HALVES and hd == cshape[3] and qs[2] == 1 and q.get_device() == dev and
+                kv_len.shape == (S,) and row_start.shape == (S + 1,) and err.shape == (2,) and
+                _flat((table, kv_len, row_start, err), dev) and lse.shape == shape[:2] and
+                weights.shape == (n_pages, KV8_PAGE) and _flat((lse, weights), dev, _F32) and
+                _cache_ok(cshape, k_codes, v_codes, k_scale, v_scale, dev) and
+                (count is None or (count.shape == (S,) and _flat((count,), dev))))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _need_cache(k_codes, v_codes, k_scale, v_scale)
+        n_pages, n_kv, _, hd = k_codes.shape
+        _need_heads(q, "q", _HALVES, (None, None, hd))
+        rows, n_q, _ = q.shape
+        i32 = (_I32,)
+        _need(table, "table", i32, (None, None))
+        S, max_pages = table.shape
+        _need(kv_len, "kv_len", i32, (S,))
+        _need(row_start, "row_start", i32, (S + 1,))
+        _need(lse, "lse", (_F32,), (rows, n_q))
+        _need(weights, "weights", (_F32,), (n_pages, KV8_PAGE))
+        if count is not None:
+            _need(count, "count", i32, (S,))
+        _need(err, "err", i32, (2,))
+        _here(q=q, lse=lse, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, table=table,
+              kv_len=kv_len, row_start=row_start, weights=weights, err=err, count=count)
+        dev, kind, qs = q.get_device(), q.dtype, q.stride()
+    if n_pages > _MOST or rows > _MOST or S > _MOST or max_pages > _MOST:
+        _counts(n_pages=n_pages, rows=rows, S=S, max_pages=max_pages)
+    if not 0 <= observe <= _MOST:
+        raise DFlashError(DFLASH_ERR_ARG, f"observe {observe!r}: 0 or a number of rows (an int32)")
+    cache = _CACHE.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        n_pages, n_kv, hd, 0)
+    try:
+        args = _QUERY.pack(q.data_ptr(), 0, lse.data_ptr(), table.data_ptr(), kv_len.data_ptr(),
+                           row_start.data_ptr(), qs[0], qs[1], 0, 0, rows, n_q, S, max_pages, _KINDS[kind],
+                           1 if causal else 0, window, hd ** -0.5 if scale is None else scale)
+    except struct.error as e:
+        raise DFlashError(DFLASH_ERR_ARG, f"window {window!r} (an int32), scale {scale!r} (a number): {e}") from None
+    rc = lib.dflash_kv8_weigh(cache, args, weights.data_ptr(), None if count is None else count.data_ptr(), observe,
+                              1 if fresh else 0, err.data_ptr(), _raw(stream, dev))
+    if rc:
+        check(rc)
+
+
+class kv8_layers:
+    """The pools of a model's layers, [(k_codes, v_codes, k_scale, v_scale), ..],
+    all of one shape on one device, checked and packed once for
+    dflash_kv8_evict.  Holds the tensors."""
+
+    def __init__(self, caches):
+        self.caches = [tuple(c) for c in caches]
+        if not self.caches:
+            raise DFlashError(DFLASH_ERR_ARG, "layers: at least one")
+        shape = None
+        for c in self.caches:
+            if len(c) != 4:
+                raise DFlashError(DFLASH_ERR_ARG, "layers: (k_codes, v_codes, k_scale, v_scale) each")
+            _need_cache(*c)
+            shape = shape or c[0].shape
+            if c[0].shape != shape:
+                raise DFlashError(DFLASH_ERR_ARG, f"layers: shapes {tuple(shape)} and {tuple(c[0].shape)}")
+        _on_gpu(**{f"layer {i} {n}": t for i, c in enumerate(self.caches)
+                   for n, t in zip(("k_codes", "v_codes", "k_scale", "v_scale"), c)})
+        self.n_pages, self.n_kv, _, self.head_dim = shape
+        _counts(n_pages=self.n_pages)
+        self.device = self.caches[0][0].get_device()
+        self.packed = b"".join(_CACHE.pack(*(t.data_ptr() for t in c), self.n_pages, self.n_kv, self.head_dim, 0)
+                               for c in self.caches)
+
+
+def dflash_kv8_evict_workspace_bytes(S: int, max_pages: int) -> int:
+    return lib.dflash_kv8_evict_workspace_bytes(S, max_pages)
+
+
+def dflash_kv8_evict(layers, table, kv_len, weights, budget, new_len, source, workspace, err, weights_out=None,
+                     dropped=None, keep_first=0, keep_last=0, stream=None):
+    """Sequences above their budget [S] keep their first and last positions and
+    the heaviest of the others, moved down in order in every layer of `layers`
+    (a kv8_layers) and in weights_out (None: in place); new_len [S] and source
+    [S][max_pages * 64] say what stayed, dropped [S] grows by what went.
+    dflash_pages_trim(kv_len, new_len, ..) takes the pages back."""
+    weights_out = weights if weights_out is None else weights_out
+    try:
+        dev = _current(table)
+        S, max_pages = table.shape
+        one, plane = (S,), (layers.n_pages, KV8_PAGE)
+        fine = (layers.device == dev and kv_len.shape == one and budget.shape == one and new_len.shape == one and
+                source.shape == (S, max_pages * KV8_PAGE) and weights.shape == plane and weights_out.shape == plane and
+                err.shape == (2,) and _flat((table, kv_len, budget, new_len, source, err), dev) and
+                _flat((weights, weights_out), dev, _F32) and workspace.get_device() == dev and
+                workspace.is_contiguous() and (dropped is None or (dropped.shape == one and _flat((dropped,), dev))))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        if not isinstance(layers, kv8_layers):
+            raise DFlashError(DFLASH_ERR_ARG, "layers: a kv8_layers is required")
+        i32 = (_I32,)
+        _need(table, "table", i32, (None, None))
+        S, max_pages = table.shape
+        for name, t in (("kv_len", kv_len), ("budget", budget), ("new_len", new_len)):
+            _need(t, name, i32, (S,))
+        if dropped is not None:
+            _need(dropped, "dropped", i32, (S,))
+        _need(source, "source", i32, (S, max_pages * KV8_PAGE))
+        _need(weights, "weights", (_F32,), (layers.n_pages, KV8_PAGE))
+        _need(weights_out, "weights_out", (_F32,), (layers.n_pages, KV8_PAGE))
+        _need(workspace, "workspace", None, None)
+        _need(err, "err", i32, (2,))
+        _here(k_codes=layers.caches[0][0], table=table, kv_len=kv_len, budget=budget, new_len=new_len, source=source,
+              weights=weights, weights_out=weights_out, workspace=workspace, err=err, dropped=dropped)
+        dev = table.get_device()
+    if S > _MOST or max_pages > _MOST:
+        _counts(S=S, max_pages=max_pages)
+    try:
+        args = _EVICT.pack(table.data_ptr(), kv_len.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+                           budget.data_ptr(), new_len.data_ptr(), 0 if dropped is None else dropped.data_ptr(),
+                           source.data_ptr(), S, max_pages, keep_first, keep_last)
+    except struct.error as e:
+        raise DFlashError(DFLASH_ERR_ARG, f"keep_first {keep_first!r}, keep_last {keep_last!r} (int32): {e}") from None
+    rc = lib.dflash_kv8_evict(layers.packed, len(layers.caches), args, workspace.data_ptr(), workspace.nbytes,
+                              err.data_ptr(), _raw(stream, dev))
+    if rc:
+        check(rc)
+
+
+def dflash_pages_shift(positions, row_start, dropped, out, stream=None):
+    """out[r] = positions[r] + dropped[sequence of r] (-1 stays): where to rotate
+    a step's rows behind evictions; a sequence that begins at position 0 has its
+    dropped set to 0."""
+    try:
+        dev = _current(positions)
+        (rows,), (S,) = positions.shape, dropped.shape
+        fine = (out.shape == (rows,) and row_start.shape == (S + 1,) and _flat((positions, row_start, dropped, out), dev))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        i32 = (_I32,)
+        _need(positions, "positions", i32, (None,))
+        _need(dropped, "dropped", i32, (None,))
+        rows, S = positions.shape[0], dropped.shape[0]
+        _need(row_start, "row_start", i32, (S + 1,))
+        _need(out, "out", i32, (rows,))
+        _here(positions=positions, row_start=row_start, dropped=dropped, out=out)
+        dev = positions.get_device()
+    if rows > _MOST or S > _MOST:
+        _counts(rows=rows, S=S)
+    rc = lib.dflash_pages_shift(positions.data_ptr(), row_start.data_ptr(), dropped.data_ptr(), rows, S,
+                                out.data_ptr(), _raw(stream, dev))
     if rc:
         check(rc)

@@ -116,6 +116,58 @@ int launch_kv8_attention(const CUtensorMap& k_map, const CUtensorMap& v_map, con
                          int form, int head_dim, int sms, cudaStream_t s);
 int launch_kv8_attention_tc(const CUtensorMap& k_map, const CUtensorMap& v_map, const Kv8AttnArgs& a,
                             int head_dim, int sms, cudaStream_t s);
+struct Kv8WeighArgs {
+    const void* q;
+    const float* lse;           // [rows][n_q]
+    long long q_row, q_head;
+    const uint8_t* k_codes;
+    const float* k_scale;
+    const int* table;
+    const int* kv_len;
+    const int* row_start;
+    const int* count;           // [S] or NULL
+    float* weights;             // [n_pages][64]
+    int rows, S, n_q, n_kv, group, max_pages, n_pages, dtype;
+    int causal, window, observe, fresh;
+    float scale_log2;
+    int* err;
+};
+int launch_kv8_weigh(const Kv8WeighArgs& a, int head_dim, cudaStream_t s);
+
+constexpr int KV8_LAYERS = 32;  // of one launch: the kernel arguments hold their pools' addresses
+struct Kv8MoveLayers {
+    uint8_t* k_codes[KV8_LAYERS];
+    uint8_t* v_codes[KV8_LAYERS];
+    float* k_scale[KV8_LAYERS];
+    float* v_scale[KV8_LAYERS];
+    int n;
+};
+struct Kv8EvictArgs {
+    const int* table;
+    const int* kv_len;
+    const float* weights;
+    float* weights_out;         // may be weights
+    const int* budget;
+    int* new_len;
+    int* dropped;               // [S] or NULL
+    int* source;                // [S][max_pages * 64]
+    int* from;                  // the same as slots
+    int* first_moved;           // [S] first position that holds another than before; new_len: none
+    int S, max_pages, n_pages, n_kv, keep_first, keep_last;
+    int* err;
+};
+// `choose`: with the choice (the first launch of a call), else the move of more layers.
+int launch_kv8_evict(const Kv8EvictArgs& a, const Kv8MoveLayers& l, bool choose, int head_dim, cudaStream_t s);
+
+struct PagesShiftArgs {
+    const int* positions;
+    const int* row_start;
+    int* dropped;
+    int* out;
+    int rows, S;
+};
+int launch_pages_shift(const PagesShiftArgs& a, cudaStream_t s);
+
 // The largest dynamic shared memory, allowed once per kernel and device.
 cudaError_t allow_smem(const void* kern);
 

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int KV8_MAX_SEQS = 4096;        // a lane of an attention CTA's finding warp scans S / 32 of them
 constexpr int KV8_MAX_PAGES = 1 << 25;    // slots are int32
+constexpr int KV8_EVICT_PAGES = 1 << 24;  // positions, and a step beyond, are int32
 constexpr int MAX_COUNT = 1 << 30;        // rows or sequences: sums of two of them, and a step beyond, are int32
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -271,6 +272,112 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
     a.err = err;
     return launched(launch_kv8_attention(k_map, v_map, a, plan.form, hd, sms, reinterpret_cast<cudaStream_t>(stream)),
                     "cache attention");
+}
+
+int dflash_kv8_weigh(const dflash_kv8_cache* cache, const dflash_kv8_query* q, float* weights, const int32_t* count,
+                     int32_t observe, int32_t fresh, int32_t* err, dflash_stream_t stream) {
+    if (const int r = check_cache(cache)) return r;
+    if (!q || !weights || !aligned(weights, 16) || !err || !aligned(err, 8))
+        return report_error(DFLASH_ERR_ARG, "NULL or misaligned argument");
+    if (const int r = check_attn_shape(q->rows, q->S, q->n_q, cache->n_kv, cache->head_dim, q->max_pages)) return r;
+    if (q->dtype != DFLASH_BF16 && q->dtype != DFLASH_F16)
+        return report_error(DFLASH_ERR_ARG, "dtype %d: BF16 or F16", q->dtype);
+    if (!(q->scale > 0.f) || !std::isfinite(q->scale * 1.4426950408889634f) || q->window < 0 || observe < 0)
+        return report_error(DFLASH_ERR_ARG, "scale %g (above 0) window %d observe %d", (double)q->scale, q->window,
+                            observe);
+    if (q->rows == 0) return DFLASH_OK;
+    if (!q->q || !q->lse || !q->table || !q->kv_len || !q->row_start) return report_error(DFLASH_ERR_ARG, "NULL argument");
+    if (!aligned(q->q, 16) || q->q_row % 8 || q->q_head % 8 || !aligned(q->lse, 4))
+        return report_error(DFLASH_ERR_ARG, "q: 16-byte aligned rows of every head");
+    if (const int r = pending()) return r;
+    Kv8WeighArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = q->q;
+    a.lse = q->lse;
+    a.q_row = q->q_row;
+    a.q_head = q->q_head;
+    a.k_codes = cache->k_codes;
+    a.k_scale = cache->k_scale;
+    a.table = q->table;
+    a.kv_len = q->kv_len;
+    a.row_start = q->row_start;
+    a.count = count;
+    a.weights = weights;
+    a.rows = q->rows;
+    a.S = q->S;
+    a.n_q = q->n_q;
+    a.n_kv = cache->n_kv;
+    a.group = q->n_q / cache->n_kv;
+    a.max_pages = q->max_pages;
+    a.n_pages = cache->n_pages;
+    a.dtype = q->dtype == DFLASH_BF16 ? 1 : 2;
+    a.causal = q->causal != 0;
+    a.window = q->window;
+    a.observe = observe;
+    a.fresh = fresh != 0;
+    a.scale_log2 = q->scale * 1.4426950408889634f;
+    a.err = err;
+    return launched(launch_kv8_weigh(a, cache->head_dim, reinterpret_cast<cudaStream_t>(stream)), "cache weigh");
+}
+
+size_t dflash_kv8_evict_workspace_bytes(int32_t S, int32_t max_pages) {
+    if (S < 1 || S > KV8_MAX_SEQS || max_pages < 1 || max_pages > KV8_EVICT_PAGES) {
+        report_error(DFLASH_ERR_CONFIG, "S %d (1 to %d) max_pages %d (1 to 2^24)", S, KV8_MAX_SEQS, max_pages);
+        return 0;
+    }
+    return ((size_t)S * max_pages * KV8_PAGE + S) * sizeof(int);
+}
+
+int dflash_kv8_evict(const dflash_kv8_cache* layers, int32_t n_layers, const dflash_evict* e, void* workspace,
+                     size_t workspace_bytes, int32_t* err, dflash_stream_t stream) {
+    if (!layers || !e || !workspace || !aligned(workspace, 256) || !err || !aligned(err, 8))
+        return report_error(DFLASH_ERR_ARG, "NULL or misaligned argument");
+    if (n_layers < 1 || n_layers > 1024) return report_error(DFLASH_ERR_ARG, "%d layers: 1 to 1024", n_layers);
+    for (int i = 0; i < n_layers; ++i) {
+        if (const int r = check_cache(layers + i)) return r;
+        if (layers[i].n_pages != layers[0].n_pages || layers[i].n_kv != layers[0].n_kv ||
+            layers[i].head_dim != layers[0].head_dim)
+            return report_error(DFLASH_ERR_CONFIG, "layer %d: another shape than layer 0", i);
+    }
+    const size_t need = dflash_kv8_evict_workspace_bytes(e->S, e->max_pages);
+    if (need == 0) return DFLASH_ERR_CONFIG;
+    if (!e->table || !e->kv_len || !e->weights || !e->weights_out || !e->budget || !e->new_len || !e->source)
+        return report_error(DFLASH_ERR_ARG, "NULL argument");
+    if (e->new_len == e->kv_len) return report_error(DFLASH_ERR_ARG, "new_len is kv_len: the move needs both");
+    if (e->keep_first < 0 || e->keep_last < 0)
+        return report_error(DFLASH_ERR_ARG, "keep_first %d keep_last %d", e->keep_first, e->keep_last);
+    if (workspace_bytes < need) return report_error(DFLASH_ERR_ARG, "workspace %zu < %zu", workspace_bytes, need);
+    if (const int r = pending()) return r;
+    const dflash_kv8_cache& c = layers[0];
+    int* ws = static_cast<int*>(workspace);
+    Kv8EvictArgs a{e->table, e->kv_len, e->weights, e->weights_out, e->budget, e->new_len, e->dropped, e->source,
+                   ws + e->S, ws, e->S, e->max_pages, c.n_pages, c.n_kv, e->keep_first, e->keep_last, err};
+    for (int i = 0; i < n_layers; i += KV8_LAYERS) {
+        Kv8MoveLayers l;
+        memset(&l, 0, sizeof l);
+        l.n = n_layers - i < KV8_LAYERS ? n_layers - i : KV8_LAYERS;
+        for (int j = 0; j < l.n; ++j) {
+            l.k_codes[j] = layers[i + j].k_codes;
+            l.v_codes[j] = layers[i + j].v_codes;
+            l.k_scale[j] = layers[i + j].k_scale;
+            l.v_scale[j] = layers[i + j].v_scale;
+        }
+        const int r = launched(launch_kv8_evict(a, l, i == 0, c.head_dim, reinterpret_cast<cudaStream_t>(stream)),
+                               "cache eviction");
+        if (r) return r;
+    }
+    return DFLASH_OK;
+}
+
+int dflash_pages_shift(const int32_t* positions, const int32_t* row_start, int32_t* dropped, int32_t rows, int32_t S,
+                       int32_t* out, dflash_stream_t stream) {
+    if (!row_start || !dropped || (rows > 0 && (!positions || !out))) return report_error(DFLASH_ERR_ARG, "NULL argument");
+    if (S < 1 || S > MAX_COUNT || rows < 0 || rows > MAX_COUNT)
+        return report_error(DFLASH_ERR_ARG, "S %d rows %d out of range", S, rows);
+    if (rows == 0) return DFLASH_OK;
+    if (const int r = pending()) return r;
+    PagesShiftArgs a{positions, row_start, dropped, out, rows, S};
+    return launched(launch_pages_shift(a, reinterpret_cast<cudaStream_t>(stream)), "position shift");
 }
 
 }  // extern "C"

@@ -1,0 +1,44 @@
+// Sampled decoding: launch arguments of the probability and verification kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace dfl {
+
+struct ProbsArgs {
+    const void* x;              // logits [rows][vocab]
+    long long x_row, p_row;     // elements between rows
+    const float* temperature;   // [rows]
+    const float* min_p;         // [rows] or NULL
+    float* p;
+    int rows, vocab, dtype;     // dtype 0 fp32, 1 bf16, 2 f16
+};
+int launch_probs(const ProbsArgs& a, cudaStream_t s);
+
+constexpr int VERIFY_MAX_SEQS = 65535;
+constexpr int VERIFY_MAX_VOCAB = 1 << 24;
+constexpr int VERIFY_CHUNK = 4096;       // tokens of a CTA
+// tickets first, at the same place in every call, so that calls of different
+// shapes can share a workspace: none's sums lie where another counts
+constexpr size_t VERIFY_TICKET_BYTES = 65536 * sizeof(int);
+
+struct VerifyArgs {
+    const float* p;             // [rows][vocab]
+    const float* q;             // [rows][vocab] or NULL: drafts are certain
+    long long p_row, q_row;
+    const int* ids;
+    const float* u;
+    const int* row_start;
+    const int* kv_len;          // [S] or NULL
+    int* tokens;
+    int* n_tokens;
+    int* new_len;               // [S] or NULL
+    int* tickets;               // [S], zero between calls
+    double* part;               // [S][chunks] sums of weights
+    int rows, vocab, S, chunks;
+    int wide;                   // rows of p and q are 16-byte aligned
+    int* err;
+};
+int launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
+
+}  // namespace dfl

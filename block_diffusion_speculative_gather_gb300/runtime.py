@@ -365,12 +365,25 @@ class PagedKV8:
             out = kv.attend(i, q, k, v)       # appends k and v, then attends
         kv.trim(new_len)                      # rejected rows; 0 ends a sequence
 
+    With `vocab`, drafts are verified by given random numbers; with `evict`, the
+    attention that positions get is accumulated and the cache bounded by it:
+
+        kv.plan(q_len)
+        for i in range(layers):
+            kv.rotate(q, k)                   # at true positions, whatever was evicted before
+            out = kv.attend(i, q, k, v, lse=lse)
+            kv.weigh(i, q, lse)
+        tokens, n = kv.accept(probs, ids, uniform, draft_probs)
+        kv.trim()                             # to the lengths that `accept` left
+        kv.evict(budget, keep_first=4, keep_last=256)
+
     Everything stays on the device, on the current stream (with the lengths
     in `q_len` and `new_len` a step can be captured in a graph); `check`
     raises what the kernels reported."""
 
     def __init__(self, layers: int, n_q: int, n_kv: int, head_dim: int, S: int, pages: int, max_pages: int,
-                 rows: int, rope: Optional[capi.dflash_rope_config] = None, device: str = "cuda"):
+                 rows: int, rope: Optional[capi.dflash_rope_config] = None, device: str = "cuda", vocab: int = 0,
+                 evict: bool = False):
         self.S, self.rows = S, rows
         with torch.cuda.device(torch.device(device)):
             size = capi.dflash_kv8_workspace_bytes(rows, S, n_q, n_kv, head_dim, max_pages)
@@ -392,6 +405,23 @@ class PagedKV8:
             if rope is not None:
                 self.turns = torch.zeros(rope.rotary_dim // 2, dtype=torch.int64, device="cuda")
                 capi.dflash_rope_turns(rope, self.turns)
+            self.tokens = self.weights = None
+            if vocab:
+                size = capi.dflash_verify_workspace_bytes(S, vocab)
+                if size == 0:
+                    capi.check(-1)
+                self.tokens, self.n_tokens = torch.full((rows,), -1, **i32), torch.zeros(S, **i32)
+                self.verify_workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
+            if evict:
+                size = capi.dflash_kv8_evict_workspace_bytes(S, max_pages)
+                if size == 0:
+                    capi.check(-1)
+                self.layers = capi.kv8_layers(self.caches)
+                self.weights = torch.zeros(pages, capi.KV8_PAGE, device="cuda")
+                self.budget, self.kept, self.dropped = (torch.zeros(S, **i32) for _ in range(3))
+                self.source = torch.full((S, max_pages * capi.KV8_PAGE), -1, **i32)
+                self.angles = torch.full((rows,), -1, **i32)
+                self.evict_workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
             torch.cuda.synchronize()
 
     def _set(self, buf: torch.Tensor, lens):
@@ -404,12 +434,16 @@ class PagedKV8:
             self._set(self.q_len, q_len)
         capi.dflash_pages_plan(self.kv_len, self.q_len, self.free, self.n_free, self.table, self.row_start,
                                self.positions, self.slots, self.kv_len, self.n_free)
+        if self.weights is not None:
+            capi.dflash_pages_shift(self.positions, self.row_start, self.dropped, self.angles)
 
     def rotate(self, q: torch.Tensor, k: torch.Tensor):
-        """Rotary positions of the step's rows, in place."""
+        """Rotary positions of the step's rows, in place: with `evict` their
+        true ones, which evictions do not change."""
         if self.rope is None:
             raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without rope: no rotary settings")
-        capi.dflash_rope(self.rope, self.turns, self.positions, q, q, k, k)
+        positions = self.positions if getattr(self, "weights", None) is None else self.angles
+        capi.dflash_rope(self.rope, self.turns, positions, q, q, k, k)
 
     def attend(self, layer: int, q, k, v, out=None, lse=None, scale=None, causal=True, window=0):
         """Append the step's rows to a layer's pool, attend over it."""
@@ -419,6 +453,40 @@ class PagedKV8:
         capi.dflash_kv8_attention(q, *cache, self.table, self.kv_len, self.row_start, out, self.workspace, self.err,
                                   lse=lse, scale=scale, causal=causal, window=window)
         return out
+
+    def weigh(self, layer: int, q, lse, count=None, observe=0, fresh=None, scale=None, causal=True, window=0):
+        """Add the attention that the step's rows gave each cached position of a
+        layer (lse as `attend` left it) to `self.weights`; `fresh` (by default in
+        layer 0) starts the step's own positions from 0."""
+        if self.weights is None:
+            raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without evict: no weights")
+        capi.dflash_kv8_weigh(q, lse, *self.caches[layer], self.table, self.kv_len, self.row_start, self.weights,
+                              self.err, count=count, observe=observe, fresh=layer == 0 if fresh is None else fresh,
+                              scale=scale, causal=causal, window=window)
+
+    def accept(self, probs, ids, uniform, draft_probs=None):
+        """Verify the step's drafts and draw each sequence's last token:
+        -> tokens [rows], n_tokens [S].  The lengths that stay are left in
+        `self.new_len`, for `trim`."""
+        if self.tokens is None:
+            raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without vocab: nothing to verify with")
+        capi.dflash_verify_drafts(probs, ids, uniform, self.row_start, self.tokens, self.n_tokens,
+                                  self.verify_workspace, self.err, draft_probs=draft_probs, kv_len=self.kv_len,
+                                  new_len=self.new_len)
+        return self.tokens, self.n_tokens
+
+    def evict(self, budget=None, keep_first=0, keep_last=0):
+        """Cut sequences of more than budget[s] positions (None: as
+        `self.budget` stands; 0 leaves a sequence alone) to their first, last
+        and heaviest ones, and take the pages back."""
+        if self.weights is None:
+            raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without evict: no weights")
+        if budget is not None:
+            self._set(self.budget, budget)
+        capi.dflash_kv8_evict(self.layers, self.table, self.kv_len, self.weights, self.budget, self.kept, self.source,
+                              self.evict_workspace, self.err, dropped=self.dropped, keep_first=keep_first,
+                              keep_last=keep_last)
+        capi.dflash_pages_trim(self.kv_len, self.kept, self.free, self.n_free, self.table)
 
     def trim(self, new_len=None):
         """Shorten sequences to new_len[s] where that is smaller (None: as
@@ -433,6 +501,8 @@ class PagedKV8:
         if code:
             self.err.zero_()          # report once, then clear
             self.workspace.zero_()    # a kernel that gave up may have left counters set
+            if getattr(self, "tokens", None) is not None:
+                self.verify_workspace.zero_()
             if code == 1:
                 raise capi.DFlashError(-6, f"bounded wait expired (site {where})")
             raise capi.DFlashError(-5, f"cache kernels: index out of range (at {where})")

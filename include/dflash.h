@@ -663,6 +663,147 @@ int dflash_rope(const dflash_rope_config* cfg /*host*/, const uint64_t* turns, c
                 int32_t rows, int32_t head_dim, int32_t dtype, const dflash_heads* a /*host*/,
                 const dflash_heads* b /*host*/, dflash_stream_t stream);
 
+/* ---- sampled tokens ----------------------------------------------------- */
+
+/*
+ * Probabilities of rows of logits (dtype F32, BF16 or F16):
+ *   probs[r][v] = w_v / sum w, w_v = exp((x_v - m) / T), m the row's maximum,
+ * T = temperature[r]; T = 0: 1 at the first maximum, else 0 (greedy).  With
+ * min_p (NULL: none) only tokens with w_v >= min_p[r] count (x_v >= m + T ln
+ * min_p in 64 bits, that border rounded up to fp32); a min_p of 0 or less and
+ * NaN cut nothing, one above 1 leaves the maxima.  NaN logits count as -inf; the
+ * holders of +inf share their row; a row without a logit above -inf gets zeros.
+ * Weights below 2^-126 of the largest are 0.  A row whose temperature is
+ * negative or not finite is left as it was.  logits_row and probs_row:
+ * elements between rows, tokens contiguous; at any alignment of the types (rows
+ * that are 16-byte aligned together are faster).  fp32 probabilities may be
+ * written over their logits (same address and row).  The sampled counterpart of
+ * the round's argmax; no counterpart in the source pages, which decode greedily.
+ * Errors: ARG, CUDA.
+ */
+int dflash_probs(const void* logits, int64_t logits_row, int32_t dtype, const float* temperature,
+                 const float* min_p, int32_t rows, int32_t vocab, float* probs, int64_t probs_row,
+                 dflash_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities from given
+ * random numbers (the sampled form of first-mismatch acceptance; greedy rows
+ * are probabilities of 0 and 1).  Sequence s has rows r0 = row_start[s] ..
+ * row_start[s+1] - 1 of the step, n of them: the pending token, then its drafts.
+ * probs[r] is the target's distribution of the token behind row r; ids[r] the
+ * token of row r (of a sequence's first row it is not read), negative: no draft
+ * there; draft_probs[r] the distribution that ids[r] was drawn from (a
+ * sequence's first row is not read), NULL: every draft was certain.
+ *   Draft i (row r0 + i, i >= 1) is accepted where uniform[r0+i] *
+ * draft_probs[r0+i][ids[r0+i]] < probs[r0+i-1][ids[r0+i]]; a = the drafts before
+ * the first that is not.  The last token is the first v with w_0 + .. + w_v >
+ * uniform[r0] * sum w, w = probs[r0+a], after a refused draft max(probs[r0+a] -
+ * draft_probs[r0+a+1], 0) (certain drafts: probs[r0+a] without the draft; where
+ * that has no weight probs[r0+a]).  A uniform number of 1 or more, or NaN, draws the last token
+ * with weight, a negative one the first.  Probabilities need not be normalised;
+ * negative and NaN ones, and those of 2^100 or more, count as 0.
+ *   tokens [rows]: the a accepted drafts and the last token at rows r0 ..,
+ * -1 in the sequence's rows behind; rows in no sequence are not written.
+ * n_tokens [S] = a + 1, the rows that stay; new_len [S] (NULL: not wanted)
+ * = kv_len[s] - (n - 1 - a), for dflash_pages_trim.  A row without weight
+ * draws no token: n_tokens is a, tokens -1 (new_len as above).  A sequence of no rows: 0 tokens, its
+ * length.  So a sequence of one row draws one token.
+ * vocab up to 2^24, S up to 65535, any number of rows a sequence.
+ * Workspace: dflash_verify_workspace_bytes, 256-byte aligned, zero-filled before its first use
+ * (completed calls leave its counters at zero); calls of any shapes can share
+ * one that is large enough for each, but must not overlap on the GPU.
+ * err: device int32[2], zero before the first call: an id of vocab or above (no
+ * draft there) writes {2, row}, row starts outside the rows {2, sequence} (that
+ * sequence gets 0 tokens); the first error stays until the caller clears it.
+ * Results are the same on every run.  Errors: CONFIG, ARG, CUDA.
+ */
+typedef struct {
+    const float* probs;         /* [rows][vocab], tokens contiguous */
+    const float* draft_probs;   /* [rows][vocab] or NULL */
+    const int32_t* ids;         /* [rows] */
+    const float* uniform;       /* [rows], [0, 1) */
+    const int32_t* row_start;   /* [S + 1] */
+    const int32_t* kv_len;      /* [S]; NULL with new_len */
+    int32_t* tokens;            /* [rows] */
+    int32_t* n_tokens;          /* [S] */
+    int32_t* new_len;           /* [S] or NULL; may be kv_len */
+    int64_t probs_row, draft_row;
+    int32_t rows, vocab, S, pad_;
+} dflash_drafts;
+
+size_t dflash_verify_workspace_bytes(int32_t S, int32_t vocab);
+int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_t workspace_bytes,
+                         int32_t* err, dflash_stream_t stream);
+
+/* ---- eviction from the 8-bit paged cache -------------------------------- */
+
+/*
+ * Accumulated attention weight of the cached positions, for dflash_kv8_evict:
+ *   weights[slot of j] += sum over rows i and q heads h of exp(scale * q_ih . k_j - lse_ih)
+ * over the rows that see position j (masks as in dflash_kv8_attention, whose lse
+ * this takes; q->out is not used).  Of a sequence's rows the first count[s]
+ * count (NULL: all; below 0: none), of those with observe > 0 the last `observe`: after
+ * verification count = n_tokens leaves rejected rows out, and a long prompt's last rows stand
+ * for it.  fresh 1: the step's own positions (every row's) start from 0 (the
+ * first layer's call of a step; the others add).  weights: fp32 [n_pages]
+ * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  All kv_len
+ * positions' terms are added in one fixed order, without atomics; a sequence's results do not depend on the
+ * others.  A position's NaN code makes its own weight NaN; codes that no counted row
+ * sees do not matter.  A row whose lse is -inf or NaN adds nothing.
+ * Shapes, strides and types as dflash_kv8_attention; err {2, site} for lengths and pages out of range, whose
+ * sequence (page) is left out.
+ * Errors: CONFIG, ARG, CUDA.
+ */
+int dflash_kv8_weigh(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_query* q /*host*/, float* weights,
+                     const int32_t* count, int32_t observe, int32_t fresh, int32_t* err, dflash_stream_t stream);
+
+/*
+ * Eviction: sequence s keeps budget[s] of its kv_len[s] positions where it has
+ * more (a budget of 0 or less: it is left alone): the last keep_last (at most
+ * the budget), the first keep_first (of what is left of it), and the heaviest of
+ * those between by weights (equal ones: the lowest positions; NaN below all).
+ * What stays moves down in order to positions 0 .. budget - 1, in the pools of
+ * all n_layers layers (one table; all of one shape) and in weights_out (may be
+ * weights; only kept positions are written).  A page's scale becomes the largest
+ * of the scales that its positions came with, codes with a smaller one are
+ * rounded to it (nearest even); pages whose positions stay where they are do
+ * not change.  source [S][max_pages * DFLASH_KV8_PAGE]: the earlier position of
+ * each kept one, the rest is left as it was; new_len [S] = the positions kept (not kv_len);
+ * dropped [S] (NULL: not wanted) grows by those that went.  kv_len and table do not change:
+ * dflash_pages_trim with new_len takes the pages back.  Later rows attend over what is left; the
+ * kept keys hold their true rotary positions, so new rows are rotated at the
+ * cache's position + dropped (dflash_pages_shift), and masks (causal, window) count cached positions.
+ * Pages belong to one sequence each.  Workspace: any contents, not shared by calls that overlap.
+ * err {2, site}: a length or page out of range; that sequence is left alone
+ * (new_len = kv_len).  S up to 4096, max_pages up to 2^24.  Errors: CONFIG, ARG, CUDA.
+ */
+typedef struct {
+    const int32_t* table;       /* [S][max_pages] */
+    const int32_t* kv_len;      /* [S] */
+    const float* weights;       /* [n_pages][DFLASH_KV8_PAGE] */
+    float* weights_out;         /* the same shape */
+    const int32_t* budget;      /* [S] */
+    int32_t* new_len;           /* [S], not kv_len */
+    int32_t* dropped;           /* [S] or NULL */
+    int32_t* source;            /* [S][max_pages * DFLASH_KV8_PAGE] */
+    int32_t S, max_pages, keep_first, keep_last;
+} dflash_evict;
+
+size_t dflash_kv8_evict_workspace_bytes(int32_t S, int32_t max_pages);
+int dflash_kv8_evict(const dflash_kv8_cache* layers /*host [n_layers]*/, int32_t n_layers,
+                     const dflash_evict* e /*host*/, void* workspace, size_t workspace_bytes, int32_t* err,
+                     dflash_stream_t stream);
+
+/*
+ * True positions of a step's rows behind evictions, for dflash_rope:
+ * out[r] = positions[r] + dropped[s] for the rows of sequence s, -1 where
+ * positions[r] is negative.  A sequence whose first row is at position 0 begins
+ * anew: its dropped[s] becomes 0.  positions and row_start as dflash_pages_plan
+ * writes them; out may be positions.  Errors: ARG, CUDA.
+ */
+int dflash_pages_shift(const int32_t* positions, const int32_t* row_start, int32_t* dropped, int32_t rows,
+                       int32_t S, int32_t* out, dflash_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
