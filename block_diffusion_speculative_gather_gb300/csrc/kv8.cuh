@@ -132,7 +132,7 @@ struct Kv8WeighArgs {
     float scale_log2;
     int* err;
 };
-int launch_kv8_weigh(const Kv8WeighArgs& a, int head_dim, cudaStream_t s);
+int launch_kv8_weigh(const Kv8WeighArgs& a, int head_dim, int sms, cudaStream_t s);
 
 constexpr int KV8_LAYERS = 32;  // of one launch: the kernel arguments hold their pools' addresses
 struct Kv8MoveLayers {

@@ -317,7 +317,9 @@ int dflash_kv8_weigh(const dflash_kv8_cache* cache, const dflash_kv8_query* q, f
     a.fresh = fresh != 0;
     a.scale_log2 = q->scale * 1.4426950408889634f;
     a.err = err;
-    return launched(launch_kv8_weigh(a, cache->head_dim, reinterpret_cast<cudaStream_t>(stream)), "cache weigh");
+    int sms = 0;
+    if (const int r = sm_count(&sms)) return r;
+    return launched(launch_kv8_weigh(a, cache->head_dim, sms, reinterpret_cast<cudaStream_t>(stream)), "cache weigh");
 }
 
 size_t dflash_kv8_evict_workspace_bytes(int32_t S, int32_t max_pages) {

@@ -748,8 +748,7 @@ int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_
  * first layer's call of a step; the others add).  weights: fp32 [n_pages]
  * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  All kv_len
  * positions' terms are added in one fixed order, without atomics; a sequence's results do not depend on the
- * others.  A position's NaN code makes its own weight NaN; codes that no counted row
- * sees do not matter.  A row whose lse is -inf or NaN adds nothing.
+ * others.  Scores that are NaN (a NaN code) add nothing, nor does a row whose lse is -inf or NaN.
  * Shapes, strides and types as dflash_kv8_attention; err {2, site} for lengths and pages out of range, whose
  * sequence (page) is left out.
  * Errors: CONFIG, ARG, CUDA.
