@@ -13,11 +13,11 @@ struct ProbsArgs {
     float* p;
     int rows, vocab, dtype;     // dtype 0 fp32, 1 bf16, 2 f16
 };
-int launch_probs(const ProbsArgs& a, cudaStream_t s);
+int launch_probs(const ProbsArgs& a, int sms, cudaStream_t s);
 
 constexpr int VERIFY_MAX_SEQS = 65535;
 constexpr int VERIFY_MAX_VOCAB = 1 << 24;
-constexpr int VERIFY_CHUNK = 4096;       // tokens of a CTA
+constexpr int VERIFY_UNIT = 512;         // tokens that a warp sums at a time
 // tickets first, at the same place in every call, so that calls of different
 // shapes can share a workspace: none's sums lie where another counts
 constexpr size_t VERIFY_TICKET_BYTES = 65536 * sizeof(int);
@@ -34,11 +34,11 @@ struct VerifyArgs {
     int* n_tokens;
     int* new_len;               // [S] or NULL
     int* tickets;               // [S], zero between calls
-    double* part;               // [S][chunks] sums of weights
-    int rows, vocab, S, chunks;
+    float2* part;               // [S][units] sums of weights, each as two fp32 numbers
+    int rows, vocab, S, units;
     int wide;                   // rows of p and q are 16-byte aligned
     int* err;
 };
-int launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
+int launch_verify_drafts(const VerifyArgs& a, int sms, cudaStream_t s);
 
 }  // namespace dfl

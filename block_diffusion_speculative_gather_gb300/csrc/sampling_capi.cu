@@ -25,7 +25,14 @@ int pending() {
                                            cudaGetErrorString(e));
 }
 
-int chunks_of(int vocab) { return (vocab + VERIFY_CHUNK - 1) / VERIFY_CHUNK; }
+int units_of(int vocab) { return (vocab + VERIFY_UNIT - 1) / VERIFY_UNIT; }
+
+int sm_count(int* sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return e == cudaSuccess ? DFLASH_OK : report_error(DFLASH_ERR_CUDA, "SM count: %s", cudaGetErrorString(e));
+}
 
 }  // namespace
 
@@ -50,7 +57,9 @@ int dflash_probs(const void* logits, int64_t logits_row, int32_t dtype, const fl
     if (const int r = pending()) return r;
     ProbsArgs a{logits, logits_row, probs_row, temperature, min_p, probs, rows, vocab,
                 dtype == DFLASH_F32 ? 0 : (dtype == DFLASH_BF16 ? 1 : 2)};
-    return launched(launch_probs(a, reinterpret_cast<cudaStream_t>(stream)), "probabilities");
+    int sms = 0;
+    if (const int r = sm_count(&sms)) return r;
+    return launched(launch_probs(a, sms, reinterpret_cast<cudaStream_t>(stream)), "probabilities");
 }
 
 size_t dflash_verify_workspace_bytes(int32_t S, int32_t vocab) {
@@ -58,7 +67,7 @@ size_t dflash_verify_workspace_bytes(int32_t S, int32_t vocab) {
         report_error(DFLASH_ERR_CONFIG, "S %d (1 to %d) vocab %d (1 to 2^24)", S, VERIFY_MAX_SEQS, vocab);
         return 0;
     }
-    return VERIFY_TICKET_BYTES + (size_t)S * chunks_of(vocab) * sizeof(double);
+    return VERIFY_TICKET_BYTES + (size_t)S * units_of(vocab) * sizeof(float2);
 }
 
 int dflash_verify_drafts(const dflash_drafts* d, void* workspace, size_t workspace_bytes, int32_t* err,
@@ -91,15 +100,17 @@ int dflash_verify_drafts(const dflash_drafts* d, void* workspace, size_t workspa
     a.n_tokens = d->n_tokens;
     a.new_len = d->new_len;
     a.tickets = static_cast<int*>(workspace);
-    a.part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + VERIFY_TICKET_BYTES);
+    a.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + VERIFY_TICKET_BYTES);
     a.rows = d->rows;
     a.vocab = d->vocab;
     a.S = d->S;
-    a.chunks = chunks_of(d->vocab);
+    a.units = units_of(d->vocab);
     a.wide = d->vocab % 4 == 0 && aligned(d->probs, 16) && aligned(d->draft_probs, 16) && d->probs_row % 4 == 0 &&
              d->draft_row % 4 == 0;
     a.err = err;
-    return launched(launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream)), "draft verification");
+    int sms = 0;
+    if (const int r = sm_count(&sms)) return r;
+    return launched(launch_verify_drafts(a, sms, reinterpret_cast<cudaStream_t>(stream)), "draft verification");
 }
 
 }  // extern "C"

@@ -13,10 +13,10 @@
 // of terms: differences are taken exactly (two fp32 numbers each), sums are kept
 // as pairs of fp32 numbers within a warp and in fp64 above, in a fixed order.
 //
-// Only one row of p and q is read whole.  A CTA takes 4096 tokens of it (and
-// finds by itself, from two numbers a draft, which row that is); the last of a
-// sequence's CTAs finds the 4096 tokens that u_0 falls into and reads them again.
-// No CTA waits for another.
+// Only one row of p and q is read whole.  Its tokens are dealt in units of 512 to
+// warps (each CTA finds by itself, from two numbers a draft, which row that is),
+// a unit's sum goes to memory, and the last of a sequence's CTAs finds the unit
+// that u_0 falls into and reads it again.  No CTA waits for another.
 
 #include "sampling.cuh"
 
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int VT = 256;                        // threads
 constexpr int VW = VT / 32;
-constexpr int PER = VERIFY_CHUNK / VT;         // tokens of a thread
+constexpr int PER = VERIFY_UNIT / 32;          // tokens of a lane
 
 // A sum as hi + lo, |lo| below half a step of hi.
 struct Pair {
@@ -112,65 +112,80 @@ struct Row {
     int certain;        // but for this token (-1: none), which has no weight
 };
 
+// The lane's k-th token of a unit: in order of k / 4 (k), then of lanes.
 template <bool WIDE>
-__device__ __forceinline__ int token_of(int base, int k) {
-    return WIDE ? base + (k / 4) * (VT * 4) + threadIdx.x * 4 + k % 4 : base + k * VT + threadIdx.x;
+__device__ __forceinline__ int token_of(int unit, int k) {
+    const int lane = threadIdx.x & 31;
+    return unit * VERIFY_UNIT + (WIDE ? (k / 4) * 128 + lane * 4 + k % 4 : k * 32 + lane);
 }
 
-// Weights of the thread's tokens of a chunk, in the order of token_of.
-template <bool WIDE>
-__device__ __forceinline__ void load_chunk(const Row& r, int vocab, int base, Pair (&w)[PER]) {
+struct Tokens {
     float p[PER], q[PER];
+};
+
+template <bool WIDE, bool Q>
+__device__ __forceinline__ void load_unit(const Row& r, int vocab, int unit, Tokens& t) {
     if (WIDE) {
 #pragma unroll
         for (int k = 0; k < PER; k += 4) {
-            const int v = token_of<true>(base, k);
+            const int v = token_of<true>(unit, k);
             const bool in = v < vocab;          // vocab is a multiple of 4
             const float4 x = in ? *reinterpret_cast<const float4*>(r.p + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-            p[k] = x.x, p[k + 1] = x.y, p[k + 2] = x.z, p[k + 3] = x.w;
+            t.p[k] = x.x, t.p[k + 1] = x.y, t.p[k + 2] = x.z, t.p[k + 3] = x.w;
+            if (!Q) continue;
             const float4 y = in && r.q ? *reinterpret_cast<const float4*>(r.q + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-            q[k] = y.x, q[k + 1] = y.y, q[k + 2] = y.z, q[k + 3] = y.w;
+            t.q[k] = y.x, t.q[k + 1] = y.y, t.q[k + 2] = y.z, t.q[k + 3] = y.w;
         }
     } else {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int v = token_of<false>(base, k);
-            p[k] = v < vocab ? r.p[v] : 0.f;
-            q[k] = v < vocab && r.q ? r.q[v] : 0.f;
+            const int v = token_of<false>(unit, k);
+            t.p[k] = v < vocab ? r.p[v] : 0.f;
+            if (Q) t.q[k] = v < vocab && r.q ? r.q[v] : 0.f;
         }
     }
-#pragma unroll
-    for (int k = 0; k < PER; ++k) w[k] = weight(token_of<WIDE>(base, k) == r.certain ? 0.f : p[k], q[k]);
 }
 
-// Sum of a chunk's weights, the same in all threads.
-template <bool WIDE>
-__device__ __forceinline__ double chunk_sum(const Row& r, int vocab, int base, double* red) {
-    Pair w[PER], s{0.f, 0.f};
-    load_chunk<WIDE>(r, vocab, base, w);
+// Weights of the tokens, and their sum over the warp (the same in all lanes).
+template <bool WIDE, bool Q>
+__device__ __forceinline__ Pair weigh_unit(const Row& r, int unit, const Tokens& t, Pair (&w)[PER]) {
+    Pair s{0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < PER; ++k) s = add(s, w[k].hi, w[k].lo);
-    s = warp_total(s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = value(s);
-    __syncthreads();
-    double t = 0.0;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) t += red[i];
-    return t;
+    for (int k = 0; k < PER; ++k) {
+        if (Q) w[k] = weight(t.p[k], t.q[k]);
+        else w[k] = {token_of<WIDE>(unit, k) == r.certain ? 0.f : clean(t.p[k]), 0.f};
+        s = add(s, w[k].hi, w[k].lo);
+    }
+    return warp_total(s);
 }
 
-// First token of the chunk whose running sum, from `before` on, passes `goal`;
-// -1: none.  Its last token with weight where `last` is set.
-template <bool WIDE>
-__device__ int find_token(const Row& r, int vocab, int base, double before, double goal, bool last, double* red,
-                          int* s_v) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int STEP = WIDE ? 4 : 1;        // tokens of a thread that stand together
+// By a warp: sums of units `unit`, unit + step, .. into part.  The next unit is on
+// its way while one is summed.
+template <bool WIDE, bool Q>
+__device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int unit, int step, float2* part) {
+    Tokens t;
+    if (unit < a.units) load_unit<WIDE, Q>(r, a.vocab, unit, t);
+    for (; unit < a.units; unit += step) {
+        const Tokens now = t;
+        if (unit + step < a.units) load_unit<WIDE, Q>(r, a.vocab, unit + step, t);
+        Pair w[PER];
+        const Pair s = weigh_unit<WIDE, Q>(r, unit, now, w);
+        if ((threadIdx.x & 31) == 0) __stcg(part + unit, make_float2(s.hi, s.lo));
+    }
+}
+
+// By a warp: the first token of the unit whose running sum, from `before` on,
+// passes `goal`, else its last token with weight (a running sum can fall short of
+// the unit's by its last bits); -1: it has none.
+template <bool WIDE, bool Q>
+__device__ int find_token(const VerifyArgs& a, const Row& r, int unit, double before, double goal) {
+    const int lane = threadIdx.x & 31;
+    constexpr int STEP = WIDE ? 4 : 1;        // tokens of a lane that stand together
+    Tokens t;
     Pair w[PER];
-    load_chunk<WIDE>(r, vocab, base, w);
-    if (threadIdx.x == 0) *s_v = last ? -1 : 0x7fffffff;
-    __syncthreads();
+    load_unit<WIDE, Q>(r, a.vocab, unit, t);
+    weigh_unit<WIDE, Q>(r, unit, t, w);
+    int first = 0x7fffffff, last = -1;
 #pragma unroll
     for (int k = 0; k < PER; k += STEP) {
         double own = 0.0;
@@ -182,118 +197,148 @@ __device__ int find_token(const Row& r, int vocab, int base, double before, doub
             const double x = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += x;
         }
-        if (lane == 31) red[warp] = inc;
-        __syncthreads();
-        double run = before;
-        for (int i = 0; i < warp; ++i) run += red[i];
-        for (int i = 0; i < VW; ++i) before += red[i];
-        run += inc - own;
+        double run = before + (inc - own);
+        before += __shfl_sync(0xffffffffu, inc, 31);
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
             run += value(w[k + j]);
             if (w[k + j].hi > 0.f) {
-                if (last) atomicMax(s_v, token_of<WIDE>(base, k + j));
-                else if (run > goal) atomicMin(s_v, token_of<WIDE>(base, k + j));
+                const int v = token_of<WIDE>(unit, k + j);
+                last = max(last, v);
+                if (run > goal) first = min(first, v);
             }
         }
-        __syncthreads();
     }
-    const int v = *s_v;
-    __syncthreads();
-    return v == 0x7fffffff ? -1 : v;
+    first = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    return first != 0x7fffffff ? first : last;
 }
 
-// The last token of a row whose chunks' sums are `part`; -1: it has no weight.
-template <bool WIDE>
-__device__ int draw(const VerifyArgs& a, const Row& r, const double* part, float u, double* red, int* s_v) {
-    __shared__ double s_total, s_before;
-    __shared__ int s_c, s_end;
-    if (threadIdx.x == 0) {
-        double total = 0.0;
-        int end = -1;
-        for (int c = 0; c < a.chunks; ++c) {
-            const double x = __ldcg(part + c);
-            total += x;
-            if (x > 0.0) end = c;
-        }
-        const double goal = (double)u * total;
-        double run = 0.0;
-        int at = -1;
-        for (int c = 0; c < a.chunks && at < 0; ++c) {
-            const double x = __ldcg(part + c);
-            if (x > 0.0 && run + x > goal) at = c;
-            else run += x;
-        }
-        s_total = total;
-        s_before = run;
-        s_c = at;
-        s_end = end;
+__device__ __forceinline__ double unit_sum(const float2* p) {
+    const float2 s = __ldcg(p);
+    return value(Pair{s.x, s.y});
+}
+
+// By the whole CTA: the token that u draws from a row whose units' sums are
+// `part`; -1: it has no weight.
+template <bool WIDE, bool Q>
+__device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float u, double* red, int* s_v) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // each thread a run of units
+    const int per = (a.units + VT - 1) / VT, b0 = tid * per, b1 = min(b0 + per, a.units);
+    double own = 0.0;
+    int end = -1;                      // last unit with weight
+    for (int c = b0; c < b1; ++c) {
+        const double x = unit_sum(part + c);
+        own += x;
+        if (x > 0.0) end = c;
+    }
+    double inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) red[warp] = inc;
+    if (tid == 0) s_v[0] = 0x7fffffff, s_v[1] = -1;
+    __syncthreads();
+    double total = 0.0, before = 0.0;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) {
+        if (i < warp) before += red[i];
+        total += red[i];
+    }
+    const double goal = (double)u * total;
+    before += inc - own;
+    // the first run that passes the goal, and in it the first unit
+    if (end >= 0) {
+        atomicMax(s_v + 1, end);
+        if (before + own > goal) atomicMin(s_v, tid);
     }
     __syncthreads();
-    const double goal = (double)u * s_total, before = s_before;
-    const int at = s_c, end = s_end;
+    const int at = s_v[0], last = s_v[1];
     __syncthreads();
-    if (end < 0) return -1;
-    int v = -1;
-    // a running sum can fall short of the chunk's by its last bits: then the
-    // token is the chunk's last one with weight
-    if (at >= 0) v = find_token<WIDE>(r, a.vocab, at * VERIFY_CHUNK, before, goal, false, red, s_v);
-    if (v < 0) v = find_token<WIDE>(r, a.vocab, (at >= 0 ? at : end) * VERIFY_CHUNK, 0.0, 0.0, true, red, s_v);
+    if (last < 0) return -1;
+    if (at == 0x7fffffff ? warp == 0 : warp == at / 32) {
+        int unit = last;
+        double run = 0.0, g = INFINITY;            // past the goal: the last token with weight
+        if (at != 0x7fffffff) {
+            unit = end;
+            run = before;
+            g = goal;
+            for (int c = b0; c < b1; ++c) {        // in the lane whose run it is
+                const double x = unit_sum(part + c);
+                if (x > 0.0) {
+                    unit = c;
+                    if (run + x > goal) break;
+                    if (c < end) run += x;
+                }
+            }
+            unit = __shfl_sync(0xffffffffu, unit, at % 32);
+            run = __shfl_sync(0xffffffffu, run, at % 32);
+        }
+        const int v = find_token<WIDE, Q>(a, r, unit, run, g);
+        if (lane == 0) s_v[0] = v;
+    }
+    __syncthreads();
+    const int v = s_v[0];
+    __syncthreads();
     return v;
 }
 
-template <bool WIDE>
-__global__ void __launch_bounds__(VT) verify_kernel(VerifyArgs a) {
+template <bool WIDE, bool Q>
+__global__ void __launch_bounds__(VT, Q ? 3 : 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ double red[VW];
-    __shared__ int s_v, s_last;
+    __shared__ int s_v[2], s_last;
     __shared__ Verdict s_verdict;
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, s = blockIdx.y, chunk = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, s = blockIdx.y;
     const int r0 = a.row_start[s], n = a.row_start[s + 1] - r0;
     const bool fine = r0 >= 0 && n >= 0 && r0 + n <= a.rows;
     if (!fine || n == 0) {
-        if (chunk == 0 && tid == 0) {
+        if (blockIdx.x == 0 && tid == 0) {
             if (!fine) report(a.err, s);
             a.n_tokens[s] = 0;
             if (a.new_len) a.new_len[s] = a.kv_len[s];
         }
         return;
     }
-    if (tid < 32) {
-        const Verdict v = judge(a, r0, n, chunk == 0);
-        if (tid == 0) s_verdict = v;
+    Verdict ve{0, -1};
+    if (n > 1) {
+        if (tid < 32) {
+            const Verdict v = judge(a, r0, n, blockIdx.x == 0);
+            if (tid == 0) s_verdict = v;
+        }
+        __syncthreads();
+        ve = s_verdict;
     }
-    __syncthreads();
-    const Verdict ve = s_verdict;
     Row row{a.p + (long long)(r0 + ve.a) * a.p_row, nullptr, -1};
     if (ve.draft >= 0) {
-        if (a.q) row.q = a.q + (long long)(r0 + ve.a + 1) * a.q_row;
+        if (Q) row.q = a.q + (long long)(r0 + ve.a + 1) * a.q_row;
         else row.certain = ve.draft;
     }
-    double* part = a.part + (long long)s * a.chunks;
-    const double sum = chunk_sum<WIDE>(row, a.vocab, chunk * VERIFY_CHUNK, red);
-    if (tid == 0) {
-        __stcg(part + chunk, sum);
-        __threadfence();
-        s_last = atomicAdd(a.tickets + s, 1) == a.chunks - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    if (tid == 0) a.tickets[s] = 0;
+    float2* part = a.part + (long long)s * a.units;
+    sum_units<WIDE, Q>(a, row, blockIdx.x * VW + warp, gridDim.x * VW, part);
     __threadfence();
+    __syncthreads();
+    if (gridDim.x > 1) {
+        if (tid == 0) s_last = atomicAdd(a.tickets + s, 1) == (int)gridDim.x - 1;
+        __syncthreads();
+        if (!s_last) return;
+        if (tid == 0) a.tickets[s] = 0;
+        __threadfence();
+    }
     const float u = a.u[r0];
-    int v = draw<WIDE>(a, row, part, u, red, &s_v);
+    int v = draw<WIDE, Q>(a, row, part, u, red, s_v);
     if (v < 0 && ve.draft >= 0) {
         // nothing is left of p behind q: p itself
         row.q = nullptr;
         row.certain = -1;
-        for (int c = 0; c < a.chunks; ++c) {
-            const double x = chunk_sum<WIDE>(row, a.vocab, c * VERIFY_CHUNK, red);
-            if (tid == 0) __stcg(part + c, x);
-        }
+        sum_units<WIDE, Q>(a, row, warp, VW, part);
+        __threadfence();
         __syncthreads();
-        v = draw<WIDE>(a, row, part, u, red, &s_v);
+        v = draw<WIDE, Q>(a, row, part, u, red, s_v);
     }
     const int out = ve.a + (v >= 0);
     for (int i = tid; i < n; i += VT) a.tokens[r0 + i] = i < ve.a ? a.ids[r0 + i + 1] : (i == ve.a ? v : -1);
@@ -305,10 +350,19 @@ __global__ void __launch_bounds__(VT) verify_kernel(VerifyArgs a) {
 
 }  // namespace
 
-int launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
-    const dim3 grid((unsigned)a.chunks, (unsigned)a.S), block(VT);
-    return (int)(a.wide ? launch_k(verify_kernel<true>, grid, block, 0, s, a)
-                        : launch_k(verify_kernel<false>, grid, block, 0, s, a));
+int launch_verify_drafts(const VerifyArgs& a, int sms, cudaStream_t s) {
+    // a unit a warp while they are few, up to four in a row where there are many:
+    // CTAs come and go less often
+    int x = (a.units + VW - 1) / VW;
+    const long long all = (long long)x * a.S, room = 8LL * sms;
+    const int each = all >= 4 * room ? 4 : (all >= 2 * room ? 2 : 1);
+    x = (x + each - 1) / each;
+    const dim3 grid((unsigned)x, (unsigned)a.S), block(VT);
+    if (a.q)
+        return (int)(a.wide ? launch_k(verify_kernel<true, true>, grid, block, 0, s, a)
+                            : launch_k(verify_kernel<false, true>, grid, block, 0, s, a));
+    return (int)(a.wide ? launch_k(verify_kernel<true, false>, grid, block, 0, s, a)
+                        : launch_k(verify_kernel<false, false>, grid, block, 0, s, a));
 }
 
 }  // namespace dfl
