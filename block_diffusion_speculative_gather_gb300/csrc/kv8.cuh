@@ -155,6 +155,7 @@ struct Kv8EvictArgs {
     int* first_moved;           // [S] first position that holds another than before; new_len: none
     int S, max_pages, n_pages, n_kv, keep_first, keep_last;
     int* err;
+    int keys;                   // weights held in shared memory by the choice (set by the launch)
 };
 // `choose`: with the choice (the first launch of a call), else the move of more layers.
 int launch_kv8_evict(const Kv8EvictArgs& a, const Kv8MoveLayers& l, bool choose, int head_dim, cudaStream_t s);
