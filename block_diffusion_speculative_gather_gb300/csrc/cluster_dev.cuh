@@ -1,0 +1,50 @@
+// Thread-block clusters: barriers, a word of another CTA's shared memory, launch.
+#pragma once
+
+#include "common.cuh"
+
+namespace dfl {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Arrive (what the thread wrote before is seen behind the others' wait) and wait.
+// A warp whose lanes come from different branches arrives as one.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Writes the word that lies in CTA `rank` where p lies in this one.
+__device__ __forceinline__ void put_remote(void* p, uint32_t rank, uint32_t v) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// launch_k with clusters of `ranks` CTAs in a row.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster_k(void (*kern)(KArgs...), dim3 grid, dim3 block, int ranks, cudaStream_t s,
+                                    Args&&... args) {
+    set_carveout_once(reinterpret_cast<const void*>(kern));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = g_pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    ++g_launches;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+}  // namespace dfl

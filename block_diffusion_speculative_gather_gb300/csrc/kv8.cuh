@@ -158,7 +158,7 @@ struct Kv8EvictArgs {
     int keys;                   // weights held in shared memory by the choice (set by the launch)
 };
 // `choose`: with the choice (the first launch of a call), else the move of more layers.
-int launch_kv8_evict(const Kv8EvictArgs& a, const Kv8MoveLayers& l, bool choose, int head_dim, cudaStream_t s);
+int launch_kv8_evict(const Kv8EvictArgs& a, const Kv8MoveLayers& l, bool choose, int head_dim, int sms, cudaStream_t s);
 
 struct PagesShiftArgs {
     const int* positions;

@@ -350,6 +350,8 @@ int dflash_kv8_evict(const dflash_kv8_cache* layers, int32_t n_layers, const dfl
         return report_error(DFLASH_ERR_ARG, "keep_first %d keep_last %d", e->keep_first, e->keep_last);
     if (workspace_bytes < need) return report_error(DFLASH_ERR_ARG, "workspace %zu < %zu", workspace_bytes, need);
     if (const int r = pending()) return r;
+    int sms = 0;
+    if (const int r = sm_count(&sms)) return r;
     const dflash_kv8_cache& c = layers[0];
     int* ws = static_cast<int*>(workspace);
     Kv8EvictArgs a{e->table, e->kv_len, e->weights, e->weights_out, e->budget, e->new_len, e->dropped, e->source,
@@ -364,7 +366,7 @@ int dflash_kv8_evict(const dflash_kv8_cache* layers, int32_t n_layers, const dfl
             l.k_scale[j] = layers[i + j].k_scale;
             l.v_scale[j] = layers[i + j].v_scale;
         }
-        const int r = launched(launch_kv8_evict(a, l, i == 0, c.head_dim, reinterpret_cast<cudaStream_t>(stream)),
+        const int r = launched(launch_kv8_evict(a, l, i == 0, c.head_dim, sms, reinterpret_cast<cudaStream_t>(stream)),
                                "cache eviction");
         if (r) return r;
     }

@@ -8,16 +8,20 @@
 // rounded to it (powers of two: exact but where values fall below the format's
 // normal range).
 //
-// The choice: one CTA a sequence, a radix selection over the weights' bits (11, 11
-// and 10 of them), then one pass in order.  The keys lie in shared memory, up to
-// 49152 positions; those of longer sequences are looked up again in every pass.
+// The choice: one CTA a sequence.  Up to 8192 positions their weights stay in
+// registers, eight a thread, and the budget's smallest weight is found bit by bit,
+// two bits a round; longer ones take a radix selection (11, 11 and 10 bits), the
+// keys in shared memory up to 49152 positions, looked up again above.  Then one
+// pass in order.
 //
 // The move: a position only ever moves to a lower or its own place, so a page may
 // be written once the positions that go into it and into lower pages have been
-// read.  A CTA has one kv head's K or V of a sequence and layer and does its pages
-// in order, four at a time: the next four are on their way while four are
-// written, which none of them reads.
+// read.  A CTA has one kv head's K or V of a sequence and layer (or a part of its
+// dims, where they are few) and goes through the pages in order, 32 KB at a time:
+// the next ones are on their way while these are written, which none of them
+// reads.
 
+#include "cluster_dev.cuh"
 #include "gemm.cuh"
 #include "kv8.cuh"
 #include "kv8_attn_dev.cuh"
@@ -57,12 +61,57 @@ __device__ __forceinline__ int block_exclusive(int v, int* total, int* sm) {
     return (warp ? before : 0) + inc - v;
 }
 
+// The smallest key that stays of `want` (above 0) among the keys of positions
+// first .. to - 1, and how many of those that have it.
+struct Border {
+    uint32_t key;
+    int ties;
+};
+
+constexpr int HELD = 8;               // keys of a thread
+constexpr int SHORT = ST * HELD;      // positions whose keys the threads hold
+
+// key[u] is position u * ST + tid's; 0 .. 2^32 - 1 are searched two bits at a time,
+// as counts of keys at or above three borders (at most SHORT, 14 bits: two in a
+// word's halves would not do, so three words).
+__device__ __forceinline__ Border border_of_held(const uint32_t (&key)[HELD], const bool (&in)[HELD], int want, int* sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t low = 0;                 // at least `want` keys are at or above it
+    int above = 0;                    // keys above the searched range
+    for (int shift = 30; shift >= 0; shift -= 2) {
+        int c1 = 0, c2 = 0, c3 = 0;
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
+            const uint32_t d = in[u] && key[u] >= low ? (key[u] - low) >> shift : 0;   // 3 and more: above the range, too
+            c1 += d >= 1;
+            c2 += d >= 2;
+            c3 += d >= 3;
+        }
+        c1 = __reduce_add_sync(0xffffffffu, c1);
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        c3 = __reduce_add_sync(0xffffffffu, c3);
+        int* at = sm + (shift & 2) * (3 * SW / 2);      // in turn: one barrier a round
+        if (lane == 0) at[warp] = c1, at[SW + warp] = c2, at[2 * SW + warp] = c3;
+        __syncthreads();
+        c1 = __reduce_add_sync(0xffffffffu, at[lane]);
+        c2 = __reduce_add_sync(0xffffffffu, at[SW + lane]);
+        c3 = __reduce_add_sync(0xffffffffu, at[2 * SW + lane]);
+        // the highest quarter that still leaves `want`
+        if (c3 >= want) low += 3u << shift;
+        else if (c2 >= want) low += 2u << shift, above = c3;
+        else if (c1 >= want) low += 1u << shift, above = c2;
+        else above = c1;
+    }
+    return {low, want - above};
+}
+
 __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ Kv8EvictArgs a) {
-    extern __shared__ uint32_t keys[];      // [min(n, KEYS)]
-    __shared__ int hist[BINS], sm[32], s_bin, s_left, s_bad, s_moved;
+    extern __shared__ uint32_t keys[];      // [a.keys]
+    __shared__ int hist[BINS], sm[2 * 3 * SW], s_bin, s_left, s_bad, s_moved;
+    __shared__ int s_table[SHORT / KV8_PAGE];
     pdl_trigger();
     pdl_wait();
-    const int s = blockIdx.x, tid = threadIdx.x;
+    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long cap = (long long)a.max_pages * KV8_PAGE;
     const int* table = a.table + (size_t)s * a.max_pages;
     const int n = a.kv_len[s], b = a.budget[s];
@@ -73,6 +122,7 @@ __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ 
     for (int p = tid; p < pages; p += ST) {
         const int pg = table[p];
         if (pg < 0 || pg >= a.n_pages) s_bad = 1;
+        if (p < SHORT / KV8_PAGE) s_table[p] = pg;
     }
     __syncthreads();
     const int site = bad ? SITE_LEN : SITE_PAGE;
@@ -89,107 +139,182 @@ __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ 
     if (bad) return;
     int* source = a.source + (size_t)s * cap;
     int* from = a.from + (size_t)s * cap;
-    auto place = [&](int j) { return (size_t)table[j / KV8_PAGE] * KV8_PAGE + j % KV8_PAGE; };
     const int last = goes ? min(a.keep_last, b) : 0, first = goes ? min(a.keep_first, b - last) : n;
     const int want = kept - last - first;             // of positions first .. n - last - 1
-    uint32_t prefix = 0;
-    int left = want;                                  // of those with this prefix
-    if (want > 0) {
-        const int from_j = first, to_j = n - last;
-        const bool held = to_j - from_j <= a.keys;
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < BINS; i += ST) hist[i] = 0;
+    int moved = kept;
+    if (n <= SHORT) {
+        auto place = [&](int j) { return s_table[j / KV8_PAGE] * KV8_PAGE + j % KV8_PAGE; };
+        float w[HELD];
+        uint32_t key[HELD];
+        bool in[HELD], stays[HELD];
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
+            const int j = u * ST + tid;
+            w[u] = j < n ? a.weights[place(j)] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
+            const int j = u * ST + tid;
+            key[u] = key_of_weight(w[u]);
+            in[u] = j >= first && j < n - last;
+            stays[u] = j < n && !in[u];
+        }
+        if (want > 0) {
+            const Border r = border_of_held(key, in, want, sm);
+            // the first `ties` of those on the border, in order of u, then of threads
             __syncthreads();
-            for (int j0 = from_j; j0 < to_j; j0 += 4 * ST) {
-                uint32_t k[4];
+            int mine[HELD];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int j = j0 + u * ST + tid;
-                    if (j >= to_j) continue;
-                    if (held && pass) k[u] = keys[j - from_j];
-                    else k[u] = key_of_weight(a.weights[place(j)]);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int j = j0 + u * ST + tid;
-                    if (j >= to_j) continue;
-                    if (held && !pass) keys[j - from_j] = k[u];
-                    if (pass == 0 || (k[u] ^ prefix) >> (shift + bits) == 0) atomicAdd(hist + ((k[u] >> shift) & ((1 << bits) - 1)), 1);
-                }
+            for (int u = 0; u < HELD; ++u) {
+                const unsigned m = __ballot_sync(0xffffffffu, in[u] && key[u] == r.key);
+                mine[u] = __popc(m & ((1u << lane) - 1));
+                if (lane == 0) hist[u * SW + warp] = __popc(m);
             }
             __syncthreads();
-            // bins from the top: a thread has two
-            const int hi = hist[BINS - 1 - 2 * tid], lo = hist[BINS - 2 - 2 * tid];
-            int total;
-            const int above = block_exclusive(hi + lo, &total, sm);
-            if (above < left && above + hi + lo >= left) {
-                const bool top = above + hi >= left;
-                s_bin = BINS - (top ? 1 : 2) - 2 * tid;
-                s_left = left - above - (top ? 0 : hi);
+            if (warp == 0) {                          // HELD * SW counts, HELD a lane
+                int run[HELD], sum = 0;
+#pragma unroll
+                for (int u = 0; u < HELD; ++u) run[u] = hist[lane * HELD + u], sum += run[u];
+                int before = warp_inclusive(sum, lane) - sum;
+#pragma unroll
+                for (int u = 0; u < HELD; ++u) hist[lane * HELD + u] = before, before += run[u];
             }
             __syncthreads();
-            prefix |= (uint32_t)s_bin << shift;
-            left = s_left;
-        }
-    }
-    // in order: positions with larger keys, and the first `left` with this one.
-    // A thread has four in a row at a time.
-    int ties = 0, out = 0, moved = kept;
-    for (int base = 0; base < n; base += 4 * ST) {
-        float w[4];
-        bool tie[4], stays[4];
-        size_t at_slot[4];
-        int my_ties = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int j = base + 4 * tid + u;
-            tie[u] = stays[u] = false;
-            if (j >= n) continue;
-            at_slot[u] = place(j);
-            w[u] = a.weights[at_slot[u]];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int j = base + 4 * tid + u;
-            if (j >= n) continue;
-            stays[u] = j < first || j >= n - last;
-            if (!stays[u] && want > 0) {
-                const uint32_t k = key_of_weight(w[u]);
-                stays[u] = k > prefix;
-                tie[u] = k == prefix;
-                my_ties += tie[u];
+            for (int u = 0; u < HELD; ++u) {
+                if (!in[u]) continue;
+                stays[u] = key[u] > r.key || (key[u] == r.key && hist[u * SW + warp] + mine[u] < r.ties);
             }
+            __syncthreads();
         }
-        int total;
-        int rank = ties + block_exclusive(my_ties, &total, sm), mine = 0;
-        ties += total;
+        int mine[HELD];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (tie[u]) stays[u] = rank++ < left;
-            mine += stays[u];
+        for (int u = 0; u < HELD; ++u) {
+            const unsigned m = __ballot_sync(0xffffffffu, stays[u]);
+            mine[u] = __popc(m & ((1u << lane) - 1));
+            if (lane == 0) hist[u * SW + warp] = __popc(m);
         }
-        int at = out + block_exclusive(mine, &total, sm);
-        out += total;
-        // every weight of these positions has been read, here and by the others
+        __syncthreads();
+        if (warp == 0) {
+            int run[HELD], sum = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < HELD; ++u) run[u] = hist[lane * HELD + u], sum += run[u];
+            int before = warp_inclusive(sum, lane) - sum;
+#pragma unroll
+            for (int u = 0; u < HELD; ++u) hist[lane * HELD + u] = before, before += run[u];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) {
             if (!stays[u]) continue;
-            const int j = base + 4 * tid + u;
+            const int j = u * ST + tid, at = hist[u * SW + warp] + mine[u];
             source[at] = j;
-            from[at] = (int)at_slot[u];
+            from[at] = place(j);
             if (at != j) moved = min(moved, at);
             if (at != j || a.weights_out != a.weights) a.weights_out[place(at)] = w[u];
-            ++at;
+        }
+    } else {
+        auto place = [&](int j) { return (size_t)table[j / KV8_PAGE] * KV8_PAGE + j % KV8_PAGE; };
+        uint32_t prefix = 0;
+        int left = want;                              // of those with this prefix
+        if (want > 0) {
+            const int from_j = first, to_j = n - last;
+            const bool held = to_j - from_j <= a.keys;
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+                for (int i = tid; i < BINS; i += ST) hist[i] = 0;
+                __syncthreads();
+                for (int j0 = from_j; j0 < to_j; j0 += 4 * ST) {
+                    uint32_t k[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int j = j0 + u * ST + tid;
+                        if (j >= to_j) continue;
+                        if (held && pass) k[u] = keys[j - from_j];
+                        else k[u] = key_of_weight(a.weights[place(j)]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int j = j0 + u * ST + tid;
+                        if (j >= to_j) continue;
+                        if (held && !pass) keys[j - from_j] = k[u];
+                        if (pass == 0 || (k[u] ^ prefix) >> (shift + bits) == 0)
+                            atomicAdd(hist + ((k[u] >> shift) & ((1 << bits) - 1)), 1);
+                    }
+                }
+                __syncthreads();
+                // bins from the top: a thread has two
+                const int hi = hist[BINS - 1 - 2 * tid], lo = hist[BINS - 2 - 2 * tid];
+                int total;
+                const int above = block_exclusive(hi + lo, &total, sm);
+                if (above < left && above + hi + lo >= left) {
+                    const bool top = above + hi >= left;
+                    s_bin = BINS - (top ? 1 : 2) - 2 * tid;
+                    s_left = left - above - (top ? 0 : hi);
+                }
+                __syncthreads();
+                prefix |= (uint32_t)s_bin << shift;
+                left = s_left;
+            }
+        }
+        // in order: positions with larger keys, and the first `left` with this one.
+        // A thread has four in a row at a time.
+        int ties = 0, out = 0;
+        for (int base = 0; base < n; base += 4 * ST) {
+            float w[4];
+            bool tie[4], stays[4];
+            size_t at_slot[4];
+            int my_ties = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = base + 4 * tid + u;
+                tie[u] = stays[u] = false;
+                if (j >= n) continue;
+                at_slot[u] = place(j);
+                w[u] = a.weights[at_slot[u]];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = base + 4 * tid + u;
+                if (j >= n) continue;
+                stays[u] = j < first || j >= n - last;
+                if (!stays[u] && want > 0) {
+                    const uint32_t k = key_of_weight(w[u]);
+                    stays[u] = k > prefix;
+                    tie[u] = k == prefix;
+                    my_ties += tie[u];
+                }
+            }
+            int total;
+            int rank = ties + block_exclusive(my_ties, &total, sm), mine = 0;
+            ties += total;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (tie[u]) stays[u] = rank++ < left;
+                mine += stays[u];
+            }
+            int at = out + block_exclusive(mine, &total, sm);
+            out += total;
+            // every weight of these positions has been read, here and by the others
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!stays[u]) continue;
+                const int j = base + 4 * tid + u;
+                source[at] = j;
+                from[at] = (int)at_slot[u];
+                if (at != j) moved = min(moved, at);
+                if (at != j || a.weights_out != a.weights) a.weights_out[place(at)] = w[u];
+                ++at;
+            }
         }
     }
     moved = (int)__reduce_min_sync(0xffffffffu, (unsigned)moved);
-    if ((tid & 31) == 0) atomicMin(&s_moved, moved);
+    if (lane == 0) atomicMin(&s_moved, moved);
     __syncthreads();
     if (tid == 0) a.first_moved[s] = s_moved;
 }
 
-// 16 codes times a factor.
+// Four codes times a factor.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
     const uint32_t lo2 = f16_of_codes(w), hi2 = f16_of_codes(w >> 16);
     const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
@@ -203,78 +328,121 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
     return r;
 }
 
-constexpr int MT = 512;               // threads of the move
-constexpr int MP = 4;                 // pages at a time
-constexpr int MROWS = MP * KV8_PAGE;
+// The same by a power of two of at most 1, in f16: a code times 2^-15 is exact
+// there, what is below lies far under half of the format's smallest step.
+__device__ __forceinline__ uint32_t rescale4_f16(uint32_t w, __half2 f) {
+    const uint32_t lo = f16_of_codes(w), hi = f16_of_codes(w >> 16);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), f), b = __hmul2(*reinterpret_cast<const __half2*>(&hi), f);
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r) : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+    return r;
+}
 
-template <int HD>
+constexpr int MT = 512;               // threads of the move
+constexpr int MN = 4;                 // 16-byte pieces of a thread at a time
+
+// PB: bytes of a row that the CTA moves (a row, or 32 of it: the parts' CTAs are a
+// cluster, since they read the scales that the first one writes).
+template <int HD, int PB>
 __global__ void __launch_bounds__(MT, 2) kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a,
                                                          const __grid_constant__ Kv8MoveLayers l) {
-    constexpr int PER_ROW = HD / 16, N = MROWS * PER_ROW / MT;      // uint4s of a row, of a thread
-    __shared__ float s_scale[2][MROWS];
-    __shared__ float s_top[2][MROWS / 32];
+    constexpr int PER_ROW = PB / 16, ROWS = MT * MN / PER_ROW, PARTS = HD / PB, PAGES = ROWS / KV8_PAGE;
+    constexpr int EACH = (ROWS + MT - 1) / MT;                      // rows whose scales a thread looks up
+    __shared__ float s_ratio[2][ROWS];
+    __shared__ float s_top[2][ROWS / 32];
     pdl_trigger();
     pdl_wait();
-    const int s = blockIdx.x / a.n_kv, head = blockIdx.x % a.n_kv, layer = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int part = blockIdx.x % PARTS, chain = blockIdx.x / PARTS, s = chain / a.n_kv, head = chain - s * a.n_kv;
+    const int layer = blockIdx.y, which = blockIdx.z;
     const int kept = a.new_len[s], begin = a.first_moved[s];
     if (begin >= kept) return;
-    const long long cap = (long long)a.max_pages * KV8_PAGE;
-    const int* from = a.from + (size_t)s * cap;
+    const int* from = a.from + (size_t)s * ((long long)a.max_pages * KV8_PAGE);
     const int* table = a.table + (size_t)s * a.max_pages;
-    uint8_t* codes = which ? l.v_codes[layer] : l.k_codes[layer];
-    float* scale = which ? l.v_scale[layer] : l.k_scale[layer];
-    uint4 x[N], y[N];
-    int slot[N], scale_slot = 0;
-    float sc = 0.f;
+    const int c = tid % PER_ROW, r0 = tid / PER_ROW;                // this thread's piece of rows r0, r0 + MT / PER_ROW, ..
+    uint8_t* codes = (which ? l.v_codes[layer] : l.k_codes[layer]) + (size_t)head * KV8_PAGE * HD + part * PB + c * 16;
+    float* scale = (which ? l.v_scale[layer] : l.k_scale[layer]) + head;
+    const int page_rows = a.n_kv * KV8_PAGE;                        // rows of a page, all heads (slots x heads fit int32)
+    auto row_of = [&](int slot) { return (size_t)(unsigned)((slot / KV8_PAGE) * page_rows + slot % KV8_PAGE) * HD; };
+    uint4 x[MN], y[MN];
+    int slot[MN], scale_slot[EACH];
+    float sc[EACH];
     // slots of the positions d0 .. that this thread reads
     auto look = [&](int d0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int d = d0 + (i * MT + tid) / PER_ROW;
+        for (int i = 0; i < MN; ++i) {
+            const int d = d0 + r0 + i * (MT / PER_ROW);
             slot[i] = d < kept ? from[d] : -1;
         }
-        if (tid < MROWS) scale_slot = d0 + tid < kept ? from[d0 + tid] : -1;
-    };
-    auto fetch = [&](uint4 (&v)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (slot[i] >= 0) {
-                const size_t at = ((size_t)(slot[i] / KV8_PAGE) * a.n_kv + head) * KV8_PAGE + slot[i] % KV8_PAGE;
-                v[i] = reinterpret_cast<const uint4*>(codes + at * HD)[(i * MT + tid) % PER_ROW];
-            }
-        if (tid < MROWS) sc = scale_slot >= 0 ? scale[(size_t)(scale_slot / KV8_PAGE) * a.n_kv + head] : 0.f;
+        for (int e = 0; e < EACH; ++e) {
+            const int d = d0 + e * MT + tid;
+            scale_slot[e] = e * MT + tid < ROWS && d < kept ? from[d] : -1;
+        }
+    };
+    auto fetch = [&](uint4 (&v)[MN]) {
+#pragma unroll
+        for (int i = 0; i < MN; ++i)
+            if (slot[i] >= 0) v[i] = *reinterpret_cast<const uint4*>(codes + row_of(slot[i]));
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) sc[e] = scale_slot[e] >= 0 ? scale[(size_t)(scale_slot[e] / KV8_PAGE) * a.n_kv] : 0.f;
     };
     int d0 = begin / KV8_PAGE * KV8_PAGE;
     look(d0);
     fetch(x);
-    look(d0 + MROWS);
-    for (int turn = 0; d0 < kept; d0 += MROWS, turn ^= 1) {
-        if (tid < MROWS) {
-            s_scale[turn][tid] = sc;
-            const float top = warp_max(sc);
-            if ((tid & 31) == 0) s_top[turn][tid >> 5] = top;
+    look(d0 + ROWS);
+    for (int turn = 0; d0 < kept; d0 += ROWS, turn ^= 1) {
+        float own[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            own[e] = sc[e];
+            const float top = warp_max(sc[e]);
+            if (lane == 0 && e * MT + tid < ROWS) s_top[turn][(e * MT + tid) >> 5] = top;
         }
-        // these pages have been read, by every thread
-        __syncthreads();
+        // these pages have been read, by every thread (of the row's other parts, too)
+        if (PARTS > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
         fetch(y);
-        look(d0 + 2 * MROWS);
+        look(d0 + 2 * ROWS);
+        // a row's factor; -1: as it is
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int row = (i * MT + tid) / PER_ROW, d = d0 + row;
-            if (d >= kept) continue;
+        for (int e = 0; e < EACH; ++e) {
+            const int row = e * MT + tid;
+            if (row >= ROWS) continue;
             const float top = fmaxf(s_top[turn][row / KV8_PAGE * 2], s_top[turn][row / KV8_PAGE * 2 + 1]);
-            if (s_scale[turn][row] != top) {
-                const float f = s_scale[turn][row] / top;
-                x[i] = make_uint4(rescale4(x[i].x, f), rescale4(x[i].y, f), rescale4(x[i].z, f), rescale4(x[i].w, f));
-            }
-            const size_t at = ((size_t)table[d / KV8_PAGE] * a.n_kv + head) * KV8_PAGE + d % KV8_PAGE;
-            reinterpret_cast<uint4*>(codes + at * HD)[(i * MT + tid) % PER_ROW] = x[i];
+            s_ratio[turn][row] = own[e] == top ? -1.f : own[e] / top;
+            const int d = d0 + row;
+            if (part == 0 && row % KV8_PAGE == 0 && d < kept) scale[(size_t)table[d / KV8_PAGE] * a.n_kv] = top;
         }
-        if (tid < MP && d0 + tid * KV8_PAGE < kept)
-            scale[(size_t)table[d0 / KV8_PAGE + tid] * a.n_kv + head] = fmaxf(s_top[turn][2 * tid], s_top[turn][2 * tid + 1]);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = y[i];
+        for (int i = 0; i < MN; ++i) {
+            const int row = r0 + i * (MT / PER_ROW), d = d0 + row;
+            if (d >= kept) continue;
+            const float f = s_ratio[turn][row];
+            if (f != -1.f) {
+                if ((__float_as_uint(f) & 0x807fffffu) == 0) {      // a power of two (or 0)
+                    const __half2 h = __float2half2_rn(f);
+                    x[i] = make_uint4(rescale4_f16(x[i].x, h), rescale4_f16(x[i].y, h), rescale4_f16(x[i].z, h),
+                                      rescale4_f16(x[i].w, h));
+                } else {
+                    x[i] = make_uint4(rescale4(x[i].x, f), rescale4(x[i].y, f), rescale4(x[i].z, f), rescale4(x[i].w, f));
+                }
+            }
+            *reinterpret_cast<uint4*>(codes + row_of(table[d / KV8_PAGE] * KV8_PAGE + d % KV8_PAGE)) = x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < MN; ++i) x[i] = y[i];
     }
+    static_assert(PAGES >= 1 && ROWS % KV8_PAGE == 0, "whole pages at a time");
 }
 
 // True positions of a step's rows: the cache's, and those the sequence has lost.
@@ -305,7 +473,7 @@ __global__ void pages_shift_kernel(PagesShiftArgs a) {
 
 }  // namespace
 
-int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choose, int head_dim, cudaStream_t s) {
+int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choose, int head_dim, int sms, cudaStream_t s) {
     Kv8EvictArgs a = args;
     const long long cap = (long long)a.max_pages * KV8_PAGE;
     a.keys = (int)(cap < KEYS ? cap : KEYS);
@@ -315,9 +483,16 @@ int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choo
             e = launch_k(kv8_choose_kernel, dim3((unsigned)a.S), dim3(ST), (size_t)a.keys * 4, s, a);
         if (e != cudaSuccess) return (int)e;
     }
-    const dim3 grid((unsigned)(a.S * a.n_kv), (unsigned)l.n, 2), block(MT);
-    return (int)(head_dim == 128 ? launch_k(kv8_move_kernel<128>, grid, block, 0, s, a, l)
-                                 : launch_k(kv8_move_kernel<64>, grid, block, 0, s, a, l));
+    // parts of 32 bytes a row while whole rows leave SMs without work: a CTA then has
+    // that many more pages at a time
+    const bool parts = 2LL * a.S * a.n_kv * l.n < sms;
+    const int each = parts ? head_dim / 32 : 1;
+    const dim3 grid((unsigned)(a.S * a.n_kv * each), (unsigned)l.n, 2), block(MT);
+    if (head_dim == 128)
+        return (int)(parts ? launch_cluster_k(kv8_move_kernel<128, 32>, grid, block, each, s, a, l)
+                           : launch_k(kv8_move_kernel<128, 128>, grid, block, 0, s, a, l));
+    return (int)(parts ? launch_cluster_k(kv8_move_kernel<64, 32>, grid, block, each, s, a, l)
+                       : launch_k(kv8_move_kernel<64, 64>, grid, block, 0, s, a, l));
 }
 
 int launch_pages_shift(const PagesShiftArgs& a, cudaStream_t s) {

@@ -18,6 +18,7 @@
 
 #include <mutex>
 
+#include "cluster_dev.cuh"
 #include "gemm.cuh"
 #include "sampling.cuh"
 
@@ -32,7 +33,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ float no_nan(float x) { return x == x ? x : -INFINITY; }
 
-// What a row's temperature and min_p come to, by one thread: fp64 is slow here.
+// What a row's temperature and min_p come to, by one thread.
 struct RowSetup {
     float c, c_lo;        // log2(e) / T
     float cut, cut_lo;    // T ln(min_p)
@@ -40,34 +41,39 @@ struct RowSetup {
 
 __device__ __forceinline__ RowSetup setup_of(float t, float min_p) {
     RowSetup r;
-    const double c = fmin(1.4426950408889634 / (double)t, 1e38);    // no 0 * inf at the smallest T
-    r.c = (float)c;
-    r.c_lo = (float)(c - (double)r.c);
-    const double cut = min_p > 0.f ? (double)t * log((double)fminf(min_p, 1.f)) : -INFINITY;
-    r.cut = (float)cut;
-    r.cut_lo = isinf(r.cut) ? 0.f : (float)(cut - (double)r.cut);
+    r.c = fminf(1.44269502f / t, 1e38f);          // no 0 * inf at the smallest T
+    // what the quotient and log2(e)'s fp32 value leave over
+    r.c_lo = r.c < 1e38f ? (fmaf(-r.c, t, 1.44269502f) + 1.92596303e-8f) / t : 0.f;
+    r.cut = -INFINITY;
+    r.cut_lo = 0.f;
+    if (min_p > 0.f) {
+        const double cut = (double)t * log((double)fminf(min_p, 1.f));
+        r.cut = (float)cut;
+        if (r.cut > -INFINITY) r.cut_lo = (float)(cut - (double)r.cut);
+    }
     return r;
 }
 
 struct RowRule {
-    float m, border;      // maximum, smallest logit that counts
+    float m, border;      // maximum (finite), smallest logit that counts (finite)
     float c, c_lo;
 };
 
 __device__ __forceinline__ RowRule rule_of(float m, const RowSetup& u) {
-    RowRule r{m, -INFINITY, u.c, u.c_lo};
+    RowRule r{m, -3.402823466e38f, u.c, u.c_lo};
     // m + cut as s + e, exactly, then rounded up
     const float s = __fadd_rn(m, u.cut), b = __fsub_rn(s, m);
     const float e = __fadd_rn(__fsub_rn(m, __fsub_rn(s, b)), __fsub_rn(u.cut, b));
-    if (fabsf(s) < INFINITY) r.border = __fadd_ru(s, __fadd_rn(e, u.cut_lo));
+    if (s > -INFINITY) r.border = __fadd_ru(s, __fadd_rn(e, u.cut_lo));
     return r;
 }
 
+// NaN and -inf are below any border; a NaN exponent (of a difference beyond fp32)
+// is one of nothing.
 __device__ __forceinline__ float weight(const RowRule& r, float x) {
-    const float d = x == r.m ? 0.f : x - r.m;      // inf - inf
-    // -inf * c_lo may be inf: the sum's NaN is a weight of nothing
+    const float d = x - r.m;
     const float y = fmaxf(fmaf(d, r.c, d * r.c_lo), -256.f);
-    return x >= r.border && x > -INFINITY ? ex2(y) : 0.f;
+    return x >= r.border ? ex2(y) : 0.f;
 }
 
 __device__ __forceinline__ float row_min_p(const ProbsArgs& a, long long row) { return a.min_p ? a.min_p[row] : 0.f; }
@@ -77,23 +83,6 @@ __device__ __forceinline__ float row_min_p(const ProbsArgs& a, long long row) { 
 constexpr int CT = 512, CW = CT / 32;
 
 template <typename T> constexpr int per_vec() { return 16 / (int)sizeof(T); }
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// A word of another CTA's shared memory, at the place of this CTA's p.
-__device__ __forceinline__ void put_remote(void* p, uint32_t rank, uint32_t v) {
-    uint32_t at;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
 
 struct Trade {
     uint32_t warp[CW];
@@ -120,8 +109,8 @@ __device__ __forceinline__ float trade(Trade& t, float v, int ranks, uint32_t ra
     return r;
 }
 
-// K vectors of 16 bytes a thread.  WIDE: full vectors of probabilities are
-// 16-byte aligned where the logits' are.
+// K vectors of 16 bytes a thread.  The vectors begin at 16-byte boundaries of the
+// logits; the few before the first and behind the last are one more a thread.
 template <typename T, int K>
 __global__ void __launch_bounds__(CT, K * per_vec<T>() > 12 ? 2 : 3)
 probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
@@ -139,49 +128,51 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     if (ranks > 1) cluster_arrive();
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
     float* p = a.p + row * a.p_row;
-    // vectors begin at 16-byte boundaries: the first may begin before the row
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int vecs = (int)(((long long)a.vocab + off + VE - 1) / VE), per = (vecs + ranks - 1) / ranks;
-    const int v0 = (int)rank * per, v1 = min(v0 + per, vecs);
-    float w[K * VE];
+    const int head = min(off ? VE - off : 0, a.vocab);
+    const int vecs = (a.vocab - head) / VE, per = (vecs + ranks - 1) / ranks;
+    const int v0 = (int)rank * per, n = min(per, vecs - v0);      // this CTA's vectors (n may be negative)
+    const T* xv = x + head + (long long)v0 * VE;
+    float w[K * VE], extra = -INFINITY;
+    int e = -1;                                                   // the extra one's index
     {
         uint4 raw[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = v0 + k * CT + tid;
-            const int e = v * VE - off;
-            if (v < v1 && e >= 0 && e + VE <= a.vocab) raw[k] = *reinterpret_cast<const uint4*>(x + e);
+            const int v = k * CT + tid;
+            if (v < n) raw[k] = reinterpret_cast<const uint4*>(xv)[v];
         }
-        if (tid == 0) {      // while they are on their way
+        if (rank == 0) {
+            const int tail = a.vocab - head - vecs * VE;
+            if (tid < head) e = tid;
+            else if (tid >= 16 && tid < 16 + tail) e = a.vocab - tail + tid - 16;
+            if (e >= 0) extra = to_f32(x[e]);
+        }
+        if (tid == CT - 1) {      // while they are on their way
             s_setup = setup_of(t, row_min_p(a, row));
             s_best = 0x7fffffff;
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = v0 + k * CT + tid;
-            const int e = v * VE - off;
             const T* r = reinterpret_cast<const T*>(&raw[k]);
-            const bool full = v < v1 && e >= 0 && e + VE <= a.vocab;
 #pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = full ? no_nan(to_f32(r[i])) : -INFINITY;
-            if (v < v1 && !full)
-#pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (e + i >= 0 && e + i < a.vocab) w[k * VE + i] = no_nan(to_f32(x[e + i]));
+            for (int i = 0; i < VE; ++i) w[k * VE + i] = k * CT + tid < n ? to_f32(r[i]) : -INFINITY;
         }
     }
-    float m = -INFINITY;
+    float m = no_nan(extra);                       // fmaxf leaves NaN out
 #pragma unroll
     for (int i = 0; i < K * VE; ++i) m = fmaxf(m, w[i]);
     m = trade(s_max, warp_max(m), ranks, rank, true, [](float x, float y) { return fmaxf(x, y); });
     if (t == 0.f || m == -INFINITY) {
         int best = 0x7fffffff;
-        if (m != -INFINITY)
+        if (m != -INFINITY) {
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int k = K - 1; k >= 0; --k)
 #pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (w[k * VE + i] == m) best = min(best, (v0 + k * CT + tid) * VE - off + i);
+                for (int i = VE - 1; i >= 0; --i)
+                    if (w[k * VE + i] == m) best = head + (v0 + k * CT + tid) * VE + i;
+            if (extra == m) best = min(best, e);
+        }
         best = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
         if ((tid & 31) == 0) atomicMin(&s_best, best);
         __syncthreads();
@@ -195,36 +186,48 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = (v0 + k * CT + tid) * VE - off + i == best ? 1.f : 0.f;
+            for (int i = 0; i < VE; ++i) w[k * VE + i] = head + (v0 + k * CT + tid) * VE + i == best ? 1.f : 0.f;
+        extra = e == best ? 1.f : 0.f;
     } else {
-        const RowRule r = rule_of(m, s_setup);
-        float sum = 0.f;
+        float sum;
+        if (m < INFINITY) {
+            const RowRule r = rule_of(m, s_setup);
+            sum = extra = weight(r, extra);
 #pragma unroll
-        for (int i = 0; i < K * VE; ++i) {
-            w[i] = weight(r, w[i]);
-            sum += w[i];
+            for (int i = 0; i < K * VE; ++i) {
+                w[i] = weight(r, w[i]);
+                sum += w[i];
+            }
+        } else {
+            sum = extra = extra == INFINITY ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < K * VE; ++i) {
+                w[i] = w[i] == INFINITY ? 1.f : 0.f;
+                sum += w[i];
+            }
         }
         sum = trade(s_sum, warp_sum(sum), ranks, rank, false, [](float x, float y) { return x + y; });
         const float inv = 1.f / sum;
+        extra *= inv;
 #pragma unroll
         for (int i = 0; i < K * VE; ++i) w[i] *= inv;
     }
-    const bool wide = ((reinterpret_cast<uintptr_t>(p) / 4 - off) & 3) == 0;
+    if (e >= 0) p[e] = extra;
+    float* pv = p + head + (long long)v0 * VE;
+    if ((reinterpret_cast<uintptr_t>(pv) & 15) == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int v = v0 + k * CT + tid;
-        const int e = v * VE - off;
-        if (v >= v1) continue;
-        if (wide && e >= 0 && e + VE <= a.vocab) {
+        for (int k = 0; k < K; ++k)
+            if (k * CT + tid < n)
 #pragma unroll
-            for (int i = 0; i < VE; i += 4)
-                *reinterpret_cast<float4*>(p + e + i) =
-                    make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
-        } else {
+                for (int i = 0; i < VE; i += 4)
+                    reinterpret_cast<float4*>(pv)[(k * CT + tid) * (VE / 4) + i / 4] =
+                        make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (e + i >= 0 && e + i < a.vocab) p[e + i] = w[k * VE + i];
-        }
+        for (int k = 0; k < K; ++k)
+            if (k * CT + tid < n)
+#pragma unroll
+                for (int i = 0; i < VE; ++i) pv[(k * CT + tid) * VE + i] = w[k * VE + i];
     }
 }
 
@@ -265,14 +268,15 @@ __global__ void __launch_bounds__(PT) probs_rows_kernel(const __grid_constant__ 
         return;
     }
     const RowRule r = rule_of(m, s_setup);
+    auto weigh = [&](float v) { return m < INFINITY ? weight(r, v) : (v == INFINITY ? 1.f : 0.f); };
     float sum = 0.f;
-    for (int i = tid; i < a.vocab; i += PT) sum += weight(r, no_nan(to_f32(x[i])));
+    for (int i = tid; i < a.vocab; i += PT) sum += weigh(to_f32(x[i]));
     sum = warp_sum(sum);
     if (lane == 0) red[warp] = sum;
     __syncthreads();
     sum = warp_sum(red[lane]);
     const float inv = 1.f / sum;
-    for (int i = tid; i < a.vocab; i += PT) p[i] = weight(r, no_nan(to_f32(x[i]))) * inv;
+    for (int i = tid; i < a.vocab; i += PT) p[i] = weigh(to_f32(x[i])) * inv;
 }
 
 // Clusters of 16 are allowed once per kernel and device.
@@ -302,21 +306,8 @@ int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
         const cudaError_t e = allow_cluster(kern);
         if (e != cudaSuccess) return (int)e;
     }
-    set_carveout_once(kern);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.rows * ranks));
-    cfg.blockDim = dim3(CT);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = g_pdl ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)ranks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    ++g_launches;
-    return (int)cudaLaunchKernelEx(&cfg, probs_cluster_kernel<T, K>, a, ranks);
+    return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)((long long)a.rows * ranks)), dim3(CT), ranks, s,
+                                 a, ranks);
 }
 
 template <typename T>

@@ -112,11 +112,9 @@ struct Row {
     int certain;        // but for this token (-1: none), which has no weight
 };
 
-// The lane's k-th token of a unit: in order of k / 4 (k), then of lanes.
-template <bool WIDE>
+// The lane's k-th token of a unit: in order of k / 4, then of lanes, then of k.
 __device__ __forceinline__ int token_of(int unit, int k) {
-    const int lane = threadIdx.x & 31;
-    return unit * VERIFY_UNIT + (WIDE ? (k / 4) * 128 + lane * 4 + k % 4 : k * 32 + lane);
+    return unit * VERIFY_UNIT + (k / 4) * 128 + (threadIdx.x & 31) * 4 + k % 4;
 }
 
 struct Tokens {
@@ -128,7 +126,7 @@ __device__ __forceinline__ void load_unit(const Row& r, int vocab, int unit, Tok
     if (WIDE) {
 #pragma unroll
         for (int k = 0; k < PER; k += 4) {
-            const int v = token_of<true>(unit, k);
+            const int v = token_of(unit, k);
             const bool in = v < vocab;          // vocab is a multiple of 4
             const float4 x = in ? *reinterpret_cast<const float4*>(r.p + v) : make_float4(0.f, 0.f, 0.f, 0.f);
             t.p[k] = x.x, t.p[k + 1] = x.y, t.p[k + 2] = x.z, t.p[k + 3] = x.w;
@@ -139,7 +137,7 @@ __device__ __forceinline__ void load_unit(const Row& r, int vocab, int unit, Tok
     } else {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int v = token_of<false>(unit, k);
+            const int v = token_of(unit, k);
             t.p[k] = v < vocab ? r.p[v] : 0.f;
             if (Q) t.q[k] = v < vocab && r.q ? r.q[v] : 0.f;
         }
@@ -147,13 +145,13 @@ __device__ __forceinline__ void load_unit(const Row& r, int vocab, int unit, Tok
 }
 
 // Weights of the tokens, and their sum over the warp (the same in all lanes).
-template <bool WIDE, bool Q>
+template <bool Q>
 __device__ __forceinline__ Pair weigh_unit(const Row& r, int unit, const Tokens& t, Pair (&w)[PER]) {
     Pair s{0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         if (Q) w[k] = weight(t.p[k], t.q[k]);
-        else w[k] = {token_of<WIDE>(unit, k) == r.certain ? 0.f : clean(t.p[k]), 0.f};
+        else w[k] = {token_of(unit, k) == r.certain ? 0.f : clean(t.p[k]), 0.f};
         s = add(s, w[k].hi, w[k].lo);
     }
     return warp_total(s);
@@ -169,7 +167,7 @@ __device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int
         const Tokens now = t;
         if (unit + step < a.units) load_unit<WIDE, Q>(r, a.vocab, unit + step, t);
         Pair w[PER];
-        const Pair s = weigh_unit<WIDE, Q>(r, unit, now, w);
+        const Pair s = weigh_unit<Q>(r, unit, now, w);
         if ((threadIdx.x & 31) == 0) __stcg(part + unit, make_float2(s.hi, s.lo));
     }
 }
@@ -180,30 +178,37 @@ __device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int
 template <bool WIDE, bool Q>
 __device__ int find_token(const VerifyArgs& a, const Row& r, int unit, double before, double goal) {
     const int lane = threadIdx.x & 31;
-    constexpr int STEP = WIDE ? 4 : 1;        // tokens of a lane that stand together
+    constexpr int STEP = 4;        // tokens of a lane that stand together
     Tokens t;
     Pair w[PER];
     load_unit<WIDE, Q>(r, a.vocab, unit, t);
-    weigh_unit<WIDE, Q>(r, unit, t, w);
+    weigh_unit<Q>(r, unit, t, w);
+    // sums before each of the lane's groups: PER / STEP scans side by side
+    double own[PER / STEP], inc[PER / STEP];
+#pragma unroll
+    for (int k = 0; k < PER / STEP; ++k) {
+        Pair x{0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < STEP; ++j) x = add(x, w[STEP * k + j].hi, w[STEP * k + j].lo);
+        own[k] = inc[k] = value(x);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < PER / STEP; ++k) {
+            const double x = __shfl_up_sync(0xffffffffu, inc[k], o);
+            if (lane >= o) inc[k] += x;
+        }
     int first = 0x7fffffff, last = -1;
 #pragma unroll
-    for (int k = 0; k < PER; k += STEP) {
-        double own = 0.0;
-#pragma unroll
-        for (int j = 0; j < STEP; ++j) own += value(w[k + j]);
-        double inc = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
-        }
-        double run = before + (inc - own);
-        before += __shfl_sync(0xffffffffu, inc, 31);
+    for (int k = 0; k < PER / STEP; ++k) {
+        double run = before + (inc[k] - own[k]);
+        before += __shfl_sync(0xffffffffu, inc[k], 31);
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
-            run += value(w[k + j]);
-            if (w[k + j].hi > 0.f) {
-                const int v = token_of<WIDE>(unit, k + j);
+            run += value(w[STEP * k + j]);
+            if (w[STEP * k + j].hi > 0.f) {
+                const int v = token_of(unit, STEP * k + j);
                 last = max(last, v);
                 if (run > goal) first = min(first, v);
             }
