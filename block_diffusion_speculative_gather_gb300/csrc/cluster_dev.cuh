@@ -28,12 +28,13 @@ __device__ __forceinline__ void put_remote(void* p, uint32_t rank, uint32_t v) {
 
 // launch_k with clusters of `ranks` CTAs in a row.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_cluster_k(void (*kern)(KArgs...), dim3 grid, dim3 block, int ranks, cudaStream_t s,
+inline cudaError_t launch_cluster_k(void (*kern)(KArgs...), dim3 grid, dim3 block, int ranks, cudaStream_t s, size_t smem,
                                     Args&&... args) {
     set_carveout_once(reinterpret_cast<const void*>(kern));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -8,18 +8,17 @@
 // rounded to it (powers of two: exact but where values fall below the format's
 // normal range).
 //
-// The choice: one CTA a sequence.  Up to 8192 positions their weights stay in
-// registers, eight a thread, and the budget's smallest weight is found bit by bit,
-// two bits a round; longer ones take a radix selection (11, 11 and 10 bits), the
-// keys in shared memory up to 49152 positions, looked up again above.  Then one
-// pass in order.
+// The choice: one CTA a sequence, a radix selection over the weights' bits (11, 11
+// and 10 of them), then one pass in order.  Up to 8192 positions the weights stay
+// in registers, eight a thread; the keys of longer sequences lie in shared memory
+// up to 49152 positions and are looked up again in every pass above.
 //
 // The move: a position only ever moves to a lower or its own place, so a page may
 // be written once the positions that go into it and into lower pages have been
-// read.  A CTA has one kv head's K or V of a sequence and layer (or a part of its
-// dims, where they are few) and goes through the pages in order, 32 KB at a time:
-// the next ones are on their way while these are written, which none of them
-// reads.
+// read.  A CTA has one kv head's K or V of a sequence and layer and goes through
+// its pages in order, 16 KB at a time, by a ring in shared memory: the copies of
+// the next three turns are on their way while one is written, which none of them
+// reads.  Where CTAs are few, a cluster shares the pages of a turn.
 
 #include "cluster_dev.cuh"
 #include "gemm.cuh"
@@ -61,53 +60,41 @@ __device__ __forceinline__ int block_exclusive(int v, int* total, int* sm) {
     return (warp ? before : 0) + inc - v;
 }
 
-// The smallest key that stays of `want` (above 0) among the keys of positions
-// first .. to - 1, and how many of those that have it.
-struct Border {
-    uint32_t key;
-    int ties;
-};
-
 constexpr int HELD = 8;               // keys of a thread
 constexpr int SHORT = ST * HELD;      // positions whose keys the threads hold
 
-// key[u] is position u * ST + tid's; 0 .. 2^32 - 1 are searched two bits at a time,
-// as counts of keys at or above three borders (at most SHORT, 14 bits: two in a
-// word's halves would not do, so three words).
-__device__ __forceinline__ Border border_of_held(const uint32_t (&key)[HELD], const bool (&in)[HELD], int want, int* sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t low = 0;                 // at least `want` keys are at or above it
-    int above = 0;                    // keys above the searched range
-    for (int shift = 30; shift >= 0; shift -= 2) {
-        int c1 = 0, c2 = 0, c3 = 0;
-#pragma unroll
-        for (int u = 0; u < HELD; ++u) {
-            const uint32_t d = in[u] && key[u] >= low ? (key[u] - low) >> shift : 0;   // 3 and more: above the range, too
-            c1 += d >= 1;
-            c2 += d >= 2;
-            c3 += d >= 3;
-        }
-        c1 = __reduce_add_sync(0xffffffffu, c1);
-        c2 = __reduce_add_sync(0xffffffffu, c2);
-        c3 = __reduce_add_sync(0xffffffffu, c3);
-        int* at = sm + (shift & 2) * (3 * SW / 2);      // in turn: one barrier a round
-        if (lane == 0) at[warp] = c1, at[SW + warp] = c2, at[2 * SW + warp] = c3;
-        __syncthreads();
-        c1 = __reduce_add_sync(0xffffffffu, at[lane]);
-        c2 = __reduce_add_sync(0xffffffffu, at[SW + lane]);
-        c3 = __reduce_add_sync(0xffffffffu, at[2 * SW + lane]);
-        // the highest quarter that still leaves `want`
-        if (c3 >= want) low += 3u << shift;
-        else if (c2 >= want) low += 2u << shift, above = c3;
-        else if (c1 >= want) low += 1u << shift, above = c2;
-        else above = c1;
+// One digit of the selection, once the bins are counted: the bin that the
+// `left`-th largest key falls into and what is left of it there, two bins a thread.
+__device__ __forceinline__ void pick_bin(const int* hist, int* sm, int* s_bin, int* s_left, int left) {
+    const int tid = threadIdx.x, hi = hist[BINS - 1 - 2 * tid], lo = hist[BINS - 2 - 2 * tid];
+    int total;
+    const int above = block_exclusive(hi + lo, &total, sm);
+    if (above < left && above + hi + lo >= left) {
+        const bool top = above + hi >= left;
+        *s_bin = BINS - (top ? 1 : 2) - 2 * tid;
+        *s_left = left - above - (top ? 0 : hi);
     }
-    return {low, want - above};
+    __syncthreads();
+}
+
+// Counts of (u, warp) in hist to the counts before each, by warp 0.
+__device__ __forceinline__ void counts_before(int* hist) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int run[HELD], sum = 0;
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) run[u] = hist[lane * HELD + u], sum += run[u];
+        int before = warp_inclusive(sum, lane) - sum;
+#pragma unroll
+        for (int u = 0; u < HELD; ++u) hist[lane * HELD + u] = before, before += run[u];
+    }
+    __syncthreads();
 }
 
 __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ Kv8EvictArgs a) {
     extern __shared__ uint32_t keys[];      // [a.keys]
-    __shared__ int hist[BINS], sm[2 * 3 * SW], s_bin, s_left, s_bad, s_moved;
+    __shared__ int hist[BINS], sm[SW], s_bin, s_left, s_bad, s_moved;
     __shared__ int s_table[SHORT / KV8_PAGE];
     pdl_trigger();
     pdl_wait();
@@ -160,31 +147,33 @@ __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ 
             stays[u] = j < n && !in[u];
         }
         if (want > 0) {
-            const Border r = border_of_held(key, in, want, sm);
-            // the first `ties` of those on the border, in order of u, then of threads
-            __syncthreads();
+            uint32_t prefix = 0;
+            int left = want;                          // of those with this prefix
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+                hist[tid] = hist[tid + ST] = 0;
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < HELD; ++u)
+                    if (in[u] && (pass == 0 || (key[u] ^ prefix) >> (shift + bits) == 0))
+                        atomicAdd(hist + ((key[u] >> shift) & ((1 << bits) - 1)), 1);
+                __syncthreads();
+                pick_bin(hist, sm, &s_bin, &s_left, left);
+                prefix |= (uint32_t)s_bin << shift;
+                left = s_left;
+            }
+            // the first `left` of those with this key, in order of u, then of threads
             int mine[HELD];
 #pragma unroll
             for (int u = 0; u < HELD; ++u) {
-                const unsigned m = __ballot_sync(0xffffffffu, in[u] && key[u] == r.key);
+                const unsigned m = __ballot_sync(0xffffffffu, in[u] && key[u] == prefix);
                 mine[u] = __popc(m & ((1u << lane) - 1));
                 if (lane == 0) hist[u * SW + warp] = __popc(m);
             }
-            __syncthreads();
-            if (warp == 0) {                          // HELD * SW counts, HELD a lane
-                int run[HELD], sum = 0;
+            counts_before(hist);
 #pragma unroll
-                for (int u = 0; u < HELD; ++u) run[u] = hist[lane * HELD + u], sum += run[u];
-                int before = warp_inclusive(sum, lane) - sum;
-#pragma unroll
-                for (int u = 0; u < HELD; ++u) hist[lane * HELD + u] = before, before += run[u];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < HELD; ++u) {
-                if (!in[u]) continue;
-                stays[u] = key[u] > r.key || (key[u] == r.key && hist[u * SW + warp] + mine[u] < r.ties);
-            }
+            for (int u = 0; u < HELD; ++u)
+                if (in[u]) stays[u] = key[u] > prefix || (key[u] == prefix && hist[u * SW + warp] + mine[u] < left);
             __syncthreads();
         }
         int mine[HELD];
@@ -194,16 +183,7 @@ __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ 
             mine[u] = __popc(m & ((1u << lane) - 1));
             if (lane == 0) hist[u * SW + warp] = __popc(m);
         }
-        __syncthreads();
-        if (warp == 0) {
-            int run[HELD], sum = 0;
-#pragma unroll
-            for (int u = 0; u < HELD; ++u) run[u] = hist[lane * HELD + u], sum += run[u];
-            int before = warp_inclusive(sum, lane) - sum;
-#pragma unroll
-            for (int u = 0; u < HELD; ++u) hist[lane * HELD + u] = before, before += run[u];
-        }
-        __syncthreads();
+        counts_before(hist);
 #pragma unroll
         for (int u = 0; u < HELD; ++u) {
             if (!stays[u]) continue;
@@ -243,16 +223,7 @@ __global__ void __launch_bounds__(ST) kv8_choose_kernel(const __grid_constant__ 
                     }
                 }
                 __syncthreads();
-                // bins from the top: a thread has two
-                const int hi = hist[BINS - 1 - 2 * tid], lo = hist[BINS - 2 - 2 * tid];
-                int total;
-                const int above = block_exclusive(hi + lo, &total, sm);
-                if (above < left && above + hi + lo >= left) {
-                    const bool top = above + hi >= left;
-                    s_bin = BINS - (top ? 1 : 2) - 2 * tid;
-                    s_left = left - above - (top ? 0 : hi);
-                }
-                __syncthreads();
+                pick_bin(hist, sm, &s_bin, &s_left, left);
                 prefix |= (uint32_t)s_bin << shift;
                 left = s_left;
             }
@@ -342,107 +313,122 @@ __device__ __forceinline__ uint32_t rescale4_f16(uint32_t w, __half2 f) {
     return r;
 }
 
-constexpr int MT = 512;               // threads of the move
-constexpr int MN = 4;                 // 16-byte pieces of a thread at a time
+constexpr int MT = 256;               // threads of the move
+constexpr int MN = 4;                 // 16-byte pieces of a thread a turn
+constexpr int MS = 4;                 // turns in the ring
+constexpr int MRANKS = 8;             // CTAs of a cluster at most
 
-// PB: bytes of a row that the CTA moves (a row, or 32 of it: the parts' CTAs are a
-// cluster, since they read the scales that the first one writes).
-template <int HD, int PB>
-__global__ void __launch_bounds__(MT, 2) kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a,
-                                                         const __grid_constant__ Kv8MoveLayers l) {
-    constexpr int PER_ROW = PB / 16, ROWS = MT * MN / PER_ROW, PARTS = HD / PB, PAGES = ROWS / KV8_PAGE;
-    constexpr int EACH = (ROWS + MT - 1) / MT;                      // rows whose scales a thread looks up
-    __shared__ float s_ratio[2][ROWS];
-    __shared__ float s_top[2][ROWS / 32];
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int HD> struct MoveSmem {
+    static constexpr int rows = MT * MN * 16 / HD;                  // of a CTA and turn: whole pages
+    uint4 codes[MS][MT * MN];
+    float scale[MS][rows];                                          // the rows' old scales
+};
+
+template <int HD>
+__global__ void __launch_bounds__(MT, 3) kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a,
+                                                         const __grid_constant__ Kv8MoveLayers l, int ranks) {
+    using S_ = MoveSmem<HD>;
+    constexpr int PER_ROW = HD / 16, ROWS = S_::rows, PAGES = ROWS / KV8_PAGE, STEP = MT / PER_ROW;
+    static_assert(ROWS % KV8_PAGE == 0 && ROWS <= MT && KV8_PAGE % STEP == 0, "whole pages at a time");
+    extern __shared__ __align__(16) uint8_t raw[];
+    S_& sm = *reinterpret_cast<S_*>(raw);
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int part = blockIdx.x % PARTS, chain = blockIdx.x / PARTS, s = chain / a.n_kv, head = chain - s * a.n_kv;
+    const int chain = blockIdx.x / ranks, rank = blockIdx.x - chain * ranks, s = chain / a.n_kv, head = chain - s * a.n_kv;
     const int layer = blockIdx.y, which = blockIdx.z;
     const int kept = a.new_len[s], begin = a.first_moved[s];
-    if (begin >= kept) return;
+    if (begin >= kept) return;                                      // all of a cluster
     const int* from = a.from + (size_t)s * ((long long)a.max_pages * KV8_PAGE);
     const int* table = a.table + (size_t)s * a.max_pages;
-    const int c = tid % PER_ROW, r0 = tid / PER_ROW;                // this thread's piece of rows r0, r0 + MT / PER_ROW, ..
-    uint8_t* codes = (which ? l.v_codes[layer] : l.k_codes[layer]) + (size_t)head * KV8_PAGE * HD + part * PB + c * 16;
+    const int c = tid % PER_ROW, r0 = tid / PER_ROW;                // this thread's piece of rows r0, r0 + STEP, ..
+    uint8_t* codes = (which ? l.v_codes[layer] : l.k_codes[layer]) + (size_t)head * KV8_PAGE * HD + c * 16;
     float* scale = (which ? l.v_scale[layer] : l.k_scale[layer]) + head;
-    const int page_rows = a.n_kv * KV8_PAGE;                        // rows of a page, all heads (slots x heads fit int32)
+    const int page_rows = a.n_kv * KV8_PAGE;                        // rows of a page, all heads (rows fit int32)
     auto row_of = [&](int slot) { return (size_t)(unsigned)((slot / KV8_PAGE) * page_rows + slot % KV8_PAGE) * HD; };
-    uint4 x[MN], y[MN];
-    int slot[MN], scale_slot[EACH];
-    float sc[EACH];
-    // slots of the positions d0 .. that this thread reads
-    auto look = [&](int d0) {
+    const int base = begin / KV8_PAGE * KV8_PAGE + rank * ROWS, turn_rows = ranks * ROWS;
+    const int turns = (kept - begin / KV8_PAGE * KV8_PAGE + turn_rows - 1) / turn_rows;
+    int slot[MN], scale_slot = -1;
+    auto look = [&](int t) {            // where the positions of turn t come from
+        const int d0 = base + t * turn_rows;
 #pragma unroll
         for (int i = 0; i < MN; ++i) {
-            const int d = d0 + r0 + i * (MT / PER_ROW);
-            slot[i] = d < kept ? from[d] : -1;
+            const int d = d0 + r0 + i * STEP;
+            slot[i] = t < turns && d < kept ? from[d] : -1;
         }
-#pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            const int d = d0 + e * MT + tid;
-            scale_slot[e] = e * MT + tid < ROWS && d < kept ? from[d] : -1;
-        }
+        scale_slot = t < turns && tid < ROWS && d0 + tid < kept ? from[d0 + tid] : -1;
     };
-    auto fetch = [&](uint4 (&v)[MN]) {
+    auto fetch = [&](int t) {           // the copies of turn t (an empty group behind the last)
 #pragma unroll
         for (int i = 0; i < MN; ++i)
-            if (slot[i] >= 0) v[i] = *reinterpret_cast<const uint4*>(codes + row_of(slot[i]));
-#pragma unroll
-        for (int e = 0; e < EACH; ++e) sc[e] = scale_slot[e] >= 0 ? scale[(size_t)(scale_slot[e] / KV8_PAGE) * a.n_kv] : 0.f;
+            if (slot[i] >= 0) copy_async16(&sm.codes[t % MS][i * MT + tid], codes + row_of(slot[i]));
+        if (scale_slot >= 0) copy_async4(&sm.scale[t % MS][tid], scale + (size_t)(scale_slot / KV8_PAGE) * a.n_kv);
+        copy_commit();
     };
-    int d0 = begin / KV8_PAGE * KV8_PAGE;
-    look(d0);
-    fetch(x);
-    look(d0 + ROWS);
-    for (int turn = 0; d0 < kept; d0 += ROWS, turn ^= 1) {
-        float own[EACH];
+    look(0);
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            own[e] = sc[e];
-            const float top = warp_max(sc[e]);
-            if (lane == 0 && e * MT + tid < ROWS) s_top[turn][(e * MT + tid) >> 5] = top;
+    for (int t = 0; t < MS - 1; ++t) {
+        fetch(t);
+        look(t + 1);
+    }
+    int page[PAGES];                    // of the turn at hand
+    auto pages_at = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PAGES; ++i) {
+            const int d = base + t * turn_rows + i * KV8_PAGE;
+            page[i] = t < turns && d < kept ? table[d / KV8_PAGE] : 0;
         }
-        // these pages have been read, by every thread (of the row's other parts, too)
-        if (PARTS > 1) {
+    };
+    pages_at(0);
+    for (int t = 0; t < turns; ++t) {
+        copy_wait<MS - 2>();
+        // the turn's positions have been read, by every thread that reads any of them
+        if (ranks > 1) {
             cluster_arrive();
             cluster_wait();
         } else {
             __syncthreads();
         }
-        fetch(y);
-        look(d0 + 2 * ROWS);
-        // a row's factor; -1: as it is
+        fetch(t + MS - 1);              // into the ring's place of turn t - 1
+        look(t + MS);
+        const int d0 = base + t * turn_rows;
+        float top[PAGES];
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            const int row = e * MT + tid;
-            if (row >= ROWS) continue;
-            const float top = fmaxf(s_top[turn][row / KV8_PAGE * 2], s_top[turn][row / KV8_PAGE * 2 + 1]);
-            s_ratio[turn][row] = own[e] == top ? -1.f : own[e] / top;
-            const int d = d0 + row;
-            if (part == 0 && row % KV8_PAGE == 0 && d < kept) scale[(size_t)table[d / KV8_PAGE] * a.n_kv] = top;
+        for (int i = 0; i < PAGES; ++i) {
+            const int d = d0 + i * KV8_PAGE;
+            const float* sc = sm.scale[t % MS] + i * KV8_PAGE;
+            top[i] = warp_max(fmaxf(d + lane < kept ? sc[lane] : 0.f, d + 32 + lane < kept ? sc[32 + lane] : 0.f));
+            if (tid == 0 && d < kept) scale[(size_t)page[i] * a.n_kv] = top[i];
         }
-        __syncthreads();
 #pragma unroll
         for (int i = 0; i < MN; ++i) {
-            const int row = r0 + i * (MT / PER_ROW), d = d0 + row;
+            const int row = r0 + i * STEP, d = d0 + row;
             if (d >= kept) continue;
-            const float f = s_ratio[turn][row];
-            if (f != -1.f) {
-                if ((__float_as_uint(f) & 0x807fffffu) == 0) {      // a power of two (or 0)
+            const int pi = i * STEP / KV8_PAGE;                     // the same for all of the thread's i-th rows
+            uint4 x = sm.codes[t % MS][i * MT + tid];
+            const float own = sm.scale[t % MS][row];
+            if (own != top[pi]) {
+                const float f = own * (1.f / top[pi]);              // exact: powers of two
+                if ((__float_as_uint(f) & 0x807fffffu) == 0) {
                     const __half2 h = __float2half2_rn(f);
-                    x[i] = make_uint4(rescale4_f16(x[i].x, h), rescale4_f16(x[i].y, h), rescale4_f16(x[i].z, h),
-                                      rescale4_f16(x[i].w, h));
+                    x = make_uint4(rescale4_f16(x.x, h), rescale4_f16(x.y, h), rescale4_f16(x.z, h), rescale4_f16(x.w, h));
                 } else {
-                    x[i] = make_uint4(rescale4(x[i].x, f), rescale4(x[i].y, f), rescale4(x[i].z, f), rescale4(x[i].w, f));
+                    x = make_uint4(rescale4(x.x, f), rescale4(x.y, f), rescale4(x.z, f), rescale4(x.w, f));
                 }
             }
-            *reinterpret_cast<uint4*>(codes + row_of(table[d / KV8_PAGE] * KV8_PAGE + d % KV8_PAGE)) = x[i];
+            *reinterpret_cast<uint4*>(codes + row_of(page[pi] * KV8_PAGE + d % KV8_PAGE)) = x;
         }
-#pragma unroll
-        for (int i = 0; i < MN; ++i) x[i] = y[i];
+        pages_at(t + 1);
     }
-    static_assert(PAGES >= 1 && ROWS % KV8_PAGE == 0, "whole pages at a time");
 }
 
 // True positions of a step's rows: the cache's, and those the sequence has lost.
@@ -483,16 +469,15 @@ int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choo
             e = launch_k(kv8_choose_kernel, dim3((unsigned)a.S), dim3(ST), (size_t)a.keys * 4, s, a);
         if (e != cudaSuccess) return (int)e;
     }
-    // parts of 32 bytes a row while whole rows leave SMs without work: a CTA then has
-    // that many more pages at a time
-    const bool parts = 2LL * a.S * a.n_kv * l.n < sms;
-    const int each = parts ? head_dim / 32 : 1;
-    const dim3 grid((unsigned)(a.S * a.n_kv * each), (unsigned)l.n, 2), block(MT);
-    if (head_dim == 128)
-        return (int)(parts ? launch_cluster_k(kv8_move_kernel<128, 32>, grid, block, each, s, a, l)
-                           : launch_k(kv8_move_kernel<128, 128>, grid, block, 0, s, a, l));
-    return (int)(parts ? launch_cluster_k(kv8_move_kernel<64, 32>, grid, block, each, s, a, l)
-                       : launch_k(kv8_move_kernel<64, 64>, grid, block, 0, s, a, l));
+    const int chains = a.S * a.n_kv;
+    int ranks = 1;
+    while (ranks < MRANKS && 2LL * chains * l.n * ranks * 2 <= 3 * sms) ranks *= 2;
+    const dim3 grid((unsigned)(chains * ranks), (unsigned)l.n, 2), block(MT);
+    auto go = [&](auto kern, size_t smem) {
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern));
+        return (int)(e == cudaSuccess ? launch_cluster_k(kern, grid, block, ranks, s, smem, a, l, ranks) : e);
+    };
+    return head_dim == 128 ? go(kv8_move_kernel<128>, sizeof(MoveSmem<128>)) : go(kv8_move_kernel<64>, sizeof(MoveSmem<64>));
 }
 
 int launch_pages_shift(const PagesShiftArgs& a, cudaStream_t s) {

@@ -307,7 +307,7 @@ int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
         if (e != cudaSuccess) return (int)e;
     }
     return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)((long long)a.rows * ranks)), dim3(CT), ranks, s,
-                                 a, ranks);
+                                 0, a, ranks);
 }
 
 template <typename T>
