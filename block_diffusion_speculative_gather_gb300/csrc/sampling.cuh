@@ -17,7 +17,7 @@ int launch_probs(const ProbsArgs& a, int sms, cudaStream_t s);
 
 constexpr int VERIFY_MAX_SEQS = 65535;
 constexpr int VERIFY_MAX_VOCAB = 1 << 24;
-constexpr int VERIFY_UNIT = 512;         // tokens that a warp sums at a time
+constexpr int VERIFY_UNIT = 1024;        // tokens that a warp sums at a time
 // tickets first, at the same place in every call, so that calls of different
 // shapes can share a workspace: none's sums lie where another counts
 constexpr size_t VERIFY_TICKET_BYTES = 65536 * sizeof(int);

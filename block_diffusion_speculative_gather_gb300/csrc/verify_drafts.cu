@@ -13,7 +13,7 @@
 // of terms: differences are taken exactly (two fp32 numbers each), sums are kept
 // as pairs of fp32 numbers within a warp and in fp64 above, in a fixed order.
 //
-// Only one row of p and q is read whole.  Its tokens are dealt in units of 512 to
+// Only one row of p and q is read whole.  Its tokens are dealt in units of 1024 to
 // warps (each CTA finds by itself, from two numbers a draft, which row that is),
 // a unit's sum goes to memory, and the last of a sequence's CTAs finds the unit
 // that u_0 falls into and reads it again.  No CTA waits for another.
@@ -25,7 +25,9 @@ namespace {
 
 constexpr int VT = 256;                        // threads
 constexpr int VW = VT / 32;
-constexpr int PER = VERIFY_UNIT / 32;          // tokens of a lane
+constexpr int PER = 8;                         // tokens of a lane at a time
+constexpr int BLOCK = 32 * PER;                // tokens of a warp at a time
+static_assert(VERIFY_UNIT == 4 * VT && VERIFY_UNIT % BLOCK == 0, "four tokens a thread of the search");
 
 // A sum as hi + lo, |lo| below half a step of hi.
 struct Pair {
@@ -40,14 +42,12 @@ __device__ __forceinline__ Pair add(Pair a, float x, float e) {
 
 __device__ __forceinline__ double value(Pair a) { return (double)a.hi + (double)a.lo; }
 
+// The same in all lanes: a sum's rounding error does not depend on the operands' order.
 __device__ __forceinline__ Pair warp_total(Pair a) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        const Pair b{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
-        // the same operands in the same order on both sides
-        const bool first = !(threadIdx.x & o);
-        const Pair x = first ? a : b, y = first ? b : a;
-        a = add(x, y.hi, y.lo);
+        const float hi = __shfl_xor_sync(0xffffffffu, a.hi, o), lo = __fadd_rn(a.lo, __shfl_xor_sync(0xffffffffu, a.lo, o));
+        a = add(Pair{a.hi, lo}, hi, 0.f);
     }
     return a;
 }
@@ -57,12 +57,10 @@ __device__ __forceinline__ Pair warp_total(Pair a) {
 __device__ __forceinline__ float clean(float p) { return p > 0.f && p < 0x1p100f ? p : 0.f; }
 
 // Weight of a token: p - q where that is positive, exactly.
-__device__ __forceinline__ Pair weight(float p, float q) {
-    p = clean(p);
-    q = clean(q);
-    if (!(p > q)) return {0.f, 0.f};
+__device__ __forceinline__ Pair less(float p, float q) {
     const float d = __fsub_rn(p, q), b = __fsub_rn(d, p);
-    return {d, __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b))};
+    const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
+    return p > q ? Pair{d, e} : Pair{0.f, 0.f};
 }
 
 __device__ __forceinline__ void report(int* err, int info) {
@@ -112,111 +110,93 @@ struct Row {
     int certain;        // but for this token (-1: none), which has no weight
 };
 
-// The lane's k-th token of a unit: in order of k / 4, then of lanes, then of k.
-__device__ __forceinline__ int token_of(int unit, int k) {
-    return unit * VERIFY_UNIT + (k / 4) * 128 + (threadIdx.x & 31) * 4 + k % 4;
-}
-
-struct Tokens {
-    float p[PER], q[PER];
-};
-
-template <bool WIDE, bool Q>
-__device__ __forceinline__ void load_unit(const Row& r, int vocab, int unit, Tokens& t) {
-    if (WIDE) {
-#pragma unroll
-        for (int k = 0; k < PER; k += 4) {
-            const int v = token_of(unit, k);
-            const bool in = v < vocab;          // vocab is a multiple of 4
-            const float4 x = in ? *reinterpret_cast<const float4*>(r.p + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-            t.p[k] = x.x, t.p[k + 1] = x.y, t.p[k + 2] = x.z, t.p[k + 3] = x.w;
-            if (!Q) continue;
-            const float4 y = in && r.q ? *reinterpret_cast<const float4*>(r.q + v) : make_float4(0.f, 0.f, 0.f, 0.f);
-            t.q[k] = y.x, t.q[k + 1] = y.y, t.q[k + 2] = y.z, t.q[k + 3] = y.w;
-        }
+// Four tokens from v on (v < vocab); those behind the vocabulary are 0.
+template <bool WIDE>
+__device__ __forceinline__ void load4(const float* row, int vocab, int v, float* x) {
+    if (WIDE) {                                 // vocab is a multiple of 4
+        const float4 f = *reinterpret_cast<const float4*>(row + v);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
     } else {
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int v = token_of(unit, k);
-            t.p[k] = v < vocab ? r.p[v] : 0.f;
-            if (Q) t.q[k] = v < vocab && r.q ? r.q[v] : 0.f;
+        for (int j = 0; j < 4; ++j) x[j] = v + j < vocab ? row[v + j] : 0.f;
+    }
+}
+
+template <bool Q> struct Tokens {
+    float p[PER], q[Q ? PER : 1];
+};
+
+// A warp's BLOCK tokens from v0 on.
+template <bool WIDE, bool Q>
+__device__ __forceinline__ void load_block(const Row& r, int vocab, int v0, Tokens<Q>& t) {
+#pragma unroll
+    for (int k = 0; k < PER; k += 4) {
+        const int v = v0 + k * 32 + (threadIdx.x & 31) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            t.p[k + j] = 0.f;
+            if (Q) t.q[k + j] = 0.f;
+        }
+        if (v < vocab) {
+            load4<WIDE>(r.p, vocab, v, t.p + k);
+            if (Q && r.q) load4<WIDE>(r.q, vocab, v, t.q + k);
         }
     }
 }
 
-// Weights of the tokens, and their sum over the warp (the same in all lanes).
-template <bool Q>
-__device__ __forceinline__ Pair weigh_unit(const Row& r, int unit, const Tokens& t, Pair (&w)[PER]) {
-    Pair s{0.f, 0.f};
+// CLEAN false: numbers of 2^100 and more are left in; a sum below it holds none.
+template <bool Q, bool CLEAN>
+__device__ __forceinline__ Pair add_block(const Row& r, int v0, const Tokens<Q>& t, Pair s) {
+    const int mine = r.certain - v0 - (threadIdx.x & 31) * 4;      // where the refused token is the lane's
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-        if (Q) w[k] = weight(t.p[k], t.q[k]);
-        else w[k] = {token_of(unit, k) == r.certain ? 0.f : clean(t.p[k]), 0.f};
-        s = add(s, w[k].hi, w[k].lo);
+        float p = CLEAN ? clean(t.p[k]) : fmaxf(t.p[k], 0.f);      // fmaxf: NaN is 0
+        if constexpr (Q) {
+            const Pair w = less(p, clean(t.q[k]));
+            s = add(s, w.hi, w.lo);
+        } else {
+            if (r.certain >= 0 && mine == (k / 4) * 128 + k % 4) p = 0.f;
+            s = add(s, p, 0.f);
+        }
+    }
+    return s;
+}
+
+// By a warp: the sum of a unit's weights, read anew.
+template <bool WIDE, bool Q>
+__device__ __noinline__ Pair sum_unit(const Row& r, int vocab, int unit) {
+    Pair s{0.f, 0.f};
+    for (int v0 = unit * VERIFY_UNIT; v0 < min((unit + 1) * VERIFY_UNIT, vocab); v0 += BLOCK) {
+        Tokens<Q> t;
+        load_block<WIDE, Q>(r, vocab, v0, t);
+        s = add_block<Q, true>(r, v0, t, s);
     }
     return warp_total(s);
 }
 
-// By a warp: sums of units `unit`, unit + step, .. into part.  The next unit is on
-// its way while one is summed.
+// By a warp: sums of units `unit`, unit + step, .. into part.  The next tokens are
+// on their way while these are summed.
 template <bool WIDE, bool Q>
 __device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int unit, int step, float2* part) {
-    Tokens t;
-    if (unit < a.units) load_unit<WIDE, Q>(r, a.vocab, unit, t);
+    Tokens<Q> t;
+    if (unit < a.units) load_block<WIDE, Q>(r, a.vocab, unit * VERIFY_UNIT, t);
     for (; unit < a.units; unit += step) {
-        const Tokens now = t;
-        if (unit + step < a.units) load_unit<WIDE, Q>(r, a.vocab, unit + step, t);
-        Pair w[PER];
-        const Pair s = weigh_unit<Q>(r, unit, now, w);
+        Pair s{0.f, 0.f};
+#pragma unroll
+        for (int b = 0; b < VERIFY_UNIT / BLOCK; ++b) {
+            const Tokens<Q> now = t;
+            const int v0 = unit * VERIFY_UNIT + b * BLOCK;
+            if (b + 1 < VERIFY_UNIT / BLOCK) load_block<WIDE, Q>(r, a.vocab, v0 + BLOCK, t);
+            else if (unit + step < a.units) load_block<WIDE, Q>(r, a.vocab, (unit + step) * VERIFY_UNIT, t);
+            s = add_block<Q, Q>(r, v0, now, s);
+        }
+        s = warp_total(s);
+        if (!Q && !(s.hi < 0x1p100f)) {
+            const Row copy = r;      // what a call names lies in memory
+            s = sum_unit<WIDE, Q>(copy, a.vocab, unit);
+        }
         if ((threadIdx.x & 31) == 0) __stcg(part + unit, make_float2(s.hi, s.lo));
     }
-}
-
-// By a warp: the first token of the unit whose running sum, from `before` on,
-// passes `goal`, else its last token with weight (a running sum can fall short of
-// the unit's by its last bits); -1: it has none.
-template <bool WIDE, bool Q>
-__device__ int find_token(const VerifyArgs& a, const Row& r, int unit, double before, double goal) {
-    const int lane = threadIdx.x & 31;
-    constexpr int STEP = 4;        // tokens of a lane that stand together
-    Tokens t;
-    Pair w[PER];
-    load_unit<WIDE, Q>(r, a.vocab, unit, t);
-    weigh_unit<Q>(r, unit, t, w);
-    // sums before each of the lane's groups: PER / STEP scans side by side
-    double own[PER / STEP], inc[PER / STEP];
-#pragma unroll
-    for (int k = 0; k < PER / STEP; ++k) {
-        Pair x{0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < STEP; ++j) x = add(x, w[STEP * k + j].hi, w[STEP * k + j].lo);
-        own[k] = inc[k] = value(x);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < PER / STEP; ++k) {
-            const double x = __shfl_up_sync(0xffffffffu, inc[k], o);
-            if (lane >= o) inc[k] += x;
-        }
-    int first = 0x7fffffff, last = -1;
-#pragma unroll
-    for (int k = 0; k < PER / STEP; ++k) {
-        double run = before + (inc[k] - own[k]);
-        before += __shfl_sync(0xffffffffu, inc[k], 31);
-#pragma unroll
-        for (int j = 0; j < STEP; ++j) {
-            run += value(w[STEP * k + j]);
-            if (w[STEP * k + j].hi > 0.f) {
-                const int v = token_of(unit, STEP * k + j);
-                last = max(last, v);
-                if (run > goal) first = min(first, v);
-            }
-        }
-    }
-    first = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
-    last = __reduce_max_sync(0xffffffffu, last);
-    return first != 0x7fffffff ? first : last;
 }
 
 __device__ __forceinline__ double unit_sum(const float2* p) {
@@ -224,11 +204,38 @@ __device__ __forceinline__ double unit_sum(const float2* p) {
     return value(Pair{s.x, s.y});
 }
 
+// Exclusive sums over the CTA, and the total.
+__device__ __forceinline__ double block_before(double v, double* total, double* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    double inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) red[warp] = inc;
+    __syncthreads();
+    double before = 0.0, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) {
+        if (i < warp) before += red[i];
+        sum += red[i];
+    }
+    *total = sum;
+    return before + (inc - v);
+}
+
+struct Search {
+    double red[2][VW];
+    double run;
+    int thread, last, unit, token;
+};
+
 // By the whole CTA: the token that u draws from a row whose units' sums are
 // `part`; -1: it has no weight.
 template <bool WIDE, bool Q>
-__device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float u, double* red, int* s_v) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float u, Search& sm) {
+    const int tid = threadIdx.x;
     // each thread a run of units
     const int per = (a.units + VT - 1) / VT, b0 = tid * per, b1 = min(b0 + per, a.units);
     double own = 0.0;
@@ -238,63 +245,80 @@ __device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float
         own += x;
         if (x > 0.0) end = c;
     }
-    double inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) red[warp] = inc;
-    if (tid == 0) s_v[0] = 0x7fffffff, s_v[1] = -1;
-    __syncthreads();
-    double total = 0.0, before = 0.0;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) {
-        if (i < warp) before += red[i];
-        total += red[i];
-    }
+    if (tid == 0) sm.thread = 0x7fffffff, sm.last = -1;
+    double total;
+    const double before = block_before(own, &total, sm.red[0]);
     const double goal = (double)u * total;
-    before += inc - own;
-    // the first run that passes the goal, and in it the first unit
-    if (end >= 0) {
-        atomicMax(s_v + 1, end);
-        if (before + own > goal) atomicMin(s_v, tid);
+    // the first run that passes the goal
+    const bool past = end >= 0 && before + own > goal;
+    const unsigned m = __ballot_sync(0xffffffffu, past);
+    const int top = __reduce_max_sync(0xffffffffu, end);
+    if ((tid & 31) == 0) {
+        if (m) atomicMin(&sm.thread, tid + __ffs(m) - 1);
+        if (top >= 0) atomicMax(&sm.last, top);
     }
     __syncthreads();
-    const int at = s_v[0], last = s_v[1];
+    const int last = sm.last, thread = sm.thread;
     __syncthreads();
     if (last < 0) return -1;
-    if (at == 0x7fffffff ? warp == 0 : warp == at / 32) {
-        int unit = last;
-        double run = 0.0, g = INFINITY;            // past the goal: the last token with weight
-        if (at != 0x7fffffff) {
-            unit = end;
-            run = before;
-            g = goal;
-            for (int c = b0; c < b1; ++c) {        // in the lane whose run it is
-                const double x = unit_sum(part + c);
-                if (x > 0.0) {
-                    unit = c;
-                    if (run + x > goal) break;
-                    if (c < end) run += x;
-                }
+    const bool none = thread == 0x7fffffff;          // u at or above 1, or NaN: the last token with weight
+    if (tid == (none ? 0 : thread)) {
+        // the run's first unit that passes it (by rounding maybe none: its last one with weight)
+        int unit = none ? last : end;
+        double run = none ? 0.0 : before;
+        for (int c = b0; c < b1 && !none; ++c) {
+            const double x = unit_sum(part + c);
+            if (x > 0.0 && run + x > goal) {
+                unit = c;
+                break;
             }
-            unit = __shfl_sync(0xffffffffu, unit, at % 32);
-            run = __shfl_sync(0xffffffffu, run, at % 32);
+            if (c < end) run += x;
         }
-        const int v = find_token<WIDE, Q>(a, r, unit, run, g);
-        if (lane == 0) s_v[0] = v;
+        sm.unit = unit;
+        sm.run = run;
+        sm.token = 0x7fffffff;
+        sm.last = -1;
     }
     __syncthreads();
-    const int v = s_v[0];
+    // the unit's tokens, four a thread
+    const int v = sm.unit * VERIFY_UNIT + 4 * tid;
+    float p[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
+    if (v < a.vocab) {
+        load4<WIDE>(r.p, a.vocab, v, p);
+        if (Q && r.q) load4<WIDE>(r.q, a.vocab, v, q);
+    }
+    Pair w[4], s{0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = Q ? less(clean(p[j]), clean(q[j])) : Pair{v + j == r.certain ? 0.f : clean(p[j]), 0.f};
+        s = add(s, w[j].hi, w[j].lo);
+    }
+    double run = sm.run + block_before(value(s), &total, sm.red[1]);
+    int hit = 0x7fffffff, any = -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        run += value(w[j]);
+        if (w[j].hi > 0.f) {
+            any = v + j;
+            if (!none && run > goal) hit = min(hit, v + j);
+        }
+    }
+    hit = (int)__reduce_min_sync(0xffffffffu, (unsigned)hit);
+    any = __reduce_max_sync(0xffffffffu, any);
+    if ((tid & 31) == 0) {
+        if (hit != 0x7fffffff) atomicMin(&sm.token, hit);
+        if (any >= 0) atomicMax(&sm.last, any);
+    }
     __syncthreads();
-    return v;
+    const int token = sm.token != 0x7fffffff ? sm.token : sm.last;
+    __syncthreads();
+    return token;
 }
 
 template <bool WIDE, bool Q>
-__global__ void __launch_bounds__(VT, Q ? 3 : 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
-    __shared__ double red[VW];
-    __shared__ int s_v[2], s_last;
+__global__ void __launch_bounds__(VT, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ Search s_search;
+    __shared__ int s_last;
     __shared__ Verdict s_verdict;
     pdl_trigger();
     pdl_wait();
@@ -335,7 +359,7 @@ __global__ void __launch_bounds__(VT, Q ? 3 : 4) verify_kernel(const __grid_cons
         __threadfence();
     }
     const float u = a.u[r0];
-    int v = draw<WIDE, Q>(a, row, part, u, red, s_v);
+    int v = draw<WIDE, Q>(a, row, part, u, s_search);
     if (v < 0 && ve.draft >= 0) {
         // nothing is left of p behind q: p itself
         row.q = nullptr;
@@ -343,7 +367,7 @@ __global__ void __launch_bounds__(VT, Q ? 3 : 4) verify_kernel(const __grid_cons
         sum_units<WIDE, Q>(a, row, warp, VW, part);
         __threadfence();
         __syncthreads();
-        v = draw<WIDE, Q>(a, row, part, u, red, s_v);
+        v = draw<WIDE, Q>(a, row, part, u, s_search);
     }
     const int out = ve.a + (v >= 0);
     for (int i = tid; i < n; i += VT) a.tokens[r0 + i] = i < ve.a ? a.ids[r0 + i + 1] : (i == ve.a ? v : -1);
@@ -356,12 +380,13 @@ __global__ void __launch_bounds__(VT, Q ? 3 : 4) verify_kernel(const __grid_cons
 }  // namespace
 
 int launch_verify_drafts(const VerifyArgs& a, int sms, cudaStream_t s) {
-    // a unit a warp while they are few, up to four in a row where there are many:
-    // CTAs come and go less often
-    int x = (a.units + VW - 1) / VW;
-    const long long all = (long long)x * a.S, room = 8LL * sms;
-    const int each = all >= 4 * room ? 4 : (all >= 2 * room ? 2 : 1);
-    x = (x + each - 1) / each;
+    // a unit a warp while all CTAs run at once, else as many CTAs a sequence as do; many
+    // sequences: about four rounds of them, so that the last one is short
+    const int most = (a.units + VW - 1) / VW;
+    const long long room = 4LL * sms;
+    long long x = most;
+    if (x * a.S > room) x = a.S <= room / 2 ? room / a.S : (4 * room + a.S - 1) / a.S;
+    if (x > most) x = most;
     const dim3 grid((unsigned)x, (unsigned)a.S), block(VT);
     if (a.q)
         return (int)(a.wide ? launch_k(verify_kernel<true, true>, grid, block, 0, s, a)
