@@ -20,5 +20,9 @@ const dflash_weights& ctx_weights(const dflash_ctx* c);
 // 2D tensor map over a row-major [rows][inner] matrix of es-byte elements.
 int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es, uint64_t inner,
                uint64_t rows, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
+// 3D tensor map [rows][heads][dim] of 16-bit elements by element strides (whole 16
+// bytes, above 0), boxes of 64 elements (128-byte swizzle) x box_heads x box_rows.
+int encode_map_heads(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t dim, uint64_t heads,
+                     uint64_t rows, int64_t head_stride, int64_t row_stride, uint32_t box_heads, uint32_t box_rows);
 
 }  // namespace dfl

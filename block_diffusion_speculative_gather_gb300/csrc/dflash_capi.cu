@@ -785,6 +785,19 @@ int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int es,
     return make_map_raw(m, base, dt, es, inner, rows, box_inner, box_rows, swz);
 }
 
+int encode_map_heads(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t dim, uint64_t heads,
+                     uint64_t rows, int64_t head_stride, int64_t row_stride, uint32_t box_heads, uint32_t box_rows) {
+    const int e = get_encode();
+    if (e) return e;
+    cuuint64_t dims[3] = {dim, heads, rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+    cuuint32_t box[3] = {64, box_heads, box_rows}, estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, DFL_L2_PROMOTION, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DFLASH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return DFLASH_OK;
+}
+
 int run_linear_store(const void* w, const void* x, int n, int k, float* y, float* slots,
                      int* counters, DevState* st, void* clear, size_t clear_bytes, int32_t* err,
                      int sms, cudaStream_t s) {

@@ -133,6 +133,10 @@ struct Kv8WeighArgs {
     int* err;
 };
 int launch_kv8_weigh(const Kv8WeighArgs& a, int head_dim, int sms, cudaStream_t s);
+// The tcgen05 form: whether it is the faster one for a call's rows (and can take their strides), and its launch; q_map in
+// boxes of 64 dims x group heads x (128 / group) rows.
+bool kv8_weigh_by_tc(const Kv8WeighArgs& a);
+int launch_kv8_weigh_tc(const CUtensorMap& q_map, const Kv8WeighArgs& a, int head_dim, int sms, cudaStream_t s);
 
 constexpr int KV8_LAYERS = 32;  // of one launch: the kernel arguments hold their pools' addresses
 struct Kv8MoveLayers {

@@ -319,6 +319,13 @@ int dflash_kv8_weigh(const dflash_kv8_cache* cache, const dflash_kv8_query* q, f
     a.err = err;
     int sms = 0;
     if (const int r = sm_count(&sms)) return r;
+    if (kv8_weigh_by_tc(a)) {
+        CUtensorMap q_map;
+        const int r = encode_map_heads(&q_map, q->q, a.dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                       cache->head_dim, q->n_q, q->rows, q->q_head, q->q_row, a.group, 128 / a.group);
+        if (r) return r;
+        return launched(launch_kv8_weigh_tc(q_map, a, cache->head_dim, sms, reinterpret_cast<cudaStream_t>(stream)), "cache weigh");
+    }
     return launched(launch_kv8_weigh(a, cache->head_dim, sms, reinterpret_cast<cudaStream_t>(stream)), "cache weigh");
 }
 

@@ -24,49 +24,12 @@
 #include "gemm.cuh"
 #include "kv8.cuh"
 #include "kv8_attn_dev.cuh"
+#include "kv8_weigh_dev.cuh"
 
 namespace dfl {
 namespace {
 
 using namespace kv8;
-
-constexpr int WSEQS = 4096;
-
-// A sequence's counted rows [i0, i1) and the positions [lo, hi) to go through.
-struct Span {
-    int r0, i0, i1, first, kv, lo, hi;
-};
-
-__device__ __forceinline__ Span span_of(const Kv8WeighArgs& a, int s, bool tell) {
-    Span q{};
-    const int r0 = a.row_start[s], r1 = a.row_start[s + 1], kv = a.kv_len[s];
-    if (r0 < 0 || r1 < r0 || r1 > a.rows || kv < 0 || kv > (long long)a.max_pages * KV8_PAGE) {
-        if (tell) report(a.err, DERR_INDEX, SITE_LEN);    // such a sequence is left out
-        return q;
-    }
-    const int n = r1 - r0;
-    q.r0 = r0;
-    q.kv = kv;
-    q.first = kv - n;
-    q.i1 = a.count ? min(max(a.count[s], 0), n) : n;
-    q.i0 = a.observe > 0 ? max(q.i1 - a.observe, 0) : 0;
-    if (q.i1 > q.i0) {
-        q.hi = a.causal ? max(q.first + q.i1, 0) : kv;
-        const int end = a.causal ? q.first + q.i0 + 1 : q.first;
-        if (a.window > 0 && end > a.window) q.lo = end - a.window;
-    } else {
-        q.lo = kv;
-    }
-    if (a.fresh && n > 0) {
-        q.lo = min(q.lo, max(q.first, 0));
-        q.hi = kv;
-    }
-    return q;
-}
-
-template <int W> __device__ __forceinline__ int items_of(const Span& q) {
-    return q.hi > q.lo ? (q.hi - 1) / (16 * W) - q.lo / (16 * W) + 1 : 0;
-}
 
 template <int HD, int W> struct WeighSmem {
     static constexpr int pitch = HD * 2 + 16;      // bytes: 8 lanes' rows fall on all banks
@@ -87,45 +50,16 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    // items before each sequence
-    const int each = (a.S + WT - 1) / WT;
-    int mine = 0;
-    for (int s = tid * each; s < a.S && s < (tid + 1) * each; ++s)
-        mine = add_counts(mine, items_of<W>(span_of(a, s, blockIdx.x == 0)));
-    const int inc = warp_inclusive(mine, lane);
-    if (lane == 31) sm.warp[warp] = inc;
-    __syncthreads();
-    int run = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) run = add_counts(run, sm.warp[w]);
-        total = add_counts(total, sm.warp[w]);
-    }
-    run = add_counts(run, inc - mine);
-    for (int s = tid * each; s < a.S && s < (tid + 1) * each; ++s) {
-        sm.before[s] = run;
-        if (each > 1) run = add_counts(run, items_of<W>(span_of(a, s, false)));
-    }
-    if (tid == 0) sm.before[a.S] = total;
-    __syncthreads();
-
-    const int first_item = (int)((long long)total * blockIdx.x / gridDim.x);
-    const int last_item = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
-    if (first_item >= last_item) return;
-    int s = 0;
-    for (int len = a.S; len > 1;) {        // the last sequence that begins at or before the first item
-        const int st = (len + 31) / 32, at = lane * st;
-        const int m = __popc(__ballot_sync(0xffffffffu, at < len && sm.before[s + at] <= first_item)) - 1;
-        s += m * st;
-        len = min(st, len - m * st);
-    }
+    const Run run = my_items<KEYS, WT>(a, sm.before, sm.warp);
+    if (run.first >= run.last) return;
+    int s = run.s;
     const int depth = a.n_kv > 1 ? 2 : 1;          // heads that keys are fetched ahead
     uint4 ahead[2][HD / 32];
     float ahead_scale[2] = {0.f, 0.f};
     bool carried = false, fresh_rows = true;
     int carried_page = -1;
     Span q = span_of(a, s, false);
-    for (int item = first_item; item < last_item; ++item) {
+    for (int item = run.first; item < run.last; ++item) {
         if (item >= sm.before[s + 1]) {
             do ++s;
             while (item >= sm.before[s + 1]);
@@ -160,7 +94,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
             fetch(pg, 0, ahead[0], ahead_scale);
             if (depth > 1) fetch(pg, 1, ahead[1], ahead_scale + 1);
         }
-        const int next_pg = item + 1 < min(last_item, sm.before[s + 1]) ? page_of(key0 + KEYS) : -1;
+        const int next_pg = item + 1 < min(run.last, sm.before[s + 1]) ? page_of(key0 + KEYS) : -1;
         carried = false;
         float* wp = a.weights + (size_t)max(pg, 0) * KV8_PAGE + off + g;
         float old[2] = {0.f, 0.f};

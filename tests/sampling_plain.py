@@ -126,14 +126,17 @@ def weigh(q, lse, kc, k_scale, table, kv_len, row_start, weights, count=None, ob
                     continue
                 k = np.repeat(kc[pg, :, off] * k_scale[pg][:, None], group, 0)
                 x = (q[r0 + i] * k).sum(1) * scale
-                t = np.where(np.isnan(x) | np.isnan(lse[r0 + i]) | (lse[r0 + i] == -np.inf), 0.0, np.exp(x - lse[r0 + i]))
+                with np.errstate(invalid="ignore"):
+                    e = x - lse[r0 + i]                  # NaN (a NaN code, inf - inf) adds nothing
+                    t = np.where(np.isnan(e) | (lse[r0 + i] == -np.inf), 0.0, np.exp(e))
                 # dim products in fp32, the factor and its product; elements of q held as
                 # f16 beside the row's largest; lse in base 2; the difference; ex2
-                d = (dim + 10) * 2.0 ** -24 * np.abs(q[r0 + i] * k).sum(1) * scale
-                d += 2.0 ** -25 * np.abs(q[r0 + i]).max(1) * np.abs(k).sum(1) * scale
+                with np.errstate(invalid="ignore"):
+                    d = (dim + 10) * 2.0 ** -24 * np.abs(q[r0 + i] * k).sum(1) * scale
+                    d += 2.0 ** -25 * np.abs(q[r0 + i]).max(1) * np.abs(k).sum(1) * scale
                 l = np.where(np.isfinite(lse[r0 + i]), np.abs(lse[r0 + i]), 0.0)
-                d = np.where(np.isnan(x), 0.0, d)
-                x = np.where(np.isnan(x), 0.0, x)
+                d = np.where(np.isfinite(x), d, 0.0)
+                x = np.where(np.isfinite(x), x, 0.0)
                 d += 2.0 ** -23 * l + 2.0 ** -24 * (np.abs(x) + l) + 2.0 ** -22
                 got += t.sum()
                 err += (t * (d + d * d)).sum()

@@ -81,6 +81,12 @@ SHAPES = [
     (4, 2, 128, [70], [140]),
     (12, 4, 64, [33, 1], [70, 257]),
     (20, 4, 128, [17, 2], [17, 66]),
+    # many rows: the tcgen05 form, with groups that fill a tile and ones that do not
+    (32, 8, 128, [64, 40], [300, 100]),
+    (20, 4, 128, [64], [190]),
+    (16, 1, 64, [33, 70], [200, 130]),
+    (6, 2, 64, [70, 0, 3], [90, 64, 260]),
+    (7, 1, 128, [129, 20, 64], [130, 20, 64]),
 ]
 
 
@@ -91,6 +97,56 @@ def test_weigh(capi, n_q, n_kv, dim, rows, held, causal, window, kind):
     st = attn_state(n_q, n_kv, dim, rows, held, kind, seed=len(held))
     attend(capi, st, causal=causal, window=window)
     check_weigh(capi, st, causal=causal, window=window, fresh=causal)
+
+
+def test_weigh_many_rows_counted(capi):
+    """The tcgen05 form: counted and observed rows, a window, sequences without rows."""
+    st = attn_state(16, 4, 128, [90, 0, 64, 5, 33], [200, 70, 64, 300, 129], BF, seed=21)
+    for kw in (dict(), dict(window=50)):
+        attend(capi, st, **kw)
+        for more in (dict(observe=32, fresh=True), dict(count=[0, 0, 40, 5, 33], fresh=True),
+                     dict(count=[90, 9, 64, -1, 12], observe=20)):
+            check_weigh(capi, st, **kw, **more)
+
+
+def test_weigh_many_rows_strides_nan_and_pages(capi):
+    st = attn_state(8, 2, 64, [64, 50], [140, 300], F16, seed=22)
+    attend(capi, st)
+    big = torch.full((st["q"].shape[0] + 3, 3, 8, 72), NAN, dtype=F16, device="cuda")
+    view = big[1:-2, 1, :, :64]
+    view.copy_(st["q"])
+    st["q"] = view
+    check_weigh(capi, st)
+    st["q"][5] = NAN                                  # a row that adds nothing
+    st["q"][9, :, 3] = INF
+    st["lse"][5], st["lse"][9] = NAN, INF
+    st["cache"][0][st["table"][1][1], 1, 5, 7] = 0x7f
+    check_weigh(capi, st)
+    _, good = weigh(capi, st)
+    table = [list(t) for t in st["table"]]
+    table[1][0] = -1
+    _, w = weigh(capi, dict(st, table=table), want_err=(2, 303))
+    for p in st["table"][0][:3] + st["table"][1][1:5]:
+        assert torch.equal(w[p], good[p])
+    _, w = weigh(capi, dict(st, held=[140, 10 ** 6]), want_err=(2, 304))
+    assert torch.equal(w[st["table"][0][:3]], good[st["table"][0][:3]])
+    st["cache"][2][st["table"][1][0], 0] = -1.0       # a scale that no append writes: nothing from that head
+    _, w = weigh(capi, st, want_err=(2, 305))
+    assert torch.equal(w[st["table"][1][1:5]], good[st["table"][1][1:5]])
+
+
+@pytest.mark.parametrize("n_q,n_kv,dim,S,n,kv", [(32, 8, 128, 40, 16, 3000), (8, 8, 64, 9, 40, 5000), (40, 8, 128, 3, 200, 2000)])
+def test_weigh_many_rows_repeat_their_bits(capi, n_q, n_kv, dim, S, n, kv):
+    st = attn_state(n_q, n_kv, dim, [n - s % 3 for s in range(S)], [kv - 37 * s for s in range(S)], BF, seed=23)
+    attend(capi, st)
+    before, w = weigh(capi, st, fresh=True)
+    for _ in range(10):
+        assert torch.equal(weigh(capi, st, fresh=True)[1], w)
+    for s in range(S):
+        pages = st["table"][s][:-(-st["held"][s] // 64)]
+        got = (w[pages].double().flatten()[:st["held"][s]].sum() -
+               before[pages].double().flatten()[:st["held"][s] - (n - s % 3)].sum()).item()
+        assert abs(got - (n - s % 3) * n_q) < (n - s % 3) * n_q * 1e-4
 
 
 @pytest.mark.parametrize("count,observe,fresh", [([3, 0, 16, 1], 0, True), ([16, -4, 99, 2], 5, True), (None, 4, False),
