@@ -21,6 +21,7 @@
 // reads.  Where CTAs are few, a cluster shares the pages of a turn.
 
 #include "cluster_dev.cuh"
+#include "copy_dev.cuh"
 #include "gemm.cuh"
 #include "kv8.cuh"
 #include "kv8_attn_dev.cuh"
@@ -317,15 +318,6 @@ constexpr int MT = 256;               // threads of the move
 constexpr int MN = 4;                 // 16-byte pieces of a thread a turn
 constexpr int MS = 4;                 // turns in the ring
 constexpr int MRANKS = 8;             // CTAs of a cluster at most
-
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int HD> struct MoveSmem {
     static constexpr int rows = MT * MN * 16 / HD;                  // of a CTA and turn: whole pages

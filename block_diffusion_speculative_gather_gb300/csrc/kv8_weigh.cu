@@ -13,14 +13,16 @@
 // scores, exponents and sums are fp32.  tcgen05 would need the scores moved out
 // of tensor memory for the same exponentials, which are what many rows cost.
 //
-// An item is the 16 keys of each warp, all kv heads: no two CTAs add to the same
+// An item is 128 keys, 16 a warp, all kv heads: no two CTAs add to the same
 // position, so there are no atomics, and the order of the terms is fixed.  A CTA
 // has a run of neighbouring items.  Their rows pass through shared memory, 8 a warp
-// at a time, and stay there from item to item where a sequence has no more; keys go
-// straight to registers, two heads ahead, from one item into the next.
+// at a time, and stay there from item to item where a sequence has no more.  A warp's
+// keys come by asynchronous copies, three heads ahead, from one item into the
+// next; a lane reads what it copied itself, so that no barrier stands between.
 
 #include <type_traits>
 
+#include "copy_dev.cuh"
 #include "gemm.cuh"
 #include "kv8.cuh"
 #include "kv8_attn_dev.cuh"
@@ -31,20 +33,23 @@ namespace {
 
 using namespace kv8;
 
-template <int HD, int W> struct WeighSmem {
+constexpr int W = 8, WT = 32 * W, KEYS = 16 * W;
+constexpr int RING = 4;              // heads of a warp's keys, on their way or at hand
+
+template <int HD> struct WeighSmem {
     static constexpr int pitch = HD * 2 + 16;      // bytes: 8 lanes' rows fall on all banks
     uint8_t q[8 * W * pitch];
+    uint4 keys[W][RING][HD / 32][32];
+    float scale[W][RING];
     float2 col[8 * W];           // score factor, lse in base 2 (inf: the column does not count)
     int row[8 * W];
     int before[WSEQS + 1];       // items before each sequence
     int warp[W];
 };
 
-// W warps.
-template <typename T, int HD, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_constant__ Kv8WeighArgs a) {
-    using S_ = WeighSmem<HD, W>;
-    constexpr int WT = 32 * W, KEYS = 16 * W;
+template <typename T, int HD>
+__global__ void __launch_bounds__(WT, 2) kv8_weigh_kernel(const __grid_constant__ Kv8WeighArgs a) {
+    using S_ = WeighSmem<HD>;
     extern __shared__ __align__(16) uint8_t raw[];
     S_& sm = *reinterpret_cast<S_*>(raw);
     pdl_trigger();
@@ -53,50 +58,77 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
     const Run run = my_items<KEYS, WT>(a, sm.before, sm.warp);
     if (run.first >= run.last) return;
     int s = run.s;
-    const int depth = a.n_kv > 1 ? 2 : 1;          // heads that keys are fetched ahead
-    uint4 ahead[2][HD / 32];
-    float ahead_scale[2] = {0.f, 0.f};
-    bool carried = false, fresh_rows = true;
-    int carried_page = -1;
+    bool begins = true;                  // the item is the first of its sequence here
+    bool fresh_rows = true;
     Span q = span_of(a, s, false);
+    const int* table = nullptr;
+    const int off = 16 * warp % KV8_PAGE + g;        // of the lane's first key in its page
+    // the copies: head `h` of item `at` comes next, from `src`; `pg` its page (-1: none),
+    // `ahead` the table's entry for the item behind it, `end` the sequence's last here
+    int at = 0, h_next = 0, pg_next = -1, ahead = -1, end = 0;
+    unsigned step = 0, fetched = 0;                  // heads used, asked for
+    const uint8_t* src = nullptr;
+    auto key_of_item = [&](int item) { return (q.lo / KEYS + (item - sm.before[s])) * KEYS + 16 * warp; };
+    auto entry = [&](int item) {                     // raw: not looked at before it has arrived
+        const int key = key_of_item(item);
+        return item < end && key < q.hi && key + 16 > q.lo ? table[key / KV8_PAGE] : -0x7fffffff;
+    };
+    auto page = [&](int e) {
+        if (e >= 0 && e < a.n_pages) return e;
+        if (e != -0x7fffffff) report(a.err, DERR_INDEX, SITE_PAGE);
+        return -1;
+    };
+    auto fetch = [&]() {
+        const int slot = fetched % RING;
+        if (at < end && pg_next >= 0) {
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) {
+                copy_async16(&sm.keys[warp][slot][2 * i][lane], src + 64 * i);
+                copy_async16(&sm.keys[warp][slot][2 * i + 1][lane], src + 8 * HD + 64 * i);
+            }
+            if (lane == 0) copy_async4(&sm.scale[warp][slot], a.k_scale + (size_t)pg_next * a.n_kv + h_next);
+        }
+        copy_commit();
+        ++fetched;
+        src += KV8_PAGE * HD;
+        if (++h_next == a.n_kv) {
+            h_next = 0;
+            ++at;
+            pg_next = page(ahead);
+            src = a.k_codes + ((size_t)max(pg_next, 0) * a.n_kv * KV8_PAGE + off) * HD + 16 * c;
+            ahead = entry(at + 1);
+        }
+    };
     for (int item = run.first; item < run.last; ++item) {
         if (item >= sm.before[s + 1]) {
             do ++s;
             while (item >= sm.before[s + 1]);
             q = span_of(a, s, false);
-            carried = false;
+            begins = true;
+        }
+        if (begins) {
+            begins = false;
             fresh_rows = true;
+            table = a.table + (size_t)s * a.max_pages;
+            end = min(run.last, sm.before[s + 1]);
+            copy_wait<0>();              // (all groups are empty: nothing is asked for behind a sequence's end)
+            __syncwarp();
+            step = fetched = 0;
+            at = item;
+            h_next = 0;
+            pg_next = page(entry(item));
+            src = a.k_codes + ((size_t)max(pg_next, 0) * a.n_kv * KV8_PAGE + off) * HD + 16 * c;
+            ahead = entry(item + 1);
+            for (int i = 0; i < RING - 1; ++i) fetch();
         }
-        const int* table = a.table + (size_t)s * a.max_pages;
-        const int key0 = (q.lo / KEYS + (item - sm.before[s])) * KEYS + 16 * warp;   // the warp's first key
-        auto page_of = [&](int key) {              // -1: nothing to do there
-            if (!(key < q.hi && key + 16 > q.lo)) return -1;
-            const int pg = table[key / KV8_PAGE];
-            if (pg >= 0 && pg < a.n_pages) return pg;
-            report(a.err, DERR_INDEX, SITE_PAGE);
-            return -1;
-        };
-        const int off = key0 % KV8_PAGE;           // the same in every item (items are whole pages)
-        auto fetch = [&](int page, int h, uint4 (&x)[HD / 32], float* scale) {
-            if (page < 0) return;
-            const size_t at = (size_t)page * a.n_kv + h;
-            const uint8_t* src = a.k_codes + (at * KV8_PAGE + off + g) * HD + 16 * c;
-#pragma unroll
-            for (int i = 0; i < HD / 64; ++i) {
-                x[2 * i] = *reinterpret_cast<const uint4*>(src + 64 * i);
-                x[2 * i + 1] = *reinterpret_cast<const uint4*>(src + 8 * HD + 64 * i);
-            }
-            *scale = a.k_scale[at];
-        };
-        const int pg = carried ? carried_page : page_of(key0);
+        const int key0 = key_of_item(item);          // the warp's first key
+        int pg = -1;
+        if (key0 < q.hi && key0 + 16 > q.lo) {
+            pg = table[key0 / KV8_PAGE];
+            if (pg < 0 || pg >= a.n_pages) pg = -1;  // reported with the copies
+        }
         const bool active = pg >= 0;
-        if (!carried) {
-            fetch(pg, 0, ahead[0], ahead_scale);
-            if (depth > 1) fetch(pg, 1, ahead[1], ahead_scale + 1);
-        }
-        const int next_pg = item + 1 < min(run.last, sm.before[s + 1]) ? page_of(key0 + KEYS) : -1;
-        carried = false;
-        float* wp = a.weights + (size_t)max(pg, 0) * KV8_PAGE + off + g;
+        float* wp = a.weights + (size_t)max(pg, 0) * KV8_PAGE + off;
         float old[2] = {0.f, 0.f};
         if (active && c == 0)
 #pragma unroll
@@ -117,7 +149,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
         }
         uint32_t k[HD / 16][4];
         float scale = 0.f, sum[2] = {0.f, 0.f};
-        int head = -1, in_head = per_head;         // of the next block: its head's first in_head have been done
+        int in_head = per_head;          // of the next block: its head's first in_head have been done
+        const unsigned done = step + a.n_kv;
         for (int b0 = 0; b0 < blocks; b0 += W) {
             if (fresh_rows) {
                 __syncthreads();                   // the rows before have been used
@@ -216,12 +249,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
             for (int b = 0; b < most;) {
                 if (in_head == per_head) {         // the next head's keys
                     in_head = 0;
-                    ++head;
+                    __syncwarp();                  // the scale's place has been read
+                    fetch();
+                    copy_wait<RING - 1>();
+                    __syncwarp();                  // lane 0's copy of the scale
+                    const int slot = step++ % RING;
 #pragma unroll
                     for (int i = 0; i < HD / 64; ++i) {
-                        const uint32_t lo[4] = {ahead[0][2 * i].x, ahead[0][2 * i].y, ahead[0][2 * i].z, ahead[0][2 * i].w};
-                        const uint32_t up[4] = {ahead[0][2 * i + 1].x, ahead[0][2 * i + 1].y, ahead[0][2 * i + 1].z,
-                                                ahead[0][2 * i + 1].w};
+                        const uint4 x = sm.keys[warp][slot][2 * i][lane], y = sm.keys[warp][slot][2 * i + 1][lane];
+                        const uint32_t lo[4] = {x.x, x.y, x.z, x.w}, up[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             k[4 * i + j][0] = f16_of_codes(lo[j]);
@@ -230,21 +266,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
                             k[4 * i + j][3] = f16_of_codes(up[j] >> 16);
                         }
                     }
-                    scale = ahead_scale[0];
+                    scale = sm.scale[warp][slot];
                     if (!(scale >= 0.f && scale < INFINITY)) {
                         report(a.err, DERR_INDEX, SITE_SCALE);
                         scale = __int_as_float(0x7fffffff);     // scores that add nothing
-                    }
-                    const int h = head + depth;
-                    const bool here = h < a.n_kv;
-                    const int page = here ? pg : next_pg, hh = here ? h : h - a.n_kv;
-                    if (depth > 1) {
-#pragma unroll
-                        for (int i = 0; i < HD / 32; ++i) ahead[0][i] = ahead[1][i];
-                        ahead_scale[0] = ahead_scale[1];
-                        fetch(page, hh, ahead[1], ahead_scale + 1);
-                    } else {
-                        fetch(page, hh, ahead[0], ahead_scale);
                     }
                 }
                 float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -264,9 +289,10 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
                 }
             }
         }
-        if (!none && blocks > 0 && next_pg >= 0) {
-            carried = true;                        // the first heads of the next item are on their way
-            carried_page = next_pg;
+        while (step != done) {           // heads that were not looked at: their places are free once written
+            fetch();
+            copy_wait<RING - 1>();
+            ++step;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -278,30 +304,21 @@ __global__ void __launch_bounds__(32 * W, 16 / W) kv8_weigh_kernel(const __grid_
     }
 }
 
-template <typename T, int HD, int W>
-int launch_weigh(const Kv8WeighArgs& a, int sms, cudaStream_t s) {
-    const size_t smem = sizeof(WeighSmem<HD, W>);
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_weigh_kernel<T, HD, W>));
+template <typename T, int HD>
+int launch_t(const Kv8WeighArgs& a, int sms, cudaStream_t s) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv8_weigh_kernel<T, HD>));
     if (e != cudaSuccess) return (int)e;
-    const int room = 16 / W * sms;
-    const long long most = (long long)a.S * (((long long)a.max_pages * KV8_PAGE + 16 * W - 1) / (16 * W));   // items
-    return (int)launch_k(kv8_weigh_kernel<T, HD, W>, dim3((unsigned)(most < room ? most : room)), dim3(32 * W), smem, s, a);
-}
-
-template <typename T>
-int launch_t(const Kv8WeighArgs& a, int head_dim, bool many, int sms, cudaStream_t s) {
-    if (head_dim == 128) return many ? launch_weigh<T, 128, 16>(a, sms, s) : launch_weigh<T, 128, 8>(a, sms, s);
-    return many ? launch_weigh<T, 64, 16>(a, sms, s) : launch_weigh<T, 64, 8>(a, sms, s);
+    const long long most = (long long)a.S * ((a.max_pages + 1) / 2);   // items
+    return (int)launch_k(kv8_weigh_kernel<T, HD>, dim3((unsigned)(most < 2 * sms ? most : 2 * sms)), dim3(WT),
+                         sizeof(WeighSmem<HD>), s, a);
 }
 
 }  // namespace
 
 int launch_kv8_weigh(const Kv8WeighArgs& a, int head_dim, int sms, cudaStream_t s) {
-    // many rows a sequence: more warps share what passes through shared memory
-    long long rows = a.rows;
-    if (a.observe > 0 && rows > (long long)a.observe * a.S) rows = (long long)a.observe * a.S;
-    const bool many = rows * a.n_q > 128LL * a.S;
-    return a.dtype == 1 ? launch_t<__nv_bfloat16>(a, head_dim, many, sms, s) : launch_t<__half>(a, head_dim, many, sms, s);
+    if (a.dtype == 1)
+        return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, sms, s) : launch_t<__nv_bfloat16, 64>(a, sms, s);
+    return head_dim == 128 ? launch_t<__half, 128>(a, sms, s) : launch_t<__half, 64>(a, sms, s);
 }
 
 }  // namespace dfl

@@ -32,7 +32,7 @@ namespace {
 using namespace kv8;
 
 constexpr int TILE = 128;                      // keys of an item, columns of a tile at most
-constexpr int CONV_WARP = 8, CONV = 4, ISSUE_WARP = 12, LOAD_WARP = 13, TCT = 32 * 14;
+constexpr int CONV_WARP = 8, CONV = 4, ISSUE_WARP = 12, TCT = 32 * 14;      // and a warp that loads
 constexpr int SITE_WEIGH = 340;                // + role
 
 template <int HD> struct TcWeighSmem {
@@ -186,8 +186,6 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         float* part = reinterpret_cast<float*>(sm + L::part);
         unsigned n = 0;                              // tiles so far
         bool ok = true;
-        float held = 0.f;                            // -lse of column r of this group's next tile
-        bool holds;
         // once a wait has run out these warps go on to the end without waiting, so that
         // none stays behind at a barrier
         for (w.item = run.first; w.item < run.last; ++w.item) {
@@ -198,38 +196,38 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             float old = 0.f;
             if (t == 0 && mine && !(a.fresh && j >= w.q.first)) old = *wp;
             // pairs that see the key: [from, to)
-            long long from = 0, to = w.packed;
+            int from = 0, to = w.packed;
             if (a.causal) {
                 const long long i = (long long)j - w.q.first - w.q.i0;
-                from = i > 0 ? i * a.group : 0;
-                if (a.window > 0) to = min(to, (i + a.window) * a.group);
+                from = (int)min(max(i, 0ll) * a.group, (long long)w.packed);
+                if (a.window > 0) to = (int)min(max(i + a.window, 0ll) * a.group, (long long)w.packed);
             } else if (a.window > 0 && j < (long long)w.q.first - a.window) {
                 to = 0;
             }
             if (!mine || to < from) from = to = 0;
             const int tiles = w.t1 - w.t0, all = tiles * a.n_kv;
-            // -lse of column r of the item's idx-th tile
-            auto neg_lse = [&](int idx) {
-                const int h = idx / tiles, p = (w.t0 + idx - h * tiles) * per_tile + r, i = p / a.group;
-                if (r >= per_tile || p >= w.packed) return -INFINITY;
-                const float v = a.lse[(long long)(w.q.r0 + w.q.i0 + i) * a.n_q + h * a.group + p - i * a.group];
-                return v > -INFINITY ? -v * 1.4426950408889634f : -INFINITY;
+            // lse of column r of a tile of head h (-inf: it does not count)
+            const int ri = r / a.group, rg = r - ri * a.group;
+            auto lse_at = [&](int h, int tile) {
+                if (r >= per_tile || tile * per_tile + r >= w.packed) return -INFINITY;
+                return a.lse[(long long)(w.q.r0 + w.q.i0 + tile * rows_tile + ri) * a.n_q + h * a.group + rg];
             };
             auto scale_of = [&](int h) { return pg >= 0 && h < a.n_kv ? a.k_scale[(size_t)pg * a.n_kv + h] : 0.f; };
             const int idx0 = (int)((n & 1) != (unsigned)t);        // this group's first tile of the item
-            int head = -1;
-            float scale = 0.f, next_scale = scale_of(0);
+            int h = 0, tile = w.t0 + idx0, head = -1;              // the tile at hand
+            if (tile >= w.t1) tile -= tiles, ++h;
+            float scale = 0.f, next_scale = scale_of(0), lse = idx0 < all ? lse_at(h, tile) : 0.f;
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            holds = false;
             for (int idx = idx0; idx < all; idx += 2) {
                 const unsigned m = n + idx;                        // the CTA's m-th tile
-                const unsigned mine_n = m >> 1;                    // this group's
-                const float nl = holds ? held : neg_lse(idx);
-                col[(mine_n & 1) * TILE + r] = nl;
-                holds = idx + 2 < all;
-                if (holds) held = neg_lse(idx + 2);
-                const int h = idx / tiles, c0 = (w.t0 + idx - h * tiles) * per_tile;
-                while (head < h) {
+                float* cl = col + ((m >> 1) & 1) * TILE;
+                cl[r] = lse > -INFINITY ? lse * -1.4426950408889634f : -INFINITY;
+                // the next one's; what it loads is not used before
+                const int c0 = tile * per_tile, now = h;
+                tile += 2;
+                while (tile >= w.t1) tile -= tiles, ++h;
+                if (idx + 2 < all) lse = lse_at(h, tile);
+                while (head < now) {
                     scale = next_scale;
                     ++head;
                     next_scale = scale_of(head + 1);
@@ -244,14 +242,13 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
                 tc::fence_after_sync();
                 const float f = scale * a.scale_log2;
                 const float2 f2 = make_float2(f, f);
-                const float* cl = col + (mine_n & 1) * TILE;
                 const bool whole = __all_sync(0xffffffffu, from <= c0 && to >= min(c0 + per_tile, w.packed));
                 const int cols = min((min(per_tile, w.packed - c0) + 31) / 32, 4);
-                uint32_t d[32];
-                for (int b = 0; b < cols; ++b) {
-                    tc::ld_x32_async(tm + (m & 3) * TILE + lanes + 32 * b, d);
+                auto take = [&](int b, uint32_t (&d)[32], uint32_t (&ahead)[32]) {
                     tc::ld_wait(d);
-                    if (b == cols - 1) {
+                    if (b + 1 < cols) {
+                        tc::ld_x32_async(tm + (m & 3) * TILE + lanes + 32 * (b + 1), ahead);
+                    } else {
                         tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(s_free + (m & 3));
@@ -267,14 +264,24 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
                             acc[1] = add2(acc[1], make_float2(ex2(fmaxf(v.x, -200.f)), ex2(fmaxf(v.y, -200.f))));
                         }
                     } else {
+                        const int at = c0 + 32 * b - from;
+                        const unsigned seen = (unsigned)(to - from);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const long long p = c0 + 32 * b + x;
-                            const float y = fmaxf(fmaf(__uint_as_float(d[x]), f, cl[32 * b + x]), -200.f);
-                            acc[x & 1].x += p >= from && p < to ? ex2(y) : 0.f;
+                        for (int x = 0; x < 32; x += 2) {
+                            const float2 l = *reinterpret_cast<const float2*>(cl + 32 * b + x);
+                            const float2 u = fma2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), f2, l);
+                            acc[0] = add2(acc[0], make_float2((unsigned)(at + x) < seen ? ex2(fmaxf(u.x, -200.f)) : 0.f,
+                                                              (unsigned)(at + x + 1) < seen ? ex2(fmaxf(u.y, -200.f)) : 0.f));
                         }
                     }
-                }
+                };
+                // 32 columns are on their way while 32 are summed
+                uint32_t d0[32], d1[32];
+                tc::ld_x32_async(tm + (m & 3) * TILE + lanes, d0);
+                take(0, d0, d1);
+                if (cols > 1) take(1, d1, d0);
+                if (cols > 2) take(2, d0, d1);
+                if (cols > 3) take(3, d1, d0);
             }
             n += all;
             // the second group's sums to the first
@@ -299,28 +306,33 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
                 if (!ok) break;
                 const uint8_t* src = sm + L::raw + b * L::RB;
                 uint8_t* dst = sm + L::k + b * L::KB;
-                constexpr int CH = HD / 16;          // 16-byte chunks of a key
+                constexpr int CH = HD / 16, ALL = TILE * CH / (32 * CONV), N = 4;    // 16-byte chunks of a key, of a lane
 #pragma unroll
-                for (int i = 0; i < TILE * CH / (32 * CONV); ++i) {
-                    const int at = (i * CONV + cw) * 32 + lane, key = at / CH, ch = at % CH;
-                    const uint4 x = lds128(src + at * 16);
-                    const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[8];
+                for (int i0 = 0; i0 < ALL; i0 += N) {
+                    uint4 x[N];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = f16_of_codes(e[k]);
-                        o[2 * k + 1] = f16_of_codes(e[k] >> 16);
-                    }
-                    if constexpr (!std::is_same<T, __half>::value) {
+                    for (int i = 0; i < N; ++i) x[i] = lds128(src + (((i0 + i) * CONV + cw) * 32 + lane) * 16);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
-                            o[k] = pack_bf16x2(v.x, v.y);
+                    for (int i = 0; i < N; ++i) {
+                        const int at = ((i0 + i) * CONV + cw) * 32 + lane, key = at / CH, ch = at % CH;
+                        const uint32_t e[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            o[2 * k] = f16_of_codes(e[k]);
+                            o[2 * k + 1] = f16_of_codes(e[k] >> 16);
                         }
+                        if constexpr (!std::is_same<T, __half>::value) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                                o[k] = pack_bf16x2(v.x, v.y);
+                            }
+                        }
+                        uint8_t* d = dst + (ch >> 2) * TILE * 128;
+                        *reinterpret_cast<uint4*>(d + swz128(key, 2 * (ch & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(d + swz128(key, 2 * (ch & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    uint8_t* d = dst + (ch >> 2) * TILE * 128;
-                    *reinterpret_cast<uint4*>(d + swz128(key, 2 * (ch & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(d + swz128(key, 2 * (ch & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 tc::fence_async_smem();
                 __threadfence_block();               // the codes have been read before their place goes back
@@ -426,10 +438,10 @@ int launch_tc(const CUtensorMap& q_map, const Kv8WeighArgs& a, int sms, cudaStre
 }  // namespace
 
 #ifndef WEIGH_TC_FROM
-#define WEIGH_TC_FROM 32
+#define WEIGH_TC_FROM 20
 #endif
 bool kv8_weigh_by_tc(const Kv8WeighArgs& a) {
-    long long rows = (a.rows + a.S - 1) / a.S;
+    long long rows = a.rows / a.S;
     if (a.observe > 0 && rows > a.observe) rows = a.observe;
     // a tensor map's strides are above 0 and below 2^40 bytes
     const bool fits = a.q_row > 0 && a.q_head > 0 && a.q_row < (1LL << 39) && a.q_head < (1LL << 39);
