@@ -217,7 +217,7 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             int h = 0, tile = w.t0 + idx0, head = -1;              // the tile at hand
             if (tile >= w.t1) tile -= tiles, ++h;
             float scale = 0.f, next_scale = scale_of(0), lse = idx0 < all ? lse_at(h, tile) : 0.f;
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int idx = idx0; idx < all; idx += 2) {
                 const unsigned m = n + idx;                        // the CTA's m-th tile
                 float* cl = col + ((m >> 1) & 1) * TILE;
@@ -243,50 +243,54 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
                 const float f = scale * a.scale_log2;
                 const float2 f2 = make_float2(f, f);
                 const bool whole = __all_sync(0xffffffffu, from <= c0 && to >= min(c0 + per_tile, w.packed));
-                const int cols = min((min(per_tile, w.packed - c0) + 31) / 32, 4);
-                auto take = [&](int b, uint32_t (&d)[32], uint32_t (&ahead)[32]) {
-                    tc::ld_wait(d);
-                    if (b + 1 < cols) {
-                        tc::ld_x32_async(tm + (m & 3) * TILE + lanes + 32 * (b + 1), ahead);
+                const int cols = (min(per_tile, w.packed - c0) + 31) / 32 * 2;      // by 16
+                // 16 columns: their scores, then their weights, side by side
+                auto take = [&](int b, uint32_t (&d)[16]) {
+                    float2 u[8];
+#pragma unroll
+                    for (int x = 0; x < 8; x += 2) {
+                        const float4 l = *reinterpret_cast<const float4*>(cl + 16 * b + 2 * x);
+                        u[x] = fma2(make_float2(__uint_as_float(d[2 * x]), __uint_as_float(d[2 * x + 1])), f2, make_float2(l.x, l.y));
+                        u[x + 1] = fma2(make_float2(__uint_as_float(d[2 * x + 2]), __uint_as_float(d[2 * x + 3])), f2, make_float2(l.z, l.w));
+                    }
+                    if (!whole) {
+                        const int at = c0 + 16 * b - from;
+                        const unsigned seen = (unsigned)(to - from);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            if ((unsigned)(at + 2 * x) >= seen) u[x].x = -200.f;
+                            if ((unsigned)(at + 2 * x + 1) >= seen) u[x].y = -200.f;
+                        }
+                    }
+                    // a NaN score (a NaN code) adds nothing: 2^-200 is 0
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) u[x] = make_float2(ex2(fmaxf(u[x].x, -200.f)), ex2(fmaxf(u[x].y, -200.f)));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[x] = add2(acc[x], add2(u[x], u[x + 4]));
+                };
+                uint32_t d0[16], d1[16];
+                const uint32_t sc = tm + (m & 3) * TILE + lanes;
+                tc::ld_x16_async(sc, d0);
+                for (int b = 0; b < cols; b += 2) {            // 16 columns are on their way while 16 are summed
+                    tc::ld_wait16(d0);
+                    tc::ld_x16_async(sc + 16 * (b + 1), d1);
+                    take(b, d0);
+                    tc::ld_wait16(d1);
+                    if (b + 2 < cols) {
+                        tc::ld_x16_async(sc + 16 * (b + 2), d0);
                     } else {
                         tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(s_free + (m & 3));
                     }
-                    if (whole) {
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(cl + 32 * b + x);
-                            const float2 u = fma2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), f2, make_float2(l.x, l.y));
-                            const float2 v = fma2(make_float2(__uint_as_float(d[x + 2]), __uint_as_float(d[x + 3])), f2, make_float2(l.z, l.w));
-                            // a NaN score (a NaN code) adds nothing: 2^-200 is 0
-                            acc[0] = add2(acc[0], make_float2(ex2(fmaxf(u.x, -200.f)), ex2(fmaxf(u.y, -200.f))));
-                            acc[1] = add2(acc[1], make_float2(ex2(fmaxf(v.x, -200.f)), ex2(fmaxf(v.y, -200.f))));
-                        }
-                    } else {
-                        const int at = c0 + 32 * b - from;
-                        const unsigned seen = (unsigned)(to - from);
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            const float2 l = *reinterpret_cast<const float2*>(cl + 32 * b + x);
-                            const float2 u = fma2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), f2, l);
-                            acc[0] = add2(acc[0], make_float2((unsigned)(at + x) < seen ? ex2(fmaxf(u.x, -200.f)) : 0.f,
-                                                              (unsigned)(at + x + 1) < seen ? ex2(fmaxf(u.y, -200.f)) : 0.f));
-                        }
-                    }
-                };
-                // 32 columns are on their way while 32 are summed
-                uint32_t d0[32], d1[32];
-                tc::ld_x32_async(tm + (m & 3) * TILE + lanes, d0);
-                take(0, d0, d1);
-                if (cols > 1) take(1, d1, d0);
-                if (cols > 2) take(2, d0, d1);
-                if (cols > 3) take(3, d1, d0);
+                    take(b + 1, d1);
+                }
             }
             n += all;
             // the second group's sums to the first
             const int par = w.item & 1;
-            const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            const float2 both = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+            const float sum = both.x + both.y;
             if (t == 1) part[par * TILE + r] = sum;
             asm volatile("bar.sync 3, 256;" ::: "memory");
             if (t == 0 && mine && ok) *wp = old + (sum + part[par * TILE + r]);
