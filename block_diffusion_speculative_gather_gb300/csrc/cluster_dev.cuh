@@ -1,4 +1,4 @@
-// Thread-block clusters: barriers, a word of another CTA's shared memory, launch.
+// Thread-block clusters: barriers, words sent to another CTA, launch.
 #pragma once
 
 #include "common.cuh"
@@ -19,11 +19,22 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// Writes the word that lies in CTA `rank` where p lies in this one.
-__device__ __forceinline__ void put_remote(void* p, uint32_t rank, uint32_t v) {
-    uint32_t at;
+// The opening barrier of CTAs that send to each other's mbarriers: initialised ones
+// (fence_mbar_init) are seen behind the wait.  No other memory is ordered, so no
+// store or load in flight is waited for.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+
+// Sends a word to where p lies in this CTA, in CTA `rank`, and four bytes to its
+// mbarrier that lies where bar does.
+__device__ __forceinline__ void send_word(void* p, uint64_t* bar, uint32_t rank, uint32_t v) {
+    uint32_t at, b;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(at), "r"(v), "r"(b)
+                 : "memory");
 }
 
 // launch_k with clusters of `ranks` CTAs in a row.

@@ -84,26 +84,40 @@ constexpr int CT = 512, CW = CT / 32;
 
 template <typename T> constexpr int per_vec() { return 16 / (int)sizeof(T); }
 
+// One exchange between the CTAs of a cluster: each sends its word to all, and waits
+// for all words by an mbarrier that counts their bytes (a barrier of the cluster
+// that orders memory took 3 us in its place).
 struct Trade {
-    uint32_t warp[CW];
     uint32_t all[16];
+    uint64_t bar;
 };
 
-// The largest / the sum of a warp value over the cluster, the same everywhere.
-// `first`: the cluster's opening barrier is still to be waited for.
+// By one thread, then the cluster's opening barrier.
+__device__ __forceinline__ void open_trade(Trade& t, int ranks) {
+    mbar_init(&t.bar, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&t.bar, 4 * ranks);
+}
+
+// By all threads, v the same in all of the CTA; false: the others' did not come.
+__device__ __forceinline__ bool trade(Trade& t, uint32_t v, int ranks, uint32_t rank) {
+    if ((int)threadIdx.x < ranks) send_word(&t.all[rank], &t.bar, threadIdx.x, v);
+    return mbar_wait_bounded(&t.bar, 0);
+}
+
+// The largest / the sum of a warp value over the cluster, the same everywhere; NaN
+// if the other CTAs' did not come.  `first`: the opening barrier is still to be waited for.
 template <typename F>
-__device__ __forceinline__ float trade(Trade& t, float v, int ranks, uint32_t rank, bool first, F op) {
+__device__ __forceinline__ float over_cluster(Trade& t, float* warps, float v, int ranks, uint32_t rank, bool first, F op) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) t.warp[warp] = __float_as_uint(v);
+    if (lane == 0) warps[warp] = v;
     __syncthreads();
-    if (first && ranks > 1) cluster_wait();
-    float r = __uint_as_float(t.warp[0]);
+    float r = warps[0];
 #pragma unroll
-    for (int i = 1; i < CW; ++i) r = op(r, __uint_as_float(t.warp[i]));
+    for (int i = 1; i < CW; ++i) r = op(r, warps[i]);
     if (ranks == 1) return r;
-    if ((int)threadIdx.x < ranks) put_remote(&t.all[rank], threadIdx.x, __float_as_uint(r));
-    cluster_arrive();
-    cluster_wait();
+    if (first) cluster_wait();
+    if (!trade(t, __float_as_uint(r), ranks, rank)) return __int_as_float(0x7fffffff);
     r = __uint_as_float(t.all[0]);
     for (int i = 1; i < ranks; ++i) r = op(r, __uint_as_float(t.all[i]));
     return r;
@@ -116,6 +130,7 @@ __global__ void __launch_bounds__(CT, K * per_vec<T>() > 12 ? 2 : 3)
 probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     constexpr int VE = per_vec<T>();
     __shared__ Trade s_max, s_sum;
+    __shared__ float s_warps[2][CW];
     __shared__ RowSetup s_setup;
     __shared__ int s_best;
     pdl_trigger();
@@ -125,7 +140,13 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     pdl_wait();
     const float t = a.temperature[row];
     if (!(t >= 0.f) || t == INFINITY) return;      // such a row is left as it was, by all of the cluster
-    if (ranks > 1) cluster_arrive();
+    if (ranks > 1) {
+        if (tid == 0) {
+            open_trade(s_max, ranks);
+            open_trade(s_sum, ranks);
+        }
+        cluster_arrive_relaxed();
+    }
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
     float* p = a.p + row * a.p_row;
     const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
@@ -162,8 +183,8 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     float m = no_nan(extra);                       // fmaxf leaves NaN out
 #pragma unroll
     for (int i = 0; i < K * VE; ++i) m = fmaxf(m, w[i]);
-    m = trade(s_max, warp_max(m), ranks, rank, true, [](float x, float y) { return fmaxf(x, y); });
-    if (t == 0.f || m == -INFINITY) {
+    m = over_cluster(s_max, s_warps[0], warp_max(m), ranks, rank, true, [](float x, float y) { return fmaxf(x, y); });
+    if (t == 0.f || m == -INFINITY) {     // (a NaN m, of a wait that ran out, makes the row NaN)
         int best = 0x7fffffff;
         if (m != -INFINITY) {
 #pragma unroll
@@ -177,12 +198,8 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
         if ((tid & 31) == 0) atomicMin(&s_best, best);
         __syncthreads();
         best = s_best;
-        if (ranks > 1) {
-            if (tid < ranks) put_remote(&s_sum.all[rank], tid, (uint32_t)best);
-            cluster_arrive();
-            cluster_wait();
+        if (ranks > 1 && trade(s_sum, (uint32_t)best, ranks, rank))
             for (int i = 0; i < ranks; ++i) best = min(best, (int)s_sum.all[i]);
-        }
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -206,7 +223,7 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
                 sum += w[i];
             }
         }
-        sum = trade(s_sum, warp_sum(sum), ranks, rank, false, [](float x, float y) { return x + y; });
+        sum = over_cluster(s_sum, s_warps[1], warp_sum(sum), ranks, rank, false, [](float x, float y) { return x + y; });
         const float inv = 1.f / sum;
         extra *= inv;
 #pragma unroll
