@@ -12,14 +12,17 @@
 //
 // A row's maximum is needed before its sum and its sum before its first output:
 // the row stays on the SMs between.  A cluster of up to 16 CTAs holds it in
-// registers (up to 40 logits a thread, 512 threads a CTA), trades maxima and sums
-// through distributed shared memory, and writes what it read once.  Larger rows
-// (above 327680 logits) are read three times, by one CTA.
+// registers (up to 40 logits a thread), trades maxima and sums through distributed
+// shared memory, and writes what it read once.  Rows that all run at once are
+// read straight into registers; more of them go through clusters that stay, whose
+// next row comes by a bulk copy to shared memory while one is worked on.  Larger
+// rows (above 307200 logits) are read three times, by one CTA.
 
 #include <mutex>
 
 #include "cluster_dev.cuh"
 #include "gemm.cuh"
+#include "kv8.cuh"
 #include "sampling.cuh"
 
 namespace dfl {
@@ -80,135 +83,138 @@ __device__ __forceinline__ float row_min_p(const ProbsArgs& a, long long row) { 
 
 // ---- rows held by a cluster
 
-constexpr int CT = 512, CW = CT / 32;
+constexpr int CT = 512;                // threads of a CTA that has a row,
+constexpr int ST = 1024, STREAM_CT = ST - 32;      // of one that stays: all, and those at work
 
 template <typename T> constexpr int per_vec() { return 16 / (int)sizeof(T); }
 
 // One exchange between the CTAs of a cluster: each sends its word to all, and waits
 // for all words by an mbarrier that counts their bytes (a barrier of the cluster
-// that orders memory took 3 us in its place).
+// that orders memory took 3 us in its place).  A CTA's words of the next row cannot
+// come before it has this row's: nobody passes the second exchange without it.
 struct Trade {
     uint32_t all[16];
     uint64_t bar;
 };
 
+// What the threads at work on a row share.
+struct RowShared {
+    Trade max, sum;
+    float warps[2][ST / 32];
+    int best[2];
+};
+
 // By one thread, then the cluster's opening barrier.
-__device__ __forceinline__ void open_trade(Trade& t, int ranks) {
-    mbar_init(&t.bar, 1);
+__device__ __forceinline__ void open_row(RowShared& sh) {
+    mbar_init(&sh.max.bar, 1);
+    mbar_init(&sh.sum.bar, 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(&t.bar, 4 * ranks);
+    sh.best[0] = sh.best[1] = 0x7fffffff;
 }
 
-// By all threads, v the same in all of the CTA; false: the others' did not come.
-__device__ __forceinline__ bool trade(Trade& t, uint32_t v, int ranks, uint32_t rank) {
+// A barrier of the NT threads at work.
+template <int NT> __device__ __forceinline__ void work_sync() {
+    if (NT == CT) __syncthreads();
+    else asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+}
+
+// v the same in all of the CTA, the turn-th exchange by t; false: the others' did not come.
+__device__ __forceinline__ bool trade(Trade& t, uint32_t v, int ranks, uint32_t rank, unsigned turn) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&t.bar, 4 * ranks);
     if ((int)threadIdx.x < ranks) send_word(&t.all[rank], &t.bar, threadIdx.x, v);
-    return mbar_wait_bounded(&t.bar, 0);
+    return mbar_wait_bounded(&t.bar, turn & 1);
 }
 
-// The largest / the sum of a warp value over the cluster, the same everywhere; NaN
+__device__ __forceinline__ float warp_all(float v, bool sum) { return sum ? warp_sum(v) : warp_max(v); }
+
+// The sum (or the largest) of a warp value over the cluster, the same everywhere; NaN
 // if the other CTAs' did not come.  `first`: the opening barrier is still to be waited for.
-template <typename F>
-__device__ __forceinline__ float over_cluster(Trade& t, float* warps, float v, int ranks, uint32_t rank, bool first, F op) {
+// A lane takes a warp's (a CTA's) value and the warp joins them: every thread
+// reading all of them cost as many instructions as 20 logits.
+template <int NT>
+__device__ __forceinline__ float over_cluster(Trade& t, float* warps, float v, bool sum, int ranks, uint32_t rank, unsigned turn,
+                                              bool first) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float none = sum ? 0.f : -INFINITY;
     if (lane == 0) warps[warp] = v;
-    __syncthreads();
-    float r = warps[0];
-#pragma unroll
-    for (int i = 1; i < CW; ++i) r = op(r, warps[i]);
+    work_sync<NT>();
+    const float r = warp_all(lane < NT / 32 ? warps[lane] : none, sum);
     if (ranks == 1) return r;
     if (first) cluster_wait();
-    if (!trade(t, __float_as_uint(r), ranks, rank)) return __int_as_float(0x7fffffff);
-    r = __uint_as_float(t.all[0]);
-    for (int i = 1; i < ranks; ++i) r = op(r, __uint_as_float(t.all[i]));
-    return r;
+    if (!trade(t, __float_as_uint(r), ranks, rank, turn)) return __int_as_float(0x7fffffff);
+    return warp_all(lane < ranks ? __uint_as_float(t.all[lane]) : none, sum);
 }
 
-// K vectors of 16 bytes a thread.  The vectors begin at 16-byte boundaries of the
-// logits; the few before the first and behind the last are one more a thread.
-template <typename T, int K>
-__global__ void __launch_bounds__(CT, K * per_vec<T>() > 12 ? 2 : 3)
-probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
+// Where a CTA's part of a row lies: vectors of 16 bytes that begin at 16-byte
+// boundaries of the logits; the few tokens before the first and behind the last
+// are one more a thread of the first CTA.
+struct Part {
+    int head, v0, n;          // tokens before the vectors; this CTA's n (may be negative) from the v0-th on
+    int tail, tail_at;        // tokens behind the vectors, the first of them
+};
+
+// RAGGED false: rows of whole vectors.
+template <typename T, bool RAGGED>
+__device__ __forceinline__ Part part_of_row(const T* x, int vocab, int ranks, uint32_t rank) {
     constexpr int VE = per_vec<T>();
-    __shared__ Trade s_max, s_sum;
-    __shared__ float s_warps[2][CW];
-    __shared__ RowSetup s_setup;
-    __shared__ int s_best;
-    pdl_trigger();
+    const int off = RAGGED ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0;
+    Part p;
+    p.head = min(off ? VE - off : 0, vocab);
+    const int vecs = (vocab - p.head) / VE, per = (vecs + ranks - 1) / ranks;
+    p.v0 = (int)rank * per;
+    p.n = min(per, vecs - p.v0);
+    p.tail_at = p.head + vecs * VE;
+    p.tail = RAGGED ? vocab - p.tail_at : 0;
+    return p;
+}
+
+// The extra token of this thread; -1: none.
+template <bool RAGGED>
+__device__ __forceinline__ int extra_of(const Part& p, uint32_t rank) {
     const int tid = threadIdx.x;
-    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
-    const long long row = blockIdx.x / (unsigned)ranks;
-    pdl_wait();
-    const float t = a.temperature[row];
-    if (!(t >= 0.f) || t == INFINITY) return;      // such a row is left as it was, by all of the cluster
-    if (ranks > 1) {
-        if (tid == 0) {
-            open_trade(s_max, ranks);
-            open_trade(s_sum, ranks);
-        }
-        cluster_arrive_relaxed();
-    }
-    const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
-    float* p = a.p + row * a.p_row;
-    const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int head = min(off ? VE - off : 0, a.vocab);
-    const int vecs = (a.vocab - head) / VE, per = (vecs + ranks - 1) / ranks;
-    const int v0 = (int)rank * per, n = min(per, vecs - v0);      // this CTA's vectors (n may be negative)
-    const T* xv = x + head + (long long)v0 * VE;
-    float w[K * VE], extra = -INFINITY;
-    int e = -1;                                                   // the extra one's index
-    {
-        uint4 raw[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int v = k * CT + tid;
-            if (v < n) raw[k] = reinterpret_cast<const uint4*>(xv)[v];
-        }
-        if (rank == 0) {
-            const int tail = a.vocab - head - vecs * VE;
-            if (tid < head) e = tid;
-            else if (tid >= 16 && tid < 16 + tail) e = a.vocab - tail + tid - 16;
-            if (e >= 0) extra = to_f32(x[e]);
-        }
-        if (tid == CT - 1) {      // while they are on their way
-            s_setup = setup_of(t, row_min_p(a, row));
-            s_best = 0x7fffffff;
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const T* r = reinterpret_cast<const T*>(&raw[k]);
-#pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = k * CT + tid < n ? to_f32(r[i]) : -INFINITY;
-        }
-    }
+    if (!RAGGED || rank) return -1;
+    if (tid < p.head) return tid;
+    return tid >= 16 && tid < 16 + p.tail ? p.tail_at + tid - 16 : -1;
+}
+
+// A row's logits in registers (w: -inf where there is none) to its probabilities, by
+// the NT threads at work of each of the cluster's CTAs; the turn-th row of theirs.
+template <typename T, int K, int NT>
+__device__ __forceinline__ void finish_row(const Part& part, float (&w)[K * per_vec<T>()], float& extra, int e, float t,
+                                           const RowSetup& setup, RowShared& sh, int ranks, uint32_t rank, unsigned turn,
+                                           bool first) {
+    constexpr int VE = per_vec<T>();
+    const int tid = threadIdx.x;
     float m = no_nan(extra);                       // fmaxf leaves NaN out
 #pragma unroll
     for (int i = 0; i < K * VE; ++i) m = fmaxf(m, w[i]);
-    m = over_cluster(s_max, s_warps[0], warp_max(m), ranks, rank, true, [](float x, float y) { return fmaxf(x, y); });
-    if (t == 0.f || m == -INFINITY) {     // (a NaN m, of a wait that ran out, makes the row NaN)
+    m = over_cluster<NT>(sh.max, sh.warps[0], warp_max(m), false, ranks, rank, turn, first);
+    if (tid == 0) sh.best[(turn & 1) ^ 1] = 0x7fffffff;      // the next row's: the last one's has been read
+    if (t == 0.f || m == -INFINITY) {              // (a NaN m, of a wait that ran out, makes the row NaN)
         int best = 0x7fffffff;
         if (m != -INFINITY) {
 #pragma unroll
             for (int k = K - 1; k >= 0; --k)
 #pragma unroll
                 for (int i = VE - 1; i >= 0; --i)
-                    if (w[k * VE + i] == m) best = head + (v0 + k * CT + tid) * VE + i;
+                    if (w[k * VE + i] == m) best = part.head + (part.v0 + k * NT + tid) * VE + i;
             if (extra == m) best = min(best, e);
         }
         best = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
-        if ((tid & 31) == 0) atomicMin(&s_best, best);
-        __syncthreads();
-        best = s_best;
-        if (ranks > 1 && trade(s_sum, (uint32_t)best, ranks, rank))
-            for (int i = 0; i < ranks; ++i) best = min(best, (int)s_sum.all[i]);
+        if ((tid & 31) == 0) atomicMin(&sh.best[turn & 1], best);
+        work_sync<NT>();
+        best = sh.best[turn & 1];
+        if (ranks > 1 && trade(sh.sum, (uint32_t)best, ranks, rank, turn))
+            for (int i = 0; i < ranks; ++i) best = min(best, (int)sh.sum.all[i]);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = head + (v0 + k * CT + tid) * VE + i == best ? 1.f : 0.f;
+            for (int i = 0; i < VE; ++i) w[k * VE + i] = part.head + (part.v0 + k * NT + tid) * VE + i == best ? 1.f : 0.f;
         extra = e == best ? 1.f : 0.f;
     } else {
         float sum;
         if (m < INFINITY) {
-            const RowRule r = rule_of(m, s_setup);
+            const RowRule r = rule_of(m, setup);
             sum = extra = weight(r, extra);
 #pragma unroll
             for (int i = 0; i < K * VE; ++i) {
@@ -223,29 +229,192 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
                 sum += w[i];
             }
         }
-        sum = over_cluster(s_sum, s_warps[1], warp_sum(sum), ranks, rank, false, [](float x, float y) { return x + y; });
+        sum = over_cluster<NT>(sh.sum, sh.warps[1], warp_sum(sum), true, ranks, rank, turn, false);
         const float inv = 1.f / sum;
         extra *= inv;
 #pragma unroll
         for (int i = 0; i < K * VE; ++i) w[i] *= inv;
     }
+}
+
+// They to memory.
+template <typename T, int K, int NT>
+__device__ __forceinline__ void store_row(float* p, const Part& part, const float (&w)[K * per_vec<T>()], float extra, int e) {
+    constexpr int VE = per_vec<T>();
+    const int tid = threadIdx.x;
     if (e >= 0) p[e] = extra;
-    float* pv = p + head + (long long)v0 * VE;
+    float* pv = p + part.head + (long long)part.v0 * VE;
     if ((reinterpret_cast<uintptr_t>(pv) & 15) == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k * CT + tid < n)
+            if (k * NT + tid < part.n)
 #pragma unroll
                 for (int i = 0; i < VE; i += 4)
-                    reinterpret_cast<float4*>(pv)[(k * CT + tid) * (VE / 4) + i / 4] =
+                    reinterpret_cast<float4*>(pv)[(k * NT + tid) * (VE / 4) + i / 4] =
                         make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k * CT + tid < n)
+            if (k * NT + tid < part.n)
 #pragma unroll
-                for (int i = 0; i < VE; ++i) pv[(k * CT + tid) * VE + i] = w[k * VE + i];
+                for (int i = 0; i < VE; ++i) pv[(k * NT + tid) * VE + i] = w[k * VE + i];
     }
+}
+
+// K vectors of a thread to numbers.
+template <typename T, int K, int NT>
+__device__ __forceinline__ void to_numbers(const uint4 (&raw)[K], int n, float (&w)[K * per_vec<T>()]) {
+    constexpr int VE = per_vec<T>();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const T* r = reinterpret_cast<const T*>(&raw[k]);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) w[k * VE + i] = k * NT + (int)threadIdx.x < n ? to_f32(r[i]) : -INFINITY;
+    }
+}
+
+// A cluster a row.
+template <typename T, int K>
+__global__ void __launch_bounds__(CT, K * per_vec<T>() > 12 ? 2 : 3)
+probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
+    __shared__ RowShared sh;
+    __shared__ RowSetup s_setup;
+    pdl_trigger();
+    const int tid = threadIdx.x;
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+    const long long row = blockIdx.x / (unsigned)ranks;
+    if (tid == 0) open_row(sh);
+    if (ranks > 1) cluster_arrive_relaxed();
+    pdl_wait();
+    const float t = a.temperature[row];
+    const bool fine = t >= 0.f && t < INFINITY;    // else the row is left as it was, by all of the cluster
+    if (!fine) {
+        if (ranks > 1) cluster_wait();
+        return;
+    }
+    const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
+    const Part part = part_of_row<T, true>(x, a.vocab, ranks, rank);
+    const uint4* xv = reinterpret_cast<const uint4*>(x + part.head) + part.v0;
+    float w[K * per_vec<T>()], extra = -INFINITY;
+    const int e = extra_of<true>(part, rank);
+    uint4 raw[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (k * CT + tid < part.n) raw[k] = xv[k * CT + tid];
+    if (e >= 0) extra = to_f32(x[e]);
+    if (tid == CT - 1) s_setup = setup_of(t, row_min_p(a, row));      // while they are on their way
+    to_numbers<T, K, CT>(raw, part.n, w);
+    finish_row<T, K, CT>(part, w, extra, e, t, s_setup, sh, ranks, rank, 0, true);
+    store_row<T, K, CT>(a.p + row * a.p_row, part, w, extra, e);
+}
+
+__device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;"
+                 ::"l"((uint64_t)dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Clusters that take every gridDim.x / ranks-th row.  The last warp brings a CTA's
+// part of the next row to shared memory while one is worked on, and the rows'
+// setups; outputs leave by bulk copies, too (stores of the threads themselves held
+// up what they read behind them: 177 us for 512 rows of 151936).  RAGGED: rows whose
+// vectors are not whole, or not 16-byte aligned in the output, leave by plain stores.
+template <typename T, int K, bool RAGGED>
+__global__ void __launch_bounds__(ST, 1) probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap) {
+    constexpr int NT = STREAM_CT, VE = per_vec<T>();
+    extern __shared__ uint4 in[];                  // [2][cap], cap the vectors of a part; then the outputs
+    float4* out = reinterpret_cast<float4*>(in + 2 * cap);
+    __shared__ RowShared sh;
+    __shared__ RowSetup s_setup[2];
+    __shared__ float s_t[2];
+    __shared__ uint64_t full[2], empty[2];
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+    const int first_row = blockIdx.x / (unsigned)ranks, step = gridDim.x / (unsigned)ranks;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, NT / 32);
+        }
+        open_row(sh);
+    }
+    __syncthreads();
+    if (ranks > 1) {
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
+    pdl_wait();
+    const T* x0 = reinterpret_cast<const T*>(a.x);
+    if (tid >= NT) {
+        if (lane == 0) {
+            unsigned n = 0;
+            for (long long row = first_row; row < a.rows; row += step, ++n) {
+                const float t = a.temperature[row];
+                const RowSetup setup = setup_of(t, row_min_p(a, row));
+                const T* x = x0 + row * a.x_row;
+                const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
+                const int b = n & 1;
+                if (n >= 2 && !mbar_wait_bounded(empty + b, (n / 2 - 1) & 1)) break;
+                s_t[b] = t;
+                s_setup[b] = setup;
+                if (part.n > 0 && t >= 0.f && t < INFINITY) {
+                    mbar_arrive_expect_tx(full + b, part.n * 16);
+                    bulk_load_1d(in + b * cap, reinterpret_cast<const uint4*>(x + part.head) + part.v0, part.n * 16, full + b);
+                } else {
+                    mbar_arrive(full + b);
+                }
+            }
+        }
+        __syncwarp();
+        return;
+    }
+    unsigned n = 0, turn = 0;
+    for (long long row = first_row; row < a.rows; row += step, ++n) {
+        const T* x = x0 + row * a.x_row;
+        float* p = a.p + row * a.p_row;
+        const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
+        const int e = extra_of<RAGGED>(part, rank), b = n & 1;
+        float extra = e >= 0 ? to_f32(x[e]) : -INFINITY;
+        const bool came = mbar_wait_bounded(full + b, (n / 2) & 1);
+        const float t = came ? s_t[b] : -1.f;
+        const bool fine = t >= 0.f && t < INFINITY;      // else the row is left as it was, by all of the cluster
+        const RowSetup setup = s_setup[b];
+        uint4 raw[K];
+        if (fine)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k * NT + tid < part.n) raw[k] = in[b * cap + k * NT + tid];
+        float w[K * VE];
+        to_numbers<T, K, NT>(raw, fine ? part.n : 0, w);
+        // what was read is in registers before its place goes back (a fence would wait
+        // for stores as well)
+#pragma unroll
+        for (int i = 0; i < K * VE; ++i) asm volatile("" ::"f"(w[i]) : "memory");
+        asm volatile("" ::"f"(setup.c), "f"(setup.c_lo), "f"(setup.cut), "f"(setup.cut_lo) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + b);
+        if (!came) break;
+        if (!fine) continue;
+        // (the last row's outputs have left their place once thread 0 comes to the second barrier)
+        if (!RAGGED && tid == 0) bulk_store_read();
+        finish_row<T, K, NT>(part, w, extra, e, t, setup, sh, ranks, rank, turn++, false);
+        if constexpr (RAGGED) {
+            store_row<T, K, NT>(p, part, w, extra, e);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k * NT + tid < part.n)
+#pragma unroll
+                    for (int i = 0; i < VE; i += 4)
+                        out[(k * NT + tid) * (VE / 4) + i / 4] =
+                            make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            work_sync<NT>();
+            if (tid == 0 && part.n > 0) bulk_store_1d(p + (long long)part.v0 * VE, out, part.n * VE * 4);
+        }
+    }
+    if (!RAGGED && tid == 0) bulk_store_read();    // shared memory outlives what reads it
 }
 
 // ---- rows of any length
@@ -316,6 +485,42 @@ cudaError_t allow_cluster(const void* kern) {
     return e;
 }
 
+// Clusters of a kernel that run at once on the current device, asked for once.
+cudaError_t clusters_at_once(const void* kern, int ranks, int threads, size_t smem, int* most) {
+    static std::mutex mu;
+    constexpr int MAX = 256;
+    struct Known {
+        const void* kern;
+        int dev, ranks, most;
+    };
+    static Known known[MAX];
+    static int n = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (known[i].kern == kern && known[i].dev == dev && known[i].ranks == ranks) {
+            *most = known[i].most;
+            return cudaSuccess;
+        }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ranks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(most, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*most < 1) *most = 1;
+    if (n < MAX) known[n++] = Known{kern, dev, ranks, *most};
+    return cudaSuccess;
+}
+
 template <typename T, int K>
 int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
     const void* kern = reinterpret_cast<const void*>(probs_cluster_kernel<T, K>);
@@ -323,22 +528,50 @@ int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
         const cudaError_t e = allow_cluster(kern);
         if (e != cudaSuccess) return (int)e;
     }
-    return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)((long long)a.rows * ranks)), dim3(CT), ranks, s,
-                                 0, a, ranks);
+    return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)(a.rows * ranks)), dim3(CT), ranks, s, 0, a, ranks);
+}
+
+// Shared memory of a vector: in twice, and its outputs.
+template <typename T> constexpr int stream_bytes(bool ragged) { return 2 * 16 + (ragged ? 0 : per_vec<T>() * 4); }
+
+template <typename T, int K, bool RAGGED>
+int launch_stream(const ProbsArgs& a, int ranks, int cap, cudaStream_t s) {
+    const void* kern = reinterpret_cast<const void*>(probs_stream_kernel<T, K, RAGGED>);
+    const size_t smem = (size_t)cap * stream_bytes<T>(RAGGED);
+    int most = 0;
+    cudaError_t e = allow_smem(kern);
+    if (e == cudaSuccess && ranks > 8) e = allow_cluster(kern);
+    if (e == cudaSuccess) e = clusters_at_once(kern, ranks, ST, smem, &most);
+    if (e != cudaSuccess) return (int)e;
+    // the rounds that the clusters need, and no more clusters than fill them
+    const int rounds = (a.rows + most - 1) / most, clusters = (a.rows + rounds - 1) / rounds;
+    return (int)launch_cluster_k(probs_stream_kernel<T, K, RAGGED>, dim3((unsigned)(clusters * ranks)), dim3(ST), ranks, s, smem,
+                                 a, ranks, cap);
 }
 
 template <typename T>
 int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
-    constexpr int VE = per_vec<T>(), MOST = 40 / VE;      // vectors of a thread
-    const long long vecs = ((long long)a.vocab + VE - 1) / VE + 1;      // and one for a row that begins between two
+    constexpr int VE = per_vec<T>(), MOST = 40 / VE, STREAM_MOST = VE == 4 ? 5 : 3;      // vectors of a thread
+    const long long vecs = ((long long)a.vocab + VE - 1) / VE;
+    auto of_thread = [&](int ranks, int threads) { return (int)(((vecs + ranks - 1) / ranks + threads - 1) / threads); };
     int ranks = 1;
-    while (ranks < 16 && (vecs + ranks - 1) / ranks > CT * MOST) ranks *= 2;
-    const long long left = (vecs + ranks - 1) / ranks;
-    if (left > CT * MOST || (long long)a.rows * ranks > 0x7fffffffll)
+    while (ranks < 16 && of_thread(ranks, CT) > MOST) ranks *= 2;
+    const bool held = of_thread(ranks, CT) <= MOST;
+    if (!held || (long long)a.rows * ranks > 0x7fffffffll)
         return (int)launch_k(probs_rows_kernel<T>, dim3((unsigned)a.rows), dim3(PT), 0, s, a);
+#ifndef PROBS_STREAM
+#define PROBS_STREAM 1
+#endif
+    // more rows than run at once, and long ones: clusters that stay
+    const int cap = (int)((vecs + ranks - 1) / ranks), k_stream = of_thread(ranks, STREAM_CT);
+    const bool ragged = a.vocab % VE || (reinterpret_cast<uintptr_t>(a.x) & 15) || a.x_row % VE ||
+                        (reinterpret_cast<uintptr_t>(a.p) & 15) || a.p_row % 4;
+    if (PROBS_STREAM && (long long)a.rows * ranks > 4 * sms && k_stream > STREAM_MOST / 2 && k_stream <= STREAM_MOST &&
+        cap * stream_bytes<T>(ragged) <= 225 * 1024)
+        return ragged ? launch_stream<T, STREAM_MOST, true>(a, ranks, cap, s) : launch_stream<T, STREAM_MOST, false>(a, ranks, cap, s);
     // few rows: more CTAs each, while all are resident at once
-    while (ranks < 8 && (long long)a.rows * ranks * 2 <= sms && (vecs + ranks - 1) / ranks > CT) ranks *= 2;
-    const int k = (int)(((vecs + ranks - 1) / ranks + CT - 1) / CT);
+    while (ranks < 8 && (long long)a.rows * ranks * 2 <= sms && of_thread(ranks, CT) > 1) ranks *= 2;
+    const int k = of_thread(ranks, CT);
     if (k <= 1) return launch_cluster<T, 1>(a, ranks, s);
     if (k <= 2) return launch_cluster<T, 2>(a, ranks, s);
     if (k <= 3) return launch_cluster<T, 3>(a, ranks, s);
