@@ -572,18 +572,30 @@ def dflash_pages_plan(kv_len, q_len, free_pages, n_free, table, row_start, posit
 def dflash_pages_trim(kv_len, new_len, free_pages, n_free, table, stream=None):
     """kv_len[s] = min(kv_len[s], new_len[s]); pages no longer needed go back
     onto free_pages."""
-    i32 = (_I32,)
-    _need(table, "table", i32, (None, None))
-    S, max_pages = table.shape
-    _need(kv_len, "kv_len", i32, (S,))
-    _need(new_len, "new_len", i32, (S,))
-    _need(free_pages, "free_pages", i32, (None,))
-    _need(n_free, "n_free", i32, (1,))
-    _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
-    _counts(S=S, max_pages=max_pages, free_pages=free_pages.shape[0])
-    check(lib.dflash_pages_trim(kv_len.data_ptr(), new_len.data_ptr(), S, free_pages.data_ptr(),
-                                free_pages.shape[0], n_free.data_ptr(), table.data_ptr(), max_pages,
-                                _raw(stream, table.get_device())))
+    try:
+        dev = _current(table)
+        S, max_pages = table.shape
+        (pool,) = free_pages.shape
+        fine = (kv_len.shape == (S,) and new_len.shape == (S,) and n_free.shape == (1,) and
+                _flat((table, kv_len, new_len, free_pages, n_free), dev))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        i32 = (_I32,)
+        _need(table, "table", i32, (None, None))
+        S, max_pages = table.shape
+        _need(kv_len, "kv_len", i32, (S,))
+        _need(new_len, "new_len", i32, (S,))
+        _need(free_pages, "free_pages", i32, (None,))
+        _need(n_free, "n_free", i32, (1,))
+        _here(kv_len=kv_len, new_len=new_len, free_pages=free_pages, n_free=n_free, table=table)
+        dev, pool = table.get_device(), free_pages.shape[0]
+    if S > _MOST or max_pages > _MOST or pool > _MOST:
+        _counts(S=S, max_pages=max_pages, free_pages=pool)
+    rc = lib.dflash_pages_trim(kv_len.data_ptr(), new_len.data_ptr(), S, free_pages.data_ptr(), pool,
+                               n_free.data_ptr(), table.data_ptr(), max_pages, _raw(stream, dev))
+    if rc:
+        check(rc)
 
 
 def _cache_ok(shape, k_codes, v_codes, k_scale, v_scale, dev: int) -> bool:

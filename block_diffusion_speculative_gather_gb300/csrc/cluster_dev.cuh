@@ -11,17 +11,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// Arrive (what the thread wrote before is seen behind the others' wait) and wait.
-// A warp whose lanes come from different branches arrives as one.
-__device__ __forceinline__ void cluster_arrive() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// The opening barrier of CTAs that send to each other's mbarriers: initialised ones
-// (fence_mbar_init) are seen behind the wait.  No other memory is ordered, so no
-// store or load in flight is waited for.
+// Arrival at a barrier of the cluster that orders no memory but what a fence before
+// it does (fence_mbar_init for mbarriers), so that no store in flight is waited for.
+// A warp whose lanes come from different branches arrives as one.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");

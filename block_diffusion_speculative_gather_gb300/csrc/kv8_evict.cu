@@ -383,9 +383,11 @@ __global__ void __launch_bounds__(MT, 3) kv8_move_kernel(const __grid_constant__
     pages_at(0);
     for (int t = 0; t < turns; ++t) {
         copy_wait<MS - 2>();
-        // the turn's positions have been read, by every thread that reads any of them
+        // the turn's positions have been read, by every thread that reads any of them:
+        // the copies are complete, so no memory has to be ordered (a barrier that orders
+        // it would wait for the last turn's stores)
         if (ranks > 1) {
-            cluster_arrive();
+            cluster_arrive_relaxed();
             cluster_wait();
         } else {
             __syncthreads();

@@ -11,7 +11,7 @@
 //
 // Which token a uniform number falls on is a matter of sums of up to a vocabulary
 // of terms: differences are taken exactly (two fp32 numbers each), sums are kept
-// as pairs of fp32 numbers within a warp and in fp64 above, in a fixed order.
+// as pairs of fp32 numbers (48 bits, an addition off by about 2^-47), in a fixed order.
 //
 // Only one row of p and q is read whole.  Its tokens are dealt in units of 1024 to
 // warps (each CTA finds by itself, from two numbers a draft, which row that is),
@@ -25,9 +25,11 @@ namespace {
 
 constexpr int VT = 256;                        // threads
 constexpr int VW = VT / 32;
-constexpr int PER = 8;                         // tokens of a lane at a time
-constexpr int BLOCK = 32 * PER;                // tokens of a warp at a time
-static_assert(VERIFY_UNIT == 4 * VT && VERIFY_UNIT % BLOCK == 0, "four tokens a thread of the search");
+// Tokens of a lane and of a warp at a time: as many again are on their way, 2 KB a warp
+// with q or without.
+template <bool Q> constexpr int per() { return Q ? 8 : 16; }
+template <bool Q> constexpr int block() { return 32 * per<Q>(); }
+static_assert(VERIFY_UNIT == 4 * VT && VERIFY_UNIT % block<false>() == 0, "four tokens a thread of the search");
 
 // A sum as hi + lo, |lo| below half a step of hi.
 struct Pair {
@@ -40,7 +42,22 @@ __device__ __forceinline__ Pair add(Pair a, float x, float e) {
     return {s, __fadd_rn(a.lo, __fadd_rn(err, e))};
 }
 
-__device__ __forceinline__ double value(Pair a) { return (double)a.hi + (double)a.lo; }
+__device__ __forceinline__ Pair plus(Pair a, Pair b) { return add(a, b.hi, b.lo); }
+// The sign of the difference is the rounded one's: where the high parts are close
+// theirs is exact.
+__device__ __forceinline__ bool above(Pair a, Pair b) { return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) > 0.f; }
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+    return {__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
+}
+// Sums over this and the lower lanes of the warp.
+__device__ __forceinline__ Pair warp_running(Pair a, int lanes = 32) {
+    const int lane = threadIdx.x & 31;
+    for (int o = 1; o < lanes; o <<= 1) {
+        const Pair b{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        if (lane >= o) a = plus(b, a);
+    }
+    return a;
+}
 
 // The same in all lanes: a sum's rounding error does not depend on the operands' order.
 __device__ __forceinline__ Pair warp_total(Pair a) {
@@ -123,14 +140,14 @@ __device__ __forceinline__ void load4(const float* row, int vocab, int v, float*
 }
 
 template <bool Q> struct Tokens {
-    float p[PER], q[Q ? PER : 1];
+    float p[per<Q>()], q[Q ? per<Q>() : 1];
 };
 
-// A warp's BLOCK tokens from v0 on.
+// A warp's tokens from v0 on.
 template <bool WIDE, bool Q>
 __device__ __forceinline__ void load_block(const Row& r, int vocab, int v0, Tokens<Q>& t) {
 #pragma unroll
-    for (int k = 0; k < PER; k += 4) {
+    for (int k = 0; k < per<Q>(); k += 4) {
         const int v = v0 + k * 32 + (threadIdx.x & 31) * 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -149,7 +166,7 @@ template <bool Q, bool CLEAN>
 __device__ __forceinline__ Pair add_block(const Row& r, int v0, const Tokens<Q>& t, Pair s) {
     const int mine = r.certain - v0 - (threadIdx.x & 31) * 4;      // where the refused token is the lane's
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
+    for (int k = 0; k < per<Q>(); ++k) {
         float p = CLEAN ? clean(t.p[k]) : fmaxf(t.p[k], 0.f);      // fmaxf: NaN is 0
         if constexpr (Q) {
             const Pair w = less(p, clean(t.q[k]));
@@ -166,7 +183,7 @@ __device__ __forceinline__ Pair add_block(const Row& r, int v0, const Tokens<Q>&
 template <bool WIDE, bool Q>
 __device__ __noinline__ Pair sum_unit(const Row& r, int vocab, int unit) {
     Pair s{0.f, 0.f};
-    for (int v0 = unit * VERIFY_UNIT; v0 < min((unit + 1) * VERIFY_UNIT, vocab); v0 += BLOCK) {
+    for (int v0 = unit * VERIFY_UNIT; v0 < min((unit + 1) * VERIFY_UNIT, vocab); v0 += block<Q>()) {
         Tokens<Q> t;
         load_block<WIDE, Q>(r, vocab, v0, t);
         s = add_block<Q, true>(r, v0, t, s);
@@ -179,6 +196,7 @@ __device__ __noinline__ Pair sum_unit(const Row& r, int vocab, int unit) {
 template <bool WIDE, bool Q>
 __device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int unit, int step, float2* part) {
     Tokens<Q> t;
+    constexpr int BLOCK = block<Q>();
     if (unit < a.units) load_block<WIDE, Q>(r, a.vocab, unit * VERIFY_UNIT, t);
     for (; unit < a.units; unit += step) {
         Pair s{0.f, 0.f};
@@ -199,58 +217,55 @@ __device__ __forceinline__ void sum_units(const VerifyArgs& a, const Row& r, int
     }
 }
 
-__device__ __forceinline__ double unit_sum(const float2* p) {
+__device__ __forceinline__ Pair unit_sum(const float2* p) {
     const float2 s = __ldcg(p);
-    return value(Pair{s.x, s.y});
+    return {s.x, s.y};
 }
 
-// Exclusive sums over the CTA, and the total.
-__device__ __forceinline__ double block_before(double v, double* total, double* red) {
+// Sums before each thread of the CTA, and the total.
+__device__ __forceinline__ Pair block_before(Pair v, Pair* total, float2* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) red[warp] = inc;
+    const Pair run = warp_running(v);
+    if (lane == 31) red[warp] = make_float2(run.hi, run.lo);
     __syncthreads();
-    double before = 0.0, sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) {
-        if (i < warp) before += red[i];
-        sum += red[i];
-    }
-    *total = sum;
-    return before + (inc - v);
+    const float2 w = red[lane % VW];
+    const Pair warps = warp_running(Pair{w.x, w.y}, VW);      // its first VW lanes
+    *total = shfl(warps, VW - 1);
+    const Pair lower = shfl(warps, warp ? warp - 1 : 0);
+    Pair up{__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+    if (lane == 0) up = {0.f, 0.f};
+    return warp ? plus(lower, up) : up;
 }
 
 struct Search {
-    double red[2][VW];
-    double run;
+    float2 red[2][VW];
+    Pair run;
     int thread, last, unit, token;
 };
 
 // By the whole CTA: the token that u draws from a row whose units' sums are
-// `part`; -1: it has no weight.
+// `part`; -1: it has no weight.  In pairs of fp32 numbers throughout (fp64 sums
+// took 6 us of a call).
 template <bool WIDE, bool Q>
 __device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float u, Search& sm) {
     const int tid = threadIdx.x;
     // each thread a run of units
     const int per = (a.units + VT - 1) / VT, b0 = tid * per, b1 = min(b0 + per, a.units);
-    double own = 0.0;
+    Pair own{0.f, 0.f};
     int end = -1;                      // last unit with weight
     for (int c = b0; c < b1; ++c) {
-        const double x = unit_sum(part + c);
-        own += x;
-        if (x > 0.0) end = c;
+        const Pair x = unit_sum(part + c);
+        own = plus(own, x);
+        if (x.hi > 0.f) end = c;
     }
     if (tid == 0) sm.thread = 0x7fffffff, sm.last = -1;
-    double total;
-    const double before = block_before(own, &total, sm.red[0]);
-    const double goal = (double)u * total;
+    Pair total;
+    const Pair before = block_before(own, &total, sm.red[0]);
+    // u * total: the product of the high parts exactly, and the low one's
+    const float prod = __fmul_rn(u, total.hi);
+    const Pair goal{prod, fmaf(u, total.lo, fmaf(u, total.hi, -prod))};
     // the first run that passes the goal
-    const bool past = end >= 0 && before + own > goal;
+    const bool past = end >= 0 && above(plus(before, own), goal);
     const unsigned m = __ballot_sync(0xffffffffu, past);
     const int top = __reduce_max_sync(0xffffffffu, end);
     if ((tid & 31) == 0) {
@@ -265,14 +280,14 @@ __device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float
     if (tid == (none ? 0 : thread)) {
         // the run's first unit that passes it (by rounding maybe none: its last one with weight)
         int unit = none ? last : end;
-        double run = none ? 0.0 : before;
-        for (int c = b0; c < b1 && !none; ++c) {
-            const double x = unit_sum(part + c);
-            if (x > 0.0 && run + x > goal) {
+        Pair run = none ? Pair{0.f, 0.f} : before;
+        for (int c = b0; c < b1 && !none && b1 - b0 > 1; ++c) {
+            const Pair x = unit_sum(part + c), next = plus(run, x);
+            if (x.hi > 0.f && above(next, goal)) {
                 unit = c;
                 break;
             }
-            if (c < end) run += x;
+            if (c < end) run = next;
         }
         sm.unit = unit;
         sm.run = run;
@@ -291,16 +306,16 @@ __device__ int draw(const VerifyArgs& a, const Row& r, const float2* part, float
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         w[j] = Q ? less(clean(p[j]), clean(q[j])) : Pair{v + j == r.certain ? 0.f : clean(p[j]), 0.f};
-        s = add(s, w[j].hi, w[j].lo);
+        s = plus(s, w[j]);
     }
-    double run = sm.run + block_before(value(s), &total, sm.red[1]);
+    Pair run = plus(sm.run, block_before(s, &total, sm.red[1]));
     int hit = 0x7fffffff, any = -1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        run += value(w[j]);
+        run = plus(run, w[j]);
         if (w[j].hi > 0.f) {
             any = v + j;
-            if (!none && run > goal) hit = min(hit, v + j);
+            if (!none && above(run, goal)) hit = min(hit, v + j);
         }
     }
     hit = (int)__reduce_min_sync(0xffffffffu, (unsigned)hit);
@@ -358,7 +373,8 @@ __global__ void __launch_bounds__(VT, 4) verify_kernel(const __grid_constant__ V
         if (tid == 0) a.tickets[s] = 0;
         __threadfence();
     }
-    const float u = a.u[r0];
+    float u = a.u[r0];
+    u = u < 0.f ? -1.f : (u < 1.f ? u : 2.f);      // outside [0, 1), and NaN: the ends
     int v = draw<WIDE, Q>(a, row, part, u, s_search);
     if (v < 0 && ve.draft >= 0) {
         // nothing is left of p behind q: p itself

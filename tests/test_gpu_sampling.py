@@ -285,13 +285,14 @@ def test_verify_on_the_borders_of_running_sums(capi):
 
 def test_verify_special_numbers(capi):
     """Probabilities that do not count, rows without weight, uniform numbers outside [0, 1)."""
-    V, rows = 4100, [1] * 12 + [3] * 4
+    V, rows = 4100, [1] * 12 + [3] * 4 + [1] * 4
     c = Call(capi, rows, V, 4)
     c.p[0] = 0
     c.p[1] = NAN
     c.p[2, ::2] = INF
     c.p[3, 1::2] = -1.0
     c.u[4:9] = floats([-0.5, 1.0, 2.0, NAN, 0.0])
+    c.u[24:28] = floats([-3e38, 3e38, -INF, INF])
     c.p[9], c.p[10] = 0, 0
     c.p[9, V - 1] = 1e-42                        # one token with a subnormal weight
     c.p[10, 0] = 1e30                            # the largest that count, and one above
