@@ -277,7 +277,7 @@ int dflash_kv8_attention(const dflash_kv8_cache* cache, const dflash_kv8_query* 
 int dflash_kv8_weigh(const dflash_kv8_cache* cache, const dflash_kv8_query* q, float* weights, const int32_t* count,
                      int32_t observe, int32_t fresh, int32_t* err, dflash_stream_t stream) {
     if (const int r = check_cache(cache)) return r;
-    if (!q || !weights || !aligned(weights, 16) || !err || !aligned(err, 8))
+    if (!q || !weights || !aligned(weights, 4) || !err || !aligned(err, 8))
         return report_error(DFLASH_ERR_ARG, "NULL or misaligned argument");
     if (const int r = check_attn_shape(q->rows, q->S, q->n_q, cache->n_kv, cache->head_dim, q->max_pages)) return r;
     if (q->dtype != DFLASH_BF16 && q->dtype != DFLASH_F16)

@@ -83,6 +83,7 @@ int dflash_verify_drafts(const dflash_drafts* d, void* workspace, size_t workspa
         return report_error(DFLASH_ERR_ARG, "NULL row_start or n_tokens, or one of kv_len and new_len");
     if (d->rows > 0 && (!d->probs || !d->ids || !d->uniform || !d->tokens))
         return report_error(DFLASH_ERR_ARG, "NULL argument");
+    if (d->rows > 0 && d->tokens == d->ids) return report_error(DFLASH_ERR_ARG, "tokens is ids: both are needed");
     if (!aligned(d->probs, 4) || !aligned(d->draft_probs, 4)) return report_error(DFLASH_ERR_ARG, "misaligned rows");
     if (workspace_bytes < need) return report_error(DFLASH_ERR_ARG, "workspace %zu < %zu", workspace_bytes, need);
     if (const int r = pending()) return r;

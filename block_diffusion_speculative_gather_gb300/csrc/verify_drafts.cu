@@ -338,9 +338,10 @@ __global__ void __launch_bounds__(VT, 4) verify_kernel(const __grid_constant__ V
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, s = blockIdx.y;
-    const int r0 = a.row_start[s], n = a.row_start[s + 1] - r0;
-    const bool fine = r0 >= 0 && n >= 0 && r0 + n <= a.rows;
-    if (!fine || n == 0) {
+    const int r0 = a.row_start[s], r1 = a.row_start[s + 1];
+    const bool fine = r0 >= 0 && r1 >= r0 && r1 <= a.rows;
+    const int n = fine ? r1 - r0 : 0;
+    if (n == 0) {
         if (blockIdx.x == 0 && tid == 0) {
             if (!fine) report(a.err, s);
             a.n_tokens[s] = 0;

@@ -677,7 +677,8 @@ int dflash_rope(const dflash_rope_config* cfg /*host*/, const uint64_t* turns, c
  * negative or not finite is left as it was.  logits_row and probs_row:
  * elements between rows, tokens contiguous; at any alignment of the types (rows
  * that are 16-byte aligned together are faster).  fp32 probabilities may be
- * written over their logits (same address and row).  The sampled counterpart of
+ * written over their logits (same address and row).  A row's last bits can follow
+ * from the number of rows (the order of its sum).  The sampled counterpart of
  * the round's argmax; no counterpart in the source pages, which decode greedily.
  * Errors: ARG, CUDA.
  */
@@ -724,7 +725,7 @@ typedef struct {
     const float* uniform;       /* [rows], [0, 1) */
     const int32_t* row_start;   /* [S + 1] */
     const int32_t* kv_len;      /* [S]; NULL with new_len */
-    int32_t* tokens;            /* [rows] */
+    int32_t* tokens;            /* [rows], not ids */
     int32_t* n_tokens;          /* [S] */
     int32_t* new_len;           /* [S] or NULL; may be kv_len */
     int64_t probs_row, draft_row;
@@ -746,9 +747,11 @@ int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_
  * verification count = n_tokens leaves rejected rows out, and a long prompt's last rows stand
  * for it.  fresh 1: the step's own positions (every row's) start from 0 (the
  * first layer's call of a step; the others add).  weights: fp32 [n_pages]
- * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  All kv_len
- * positions' terms are added in one fixed order, without atomics; a sequence's results do not depend on the
- * others.  Scores that are NaN (a NaN code) add nothing, nor does a row whose lse is -inf or NaN.
+ * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  A page belongs to
+ * one sequence.  Terms are added in a fixed order, without atomics; a sequence's
+ * results depend on its own rows and positions and the call's counts, not on the
+ * others.  Scores that are NaN (a NaN code) add nothing, nor does a row whose lse is
+ * -inf or NaN.
  * Shapes, strides and types as dflash_kv8_attention; err {2, site} for lengths and pages out of range, whose
  * sequence (page) is left out.
  * Errors: CONFIG, ARG, CUDA.

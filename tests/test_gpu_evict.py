@@ -191,6 +191,22 @@ def test_weigh_strides_scale_and_layers(capi):
     assert ((two - one) - (_ - before)).abs().max() < 1e-4
 
 
+@pytest.mark.parametrize("n", [2, 40])
+def test_weigh_rows_that_share_their_memory(capi, n):
+    """A row stride of 0, and weights at an odd place."""
+    st = attn_state(4, 2, 64, [n], [100], BF, seed=6)
+    st["q"] = st["q"][:1].expand(n + 2, -1, -1)
+    attend(capi, dict(st, q=st["q"].contiguous()))
+    check_weigh(capi, st)
+    before, want = weigh(capi, st)
+    held = torch.zeros(before.numel() + 1, device="cuda")
+    w = held[1:].view_as(before)
+    w.copy_(before)
+    capi.dflash_kv8_weigh(st["q"], st["lse"], *st["cache"], ints(st["table"]), ints(st["held"]), ints(st["start"]), w,
+                          ints([0, 0]))
+    assert torch.equal(w, want) and held[0] == 0
+
+
 def test_weigh_rows_without_keys_and_with_nan(capi):
     """More rows than positions; NaN codes add nothing, to their own position
     alone, and rows that saw one (an lse of NaN) none at all."""

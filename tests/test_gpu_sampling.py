@@ -178,6 +178,84 @@ def test_probs_rows_do_not_depend_on_the_others(capi, rows):
     assert torch.equal(out, again)
 
 
+MANY = [(700, 16000, F32), (700, 16003, F32), (1300, 20000, BF), (640, 20001, F16), (330, 40000, F32), (90, 151936, F32),
+        (100, 151936, BF)]
+
+
+def many_rows(rows, V, kind):
+    """More rows than run at once, with temperatures, cuts and logits of every kind among them."""
+    x = logits(rows, V, kind, rows)
+    x[3] = -INF
+    x[5, 1::2] = NAN
+    x[7, [2, V - 1]] = INF
+    x[rows - 2, : V - 1] = -INF
+    t = 0.3 + torch.rand(rows, device="cuda", generator=torch.Generator(device="cuda").manual_seed(rows))
+    t[::7] = 0.0
+    t[4], t[rows - 1], t[rows // 2] = -1.0, NAN, INF
+    min_p = torch.where(torch.arange(rows, device="cuda") % 3 == 0, 0.05, 0.0)
+    left = [4, rows // 2, rows - 1]
+    some = sorted(set(list(range(12)) + list(range(0, rows, 37)) + [rows - 3, rows - 2]) - set(left))
+    return x, t, min_p, left, some
+
+
+@pytest.mark.parametrize("rows,V,kind", MANY)
+def test_probs_many_rows(capi, rows, V, kind):
+    x, t, min_p, left, some = many_rows(rows, V, kind)
+    out = torch.full((rows, V), 7.0, device="cuda")
+    capi.dflash_probs(x, t, out, min_p=min_p)
+    check_probs(x, t, out, min_p, rows=some)
+    assert (out[left] == 7.0).all()
+    sums = out.double().sum(1)
+    ok = torch.ones(rows, dtype=torch.bool, device="cuda")
+    ok[left], ok[3] = False, False
+    assert ((sums - 1).abs()[ok] < 1e-4).all()
+    for _ in range(3):
+        again = torch.full_like(out, 7.0)
+        capi.dflash_probs(x, t, again, min_p=min_p)
+        assert torch.equal(out, again)
+    # outputs that are not 16-byte aligned, with gaps between their rows
+    held = torch.full((rows * (V + 3) + 1,), 7.0, device="cuda")
+    view = held[1:].view(rows, V + 3)[:, :V]
+    capi.dflash_probs(x, t, view, min_p=min_p)
+    check_probs(x, t, view, min_p, rows=some[:20])
+    assert (held[1:].view(rows, V + 3)[:, V:] == 7.0).all() and held[0] == 7.0 and (view[left] == 7.0).all()
+    if kind is F32:
+        same = x.clone()
+        capi.dflash_probs(same, t, same, min_p=min_p)
+        keep = [r for r in range(rows) if r not in left]
+        assert torch.equal(same[keep], out[keep])
+        assert torch.equal(same[left].nan_to_num(1.5), x[left].nan_to_num(1.5))
+
+
+def test_probs_many_rows_captured_and_side_by_side(capi):
+    """The clusters that stay, in a graph, and two calls at once on two streams."""
+    x, t, min_p, left, some = many_rows(700, 16000, F32)
+    y, u, cut, _, other = many_rows(1300, 20000, BF)
+    a, b = torch.full((700, 16000), 7.0, device="cuda"), torch.full((1300, 20000), 7.0, device="cuda")
+    capi.dflash_probs(x, t, a, min_p=min_p)
+    capi.dflash_probs(y, u, b, min_p=cut)
+    want = a.clone(), b.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        capi.dflash_probs(x, t, a, min_p=min_p)
+        capi.dflash_probs(y, u, b, min_p=cut)
+    for _ in range(3):
+        a.fill_(7.0), b.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    s = torch.cuda.Stream()
+    for _ in range(10):
+        a.fill_(7.0), b.fill_(7.0)
+        torch.cuda.synchronize()
+        capi.dflash_probs(x, t, a, min_p=min_p, stream=s)
+        capi.dflash_probs(y, u, b, min_p=cut, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
 # ------------------------------------------------------------------ verification
 
 class Call:
@@ -331,7 +409,7 @@ def test_verify_reports_impossible_ids_and_rows(capi):
     c.ids[2] = 300
     _, n = c.run(capi).check(err=(2, 2))
     assert n[0] == 2
-    for start, bad in (([0, 4, 11], 1), ([-1, 4, 8], 0), ([0, 5, 4], 1)):
+    for start, bad in (([0, 4, 11], 1), ([-1, 4, 8], 0), ([0, 5, 4], 1), ([0, 5, -2 ** 31], 1), ([-2 ** 31, 0, 4], 0)):
         c = Call(capi, [4, 4], 300, 6)
         c.row_start = ints(start)
         c.run(capi)
@@ -444,6 +522,14 @@ def test_nothing_to_do(capi):
     c = Call(capi, [0, 0], 100, 1, pad=0)
     c.run(capi)
     assert c.n.tolist() == [0, 0] and c.new.tolist() == c.kv.tolist()
+
+
+def test_tokens_over_ids_are_refused(capi):
+    c = Call(capi, [3, 3], 500, 1)
+    c.tokens = c.ids
+    with pytest.raises(capi.DFlashError) as e:
+        c.run(capi)
+    assert e.value.code == -3 and "ids" in str(e.value)
 
 
 def test_a_small_workspace_is_refused(capi):

@@ -35,7 +35,7 @@ def test_probs_guards(capi):      # noqa: F811
 
 
 def _drafts(capi, **kw):      # noqa: F811
-    d = dict(probs=PTR, draft_probs=PTR, ids=PTR, uniform=PTR, row_start=PTR, kv_len=PTR, tokens=PTR, n_tokens=PTR,
+    d = dict(probs=PTR, draft_probs=PTR, ids=PTR, uniform=PTR, row_start=PTR, kv_len=PTR, tokens=PTR + 64, n_tokens=PTR,
              new_len=PTR, probs_row=100, draft_row=100, rows=3, vocab=100, S=2, pad_=0)
     d.update(kw)
     return capi.dflash_drafts(*(d[n] for n, _ in capi.dflash_drafts._fields_))
@@ -44,7 +44,7 @@ def _drafts(capi, **kw):      # noqa: F811
 @pytest.mark.parametrize("kw,code", [
     (dict(probs=None), ARG), (dict(probs=PTR + 2), ARG), (dict(draft_probs=PTR + 1), ARG), (dict(ids=None), ARG),
     (dict(uniform=None), ARG), (dict(row_start=None), ARG), (dict(kv_len=None), ARG), (dict(new_len=None), ARG),
-    (dict(tokens=None), ARG), (dict(n_tokens=None), ARG), (dict(probs_row=-1), ARG), (dict(draft_row=-1), ARG),
+    (dict(tokens=None), ARG), (dict(tokens=PTR), ARG), (dict(n_tokens=None), ARG), (dict(probs_row=-1), ARG), (dict(draft_row=-1), ARG),
     (dict(rows=-1), ARG), (dict(rows=(1 << 30) + 1), ARG), (dict(vocab=0), CONFIG), (dict(vocab=(1 << 24) + 1), CONFIG),
     (dict(S=0), CONFIG), (dict(S=65536), CONFIG)])
 def test_verify_guards(capi, kw, code):      # noqa: F811
@@ -79,7 +79,7 @@ def test_weigh_guards(capi, kw, code):      # noqa: F811
 def test_weigh_other_guards(capi):      # noqa: F811
     c, q = _cache(capi), _query(capi, lse=PTR)
     ok = [C.byref(c), C.byref(q), PTR, None, 0, 0, PTR, None]
-    for at, bad in ((0, None), (1, None), (2, None), (2, PTR + 4), (4, -1), (6, None), (6, PTR + 4)):
+    for at, bad in ((0, None), (1, None), (2, None), (2, PTR + 2), (4, -1), (6, None), (6, PTR + 4)):
         a = list(ok)
         a[at] = bad
         assert capi.lib.dflash_kv8_weigh(*a) == ARG, (at, bad)
