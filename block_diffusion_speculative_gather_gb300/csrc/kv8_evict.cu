@@ -464,8 +464,15 @@ int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choo
         if (e != cudaSuccess) return (int)e;
     }
     const int chains = a.S * a.n_kv;
+    // Three CTAs of the move run on an SM.  Few chains: as many CTAs each as run at once (one
+    // sequence of 4095 positions to 2048, 5 layers: 17.7 us, by one CTA each 28.3).  More
+    // than run at once: two each where that takes at least an eighth less rounds (of 6000
+    // positions to 2500: 576 chains 91 us, by one CTA each 113; 960 chains 117 and 124; where
+    // it does not, 1280 chains 147 and 139).
+    const long long all = 2LL * chains * l.n, room = 3LL * sms;
     int ranks = 1;
-    while (ranks < MRANKS && 2LL * chains * l.n * ranks * 2 <= 3 * sms) ranks *= 2;
+    while (ranks < MRANKS && all * ranks * 2 <= room) ranks *= 2;
+    if (ranks == 1 && 8 * ((all * 2 + room - 1) / room) <= 14 * ((all + room - 1) / room)) ranks = 2;
     const dim3 grid((unsigned)(chains * ranks), (unsigned)l.n, 2), block(MT);
     auto go = [&](auto kern, size_t smem) {
         const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern));

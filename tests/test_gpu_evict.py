@@ -409,6 +409,12 @@ def test_evict_shapes(capi, n_kv, dim, layers):
     e.check(capi, [150, 100], 2, 20)
 
 
+def test_evict_more_pools_than_run_at_once(capi):
+    """Chains of pages in a little more than one round: two CTAs each."""
+    Evict(capi, [1200], 8, 64, 31, seed=12).check(capi, [700], 4, 64)
+    Evict(capi, [500, 80], 4, 128, 31, seed=13).check(capi, [130, 70], 4, 64)
+
+
 def test_evict_special_weights(capi):
     e = Evict(capi, [400], seed=3)
     w = e.w.view(-1)
