@@ -560,15 +560,16 @@ int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
     const bool held = of_thread(ranks, CT) <= MOST;
     if (!held || (long long)a.rows * ranks > 0x7fffffffll)
         return (int)launch_k(probs_rows_kernel<T>, dim3((unsigned)a.rows), dim3(PT), 0, s, a);
-    // Clusters that stay where rows are twice as many as run at once, and fill more than
-    // half of what their threads hold (rows of 151936 fp32 logits, in us, by them and by a
-    // cluster a row: 512 rows 142, 166; 200 rows 62, 69; 100 rows 34.5, 37.3; bf16 512 rows
-    // 150, 164; 300 rows of 100000 74, 70).
+    // Clusters that stay where rows are twice as many as run at once, and fill three quarters
+    // of what their threads hold, or are of 16 CTAs (in us, by them and by a cluster a row:
+    // 151936 fp32 logits, 512 rows 142, 166; 160 rows 50, 56; 80 rows 30.3, 30.5; bf16 512 rows
+    // 150, 164; 320 rows of 202048, in clusters of 16, 164, 175; and where they fill less,
+    // 320 rows of 100000 80, 75; bf16 83, 83; 160 rows of 48000 22.7, 20.1).
     const int cap = (int)((vecs + ranks - 1) / ranks), k_stream = of_thread(ranks, STREAM_CT);
     const bool ragged = a.vocab % VE || (reinterpret_cast<uintptr_t>(a.x) & 15) || a.x_row % VE ||
                         (reinterpret_cast<uintptr_t>(a.p) & 15) || a.p_row % 4;
-    if ((long long)a.rows * ranks > 4 * sms && k_stream > STREAM_MOST / 2 && k_stream <= STREAM_MOST &&
-        cap * stream_bytes<T>(ragged) <= 225 * 1024)
+    if ((long long)a.rows * ranks > 4 * sms && k_stream <= STREAM_MOST &&
+        (ranks > 8 || 4 * cap >= 3 * STREAM_MOST * STREAM_CT) && cap * stream_bytes<T>(ragged) <= 225 * 1024)
         return ragged ? launch_stream<T, STREAM_MOST, true>(a, ranks, cap, s) : launch_stream<T, STREAM_MOST, false>(a, ranks, cap, s);
     // few rows: more CTAs each, up to two an SM (50 rows of 32003 bf16 logits 8.3 -> 7.2 us;
     // three: 77 rows 9.7 -> 10.7)
