@@ -16,11 +16,17 @@
 // shared memory, and writes what it read once.  Rows that all run at once are
 // read straight into registers; more of them go through clusters that stay, whose
 // next row comes by a bulk copy to shared memory while one is worked on.  Larger
-// rows (above 307200 logits) are read three times, by one CTA.
+// rows (above 327680 logits) are read three times, by one CTA.
+//
+// One row of 151936 fp32 logits takes 5.0 us, launch, load, two exchanges and store one
+// after the other.  512 of them move 622 MB in 137 us, 4.5 TB/s: what holds them up is
+// each row's two exchanges, in which an SM has no other row to work on, and that clusters
+// of 8 with an SM a CTA find room on 120 of the 152 SMs.
 
 #include <mutex>
 
 #include "cluster_dev.cuh"
+#include "f32x2.cuh"
 #include "gemm.cuh"
 #include "kv8.cuh"
 #include "sampling.cuh"
@@ -79,12 +85,17 @@ __device__ __forceinline__ float weight(const RowRule& r, float x) {
     return x >= r.border ? ex2(y) : 0.f;
 }
 
+__device__ __forceinline__ float2 weight2(const RowRule& r, float2 x) {
+    const float2 d = add2(x, make_float2(-r.m, -r.m));
+    const float2 y = fma2(d, make_float2(r.c, r.c), mul2(d, make_float2(r.c_lo, r.c_lo)));
+    return make_float2(x.x >= r.border ? ex2(fmaxf(y.x, -256.f)) : 0.f, x.y >= r.border ? ex2(fmaxf(y.y, -256.f)) : 0.f);
+}
+
 __device__ __forceinline__ float row_min_p(const ProbsArgs& a, long long row) { return a.min_p ? a.min_p[row] : 0.f; }
 
 // ---- rows held by a cluster
 
-constexpr int CT = 512;                // threads of a CTA that has a row,
-constexpr int ST = 1024, STREAM_CT = ST - 32;      // of one that stays: all, and those at work
+constexpr int CT = 512;                // threads of a CTA
 
 template <typename T> constexpr int per_vec() { return 16 / (int)sizeof(T); }
 
@@ -100,7 +111,7 @@ struct Trade {
 // What the threads at work on a row share.
 struct RowShared {
     Trade max, sum;
-    float warps[2][ST / 32];
+    float warps[2][32];
     int best[2];
 };
 
@@ -177,10 +188,17 @@ __device__ __forceinline__ int extra_of(const Part& p, uint32_t rank) {
     return tid >= 16 && tid < 16 + p.tail ? p.tail_at + tid - 16 : -1;
 }
 
+// The vectors of a thread: at + k * step where below limit, k from 0 on.
+struct Mine {
+    int at, step, limit;
+    __device__ __forceinline__ int operator()(int k) const { return at + k * step; }
+    __device__ __forceinline__ bool has(int k) const { return at + k * step < limit; }
+};
+
 // A row's logits in registers (w: -inf where there is none) to its probabilities, by
 // the NT threads at work of each of the cluster's CTAs; the turn-th row of theirs.
 template <typename T, int K, int NT>
-__device__ __forceinline__ void finish_row(const Part& part, float (&w)[K * per_vec<T>()], float& extra, int e, float t,
+__device__ __forceinline__ void finish_row(const Part& part, const Mine& mine, float (&w)[K * per_vec<T>()], float& extra, int e, float t,
                                            const RowSetup& setup, RowShared& sh, int ranks, uint32_t rank, unsigned turn,
                                            bool first) {
     constexpr int VE = per_vec<T>();
@@ -197,7 +215,7 @@ __device__ __forceinline__ void finish_row(const Part& part, float (&w)[K * per_
             for (int k = K - 1; k >= 0; --k)
 #pragma unroll
                 for (int i = VE - 1; i >= 0; --i)
-                    if (w[k * VE + i] == m) best = part.head + (part.v0 + k * NT + tid) * VE + i;
+                    if (w[k * VE + i] == m) best = part.head + (part.v0 + mine(k)) * VE + i;
             if (extra == m) best = min(best, e);
         }
         best = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
@@ -209,18 +227,21 @@ __device__ __forceinline__ void finish_row(const Part& part, float (&w)[K * per_
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = part.head + (part.v0 + k * NT + tid) * VE + i == best ? 1.f : 0.f;
+            for (int i = 0; i < VE; ++i) w[k * VE + i] = part.head + (part.v0 + mine(k)) * VE + i == best ? 1.f : 0.f;
         extra = e == best ? 1.f : 0.f;
     } else {
         float sum;
         if (m < INFINITY) {
             const RowRule r = rule_of(m, setup);
-            sum = extra = weight(r, extra);
+            extra = weight(r, extra);
+            float2 sums = make_float2(extra, 0.f);
 #pragma unroll
-            for (int i = 0; i < K * VE; ++i) {
-                w[i] = weight(r, w[i]);
-                sum += w[i];
+            for (int i = 0; i < K * VE; i += 2) {
+                const float2 y = weight2(r, make_float2(w[i], w[i + 1]));
+                w[i] = y.x, w[i + 1] = y.y;
+                sums = add2(sums, y);
             }
+            sum = sums.x + sums.y;
         } else {
             sum = extra = extra == INFINITY ? 1.f : 0.f;
 #pragma unroll
@@ -233,43 +254,45 @@ __device__ __forceinline__ void finish_row(const Part& part, float (&w)[K * per_
         const float inv = 1.f / sum;
         extra *= inv;
 #pragma unroll
-        for (int i = 0; i < K * VE; ++i) w[i] *= inv;
+        for (int i = 0; i < K * VE; i += 2) {
+            const float2 y = mul2(make_float2(w[i], w[i + 1]), make_float2(inv, inv));
+            w[i] = y.x, w[i + 1] = y.y;
+        }
     }
 }
 
 // They to memory.
-template <typename T, int K, int NT>
-__device__ __forceinline__ void store_row(float* p, const Part& part, const float (&w)[K * per_vec<T>()], float extra, int e) {
+template <typename T, int K>
+__device__ __forceinline__ void store_row(float* p, const Part& part, const Mine& mine, const float (&w)[K * per_vec<T>()], float extra, int e) {
     constexpr int VE = per_vec<T>();
-    const int tid = threadIdx.x;
     if (e >= 0) p[e] = extra;
     float* pv = p + part.head + (long long)part.v0 * VE;
     if ((reinterpret_cast<uintptr_t>(pv) & 15) == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k * NT + tid < part.n)
+            if (mine.has(k))
 #pragma unroll
                 for (int i = 0; i < VE; i += 4)
-                    reinterpret_cast<float4*>(pv)[(k * NT + tid) * (VE / 4) + i / 4] =
+                    reinterpret_cast<float4*>(pv)[mine(k) * (VE / 4) + i / 4] =
                         make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k * NT + tid < part.n)
+            if (mine.has(k))
 #pragma unroll
-                for (int i = 0; i < VE; ++i) pv[(k * NT + tid) * VE + i] = w[k * VE + i];
+                for (int i = 0; i < VE; ++i) pv[mine(k) * VE + i] = w[k * VE + i];
     }
 }
 
 // K vectors of a thread to numbers.
-template <typename T, int K, int NT>
-__device__ __forceinline__ void to_numbers(const uint4 (&raw)[K], int n, float (&w)[K * per_vec<T>()]) {
+template <typename T, int K>
+__device__ __forceinline__ void to_numbers(const uint4 (&raw)[K], const Mine& mine, float (&w)[K * per_vec<T>()]) {
     constexpr int VE = per_vec<T>();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const T* r = reinterpret_cast<const T*>(&raw[k]);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) w[k * VE + i] = k * NT + (int)threadIdx.x < n ? to_f32(r[i]) : -INFINITY;
+        for (int i = 0; i < VE; ++i) w[k * VE + i] = mine.has(k) ? to_f32(r[i]) : -INFINITY;
     }
 }
 
@@ -294,43 +317,66 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     }
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
     const Part part = part_of_row<T, true>(x, a.vocab, ranks, rank);
+    const Mine mine{tid, CT, part.n};
     const uint4* xv = reinterpret_cast<const uint4*>(x + part.head) + part.v0;
     float w[K * per_vec<T>()], extra = -INFINITY;
     const int e = extra_of<true>(part, rank);
     uint4 raw[K];
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (k * CT + tid < part.n) raw[k] = xv[k * CT + tid];
+        if (mine.has(k)) raw[k] = xv[mine(k)];
     if (e >= 0) extra = to_f32(x[e]);
     if (tid == CT - 1) s_setup = setup_of(t, row_min_p(a, row));      // while they are on their way
-    to_numbers<T, K, CT>(raw, part.n, w);
-    finish_row<T, K, CT>(part, w, extra, e, t, s_setup, sh, ranks, rank, 0, true);
-    store_row<T, K, CT>(a.p + row * a.p_row, part, w, extra, e);
+    to_numbers<T, K>(raw, mine, w);
+    finish_row<T, K, CT>(part, mine, w, extra, e, t, s_setup, sh, ranks, rank, 0, true);
+    store_row<T, K>(a.p + row * a.p_row, part, mine, w, extra, e);
 }
 
 __device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;"
                  ::"l"((uint64_t)dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void bulk_store_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Clusters that take every gridDim.x / ranks-th row.  The last warp brings a CTA's
-// part of the next row to shared memory while one is worked on, and the rows'
-// setups; outputs leave by bulk copies, too (stores of the threads themselves held
-// up what they read behind them: 177 us for 512 rows of 151936).  RAGGED: rows whose
-// vectors are not whole, or not 16-byte aligned in the output, leave by plain stores.
-template <typename T, int K, bool RAGGED>
-__global__ void __launch_bounds__(ST, 1) probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap) {
-    constexpr int NT = STREAM_CT, VE = per_vec<T>();
-    extern __shared__ uint4 in[];                  // [2][cap], cap the vectors of a part; then the outputs
-    float4* out = reinterpret_cast<float4*>(in + 2 * cap);
+// Clusters that stay: threads of a CTA, CTAs an SM, threads at work on a row; vectors of a
+// lane in a piece of its warp's outputs, and the places for pieces.
+// Of 16-bit logits the next row takes half as much shared memory as its outputs would: two
+// CTAs fit an SM, one works while the other waits for its cluster, and outputs leave by
+// 1 KB pieces (512 rows of 151936: 132 us; by one CTA of 1024 threads an SM 150).  fp32
+// rows have one CTA and a place for all of a warp's outputs (137 us; in 1 KB pieces 153; two
+// CTAs in clusters of 16 150; two without a place for the next row 187).
+template <typename T> struct Stream {
+    static constexpr bool wide = sizeof(T) == 4;
+    static constexpr int threads = wide ? 1024 : 512, per_sm = wide ? 1 : 2, work = threads - 32;
+    static constexpr int most = 5;         // vectors of a thread
+    static constexpr int piece = wide ? most : 1, places = wide ? 1 : 2;
+    // of parts of cap vectors
+    static size_t smem(int cap, bool ragged) {
+        return (size_t)2 * cap * 16 + (ragged ? 0 : wide ? (size_t)cap * 16 : (size_t)work * places * piece * per_vec<T>() * 4);
+    }
+};
+
+// Clusters that take every gridDim.x / ranks-th row.  The last warp brings a CTA's part of
+// the next row to shared memory while one is worked on, and the rows' setups.  A warp's
+// vectors lie in a row, k_row a lane, so that its outputs leave by bulk copies of its own
+// (stores of the threads held up what they read behind them: 512 rows of 151936 fp32
+// logits 177 us).  RAGGED: rows whose vectors are not whole, or not 16-byte aligned in the
+// output, leave by plain stores.
+template <typename T, bool RAGGED>
+__global__ void __launch_bounds__(Stream<T>::threads, Stream<T>::per_sm)
+probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int k_row) {
+    using S_ = Stream<T>;
+    constexpr int NT = S_::work, K = S_::most, VE = per_vec<T>(), P = S_::piece;
+    extern __shared__ uint4 in[];                  // [2][cap], cap the vectors of a part; then the pieces
     __shared__ RowShared sh;
-    __shared__ RowSetup s_setup[2];
-    __shared__ float s_t[2];
+    __shared__ RowSetup s_setup[3];                // a row's stays until that of the third one behind it comes
+    __shared__ float s_t[3];
     __shared__ uint64_t full[2], empty[2];
     pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
     const int first_row = blockIdx.x / (unsigned)ranks, step = gridDim.x / (unsigned)ranks;
     if (tid == 0) {
@@ -357,8 +403,8 @@ __global__ void __launch_bounds__(ST, 1) probs_stream_kernel(const __grid_consta
                 const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
                 const int b = n & 1;
                 if (n >= 2 && !mbar_wait_bounded(empty + b, (n / 2 - 1) & 1)) break;
-                s_t[b] = t;
-                s_setup[b] = setup;
+                s_t[n % 3] = t;
+                s_setup[n % 3] = setup;
                 if (part.n > 0 && t >= 0.f && t < INFINITY) {
                     mbar_arrive_expect_tx(full + b, part.n * 16);
                     bulk_load_1d(in + b * cap, reinterpret_cast<const uint4*>(x + part.head) + part.v0, part.n * 16, full + b);
@@ -370,52 +416,60 @@ __global__ void __launch_bounds__(ST, 1) probs_stream_kernel(const __grid_consta
         __syncwarp();
         return;
     }
-    unsigned n = 0, turn = 0;
+    uint4* const pieces = in + 2 * cap + warp * (S_::wide ? k_row * 32 : S_::places * P * 32 * VE / 4);
+    unsigned n = 0, turn = 0, at_piece = 0;
     for (long long row = first_row; row < a.rows; row += step, ++n) {
         const T* x = x0 + row * a.x_row;
-        float* p = a.p + row * a.p_row;
         const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
+        const Mine mine{warp * k_row * 32 + lane, 32, min(part.n, (warp + 1) * k_row * 32)};
         const int e = extra_of<RAGGED>(part, rank), b = n & 1;
         float extra = e >= 0 ? to_f32(x[e]) : -INFINITY;
         const bool came = mbar_wait_bounded(full + b, (n / 2) & 1);
-        const float t = came ? s_t[b] : -1.f;
-        const bool fine = t >= 0.f && t < INFINITY;      // else the row is left as it was, by all of the cluster
-        const RowSetup setup = s_setup[b];
+        const float& t = s_t[n % 3];
+        const bool fine = came && t >= 0.f && t < INFINITY;      // else the row is left as it was, by all of the cluster
         uint4 raw[K];
         if (fine)
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (k * NT + tid < part.n) raw[k] = in[b * cap + k * NT + tid];
+                if (mine.has(k)) raw[k] = in[b * cap + mine(k)];
         float w[K * VE];
-        to_numbers<T, K, NT>(raw, fine ? part.n : 0, w);
+        to_numbers<T, K>(raw, fine ? mine : Mine{0, 0, 0}, w);
         // what was read is in registers before its place goes back (a fence would wait
         // for stores as well)
 #pragma unroll
         for (int i = 0; i < K * VE; ++i) asm volatile("" ::"f"(w[i]) : "memory");
-        asm volatile("" ::"f"(setup.c), "f"(setup.c_lo), "f"(setup.cut), "f"(setup.cut_lo) : "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + b);
         if (!came) break;
         if (!fine) continue;
-        // (the last row's outputs have left their place once thread 0 comes to the second barrier)
-        if (!RAGGED && tid == 0) bulk_store_read();
-        finish_row<T, K, NT>(part, w, extra, e, t, setup, sh, ranks, rank, turn++, false);
+        finish_row<T, K, NT>(part, mine, w, extra, e, t, s_setup[n % 3], sh, ranks, rank, turn++, false);
+        float* p = a.p + row * a.p_row;
         if constexpr (RAGGED) {
-            store_row<T, K, NT>(p, part, w, extra, e);
+            store_row<T, K>(p, part, mine, w, extra, e);
         } else {
+            float* const warp_p = p + ((long long)part.v0 + warp * k_row * 32) * VE;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k * NT + tid < part.n)
+            for (int k0 = 0; k0 < K; k0 += P) {
+                const int left = mine.limit - warp * k_row * 32 - k0 * 32;      // of the warp's vectors
+                if (left <= 0) break;
+                float4* out = reinterpret_cast<float4*>(pieces + (S_::wide ? 0 : at_piece++ % S_::places * (P * 32 * VE / 4)));
+                if (lane == 0) bulk_store_read<S_::places - 1>();               // the place's last piece has left it
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < VE; i += 4)
-                        out[(k * NT + tid) * (VE / 4) + i / 4] =
-                            make_float4(w[k * VE + i], w[k * VE + i + 1], w[k * VE + i + 2], w[k * VE + i + 3]);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            work_sync<NT>();
-            if (tid == 0 && part.n > 0) bulk_store_1d(p + (long long)part.v0 * VE, out, part.n * VE * 4);
+                for (int k = 0; k < P; ++k)
+                    if (!S_::wide || mine.has(k0 + k))
+#pragma unroll
+                        for (int i = 0; i < VE; i += 4) {
+                            const float* v = w + (k0 + k) * VE + i;
+                            out[(k * 32 + lane) * (VE / 4) + i / 4] = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bulk_store_1d(warp_p + k0 * 32 * VE, out, min(left, P * 32) * VE * 4);
+            }
         }
     }
-    if (!RAGGED && tid == 0) bulk_store_done();
+    if (!RAGGED && lane == 0) bulk_store_done();
 }
 
 // ---- rows of any length
@@ -532,27 +586,24 @@ int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
     return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)(a.rows * ranks)), dim3(CT), ranks, s, 0, a, ranks);
 }
 
-// Shared memory of a vector: in twice, and its outputs.
-template <typename T> constexpr int stream_bytes(bool ragged) { return 2 * 16 + (ragged ? 0 : per_vec<T>() * 4); }
-
-template <typename T, int K, bool RAGGED>
+template <typename T, bool RAGGED>
 int launch_stream(const ProbsArgs& a, int ranks, int cap, cudaStream_t s) {
-    const void* kern = reinterpret_cast<const void*>(probs_stream_kernel<T, K, RAGGED>);
-    const size_t smem = (size_t)cap * stream_bytes<T>(RAGGED);
+    const void* kern = reinterpret_cast<const void*>(probs_stream_kernel<T, RAGGED>);
+    const size_t smem = Stream<T>::smem(cap, RAGGED);
     int most = 0;
     cudaError_t e = allow_smem(kern);
     if (e == cudaSuccess && ranks > 8) e = allow_cluster(kern);
-    if (e == cudaSuccess) e = clusters_at_once(kern, ranks, ST, smem, &most);
+    if (e == cudaSuccess) e = clusters_at_once(kern, ranks, Stream<T>::threads, smem, &most);
     if (e != cudaSuccess) return (int)e;
     // the rounds that the clusters need, and no more clusters than fill them
     const int rounds = (a.rows + most - 1) / most, clusters = (a.rows + rounds - 1) / rounds;
-    return (int)launch_cluster_k(probs_stream_kernel<T, K, RAGGED>, dim3((unsigned)(clusters * ranks)), dim3(ST), ranks, s, smem,
-                                 a, ranks, cap);
+    return (int)launch_cluster_k(probs_stream_kernel<T, RAGGED>, dim3((unsigned)(clusters * ranks)), dim3(Stream<T>::threads), ranks, s, smem,
+                                 a, ranks, cap, (cap + Stream<T>::work - 1) / Stream<T>::work);
 }
 
 template <typename T>
 int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
-    constexpr int VE = per_vec<T>(), MOST = 40 / VE, STREAM_MOST = VE == 4 ? 5 : 3;      // vectors of a thread
+    constexpr int VE = per_vec<T>(), MOST = 40 / VE;      // vectors of a thread
     const long long vecs = ((long long)a.vocab + VE - 1) / VE;
     auto of_thread = [&](int ranks, int threads) { return (int)(((vecs + ranks - 1) / ranks + threads - 1) / threads); };
     int ranks = 1;
@@ -560,17 +611,20 @@ int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
     const bool held = of_thread(ranks, CT) <= MOST;
     if (!held || (long long)a.rows * ranks > 0x7fffffffll)
         return (int)launch_k(probs_rows_kernel<T>, dim3((unsigned)a.rows), dim3(PT), 0, s, a);
-    // Clusters that stay where rows are twice as many as run at once, and fill three quarters
-    // of what their threads hold, or are of 16 CTAs (in us, by them and by a cluster a row:
-    // 151936 fp32 logits, 512 rows 142, 166; 160 rows 50, 56; 80 rows 30.3, 30.5; bf16 512 rows
-    // 150, 164; 320 rows of 202048, in clusters of 16, 164, 175; and where they fill less,
-    // 320 rows of 100000 80, 75; bf16 83, 83; 160 rows of 48000 22.7, 20.1).
-    const int cap = (int)((vecs + ranks - 1) / ranks), k_stream = of_thread(ranks, STREAM_CT);
+    // Clusters that stay where rows are more than twice what run at once by a cluster a row, and
+    // the registers mostly filled, or the clusters of 16 CTAs (in us, by them and by a cluster a
+    // row: 151936 logits, fp32 320 rows 89, 101; 160 rows 48, 53; 80 rows 29.6, 29.5; bf16 320
+    // rows 91, 102; 100 rows 33, 36; of 262144 logits, in clusters of 16, fp32 320 rows 171, 203;
+    // bf16 320 rows of 100000 73, 80; where they fill less, fp32 320 rows of 100000 80, 74, bf16 of
+    // 48000 39, 36; of fewer rows, bf16 160 rows of 64000, 640 CTAs, 27.5, 26.1).
+    const int cap = (int)((vecs + ranks - 1) / ranks), k_stream = of_thread(ranks, Stream<T>::work);
     const bool ragged = a.vocab % VE || (reinterpret_cast<uintptr_t>(a.x) & 15) || a.x_row % VE ||
                         (reinterpret_cast<uintptr_t>(a.p) & 15) || a.p_row % 4;
-    if ((long long)a.rows * ranks > 4 * sms && k_stream <= STREAM_MOST &&
-        (ranks > 8 || 4 * cap >= 3 * STREAM_MOST * STREAM_CT) && cap * stream_bytes<T>(ragged) <= 225 * 1024)
-        return ragged ? launch_stream<T, STREAM_MOST, true>(a, ranks, cap, s) : launch_stream<T, STREAM_MOST, false>(a, ranks, cap, s);
+    const bool filled = VE == 4 ? 4 * cap >= 3 * Stream<T>::most * Stream<T>::work : 8 * cap > 5 * Stream<T>::most * Stream<T>::work;
+    const bool many = (long long)a.rows * ranks > (VE == 4 || ranks > 8 ? 4 : 5) * sms;
+    if (many && (filled || ranks > 8) && k_stream <= Stream<T>::most &&
+        Stream<T>::smem(cap, ragged) <= 226 * 1024 / Stream<T>::per_sm)
+        return ragged ? launch_stream<T, true>(a, ranks, cap, s) : launch_stream<T, false>(a, ranks, cap, s);
     // few rows: more CTAs each, up to two an SM (50 rows of 32003 bf16 logits 8.3 -> 7.2 us;
     // three: 77 rows 9.7 -> 10.7)
     while (ranks < 8 && (long long)a.rows * ranks * 2 <= 2 * sms && of_thread(ranks, CT) > 1) ranks *= 2;

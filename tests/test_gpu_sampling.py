@@ -178,8 +178,9 @@ def test_probs_rows_do_not_depend_on_the_others(capi, rows):
     assert torch.equal(out, again)
 
 
-MANY = [(700, 16000, F32), (700, 16003, F32), (1300, 20000, BF), (640, 20001, F16), (330, 40000, F32), (90, 151936, F32),
-        (100, 151936, BF), (45, 210000, F32), (45, 210001, F32), (50, 300001, BF)]
+MANY = [(700, 16000, F32), (700, 16003, F32), (1300, 20000, BF), (640, 20001, F16), (1240, 20001, F16),
+        (330, 40000, F32), (90, 151936, F32), (100, 151936, BF), (170, 151936, BF), (45, 210000, F32), (45, 210001, F32),
+        (50, 300000, BF), (50, 300001, BF)]
 
 
 def many_rows(rows, V, kind):
