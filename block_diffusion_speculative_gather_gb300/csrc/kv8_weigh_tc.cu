@@ -15,7 +15,10 @@
 // tiles in turn, one thread to a key: 128 columns of tensor memory, an
 // exponential each, summed.  Each group has two tiles of tensor memory, so that the
 // next one's scores are there when it comes.  Bound by the exponentials (16 a
-// cycle and SM: 1024 cycles a tile, whose MMAs take 512).
+// cycle and SM: 1024 cycles a tile, whose MMAs take 512) and the instructions around
+// them: the last 64 rows of four prompts behind up to 8192 positions (32 heads on 8) take
+// 24.3 us, a third of the exponentials' rate: a CTA has one or two items, whose start
+// (tables, tensor memory, the first keys and rows) nothing hides.
 
 #include <type_traits>
 
@@ -426,15 +429,18 @@ int launch_tc(const CUtensorMap& q_map, const Kv8WeighArgs& a, int sms, cudaStre
 
 }  // namespace
 
-#ifndef WEIGH_TC_FROM
-#define WEIGH_TC_FROM 20
-#endif
+// From this many (row, q head) pairs of a kv head a sequence on, of the call's rows on
+// average.  32 heads on 8, bf16, in us by this form and by kv8_weigh.cu: 32 sequences of 8000
+// positions, 4 pairs 70, 35; 16 pairs 64, 52; 32 pairs 64, 87; 64 pairs 67, 151; one
+// sequence of 1088, 4 pairs 10.8, 8.3; 16 pairs 10.8, 11.4; 64 pairs 11.7, 30.
+constexpr int TC_PAIRS = 20;
+
 bool kv8_weigh_by_tc(const Kv8WeighArgs& a) {
     long long rows = a.rows / a.S;
     if (a.observe > 0 && rows > a.observe) rows = a.observe;
     // a tensor map's strides are above 0 and below 2^40 bytes
     const bool fits = a.q_row > 0 && a.q_head > 0 && a.q_row < (1LL << 39) && a.q_head < (1LL << 39);
-    return fits && rows * a.group >= WEIGH_TC_FROM;
+    return fits && rows * a.group >= TC_PAIRS;
 }
 
 int launch_kv8_weigh_tc(const CUtensorMap& q_map, const Kv8WeighArgs& a, int head_dim, int sms, cudaStream_t s) {

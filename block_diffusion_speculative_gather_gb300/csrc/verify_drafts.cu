@@ -17,6 +17,12 @@
 // warps (each CTA finds by itself, from two numbers a draft, which row that is),
 // a unit's sum goes to memory, and the last of a sequence's CTAs finds the unit
 // that u_0 falls into and reads it again.  No CTA waits for another.
+//
+// With 151936 tokens and 16 rows a sequence one takes 7.4 us, a chain of trips to
+// memory: row starts, ids, p and q of the drafts, the row, the ticket, the sums, the unit.
+// 32 take 11.6 us for 38.9 MB, the same chain with the reading at 6 TB/s in it; 480 rows
+// without drafts 57 us, 5.1 TB/s, where a pair's additions (7 instructions a token) and
+// the chain at each CTA's end stand beside the reads.
 
 #include "sampling.cuh"
 
@@ -397,8 +403,10 @@ __global__ void __launch_bounds__(VT, 4) verify_kernel(const __grid_constant__ V
 }  // namespace
 
 int launch_verify_drafts(const VerifyArgs& a, int sms, cudaStream_t s) {
-    // a unit a warp while all CTAs run at once, else as many CTAs a sequence as do; many
-    // sequences: about four rounds of them, so that the last one is short
+    // a unit a warp while all CTAs run at once (four an SM), else as many CTAs a sequence as
+    // do; many sequences: about four rounds of them, so that the last one is short (151936
+    // tokens: 100 sequences 17.4 us, with a unit a warp 19.4; 480 in four rounds 57, in one
+    // 64, with a unit a warp 65)
     const int most = (a.units + VW - 1) / VW;
     const long long room = 4LL * sms;
     long long x = most;
