@@ -700,19 +700,21 @@ int dflash_probs(const void* logits, int64_t logits_row, int32_t dtype, const fl
  * the first that is not.  The last token is the first v with w_0 + .. + w_v >
  * uniform[r0] * sum w, w = probs[r0+a], after a refused draft max(probs[r0+a] -
  * draft_probs[r0+a+1], 0) (certain drafts: probs[r0+a] without the draft; where
- * that has no weight probs[r0+a]).  A uniform number of 1 or more, or NaN, draws the last token
- * with weight, a negative one the first.  Probabilities need not be normalised;
- * negative and NaN ones, and those of 2^100 or more, count as 0.
+ * that has no weight probs[r0+a]).  A uniform number of 1 or more, or NaN,
+ * draws the last token with weight, a negative one the first.  Probabilities
+ * need not be normalised; negative and NaN ones, and those of 2^100 or more,
+ * count as 0.
  *   tokens [rows]: the a accepted drafts and the last token at rows r0 ..,
  * -1 in the sequence's rows behind; rows in no sequence are not written.
  * n_tokens [S] = a + 1, the rows that stay; new_len [S] (NULL: not wanted)
  * = kv_len[s] - (n - 1 - a), for dflash_pages_trim.  A row without weight
- * draws no token: n_tokens is a, tokens -1 (new_len as above).  A sequence of no rows: 0 tokens, its
- * length.  So a sequence of one row draws one token.
+ * draws no token: n_tokens is a, tokens -1 (new_len as above).  A sequence of
+ * no rows: 0 tokens, its length.  So a sequence of one row draws one token.
  * vocab up to 2^24, S up to 65535, any number of rows a sequence.
- * Workspace: dflash_verify_workspace_bytes, 256-byte aligned, zero-filled before its first use
- * (completed calls leave its counters at zero); calls of any shapes can share
- * one that is large enough for each, but must not overlap on the GPU.
+ * Workspace: dflash_verify_workspace_bytes, 256-byte aligned, zero-filled
+ * before its first use (completed calls leave its counters at zero); calls of
+ * any shapes can share one that is large enough for each, but must not overlap
+ * on the GPU.
  * err: device int32[2], zero before the first call: an id of vocab or above (no
  * draft there) writes {2, row}, row starts outside the rows {2, sequence} (that
  * sequence gets 0 tokens); the first error stays until the caller clears it.
@@ -740,21 +742,21 @@ int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_
 
 /*
  * Accumulated attention weight of the cached positions, for dflash_kv8_evict:
- *   weights[slot of j] += sum over rows i and q heads h of exp(scale * q_ih . k_j - lse_ih)
- * over the rows that see position j (masks as in dflash_kv8_attention, whose lse
- * this takes; q->out is not used).  Of a sequence's rows the first count[s]
- * count (NULL: all; below 0: none), of those with observe > 0 the last `observe`: after
- * verification count = n_tokens leaves rejected rows out, and a long prompt's last rows stand
- * for it.  fresh 1: the step's own positions (every row's) start from 0 (the
- * first layer's call of a step; the others add).  weights: fp32 [n_pages]
- * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  A page belongs to
- * one sequence.  Terms are added in a fixed order, without atomics; a sequence's
- * results depend on its own rows and positions and the call's counts, not on the
- * others.  Scores that are NaN (a NaN code) add nothing, nor does a row whose lse is
- * -inf or NaN.
- * Shapes, strides and types as dflash_kv8_attention; err {2, site} for lengths and pages out of range, whose
- * sequence (page) is left out.
- * Errors: CONFIG, ARG, CUDA.
+ *   weights[slot of j] += sum over rows i and q heads h of
+ *                         exp(scale * q_ih . k_j - lse_ih)
+ * over the rows that see position j (masks as in dflash_kv8_attention, whose
+ * lse this takes; q->out is not used).  Of a sequence's rows the first count[s] count (NULL: all; below 0: none), of
+ * those with observe > 0 the last `observe`: after verification count =
+ * n_tokens leaves rejected rows out, and a long prompt's last rows stand for
+ * it.  fresh 1: the step's own positions (every row's) start from 0 (the first
+ * layer's call of a step; the others add).  weights: fp32 [n_pages]
+ * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  A page
+ * belongs to one sequence.  Terms are added in a fixed order, without atomics;
+ * a sequence's results depend on its own rows and positions and the call's
+ * counts, not on the others.  Scores that are NaN (a NaN code) add nothing,
+ * nor does a row whose lse is -inf or NaN.  Shapes, strides and types as
+ * dflash_kv8_attention; err {2, site} for lengths and pages out of range,
+ * whose sequence (page) is left out.  Errors: CONFIG, ARG, CUDA.
  */
 int dflash_kv8_weigh(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_query* q /*host*/, float* weights,
                      const int32_t* count, int32_t observe, int32_t fresh, int32_t* err, dflash_stream_t stream);
@@ -770,14 +772,16 @@ int dflash_kv8_weigh(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_qu
  * of the scales that its positions came with, codes with a smaller one are
  * rounded to it (nearest even); pages whose positions stay where they are do
  * not change.  source [S][max_pages * DFLASH_KV8_PAGE]: the earlier position of
- * each kept one, the rest is left as it was; new_len [S] = the positions kept (not kv_len);
- * dropped [S] (NULL: not wanted) grows by those that went.  kv_len and table do not change:
- * dflash_pages_trim with new_len takes the pages back.  Later rows attend over what is left; the
- * kept keys hold their true rotary positions, so new rows are rotated at the
- * cache's position + dropped (dflash_pages_shift), and masks (causal, window) count cached positions.
- * Pages belong to one sequence each.  Workspace: any contents, not shared by calls that overlap.
- * err {2, site}: a length or page out of range; that sequence is left alone
- * (new_len = kv_len).  S up to 4096, max_pages up to 2^24.  Errors: CONFIG, ARG, CUDA.
+ * each kept one, the rest is left as it was; new_len [S] = the positions kept
+ * (not kv_len); dropped [S] (NULL: not wanted) grows by those that went.
+ * kv_len and table do not change: dflash_pages_trim with new_len takes the
+ * pages back.  Later rows attend over what is left; the kept keys hold their
+ * true rotary positions, so new rows are rotated at the cache's position +
+ * dropped (dflash_pages_shift), and masks (causal, window) count cached
+ * positions.  Pages belong to one sequence each.
+ * Workspace: any contents, not shared by calls that overlap.  err {2, site}: a
+ * length or page out of range; that sequence is left alone (new_len = kv_len).
+ * S up to 4096, max_pages up to 2^24.  Errors: CONFIG, ARG, CUDA.
  */
 typedef struct {
     const int32_t* table;       /* [S][max_pages] */
