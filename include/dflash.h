@@ -745,18 +745,18 @@ int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_
  *   weights[slot of j] += sum over rows i and q heads h of
  *                         exp(scale * q_ih . k_j - lse_ih)
  * over the rows that see position j (masks as in dflash_kv8_attention, whose
- * lse this takes; q->out is not used).  Of a sequence's rows the first count[s] count (NULL: all; below 0: none), of
- * those with observe > 0 the last `observe`: after verification count =
- * n_tokens leaves rejected rows out, and a long prompt's last rows stand for
- * it.  fresh 1: the step's own positions (every row's) start from 0 (the first
- * layer's call of a step; the others add).  weights: fp32 [n_pages]
- * [DFLASH_KV8_PAGE], one for all layers of a table or one each.  A page
- * belongs to one sequence.  Terms are added in a fixed order, without atomics;
- * a sequence's results depend on its own rows and positions and the call's
- * counts, not on the others.  Scores that are NaN (a NaN code) add nothing,
- * nor does a row whose lse is -inf or NaN.  Shapes, strides and types as
- * dflash_kv8_attention; err {2, site} for lengths and pages out of range,
- * whose sequence (page) is left out.  Errors: CONFIG, ARG, CUDA.
+ * lse this takes; q->out is not used).  Of a sequence's rows the first count[s]
+ * count (NULL: all; below 0: none), of those with observe > 0 the last
+ * `observe`: after verification count = n_tokens leaves rejected rows out, and
+ * a long prompt's last rows stand for it.  fresh 1: the step's own positions
+ * (every row's) start from 0 (the first layer's call of a step; the others
+ * add).  weights: fp32 [n_pages][DFLASH_KV8_PAGE], one for all layers of a
+ * table or one each.  A page belongs to one sequence.  Terms are added in a
+ * fixed order, without atomics; a sequence's results depend on its own rows
+ * and positions and the call's counts, not on the others.  Scores that are NaN
+ * (a NaN code) add nothing, nor does a row whose lse is -inf or NaN.
+ * Shapes, strides and types as dflash_kv8_attention; err {2, site} for lengths
+ * and pages out of range, whose sequence (page) is left out.  Errors: CONFIG, ARG, CUDA.
  */
 int dflash_kv8_weigh(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_query* q /*host*/, float* weights,
                      const int32_t* count, int32_t observe, int32_t fresh, int32_t* err, dflash_stream_t stream);
