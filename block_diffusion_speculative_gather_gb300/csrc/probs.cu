@@ -540,7 +540,8 @@ cudaError_t allow_cluster(const void* kern) {
     return e;
 }
 
-// Clusters of a kernel that run at once on the current device, asked for once.
+// Clusters of a kernel that run at once on the current device, asked for once (how long
+// the rows are, and so how much shared memory a CTA takes, does not change how many fit).
 cudaError_t clusters_at_once(const void* kern, int ranks, int threads, size_t smem, int* most) {
     static std::mutex mu;
     constexpr int MAX = 256;
