@@ -354,8 +354,8 @@ template <typename T> struct Stream {
     static constexpr int most = 5;         // vectors of a thread
     static constexpr int piece = wide ? most : 1, places = wide ? 1 : 2;
     // of parts of cap vectors
-    static size_t smem(int cap, bool ragged) {
-        return (size_t)2 * cap * 16 + (ragged ? 0 : wide ? (size_t)cap * 16 : (size_t)work * places * piece * per_vec<T>() * 4);
+    static size_t smem(int cap) {
+        return (size_t)2 * cap * 16 + (wide ? (size_t)cap * 16 : (size_t)work * places * piece * per_vec<T>() * 4);
     }
 };
 
@@ -363,9 +363,8 @@ template <typename T> struct Stream {
 // the next row to shared memory while one is worked on, and the rows' setups.  A warp's
 // vectors lie in a row, k_row a lane, so that its outputs leave by bulk copies of its own
 // (stores of the threads held up what they read behind them: 512 rows of 151936 fp32
-// logits 177 us).  RAGGED: rows whose vectors are not whole, or not 16-byte aligned in the
-// output, leave by plain stores.
-template <typename T, bool RAGGED>
+// logits 177 us).  Rows of whole vectors, 16-byte aligned in the output.
+template <typename T>
 __global__ void __launch_bounds__(Stream<T>::threads, Stream<T>::per_sm)
 probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int k_row) {
     using S_ = Stream<T>;
@@ -400,7 +399,7 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
                 const float t = a.temperature[row];
                 const RowSetup setup = setup_of(t, row_min_p(a, row));
                 const T* x = x0 + row * a.x_row;
-                const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
+                const Part part = part_of_row<T, false>(x, a.vocab, ranks, rank);
                 const int b = n & 1;
                 if (n >= 2 && !mbar_wait_bounded(empty + b, (n / 2 - 1) & 1)) break;
                 s_t[n % 3] = t;
@@ -419,11 +418,10 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
     uint4* const pieces = in + 2 * cap + warp * (S_::wide ? k_row * 32 : S_::places * P * 32 * VE / 4);
     unsigned n = 0, turn = 0, at_piece = 0;
     for (long long row = first_row; row < a.rows; row += step, ++n) {
-        const T* x = x0 + row * a.x_row;
-        const Part part = part_of_row<T, RAGGED>(x, a.vocab, ranks, rank);
+        const Part part = part_of_row<T, false>(x0, a.vocab, ranks, rank);
         const Mine mine{warp * k_row * 32 + lane, 32, min(part.n, (warp + 1) * k_row * 32)};
-        const int e = extra_of<RAGGED>(part, rank), b = n & 1;
-        float extra = e >= 0 ? to_f32(x[e]) : -INFINITY;
+        const int b = n & 1;
+        float extra = -INFINITY;
         const bool came = mbar_wait_bounded(full + b, (n / 2) & 1);
         const float& t = s_t[n % 3];
         const bool fine = came && t >= 0.f && t < INFINITY;      // else the row is left as it was, by all of the cluster
@@ -442,34 +440,29 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
         if (lane == 0) mbar_arrive(empty + b);
         if (!came) break;
         if (!fine) continue;
-        finish_row<T, K, NT>(part, mine, w, extra, e, t, s_setup[n % 3], sh, ranks, rank, turn++, false);
-        float* p = a.p + row * a.p_row;
-        if constexpr (RAGGED) {
-            store_row<T, K>(p, part, mine, w, extra, e);
-        } else {
-            float* const warp_p = p + ((long long)part.v0 + warp * k_row * 32) * VE;
+        finish_row<T, K, NT>(part, mine, w, extra, -1, t, s_setup[n % 3], sh, ranks, rank, turn++, false);
+        float* const warp_p = a.p + row * a.p_row + ((long long)part.v0 + warp * k_row * 32) * VE;
 #pragma unroll
-            for (int k0 = 0; k0 < K; k0 += P) {
-                const int left = mine.limit - warp * k_row * 32 - k0 * 32;      // of the warp's vectors
-                if (left <= 0) break;
-                float4* out = reinterpret_cast<float4*>(pieces + (S_::wide ? 0 : at_piece++ % S_::places * (P * 32 * VE / 4)));
-                if (lane == 0) bulk_store_read<S_::places - 1>();               // the place's last piece has left it
-                __syncwarp();
+        for (int k0 = 0; k0 < K; k0 += P) {
+            const int left = mine.limit - warp * k_row * 32 - k0 * 32;      // of the warp's vectors
+            if (left <= 0) break;
+            float4* out = reinterpret_cast<float4*>(pieces + (S_::wide ? 0 : at_piece++ % S_::places * (P * 32 * VE / 4)));
+            if (lane == 0) bulk_store_read<S_::places - 1>();               // the place's last piece has left it
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < P; ++k)
-                    if (!S_::wide || mine.has(k0 + k))
+            for (int k = 0; k < P; ++k)
+                if (!S_::wide || mine.has(k0 + k))
 #pragma unroll
-                        for (int i = 0; i < VE; i += 4) {
-                            const float* v = w + (k0 + k) * VE + i;
-                            out[(k * 32 + lane) * (VE / 4) + i / 4] = make_float4(v[0], v[1], v[2], v[3]);
-                        }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) bulk_store_1d(warp_p + k0 * 32 * VE, out, min(left, P * 32) * VE * 4);
-            }
+                    for (int i = 0; i < VE; i += 4) {
+                        const float* v = w + (k0 + k) * VE + i;
+                        out[(k * 32 + lane) * (VE / 4) + i / 4] = make_float4(v[0], v[1], v[2], v[3]);
+                    }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bulk_store_1d(warp_p + k0 * 32 * VE, out, min(left, P * 32) * VE * 4);
         }
     }
-    if (!RAGGED && lane == 0) bulk_store_done();
+    if (lane == 0) bulk_store_done();
 }
 
 // ---- rows of any length
@@ -587,10 +580,10 @@ int launch_cluster(const ProbsArgs& a, int ranks, cudaStream_t s) {
     return (int)launch_cluster_k(probs_cluster_kernel<T, K>, dim3((unsigned)(a.rows * ranks)), dim3(CT), ranks, s, 0, a, ranks);
 }
 
-template <typename T, bool RAGGED>
+template <typename T>
 int launch_stream(const ProbsArgs& a, int ranks, int cap, cudaStream_t s) {
-    const void* kern = reinterpret_cast<const void*>(probs_stream_kernel<T, RAGGED>);
-    const size_t smem = Stream<T>::smem(cap, RAGGED);
+    const void* kern = reinterpret_cast<const void*>(probs_stream_kernel<T>);
+    const size_t smem = Stream<T>::smem(cap);
     int most = 0;
     cudaError_t e = allow_smem(kern);
     if (e == cudaSuccess && ranks > 8) e = allow_cluster(kern);
@@ -598,7 +591,7 @@ int launch_stream(const ProbsArgs& a, int ranks, int cap, cudaStream_t s) {
     if (e != cudaSuccess) return (int)e;
     // the rounds that the clusters need, and no more clusters than fill them
     const int rounds = (a.rows + most - 1) / most, clusters = (a.rows + rounds - 1) / rounds;
-    return (int)launch_cluster_k(probs_stream_kernel<T, RAGGED>, dim3((unsigned)(clusters * ranks)), dim3(Stream<T>::threads), ranks, s, smem,
+    return (int)launch_cluster_k(probs_stream_kernel<T>, dim3((unsigned)(clusters * ranks)), dim3(Stream<T>::threads), ranks, s, smem,
                                  a, ranks, cap, (cap + Stream<T>::work - 1) / Stream<T>::work);
 }
 
@@ -617,15 +610,17 @@ int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
     // row: 151936 logits, fp32 320 rows 89, 101; 160 rows 48, 53; 80 rows 29.6, 29.5; bf16 320
     // rows 91, 102; 100 rows 33, 36; of 262144 logits, in clusters of 16, fp32 320 rows 171, 203;
     // bf16 320 rows of 100000 73, 80; where they fill less, fp32 320 rows of 100000 80, 74, bf16 of
-    // 48000 39, 36; of fewer rows, bf16 160 rows of 64000, 640 CTAs, 27.5, 26.1).
+    // 48000 39, 36; of fewer rows, bf16 160 rows of 64000, 640 CTAs, 27.5, 26.1).  Rows that are
+    // not of whole aligned vectors would have to be stored by their threads: bf16 512 rows of
+    // 32003 41, 36; 320 of 151935 112, 103; fp32 99, 102.
     const int cap = (int)((vecs + ranks - 1) / ranks), k_stream = of_thread(ranks, Stream<T>::work);
-    const bool ragged = a.vocab % VE || (reinterpret_cast<uintptr_t>(a.x) & 15) || a.x_row % VE ||
-                        (reinterpret_cast<uintptr_t>(a.p) & 15) || a.p_row % 4;
+    const bool whole = a.vocab % VE == 0 && !(reinterpret_cast<uintptr_t>(a.x) & 15) && a.x_row % VE == 0 &&
+                       !(reinterpret_cast<uintptr_t>(a.p) & 15) && a.p_row % 4 == 0;
     const bool filled = VE == 4 ? 4 * cap >= 3 * Stream<T>::most * Stream<T>::work : 8 * cap > 5 * Stream<T>::most * Stream<T>::work;
     const bool many = (long long)a.rows * ranks > (VE == 4 || ranks > 8 ? 4 : 5) * sms;
-    if (many && (filled || ranks > 8) && k_stream <= Stream<T>::most &&
-        Stream<T>::smem(cap, ragged) <= 226 * 1024 / Stream<T>::per_sm)
-        return ragged ? launch_stream<T, true>(a, ranks, cap, s) : launch_stream<T, false>(a, ranks, cap, s);
+    if (whole && many && (filled || ranks > 8) && k_stream <= Stream<T>::most &&
+        Stream<T>::smem(cap) <= 226 * 1024 / Stream<T>::per_sm)
+        return launch_stream<T>(a, ranks, cap, s);
     // few rows: more CTAs each, up to two an SM (50 rows of 32003 bf16 logits 8.3 -> 7.2 us;
     // three: 77 rows 9.7 -> 10.7)
     while (ranks < 8 && (long long)a.rows * ranks * 2 <= 2 * sms && of_thread(ranks, CT) > 1) ranks *= 2;
