@@ -21,6 +21,10 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 
+// Orders this thread's memory accesses, and those it has seen ordered before them, with
+// the cluster's, for an arrival that orders none.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 // Sends a word to where p lies in this CTA, in CTA `rank`, and four bytes to its
 // mbarrier that lies where bar does.
 __device__ __forceinline__ void send_word(void* p, uint64_t* bar, uint32_t rank, uint32_t v) {

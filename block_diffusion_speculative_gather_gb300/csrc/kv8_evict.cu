@@ -20,10 +20,11 @@
 // read.  A CTA has one kv head's K or V of a sequence and layer and goes through
 // its pages in order, 16 KB at a time, by a ring in shared memory: the copies of
 // the next three turns are on their way while one is written, which none of them
-// reads.  Where CTAs are few, a cluster shares the pages of a turn.  Bound by DRAM where
+// reads.  Where CTAs are few, a cluster shares the pages of a turn; its barrier stands
+// between a turn's reads and its writes.  Bound by DRAM where
 // sequences and layers are many: 8 of up to 6000 positions to 2500, 10 layers of 8 heads of
 // 128, move 818 MB in 139 us with the choice, 5.9 TB/s (three turns in the ring 152 us).
-// One of 4095 to 2048, 5 layers: 17.8 us, the choice and a chain of turns.
+// One of 4095 to 2048, 5 layers: 18.6 us, the choice and a chain of turns.
 
 #include "cluster_dev.cuh"
 #include "copy_dev.cuh"
@@ -388,14 +389,15 @@ __global__ void __launch_bounds__(MT, 3) kv8_move_kernel(const __grid_constant__
     pages_at(0);
     for (int t = 0; t < turns; ++t) {
         copy_wait<MS - 2>();
-        // the turn's positions have been read, by every thread that reads any of them:
-        // the copies are complete, so no memory has to be ordered (a barrier that orders
-        // it would wait for the last turn's stores)
+        // This thread's copies of the turn are complete.  The barrier makes them the CTA's (a
+        // row's scale comes by one thread and is read by all), and the ring's place of turn
+        // t - 1 has been read.
+        __syncthreads();
+        // The other CTAs write where this one has read: one thread's fence stands for the CTA's
+        // reads, which the barrier above has put before it.
         if (ranks > 1) {
+            if (tid == 0) fence_cluster();
             cluster_arrive_relaxed();
-            cluster_wait();
-        } else {
-            __syncthreads();
         }
         fetch(t + MS - 1);              // into the ring's place of turn t - 1
         look(t + MS);
@@ -406,8 +408,11 @@ __global__ void __launch_bounds__(MT, 3) kv8_move_kernel(const __grid_constant__
             const int d = d0 + i * KV8_PAGE;
             const float* sc = sm.scale[t % MS] + i * KV8_PAGE;
             top[i] = warp_max(fmaxf(d + lane < kept ? sc[lane] : 0.f, d + 32 + lane < kept ? sc[32 + lane] : 0.f));
-            if (tid == 0 && d < kept) scale[(size_t)page[i] * a.n_kv] = top[i];
         }
+        if (ranks > 1) cluster_wait();  // the turn's positions have been read, by all who read any of them
+#pragma unroll
+        for (int i = 0; i < PAGES; ++i)
+            if (tid == 0 && d0 + i * KV8_PAGE < kept) scale[(size_t)page[i] * a.n_kv] = top[i];
 #pragma unroll
         for (int i = 0; i < MN; ++i) {
             const int row = r0 + i * STEP, d = d0 + row;
@@ -470,7 +475,7 @@ int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choo
     }
     const int chains = a.S * a.n_kv;
     // Three CTAs of the move run on an SM.  Few chains: as many CTAs each as run at once (one
-    // sequence of 4095 positions to 2048, 5 layers: 17.7 us, by one CTA each 28.3).  More
+    // sequence of 4095 positions to 2048, 5 layers: 18.6 us, by one CTA each 28.3).  More
     // than run at once: two each where that takes at least an eighth less rounds (of 6000
     // positions to 2500: 576 chains 91 us, by one CTA each 113; 960 chains 117 and 124; where
     // it does not, 1280 chains 147 and 139).

@@ -415,6 +415,21 @@ def test_evict_more_pools_than_run_at_once(capi):
     Evict(capi, [500, 80], 4, 128, 31, seed=13).check(capi, [130, 70], 4, 64)
 
 
+def test_evict_clusters_repeat_their_bits(capi):
+    """Few chains: clusters of 2, 4 and 8 CTAs share the pages of a turn, over many
+    turns.  Neighbouring pages' scales differ, so a scale of another turn would show."""
+    for held, budget, n_kv, dim, layers in (([6000], [5000], 1, 128, 2), ([5000], [4500], 4, 128, 5),
+                                            ([7000, 3000], [6000, 2900], 8, 64, 4), ([9000], [8500], 2, 64, 1)):
+        make = lambda: Evict(capi, held, n_kv, dim, layers, seed=layers, spread=6)      # noqa: E731
+        first = make()
+        first.check(capi, budget, 4, 64)
+        for _ in range(5):
+            again = make().run(capi, budget, 4, 64)
+            assert torch.equal(again.w, first.w) and torch.equal(again.source, first.source)
+            for a, b in zip(again.caches, first.caches):
+                assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_evict_special_weights(capi):
     e = Evict(capi, [400], seed=3)
     w = e.w.view(-1)
