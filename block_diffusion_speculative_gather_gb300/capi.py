@@ -169,6 +169,7 @@ def _load() -> C.CDLL:
         "dflash_rope": (C.c_int, [C.POINTER(dflash_rope_config), vp, vp, i32, i32, i32,
                                   vp, vp, vp]),
         "dflash_probs": (C.c_int, [vp, i64, i32, vp, vp, i32, i32, vp, i64, vp]),
+        "dflash_selftest_exchange": (C.c_int, [vp, vp, i32, i32, vp, i32, i32, i32, i64, vp]),
         "dflash_verify_workspace_bytes": (sz, [i32, i32]),
         "dflash_verify_drafts": (C.c_int, [vp, vp, sz, vp, vp]),
         "dflash_kv8_weigh": (C.c_int, [vp, vp, vp, vp, i32, i32, vp, vp]),
@@ -197,8 +198,8 @@ EXPORTED = ("dflash_workspace_bytes", "dflash_kv_target_bytes", "dflash_kv_draft
             "dflash_batch_draft", "dflash_batch_verify_accept", "dflash_batch_set_logits_out",
             "dflash_batch_check", "dflash_batch_destroy", "dflash_pages_plan", "dflash_pages_trim",
             "dflash_kv8_append", "dflash_kv8_workspace_bytes", "dflash_kv8_attention",
-            "dflash_rope_turns", "dflash_rope", "dflash_probs", "dflash_verify_workspace_bytes",
-            "dflash_verify_drafts", "dflash_kv8_weigh", "dflash_kv8_evict_workspace_bytes",
+            "dflash_rope_turns", "dflash_rope", "dflash_probs", "dflash_selftest_exchange",
+            "dflash_verify_workspace_bytes", "dflash_verify_drafts", "dflash_kv8_weigh", "dflash_kv8_evict_workspace_bytes",
             "dflash_kv8_evict", "dflash_pages_shift")
 
 
@@ -817,6 +818,18 @@ def dflash_probs(logits, temperature, out, min_p=None, stream=None):
                           _raw(stream, dev))
     if rc:
         check(rc)
+
+
+def dflash_selftest_exchange(logits, temperature, out, stays: bool, word: int, row: int, limit_ns: int, stream=None):
+    """dflash_probs of fp32 rows by clusters of two CTAs (one a row, or one that
+    stays for all rows) whose second CTA keeps its word of an exchange to itself."""
+    rows, vocab = logits.shape
+    _need(logits, "logits", (_F32,), (None, None))
+    _need(out, "out", (_F32,), (rows, vocab))
+    _need(temperature, "temperature", (_F32,), (rows,))
+    _here(logits=logits, out=out, temperature=temperature)
+    check(lib.dflash_selftest_exchange(logits.data_ptr(), temperature.data_ptr(), rows, vocab, out.data_ptr(),
+                                       1 if stays else 0, word, row, limit_ns, _raw(stream, logits.get_device())))
 
 
 def dflash_verify_workspace_bytes(S: int, vocab: int) -> int:

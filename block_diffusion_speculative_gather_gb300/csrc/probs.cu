@@ -42,6 +42,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ float no_nan(float x) { return x == x ? x : -INFINITY; }
 
+// A row without one is left as it was.
+__device__ __forceinline__ bool has_temperature(float t) { return t >= 0.f && t < INFINITY; }
+
 // What a row's temperature and min_p come to, by one thread.
 struct RowSetup {
     float c, c_lo;        // log2(e) / T
@@ -113,6 +116,10 @@ struct RowShared {
     Trade max, sum;
     float warps[2][32];
     int best[2];
+    unsigned stop;         // the cluster's row (by its own count) from which on this CTA works on none
+    // Behind 16 more bytes a RowSetup stays at an odd multiple of 8, and its fields are loaded one
+    // by one as they are needed; by fours they held registers (512 rows of 151936 bf16 logits 155 us).
+    unsigned pad[3];
 };
 
 // By one thread, then the cluster's opening barrier.
@@ -121,6 +128,7 @@ __device__ __forceinline__ void open_row(RowShared& sh) {
     mbar_init(&sh.sum.bar, 1);
     fence_mbar_init();
     sh.best[0] = sh.best[1] = 0x7fffffff;
+    sh.stop = 0xffffffffu;
 }
 
 // A barrier of the NT threads at work.
@@ -129,31 +137,65 @@ template <int NT> __device__ __forceinline__ void work_sync() {
     else asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
 }
 
-// v the same in all of the CTA, the turn-th exchange by t; false: the others' did not come.
-__device__ __forceinline__ bool trade(Trade& t, uint32_t v, int ranks, uint32_t rank, unsigned turn) {
+// A wait that runs out (the others of a cluster did not come within two seconds) leaves a
+// warp without a word; the others of its CTA may have got it.  So no warp changes its
+// way: it carries NaN (a greedy row's token: -1) through the same barriers and sends it
+// on, and what it writes is NaN.  A row is right, or NaN wherever it might not be.
+//
+// SELFTEST: the last CTA of a cluster keeps its word `a.quiet` (0: the maximum's, 1: the
+// sum's) of row a.quiet_row to itself, and waits end after a.limit_ns.
+constexpr unsigned long long LIMIT_NS = 2000000000ull;
+
+template <bool SELFTEST> __device__ __forceinline__ unsigned long long limit_of(const ProbsArgs& a) {
+    return SELFTEST ? a.limit_ns : LIMIT_NS;
+}
+
+// v the same in all of the CTA, the turn-th exchange by t, of the cluster's n-th row; false,
+// in all of a warp: the others' words did not come.
+template <bool SELFTEST>
+__device__ __forceinline__ bool trade(const ProbsArgs& a, RowShared& sh, bool sum, uint32_t v, int ranks, uint32_t rank, unsigned n,
+                                      unsigned turn) {
+    Trade& t = sum ? sh.sum : sh.max;
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&t.bar, 4 * ranks);
-    if ((int)threadIdx.x < ranks) send_word(&t.all[rank], &t.bar, threadIdx.x, v);
-    return mbar_wait_bounded(&t.bar, turn & 1);
+    const bool quiet = SELFTEST && (int)rank == ranks - 1 && sum == (a.quiet == 1) && n == (unsigned)a.quiet_row;
+    if ((int)threadIdx.x < ranks && !quiet) send_word(&t.all[rank], &t.bar, threadIdx.x, v);
+    const bool came = __all_sync(0xffffffffu, mbar_wait_bounded(&t.bar, turn & 1, limit_of<SELFTEST>(a)));
+    if (!came) atomicMin(&sh.stop, n + 1);
+    return came;
+}
+
+// At the end of a CTA one of whose waits has run out: its shared memory stays until the
+// cluster's other warps have ended or wait here too, and their words are in.
+template <bool SELFTEST> __device__ __noinline__ void linger(const ProbsArgs& a, RowShared& sh, unsigned turn) {
+    cluster_arrive_relaxed();
+    cluster_wait();
+    mbar_wait_bounded(&sh.max.bar, turn & 1, limit_of<SELFTEST>(a));
+    mbar_wait_bounded(&sh.sum.bar, turn & 1, limit_of<SELFTEST>(a));
 }
 
 __device__ __forceinline__ float warp_all(float v, bool sum) { return sum ? warp_sum(v) : warp_max(v); }
 
-// The sum (or the largest) of a warp value over the cluster, the same everywhere; NaN
-// if the other CTAs' did not come.  `first`: the opening barrier is still to be waited for.
-// A lane takes a warp's (a CTA's) value and the warp joins them: every thread
+// The sum (or the largest) of a warp value over the CTA, the same in all of it.
+// A lane takes a warp's (below, a CTA's) value and the warp joins them: every thread
 // reading all of them cost as many instructions as 20 logits.
-template <int NT>
-__device__ __forceinline__ float over_cluster(Trade& t, float* warps, float v, bool sum, int ranks, uint32_t rank, unsigned turn,
-                                              bool first) {
+template <int NT> __device__ __forceinline__ float over_cta(float* warps, float v, bool sum) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float none = sum ? 0.f : -INFINITY;
     if (lane == 0) warps[warp] = v;
     work_sync<NT>();
-    const float r = warp_all(lane < NT / 32 ? warps[lane] : none, sum);
-    if (ranks == 1) return r;
+    return warp_all(lane < NT / 32 ? warps[lane] : (sum ? 0.f : -INFINITY), sum);
+}
+
+// The same of a CTA's value over the cluster; NaN if the other CTAs' did not come.
+// `first`: the opening barrier is still to be waited for.
+template <bool SELFTEST>
+__device__ __forceinline__ float over_cluster(const ProbsArgs& a, RowShared& sh, float v, bool sum, int ranks, uint32_t rank, unsigned n,
+                                              unsigned turn, bool first) {
+    if (ranks == 1) return v;
     if (first) cluster_wait();
-    if (!trade(t, __float_as_uint(r), ranks, rank, turn)) return __int_as_float(0x7fffffff);
-    return warp_all(lane < ranks ? __uint_as_float(t.all[lane]) : none, sum);
+    if (!trade<SELFTEST>(a, sh, sum, __float_as_uint(v), ranks, rank, n, turn)) return NAN;
+    const int lane = threadIdx.x & 31;
+    const Trade& t = sum ? sh.sum : sh.max;
+    return warp_all(lane < ranks ? __uint_as_float(t.all[lane]) : (sum ? 0.f : -INFINITY), sum);
 }
 
 // Where a CTA's part of a row lies: vectors of 16 bytes that begin at 16-byte
@@ -196,21 +238,25 @@ struct Mine {
 };
 
 // A row's logits in registers (w: -inf where there is none) to its probabilities, by
-// the NT threads at work of each of the cluster's CTAs; the turn-th row of theirs.
-template <typename T, int K, int NT>
-__device__ __forceinline__ void finish_row(const Part& part, const Mine& mine, float (&w)[K * per_vec<T>()], float& extra, int e, float t,
-                                           const RowSetup& setup, RowShared& sh, int ranks, uint32_t rank, unsigned turn,
-                                           bool first) {
+// the NT threads at work of each of the cluster's CTAs; the cluster's n-th row, and the
+// turn-th that it works on.  greedy: T is 0.  False, in all of the CTA: it has stopped
+// before this row.
+template <typename T, int K, int NT, bool SELFTEST>
+__device__ __forceinline__ bool finish_row(const ProbsArgs& a, const Part& part, const Mine& mine, float (&w)[K * per_vec<T>()],
+                                           float& extra, int e, bool greedy, const RowSetup& setup, RowShared& sh, int ranks,
+                                           uint32_t rank, unsigned n, unsigned turn, bool first) {
     constexpr int VE = per_vec<T>();
     const int tid = threadIdx.x;
     float m = no_nan(extra);                       // fmaxf leaves NaN out
 #pragma unroll
     for (int i = 0; i < K * VE; ++i) m = fmaxf(m, w[i]);
-    m = over_cluster<NT>(sh.max, sh.warps[0], warp_max(m), false, ranks, rank, turn, first);
+    m = over_cta<NT>(sh.warps[0], warp_max(m), false);
+    if (NT != CT && sh.stop <= n) return false;
+    m = over_cluster<SELFTEST>(a, sh, m, false, ranks, rank, n, turn, first);
     if (tid == 0) sh.best[(turn & 1) ^ 1] = 0x7fffffff;      // the next row's: the last one's has been read
-    if (t == 0.f || m == -INFINITY) {              // (a NaN m, of a wait that ran out, makes the row NaN)
-        int best = 0x7fffffff;
-        if (m != -INFINITY) {
+    if (greedy) {
+        int best = m == m ? 0x7fffffff : -1;
+        if (m > -INFINITY) {
 #pragma unroll
             for (int k = K - 1; k >= 0; --k)
 #pragma unroll
@@ -218,23 +264,26 @@ __device__ __forceinline__ void finish_row(const Part& part, const Mine& mine, f
                     if (w[k * VE + i] == m) best = part.head + (part.v0 + mine(k)) * VE + i;
             if (extra == m) best = min(best, e);
         }
-        best = (int)__reduce_min_sync(0xffffffffu, (unsigned)best);
+        best = __reduce_min_sync(0xffffffffu, best);
         if ((tid & 31) == 0) atomicMin(&sh.best[turn & 1], best);
         work_sync<NT>();
         best = sh.best[turn & 1];
-        if (ranks > 1 && trade(sh.sum, (uint32_t)best, ranks, rank, turn))
-            for (int i = 0; i < ranks; ++i) best = min(best, (int)sh.sum.all[i]);
+        if (ranks > 1) {
+            const bool came = trade<SELFTEST>(a, sh, true, (uint32_t)best, ranks, rank, n, turn);
+            for (int i = 0; i < ranks; ++i) best = came ? min(best, (int)sh.sum.all[i]) : -1;
+        }
+        const float other = best < 0 ? NAN : 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) w[k * VE + i] = part.head + (part.v0 + mine(k)) * VE + i == best ? 1.f : 0.f;
-        extra = e == best ? 1.f : 0.f;
+            for (int i = 0; i < VE; ++i) w[k * VE + i] = part.head + (part.v0 + mine(k)) * VE + i == best ? 1.f : other;
+        extra = best >= 0 && e == best ? 1.f : other;
     } else {
         float sum;
-        if (m < INFINITY) {
+        if (m != INFINITY) {                       // (-inf: no logit above it, all weights are 0)
             const RowRule r = rule_of(m, setup);
             extra = weight(r, extra);
-            float2 sums = make_float2(extra, 0.f);
+            float2 sums = make_float2(extra, m == m ? 0.f : NAN);
 #pragma unroll
             for (int i = 0; i < K * VE; i += 2) {
                 const float2 y = weight2(r, make_float2(w[i], w[i + 1]));
@@ -250,8 +299,8 @@ __device__ __forceinline__ void finish_row(const Part& part, const Mine& mine, f
                 sum += w[i];
             }
         }
-        sum = over_cluster<NT>(sh.sum, sh.warps[1], warp_sum(sum), true, ranks, rank, turn, false);
-        const float inv = 1.f / sum;
+        sum = over_cluster<SELFTEST>(a, sh, over_cta<NT>(sh.warps[1], warp_sum(sum), true), true, ranks, rank, n, turn, false);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         extra *= inv;
 #pragma unroll
         for (int i = 0; i < K * VE; i += 2) {
@@ -259,6 +308,7 @@ __device__ __forceinline__ void finish_row(const Part& part, const Mine& mine, f
             w[i] = y.x, w[i + 1] = y.y;
         }
     }
+    return true;
 }
 
 // They to memory.
@@ -297,7 +347,7 @@ __device__ __forceinline__ void to_numbers(const uint4 (&raw)[K], const Mine& mi
 }
 
 // A cluster a row.
-template <typename T, int K>
+template <typename T, int K, bool SELFTEST = false>
 __global__ void __launch_bounds__(CT, K * per_vec<T>() > 12 ? 2 : 3)
 probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     __shared__ RowShared sh;
@@ -310,7 +360,7 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     if (ranks > 1) cluster_arrive_relaxed();
     pdl_wait();
     const float t = a.temperature[row];
-    const bool fine = t >= 0.f && t < INFINITY;    // else the row is left as it was, by all of the cluster
+    const bool fine = has_temperature(t);          // else the row is left as it was, by all of the cluster
     if (!fine) {
         if (ranks > 1) cluster_wait();
         return;
@@ -328,8 +378,9 @@ probs_cluster_kernel(const __grid_constant__ ProbsArgs a, int ranks) {
     if (e >= 0) extra = to_f32(x[e]);
     if (tid == CT - 1) s_setup = setup_of(t, row_min_p(a, row));      // while they are on their way
     to_numbers<T, K>(raw, mine, w);
-    finish_row<T, K, CT>(part, mine, w, extra, e, t, s_setup, sh, ranks, rank, 0, true);
+    finish_row<T, K, CT, SELFTEST>(a, part, mine, w, extra, e, t == 0.f, s_setup, sh, ranks, rank, 0, 0, true);
     store_row<T, K>(a.p + row * a.p_row, part, mine, w, extra, e);
+    if (sh.stop != 0xffffffffu) linger<SELFTEST>(a, sh, 0);
 }
 
 __device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
@@ -364,7 +415,9 @@ template <typename T> struct Stream {
 // vectors lie in a row, k_row a lane, so that its outputs leave by bulk copies of its own
 // (stores of the threads held up what they read behind them: 512 rows of 151936 fp32
 // logits 177 us).  Rows of whole vectors, 16-byte aligned in the output.
-template <typename T>
+// Once a wait has run out the CTA works on no further row: its part of them becomes NaN,
+// and the others of the cluster wait for its words in vain and do the same.
+template <typename T, bool SELFTEST = false>
 __global__ void __launch_bounds__(Stream<T>::threads, Stream<T>::per_sm)
 probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int k_row) {
     using S_ = Stream<T>;
@@ -401,30 +454,40 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
                 const T* x = x0 + row * a.x_row;
                 const Part part = part_of_row<T, false>(x, a.vocab, ranks, rank);
                 const int b = n & 1;
-                if (n >= 2 && !mbar_wait_bounded(empty + b, (n / 2 - 1) & 1)) break;
+                if (n >= 2 && !mbar_wait_bounded(empty + b, (n / 2 - 1) & 1, limit_of<SELFTEST>(a))) break;
                 s_t[n % 3] = t;
                 s_setup[n % 3] = setup;
-                if (part.n > 0 && t >= 0.f && t < INFINITY) {
+                if (part.n > 0 && has_temperature(t)) {
                     mbar_arrive_expect_tx(full + b, part.n * 16);
                     bulk_load_1d(in + b * cap, reinterpret_cast<const uint4*>(x + part.head) + part.v0, part.n * 16, full + b);
                 } else {
                     mbar_arrive(full + b);
                 }
             }
+            // no copy is in flight when this warp ends
+            for (unsigned i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_wait_bounded(full + (i & 1), (i / 2) & 1, limit_of<SELFTEST>(a));
         }
         __syncwarp();
         return;
     }
     uint4* const pieces = in + 2 * cap + warp * (S_::wide ? k_row * 32 : S_::places * P * 32 * VE / 4);
     unsigned n = 0, turn = 0, at_piece = 0;
-    for (long long row = first_row; row < a.rows; row += step, ++n) {
+    long long row = first_row;
+    for (; row < a.rows; row += step, ++n) {
         const Part part = part_of_row<T, false>(x0, a.vocab, ranks, rank);
         const Mine mine{warp * k_row * 32 + lane, 32, min(part.n, (warp + 1) * k_row * 32)};
         const int b = n & 1;
         float extra = -INFINITY;
-        const bool came = mbar_wait_bounded(full + b, (n / 2) & 1);
+        const bool came = __all_sync(0xffffffffu, mbar_wait_bounded(full + b, (n / 2) & 1, limit_of<SELFTEST>(a)));
+        if (!came) {
+            // the others of the CTA may have it: they stop behind their next barrier
+            atomicMin(&sh.stop, n);
+            while (row < a.rows && !has_temperature(a.temperature[row])) row += step;
+            if (row < a.rows) work_sync<NT>();
+            break;
+        }
         const float& t = s_t[n % 3];
-        const bool fine = came && t >= 0.f && t < INFINITY;      // else the row is left as it was, by all of the cluster
+        const bool fine = has_temperature(t);            // else the row is left as it was, by all of the cluster
         uint4 raw[K];
         if (fine)
 #pragma unroll
@@ -438,9 +501,9 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
         for (int i = 0; i < K * VE; ++i) asm volatile("" ::"f"(w[i]) : "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + b);
-        if (!came) break;
         if (!fine) continue;
-        finish_row<T, K, NT>(part, mine, w, extra, -1, t, s_setup[n % 3], sh, ranks, rank, turn++, false);
+        if (!finish_row<T, K, NT, SELFTEST>(a, part, mine, w, extra, -1, t == 0.f, s_setup[n % 3], sh, ranks, rank, n, turn, false)) break;
+        ++turn;
         float* const warp_p = a.p + row * a.p_row + ((long long)part.v0 + warp * k_row * 32) * VE;
 #pragma unroll
         for (int k0 = 0; k0 < K; k0 += P) {
@@ -463,6 +526,13 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
         }
     }
     if (lane == 0) bulk_store_done();
+    for (; row < a.rows; row += step) {                  // of a CTA that has stopped
+        if (!has_temperature(a.temperature[row])) continue;
+        const Part part = part_of_row<T, false>(x0, a.vocab, ranks, rank);
+        float* const p = a.p + row * a.p_row + (long long)part.v0 * VE;
+        for (int i = warp * k_row * 32 * VE + lane; i < min(part.n, (warp + 1) * k_row * 32) * VE; i += 32) p[i] = NAN;
+    }
+    if (ranks > 1 && sh.stop != 0xffffffffu) linger<SELFTEST>(a, sh, turn);
 }
 
 // ---- rows of any length
@@ -479,7 +549,7 @@ __global__ void __launch_bounds__(PT) probs_rows_kernel(const __grid_constant__ 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row = blockIdx.x;
     const float t = a.temperature[row];
-    if (!(t >= 0.f) || t == INFINITY) return;
+    if (!has_temperature(t)) return;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_row;
     float* p = a.p + row * a.p_row;
     if (tid == 0) {
@@ -634,6 +704,18 @@ int launch_t(const ProbsArgs& a, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+int launch_probs_selftest(const ProbsArgs& a, bool stays, cudaStream_t s) {
+    constexpr int ranks = 2;
+    if (!stays)
+        return (int)launch_cluster_k(probs_cluster_kernel<float, 1, true>, dim3((unsigned)(a.rows * ranks)), dim3(CT), ranks, s, 0, a, ranks);
+    using S_ = Stream<float>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(probs_stream_kernel<float, true>));
+    const int cap = (a.vocab / 4 + ranks - 1) / ranks;
+    return (int)(e == cudaSuccess ? launch_cluster_k(probs_stream_kernel<float, true>, dim3(ranks), dim3(S_::threads), ranks, s,
+                                                     S_::smem(cap), a, ranks, cap, (cap + S_::work - 1) / S_::work)
+                                  : e);
+}
 
 int launch_probs(const ProbsArgs& a, int sms, cudaStream_t s) {
     if (a.dtype == 0) return launch_t<float>(a, sms, s);

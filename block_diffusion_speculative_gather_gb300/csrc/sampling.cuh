@@ -12,8 +12,14 @@ struct ProbsArgs {
     const float* min_p;         // [rows] or NULL
     float* p;
     int rows, vocab, dtype;     // dtype 0 fp32, 1 bf16, 2 f16
+    // of the self-test's kernels alone: the row and exchange without one CTA's word, how long waits last
+    int quiet_row, quiet;
+    unsigned long long limit_ns;
 };
 int launch_probs(const ProbsArgs& a, int sms, cudaStream_t s);
+constexpr int SELFTEST_VOCAB = 4096;     // tokens that clusters of two hold, four a thread
+// fp32 rows of whole aligned vectors, by clusters of two: one a row, or (`stays`) one for all.
+int launch_probs_selftest(const ProbsArgs& a, bool stays, cudaStream_t s);
 
 constexpr int VERIFY_MAX_SEQS = 65535;
 constexpr int VERIFY_MAX_VOCAB = 1 << 24;

@@ -62,6 +62,19 @@ int dflash_probs(const void* logits, int64_t logits_row, int32_t dtype, const fl
     return launched(launch_probs(a, sms, reinterpret_cast<cudaStream_t>(stream)), "probabilities");
 }
 
+int dflash_selftest_exchange(const float* logits, const float* temperature, int32_t rows, int32_t vocab, float* probs,
+                             int32_t stays, int32_t word, int32_t row, int64_t limit_ns, dflash_stream_t stream) {
+    if (!logits || !temperature || !probs || !aligned(logits, 16) || !aligned(probs, 16) || !aligned(temperature, 4))
+        return report_error(DFLASH_ERR_ARG, "NULL or misaligned argument");
+    if (rows < 1 || rows > 4096 || vocab < 4 || vocab > SELFTEST_VOCAB || vocab % 4 || word < 0 || word > 1 || row < 0 ||
+        limit_ns < 1 || limit_ns > 1000000000)
+        return report_error(DFLASH_ERR_ARG, "rows %d (1 to 4096) vocab %d (4 to %d, by 4) word %d row %d limit_ns %lld (to 1 s)",
+                            rows, vocab, SELFTEST_VOCAB, word, row, (long long)limit_ns);
+    if (const int r = pending()) return r;
+    ProbsArgs a{logits, vocab, vocab, temperature, nullptr, probs, rows, vocab, 0, row, word, (unsigned long long)limit_ns};
+    return launched(launch_probs_selftest(a, stays != 0, reinterpret_cast<cudaStream_t>(stream)), "probabilities' self-test");
+}
+
 size_t dflash_verify_workspace_bytes(int32_t S, int32_t vocab) {
     if (S < 1 || S > VERIFY_MAX_SEQS || vocab < 1 || vocab > VERIFY_MAX_VOCAB) {
         report_error(DFLASH_ERR_CONFIG, "S %d (1 to %d) vocab %d (1 to 2^24)", S, VERIFY_MAX_SEQS, vocab);

@@ -678,13 +678,23 @@ int dflash_rope(const dflash_rope_config* cfg /*host*/, const uint64_t* turns, c
  * elements between rows, tokens contiguous; at any alignment of the types (rows
  * that are 16-byte aligned together are faster).  fp32 probabilities may be
  * written over their logits (same address and row).  A row's last bits can follow
- * from the number of rows (the order of its sum).  The sampled counterpart of
+ * from the number of rows (the order of its sum).  Should the CTAs of a row not
+ * hear from one another within two seconds, what they write of it, and of the rows
+ * that they would have gone on to, is NaN.  The sampled counterpart of
  * the round's argmax; no counterpart in the source pages, which decode greedily.
  * Errors: ARG, CUDA.
  */
 int dflash_probs(const void* logits, int64_t logits_row, int32_t dtype, const float* temperature,
                  const float* min_p, int32_t rows, int32_t vocab, float* probs, int64_t probs_row,
                  dflash_stream_t stream);
+
+/* Self-test of that wait: probabilities of contiguous fp32 rows (1 to 4096, of 4 to 4096
+ * tokens, a multiple of 4; 16-byte aligned) by clusters of two CTAs, one a row, or
+ * (stays 1) one for all rows, whose second CTA keeps its word of an exchange (0:
+ * the maximum's, 1: the sum's) of row `row` (by a cluster's own count from 0) to
+ * itself; waits end after limit_ns (at most 10^9).  Errors: ARG, CUDA. */
+int dflash_selftest_exchange(const float* logits, const float* temperature, int32_t rows, int32_t vocab, float* probs,
+                             int32_t stays, int32_t word, int32_t row, int64_t limit_ns, dflash_stream_t stream);
 
 /*
  * Verification of drafted tokens against the target's probabilities from given

@@ -257,6 +257,34 @@ def test_probs_many_rows_captured_and_side_by_side(capi):
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
+@pytest.mark.parametrize("word", [0, 1])
+@pytest.mark.parametrize("stays", [False, True])
+def test_probs_whose_exchange_does_not_come_about(capi, stays, word):
+    """A CTA that hears nothing of the others within its limit (5 ms here): what it
+    writes is NaN, and so is every later row of its cluster; rows before are right,
+    rows without a temperature as they were, and the next call works."""
+    rows, V, at = 9, 2004, 3
+    x = logits(rows, V, F32, 2)
+    x[5] = -INF
+    x[4, 7] = INF
+    for greedy in (False, True):
+        t = floats([0.7, 0.0, 1.0, 0.0 if greedy else 0.9, 1.0, 2.0, -1.0, 0.0, 1.5])
+        out = torch.full((rows, V), 7.0, device="cuda")
+        # where clusters have a row each, all of them have but one, their first
+        capi.dflash_selftest_exchange(x, t, out, stays, word, at if stays else 0, 5_000_000)
+        torch.cuda.synchronize()
+        assert (out[6] == 7.0).all()
+        good, lost = ([0, 1, 2], [3, 4, 5, 7, 8]) if stays else ([], [0, 1, 2, 3, 4, 5, 7, 8])
+        check_probs(x, t, out, rows=good)
+        assert torch.isnan(out[lost]).all()
+        # a row that no cluster has: nothing is withheld
+        capi.dflash_selftest_exchange(x, t, out, stays, word, 100, 5_000_000)
+        check_probs(x, t, out, rows=[r for r in range(rows) if r != 6])
+        assert (out[6] == 7.0).all()
+    capi.dflash_probs(x, t, out)
+    check_probs(x, t, out, rows=[r for r in range(rows) if r != 6])
+
+
 # ------------------------------------------------------------------ verification
 
 class Call:

@@ -34,6 +34,15 @@ def test_probs_guards(capi):      # noqa: F811
     assert call(None, 100, 0, None, None, 0, 100, None, 100, None) == 0      # no rows
 
 
+def test_selftest_exchange_guards(capi):      # noqa: F811
+    ok = [PTR, PTR, 3, 100, PTR + 4096, 0, 0, 0, 1000, None]
+    for at, bad in ((0, None), (0, PTR + 4), (1, None), (1, PTR + 2), (2, 0), (2, 4097), (3, 0), (3, 98), (3, 4100), (4, None),
+                    (4, PTR + 8), (6, -1), (6, 2), (7, -1), (8, 0), (8, 10 ** 9 + 1)):
+        a = list(ok)
+        a[at] = bad
+        assert capi.lib.dflash_selftest_exchange(*a) == ARG, (at, bad)
+
+
 def _drafts(capi, **kw):      # noqa: F811
     d = dict(probs=PTR, draft_probs=PTR, ids=PTR, uniform=PTR, row_start=PTR, kv_len=PTR, tokens=PTR + 64, n_tokens=PTR,
              new_len=PTR, probs_row=100, draft_row=100, rows=3, vocab=100, S=2, pad_=0)
