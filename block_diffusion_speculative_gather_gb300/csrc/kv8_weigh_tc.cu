@@ -46,7 +46,7 @@ template <int HD> struct TcWeighSmem {
     static constexpr int col = raw + 2 * RB;                             // [2 groups][2][128] -lse in base 2
     static constexpr int part = col + 4 * TILE * 4;                      // [2][128] the second group's sums
     static constexpr int bars = part + 2 * TILE * 4;
-    static constexpr int n_bars = 2 * QS + 4 + 4 + 8;
+    static constexpr int n_bars = 2 * QS + 4 + 4 + 8 + 1;
     static constexpr int misc = bars + n_bars * 8;                       // tensor-memory base, abort flag
     static constexpr int sums = misc + 16;
     static constexpr int before = sums + 64;
@@ -125,7 +125,7 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
     uint64_t *q_full = bars, *q_empty = bars + QS, *r_full = bars + 2 * QS, *r_empty = r_full + 2, *k_full = r_full + 4,
-             *k_empty = r_full + 6, *s_full = r_full + 8, *s_free = r_full + 12;
+             *k_empty = r_full + 6, *s_full = r_full + 8, *s_free = r_full + 12, *drain = r_full + 16;
     uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::misc);
     volatile int* abort = reinterpret_cast<volatile int*>(sm + L::misc + 4);
     int* before = reinterpret_cast<int*>(sm + L::before);
@@ -150,6 +150,7 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             mbar_init(s_full + i, 1);
             mbar_init(s_free + i, 4);
         }
+        mbar_init(drain, 1);
         fence_mbar_init();
         *abort = 0;
     }
@@ -368,6 +369,11 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
                 }
             }
         }
+        // every MMA has finished before tensor memory is given back, those too whose readers gave up
+        if (tc::elect_one()) tc::commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0);
+        __syncwarp();
     } else {
         // ---------------------------------------------------------- loads
         if (lane == 0) {
@@ -411,7 +417,6 @@ kv8_weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         __syncwarp();
     }
-    // every MMA has been waited for by the groups that read it
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
