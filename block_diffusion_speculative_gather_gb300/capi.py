@@ -956,8 +956,8 @@ def dflash_kv8_weigh(q, lse, k_codes, v_codes, k_scale, v_scale, table, kv_len, 
 
 class kv8_layers:
     """The pools of a model's layers, [(k_codes, v_codes, k_scale, v_scale), ..],
-    all of one shape on one device, checked and packed once for
-    dflash_kv8_evict.  Holds the tensors."""
+    all of one shape on one device and none given twice, checked and packed once
+    for dflash_kv8_evict.  Holds the tensors."""
 
     def __init__(self, caches):
         self.caches = [tuple(c) for c in caches]

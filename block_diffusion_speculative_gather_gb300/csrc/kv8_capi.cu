@@ -1,6 +1,7 @@
 // C entry points of the 8-bit paged KV cache and of rotary positions:
 // argument checks, tensor maps and launches.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -15,6 +16,7 @@ namespace {
 constexpr int KV8_MAX_SEQS = 4096;        // a lane of an attention CTA's finding warp scans S / 32 of them
 constexpr int KV8_MAX_PAGES = 1 << 25;    // slots are int32
 constexpr int KV8_EVICT_PAGES = 1 << 24;  // positions, and a step beyond, are int32
+constexpr int KV8_EVICT_LAYERS = 1024;
 constexpr int MAX_COUNT = 1 << 30;        // rows or sequences: sums of two of them, and a step beyond, are int32
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -42,6 +44,30 @@ int check_cache(const dflash_kv8_cache* c) {
                             c->n_pages, c->n_kv);
     if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return report_error(DFLASH_ERR_ARG, "misaligned cache buffer");
+    return DFLASH_OK;
+}
+
+// The pools of checked layers of one shape lie apart: eviction moves all at once.
+int check_apart(const dflash_kv8_cache* layers, int n) {
+    struct Range {
+        uintptr_t begin, end;
+    } all[4 * KV8_EVICT_LAYERS];
+    const size_t rows = (size_t)layers[0].n_pages * layers[0].n_kv;
+    const size_t codes = rows * KV8_PAGE * layers[0].head_dim, scales = rows * sizeof(float);
+    int m = 0;
+    auto add = [&](const void* p, size_t bytes) {
+        all[m++] = Range{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+    };
+    for (int i = 0; i < n; ++i) {
+        add(layers[i].k_codes, codes);
+        add(layers[i].v_codes, codes);
+        add(layers[i].k_scale, scales);
+        add(layers[i].v_scale, scales);
+    }
+    std::sort(all, all + m, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    for (int i = 1; i < m; ++i)
+        if (all[i].begin < all[i - 1].end)
+            return report_error(DFLASH_ERR_ARG, "two pools of the layers overlap: one given twice?");
     return DFLASH_OK;
 }
 
@@ -341,7 +367,8 @@ int dflash_kv8_evict(const dflash_kv8_cache* layers, int32_t n_layers, const dfl
                      size_t workspace_bytes, int32_t* err, dflash_stream_t stream) {
     if (!layers || !e || !workspace || !aligned(workspace, 256) || !err || !aligned(err, 8))
         return report_error(DFLASH_ERR_ARG, "NULL or misaligned argument");
-    if (n_layers < 1 || n_layers > 1024) return report_error(DFLASH_ERR_ARG, "%d layers: 1 to 1024", n_layers);
+    if (n_layers < 1 || n_layers > KV8_EVICT_LAYERS)
+        return report_error(DFLASH_ERR_ARG, "%d layers: 1 to %d", n_layers, KV8_EVICT_LAYERS);
     for (int i = 0; i < n_layers; ++i) {
         if (const int r = check_cache(layers + i)) return r;
         if (layers[i].n_pages != layers[0].n_pages || layers[i].n_kv != layers[0].n_kv ||
@@ -355,6 +382,7 @@ int dflash_kv8_evict(const dflash_kv8_cache* layers, int32_t n_layers, const dfl
     if (e->new_len == e->kv_len) return report_error(DFLASH_ERR_ARG, "new_len is kv_len: the move needs both");
     if (e->keep_first < 0 || e->keep_last < 0)
         return report_error(DFLASH_ERR_ARG, "keep_first %d keep_last %d", e->keep_first, e->keep_last);
+    if (const int r = check_apart(layers, n_layers)) return r;
     if (workspace_bytes < need) return report_error(DFLASH_ERR_ARG, "workspace %zu < %zu", workspace_bytes, need);
     if (const int r = pending()) return r;
     int sms = 0;

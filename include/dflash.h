@@ -788,7 +788,8 @@ int dflash_kv8_weigh(const dflash_kv8_cache* cache /*host*/, const dflash_kv8_qu
  * pages back.  Later rows attend over what is left; the kept keys hold their
  * true rotary positions, so new rows are rotated at the cache's position +
  * dropped (dflash_pages_shift), and masks (causal, window) count cached
- * positions.  Pages belong to one sequence each.
+ * positions.  Pages belong to one sequence each; pools that overlap (one given as
+ * two layers, or as K's and V's) are refused.
  * Workspace: any contents, not shared by calls that overlap.  err {2, site}: a
  * length or page out of range; that sequence is left alone (new_len = kv_len).
  * S up to 4096, max_pages up to 2^24.  Errors: CONFIG, ARG, CUDA.

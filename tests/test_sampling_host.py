@@ -128,6 +128,36 @@ def test_evict_other_guards(capi):      # noqa: F811
         assert capi.dflash_kv8_evict_workspace_bytes(S, pages) == 0
 
 
+@pytest.mark.parametrize("n", [1, 2, 5, 1024])
+def test_evict_refuses_pools_that_overlap(capi, n):      # noqa: F811
+    """One pool as two layers or as K's and V's, or the end of one as the start of another."""
+    codes, scales = 8 * 2 * 64 * 128, 8 * 2 * 4          # bytes of _cache's pools
+    base = 1 << 40
+
+    def call(change=None):
+        layers = (capi.dflash_kv8_cache * n)()
+        for i in range(n):
+            at = base + (n - 1 - i) * (2 * codes + 2 * scales)
+            layers[i] = _cache(capi, k_codes=at, v_codes=at + codes, k_scale=at + 2 * codes, v_scale=at + 2 * codes + scales)
+        if change:
+            change(layers)
+        e = _evict(capi)
+        assert capi.lib.dflash_kv8_evict(layers, n, C.byref(e), PTR, 1, PTR, None) == ARG
+        return capi.lib.dflash_last_error()
+
+    last = n - 1
+
+    def same(a, b):
+        return lambda x: setattr(x[last], a, getattr(x[0], b))
+
+    assert b"workspace" in call()                        # the next thing that is refused
+    for change in ([same(p, p) for p in ("k_codes", "v_codes", "k_scale", "v_scale")] if n > 1 else []) + [
+            same("v_codes", "k_codes"), same("v_scale", "k_scale"),
+            lambda x: setattr(x[last], "v_codes", x[last].k_codes + codes - 16),
+            lambda x: setattr(x[last], "v_scale", x[last].k_scale - 4)]:
+        assert b"overlap" in call(change)
+
+
 def test_shift_guards(capi):      # noqa: F811
     ok = [PTR, PTR, PTR, 3, 2, PTR, None]
     for at, bad in ((0, None), (1, None), (2, None), (3, -1), (3, (1 << 30) + 1), (4, 0), (4, (1 << 30) + 1), (5, None)):
