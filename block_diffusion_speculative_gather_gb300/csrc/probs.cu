@@ -7,8 +7,8 @@
 // The border m + T ln(min_p) is taken as a pair of fp32 numbers (48 bits) and
 // rounded up to the next fp32 value, so that comparing fp32 logits with it is exact.  log2(e) / T is
 // held as two fp32 numbers, so that a weight's exponent is off by the
-// difference's and the product's rounding alone; weights, sums and quotients are
-// fp32.
+// difference's and the product's rounding alone; weights, sums (of up to 40 terms a
+// thread) and quotients are fp32.
 //
 // A row's maximum is needed before its sum and its sum before its first output:
 // the row stays on the SMs between.  A cluster of up to 16 CTAs holds it in
@@ -539,9 +539,13 @@ probs_stream_kernel(const __grid_constant__ ProbsArgs a, int ranks, int cap, int
 
 constexpr int PT = 1024;
 
+// A thread sums TERMS weights in fp32, and those sums in 64 bits: in one fp32 number the
+// terms of 2^24 logits, 16384 a thread, came out by 10^-4 wrong where they are alike.
+constexpr int TERMS = 32;
+
 template <typename T>
 __global__ void __launch_bounds__(PT) probs_rows_kernel(const __grid_constant__ ProbsArgs a) {
-    __shared__ float red[32];
+    __shared__ double red[32];
     __shared__ unsigned long long red_key;
     __shared__ RowSetup s_setup;
     pdl_trigger();
@@ -573,13 +577,19 @@ __global__ void __launch_bounds__(PT) probs_rows_kernel(const __grid_constant__ 
     }
     const RowRule r = rule_of(m, s_setup);
     auto weigh = [&](float v) { return m < INFINITY ? weight(r, v) : (v == INFINITY ? 1.f : 0.f); };
-    float sum = 0.f;
-    for (int i = tid; i < a.vocab; i += PT) sum += weigh(to_f32(x[i]));
-    sum = warp_sum(sum);
+    double sum = 0.0;
+    for (int i0 = tid; i0 < a.vocab; i0 += TERMS * PT) {
+        const int end = min(i0 + TERMS * PT, a.vocab);
+        float part = 0.f;
+        for (int i = i0; i < end; i += PT) part += weigh(to_f32(x[i]));
+        sum += part;
+    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[warp] = sum;
     __syncthreads();
-    sum = warp_sum(red[lane]);
-    const float inv = 1.f / sum;
+    sum = red[lane];
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = (float)(1.0 / sum);
     for (int i = tid; i < a.vocab; i += PT) p[i] = weigh(to_f32(x[i])) * inv;
 }
 

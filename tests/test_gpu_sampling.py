@@ -78,6 +78,25 @@ def test_probs(capi, rows, V, kind):
         check_probs(x, t, out, min_p)
 
 
+@pytest.mark.parametrize("kind", [F32, BF, F16])
+@pytest.mark.parametrize("V,y", [(400003, 1.0), (400003, 3.0), ((1 << 24) + 5, 1.0), ((1 << 24) + 5, 0.5)])
+def test_probs_of_long_flat_rows(capi, V, y, kind):
+    """One likely token and V - 1 equal ones, whose roundings all go one way.  Weights e^-y are
+    off by 2^-22 y + 2^-21 relative; their sum by that, and as none of its fp32 parts has more
+    than 40 terms in a row and 16 levels above them, by 56 roundings of 2^-24; the quotient by
+    two more."""
+    x = torch.zeros(1, V, dtype=kind, device="cuda")
+    x[0, V // 2] = y
+    out = torch.empty(1, V, device="cuda")
+    capi.dflash_probs(x, floats([1.0]), out)
+    w = math.exp(-y)
+    tol = 2 * (y * 2.0 ** -22 + 2.0 ** -21) + 58 * 2.0 ** -24
+    top = out[0, V // 2].item()
+    out[0, V // 2] = w * top
+    for got, want in ((top, 1 / (1 + (V - 1) * w)), (out.min().item(), w / (1 + (V - 1) * w)), (out.max().item(), w / (1 + (V - 1) * w))):
+        assert abs(got - want) <= tol * want, (got / want - 1, tol)
+
+
 @pytest.mark.parametrize("V", [5, 4099, 151936])
 def test_probs_of_special_logits(capi, V):
     """Masked tokens, NaN and infinities, rows without a logit, zeros of both
