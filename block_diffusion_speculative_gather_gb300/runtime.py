@@ -424,6 +424,8 @@ class PagedKV8:
                 self.evict_workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
             torch.cuda.synchronize()
 
+    _weighed_first: Optional[int] = None      # the layer whose weights were the first since the last plan
+
     def _set(self, buf: torch.Tensor, lens):
         buf.copy_(torch.as_tensor(lens, dtype=torch.int32))
 
@@ -434,6 +436,7 @@ class PagedKV8:
             self._set(self.q_len, q_len)
         capi.dflash_pages_plan(self.kv_len, self.q_len, self.free, self.n_free, self.table, self.row_start,
                                self.positions, self.slots, self.kv_len, self.n_free)
+        self._weighed_first = None
         if self.weights is not None:
             capi.dflash_pages_shift(self.positions, self.row_start, self.dropped, self.angles)
 
@@ -456,13 +459,18 @@ class PagedKV8:
 
     def weigh(self, layer: int, q, lse, count=None, observe=0, fresh=None, scale=None, causal=True, window=0):
         """Add the attention that the step's rows gave each cached position of a
-        layer (lse as `attend` left it) to `self.weights`; `fresh` (by default in
-        layer 0) starts the step's own positions from 0."""
+        layer (lse as `attend` left it) to `self.weights`; `fresh` (by default in the
+        layer that is the first since `plan`) starts the step's own positions
+        from 0.  A step in which no layer is weighed leaves its positions
+        with what their pages held before."""
         if self.weights is None:
             raise capi.DFlashError(capi.DFLASH_ERR_ARG, "made without evict: no weights")
+        if self._weighed_first is None:
+            self._weighed_first = layer
         capi.dflash_kv8_weigh(q, lse, *self.caches[layer], self.table, self.kv_len, self.row_start, self.weights,
-                              self.err, count=count, observe=observe, fresh=layer == 0 if fresh is None else fresh,
-                              scale=scale, causal=causal, window=window)
+                              self.err, count=count, observe=observe,
+                              fresh=layer == self._weighed_first if fresh is None else fresh, scale=scale, causal=causal,
+                              window=window)
 
     def accept(self, probs, ids, uniform, draft_probs=None):
         """Verify the step's drafts and draw each sequence's last token:

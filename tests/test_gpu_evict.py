@@ -695,3 +695,47 @@ def test_captured_steps_advance_like_eager_ones(capi):
     assert eager.dropped.tolist()[0] > 0 and eager.dropped.tolist()[2] == 0
     eager.check()
     cap.check()
+
+
+@pytest.mark.parametrize("layers,order", [(2, [1]), (2, [1, 0]), (3, [2, 1]), (2, [0, 1])])
+def test_weights_of_reused_pages_start_anew_whatever_the_layers(capi, layers, order):
+    """Any of the layers weighed, in any order: a sequence's positions have what its own
+    rows gave them, n_q a row and layer, not what a page held for another one; eager
+    and where the layers' calls are captured without the plan."""
+    from block_diffusion_speculative_gather_gb300.runtime import PagedKV8
+    n_q, n_kv, dim, rows = 4, 2, 64, 200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = PagedKV8(layers, n_q, n_kv, dim, S=2, pages=8, max_pages=4, rows=rows, evict=True)
+    x = torch.randn(rows, n_q + 2 * n_kv, dim, device="cuda", generator=g).to(BF)
+    q, k, v = x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:]
+    lse, out = torch.zeros(rows, n_q, device="cuda"), torch.zeros(rows, n_q, dim, dtype=BF, device="cuda")
+
+    def step():
+        for i in order:
+            kv.attend(i, q, k, v, out=out, lse=lse)
+            kv.weigh(i, q, lse)
+
+    def check(held, n):
+        for s in range(2):
+            pages = kv.table[s, :-(-held[s] // 64)].long()
+            got = kv.weights[pages].flatten()[:held[s]].double().sum().item()
+            want = n[s] * n_q * len(order)
+            assert abs(got - want) < 1e-4 * want, (s, got, want)
+
+    kv.plan([100, 60])
+    step()
+    check([100, 60], [100, 60])
+    kv.trim([0, 0])
+    kv.plan([60, 100])
+    step()
+    check([60, 100], [60, 100])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    kv.trim([0, 0])
+    kv.plan([90, 70])
+    graph.replay()
+    check([90, 70], [90, 70])
+    kv.check()
