@@ -370,12 +370,16 @@ class PagedKV8:
 
         kv.plan(q_len)
         for i in range(layers):
-            kv.rotate(q, k)                   # at true positions, whatever was evicted before
-            out = kv.attend(i, q, k, v, lse=lse)
-            kv.weigh(i, q, lse)
+            kv.rotate(q[i], k)                # at true positions, whatever was evicted before
+            out = kv.attend(i, q[i], k, v, lse=lse[i])
         tokens, n = kv.accept(probs, ids, uniform, draft_probs)
+        for i in range(layers):               # between accept and trim: rows that stay count
+            kv.weigh(i, q[i], lse[i], count=n)
         kv.trim()                             # to the lengths that `accept` left
         kv.evict(budget, keep_first=4, keep_last=256)
+
+    `weigh` in the layer loop needs no layer's q and lse kept, but there the rows of
+    drafts that are refused later count as well.
 
     Everything stays on the device, on the current stream (with the lengths
     in `q_len` and `new_len` a step can be captured in a graph); `check`

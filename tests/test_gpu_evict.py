@@ -739,3 +739,91 @@ def test_weights_of_reused_pages_start_anew_whatever_the_layers(capi, layers, or
     graph.replay()
     check([90, 70], [90, 70])
     kv.check()
+
+
+def test_steps_whose_refused_rows_do_not_count(capi):
+    """Layers' rows and lse kept until verification: weights of the rows that stay alone
+    (count = n_tokens, before the trim), against the definitions; eviction in their
+    order; and the same steps captured."""
+    from block_diffusion_speculative_gather_gb300.runtime import PagedKV8
+    n_q, n_kv, dim, S, V, layers, rows, bud = 8, 2, 64, 3, 300, 2, 30, 90
+    g = torch.Generator(device="cuda").manual_seed(8)
+    f = lambda t: t.double().cpu().numpy()      # noqa: E731
+    make = lambda: PagedKV8(layers, n_q, n_kv, dim, S=S, pages=16, max_pages=4, rows=rows,      # noqa: E731
+                            rope=capi.rope_config(dim), vocab=V, evict=True)
+    x = torch.zeros(layers, rows, n_q + 2 * n_kv, dim, dtype=BF, device="cuda")
+    probs, q_probs = torch.zeros(rows, V, device="cuda"), torch.zeros(rows, V, device="cuda")
+    ids, u = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, device="cuda")
+
+    class Side:
+        def __init__(self):
+            self.kv, self.x = make(), torch.empty_like(x)
+            self.out, self.lse = torch.zeros_like(x[0, :, :n_q]), torch.zeros(layers, rows, n_q, device="cuda")
+
+        def forward(self):
+            self.x.copy_(x)
+            self.kv.plan()
+            for i in range(layers):
+                q, k, v = self.x[i, :, :n_q], self.x[i, :, n_q:n_q + n_kv], self.x[i, :, n_q + n_kv:]
+                self.kv.rotate(q, k)
+                self.kv.attend(i, q, k, v, out=self.out, lse=self.lse[i])
+
+        def choose(self):
+            _, n = self.kv.accept(probs, ids, u, q_probs)
+            for i in range(layers):
+                self.kv.weigh(i, self.x[i, :, :n_q], self.lse[i], count=n)
+
+        def cut(self):
+            self.kv.trim()
+            self.kv.evict(keep_first=2, keep_last=20)
+
+    eager, cap = Side(), Side()
+    for a in (eager, cap):
+        a.kv.budget.copy_(ints([bud, bud, 0]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cap.forward(), cap.choose(), cap.cut()
+    refused = 0
+    for i in range(14):
+        n = [10, 10, 10] if i % 3 else [10, 4, 7]
+        for a in (eager, cap):
+            a.kv.q_len.copy_(ints(n))
+        x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+        probs.copy_(torch.softmax(2 * torch.randn(rows, V, device="cuda", generator=g), 1))
+        q_probs.copy_(probs.roll(1, 0))
+        ids.copy_(q_probs.argmax(1))
+        u.copy_(torch.rand(rows, device="cuda", generator=g) * 1.1)      # an eleventh of the drafts is refused
+        eager.forward()
+        kv = eager.kv
+        before, table, held, start = f(kv.weights), kv.table.tolist(), kv.kv_len.tolist(), kv.row_start.tolist()
+        eager.choose()
+        count = kv.n_tokens.tolist()
+        refused += sum(n) - sum(count)
+        bound = np.zeros_like(before)
+        for layer in range(layers):
+            c = kv.caches[layer]
+            before, b = P.weigh(f(eager.x[layer, :, :n_q]), f(eager.lse[layer]), values(c[0]).numpy(), f(c[2]), table, held, start,
+                                before, count=count, fresh=layer == 0, scale=dim ** -0.5)
+            bound += b
+        e = np.abs(f(kv.weights) - before)
+        for s in range(S):
+            for p in table[s][:-(-held[s] // 64)]:
+                assert (e[p] <= bound[p] + 1e-30).all()
+        pools = [(values(c[0]).numpy().copy(), values(c[1]).numpy().copy(), f(c[2]), f(c[3])) for c in kv.caches]
+        new, source, _ = P.evict(pools, table, kv.new_len.tolist(), f(kv.weights), [bud, bud, 0], 2, 20)
+        eager.cut()
+        assert kv.kv_len.tolist() == new
+        for s in range(S):
+            if kv.dropped[s] > 0:
+                assert kv.source[s, :new[s]].tolist() == source[s]
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("kv_len", "table", "n_free", "dropped", "kept", "n_tokens", "new_len", "weights"):
+            assert torch.equal(getattr(eager.kv, name), getattr(cap.kv, name)), name
+        for a, b in zip(eager.kv.caches, cap.kv.caches):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert refused > 20 and eager.kv.dropped.tolist()[0] > 0 and eager.kv.dropped.tolist()[2] == 0
+    eager.kv.check()
+    cap.kv.check()
