@@ -11,7 +11,13 @@
 //
 // Which token a uniform number falls on is a matter of sums of up to a vocabulary
 // of terms: differences are taken exactly (two fp32 numbers each), sums are kept
-// as pairs of fp32 numbers (48 bits, an addition off by about 2^-47), in a fixed order.
+// as pairs of fp32 numbers, in a fixed order.  The k-th addition of a chain leaves up
+// to 2^-24 of the sum to the low part, which then holds up to k 2^-24 of it and is
+// rounded by k 2^-48: n additions are off by at most n (n + 3) / 2 of 2^-48, a lane's 32 of
+// a unit by 2^-38.8.  With the joins of lanes, units (one a thread up to 262144 tokens,
+// else up to 64) and warps, and the search in the unit, a running sum is within 2^-36
+// of the whole up to 262144 tokens and 2^-34 at 2^24, if all roundings are at their
+// largest and go one way.  A uniform number's own step is 2^-24.
 //
 // Only one row of p and q is read whole.  Its tokens are dealt in units of 1024 to
 // warps (each CTA finds by itself, from two numbers a draft, which row that is),
@@ -37,7 +43,7 @@ template <bool Q> constexpr int per() { return Q ? 8 : 16; }
 template <bool Q> constexpr int block() { return 32 * per<Q>(); }
 static_assert(VERIFY_UNIT == 4 * VT && VERIFY_UNIT % block<false>() == 0, "four tokens a thread of the search");
 
-// A sum as hi + lo, |lo| below half a step of hi.
+// A sum as hi + lo: the rounded sum, and what its roundings have left over.
 struct Pair {
     float hi, lo;
 };
