@@ -24,7 +24,8 @@
 // between a turn's reads and its writes.  Bound by DRAM where
 // sequences and layers are many: 8 of up to 6000 positions to 2500, 10 layers of 8 heads of
 // 128, move 818 MB in 139 us with the choice, 5.9 TB/s (three turns in the ring 152 us).
-// One of 4095 to 2048, 5 layers: 18.6 us, the choice and a chain of turns.
+// One of 4095 to 2048, 5 layers: 22.3 us (18.6 with the pools in L2), the choice and a
+// chain of turns; of 8192 to 4096 33.7, of 8193 44.1, where the choice looks its weights up.
 
 #include "cluster_dev.cuh"
 #include "copy_dev.cuh"
@@ -475,7 +476,7 @@ int launch_kv8_evict(const Kv8EvictArgs& args, const Kv8MoveLayers& l, bool choo
     }
     const int chains = a.S * a.n_kv;
     // Three CTAs of the move run on an SM.  Few chains: as many CTAs each as run at once (one
-    // sequence of 4095 positions to 2048, 5 layers: 18.6 us, by one CTA each 28.3).  More
+    // sequence of 4095 positions to 2048, 5 layers, pools in L2: 18.6 us, by one CTA each 28.3).  More
     // than run at once: two each where that takes at least an eighth less rounds (of 6000
     // positions to 2500: 576 chains 91 us, by one CTA each 113; 960 chains 117 and 124; where
     // it does not, 1280 chains 147 and 139).

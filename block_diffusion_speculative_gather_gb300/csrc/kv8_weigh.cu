@@ -19,7 +19,7 @@
 // keys come by asynchronous copies, three heads ahead, from one item into the
 // next; a lane reads what it copied itself, so that no barrier stands between.
 //
-// 32 single tokens over 10000 positions each on average (32 heads on 8) take 62 us for
+// 32 single tokens over 10000 positions each on average (32 heads on 8) take 63 us for
 // 345 MB, 5.5 TB/s: DRAM, beside the conversion of the codes (half of the issue slots).
 // One token over 1088 takes 8.3 us, a chain of trips to memory: lengths, table, keys,
 // with the rows and their lse beside, then the exponentials of eight heads.

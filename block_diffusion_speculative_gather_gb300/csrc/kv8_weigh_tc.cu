@@ -16,9 +16,11 @@
 // exponential each, summed.  Each group has two tiles of tensor memory, so that the
 // next one's scores are there when it comes.  Bound by the exponentials (16 a
 // cycle and SM: 1024 cycles a tile, whose MMAs take 512) and the instructions around
-// them: the last 64 rows of four prompts behind up to 8192 positions (32 heads on 8) take
-// 24.3 us, a third of the exponentials' rate: a CTA has one or two items, whose start
-// (tables, tensor memory, the first keys and rows) nothing hides.
+// them where rows are many: the last 64 rows of four prompts behind up to 8192 positions (32
+// heads on 8) take 24.6 us, 144 items on 152 CTAs.  About 11 us pass before the first
+// columns (tables, tensor memory, the first keys) and on eight heads' keys, then a tile
+// takes 0.8 to 0.9 us where its exponentials need 0.54 (32 rows 16.4 us, 128 38.8, 256 65).
+// Few rows: the work on a head's keys, their way in (two places) and conversion.
 
 #include <type_traits>
 
@@ -434,10 +436,12 @@ int launch_tc(const CUtensorMap& q_map, const Kv8WeighArgs& a, int sms, cudaStre
 
 }  // namespace
 
-// From this many (row, q head) pairs of a kv head a sequence on, of the call's rows on
-// average.  32 heads on 8, bf16, in us by this form and by kv8_weigh.cu: 32 sequences of 8000
-// positions, 4 pairs 70, 35; 16 pairs 64, 52; 32 pairs 64, 87; 64 pairs 67, 151; one
-// sequence of 1088, 4 pairs 10.8, 8.3; 16 pairs 10.8, 11.4; 64 pairs 11.7, 30.
+// From this many (row, q head) pairs of a kv head a sequence on, of the call's rows (its
+// padding among them) on average.  32 heads on 8, bf16, caches that are not in L2, in us by
+// this form and by kv8_weigh.cu: 32 sequences of 8000 positions, 4 pairs 107, 50; 16 pairs 107,
+// 89; 20 pairs 107, 120; 64 pairs 112, 264.  8 of them, 16 pairs 35, 29; 20 pairs 35, 38; one, 12
+// pairs 12.7, 13.9.  One of 1088, 8 pairs 10.9, 8.6; 16 pairs 10.9, 11.6; 64 pairs 11.6, 30.  f16:
+// 32 of 8000, 20 pairs 102, 102; 32 pairs 103, 124.
 constexpr int TC_PAIRS = 20;
 
 bool kv8_weigh_by_tc(const Kv8WeighArgs& a) {

@@ -19,7 +19,7 @@
 // rows (above 327680 logits) are read three times, by one CTA.
 //
 // One row of 151936 fp32 logits takes 5.0 us, launch, load, two exchanges and store one
-// after the other.  512 of them move 622 MB in 137 us, 4.5 TB/s: what holds them up is
+// after the other (6.1 with min_p, for its logarithm in 64 bits).  512 of them move 622 MB in 137 us, 4.5 TB/s: what holds them up is
 // each row's two exchanges, in which an SM has no other row to work on, and that clusters
 // of 8 with an SM a CTA find room on 120 of the 152 SMs.
 
@@ -396,7 +396,8 @@ __device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.
 // lane in a piece of its warp's outputs, and the places for pieces.
 // Of 16-bit logits the next row takes half as much shared memory as its outputs would: two
 // CTAs fit an SM, one works while the other waits for its cluster, and outputs leave by
-// 1 KB pieces (512 rows of 151936: 132 us; by one CTA of 1024 threads an SM 150).  fp32
+// 1 KB pieces (512 rows of 151936: 135 us; by one CTA of 1024 threads an SM 150), though a
+// thread's 40 weights do not all fit its 64 registers (it spills 108 bytes a row).  fp32
 // rows have one CTA and a place for all of a warp's outputs (137 us; in 1 KB pieces 153; two
 // CTAs in clusters of 16 150; two without a place for the next row 187).
 template <typename T> struct Stream {

@@ -24,9 +24,9 @@
 // a unit's sum goes to memory, and the last of a sequence's CTAs finds the unit
 // that u_0 falls into and reads it again.  No CTA waits for another.
 //
-// With 151936 tokens and 16 rows a sequence one takes 7.4 us, a chain of trips to
+// With 151936 tokens and 16 rows a sequence one takes 7.1 us, a chain of trips to
 // memory: row starts, ids, p and q of the drafts, the row, the ticket, the sums, the unit.
-// 32 take 11.6 us for 38.9 MB, the same chain with the reading at 6 TB/s in it; 480 rows
+// 32 take 14.5 us for 38.9 MB, the same chain around the reads (11.5 from L2); 480 rows
 // without drafts 57 us, 5.1 TB/s, where a pair's additions (7 instructions a token) and
 // the chain at each CTA's end stand beside the reads.
 

@@ -759,9 +759,10 @@ int dflash_verify_drafts(const dflash_drafts* d /*host*/, void* workspace, size_
  * count (NULL: all; below 0: none), of those with observe > 0 the last
  * `observe`: after verification and before the trim count = n_tokens leaves
  * rejected rows out (every layer's q and lse kept until then; a call beside each
- * layer's attention counts them too), and a long prompt's last rows stand for it.  fresh 1: the step's own positions
- * (every row's) start from 0 (the first layer's call of a step; the others
- * add).  weights: fp32 [n_pages][DFLASH_KV8_PAGE], one for all layers of a
+ * layer's attention counts them too), and a long prompt's last rows stand for it.
+ * fresh 1: the step's own positions (every row's) start from 0 (the first layer's
+ * call of a step; the others add; without one they start from what their pages
+ * held).  weights: fp32 [n_pages][DFLASH_KV8_PAGE], one for all layers of a
  * table or one each.  A page belongs to one sequence.  Terms are added in a
  * fixed order, without atomics; a sequence's results depend on its own rows
  * and positions and the call's counts, not on the others.  Scores that are NaN
